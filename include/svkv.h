@@ -1,8 +1,9 @@
 /*
  * svkv.h -- C ABI of the KV-cache steps around verification, in the same
  * library as specverify.h (libspecverify.so): committing the verified
- * entries to a sink + ring KV cache, listing its valid slots, and windowing
- * the draft model's block table.
+ * entries to a sink + ring KV cache, loading prompts into it, listing its
+ * valid slots, committing a verified path to a paged cache, and windowing the
+ * draft model's block table.
  *
  * Sources (page title and section):
  *   deferred speculative decoding page (lqnn.cn): "环形上下文与注意力沉淀机制"
@@ -35,6 +36,7 @@ extern "C" {
 /* device status bit (besides the SV_ST_* bits of specverify.h) */
 #define SV_ST_BAD_LENGTH 0x40 /* a negative position / sequence length, or an accepted
                                  count past the staged entries */
+#define SV_ST_BAD_PAGE 0x80   /* a block-table entry in use outside [0, num_pages) */
 
 /*
  * Commit the verified entries of one speculation step to a sink + ring KV
@@ -62,6 +64,54 @@ extern "C" {
 int sv_kv_commit(void* k_pool, void* v_pool, const void* k_new, const void* v_new,
                  const int32_t* num_accepted, int32_t* pos, int B, int LH, int R,
                  int row_bytes, int sink, int window, int32_t* dev_status, void* stream);
+
+/*
+ * Load prompts into a sink + ring KV cache (one layer's heads), per sequence
+ * b of n = cu_seqlens[b + 1] - cu_seqlens[b] tokens: its first `sink`
+ * positions and its last `window` ones, all of them when n <= sink + window,
+ * are copied to their slots Slot(p) of pool rows head0 .. head0 + Hkv - 1, and
+ * pos[b] = n.  The state is that of n tokens committed one by one: the next
+ * sv_kv_commit continues at position n.  Other slots stay as they are.
+ *   k, v [T][Hkv][row_bytes], packed sequences (cu_seqlens [B + 1] int32,
+ *   non-decreasing, as for sv_prompt_attn); k_pool, v_pool
+ *   [B][LH][sink + window][row_bytes]; pos [B] int32, written.
+ * A sequence whose bounds are not 0 <= cu_seqlens[b] <= cu_seqlens[b + 1] <= T
+ * is left out (its pool rows and pos[b] stay) and SV_ST_BAD_LENGTH reported.
+ * Requires row_bytes as for sv_kv_commit, all KV buffers 16-byte aligned,
+ * sink >= 0, window >= 1, 0 <= head0, head0 + Hkv <= LH, T >= 0, B <= 65535
+ * and min(T, sink + window) * Hkv * row_bytes <= 2^34.
+ */
+int sv_kv_fill(const void* k, const void* v, const int32_t* cu_seqlens, void* k_pool,
+               void* v_pool, int32_t* pos, int B, int T, int Hkv, int LH, int head0,
+               int row_bytes, int sink, int window, int32_t* dev_status, void* stream);
+
+/*
+ * Commit a verified path to a paged KV cache, per request b with
+ * k = num_accepted[b]: entry j = 0..k, staged entry 0 (the root of the tree)
+ * for j == 0 and nodes[b][j - 1] (sv_tree_verify's out_nodes) after it, is
+ * copied for every layer/head row to position seq_lens[b] + j, page
+ * block_table[b][position / page_size], row position mod page_size; then
+ * out_seq_lens[b] = seq_lens[b] + k + 1.  nodes == NULL: a chain, entry j is
+ * staged entry j (spec_verify's out_num_accepted, or a prompt of k + 1
+ * tokens).  The other entries are dropped.
+ *   k_pages, v_pages [num_pages][LH][page_size][row_bytes]
+ *   k_new, v_new     [B][LH][N][row_bytes]
+ *   block_table [B][cols], seq_lens [B], nodes [B][N], num_accepted [B],
+ *   out_seq_lens [B], int32; out_seq_lens may be seq_lens itself.
+ * k < 0: nothing is committed (a dropped request).  k >= N, or entries that
+ * would not fit the table's cols * page_size positions or 2^31 - 1
+ * (SV_ST_BAD_LENGTH), a node outside [0, N) (SV_ST_BAD_TOKEN) or a page in
+ * use outside [0, num_pages) (SV_ST_BAD_PAGE): nothing is committed and
+ * out_seq_lens[b] = seq_lens[b].  No two requests may write one page.
+ * Requires row_bytes as for sv_kv_commit, the four KV buffers 16-byte
+ * aligned, page_size >= 1, cols >= 1, num_pages >= 1, 1 <= N <= 2^20,
+ * B <= 65535.
+ */
+int sv_page_commit(void* k_pages, void* v_pages, const void* k_new, const void* v_new,
+                   const int32_t* block_table, const int32_t* seq_lens, const int32_t* nodes,
+                   const int32_t* num_accepted, int B, int LH, int N, int row_bytes,
+                   int num_pages, int page_size, int cols, int32_t* out_seq_lens,
+                   int32_t* dev_status, void* stream);
 
 /*
  * The valid physical slots of every request in logical order:

@@ -15,10 +15,12 @@ import torch
 from ._build_lib import LIB_PATH
 
 SV_F32, SV_BF16 = 0, 1
+SV_F16 = 2  # storage type of the attention calls only
 SV_OK, SV_ERR_INVALID_ARG, SV_ERR_DTYPE, SV_ERR_CUDA, SV_ERR_WORKSPACE = range(5)
 SV_ST_NONFINITE, SV_ST_BAD_TOKEN, SV_ST_BAD_TEMP = 0x1, 0x2, 0x4
 SV_ST_TIMEOUT, SV_ST_WORKSPACE, SV_ST_DEGENERATE = 0x8, 0x10, 0x20
 SV_ST_BAD_LENGTH = 0x40
+SV_ST_BAD_PAGE = 0x80
 SV_MAX_GAMMA = 32
 
 EXPORTED = ("sv_workspace_bytes", "sv_workspace_init", "spec_verify", "spec_verify_diag",
@@ -26,9 +28,10 @@ EXPORTED = ("sv_workspace_bytes", "sv_workspace_init", "spec_verify", "spec_veri
             "sv_draft_workspace_bytes", "sv_draft_sample", "sv_set_tuning",
             "sv_set_stage_events", "sv_set_tail", "sv_test_withhold_slot", "sv_error_string",
             "sv_version",
-            "sv_kv_commit", "sv_kv_valid_slots", "sv_window_cols", "sv_window_block_table",
-            "sv_window_seq_lens_host", "sv_tree_verify", "sv_tree_set_cluster",
+            "sv_kv_commit", "sv_kv_fill", "sv_page_commit", "sv_kv_valid_slots",
+            "sv_window_cols", "sv_window_block_table", "sv_window_seq_lens_host", "sv_tree_verify", "sv_tree_set_cluster",
             "sv_tree_set_warps")
+EXPORTED_ATTN = ("sv_attn_workspace_bytes", "sv_tree_attn", "sv_ring_attn", "sv_prompt_attn")
 SV_TREE_MAX_N = 256
 SV_NOALLOC_MAX_WORKSPACE = 16 << 20
 
@@ -64,6 +67,16 @@ def lib() -> ctypes.CDLL:
         L.sv_window_block_table.argtypes = [P, P, I, I, I, I, I, P, P, P, P, P]
         L.sv_window_seq_lens_host.argtypes = [P, I, I, I, I, P]
         L.sv_tree_verify.argtypes = [I, P, P, P, P, P, P, P, I, I, I, P, P, P, P, P]
+        L.sv_kv_fill.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, P]
+        L.sv_page_commit.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, P, P]
+        F = ctypes.c_float
+        L.sv_attn_workspace_bytes.argtypes = [I, I, I, I]
+        L.sv_attn_workspace_bytes.restype = Z
+        L.sv_tree_attn.argtypes = [I, P, P, P, P, P, P, P, P, F, I, I, I, I, I, I, I, I, I, I, P,
+                                   P, Z, P, P]
+        L.sv_ring_attn.argtypes = [I, P, P, P, P, P, P, F, I, I, I, I, I, I, I, I, I, P, P, Z, P,
+                                   P]
+        L.sv_prompt_attn.argtypes = [I, P, P, P, P, F, I, I, I, I, I, I, I, P, P, P]
         L.sv_tree_set_cluster.argtypes = [I]
         L.sv_tree_set_warps.argtypes = [I]
         L.sv_set_tuning.argtypes = [I]
@@ -78,6 +91,8 @@ def lib() -> ctypes.CDLL:
                      "sv_version",
                      "sv_test_withhold_slot",
                      "sv_kv_commit", "sv_kv_valid_slots", "sv_window_cols",
+                     "sv_kv_fill", "sv_page_commit", "sv_tree_attn", "sv_ring_attn",
+                     "sv_prompt_attn",
                      "sv_window_block_table", "sv_window_seq_lens_host", "sv_tree_verify",
                      "sv_tree_set_cluster", "sv_tree_set_warps"):
             getattr(L, name).restype = I
@@ -155,6 +170,13 @@ def sv_set_stage_events(events) -> None:
     around the kernels of the next calls; an empty list turns it off."""
     handles = (ctypes.c_void_p * max(1, len(events)))(*[e.cuda_event for e in events])
     _check(lib().sv_set_stage_events(handles if events else None, len(events)))
+
+
+def _counts(B: int, **tensors) -> None:
+    """Each tensor has the given number of elements."""
+    for name, (t, n) in tensors.items():
+        if t is not None and t.numel() != n:
+            raise SpecVerifyError(f"{name} must have {n} elements, got {t.numel()}")
 
 
 def _shapes(target_logits: torch.Tensor):
@@ -313,6 +335,59 @@ def sv_kv_commit(k_pool, v_pool, k_new, v_new, num_accepted, pos, sink: int, win
         _dev(dev_status, torch.int32, "dev_status"), _stream(stream, k_pool.device)))
 
 
+def sv_kv_fill(k, v, cu_seqlens, k_pool, v_pool, pos, sink: int, window: int, head0: int = 0,
+               dev_status=None, stream=None) -> None:
+    """Load packed prompts k/v [T][Hkv][D] (cu_seqlens [B+1] int32) into rows
+    head0 .. head0 + Hkv - 1 of the sink + ring pools [B][LH][sink+window][D]
+    and set pos [B] int32 to the prompts' lengths."""
+    if k.dim() != 3 or k_pool.dim() != 4:
+        raise SpecVerifyError("k must be [T][Hkv][D], pools [B][LH][sink+window][D]")
+    T, Hkv, D = k.shape
+    B, LH, C, Dp = k_pool.shape
+    if (tuple(v.shape) != tuple(k.shape) or tuple(v_pool.shape) != tuple(k_pool.shape) or Dp != D
+            or C != sink + window):
+        raise SpecVerifyError("KV shapes disagree")
+    if len({k.dtype, v.dtype, k_pool.dtype, v_pool.dtype}) != 1:
+        raise SpecVerifyError("KV buffers must share one dtype")
+    _counts(B, cu_seqlens=(cu_seqlens, B + 1), pos=(pos, B))
+    _check(lib().sv_kv_fill(
+        _dev(k, None, "k"), _dev(v, None, "v"), _dev(cu_seqlens, torch.int32, "cu_seqlens"),
+        _dev(k_pool, None, "k_pool"), _dev(v_pool, None, "v_pool"),
+        _dev(pos, torch.int32, "pos"), B, T, Hkv, LH, head0, D * k.element_size(), sink, window,
+        _dev(dev_status, torch.int32, "dev_status"), _stream(stream, k_pool.device)))
+
+
+def sv_page_commit(k_pages, v_pages, k_new, v_new, block_table, seq_lens, nodes, num_accepted,
+                   out_seq_lens, dev_status=None, stream=None) -> None:
+    """Commit the root and the accepted nodes of a tree (nodes [B][N] int32 as
+    sv_tree_verify writes them), or of a chain (nodes None), to a paged cache:
+    k_pages/v_pages [P][LH][page][D], k_new/v_new [B][LH][N][D], block_table
+    [B][cols], seq_lens / num_accepted / out_seq_lens [B] int32 (out_seq_lens
+    may be seq_lens)."""
+    if k_pages.dim() != 4 or k_new.dim() != 4 or block_table.dim() != 2:
+        raise SpecVerifyError("pages must be [P][LH][page][D], staged entries [B][LH][N][D], "
+                              "block_table [B][cols]")
+    P, LH, page, D = k_pages.shape
+    B, _, N, _ = k_new.shape
+    if (tuple(v_pages.shape) != tuple(k_pages.shape) or tuple(v_new.shape) != tuple(k_new.shape)
+            or tuple(k_new.shape) != (B, LH, N, D) or block_table.shape[0] != B):
+        raise SpecVerifyError("KV shapes disagree")
+    if nodes is not None and tuple(nodes.shape) != (B, N):
+        raise SpecVerifyError("nodes must be [B][N]")
+    if len({k_pages.dtype, v_pages.dtype, k_new.dtype, v_new.dtype}) != 1:
+        raise SpecVerifyError("KV buffers must share one dtype")
+    _counts(B, seq_lens=(seq_lens, B), num_accepted=(num_accepted, B),
+            out_seq_lens=(out_seq_lens, B))
+    _check(lib().sv_page_commit(
+        _dev(k_pages, None, "k_pages"), _dev(v_pages, None, "v_pages"),
+        _dev(k_new, None, "k_new"), _dev(v_new, None, "v_new"),
+        _dev(block_table, torch.int32, "block_table"), _dev(seq_lens, torch.int32, "seq_lens"),
+        _dev(nodes, torch.int32, "nodes"), _dev(num_accepted, torch.int32, "num_accepted"),
+        B, LH, N, D * k_pages.element_size(), P, page, block_table.shape[1],
+        _dev(out_seq_lens, torch.int32, "out_seq_lens"),
+        _dev(dev_status, torch.int32, "dev_status"), _stream(stream, k_pages.device)))
+
+
 def sv_kv_valid_slots(pos, sink: int, window: int, out_slots, out_len, dev_status=None,
                       stream=None) -> None:
     """Valid physical slots of every request in logical order: out_slots
@@ -389,3 +464,111 @@ def sv_tree_set_cluster(ctas: int = 0) -> None:
 def sv_tree_set_warps(warps: int = 0) -> None:
     """Warps per CTA for sv_tree_verify: 0 = automatic, 8 or 16 forced."""
     _check(lib().sv_tree_set_warps(int(warps)))
+
+
+# ------------------------------------------------------- attention over the caches
+
+def _attn_dtype(q, *others) -> int:
+    if any(t.dtype != q.dtype for t in others):
+        raise SpecVerifyError("queries, keys, values and output must share one dtype")
+    if any(t.device != q.device for t in others):
+        raise SpecVerifyError("queries, keys, values and output must be on one device")
+    if q.dtype == torch.bfloat16:
+        return SV_BF16
+    if q.dtype == torch.float16:
+        return SV_F16
+    raise SpecVerifyError(f"attention takes bfloat16 or float16, got {q.dtype}")
+
+
+def sv_attn_workspace_bytes(N: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(lib().sv_attn_workspace_bytes(N, Hq, Hkv, D))
+
+
+def make_attn_workspace(B: int, N: int, Hq: int, Hkv: int, D: int, device) -> torch.Tensor:
+    """Allocate a workspace for sv_tree_attn (N nodes) or sv_ring_attn (N = R
+    tokens); its size does not depend on the batch."""
+    n = sv_attn_workspace_bytes(N, Hq, Hkv, D)
+    if n == 0:
+        raise SpecVerifyError("sizes the attention calls refuse")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _staged_shapes(q, k_cache, v_cache, k_new, v_new, out, head0, kv_heads):
+    """(B, N, Hq, Hkv, D, LH) of queries [B][N][Hq][D], a cache [..][LH][..][D] and staged
+    entries [B][LH][N][D]."""
+    if q.dim() != 4 or k_cache.dim() != 4 or k_new.dim() != 4:
+        raise SpecVerifyError("queries, caches and staged entries must have four dimensions")
+    B, N, Hq, D = q.shape
+    LH = k_cache.shape[1]
+    if (tuple(out.shape) != tuple(q.shape) or tuple(v_cache.shape) != tuple(k_cache.shape)
+            or k_cache.shape[3] != D or tuple(k_new.shape) != (B, LH, N, D)
+            or tuple(v_new.shape) != tuple(k_new.shape)):
+        raise SpecVerifyError("shapes of queries, cache, staged entries and output disagree")
+    return B, N, Hq, (LH - head0 if kv_heads is None else kv_heads), D, LH
+
+
+def sv_tree_attn(q, k_pages, v_pages, block_table, seq_lens, k_new, v_new, parent, out, workspace,
+                 head0: int = 0, kv_heads: int | None = None, scale: float | None = None,
+                 dev_status=None, stream=None) -> None:
+    """Attention of a drafted tree (parent [B][N] int32; None: a chain) over a
+    paged cache: q/out [B][N][Hq][D], k_pages/v_pages [P][LH][page][D],
+    block_table [B][cols] and seq_lens [B] int32, staged k_new/v_new
+    [B][LH][N][D]; KV heads are rows head0 .. head0 + kv_heads - 1 of LH (all
+    from head0 when None); scale defaults to 1 / sqrt(D)."""
+    B, N, Hq, Hkv, D, LH = _staged_shapes(q, k_pages, v_pages, k_new, v_new, out, head0, kv_heads)
+    dt = _attn_dtype(q, k_pages, v_pages, k_new, v_new, out)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise SpecVerifyError("block_table must be [B][cols]")
+    if parent is not None and tuple(parent.shape) != (B, N):
+        raise SpecVerifyError("parent must be [B][N]")
+    _counts(B, seq_lens=(seq_lens, B))
+    _check(lib().sv_tree_attn(
+        dt, _dev(q, None, "q"), _dev(k_pages, None, "k_pages"), _dev(v_pages, None, "v_pages"),
+        _dev(block_table, torch.int32, "block_table"), _dev(seq_lens, torch.int32, "seq_lens"),
+        _dev(k_new, None, "k_new"), _dev(v_new, None, "v_new"),
+        _dev(parent, torch.int32, "parent"), D ** -0.5 if scale is None else scale, B, N, Hq, Hkv,
+        D, k_pages.shape[0], LH, head0, k_pages.shape[2], block_table.shape[1],
+        _dev(out, None, "out"), _dev(workspace, None, "workspace"),
+        workspace.numel() * workspace.element_size(),
+        _dev(dev_status, torch.int32, "dev_status"), _stream(stream, q.device)))
+
+
+def sv_ring_attn(q, k_pool, v_pool, pos, k_new, v_new, sink: int, window: int, out, workspace,
+                 head0: int = 0, kv_heads: int | None = None, scale: float | None = None,
+                 dev_status=None, stream=None) -> None:
+    """Attention of the newest R tokens over a sink + ring cache: q/out
+    [B][R][Hq][D], pools [B][LH][sink+window][D], pos [B] int32, staged
+    k_new/v_new [B][LH][R][D]; heads and scale as for sv_tree_attn."""
+    B, R, Hq, Hkv, D, LH = _staged_shapes(q, k_pool, v_pool, k_new, v_new, out, head0, kv_heads)
+    dt = _attn_dtype(q, k_pool, v_pool, k_new, v_new, out)
+    if k_pool.shape[0] != B or k_pool.shape[2] != sink + window:
+        raise SpecVerifyError("pools must be [B][LH][sink+window][D]")
+    _counts(B, pos=(pos, B))
+    _check(lib().sv_ring_attn(
+        dt, _dev(q, None, "q"), _dev(k_pool, None, "k_pool"), _dev(v_pool, None, "v_pool"),
+        _dev(pos, torch.int32, "pos"), _dev(k_new, None, "k_new"), _dev(v_new, None, "v_new"),
+        D ** -0.5 if scale is None else scale, B, R, Hq, Hkv, D, LH, head0, sink, window,
+        _dev(out, None, "out"), _dev(workspace, None, "workspace"),
+        workspace.numel() * workspace.element_size(),
+        _dev(dev_status, torch.int32, "dev_status"), _stream(stream, q.device)))
+
+
+def sv_prompt_attn(q, k, v, cu_seqlens, sink: int, window: int, out, scale: float | None = None,
+                   dev_status=None, stream=None) -> None:
+    """Attention of packed prompts under a sliding window with sinks: q/out
+    [T][Hq][D], k/v [T][Hkv][D], cu_seqlens [B+1] int32."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise SpecVerifyError("q must be [T][Hq][D], k and v [T][Hkv][D]")
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if (tuple(out.shape) != tuple(q.shape) or tuple(k.shape) != (T, Hkv, D)
+            or tuple(v.shape) != tuple(k.shape)):
+        raise SpecVerifyError("shapes of queries, keys, values and output disagree")
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise SpecVerifyError("cu_seqlens must be [B+1]")
+    dt = _attn_dtype(q, k, v, out)
+    _check(lib().sv_prompt_attn(
+        dt, _dev(q, None, "q"), _dev(k, None, "k"), _dev(v, None, "v"),
+        _dev(cu_seqlens, torch.int32, "cu_seqlens"), D ** -0.5 if scale is None else scale,
+        cu_seqlens.shape[0] - 1, T, Hq, Hkv, D, sink, window, _dev(out, None, "out"),
+        _dev(dev_status, torch.int32, "dev_status"), _stream(stream, q.device)))

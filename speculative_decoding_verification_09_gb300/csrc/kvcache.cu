@@ -4,6 +4,9 @@
 //
 //   sv_kv_commit           copy kernel (one 2-D grid: request x span of the
 //                          request's staged vectors) + position update
+//   sv_kv_fill             one copy kernel (request x span of its kept vectors)
+//   sv_page_commit         copy kernel (rows x entries x request), and a length
+//                          update when the lengths are updated in place
 //   sv_kv_valid_slots      one thread per (request, slot index)
 //   sv_window_block_table  one thread per (request, clone column)
 //
@@ -12,9 +15,9 @@
 // "C++ 环形 KV 缓存管理内核实现"; the window arithmetic follows the vllm-ascend
 // draft KV sliding-window page, sections "窗口数学" and "block table 的裁剪方式".
 //
-// All three are memory-bound gathers and scatters of whole 16-byte vectors
-// (the commit) or of int32 words (the maps); the commit moves only the
-// accepted entries: rejected drafts are never written.
+// All are memory-bound gathers and scatters of whole 16-byte vectors (the
+// commits and the fill) or of int32 words (the maps); the commits move only
+// the accepted entries: rejected drafts are never written.
 
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -130,6 +133,176 @@ __global__ void __launch_bounds__(KV_THREADS) sv_kv_advance(const KvParams K) {
     return;
   }
   if (k >= 0) K.pos[b] = p + k + 1;
+}
+
+struct FillParams {
+  const uint4* k;
+  const uint4* v;
+  const int32_t* cu;
+  uint4* k_pool;
+  uint4* v_pool;
+  int32_t* pos;
+  int32_t* status;
+  int T, Hkv, LH, head0, nvec, sink, window;
+  unsigned long long m_nvec;  // division multiplier of nvec
+};
+
+// Prompt entries to their ring slots.  Sequence b = blockIdx.y; its CTAs
+// share the vectors f = (slot * Hkv + h) * nvec + q of the slots that a
+// prompt of n tokens leaves filled.  Slot s holds position s below the sinks
+// and the newest position on it above, so every slot is written once, and a
+// token's heads are read as one contiguous run.
+__global__ void __launch_bounds__(KV_THREADS) sv_kv_fill_copy(const FillParams K) {
+  const int b = int(blockIdx.y);
+  const long long lo = __ldg(K.cu + b), hi = __ldg(K.cu + b + 1);
+  if (lo < 0 || hi < lo || hi > K.T) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) set_status(K.status, SV_ST_BAD_LENGTH);
+    return;
+  }
+  const int n = int(hi - lo);
+  if (blockIdx.x == 0 && threadIdx.x == 0) K.pos[b] = n;
+  const long long C = (long long)K.sink + K.window;
+  const int filled = n < C ? n : int(C);
+  const int total = filled * K.Hkv * K.nvec;  // <= 2^30, checked on the host
+  const int stride = int(gridDim.x) * KV_THREADS;  // KV_UNROLL strides cover every total
+  const int f0 = int(blockIdx.x) * KV_THREADS + int(threadIdx.x);
+  uint4 kv[KV_UNROLL], vv[KV_UNROLL];
+  size_t dst[KV_UNROLL];
+#pragma unroll
+  for (int u = 0; u < KV_UNROLL; ++u) {
+    const int f = f0 + u * stride;
+    if (f >= total) break;
+    const int row = div_by(f, K.m_nvec), q = f - row * K.nvec;
+    const int slot = row / K.Hkv, h = row - slot * K.Hkv;
+    int p = slot;
+    if (slot >= K.sink) p += (n - 1 - slot) / K.window * K.window;
+    const size_t src = (size_t(lo + p) * K.Hkv + h) * K.nvec + q;
+    dst[u] = ((size_t(b) * K.LH + K.head0 + h) * size_t(C) + slot) * K.nvec + q;
+    kv[u] = __ldg(K.k + src);
+    vv[u] = __ldg(K.v + src);
+  }
+#pragma unroll
+  for (int u = 0; u < KV_UNROLL; ++u) {
+    if (f0 + u * stride >= total) break;
+    K.k_pool[dst[u]] = kv[u];
+    K.v_pool[dst[u]] = vv[u];
+  }
+}
+
+constexpr int PC_ROWS = 16;     // layer/head rows per CTA
+constexpr int PC_ENTRIES = 64;  // path entries per CTA
+
+struct PageParams {
+  uint4* k_pages;
+  uint4* v_pages;
+  const uint4* k_new;
+  const uint4* v_new;
+  const int32_t* table;
+  const int32_t* seq_lens;
+  const int32_t* nodes;
+  const int32_t* num_accepted;
+  int32_t* out_seq_lens;
+  int32_t* status;
+  int B, LH, N, nvec, num_pages, page, cols;
+  unsigned long long m_nvec;
+};
+
+// The status bits of request b's commit of k + 1 entries at `len`, agreed on by
+// the whole CTA (every CTA of the request finds the same).
+__device__ int page_commit_faults(const PageParams& K, int b, int k, long long len) {
+  int bad = 0;
+  if (k >= K.N || len < 0 || len + k + 1 > (long long)K.cols * K.page ||
+      len + k + 1 > 0x7fffffffLL) {
+    bad = SV_ST_BAD_LENGTH;
+  } else {
+    if (K.nodes)
+      for (int j = int(threadIdx.x); j < k; j += KV_THREADS) {
+        const int n = __ldg(K.nodes + size_t(b) * K.N + j);
+        if (n < 0 || n >= K.N) bad |= SV_ST_BAD_TOKEN;
+      }
+    const int c0 = int(len / K.page), c1 = int((len + k) / K.page);
+    for (int c = c0 + int(threadIdx.x); c <= c1; c += KV_THREADS) {
+      const int pg = __ldg(K.table + size_t(b) * K.cols + c);
+      if (pg < 0 || pg >= K.num_pages) bad |= SV_ST_BAD_PAGE;
+    }
+  }
+  const int tok = __syncthreads_or(bad & SV_ST_BAD_TOKEN);
+  const int pg = __syncthreads_or(bad & SV_ST_BAD_PAGE);
+  return (bad & SV_ST_BAD_LENGTH) | (tok ? SV_ST_BAD_TOKEN : 0) | (pg ? SV_ST_BAD_PAGE : 0);
+}
+
+// Path entries into pages: PC_ROWS rows x PC_ENTRIES entries of request
+// blockIdx.y per CTA (entries blockIdx.z * PC_ENTRIES on), KV_UNROLL vectors of
+// K and of V per thread loaded before any is stored.  IN_PLACE: the lengths
+// are updated by the next kernel instead, after every CTA has read them.
+template <bool IN_PLACE>
+__global__ void __launch_bounds__(KV_THREADS) sv_page_copy(const PageParams K) {
+  __shared__ size_t dst_of[PC_ENTRIES];  // first row of the entry's page position
+  __shared__ int src_of[PC_ENTRIES];     // its staged entry
+  if (IN_PLACE) allow_next_kernel();
+  const int b = int(blockIdx.y);
+  const int k = __ldg(K.num_accepted + b);
+  const long long len = __ldg(K.seq_lens + b);
+  const int j0 = int(blockIdx.z) * PC_ENTRIES;
+  const bool writer = blockIdx.x == 0 && blockIdx.z == 0;
+  if (!writer && j0 > k) return;
+  const int bad = k < 0 ? 0 : page_commit_faults(K, b, k, len);
+  if (writer && threadIdx.x == 0 && !IN_PLACE) {
+    K.out_seq_lens[b] = int32_t(k < 0 || bad ? len : len + k + 1);
+    set_status(K.status, bad);
+  }
+  if (k < 0 || bad) return;
+  const int cnt = min(PC_ENTRIES, k + 1 - j0);
+  if (int(threadIdx.x) < cnt) {
+    const int j = j0 + int(threadIdx.x);
+    const long long at = len + j;
+    const int pg = __ldg(K.table + size_t(b) * K.cols + at / K.page);
+    dst_of[threadIdx.x] = size_t(pg) * K.LH * K.page + size_t(at % K.page);
+    src_of[threadIdx.x] = K.nodes && j > 0 ? __ldg(K.nodes + size_t(b) * K.N + j - 1) : j;
+  }
+  __syncthreads();
+  const int r0 = int(blockIdx.x) * PC_ROWS, rows = min(PC_ROWS, K.LH - r0);
+  const int total = cnt * PC_ROWS * K.nvec;  // <= 64 * 16 * 512
+  for (int f0 = int(threadIdx.x); f0 < total; f0 += KV_THREADS * KV_UNROLL) {
+    uint4 kv[KV_UNROLL], vv[KV_UNROLL];
+    size_t dst[KV_UNROLL];
+    bool use[KV_UNROLL];
+#pragma unroll
+    for (int u = 0; u < KV_UNROLL; ++u) {
+      const int f = f0 + u * KV_THREADS;
+      const int row = div_by(f, K.m_nvec), q = f - row * K.nvec;
+      const int r = row % PC_ROWS, j = row / PC_ROWS;
+      use[u] = f < total && r < rows;
+      dst[u] = 0;
+      if (use[u]) {
+        const size_t src = ((size_t(b) * K.LH + r0 + r) * K.N + src_of[j]) * K.nvec + q;
+        dst[u] = (dst_of[j] + size_t(r0 + r) * K.page) * K.nvec + q;
+        kv[u] = __ldg(K.k_new + src);
+        vv[u] = __ldg(K.v_new + src);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < KV_UNROLL; ++u) {
+      if (use[u]) {
+        K.k_pages[dst[u]] = kv[u];
+        K.v_pages[dst[u]] = vv[u];
+      }
+    }
+  }
+}
+
+// Lengths updated in place after the copy: one CTA per request, as its CTAs
+// of the copy judged it.
+__global__ void __launch_bounds__(KV_THREADS) sv_page_advance(const PageParams K) {
+  const int b = int(blockIdx.x);
+  wait_previous_kernel();
+  const int k = __ldg(K.num_accepted + b);
+  const long long len = K.seq_lens[b];
+  if (k < 0) return;
+  const int bad = page_commit_faults(K, b, k, len);
+  if (threadIdx.x != 0) return;
+  if (bad) set_status(K.status, bad);
+  else K.out_seq_lens[b] = int32_t(len + k + 1);
 }
 
 // Valid slots of request blockIdx.y, entries j = blockIdx.x * MAP_THREADS + tid.
@@ -252,6 +425,98 @@ int sv_kv_commit(void* k_pool, void* v_pool, const void* k_new, const void* v_ne
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, sv_kv_advance, K) != cudaSuccess) return SV_ERR_CUDA;
   return SV_OK;
+}
+
+int sv_kv_fill(const void* k, const void* v, const int32_t* cu_seqlens, void* k_pool,
+               void* v_pool, int32_t* pos, int B, int T, int Hkv, int LH, int head0,
+               int row_bytes, int sink, int window, int32_t* dev_status, void* stream) {
+  if (B < 0 || B > 65535 || T < 0 || Hkv < 1 || LH < 1 || head0 < 0 || head0 > LH - Hkv ||
+      row_bytes < 16 || (row_bytes % 16) != 0 || row_bytes / 16 > KV_MAX_NVEC || sink < 0 ||
+      window < 1 || (long long)sink + window > 0x7fffffffLL)
+    return SV_ERR_INVALID_ARG;
+  if (B == 0) return SV_OK;
+  if (!cu_seqlens || !k_pool || !v_pool || !pos || (T > 0 && (!k || !v)))
+    return SV_ERR_INVALID_ARG;
+  if (misaligned(k_pool, 16) || misaligned(v_pool, 16) || misaligned(k, 16) ||
+      misaligned(v, 16) || misaligned(cu_seqlens, 4) || misaligned(pos, 4) ||
+      (dev_status && misaligned(dev_status, 4)))
+    return SV_ERR_INVALID_ARG;
+  const long long C = (long long)sink + window;
+  const long long slots = T < C ? T : C;
+  const int nvec = row_bytes / 16;
+  if (slots * Hkv > (1LL << 30) / nvec) return SV_ERR_INVALID_ARG;  // int indexing inside
+  const long long most = slots * Hkv * nvec;
+  FillParams K;
+  K.k = static_cast<const uint4*>(k);
+  K.v = static_cast<const uint4*>(v);
+  K.cu = cu_seqlens;
+  K.k_pool = static_cast<uint4*>(k_pool);
+  K.v_pool = static_cast<uint4*>(v_pool);
+  K.pos = pos;
+  K.status = dev_status;
+  K.T = T; K.Hkv = Hkv; K.LH = LH; K.head0 = head0; K.nvec = nvec;
+  K.sink = sink; K.window = window;
+  K.m_nvec = div_magic(nvec);
+  const long long per_cta = (long long)KV_THREADS * KV_UNROLL;
+  const unsigned gx = unsigned(most > per_cta ? (most + per_cta - 1) / per_cta : 1);
+  sv_kv_fill_copy<<<dim3(gx, unsigned(B)), KV_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(K);
+  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+int sv_page_commit(void* k_pages, void* v_pages, const void* k_new, const void* v_new,
+                   const int32_t* block_table, const int32_t* seq_lens, const int32_t* nodes,
+                   const int32_t* num_accepted, int B, int LH, int N, int row_bytes,
+                   int num_pages, int page_size, int cols, int32_t* out_seq_lens,
+                   int32_t* dev_status, void* stream) {
+  if (B < 0 || B > 65535 || LH < 1 || N < 1 || N > (1 << 20) || row_bytes < 16 ||
+      (row_bytes % 16) != 0 || row_bytes / 16 > KV_MAX_NVEC || num_pages < 1 || page_size < 1 ||
+      cols < 1)
+    return SV_ERR_INVALID_ARG;
+  if (B == 0) return SV_OK;
+  if (!k_pages || !v_pages || !k_new || !v_new || !block_table || !seq_lens || !num_accepted ||
+      !out_seq_lens)
+    return SV_ERR_INVALID_ARG;
+  if (misaligned(k_pages, 16) || misaligned(v_pages, 16) || misaligned(k_new, 16) ||
+      misaligned(v_new, 16) || misaligned(block_table, 4) || misaligned(seq_lens, 4) ||
+      misaligned(nodes, 4) || misaligned(num_accepted, 4) || misaligned(out_seq_lens, 4) ||
+      (dev_status && misaligned(dev_status, 4)))
+    return SV_ERR_INVALID_ARG;
+  const bool in_place = out_seq_lens == seq_lens;
+  if (!in_place && out_seq_lens < seq_lens + B && seq_lens < out_seq_lens + B)
+    return SV_ERR_INVALID_ARG;  // shifted against each other: neither in place nor apart
+  const long long gx = ((long long)LH + PC_ROWS - 1) / PC_ROWS;
+  PageParams K;
+  K.k_pages = static_cast<uint4*>(k_pages);
+  K.v_pages = static_cast<uint4*>(v_pages);
+  K.k_new = static_cast<const uint4*>(k_new);
+  K.v_new = static_cast<const uint4*>(v_new);
+  K.table = block_table;
+  K.seq_lens = seq_lens;
+  K.nodes = nodes;
+  K.num_accepted = num_accepted;
+  K.out_seq_lens = out_seq_lens;
+  K.status = dev_status;
+  K.B = B; K.LH = LH; K.N = N; K.nvec = row_bytes / 16;
+  K.num_pages = num_pages; K.page = page_size; K.cols = cols;
+  K.m_nvec = div_magic(K.nvec);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const dim3 grid(unsigned(gx), unsigned(B), unsigned((N + PC_ENTRIES - 1) / PC_ENTRIES));
+  if (!in_place) {
+    sv_page_copy<false><<<grid, KV_THREADS, 0, st>>>(K);
+    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  }
+  sv_page_copy<true><<<grid, KV_THREADS, 0, st>>>(K);
+  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(B));
+  cfg.blockDim = dim3(KV_THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sv_page_advance, K) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 int sv_kv_valid_slots(const int32_t* pos, int B, int sink, int window, int32_t* out_slots,
