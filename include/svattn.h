@@ -66,7 +66,7 @@ size_t sv_attn_workspace_bytes(int N, int Hq, int Hkv, int D);
  *   k_pages, v_pages [num_pages][LH][page_size][D]  (LH = layers * kv heads)
  *   block_table    [B][cols] int32: position t is in page
  *                  block_table[b][t / page_size], row t mod page_size
- *   seq_lens       [B] int32, in [0, cols * page_size]
+ *   seq_lens       [B] int32, in [0, cols * page_size], at most 2^31 - 1024
  *   k_new, v_new   [B][LH][N][D]: the tree's own entries
  * The call attends for one layer: rows head0 .. head0 + Hkv - 1 of LH.
  * Requires page_size a multiple of 8 in [8, 65536], 1 <= N <= 256,
@@ -93,8 +93,8 @@ int sv_tree_attn(int dtype, const void* q, const void* k_pages, const void* v_pa
  *   k_pool, v_pool [B][LH][sink + window][D]
  *   k_new, v_new   [B][LH][R][D]: the staged entries (as sv_kv_commit takes them)
  *   pos            [B] int32: committed positions; the cache is only read
- * Requires 1 <= R <= 64, window >= R, sink >= 0, B * LH < 2^31 and
- * 0 <= head0, head0 + Hkv <= LH; B <= 65535.
+ * Requires 1 <= R <= 64, window >= R, sink >= 0, sink + window <= 2^31 - 1024,
+ * B * LH < 2^31, 0 <= head0, head0 + Hkv <= LH and B <= 65535.
  * A position outside [0, 2^31 - R) gives zeros and SV_ST_BAD_LENGTH.
  */
 int sv_ring_attn(int dtype, const void* q, const void* k_pool, const void* v_pool,

@@ -635,6 +635,17 @@ def test_same_bits_every_time():
         assert torch.equal(first, again)
 
 
+def test_long_runs():
+    """Batches large enough that every SM walks tens of key tiles of several items: right, and the same bits again."""
+    r = ring_inputs(74, 32, 8, 32, 8, 128, 4, 2048, [(911 * i + 100) % 9000 for i in range(32)], BF)
+    c = tree_inputs(75, 48, 12, 32, 8, 128, 64, [(677 * i + 30) % 3500 for i in range(48)], BF)
+    d = tree_inputs(76, 24, 70, 16, 4, 64, 32, [(677 * i + 30) % 3500 for i in range(24)], HF)
+    for check, call, x in ((ring_check, ring_call, r), (tree_check, tree_call, c), (tree_check, tree_call, d)):
+        first = check(x)
+        for _ in range(4):
+            assert torch.equal(first, call(x)[0])
+
+
 def test_other_stream_and_graph():
     """Calls on a side stream, and captured ones replayed on new data, two graphs sharing a workspace in turn."""
     c = tree_inputs(71, 3, 9, 8, 2, 64, 16, [300, 100, 1200], HF)
