@@ -21,7 +21,11 @@ constexpr int MAX_D = 128;
 constexpr int MAX_KEYS = 0x7fffffff - 1023;  // cache entries: a tile more fits an int
 
 constexpr int TILE = 128;       // query rows of a tile, and keys of a tile
-constexpr int THREADS = 320;    // two softmax warpgroups, a copy warp, a product warp
+constexpr int THREADS = 384;    // two softmax warpgroups, and one with a copy and a product warp
+// Registers: launched with 168 a thread (64512 a CTA); the softmax warpgroups
+// hold a row of scores each thread and take over what the third does not need.
+constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
+static_assert(256 * SOFTMAX_REGS + 128 * OTHER_REGS <= THREADS * 168, "register split");
 constexpr int COPY_WARP = 8, MMA_WARP = 9;
 constexpr int MAX_CTAS = 152;   // one per SM
 constexpr unsigned long long WAIT_LIMIT_NS = 1000000000ull;
@@ -84,8 +88,9 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, unsigned parity) {
 }
 // Bounded wait for a phase: false once the CTA gave up, or after one second,
 // which reports SV_ST_TIMEOUT and makes the CTA's other waits give up too.
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, unsigned parity, int32_t* status,
-                                            volatile int* abort) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, unsigned parity, int32_t* status,
+                                          volatile int* abort) {
+  if (mbar_try(bar, parity)) return true;
   const unsigned long long t0 = globaltimer();
   for (;;) {
     if (mbar_try(bar, parity)) return true;
@@ -97,11 +102,6 @@ __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, unsigned parity, int32
     }
   }
 }
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, unsigned parity, int32_t* status,
-                                          volatile int* abort) {
-  return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, status, abort);
-}
-
 // The same by a whole warp, all lanes of which get one answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, unsigned parity, int32_t* status,
                                           volatile int* abort) {
@@ -134,13 +134,15 @@ __device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {
          (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 // MN-major operand (values: the 64 dimensions of a block are contiguous):
-// 8-key groups 1024 bytes apart, 64-dimension blocks 16384.
-__device__ __forceinline__ uint64_t desc_cols(uint32_t addr) {
-  return uint64_t((addr >> 4) & 0x3fff) | (uint64_t(16384 >> 4) << 16) |
+// 8-key groups 1024 bytes apart, 64-dimension blocks `blocks` bytes.  (0: a
+// head of at most 64 dimensions taken twice to make up the 128 rows of V^T;
+// the second half of O^T is not read.)
+__device__ __forceinline__ uint64_t desc_cols(uint32_t addr, uint32_t blocks) {
+  return uint64_t((addr >> 4) & 0x3fff) | (uint64_t(blocks >> 4) << 16) |
          (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
-__device__ __forceinline__ uint32_t instr_desc(int bf16, bool b_cols, int n) {
-  return (1u << 4) | (uint32_t(bf16) << 7) | (uint32_t(bf16) << 10) |
+__device__ __forceinline__ uint32_t instr_desc(int bf16, bool a_cols, bool b_cols, int n) {
+  return (1u << 4) | (uint32_t(bf16) << 7) | (uint32_t(bf16) << 10) | (a_cols ? 1u << 15 : 0u) |
          (b_cols ? 1u << 16 : 0u) | (uint32_t(n >> 3) << 17) | (uint32_t(TILE >> 4) << 24);
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -158,6 +160,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b),
       "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// One lane of the (converged) warp: the form in which the compiler knows that a
+// single thread issues, and keeps the products' descriptors in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile(
@@ -212,6 +221,54 @@ __device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t (&r)[32]) 
       "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tm_ld8(uint32_t addr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                      "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tm_st8(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                      "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                      "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                      "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                      "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+                      "r"(r[13]), "r"(r[14]), "r"(r[15])
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tm_ldn(uint32_t addr, uint32_t (&r)[N]) {
+  if constexpr (N == 8) tm_ld8(addr, r);
+  else if constexpr (N == 16) tm_ld16(addr, r);
+  else tm_ld32(addr, r);
+}
+template <int N>
+__device__ __forceinline__ void tm_stn(uint32_t addr, const uint32_t (&r)[N]) {
+  if constexpr (N == 8) tm_st8(addr, r);
+  else if constexpr (N == 16) tm_st16(addr, r);
+  else tm_st32(addr, r);
+}
+template <int N>
+__device__ __forceinline__ void tm_loadedn(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i])::"memory");
+}
+template <int N>
+__device__ __forceinline__ void tm_waitn(uint32_t (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  tm_loadedn<N>(r);
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -246,14 +303,16 @@ struct Seg {
   int b, h, mt, j0, n, nt;
   int len;    // cache entries (TREE, RING; 0 when bad), or tokens of the sequence
   int bad;    // SV_ST_BAD_LENGTH for a length outside its range
+  int pos;    // committed positions (RING)
   int start;  // first packed row (PROMPT)
   // PROMPT: tiles t = j below `near`, then lo + (j - near)
   int near, lo;
 };
 
 // Cache entries of request b (0 with `bad` set for a length out of range).
-__device__ __forceinline__ int cache_len(const AttnParams& A, int b, int& bad) {
+__device__ __forceinline__ int cache_len(const AttnParams& A, int b, int& bad, int& pos) {
   const long long n = __ldg(A.lens + b);
+  pos = int(n);
   if (A.kind == TREE) {
     bad = n < 0 || n > (long long)A.cols * A.page || n > MAX_KEYS ? SV_ST_BAD_LENGTH : 0;
     return bad ? 0 : int(n);
@@ -272,7 +331,7 @@ __device__ __forceinline__ int tiles_of(int n) { return (n + TILE - 1) / TILE; }
 template <bool PAIR>
 struct Cursor {
   // TREE, RING
-  int b, item, j, nt, len, bad;
+  int b, item, j, nt, len, bad, pos;
   long long left;
   // PROMPT: the 32 sequences from wb on, one per lane
   long long i, cum, incl;
@@ -282,7 +341,7 @@ struct Cursor {
     left = count;
     if (count <= 0) return;
     b = b0;
-    len = cache_len(A, b, bad);
+    len = cache_len(A, b, bad, pos);
     nt = tiles_of(len) + tiles_of(A.N);
     item = int(at / nt);
     j = int(at - (long long)item * nt);
@@ -321,7 +380,7 @@ struct Cursor {
         if (++item == A.MT * A.Hkv) {
           item = 0;
           ++b;
-          len = cache_len(A, b, bad);
+          len = cache_len(A, b, bad, pos);
           nt = tiles_of(len) + tiles_of(A.N);
         }
       }
@@ -333,6 +392,7 @@ struct Cursor {
       s.nt = nt;
       s.len = len;
       s.bad = bad;
+      s.pos = pos;
       j += s.n;
       left -= s.n;
       return true;
@@ -392,18 +452,40 @@ __device__ __forceinline__ uint32_t span(int a, int b, int k0) {
   return (0xffffffffu >> (32 - b)) & (0xffffffffu << a);
 }
 
-template <int DP>
+// The three layouts of an item's products, by the rows (tokens x query heads of
+// a KV head) that share its keys:
+//   NQ == 0, PAIR: more than 128 rows.  Two tiles of 128 rows; S = Q K^T has a
+//     row per TMEM lane, every key tile serves both.
+//   NQ == 0, !PAIR: 65 to 128 rows.  One such tile, in two streams.
+//   NQ > 0: at most NQ rows.  The products are turned over, S^T = K Q^T and
+//     O^T = V^T P^T, so that the lanes hold keys (dimensions) and the few rows
+//     are columns: every thread has work however few the rows are, and the
+//     products cost NQ / 128 of a full tile's.  (A ring batch of 32 rows per
+//     item took 104 us with a row per lane.)
+template <int DP, int NQ>
 struct Smem {
-  static constexpr int BYTES = TILE * DP * 2;            // a tile of queries, keys or values
-  static constexpr int STAGES = DP == 128 ? 5 : 12;
-  static constexpr int CTRL = (2 + STAGES) * BYTES;      // offset of the control part
+  static constexpr int BYTES = TILE * DP * 2;                    // a tile of keys or values
+  static constexpr int Q_BYTES = (NQ ? NQ : TILE) * DP * 2;      // a tile of queries
+  static constexpr int P_BYTES = NQ * TILE * 2;                  // weights of a stream (NQ > 0)
+  static constexpr int P_AT = 2 * Q_BYTES;
+  static constexpr int STAGE_AT = P_AT + 2 * P_BYTES;
+  static constexpr int FIT = (229376 - STAGE_AT) / BYTES;
+  static constexpr int STAGES = FIT < 12 ? FIT : 12;
+  static constexpr int CTRL = STAGE_AT + STAGES * BYTES;         // offset of the control part
   static constexpr int TOTAL = CTRL + 3072;
 };
 struct Ctrl {
   unsigned long long full[12], empty[12], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2],
       drain;
-  float2 ml[2][TILE];       // softmax state exchanged between the streams
-  uint8_t parent[2][MAX_N]; // one copy per softmax warpgroup
+  union {
+    float2 ml[2][TILE];  // NQ == 0: softmax state exchanged between the streams
+    struct {             // NQ > 0, per stream and column
+      unsigned long long sees[2][64];  // columns that see a staged entry
+      float mc[2][64];                 // the running maximum in base-2 units; +inf: none yet
+      float fac[2][64];                // rescaling, and at the end the streams' shares
+    } few;
+  };
+  uint8_t parent[2][MAX_N];  // one copy per softmax warpgroup
   long long scan[12];
   long long start_at;
   int start_b, abort;
@@ -417,17 +499,133 @@ constexpr int DESC_THROUGH = 1 << 29;  // and runs to the CTA's end without fini
 constexpr int DESC_OUT = 1 << 28;      // the last segment leaves its item unfinished
 constexpr int DESC_LAST1 = 1 << 27;    // the last segment's partials are in slot 1
 
+// Sums of the columns over a warp's 32 lanes: lane i gets column i's (i mod 16's
+// with 16 columns) in v[0], and column 32 + i's in v[32] with 64.
+template <int NQ>
+__device__ __forceinline__ void sum_columns(float* v, int lane) {
+  constexpr int SPAN = NQ < 32 ? NQ : 32;
+#pragma unroll
+  for (int c = 0; c < NQ; c += SPAN) {
+#pragma unroll
+    for (int x = SPAN / 2; x; x >>= 1) {
+      const bool up = lane & x;
+#pragma unroll
+      for (int i = 0; i < x; ++i) {
+        const float give = up ? v[c + i] : v[c + i + x], keep = up ? v[c + i + x] : v[c + i];
+        v[c + i] = keep + __shfl_xor_sync(0xffffffffu, give, x);
+      }
+    }
+    if (SPAN == 16) v[c] += __shfl_xor_sync(0xffffffffu, v[c], 16);
+  }
+}
+
+// One tile's softmax with keys on the lanes: thread `key` takes its key's
+// scores of all NQ columns (S^T, TMEM columns from ts), adds their weights to
+// lq and stores them, rounded, as column `key` of P (a K-major operand of two
+// 64-key blocks in the 128-byte swizzle).  `sees`: the columns that see the
+// key.  All keys of a tile use one maximum per column; it is raised, the sums
+// and O (columns from to) rescaled, when a score exceeds it by 2^RAISE_LOG2.
+template <int NQ>
+__device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl& C, int st, int key,
+                                            uint32_t ts, uint32_t to, unsigned long long sees,
+                                            bool masked, bool started, bool& unset, float* lq,
+                                            unsigned char* pbuf) {
+  constexpr int W = NQ < 32 ? NQ : 32;
+  const int lane = key & 31, warp = key >> 5;
+  float* const mc = C.few.mc[st];
+  uint32_t r[NQ / W][W];
+#pragma unroll
+  for (int x = 0; x < NQ / W; ++x) tm_ldn<W>(ts + x * W, r[x]);
+  tm_waitn<W>(r[0]);
+  if (NQ > W) tm_loadedn<W>(r[NQ / W - 1]);
+  if (masked) {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+      if (!(sees >> q & 1)) r[q / W][q % W] = 0xff800000u;
+  }
+  bool raise = !started || unset;
+  if (!raise) {
+    float over = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+      over = fmaxf(over, fmaf(__uint_as_float(r[q / W][q % W]), A.c, -mc[q]));
+    raise = group_or(1 + st, TILE, over > RAISE_LOG2);
+  }
+  if (raise) {
+    float* const wmax = reinterpret_cast<float*>(pbuf);  // [warp][NQ]; P is free until stored
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      float t;
+      asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;"
+                   : "=f"(t)
+                   : "f"(__uint_as_float(r[q / W][q % W])));
+      if (lane == (q & 31)) wmax[warp * NQ + q] = t;
+    }
+    group_sync(1 + st, TILE);
+    int none = 0;
+    if (key < NQ) {
+      const float t = fmaxf(fmaxf(wmax[key], wmax[NQ + key]),
+                            fmaxf(wmax[2 * NQ + key], wmax[3 * NQ + key])) * A.c;
+      float old = started ? mc[key] : INFINITY, f = 1.0f;
+      if (old == INFINITY) {
+        if (t > -INFINITY) old = t;
+      } else if (t - old > RAISE_LOG2) {
+        f = ex2(old - t);
+        old = t;
+      }
+      mc[key] = old;
+      C.few.fac[st][key] = f;
+      none = old == INFINITY;
+    }
+    unset = group_or(1 + st, TILE, none);
+    if (started) {
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) lq[q] *= C.few.fac[st][q];
+#pragma unroll
+      for (int x = 0; x < NQ / W; ++x) {
+        uint32_t o[W];
+        tm_ldn<W>(to + x * W, o);
+        tm_waitn<W>(o);
+#pragma unroll
+        for (int q = 0; q < W; ++q)
+          o[q] = __float_as_uint(__uint_as_float(o[q]) * C.few.fac[st][x * W + q]);
+        tm_stn<W>(to + x * W, o);
+      }
+      tm_wait_st();
+    }
+  }
+  // key k of row q: block k / 64, byte (k % 64) * 2 of the 128-byte row, its
+  // 16-byte piece exchanged with that of q % 8
+  unsigned char* const prow = pbuf + (key >> 6) * (NQ * 128) + (key & 7) * 2;
+  const int piece = (key & 63) >> 3;
+#pragma unroll
+  for (int q = 0; q < NQ; q += 2) {
+    const float p0 = ex2(fmaf(__uint_as_float(r[q / W][q % W]), A.c, -mc[q]));
+    const float p1 = ex2(fmaf(__uint_as_float(r[q / W][q % W + 1]), A.c, -mc[q + 1]));
+    lq[q] += p0;
+    lq[q + 1] += p1;
+    const uint32_t w = pack16(p0, p1, A.bf16);
+    *reinterpret_cast<uint16_t*>(prow + q * 128 + ((piece ^ (q & 7)) << 4)) = uint16_t(w);
+    *reinterpret_cast<uint16_t*>(prow + (q + 1) * 128 + ((piece ^ ((q + 1) & 7)) << 4)) =
+        uint16_t(w >> 16);
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // The attention kernel.  Per CTA one copy warp (tiles by TMA into a ring of
 // stages), one product warp (S = Q K^T and O += P V on the tensor cores, S, P
 // and O in TMEM) and two softmax warpgroups, one row of a 128-row tile per
 // thread: the running maximum and sum of the softmax live in the thread's
 // registers, P overwrites S in TMEM as 16-bit weights, and O is rescaled only
 // when the maximum has risen by 2^RAISE_LOG2.
-template <int DP, bool PAIR>
+template <int DP, int NQ, bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ AttnParams A) {
-  using SM = Smem<DP>;
+  static_assert(!(NQ && PAIR), "few rows make one tile");
+  using SM = Smem<DP, NQ>;
   constexpr int STAGES = SM::STAGES, BYTES = SM::BYTES, HALVES = DP / 64;
-  constexpr int ROWS = PAIR ? 2 * TILE : TILE;
+  constexpr int ROWS = NQ ? NQ : PAIR ? 2 * TILE : TILE;
+  constexpr int TM_COLS = NQ ? 256 : 512;               // TMEM: S of both streams, then O
+  constexpr int S_COLS = NQ ? 64 : 128, O_AT = TM_COLS / 2;
   extern __shared__ __align__(1024) unsigned char smem[];
   Ctrl& C = *reinterpret_cast<Ctrl*>(smem + SM::CTRL);
   const uint32_t base = smem_addr(smem);
@@ -455,10 +653,16 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   if (warp == MMA_WARP) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                     smem_addr(&C.tmem))
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(&C.tmem)),
+                 "n"(TM_COLS)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (NQ) {  // columns past the item's rows: finite, and never used
+    for (int i = tid; i < SM::P_AT / 16; i += THREADS)
+      reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   long long run = 0;  // tiles of this CTA (TREE, RING)
   if (A.kind != PROMPT) {
@@ -467,9 +671,9 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
     const int b0 = min(tid * per, A.B), b1 = min(b0 + per, A.B);
     const long long items = (long long)A.MT * A.Hkv;
     long long mine = 0;
-    int bad;
+    int bad, pos;
     for (int b = b0; b < b1; ++b)
-      mine += items * (tiles_of(cache_len(A, b, bad)) + tiles_of(A.N));
+      mine += items * (tiles_of(cache_len(A, b, bad, pos)) + tiles_of(A.N));
     long long incl = mine;
     for (int x = 1; x < 32; x <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, incl, x);
@@ -489,7 +693,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
     if (run > 0 && lo >= before && lo < before + mine) {
       long long at = before;
       for (int b = b0; b < b1; ++b) {
-        const long long t = items * (tiles_of(cache_len(A, b, bad)) + tiles_of(A.N));
+        const long long t = items * (tiles_of(cache_len(A, b, bad, pos)) + tiles_of(A.N));
         if (lo < at + t) {
           C.start_b = b;
           C.start_at = lo - at;
@@ -507,213 +711,14 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
   const long long start_at = C.start_at;
   volatile int* abort = &C.abort;
 
-  if (warp == COPY_WARP) {
-    // ------------------------------------------------------------ copies
-    Cursor<PAIR> cur;
-    cur.open(A, start_b, start_at, run, blockIdx.x == 0);
-    Seg s;
-    uint32_t idx = 0;   // copies issued (low bits: stage and phase)
-    int segs = 0;
-    bool ok = true;
-    auto tile = [&](const Seg& s, int jj, bool is_v) {
-      const uint32_t st = idx % STAGES, use = idx / STAGES;
-      const uint32_t fb = bar(&C.full[st]);
-      const uint32_t dst = base + (2 + st) * BYTES;
-      if (use > 0 && !warp_wait(bar(&C.empty[st]), (use - 1) & 1, A.status, abort)) return false;
-      const int j = s.j0 + jj;
-      if (A.kind == PROMPT) {
-        const int t = j < s.near ? j : s.lo + (j - s.near);
-        if (lane == 0) {
-          mbar_arrive_tx(fb, BYTES);
-          for (int x = 0; x < HALVES; ++x)
-            tma_3d(dst + x * 16384, is_v ? &A.mv : &A.mk, fb, x * 64, s.h, s.start + t * TILE);
-        }
-      } else {
-        const int ct = tiles_of(s.len);
-        if (j >= ct) {
-          if (lane == 0) {
-            mbar_arrive_tx(fb, BYTES);
-            for (int x = 0; x < HALVES; ++x)
-              tma_3d(dst + x * 16384, is_v ? &A.mvn : &A.mkn, fb, x * 64, (j - ct) * TILE,
-                     s.b * A.LH + A.head0 + s.h);
-          }
-        } else if (A.kind == RING) {
-          if (lane == 0) {
-            mbar_arrive_tx(fb, BYTES);
-            for (int x = 0; x < HALVES; ++x)
-              tma_3d(dst + x * 16384, is_v ? &A.mv : &A.mk, fb, x * 64, j * TILE,
-                     s.b * A.LH + A.head0 + s.h);
-          }
-        } else {
-          // one lane per box of page rows; a page outside the pool is read as
-          // page 0 (the softmax warps report it and drop the result)
-          const int boxes = min(TILE, s.len - j * TILE + A.box - 1) / A.box;
-          if (lane == 0) mbar_arrive_tx(fb, boxes * A.box * DP * 2);
-          __syncwarp();
-          if (lane < boxes) {
-            const int t = j * TILE + lane * A.box;
-            const int col = t / A.page;
-            int pg = __ldg(A.table + size_t(s.b) * A.cols + col);
-            if (pg < 0 || pg >= A.num_pages) pg = 0;
-            for (int x = 0; x < HALVES; ++x)
-              tma_4d(dst + x * 16384 + lane * A.box * 128, is_v ? &A.mv : &A.mk, fb, x * 64,
-                     t - col * A.page, A.head0 + s.h, pg);
-          }
-        }
-      }
-      __syncwarp();
-      ++idx;
-      return true;
-    };
-    while (ok && cur.next(A, s, blockIdx.x == 0)) {
-      const int slot = PAIR ? 0 : segs & 1;
-      const int use = PAIR ? segs : segs >> 1;
-      if (use > 0 && !warp_wait(bar(&C.q_empty[slot]), (use - 1) & 1, A.status, abort)) break;
-      if (lane == 0) {
-        const uint32_t fb = bar(&C.q_full[slot]);
-        mbar_arrive_tx(fb, (PAIR ? 2 : 1) * A.q_rows * DP * 2);
-        const int tok = A.kind == PROMPT ? s.start : s.b * A.N;
-        for (int q = 0; q < (PAIR ? 2 : 1); ++q)
-          for (int x = 0; x < HALVES; ++x)
-            tma_4d(base + (PAIR ? q : slot) * BYTES + x * 16384, &A.mq, fb, x * 64, 0, s.h,
-                   tok + (s.mt * (PAIR ? 2 : 1) + q) * A.tpt);
-      }
-      __syncwarp();
-      ++segs;
-      constexpr int LAG = PAIR ? 0 : 1;
-      for (int i = 0; ok && i < s.n + LAG; ++i) {
-        if (i < s.n) ok = tile(s, i, false);
-        if (ok && i >= LAG) ok = tile(s, i - LAG, true);
-      }
-    }
-    if (*abort) {  // the copies in flight land before the CTA ends
-      const unsigned long long t0 = globaltimer();
-      for (uint32_t u = idx > STAGES ? idx - STAGES : 0; u < idx; ++u)
-        while (!mbar_try(bar(&C.full[u % STAGES]), (u / STAGES) & 1) &&
-               globaltimer() - t0 < WAIT_LIMIT_NS) {
-        }
-      for (int u = max(0, segs - (PAIR ? 1 : 2)); u < segs; ++u)
-        while (!mbar_try(bar(&C.q_full[PAIR ? 0 : u & 1]), (PAIR ? u : u >> 1) & 1) &&
-               globaltimer() - t0 < WAIT_LIMIT_NS) {
-        }
-    }
-  } else if (warp == MMA_WARP) {
-    // ------------------------------------------------------------ products
-    Cursor<PAIR> cur;
-    cur.open(A, start_b, start_at, run);
-    Seg s;
-    uint32_t idx = 0;
-    int segs = 0;
-    unsigned p_use[2] = {0, 0};
-    const uint32_t id_s = instr_desc(A.bf16, false, TILE), id_o = instr_desc(A.bf16, true, DP);
-    bool ok = true;
-    auto full = [&](uint32_t u) {
-      if (!mbar_wait(bar(&C.full[u % STAGES]), (u / STAGES) & 1, A.status, abort)) return false;
-      tc_after();
-      return true;
-    };
-    auto scores = [&](int st, int q, uint32_t u) {  // S[st] = Q[q] K^T
-      const uint32_t qa = base + q * BYTES, ka = base + (2 + u % STAGES) * BYTES;
-#pragma unroll
-      for (int k = 0; k < DP / 16; ++k) {
-        const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
-        mma_ss(tmem + st * 128, desc_rows(qa + off), desc_rows(ka + off), id_s, k > 0);
-      }
-      mma_commit(bar(&C.s_full[st]));
-    };
-    auto values = [&](int st, uint32_t u, bool more) {  // O[st] (+)= P[st] V
-      const uint32_t va = base + (2 + u % STAGES) * BYTES;
-#pragma unroll
-      for (int k = 0; k < TILE / 16; ++k)
-        mma_ts(tmem + 256 + st * 128, tmem + st * 128 + k * 8, desc_cols(va + k * 2048), id_o,
-               more || k > 0);
-    };
-    while (ok && cur.next(A, s)) {
-      if (lane == 0) {
-        const int slot = PAIR ? 0 : segs & 1;
-        const int use = PAIR ? segs : segs >> 1;
-        ok = mbar_wait(bar(&C.q_full[slot]), use & 1, A.status, abort);
-        const int n = s.n;
-        const uint32_t u0 = idx;
-        if (PAIR) {
-          ok = ok && full(u0);
-          if (ok) {
-            scores(0, 0, u0);
-            scores(1, 1, u0);
-            mma_commit(bar(&C.empty[u0 % STAGES]));
-            if (n == 1) mma_commit(bar(&C.q_empty[0]));
-          }
-          for (int j = 0; ok && j < n; ++j) {
-            const uint32_t uv = u0 + v_order<true>(j, n), uk = u0 + k_order<true>(j + 1);
-            ok = full(uv);
-#pragma unroll
-            for (int st = 0; st < 2; ++st) {
-              if (!ok) break;
-              ok = mbar_wait(bar(&C.p_full[st]), p_use[st] & 1, A.status, abort);
-              ++p_use[st];
-              if (!ok) break;
-              tc_after();
-              values(st, uv, j > 0);
-              if (st == 1) mma_commit(bar(&C.empty[uv % STAGES]));
-              if (j + 1 < n) {
-                if (st == 0 && !(ok = full(uk))) break;
-                scores(st, st, uk);
-                if (st == 1) {
-                  mma_commit(bar(&C.empty[uk % STAGES]));
-                  if (j + 2 == n) mma_commit(bar(&C.q_empty[0]));
-                }
-              } else {
-                mma_commit(bar(&C.o_full[st]));
-              }
-            }
-          }
-        } else {
-          for (int j = 0; ok && j < 2 && j < n; ++j) {
-            const uint32_t uk = u0 + k_order<false>(j);
-            ok = full(uk);
-            if (!ok) break;
-            scores(j, slot, uk);
-            mma_commit(bar(&C.empty[uk % STAGES]));
-          }
-          if (ok && n <= 2) mma_commit(bar(&C.q_empty[slot]));
-          for (int j = 0; ok && j < n; ++j) {
-            const int st = j & 1;
-            const uint32_t uv = u0 + v_order<false>(j, n), uk = u0 + k_order<false>(j + 2);
-            ok = full(uv) && mbar_wait(bar(&C.p_full[st]), p_use[st] & 1, A.status, abort);
-            ++p_use[st];
-            if (!ok) break;
-            tc_after();
-            values(st, uv, j >= 2);
-            mma_commit(bar(&C.empty[uv % STAGES]));
-            if (j + 2 < n) {
-              if (!(ok = full(uk))) break;
-              scores(st, slot, uk);
-              mma_commit(bar(&C.empty[uk % STAGES]));
-              if (j + 3 == n) mma_commit(bar(&C.q_empty[slot]));
-            } else {
-              mma_commit(bar(&C.o_full[st]));
-            }
-          }
-        }
-      }
-      idx += 2 * s.n;
-      ++segs;
-      ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
-    }
-    if (!ok && lane == 0) {  // the products in flight end before TMEM is freed
-      mma_commit(bar(&C.drain));
-      const unsigned long long t0 = globaltimer();
-      while (!mbar_try(bar(&C.drain), 0) && globaltimer() - t0 < WAIT_LIMIT_NS) {
-      }
-    }
-    __syncwarp();
-  } else {
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
     // ------------------------------------------------------------ softmax
     const int st = warp >> 2;             // the stream of this warpgroup
     const int row = tid & (TILE - 1);     // query row of the tile, and key of a value tile
     const int rt = row / A.G, rg = row - rt * A.G;
     const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's TMEM lanes
-    const uint32_t ts = tmem + lanes + st * 128, to = tmem + lanes + 256 + st * 128;
+    const uint32_t ts = tmem + lanes + st * S_COLS, to = tmem + lanes + O_AT + st * S_COLS;
     Cursor<PAIR> cur;
     cur.open(A, start_b, start_at, run);
     Seg s;
@@ -741,6 +746,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
             pages_bad |= pg < 0 || pg >= A.num_pages;
           }
         if (A.parent && s.b != parent_b && s.j0 + n > ct) {
+          if (NQ && row < 64) C.few.sees[st][row] = 0;
           int wrong = 0;
           for (int i = row; i < A.N; i += TILE) {
             const int p = __ldg(A.parent + size_t(s.b) * A.N + i);
@@ -750,22 +756,31 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           }
           parent_bad = group_or(1 + st, TILE, wrong) ? SV_ST_BAD_TOKEN : 0;
           parent_b = s.b;
+          if (NQ) {  // column `row` sees its token and those above it
+            if (row < A.N * A.G)
+              for (int i = row / A.G;; i = C.parent[st][i]) {
+                atomicOr(&C.few.sees[st][i], 1ull << row);
+                if (i == 0) break;
+              }
+            group_sync(1 + st, TILE);
+          }
         }
         if (group_or(1 + st, TILE, pages_bad)) bad |= SV_ST_BAD_PAGE;
         if (s.j0 + n > ct && A.parent) bad |= parent_bad;
       }
       if (bad && tid == 0) set_status(A.status, bad);
       // RING: the ring slot after the newest entry holds the oldest
-      int ring_at = -1, pos = 0;
-      if (A.kind == RING && !s.bad) {
-        pos = __ldg(A.lens + s.b);
-        if (pos > A.sink) ring_at = (pos - A.sink) % A.window;
-      }
-      const bool ring_full = ring_at >= 0 && pos - A.sink >= A.window;
+      int ring_at = -1;
+      if (A.kind == RING && !s.bad && s.pos > A.sink) ring_at = (s.pos - A.sink) % A.window;
+      const bool ring_full = ring_at >= 0 && s.pos - A.sink >= A.window;
       const int q0 = s.mt * tpi, q1 = min(q0 + tpi, tokens) - 1;  // the item's tokens
       const int w0 = q0 + (PAIR ? st * A.tpt : 0), w1 = min(w0 + A.tpt, tokens) - 1;  // the tile's
 
       float m = -INFINITY, l = 0.0f;
+      float lq[NQ ? NQ : 1];  // NQ > 0: this key's share of the columns' sums
+      bool unset = true;      // NQ > 0: a column has seen nothing yet
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) lq[q] = 0.0f;
       int done = 0;
       for (int jj = PAIR ? 0 : st; jj < n; jj += PAIR ? 1 : 2, ++done) {
         const int j = s.j0 + jj;
@@ -806,7 +821,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
             break;
           }
           if (dead) {
-            uint4* v = reinterpret_cast<uint4*>(smem + (2 + u % STAGES) * BYTES + row * 128);
+            uint4* v = reinterpret_cast<uint4*>(smem + SM::STAGE_AT + (u % STAGES) * BYTES + row * 128);
 #pragma unroll
             for (int x = 0; x < HALVES; ++x)
 #pragma unroll
@@ -814,7 +829,28 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        if (warp_active) {
+        if constexpr (NQ > 0) {
+          // one key per thread, all rows
+          unsigned long long sees = ~0ull;
+          if (masked) {
+            const int k = k0 + row;
+            if (j < ct) {
+              if (k >= s.len) {
+                sees = 0;
+              } else if (ring_at >= 0 && k >= A.sink) {
+                int v = k - A.sink - ring_at;  // tokens that still have the slot in their window
+                if (v < 0) v += A.window;
+                if (v < A.N) sees = (1ull << (v * A.G)) - 1;
+              }
+            } else if (k >= A.N) {
+              sees = 0;
+            } else {
+              sees = A.parent ? C.few.sees[st][k] : ~0ull << (k * A.G);
+            }
+          }
+          softmax_few<NQ>(A, C, st, row, ts, to, sees, masked, done > 0, unset, lq,
+                          smem + SM::P_AT + st * SM::P_BYTES);
+        } else if (warp_active) {
           uint32_t r[4][32];
 #pragma unroll
           for (int x = 0; x < 4; ++x) tm_ld32(ts + x * 32, r[x]);
@@ -886,18 +922,17 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           const float mc = m == -INFINITY ? 0.0f : m * A.c;
           float sum[4] = {0, 0, 0, 0};
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint32_t w[32];
+          for (int x = 0; x < 4; ++x) {
+            uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int y = x * 64 + 2 * i;
-              const float p0 = ex2(fmaf(__uint_as_float(r[y >> 5][y & 31]), A.c, -mc));
-              const float p1 = ex2(fmaf(__uint_as_float(r[y >> 5][(y & 31) + 1]), A.c, -mc));
+            for (int i = 0; i < 16; ++i) {
+              const float p0 = ex2(fmaf(__uint_as_float(r[x][2 * i]), A.c, -mc));
+              const float p1 = ex2(fmaf(__uint_as_float(r[x][2 * i + 1]), A.c, -mc));
               sum[(2 * i) & 3] += p0;
               sum[(2 * i + 1) & 3] += p1;
               w[i] = pack16(p0, p1, A.bf16);
             }
-            tm_st32(ts + x * 32, w);
+            tm_st16(ts + x * 16, w);
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tm_wait_st();
@@ -935,7 +970,72 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
                 make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
       };
-      if (PAIR) {
+      if constexpr (NQ > 0) {
+        for (int x = 0; x < 2; ++x) {
+          if (x >= n) break;
+          ok = ok && warp_wait(bar(&C.o_full[x]), o_use[x] & 1, A.status, abort);
+          ++o_use[x];
+        }
+        tc_after();
+        // sums over the keys: 32 lanes here, the four warps and two streams below
+        float* const sums = reinterpret_cast<float*>(smem + SM::P_AT);  // [stream][warp][NQ]
+        sum_columns<NQ>(lq, lane);
+        if (lane < NQ) {
+          sums[(st * 4 + (warp & 3)) * NQ + lane] = lq[0];
+          if (NQ == 64) sums[(st * 4 + (warp & 3)) * NQ + 32 + lane] = lq[NQ / 2];
+        }
+        group_sync(3, 2 * TILE);
+        if (tid < NQ) {
+          float l0 = 0.0f, l1 = 0.0f;
+          for (int w = 0; w < 4; ++w) {
+            l0 += sums[w * NQ + tid];
+            l1 += sums[(4 + w) * NQ + tid];
+          }
+          float a = C.few.mc[0][tid], b = n > 1 ? C.few.mc[1][tid] : INFINITY;
+          if (a == INFINITY) a = -INFINITY;  // nothing seen
+          if (b == INFINITY) b = -INFINITY;
+          const float mm = fmaxf(a, b), mu = mm == -INFINITY ? 0.0f : mm;
+          float f0 = ex2(a - mu), f1 = ex2(b - mu);
+          const float ll = l0 * f0 + (n > 1 ? l1 * f1 : 0.0f);
+          if (whole) {
+            f0 /= ll;
+            f1 /= ll;
+          }
+          C.few.fac[0][tid] = f0;
+          C.few.fac[1][tid] = f1;
+          if (!whole)
+            A.part_ml[(size_t(blockIdx.x) * 2 + slot) * NQ + tid] =
+                make_float2(mm, bad ? -1.0f : ll);
+        }
+        group_sync(3, 2 * TILE);
+        if (ok) {
+          constexpr int HALF = NQ / 2;  // columns of this warpgroup
+          const int q0 = st * HALF;
+          uint32_t o0[HALF], o1[HALF];
+          tm_ldn<HALF>(tmem + lanes + O_AT + q0, o0);
+          if (n > 1) tm_ldn<HALF>(tmem + lanes + O_AT + S_COLS + q0, o1);
+          tm_waitn<HALF>(o0);
+          if (n > 1) tm_loadedn<HALF>(o1);
+          int t = q0 / A.G, g = q0 - t * A.G;
+#pragma unroll
+          for (int q = 0; q < HALF; ++q) {
+            float v = __uint_as_float(o0[q]) * C.few.fac[0][q0 + q];
+            if (n > 1) v = fmaf(__uint_as_float(o1[q]), C.few.fac[1][q0 + q], v);
+            if (whole) {
+              if (row < A.D && t < A.N)
+                A.out[((size_t(s.b) * A.N + t) * A.Hq + s.h * A.G + g) * A.D + row] =
+                    bad ? 0 : uint16_t(pack16(v, 0.0f, A.bf16));
+            } else if (row < DP) {
+              A.part_o[((size_t(blockIdx.x) * 2 + slot) * NQ + q0 + q) * DP + row] = v;
+            }
+            if (++g == A.G) {
+              g = 0;
+              ++t;
+            }
+          }
+        }
+        tc_before();
+      } else if (PAIR) {
         ok = ok && warp_wait(bar(&C.o_full[st]), o_use[st] & 1, A.status, abort);
         ++o_use[st];
         tc_after();
@@ -951,7 +1051,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * f;
             put(v, x * 32);
           }
-          if (!whole && active) A.part_ml[part] = make_float2(m, bad ? -1.0f : l);
+          if (!whole && active) A.part_ml[part] = make_float2(m * A.c, bad ? -1.0f : l);
         }
         tc_before();
       } else {
@@ -974,7 +1074,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
             f0 /= ll;
             f1 /= ll;
           }
-          const uint32_t t0 = tmem + lanes + 256;
+          const uint32_t t0 = tmem + lanes + O_AT;
 #pragma unroll
           for (int x = 0; x < DP / 64; ++x) {
             const int col = st * (DP / 2) + x * 32;
@@ -985,14 +1085,14 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * f0;
             if (n > 1) {
-              tm_ld32(t0 + 128 + col, o);
+              tm_ld32(t0 + S_COLS + col, o);
               tm_wait_ld(o);
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(o[i]), f1, v[i]);
             }
             put(v, col);
           }
-          if (!whole && st == 0 && active) A.part_ml[part] = make_float2(mm, bad ? -1.0f : ll);
+          if (!whole && st == 0 && active) A.part_ml[part] = make_float2(mm * A.c, bad ? -1.0f : ll);
         }
         tc_before();
       }
@@ -1013,25 +1113,249 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       tc_after();
     }
     if (A.kind != PROMPT && tid == 0) A.desc[blockIdx.x] = make_int4(d_flags, d_item, d_b, 0);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
+  if (warp == COPY_WARP) {
+    // ------------------------------------------------------------ copies
+    Cursor<PAIR> cur;
+    cur.open(A, start_b, start_at, run, blockIdx.x == 0);
+    Seg s;
+    uint32_t idx = 0;   // copies issued (low bits: stage and phase)
+    int segs = 0;
+    bool ok = true;
+    auto tile = [&](const Seg& s, int jj, bool is_v) {
+      const uint32_t st = idx % STAGES, use = idx / STAGES;
+      const uint32_t fb = bar(&C.full[st]);
+      const uint32_t dst = base + SM::STAGE_AT + st * BYTES;
+      if (use > 0 && !warp_wait(bar(&C.empty[st]), (use - 1) & 1, A.status, abort)) return false;
+      const int j = s.j0 + jj;
+      if (A.kind == PROMPT) {
+        const int t = j < s.near ? j : s.lo + (j - s.near);
+        if (elect_one()) {
+          mbar_arrive_tx(fb, BYTES);
+          for (int x = 0; x < HALVES; ++x)
+            tma_3d(dst + x * 16384, is_v ? &A.mv : &A.mk, fb, x * 64, s.h, s.start + t * TILE);
+        }
+      } else {
+        const int ct = tiles_of(s.len);
+        if (j >= ct) {
+          if (elect_one()) {
+            mbar_arrive_tx(fb, BYTES);
+            for (int x = 0; x < HALVES; ++x)
+              tma_3d(dst + x * 16384, is_v ? &A.mvn : &A.mkn, fb, x * 64, (j - ct) * TILE,
+                     s.b * A.LH + A.head0 + s.h);
+          }
+        } else if (A.kind == RING) {
+          if (elect_one()) {
+            mbar_arrive_tx(fb, BYTES);
+            for (int x = 0; x < HALVES; ++x)
+              tma_3d(dst + x * 16384, is_v ? &A.mv : &A.mk, fb, x * 64, j * TILE,
+                     s.b * A.LH + A.head0 + s.h);
+          }
+        } else {
+          // one lane per box of page rows; a page outside the pool is read as
+          // page 0 (the softmax warps report it and drop the result)
+          const int boxes = min(TILE, s.len - j * TILE + A.box - 1) / A.box;
+          if (lane == 0) mbar_arrive_tx(fb, boxes * A.box * DP * 2);
+          __syncwarp();
+          if (lane < boxes) {
+            const int t = j * TILE + lane * A.box;
+            const int col = t / A.page;
+            int pg = __ldg(A.table + size_t(s.b) * A.cols + col);
+            if (pg < 0 || pg >= A.num_pages) pg = 0;
+            for (int x = 0; x < HALVES; ++x)
+              tma_4d(dst + x * 16384 + lane * A.box * 128, is_v ? &A.mv : &A.mk, fb, x * 64,
+                     t - col * A.page, A.head0 + s.h, pg);
+          }
+        }
+      }
+      __syncwarp();
+      ++idx;
+      return true;
+    };
+    while (ok && cur.next(A, s, blockIdx.x == 0)) {
+      const int slot = PAIR ? 0 : segs & 1;
+      const int use = PAIR ? segs : segs >> 1;
+      if (use > 0 && !warp_wait(bar(&C.q_empty[slot]), (use - 1) & 1, A.status, abort)) break;
+      if (elect_one()) {
+        const uint32_t fb = bar(&C.q_full[slot]);
+        mbar_arrive_tx(fb, (PAIR ? 2 : 1) * A.q_rows * DP * 2);
+        const int tok = A.kind == PROMPT ? s.start : s.b * A.N;
+        for (int q = 0; q < (PAIR ? 2 : 1); ++q)
+          for (int x = 0; x < HALVES; ++x)
+            tma_4d(base + (PAIR ? q : slot) * SM::Q_BYTES + x * (SM::Q_BYTES / HALVES), &A.mq, fb, x * 64, 0, s.h,
+                   tok + (s.mt * (PAIR ? 2 : 1) + q) * A.tpt);
+      }
+      __syncwarp();
+      ++segs;
+      constexpr int LAG = PAIR ? 0 : 1;
+      for (int i = 0; ok && i < s.n + LAG; ++i) {
+        if (i < s.n) ok = tile(s, i, false);
+        if (ok && i >= LAG) ok = tile(s, i - LAG, true);
+      }
+    }
+    if (*abort) {  // the copies in flight land before the CTA ends
+      const unsigned long long t0 = globaltimer();
+      for (uint32_t u = idx > STAGES ? idx - STAGES : 0; u < idx; ++u)
+        while (!mbar_try(bar(&C.full[u % STAGES]), (u / STAGES) & 1) &&
+               globaltimer() - t0 < WAIT_LIMIT_NS) {
+        }
+      for (int u = max(0, segs - (PAIR ? 1 : 2)); u < segs; ++u)
+        while (!mbar_try(bar(&C.q_full[PAIR ? 0 : u & 1]), (PAIR ? u : u >> 1) & 1) &&
+               globaltimer() - t0 < WAIT_LIMIT_NS) {
+        }
+    }
+  } else if (warp == MMA_WARP) {
+    // ------------------------------------------------------------ products
+    Cursor<PAIR> cur;
+    cur.open(A, start_b, start_at, run);
+    Seg s;
+    uint32_t idx = 0;
+    int segs = 0;
+    unsigned p_use[2] = {0, 0};
+    // (the turned products: N = NQ, and V^T is an operand whose dimensions are contiguous)
+    const uint32_t id_s = instr_desc(A.bf16, false, false, NQ ? NQ : TILE);
+    const uint32_t id_o = instr_desc(A.bf16, NQ > 0, NQ == 0, NQ ? NQ : DP);
+    bool ok = true;
+    auto full = [&](uint32_t u) {
+      if (!warp_wait(bar(&C.full[u % STAGES]), (u / STAGES) & 1, A.status, abort)) return false;
+      tc_after();
+      return true;
+    };
+    auto scores = [&](int st, int q, uint32_t u) {  // S[st] = Q[q] K^T, or K Q[q]^T
+      const uint64_t qa = desc_rows(base + q * SM::Q_BYTES);
+      const uint64_t ka = desc_rows(base + SM::STAGE_AT + (u % STAGES) * BYTES);
+#pragma unroll
+      for (int k = 0; k < DP / 16; ++k) {
+        const uint64_t dq = qa + (((k / 4) * (SM::Q_BYTES / HALVES) + (k % 4) * 32) >> 4);
+        const uint64_t dk = ka + (((k / 4) * 16384 + (k % 4) * 32) >> 4);
+        mma_ss(tmem + st * S_COLS, NQ ? dk : dq, NQ ? dq : dk, id_s, k > 0);
+      }
+      mma_commit(bar(&C.s_full[st]));
+    };
+    auto values = [&](int st, uint32_t u, bool more) {  // O[st] (+)= P[st] V, or V^T P[st]^T
+      const uint64_t va = desc_cols(base + SM::STAGE_AT + (u % STAGES) * BYTES,
+                                    NQ && DP == 64 ? 0 : 16384);
+      const uint64_t pa = desc_rows(base + SM::P_AT + st * SM::P_BYTES);
+#pragma unroll
+      for (int k = 0; k < TILE / 16; ++k) {
+        const uint64_t dv = va + ((k * 2048) >> 4);
+        const uint64_t dp = pa + (((k / 4) * (NQ * 128) + (k % 4) * 32) >> 4);
+        if (NQ) mma_ss(tmem + O_AT + st * S_COLS, dv, dp, id_o, more || k > 0);
+        else mma_ts(tmem + O_AT + st * S_COLS, tmem + st * S_COLS + k * 8, dv, id_o, more || k > 0);
+      }
+    };
+    while (ok && cur.next(A, s)) {
+      const int slot = PAIR ? 0 : segs & 1;
+      const int use = PAIR ? segs : segs >> 1;
+      ok = warp_wait(bar(&C.q_full[slot]), use & 1, A.status, abort);
+      const int n = s.n;
+      const uint32_t u0 = idx;
+      if (PAIR) {
+        ok = ok && full(u0);
+        if (ok && elect_one()) {
+          scores(0, 0, u0);
+          scores(1, 1, u0);
+          mma_commit(bar(&C.empty[u0 % STAGES]));
+          if (n == 1) mma_commit(bar(&C.q_empty[0]));
+        }
+        __syncwarp();
+        for (int j = 0; ok && j < n; ++j) {
+          const uint32_t uv = u0 + v_order<true>(j, n), uk = u0 + k_order<true>(j + 1);
+          ok = full(uv);
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            ok = ok && warp_wait(bar(&C.p_full[st]), p_use[st] & 1, A.status, abort);
+            ++p_use[st];
+            if (!ok) break;
+            tc_after();
+            if (elect_one()) {
+              values(st, uv, j > 0);
+              if (st == 1) mma_commit(bar(&C.empty[uv % STAGES]));
+              if (j + 1 == n) mma_commit(bar(&C.o_full[st]));
+            }
+            __syncwarp();
+            if (j + 1 < n) {
+              if (st == 0 && !(ok = full(uk))) break;
+              if (elect_one()) {
+                scores(st, st, uk);
+                if (st == 1) {
+                  mma_commit(bar(&C.empty[uk % STAGES]));
+                  if (j + 2 == n) mma_commit(bar(&C.q_empty[0]));
+                }
+              }
+              __syncwarp();
+            }
+          }
+        }
+      } else {
+        for (int j = 0; ok && j < 2 && j < n; ++j) {
+          const uint32_t uk = u0 + k_order<false>(j);
+          ok = full(uk);
+          if (ok && elect_one()) {
+            scores(j, slot, uk);
+            mma_commit(bar(&C.empty[uk % STAGES]));
+            if (j + 1 == n) mma_commit(bar(&C.q_empty[slot]));
+          }
+          __syncwarp();
+        }
+        for (int j = 0; ok && j < n; ++j) {
+          const int st = j & 1;
+          const uint32_t uv = u0 + v_order<false>(j, n), uk = u0 + k_order<false>(j + 2);
+          ok = full(uv) && warp_wait(bar(&C.p_full[st]), p_use[st] & 1, A.status, abort);
+          ++p_use[st];
+          if (!ok) break;
+          tc_after();
+          if (elect_one()) {
+            values(st, uv, j >= 2);
+            mma_commit(bar(&C.empty[uv % STAGES]));
+            if (j + 2 >= n) mma_commit(bar(&C.o_full[st]));
+          }
+          __syncwarp();
+          if (j + 2 < n) {
+            ok = full(uk);
+            if (ok && elect_one()) {
+              scores(st, slot, uk);
+              mma_commit(bar(&C.empty[uk % STAGES]));
+              if (j + 3 == n) mma_commit(bar(&C.q_empty[slot]));
+            }
+            __syncwarp();
+          }
+        }
+      }
+      idx += 2 * n;
+      ++segs;
+    }
+    if (!ok && lane == 0) {  // the products in flight end before TMEM is freed
+      mma_commit(bar(&C.drain));
+      const unsigned long long t0 = globaltimer();
+      while (!mbar_try(bar(&C.drain), 0) && globaltimer() - t0 < WAIT_LIMIT_NS) {
+      }
+    }
+    __syncwarp();
+    }
   }
   tc_before();
   __syncthreads();
   tc_after();
   if (warp == MMA_WARP)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "n"(TM_COLS)
+                 : "memory");
 }
 
 // Join of the items that the CTAs' runs cut: per item the parts' maxima, sums
 // and outputs, eight parts at a time (one per warp), then the warps' results.
-// A unit of work is 32 query rows x 16 columns of one cut item.
+// A unit of work is 32 query rows x 16 columns of one cut item (NQ > 0: one row).
 constexpr int JOIN_WARPS = 8;
-template <int DP, bool PAIR>
+template <int DP, int NQ, bool PAIR>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) sv_attn_join(const __grid_constant__ AttnParams A,
                                                                int ctas) {
-  constexpr int ROWS = PAIR ? 2 * TILE : TILE;
+  constexpr int ROWS = NQ ? NQ : PAIR ? 2 * TILE : TILE;
+  constexpr int VECS = NQ ? 1 : 4;  // four-column pieces per thread
   __shared__ int2 cuts[MAX_CTAS];  // (first CTA of the item, CTAs of it)
   __shared__ int found_s[JOIN_WARPS];
-  __shared__ float4 acc_s[JOIN_WARPS][4][32];
+  __shared__ float4 acc_s[JOIN_WARPS][VECS][32];
   __shared__ float2 ml_s[JOIN_WARPS][32];
   const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1059,42 +1383,44 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) sv_attn_join(const __grid_con
   if (parts) cuts[at] = make_int2(tid, parts);
   __syncthreads();
   const int row_groups = (min(A.tpt, A.N) * A.G + 31) / 32;
-  const int per_item = row_groups * (PAIR ? 2 : 1) * (DP / 16);
+  const int per_item = NQ ? A.N * A.G : row_groups * (PAIR ? 2 : 1) * (DP / 16);
   const int units = count * per_item;
   for (int u = int(blockIdx.x); u < units; u += int(gridDim.x)) {
     const int2 cut = cuts[u / per_item];
     const int w = u % per_item;
     const int cg = w % (DP / 16), rgp = w / (DP / 16);
-    const int st = PAIR ? rgp / row_groups : 0, row = (rgp % row_groups) * 32 + lane;
+    const int st = PAIR ? rgp / row_groups : 0;
+    const int row = NQ ? w : (rgp % row_groups) * 32 + lane;
     const int4 d1 = A.desc[cut.x + 1];  // its first segment is of this item
     const int item = d1.y, b = d1.z;
     const int h = item / A.MT, mt = item - h * A.MT;
     const int rt = row / A.G, rg = row - rt * A.G;
     const int tok = mt * (PAIR ? 2 : 1) * A.tpt + st * A.tpt + rt;
-    const bool active = row < TILE && rt < A.tpt && tok < A.N;
+    const bool active = NQ ? lane < DP / 4 : row < TILE && rt < A.tpt && tok < A.N;
     float m = -INFINITY, l = 0.0f;
     bool bad = false;
-    float4 acc[4];
+    float4 acc[VECS];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = make_float4(0, 0, 0, 0);
+    for (int i = 0; i < VECS; ++i) acc[i] = make_float4(0, 0, 0, 0);
     for (int p = warp; p < cut.y; p += JOIN_WARPS) {
       const int c = cut.x + p;
       const int slot = p == 0 && (A.desc[c].x & DESC_LAST1) ? 1 : 0;
       const size_t s = size_t(c) * 2 + slot;
       if (active) {
         const float2 ml = A.part_ml[s * ROWS + st * TILE + row];
-        float4 o[4];
+        float4 o[VECS];
+        const float4* const src = reinterpret_cast<const float4*>(A.part_o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          o[i] = reinterpret_cast<const float4*>(
-              A.part_o)[(s * (DP / 4) + cg * 4 + i) * ROWS + st * TILE + row];
+        for (int i = 0; i < VECS; ++i)
+          o[i] = NQ ? src[(s * ROWS + row) * (DP / 4) + lane]
+                    : src[(s * (DP / 4) + cg * 4 + i) * ROWS + st * TILE + row];
         bad |= ml.y == -1.0f;
         const float m2 = fmaxf(m, ml.x), mu = m2 == -INFINITY ? 0.0f : m2;
-        const float f = ex2((m - mu) * A.c), g = ex2((ml.x - mu) * A.c);
+        const float f = ex2(m - mu), g = ex2(ml.x - mu);
         m = m2;
         l = l * f + ml.y * g;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < VECS; ++i) {
           acc[i].x = acc[i].x * f + o[i].x * g;
           acc[i].y = acc[i].y * f + o[i].y * g;
           acc[i].z = acc[i].z * f + o[i].z * g;
@@ -1103,10 +1429,10 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) sv_attn_join(const __grid_con
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc_s[warp][i][lane] = acc[i];
+    for (int i = 0; i < VECS; ++i) acc_s[warp][i][lane] = acc[i];
     ml_s[warp][lane] = make_float2(m, bad ? -1.0f : l);
     __syncthreads();
-    if (warp < 4) {  // warp i joins the four columns of group i
+    if (warp < VECS) {  // warp i joins piece i
       float M = -INFINITY;
       bool any_bad = false;
 #pragma unroll
@@ -1119,7 +1445,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) sv_attn_join(const __grid_con
       float L = 0.0f;
 #pragma unroll
       for (int p = 0; p < JOIN_WARPS; ++p) {
-        const float g = ex2((ml_s[p][lane].x - M) * A.c);
+        const float g = ex2(ml_s[p][lane].x - M);
         const float4 a = acc_s[p][warp][lane];
         L += ml_s[p][lane].y * g;
         o.x += a.x * g;
@@ -1127,7 +1453,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) sv_attn_join(const __grid_con
         o.z += a.z * g;
         o.w += a.w * g;
       }
-      const int col = cg * 16 + warp * 4;
+      const int col = NQ ? lane * 4 : cg * 16 + warp * 4;
       if (active && col < A.D) {
         const float f = 1.0f / L;
         uint2 x = make_uint2(pack16(o.x * f, o.y * f, A.bf16), pack16(o.z * f, o.w * f, A.bf16));
@@ -1174,12 +1500,12 @@ bool make_map(CUtensorMap* m, int dtype, const void* p, int rank, const uint64_t
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DP, bool PAIR>
+template <int DP, int NQ, bool PAIR>
 int launch_as(const AttnParams& A, int grid, int ctas, cudaStream_t st) {
-  if (cudaFuncSetAttribute(sv_attn<DP, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Smem<DP>::TOTAL) != cudaSuccess)
+  if (cudaFuncSetAttribute(sv_attn<DP, NQ, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (Smem<DP, NQ>::TOTAL)) != cudaSuccess)
     return SV_ERR_CUDA;
-  sv_attn<DP, PAIR><<<grid, THREADS, Smem<DP>::TOTAL, st>>>(A);
+  sv_attn<DP, NQ, PAIR><<<grid, THREADS, (Smem<DP, NQ>::TOTAL), st>>>(A);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
   if (A.kind == PROMPT) return SV_OK;
   cudaLaunchConfig_t cfg = {};
@@ -1191,16 +1517,33 @@ int launch_as(const AttnParams& A, int grid, int ctas, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sv_attn_join<DP, PAIR>, A, ctas) == cudaSuccess ? SV_OK
+  return cudaLaunchKernelEx(&cfg, sv_attn_join<DP, NQ, PAIR>, A, ctas) == cudaSuccess ? SV_OK
                                                                                 : SV_ERR_CUDA;
 }
 
-// Query tiles of an item: two when one tile does not hold a request's rows.
-bool pair_of(int N, int G) { return N > TILE / G; }
+// The layout for items of `rows` rows (see Smem): columns of the turned
+// products, or 0 for a row per lane with one (128) or two (256) tiles.
+struct Layout { int nq, rows; };
+Layout layout_of(int N, int G) {
+  const int rows = N * G;
+  if (rows <= 16) return {16, 16};
+  if (rows <= 32) return {32, 32};
+  if (rows <= 64) return {64, 64};
+  return {0, N <= TILE / G ? TILE : 2 * TILE};
+}
 
 size_t workspace_for(int N, int G, int D) {
-  const size_t rows = pair_of(N, G) ? 2 * TILE : TILE, dp = D > 64 ? 128 : 64;
+  const size_t rows = layout_of(N, G).rows, dp = D > 64 ? 128 : 64;
   return size_t(MAX_CTAS) * (2 * rows * (dp * 4 + 8) + sizeof(int4));
+}
+
+template <int DP>
+int launch_dp(const AttnParams& A, Layout l, int grid, int ctas, cudaStream_t st) {
+  if (l.nq == 16) return launch_as<DP, 16, false>(A, grid, ctas, st);
+  if (l.nq == 32) return launch_as<DP, 32, false>(A, grid, ctas, st);
+  if (l.nq == 64) return launch_as<DP, 64, false>(A, grid, ctas, st);
+  if (l.rows == TILE) return launch_as<DP, 0, false>(A, grid, ctas, st);
+  return launch_as<DP, 0, true>(A, grid, ctas, st);
 }
 
 int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v,
@@ -1251,7 +1594,7 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
     A.mkn = A.mk;
     A.mvn = A.mv;
   }
-  bool pair;
+  Layout lay;
   int grid = ctas;
   if (A.kind != PROMPT) {
     const uint64_t dims[3] = {D, uint64_t(A.N), uint64_t(A.B) * A.LH};
@@ -1260,26 +1603,24 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
     if (!make_map(&A.mkn, dtype, k_new, 3, dims, str, box) ||
         !make_map(&A.mvn, dtype, v_new, 3, dims, str, box))
       return SV_ERR_CUDA;
-    pair = pair_of(A.N, A.G);
-    const int tpi = pair ? 2 * A.tpt : A.tpt;
+    lay = layout_of(A.N, A.G);
+    const int tpi = lay.rows == 2 * TILE ? 2 * A.tpt : A.tpt;
     A.MT = (A.N + tpi - 1) / tpi;
-    const size_t rows = pair ? 2 * TILE : TILE, dp = A.D > 64 ? 128 : 64;
+    const size_t rows = lay.rows, dp = A.D > 64 ? 128 : 64;
     unsigned char* w = static_cast<unsigned char*>(workspace);
     A.part_o = reinterpret_cast<float*>(w);
     A.part_ml = reinterpret_cast<float2*>(w + size_t(MAX_CTAS) * 2 * rows * dp * 4);
     A.desc = reinterpret_cast<int4*>(w + size_t(MAX_CTAS) * 2 * rows * (dp * 4 + 8));
   } else {
     // two query tiles per item when that leaves every SM an item
-    pair = (long long)A.Hkv * (A.T / (2 * A.tpt)) >= ctas;
-    const int tpi = pair ? 2 * A.tpt : A.tpt;
+    lay = {0, (long long)A.Hkv * (A.T / (2 * A.tpt)) >= ctas ? 2 * TILE : TILE};
+    const int tpi = lay.rows == 2 * TILE ? 2 * A.tpt : A.tpt;
     const long long items = (long long)A.Hkv * ((A.T + tpi - 1) / tpi + A.B);
     if (items < grid) grid = int(items);
     A.MT = 1;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (A.D > 64)
-    return pair ? launch_as<128, true>(A, grid, ctas, st) : launch_as<128, false>(A, grid, ctas, st);
-  return pair ? launch_as<64, true>(A, grid, ctas, st) : launch_as<64, false>(A, grid, ctas, st);
+  return A.D > 64 ? launch_dp<128>(A, lay, grid, ctas, st) : launch_dp<64>(A, lay, grid, ctas, st);
 }
 
 bool misaligned(const void* p, unsigned a) {
