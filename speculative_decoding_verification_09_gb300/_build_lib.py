@@ -4,18 +4,20 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", f) for f in ("specverify.cu", "kvcache.cu", "tree.cu",
-                                              "attention.cu")]
+                                              "attention.cu", "attn_bf16.cu", "attn_f16.cu")]
+INCLUDED = [os.path.join(PKG, "csrc", "attention.cuh")]
 HEADERS = [os.path.join(ROOT, "include", f) for f in ("specverify.h", "svkv.h", "svtree.h",
                                                      "svattn.h")]
 OUT_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libspecverify.so")
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
-              "-Xcompiler", "-fPIC", "-shared"]
+              "-Xcompiler", "-fPIC"]
 
 
 def _nvcc() -> str:
@@ -29,7 +31,7 @@ def up_to_date() -> bool:
     if not os.path.exists(LIB_PATH):
         return False
     t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(p) <= t for p in (*SRCS, *HEADERS, __file__))
+    return all(os.path.getmtime(p) <= t for p in (*SRCS, *INCLUDED, *HEADERS, __file__))
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
@@ -37,10 +39,21 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         return LIB_PATH
     os.makedirs(OUT_DIR, exist_ok=True)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *NVCC_FLAGS, *(extra_flags or []), "-I", os.path.join(ROOT, "include"), *SRCS,
-           "-o", tmp]
-    if verbose:
-        print(" ".join(cmd))
-    subprocess.run(cmd, check=True)
+    base = [_nvcc(), *NVCC_FLAGS, *(extra_flags or []), "-I", os.path.join(ROOT, "include")]
+    objs = [f"{tmp}.{i}.o" for i in range(len(SRCS))]
+
+    def run(cmd: list[str]) -> None:
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+
+    try:
+        with ThreadPoolExecutor(len(SRCS)) as pool:  # one compiler process per source
+            list(pool.map(run, [[*base, "-c", s, "-o", o] for s, o in zip(SRCS, objs)]))
+        run([*base, "-shared", *objs, "-o", tmp])
+    finally:
+        for o in objs:
+            if os.path.exists(o):
+                os.remove(o)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH

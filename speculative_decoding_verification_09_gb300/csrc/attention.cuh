@@ -1,0 +1,1547 @@
+// attention.cuh -- sm_103a kernels of the attention over the caches (the calls
+// are in attention.cu, the operations in include/svattn.h).
+#ifndef SV_ATTENTION_CUH
+#define SV_ATTENTION_CUH
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "specverify.h"
+#include "svattn.h"
+#include "svkv.h"
+
+namespace svattn {
+
+enum Kind { TREE = 0, RING = 1, PROMPT = 2 };
+
+constexpr int MAX_N = 256;      // tree nodes
+constexpr int MAX_R = 64;       // staged tokens of the ring call
+constexpr int MAX_GROUP = 128;  // query heads per KV head
+constexpr int MAX_D = 128;
+constexpr int MAX_KEYS = 0x7fffffff - 1023;  // cache entries: a tile more fits an int
+
+constexpr int ITEM_COST = 1;    // an item's fixed cost in tiles
+constexpr int TILE = 128;       // query rows of a tile, and keys of a tile
+constexpr int THREADS = 384;    // two softmax warpgroups, and one with a copy and a product warp
+// Registers: launched with 168 a thread (64512 a CTA); the softmax warpgroups
+// hold a row of scores each thread and take over what the third does not need.
+constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
+static_assert(256 * SOFTMAX_REGS + 128 * OTHER_REGS <= THREADS * 168, "register split");
+constexpr int COPY_WARP = 8, MMA_WARP = 9;
+constexpr int MAX_CTAS = 152;   // one per SM
+constexpr unsigned long long WAIT_LIMIT_NS = 1000000000ull;
+constexpr uint32_t SUSPEND_HINT_NS = 20000;
+// A row's running maximum is raised only when a score exceeds it by 2^8 in
+// the weights: until then weights of up to 2^8 are summed, which fp32 sums and
+// 16-bit weights hold without loss, and the output tile needs no rescaling.
+constexpr float RAISE_LOG2 = 8.0f;
+
+struct AttnParams {
+  CUtensorMap mq, mk, mv, mkn, mvn;  // queries, cache (or prompt) K and V, staged K and V
+  uint16_t* out;
+  const int32_t* table;
+  const int32_t* lens;    // seq_lens, pos or cu_seqlens
+  const int32_t* parent;
+  int32_t* status;
+  float* part_o;          // partial outputs  [2 * CTAs][rows][DP / 4] x 4, columns outermost
+  float2* part_ml;        // their maxima and sums [2 * CTAs][rows]
+  int4* desc;             // [CTAs] what each CTA's first and last segments are (see Desc bits)
+  float c;                // scale * log2(e)
+  int kind;
+  int B, N, Hq, Hkv, D, G;
+  int LH, head0, num_pages, page, cols, sink, window, T;
+  int box;                // page rows of one copy
+  int tpt;                // tokens per query tile, floor(128 / G)
+  int q_rows;             // rows of one query copy
+  int MT;                 // items per KV head (TREE, RING)
+};
+
+__device__ __forceinline__ void set_status(int32_t* status, int bits) {
+  if (status && bits) atomicOr(status, bits);
+}
+__device__ __forceinline__ unsigned long long globaltimer() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void mbar_init(uint32_t bar, unsigned count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_tx(uint32_t bar, unsigned bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, unsigned parity) {
+  unsigned ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(SUSPEND_HINT_NS)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait for a phase: false once the CTA gave up, or after one second,
+// which reports SV_ST_TIMEOUT and makes the CTA's other waits give up too.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, unsigned parity, int32_t* status,
+                                          volatile int* abort) {
+  if (mbar_try(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer();
+  for (;;) {
+    if (mbar_try(bar, parity)) return true;
+    if (*abort) return false;
+    if (globaltimer() - t0 > WAIT_LIMIT_NS) {
+      *abort = 1;
+      set_status(status, SV_ST_TIMEOUT);
+      return false;
+    }
+  }
+}
+// The same by a whole warp, all lanes of which get one answer.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, unsigned parity, int32_t* status,
+                                          volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, abort)) != 0;
+}
+
+// Tiled copies global -> shared; a row past a map's extent arrives as zeros.
+// The innermost coordinate is 0 or 64 elements: 16-byte boundaries.
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x,
+                                       int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst), "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x,
+                                       int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst), "l"(m), "r"(bar), "r"(x), "r"(y),
+      "r"(z), "r"(w)
+      : "memory");
+}
+
+// Tensor-core products.  Tiles lie in shared memory as 64-element (128-byte)
+// wide blocks of 128 rows in the 128-byte swizzle, one block after another.
+// K-major operand (queries, keys): rows 128 bytes apart, 8-row groups 1024.
+__device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {
+  return uint64_t((addr >> 4) & 0x3fff) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// MN-major operand (values: the 64 dimensions of a block are contiguous):
+// 8-key groups 1024 bytes apart, 64-dimension blocks `blocks` bytes.  (0: a
+// head of at most 64 dimensions taken twice to make up the 128 rows of V^T;
+// the second half of O^T is not read.)
+__device__ __forceinline__ uint64_t desc_cols(uint32_t addr, uint32_t blocks) {
+  return uint64_t((addr >> 4) & 0x3fff) | (uint64_t(blocks >> 4) << 16) |
+         (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+__device__ __forceinline__ uint32_t instr_desc(int bf16, bool a_cols, bool b_cols, int n) {
+  return (1u << 4) | (uint32_t(bf16) << 7) | (uint32_t(bf16) << 10) | (a_cols ? 1u << 15 : 0u) |
+         (b_cols ? 1u << 16 : 0u) | (uint32_t(n >> 3) << 17) | (uint32_t(TILE >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b),
+      "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b),
+      "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// One lane of the (converged) warp: the form in which the compiler knows that a
+// single thread issues, and keeps the products' descriptors in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tc_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tm_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// 32 columns of the warp's 32 lanes, one row per thread.
+__device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+// Waits for the warp's TMEM loads; passing the registers through keeps their
+// uses behind the wait.
+#define TM_REGS(r)                                                                              \
+  "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),           \
+      "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),   \
+      "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),             \
+      "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),             \
+      "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+__device__ __forceinline__ void tm_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : TM_REGS(r)::"memory");
+}
+__device__ __forceinline__ void tm_loaded(uint32_t (&r)[32]) {  // after tm_wait_ld
+  asm volatile("" : TM_REGS(r)::"memory");
+}
+__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
+      "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tm_ld8(uint32_t addr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                      "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                      "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                      "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                      "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+                      "r"(r[13]), "r"(r[14]), "r"(r[15])
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tm_ldn(uint32_t addr, uint32_t (&r)[N]) {
+  if constexpr (N == 8) tm_ld8(addr, r);
+  else if constexpr (N == 16) tm_ld16(addr, r);
+  else tm_ld32(addr, r);
+}
+template <int N>
+__device__ __forceinline__ void tm_stn(uint32_t addr, const uint32_t (&r)[N]) {
+  if constexpr (N == 16) tm_st16(addr, r);
+  else tm_st32(addr, r);
+}
+template <int N>
+__device__ __forceinline__ void tm_loadedn(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i])::"memory");
+}
+template <int N>
+__device__ __forceinline__ void tm_waitn(uint32_t (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  tm_loadedn<N>(r);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two 32-bit multiply-adds, or additions, in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mov.b64 c, {%6, %7};\n fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  uint32_t r;
+  if (BF) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void group_sync(int id, int n) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+__device__ __forceinline__ int group_or(int id, int n, int x) {
+  int r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.s32 p, %3, 0;\n"
+      " barrier.cta.red.or.pred q, %1, %2, p;\n selp.s32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"(x)
+      : "memory");
+  return r;
+}
+
+// -------------------------------------------------------------- what a CTA works on
+
+// A segment: key tiles j0 .. j0 + n - 1 of the nt tiles of an item.  An item is
+// the query rows of one KV head that share the tiles: tokens mt * tokens(item)
+// on of request b, with the Hq / Hkv query heads of h.
+struct Seg {
+  int b, h, mt, j0, n, nt;
+  int len;    // cache entries (TREE, RING; 0 when bad), or tokens of the sequence
+  int bad;    // SV_ST_BAD_LENGTH for a length outside its range
+  int pos;    // committed positions (RING)
+  int start;  // first packed row (PROMPT)
+  // PROMPT: tiles t = j below `near`, then lo + (j - near)
+  int near, lo;
+};
+
+// Cache entries of request b (0 with `bad` set for a length out of range).
+__device__ __forceinline__ int cache_len(const AttnParams& A, int b, int& bad, int& pos) {
+  const long long n = __ldg(A.lens + b);
+  pos = int(n);
+  if (A.kind == TREE) {
+    bad = n < 0 || n > (long long)A.cols * A.page || n > MAX_KEYS ? SV_ST_BAD_LENGTH : 0;
+    return bad ? 0 : int(n);
+  }
+  bad = n < 0 || n > 0x7fffffffLL - A.N ? SV_ST_BAD_LENGTH : 0;
+  const long long C = (long long)A.sink + A.window;
+  return bad ? 0 : int(n < C ? n : C);
+}
+__device__ __forceinline__ int tiles_of(int n) { return (n + TILE - 1) / TILE; }
+
+// The segments of a CTA, in order, taken by whole warps.
+// TREE and RING: the tiles of all items, in the order request, KV head, item of
+// the head, are cut into equal runs, one per CTA; an item cut by a run's end is
+// joined by the second kernel.  An item counts ITEM_COST tiles more than it has
+// (its queries, output and first tile's latency).
+// PROMPT: whole items, dealt out to the CTAs in turn; a sequence's last tokens
+// (whose items are the longest) come first.
+template <bool PAIR, bool PR>
+struct Cursor;
+
+template <bool PAIR>
+struct Cursor<PAIR, false> {
+  int b, item, j, nt, len, bad, pos;
+  long long left;
+
+  __device__ void open(const AttnParams& A, int b0, long long at, long long count, bool = false) {
+    left = count;
+    if (count <= 0) return;
+    b = b0;
+    len = cache_len(A, b, bad, pos);
+    nt = tiles_of(len) + tiles_of(A.N);
+    item = int(at / (nt + ITEM_COST));
+    j = int(at - (long long)item * (nt + ITEM_COST));
+  }
+  __device__ bool next(const AttnParams& A, Seg& s, bool = false) {
+    for (;;) {
+      if (left <= 0) return false;
+      if (j >= nt) {  // the item's fixed cost, counted behind its tiles
+        left -= nt + ITEM_COST - j;
+        j = 0;
+        if (++item == A.MT * A.Hkv) {
+          item = 0;
+          if (left <= 0) return false;
+          ++b;
+          len = cache_len(A, b, bad, pos);
+          nt = tiles_of(len) + tiles_of(A.N);
+        }
+        continue;
+      }
+      s.b = b;
+      s.h = item / A.MT;
+      s.mt = item - s.h * A.MT;
+      s.j0 = j;
+      s.n = int(left < nt - j ? left : nt - j);
+      s.nt = nt;
+      s.len = len;
+      s.bad = bad;
+      s.pos = pos;
+      j += s.n;
+      left -= s.n;
+      return true;
+    }
+  }
+};
+
+template <bool PAIR>
+struct Cursor<PAIR, true> {
+  long long i, cum, incl;     // this CTA's next item; items before, and up to, the lane's sequence
+  int wb, w_start, w_len;     // the 32 sequences from wb on, one per lane
+
+  __device__ void load_window(const AttnParams& A, bool report) {
+    const int lane = int(threadIdx.x) & 31, s = wb + lane;
+    w_start = w_len = 0;
+    if (s < A.B) {
+      const long long lo = __ldg(A.lens + s), hi = __ldg(A.lens + s + 1);
+      if (lo < 0 || hi < lo || hi > A.T) {
+        if (report) set_status(A.status, SV_ST_BAD_LENGTH);
+      } else {
+        w_start = int(lo);
+        w_len = int(hi - lo);
+      }
+    }
+    const int tpi = PAIR ? 2 * A.tpt : A.tpt;
+    incl = (long long)((w_len + tpi - 1) / tpi) * A.Hkv;
+    for (int x = 1; x < 32; x <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, x);
+      if (lane >= x) incl += y;
+    }
+  }
+  __device__ void open(const AttnParams& A, int, long long, long long, bool report = false) {
+    i = blockIdx.x;
+    cum = 0;
+    wb = 0;
+    load_window(A, report);
+  }
+  __device__ bool next(const AttnParams& A, Seg& s, bool report = false) {
+    for (;;) {
+      const long long total = __shfl_sync(0xffffffffu, incl, 31);
+      if (i < cum + total) break;
+      cum += total;
+      wb += 32;
+      if (wb >= A.B) return false;
+      load_window(A, report);
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, i < cum + incl);
+    const int src = __ffs(int(hit)) - 1;
+    const long long before = src ? __shfl_sync(0xffffffffu, incl, src - 1) : 0;
+    s.b = wb + src;
+    s.start = __shfl_sync(0xffffffffu, w_start, src);
+    s.len = __shfl_sync(0xffffffffu, w_len, src);
+    const int tpi = PAIR ? 2 * A.tpt : A.tpt;
+    const long long r = i - cum - before;
+    const int back = int(r / A.Hkv);
+    s.h = int(r - (long long)back * A.Hkv);
+    s.mt = (s.len + tpi - 1) / tpi - 1 - back;
+    s.bad = 0;
+    s.j0 = 0;
+    const int q0 = s.mt * tpi, q1 = min(q0 + tpi, s.len) - 1;
+    const int first = q0 - A.window + 1;  // (window >= 1: no overflow)
+    s.lo = first > 0 ? first / TILE : 0;
+    s.near = min(tiles_of(min(A.sink, q1 + 1)), s.lo);
+    s.n = s.nt = s.near + q1 / TILE - s.lo + 1;
+    i += gridDim.x;
+    return true;
+  }
+};
+
+// Copies of a segment in the order in which the product warp takes them.
+// PAIR (two query tiles, every key tile used by both): K0 V0 K1 V1 ...
+// otherwise (one query tile, even and odd key tiles in two streams, so that
+// one stream's product runs under the other's softmax): K0 K1 V0 K2 V1 ...
+template <bool PAIR>
+__device__ __forceinline__ int k_order(int j) { return PAIR ? 2 * j : (j ? 2 * j - 1 : 0); }
+template <bool PAIR>
+__device__ __forceinline__ int v_order(int j, int n) {
+  return PAIR ? 2 * j + 1 : (j < n - 1 ? 2 * j + 2 : 2 * n - 1);
+}
+
+// Bits a .. b - 1 of the 32 keys from k0 on.
+__device__ __forceinline__ uint32_t span(int a, int b, int k0) {
+  a = max(a - k0, 0);
+  b = min(b - k0, 32);
+  if (a >= b) return 0;
+  return (0xffffffffu >> (32 - b)) & (0xffffffffu << a);
+}
+
+// The three layouts of an item's products, by the rows (tokens x query heads of
+// a KV head) that share its keys:
+//   NQ == 0, PAIR: more than 128 rows.  Two tiles of 128 rows; S = Q K^T has a
+//     row per TMEM lane, every key tile serves both.
+//   NQ == 0, !PAIR: 65 to 128 rows.  One such tile, in two streams.
+//   NQ > 0: at most NQ rows.  The products are turned over, S^T = K Q^T and
+//     O^T = V^T P^T, so that the lanes hold keys (dimensions) and the few rows
+//     are columns: every thread has work however few the rows are, and the
+//     products cost NQ / 128 of a full tile's.  (A ring batch of 32 rows per
+//     item took 104 us with a row per lane.)
+template <int DP, int NQ>
+struct Smem {
+  static constexpr int BYTES = TILE * DP * 2;                    // a tile of keys or values
+  static constexpr int Q_BYTES = (NQ ? NQ : TILE) * DP * 2;      // a tile of queries
+  static constexpr int P_BYTES = NQ * TILE * 2;                  // weights of a stream (NQ > 0)
+  static constexpr int P_AT = 2 * Q_BYTES;
+  static constexpr int STAGE_AT = P_AT + 2 * P_BYTES;
+  static constexpr int FIT = (229376 - STAGE_AT) / BYTES;
+  static constexpr int STAGES = FIT < 12 ? FIT : 12;
+  static constexpr int CTRL = STAGE_AT + STAGES * BYTES;         // offset of the control part
+  static constexpr int TOTAL = CTRL + 3072;
+};
+struct Ctrl {
+  unsigned long long full[12], empty[12], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2],
+      drain;
+  union {
+    float2 ml[2][TILE];  // NQ == 0: softmax state exchanged between the streams
+    struct {             // NQ > 0, per stream and column
+      unsigned long long sees[2][64];  // columns that see a staged entry
+      alignas(16) float nmc[2][64];    // minus the running maximum, in base-2 units; -inf: none yet
+      alignas(16) float fac[2][64];                // rescaling, and at the end the streams' shares
+    } few;
+  };
+  uint8_t parent[2][MAX_N];  // one copy per softmax warpgroup
+  long long scan[12];
+  long long start_at;
+  int start_b, abort;
+  uint32_t tmem;
+};
+static_assert(sizeof(Ctrl) <= 3072, "control part");
+
+// desc[cta]: x = item index within the request | flags, y = request
+constexpr int DESC_IN = 1 << 30;       // the first segment starts inside its item
+constexpr int DESC_THROUGH = 1 << 29;  // and runs to the CTA's end without finishing it
+constexpr int DESC_OUT = 1 << 28;      // the last segment leaves its item unfinished
+constexpr int DESC_LAST1 = 1 << 27;    // the last segment's partials are in slot 1
+
+// Sums of the columns over a warp's 32 lanes: lane i gets column i's (i mod 16's
+// with 16 columns) in v[0], and column 32 + i's in v[32] with 64.
+template <int NQ>
+__device__ __forceinline__ void sum_columns(float* v, int lane) {
+  constexpr int SPAN = NQ < 32 ? NQ : 32;
+#pragma unroll
+  for (int c = 0; c < NQ; c += SPAN) {
+#pragma unroll
+    for (int x = SPAN / 2; x; x >>= 1) {
+      const bool up = lane & x;
+#pragma unroll
+      for (int i = 0; i < x; ++i) {
+        const float give = up ? v[c + i] : v[c + i + x], keep = up ? v[c + i + x] : v[c + i];
+        v[c + i] = keep + __shfl_xor_sync(0xffffffffu, give, x);
+      }
+    }
+    if (SPAN == 16) v[c] += __shfl_xor_sync(0xffffffffu, v[c], 16);
+  }
+}
+
+// One tile's softmax with keys on the lanes: thread `key` takes its key's
+// scores of all NQ columns (S^T, TMEM columns from ts), adds their weights to
+// lq and stores them, rounded, as column `key` of P (a K-major operand of two
+// 64-key blocks in the 128-byte swizzle).  `sees`: the columns that see the
+// key.  All keys of a tile use one maximum per column; it is raised, the sums
+// and O (columns from to) rescaled, when a score exceeds it by 2^RAISE_LOG2.
+template <int NQ, bool BF>
+__device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl& C, int st, int key,
+                                            uint32_t ts, uint32_t to, unsigned long long sees,
+                                            bool masked, bool started, bool& unset, float* lq,
+                                            unsigned char* pbuf) {
+  constexpr int W = NQ < 32 ? NQ : 32;
+  const int lane = key & 31, warp = key >> 5;
+  float* const nmc = C.few.nmc[st];
+  const float2 c2 = make_float2(A.c, A.c);
+  uint32_t r[NQ / W][W];
+  auto score = [&](int q) -> uint32_t& { return r[q / W][q % W]; };
+  auto load = [&] {
+#pragma unroll
+    for (int x = 0; x < NQ / W; ++x) tm_ldn<W>(ts + x * W, r[x]);
+    tm_waitn<W>(r[0]);
+    if (NQ > W) tm_loadedn<W>(r[NQ / W - 1]);
+    if (masked) {
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+        if (!(sees >> q & 1)) score(q) = 0xff800000u;
+    }
+  };
+  // the weights' exponents in place of the scores, and the largest
+  auto exponents = [&] {
+    float over = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < NQ; q += 4) {
+      const float4 n = *reinterpret_cast<const float4*>(nmc + q);
+      const float2 a = fma2(make_float2(__uint_as_float(score(q)), __uint_as_float(score(q + 1))),
+                            c2, make_float2(n.x, n.y));
+      const float2 b =
+          fma2(make_float2(__uint_as_float(score(q + 2)), __uint_as_float(score(q + 3))), c2,
+               make_float2(n.z, n.w));
+      score(q) = __float_as_uint(a.x);
+      score(q + 1) = __float_as_uint(a.y);
+      score(q + 2) = __float_as_uint(b.x);
+      score(q + 3) = __float_as_uint(b.y);
+      over = fmaxf(over, fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y)));
+    }
+    return over;
+  };
+  load();
+  bool raise = !started || unset;
+  if (!raise) {
+    raise = group_or(1 + st, TILE, exponents() > RAISE_LOG2);
+    if (raise) load();
+  }
+  if (raise) {
+    float* const wmax = reinterpret_cast<float*>(pbuf);  // [warp][NQ]; P is free until stored
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      float t;
+      asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;"
+                   : "=f"(t)
+                   : "f"(__uint_as_float(score(q))));
+      if (lane == (q & 31)) wmax[warp * NQ + q] = t;
+    }
+    group_sync(1 + st, TILE);
+    int none = 0;
+    if (key < NQ) {
+      const float t = fmaxf(fmaxf(wmax[key], wmax[NQ + key]),
+                            fmaxf(wmax[2 * NQ + key], wmax[3 * NQ + key])) * A.c;
+      float old = started ? -nmc[key] : INFINITY, f = 1.0f;
+      if (old == INFINITY) {
+        if (t > -INFINITY) old = t;
+      } else if (t - old > RAISE_LOG2) {
+        f = ex2(old - t);
+        old = t;
+      }
+      nmc[key] = -old;
+      C.few.fac[st][key] = f;
+      none = old == INFINITY;
+    }
+    unset = group_or(1 + st, TILE, none);
+    if (started) {
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) lq[q] *= C.few.fac[st][q];
+#pragma unroll
+      for (int x = 0; x < NQ / W; ++x) {
+        uint32_t o[W];
+        tm_ldn<W>(to + x * W, o);
+        tm_waitn<W>(o);
+#pragma unroll
+        for (int q = 0; q < W; ++q)
+          o[q] = __float_as_uint(__uint_as_float(o[q]) * C.few.fac[st][x * W + q]);
+        tm_stn<W>(to + x * W, o);
+      }
+      tm_wait_st();
+    }
+    exponents();
+  }
+  // key k of row q: block k / 64, byte (k % 64) * 2 of the 128-byte row, its
+  // 16-byte piece exchanged with that of q % 8
+  unsigned char* const prow = pbuf + (key >> 6) * (NQ * 128) + (key & 7) * 2;
+  const int piece = (key & 63) >> 3;
+#pragma unroll
+  for (int q = 0; q < NQ; q += 2) {
+    const float2 p = make_float2(ex2(__uint_as_float(score(q))), ex2(__uint_as_float(score(q + 1))));
+    const float2 l = add2(make_float2(lq[q], lq[q + 1]), p);
+    lq[q] = l.x;
+    lq[q + 1] = l.y;
+    const uint32_t w = pack16<BF>(p.x, p.y);
+    *reinterpret_cast<uint16_t*>(prow + q * 128 + ((piece ^ (q & 7)) << 4)) = uint16_t(w);
+    *reinterpret_cast<uint16_t*>(prow + (q + 1) * 128 + ((piece ^ ((q + 1) & 7)) << 4)) =
+        uint16_t(w >> 16);
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// The attention kernel.  Per CTA one copy warp (tiles by TMA into a ring of
+// stages), one product warp (S = Q K^T and O += P V on the tensor cores, S, P
+// and O in TMEM) and two softmax warpgroups, one row of a 128-row tile per
+// thread: the running maximum and sum of the softmax live in the thread's
+// registers, P overwrites S in TMEM as 16-bit weights, and O is rescaled only
+// when the maximum has risen by 2^RAISE_LOG2.
+template <int DP, int NQ, bool PAIR, bool PR, bool BF>
+__global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ AttnParams A) {
+  static_assert(!(NQ && (PAIR || PR)), "few rows make one tile, and prompts have many");
+  using SM = Smem<DP, NQ>;
+  constexpr int STAGES = SM::STAGES, BYTES = SM::BYTES, HALVES = DP / 64;
+  constexpr int ROWS = NQ ? NQ : PAIR ? 2 * TILE : TILE;
+  constexpr int TM_COLS = NQ ? 256 : 512;               // TMEM: S of both streams, then O
+  constexpr int S_COLS = NQ ? 64 : 128, O_AT = TM_COLS / 2;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  Ctrl& C = *reinterpret_cast<Ctrl*>(smem + SM::CTRL);
+  const uint32_t base = smem_addr(smem);
+  const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  auto bar = [&](unsigned long long* p) { return smem_addr(p); };
+
+  // ---- set-up: barriers, TMEM, and where this CTA's run of tiles starts
+  if (tid == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(bar(&C.full[i]), 1);
+      mbar_init(bar(&C.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(&C.q_full[i]), 1);
+      mbar_init(bar(&C.q_empty[i]), 1);
+      mbar_init(bar(&C.s_full[i]), 1);
+      mbar_init(bar(&C.p_full[i]), 4);
+      mbar_init(bar(&C.o_full[i]), 1);
+    }
+    mbar_init(bar(&C.drain), 1);
+    C.abort = 0;
+    C.start_b = 0;
+    C.start_at = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == MMA_WARP) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(&C.tmem)),
+                 "n"(TM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (NQ) {  // columns past the item's rows: finite, and never used
+    for (int i = tid; i < SM::P_AT / 16; i += THREADS)
+      reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  long long run = 0;  // tiles of this CTA (TREE, RING)
+  if (!PR) {
+    // thread t sums requests t * per .. of the batch
+    const int per = (A.B + THREADS - 1) / THREADS;
+    const int b0 = min(tid * per, A.B), b1 = min(b0 + per, A.B);
+    const long long items = (long long)A.MT * A.Hkv;
+    long long mine = 0;
+    int bad, pos;
+    for (int b = b0; b < b1; ++b)
+      mine += items * (tiles_of(cache_len(A, b, bad, pos)) + tiles_of(A.N) + ITEM_COST);
+    long long incl = mine;
+    for (int x = 1; x < 32; x <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, x);
+      if (lane >= x) incl += y;
+    }
+    if (lane == 31) C.scan[warp] = incl;
+    __syncthreads();
+    long long total = 0, before = incl - mine;
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) before += C.scan[w];
+      total += C.scan[w];
+    }
+    const long long ctas = min((long long)gridDim.x, total), c = blockIdx.x;
+    const long long lo = c < ctas ? c * total / ctas : total;
+    const long long hi = c < ctas ? (c + 1) * total / ctas : total;
+    run = hi - lo;
+    if (run > 0 && lo >= before && lo < before + mine) {
+      long long at = before;
+      for (int b = b0; b < b1; ++b) {
+        const long long t = items * (tiles_of(cache_len(A, b, bad, pos)) + tiles_of(A.N) + ITEM_COST);
+        if (lo < at + t) {
+          C.start_b = b;
+          C.start_at = lo - at;
+          break;
+        }
+        at += t;
+      }
+    }
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = C.tmem;
+  const int start_b = C.start_b;
+  const long long start_at = C.start_at;
+  volatile int* abort = &C.abort;
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
+    // ------------------------------------------------------------ softmax
+    const int st = warp >> 2;             // the stream of this warpgroup
+    const int row = tid & (TILE - 1);     // query row of the tile, and key of a value tile
+    const int rt = row / A.G, rg = row - rt * A.G;
+    const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's TMEM lanes
+    const uint32_t ts = tmem + lanes + st * S_COLS, to = tmem + lanes + O_AT + st * S_COLS;
+    Cursor<PAIR, PR> cur;
+    cur.open(A, start_b, start_at, run);
+    Seg s;
+    uint32_t idx = 0;
+    int segs = 0, parent_b = -1, parent_bad = 0;
+    unsigned s_use = 0, o_use[2] = {0, 0};
+    bool ok = true;
+    int d_flags = 0, d_item = 0, d_b = 0;
+    while (ok && cur.next(A, s)) {
+      const int n = s.n;
+      const int tpi = PAIR ? 2 * A.tpt : A.tpt;
+      const int tok = s.mt * tpi + (PAIR ? st * A.tpt : 0) + rt;  // this row's token
+      const int tokens = PR ? s.len : A.N;
+      const bool active = rt < A.tpt && tok < tokens;
+      const bool warp_active = __any_sync(0xffffffffu, active);
+      const int ct = tiles_of(s.len);
+      int bad = s.bad;
+      if (!PR && A.kind == TREE) {
+        // pages in use by this segment, and the parent array
+        int pages_bad = 0;
+        const int t1 = min(s.len, (s.j0 + n) * TILE);
+        if (s.j0 * TILE < t1)
+          for (int c = s.j0 * TILE / A.page + row; c <= (t1 - 1) / A.page; c += TILE) {
+            const int pg = __ldg(A.table + size_t(s.b) * A.cols + c);
+            pages_bad |= pg < 0 || pg >= A.num_pages;
+          }
+        if (A.parent && s.b != parent_b && s.j0 + n > ct) {
+          if (NQ && row < 64) C.few.sees[st][row] = 0;
+          int wrong = 0;
+          for (int i = row; i < A.N; i += TILE) {
+            const int p = __ldg(A.parent + size_t(s.b) * A.N + i);
+            const bool w = i == 0 ? p != -1 : (p < 0 || p >= i);
+            wrong |= w;
+            C.parent[st][i] = uint8_t(w || i == 0 ? 0 : p);
+          }
+          parent_bad = group_or(1 + st, TILE, wrong) ? SV_ST_BAD_TOKEN : 0;
+          parent_b = s.b;
+          if (NQ) {  // column `row` sees its token and those above it
+            if (row < A.N * A.G)
+              for (int i = row / A.G;; i = C.parent[st][i]) {
+                atomicOr(&C.few.sees[st][i], 1ull << row);
+                if (i == 0) break;
+              }
+            group_sync(1 + st, TILE);
+          }
+        }
+        if (group_or(1 + st, TILE, pages_bad)) bad |= SV_ST_BAD_PAGE;
+        if (s.j0 + n > ct && A.parent) bad |= parent_bad;
+      }
+      if (bad && tid == 0) set_status(A.status, bad);
+      // RING: the ring slot after the newest entry holds the oldest
+      int ring_at = -1;
+      if (!PR && A.kind == RING && !s.bad && s.pos > A.sink) ring_at = (s.pos - A.sink) % A.window;
+      const bool ring_full = ring_at >= 0 && s.pos - A.sink >= A.window;
+      const int q0 = s.mt * tpi, q1 = min(q0 + tpi, tokens) - 1;  // the item's tokens
+      const int w0 = q0 + (PAIR ? st * A.tpt : 0), w1 = min(w0 + A.tpt, tokens) - 1;  // the tile's
+
+      float m = -INFINITY, l = 0.0f;
+      float lq[NQ ? NQ : 1];  // NQ > 0: this key's share of the columns' sums
+      bool unset = true;      // NQ > 0: a column has seen nothing yet
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) lq[q] = 0.0f;
+      int done = 0;
+      for (int jj = PAIR ? 0 : st; jj < n; jj += PAIR ? 1 : 2, ++done) {
+        const int j = s.j0 + jj;
+        const int k0 = PR ? (j < s.near ? j : s.lo + (j - s.near)) * TILE
+                                        : (j < ct ? j : j - ct) * TILE;
+        // does the tile need a mask, and value rows that no query of the item sees zeroed?
+        bool masked, clean = false, dead = false;
+        if (PR) {
+          masked = k0 + TILE - 1 > w0 || (k0 <= w1 - A.window && k0 + TILE > A.sink);
+          clean = k0 + TILE - 1 > q1 || (k0 <= q0 - A.window && k0 + TILE > A.sink);
+          dead = k0 + row > q1 || (k0 + row <= q0 - A.window && k0 + row >= A.sink);
+        } else if (j >= ct) {
+          masked = true;
+        } else {
+          masked = clean = k0 + TILE > s.len;
+          dead = k0 + row >= s.len;
+          if (ring_at >= 0) {
+            const int a = A.sink + ring_at, e = ring_at + A.N - A.window;
+            masked |= (k0 < a + A.N && k0 + TILE > a) || (e > 0 && k0 < A.sink + e && k0 + TILE > A.sink);
+            if (ring_full) {
+              clean |= a >= k0 && a < k0 + TILE;
+              dead |= k0 + row == a;
+            }
+          }
+        }
+        if (!warp_wait(bar(&C.s_full[st]), s_use & 1, A.status, abort)) {
+          ok = false;
+          break;
+        }
+        ++s_use;
+        tc_after();
+        // (The scores' keys have arrived, and so has every copy before them, among
+        // them the last one into this tile's stage: its phase is the next.)
+        if (clean && (!PAIR || st == 0)) {
+          const uint32_t u = idx + v_order<PAIR>(jj, n);
+          if (!warp_wait(bar(&C.full[u % STAGES]), (u / STAGES) & 1, A.status, abort)) {
+            ok = false;
+            break;
+          }
+          if (dead) {
+            uint4* v = reinterpret_cast<uint4*>(smem + SM::STAGE_AT + (u % STAGES) * BYTES + row * 128);
+#pragma unroll
+            for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[x * 1024 + i] = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        if constexpr (NQ > 0) {
+          // one key per thread, all rows
+          unsigned long long sees = ~0ull;
+          if (masked) {
+            const int k = k0 + row;
+            if (j < ct) {
+              if (k >= s.len) {
+                sees = 0;
+              } else if (ring_at >= 0 && k >= A.sink) {
+                int v = k - A.sink - ring_at;  // tokens that still have the slot in their window
+                if (v < 0) v += A.window;
+                if (v < A.N) sees = (1ull << (v * A.G)) - 1;
+              }
+            } else if (k >= A.N) {
+              sees = 0;
+            } else {
+              sees = A.parent ? C.few.sees[st][k] : ~0ull << (k * A.G);
+            }
+          }
+          softmax_few<NQ, BF>(A, C, st, row, ts, to, sees, masked, done > 0, unset, lq,
+                          smem + SM::P_AT + st * SM::P_BYTES);
+        } else if (warp_active) {
+          uint32_t r[4][32];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) tm_ld32(ts + x * 32, r[x]);
+          tm_wait_ld(r[0]);
+          tm_loaded(r[1]);
+          tm_loaded(r[2]);
+          tm_loaded(r[3]);
+          if (masked) {
+            uint32_t see[4] = {0, 0, 0, 0};
+            if (PR) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                see[x] = span(0, min(A.sink, tok + 1), k0 + 32 * x) |
+                         span(tok - A.window + 1, tok + 1, k0 + 32 * x);
+            } else if (j < ct) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                see[x] = span(0, s.len, k0 + 32 * x);
+                if (ring_at >= 0)
+                  see[x] &= ~(span(A.sink + ring_at, A.sink + min(ring_at + tok + 1, A.window),
+                                   k0 + 32 * x) |
+                              span(A.sink, A.sink + ring_at + tok + 1 - A.window, k0 + 32 * x));
+              }
+            } else if (A.parent) {
+              for (int i = active ? tok : 0;; i = C.parent[st][i]) {
+                const int y = i - k0;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  if (y >= 32 * x && y < 32 * x + 32) see[x] |= 1u << (y & 31);
+                if (i == 0) break;
+              }
+            } else {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) see[x] = span(0, tok + 1, k0 + 32 * x);
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(see[x] >> i & 1)) r[x][i] = 0xff800000u;
+          }
+          float mx[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            mx[x] = __uint_as_float(r[x][0]);
+#pragma unroll
+            for (int i = 1; i < 32; ++i) mx[x] = fmaxf(mx[x], __uint_as_float(r[x][i]));
+          }
+          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          if (done == 0) {
+            m = mt;
+          } else {
+            const bool rise = active && (mt - m) * A.c > RAISE_LOG2;  // (-inf before: inf > 8)
+            if (__any_sync(0xffffffffu, rise)) {
+              const float f = rise ? ex2((m - mt) * A.c) : 1.0f;
+              if (rise) m = mt;
+              l *= f;
+#pragma unroll
+              for (int x = 0; x < DP / 32; ++x) {
+                uint32_t o[32];
+                tm_ld32(to + x * 32, o);
+                tm_wait_ld(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tm_st32(to + x * 32, o);
+              }
+            }
+          }
+          const float mc = m == -INFINITY ? 0.0f : m * A.c;
+          const float2 c2 = make_float2(A.c, A.c), mc2 = make_float2(-mc, -mc);
+          float2 sum[2] = {make_float2(0, 0), make_float2(0, 0)};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 e = fma2(make_float2(__uint_as_float(r[x][2 * i]),
+                                                __uint_as_float(r[x][2 * i + 1])), c2, mc2);
+              const float2 p = make_float2(ex2(e.x), ex2(e.y));
+              sum[i & 1] = add2(sum[i & 1], p);
+              w[i] = pack16<BF>(p.x, p.y);
+            }
+            tm_st16(ts + x * 16, w);
+          }
+          sum[0] = add2(sum[0], sum[1]);
+          l += sum[0].x + sum[0].y;
+          tm_wait_st();
+        }
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(&C.p_full[st]));
+      }
+
+      // ---- the segment's end: the output rows, or their partials
+      const bool whole = n == s.nt;
+      const int slot = segs == 0 ? 0 : 1;
+      const size_t part = (size_t(blockIdx.x) * 2 + slot) * ROWS + (PAIR ? st * TILE : 0) + row;
+      const size_t token_row = PR ? size_t(s.start) + tok : size_t(s.b) * A.N + tok;
+      uint16_t* const orow = A.out + (token_row * A.Hq + s.h * A.G + rg) * A.D;
+      float4* const prow = reinterpret_cast<float4*>(A.part_o);
+      const size_t pcol0 = (size_t(blockIdx.x) * 2 + slot) * (DP / 4);
+      auto put = [&](const float (&v)[32], int col) {  // 32 columns from col on
+        if (whole) {
+          if (!active) return;
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            if (col + i < A.D) {
+              uint4 o;
+              o.x = pack16<BF>(v[i], v[i + 1]);
+              o.y = pack16<BF>(v[i + 2], v[i + 3]);
+              o.z = pack16<BF>(v[i + 4], v[i + 5]);
+              o.w = pack16<BF>(v[i + 6], v[i + 7]);
+              *reinterpret_cast<uint4*>(orow + col + i) = bad ? make_uint4(0, 0, 0, 0) : o;
+            }
+        } else if (active) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            prow[(pcol0 + (col + i) / 4) * ROWS + (PAIR ? st * TILE : 0) + row] =
+                make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
+      };
+      if constexpr (NQ > 0) {
+        for (int x = 0; x < 2; ++x) {
+          if (x >= n) break;
+          ok = ok && warp_wait(bar(&C.o_full[x]), o_use[x] & 1, A.status, abort);
+          ++o_use[x];
+        }
+        tc_after();
+        // sums over the keys: 32 lanes here, the four warps and two streams below
+        float* const sums = reinterpret_cast<float*>(smem + SM::P_AT);  // [stream][warp][NQ]
+        sum_columns<NQ>(lq, lane);
+        if (lane < NQ) {
+          sums[(st * 4 + (warp & 3)) * NQ + lane] = lq[0];
+          if (NQ == 64) sums[(st * 4 + (warp & 3)) * NQ + 32 + lane] = lq[NQ / 2];
+        }
+        group_sync(3, 2 * TILE);
+        if (tid < NQ) {
+          float l0 = 0.0f, l1 = 0.0f;
+          for (int w = 0; w < 4; ++w) {
+            l0 += sums[w * NQ + tid];
+            l1 += sums[(4 + w) * NQ + tid];
+          }
+          float a = -C.few.nmc[0][tid], b = n > 1 ? -C.few.nmc[1][tid] : INFINITY;
+          if (a == INFINITY) a = -INFINITY;  // nothing seen
+          if (b == INFINITY) b = -INFINITY;
+          const float mm = fmaxf(a, b), mu = mm == -INFINITY ? 0.0f : mm;
+          float f0 = ex2(a - mu), f1 = ex2(b - mu);
+          const float ll = l0 * f0 + (n > 1 ? l1 * f1 : 0.0f);
+          if (whole) {
+            f0 /= ll;
+            f1 /= ll;
+          }
+          C.few.fac[0][tid] = f0;
+          C.few.fac[1][tid] = f1;
+          if (!whole)
+            A.part_ml[(size_t(blockIdx.x) * 2 + slot) * NQ + tid] =
+                make_float2(mm, bad ? -1.0f : ll);
+        }
+        group_sync(3, 2 * TILE);
+        if (ok) {
+          constexpr int HALF = NQ / 2;  // columns of this warpgroup
+          const int q0 = st * HALF;
+          uint32_t o0[HALF], o1[HALF];
+          tm_ldn<HALF>(tmem + lanes + O_AT + q0, o0);
+          if (n > 1) tm_ldn<HALF>(tmem + lanes + O_AT + S_COLS + q0, o1);
+          tm_waitn<HALF>(o0);
+          if (n > 1) tm_loadedn<HALF>(o1);
+#pragma unroll
+          for (int q = 0; q < HALF; ++q) {
+            float v = __uint_as_float(o0[q]) * C.few.fac[0][q0 + q];
+            if (n > 1) v = fmaf(__uint_as_float(o1[q]), C.few.fac[1][q0 + q], v);
+            o0[q] = __float_as_uint(v);
+          }
+          if (!whole) {
+            float* const to_part =
+                A.part_o + ((size_t(blockIdx.x) * 2 + slot) * NQ + q0) * DP + row;
+            if (row < DP) {
+#pragma unroll
+              for (int q = 0; q < HALF; ++q) to_part[q * DP] = __uint_as_float(o0[q]);
+            }
+          } else if (row < A.D) {
+            // column q is token q / G, head q mod G of the group
+            const int t = q0 / A.G, rows = A.N * A.G - q0;
+            int g = q0 - t * A.G;
+            uint16_t* o = A.out + ((size_t(s.b) * A.N + t) * A.Hq + s.h * A.G + g) * A.D + row;
+            const size_t wrap = size_t(A.Hq - A.G) * A.D;
+#pragma unroll
+            for (int q = 0; q < HALF; ++q) {
+              if (q < rows) *o = bad ? 0 : uint16_t(pack16<BF>(__uint_as_float(o0[q]), 0.0f));
+              o += A.D;
+              if (++g == A.G) {
+                g = 0;
+                o += wrap;
+              }
+            }
+          }
+        }
+        tc_before();
+      } else if (PAIR) {
+        ok = ok && warp_wait(bar(&C.o_full[st]), o_use[st] & 1, A.status, abort);
+        ++o_use[st];
+        tc_after();
+        if (ok && warp_active) {
+          const float f = whole ? 1.0f / l : 1.0f;
+#pragma unroll
+          for (int x = 0; x < DP / 32; ++x) {
+            uint32_t o[32];
+            float v[32];
+            tm_ld32(to + x * 32, o);
+            tm_wait_ld(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * f;
+            put(v, x * 32);
+          }
+          if (!whole && active) A.part_ml[part] = make_float2(m * A.c, bad ? -1.0f : l);
+        }
+        tc_before();
+      } else {
+        // join the two streams; warpgroup st takes half of the columns
+        C.ml[st][row] = make_float2(m, l);
+        for (int x = 0; x < 2; ++x) {
+          if (x >= n) break;
+          ok = ok && warp_wait(bar(&C.o_full[x]), o_use[x] & 1, A.status, abort);
+          ++o_use[x];
+        }
+        tc_after();
+        group_sync(3, 2 * TILE);
+        if (ok && warp_active) {
+          const float2 a = C.ml[0][row], b = C.ml[1][row];
+          const float mm = fmaxf(a.x, b.x);
+          const float mu = mm == -INFINITY ? 0.0f : mm;
+          float f0 = ex2((a.x - mu) * A.c), f1 = ex2((b.x - mu) * A.c);
+          const float ll = a.y * f0 + (n > 1 ? b.y * f1 : 0.0f);
+          if (whole) {
+            f0 /= ll;
+            f1 /= ll;
+          }
+          const uint32_t t0 = tmem + lanes + O_AT;
+#pragma unroll
+          for (int x = 0; x < DP / 64; ++x) {
+            const int col = st * (DP / 2) + x * 32;
+            uint32_t o[32];
+            float v[32];
+            tm_ld32(t0 + col, o);
+            tm_wait_ld(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * f0;
+            if (n > 1) {
+              tm_ld32(t0 + S_COLS + col, o);
+              tm_wait_ld(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(o[i]), f1, v[i]);
+            }
+            put(v, col);
+          }
+          if (!whole && st == 0 && active) A.part_ml[part] = make_float2(mm * A.c, bad ? -1.0f : ll);
+        }
+        tc_before();
+      }
+      if (segs == 0) {
+        d_item = s.h * A.MT + s.mt;
+        d_b = s.b;
+        if (s.j0 > 0) d_flags |= DESC_IN;
+        if (s.j0 > 0 && s.j0 + n < s.nt) d_flags |= DESC_THROUGH;
+      } else {
+        d_flags |= DESC_LAST1;
+      }
+      d_flags = s.j0 + n < s.nt ? d_flags | DESC_OUT : d_flags & ~DESC_OUT;
+      idx += 2 * n;
+      ++segs;
+      // The warps go on, or stop after a wait that gave up, together; and (two
+      // streams over one O) both have read O before either lets it be overwritten.
+      ok = !group_or(PAIR ? 1 + st : 3, PAIR ? TILE : 2 * TILE, !ok);
+      tc_after();
+    }
+    if (!PR && tid == 0) A.desc[blockIdx.x] = make_int4(d_flags, d_item, d_b, 0);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
+  if (warp == COPY_WARP) {
+    // ------------------------------------------------------------ copies
+    Cursor<PAIR, PR> cur;
+    cur.open(A, start_b, start_at, run, blockIdx.x == 0);
+    Seg s;
+    uint32_t idx = 0;   // copies issued (low bits: stage and phase)
+    int segs = 0;
+    bool ok = true;
+    auto tile = [&](const Seg& s, int jj, bool is_v) {
+      const uint32_t st = idx % STAGES, use = idx / STAGES;
+      const uint32_t fb = bar(&C.full[st]);
+      const uint32_t dst = base + SM::STAGE_AT + st * BYTES;
+      if (use > 0 && !warp_wait(bar(&C.empty[st]), (use - 1) & 1, A.status, abort)) return false;
+      const int j = s.j0 + jj;
+      if (PR) {
+        const int t = j < s.near ? j : s.lo + (j - s.near);
+        if (elect_one()) {
+          mbar_arrive_tx(fb, BYTES);
+          for (int x = 0; x < HALVES; ++x)
+            tma_3d(dst + x * 16384, is_v ? &A.mv : &A.mk, fb, x * 64, s.h, s.start + t * TILE);
+        }
+      } else {
+        const int ct = tiles_of(s.len);
+        if (j >= ct) {
+          if (elect_one()) {
+            mbar_arrive_tx(fb, BYTES);
+            for (int x = 0; x < HALVES; ++x)
+              tma_3d(dst + x * 16384, is_v ? &A.mvn : &A.mkn, fb, x * 64, (j - ct) * TILE,
+                     s.b * A.LH + A.head0 + s.h);
+          }
+        } else if (A.kind == RING) {
+          if (elect_one()) {
+            mbar_arrive_tx(fb, BYTES);
+            for (int x = 0; x < HALVES; ++x)
+              tma_3d(dst + x * 16384, is_v ? &A.mv : &A.mk, fb, x * 64, j * TILE,
+                     s.b * A.LH + A.head0 + s.h);
+          }
+        } else {
+          // one lane per box of page rows; a page outside the pool is read as
+          // page 0 (the softmax warps report it and drop the result)
+          const int boxes = min(TILE, s.len - j * TILE + A.box - 1) / A.box;
+          if (lane == 0) mbar_arrive_tx(fb, boxes * A.box * DP * 2);
+          __syncwarp();
+          if (lane < boxes) {
+            const int t = j * TILE + lane * A.box;
+            const int col = t / A.page;
+            int pg = __ldg(A.table + size_t(s.b) * A.cols + col);
+            if (pg < 0 || pg >= A.num_pages) pg = 0;
+            for (int x = 0; x < HALVES; ++x)
+              tma_4d(dst + x * 16384 + lane * A.box * 128, is_v ? &A.mv : &A.mk, fb, x * 64,
+                     t - col * A.page, A.head0 + s.h, pg);
+          }
+        }
+      }
+      __syncwarp();
+      ++idx;
+      return true;
+    };
+    while (ok && cur.next(A, s, blockIdx.x == 0)) {
+      const int slot = PAIR ? 0 : segs & 1;
+      const int use = PAIR ? segs : segs >> 1;
+      if (use > 0 && !warp_wait(bar(&C.q_empty[slot]), (use - 1) & 1, A.status, abort)) break;
+      if (elect_one()) {
+        const uint32_t fb = bar(&C.q_full[slot]);
+        mbar_arrive_tx(fb, (PAIR ? 2 : 1) * A.q_rows * DP * 2);
+        const int tok = PR ? s.start : s.b * A.N;
+        for (int q = 0; q < (PAIR ? 2 : 1); ++q)
+          for (int x = 0; x < HALVES; ++x)
+            tma_4d(base + (PAIR ? q : slot) * SM::Q_BYTES + x * (SM::Q_BYTES / HALVES), &A.mq, fb, x * 64, 0, s.h,
+                   tok + (s.mt * (PAIR ? 2 : 1) + q) * A.tpt);
+      }
+      __syncwarp();
+      ++segs;
+      constexpr int LAG = PAIR ? 0 : 1;
+      for (int i = 0; ok && i < s.n + LAG; ++i) {
+        if (i < s.n) ok = tile(s, i, false);
+        if (ok && i >= LAG) ok = tile(s, i - LAG, true);
+      }
+    }
+    if (*abort) {  // the copies in flight land before the CTA ends
+      const unsigned long long t0 = globaltimer();
+      for (uint32_t u = idx > STAGES ? idx - STAGES : 0; u < idx; ++u)
+        while (!mbar_try(bar(&C.full[u % STAGES]), (u / STAGES) & 1) &&
+               globaltimer() - t0 < WAIT_LIMIT_NS) {
+        }
+      for (int u = max(0, segs - (PAIR ? 1 : 2)); u < segs; ++u)
+        while (!mbar_try(bar(&C.q_full[PAIR ? 0 : u & 1]), (PAIR ? u : u >> 1) & 1) &&
+               globaltimer() - t0 < WAIT_LIMIT_NS) {
+        }
+    }
+  } else if (warp == MMA_WARP) {
+    // ------------------------------------------------------------ products
+    Cursor<PAIR, PR> cur;
+    cur.open(A, start_b, start_at, run);
+    Seg s;
+    uint32_t idx = 0;
+    int segs = 0;
+    unsigned p_use[2] = {0, 0};
+    // (the turned products: N = NQ, and V^T is an operand whose dimensions are contiguous)
+    const uint32_t id_s = instr_desc(BF, false, false, NQ ? NQ : TILE);
+    const uint32_t id_o = instr_desc(BF, NQ > 0, NQ == 0, NQ ? NQ : DP);
+    bool ok = true;
+    auto full = [&](uint32_t u) {
+      if (!warp_wait(bar(&C.full[u % STAGES]), (u / STAGES) & 1, A.status, abort)) return false;
+      tc_after();
+      return true;
+    };
+    auto scores = [&](int st, int q, uint32_t u) {  // S[st] = Q[q] K^T, or K Q[q]^T
+      const uint64_t qa = desc_rows(base + q * SM::Q_BYTES);
+      const uint64_t ka = desc_rows(base + SM::STAGE_AT + (u % STAGES) * BYTES);
+#pragma unroll
+      for (int k = 0; k < DP / 16; ++k) {
+        const uint64_t dq = qa + (((k / 4) * (SM::Q_BYTES / HALVES) + (k % 4) * 32) >> 4);
+        const uint64_t dk = ka + (((k / 4) * 16384 + (k % 4) * 32) >> 4);
+        mma_ss(tmem + st * S_COLS, NQ ? dk : dq, NQ ? dq : dk, id_s, k > 0);
+      }
+      mma_commit(bar(&C.s_full[st]));
+    };
+    auto values = [&](int st, uint32_t u, bool more) {  // O[st] (+)= P[st] V, or V^T P[st]^T
+      const uint64_t va = desc_cols(base + SM::STAGE_AT + (u % STAGES) * BYTES,
+                                    NQ && DP == 64 ? 0 : 16384);
+      const uint64_t pa = desc_rows(base + SM::P_AT + st * SM::P_BYTES);
+#pragma unroll
+      for (int k = 0; k < TILE / 16; ++k) {
+        const uint64_t dv = va + ((k * 2048) >> 4);
+        const uint64_t dp = pa + (((k / 4) * (NQ * 128) + (k % 4) * 32) >> 4);
+        if (NQ) mma_ss(tmem + O_AT + st * S_COLS, dv, dp, id_o, more || k > 0);
+        else mma_ts(tmem + O_AT + st * S_COLS, tmem + st * S_COLS + k * 8, dv, id_o, more || k > 0);
+      }
+    };
+    while (ok && cur.next(A, s)) {
+      const int slot = PAIR ? 0 : segs & 1;
+      const int use = PAIR ? segs : segs >> 1;
+      ok = warp_wait(bar(&C.q_full[slot]), use & 1, A.status, abort);
+      const int n = s.n;
+      const uint32_t u0 = idx;
+      if (PAIR) {
+        ok = ok && full(u0);
+        if (ok && elect_one()) {
+          scores(0, 0, u0);
+          scores(1, 1, u0);
+          mma_commit(bar(&C.empty[u0 % STAGES]));
+          if (n == 1) mma_commit(bar(&C.q_empty[0]));
+        }
+        __syncwarp();
+        for (int j = 0; ok && j < n; ++j) {
+          const uint32_t uv = u0 + v_order<true>(j, n), uk = u0 + k_order<true>(j + 1);
+          ok = full(uv);
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            ok = ok && warp_wait(bar(&C.p_full[st]), p_use[st] & 1, A.status, abort);
+            ++p_use[st];
+            if (!ok) break;
+            tc_after();
+            if (elect_one()) {
+              values(st, uv, j > 0);
+              if (st == 1) mma_commit(bar(&C.empty[uv % STAGES]));
+              if (j + 1 == n) mma_commit(bar(&C.o_full[st]));
+            }
+            __syncwarp();
+            if (j + 1 < n) {
+              if (st == 0 && !(ok = full(uk))) break;
+              if (elect_one()) {
+                scores(st, st, uk);
+                if (st == 1) {
+                  mma_commit(bar(&C.empty[uk % STAGES]));
+                  if (j + 2 == n) mma_commit(bar(&C.q_empty[0]));
+                }
+              }
+              __syncwarp();
+            }
+          }
+        }
+      } else {
+        for (int j = 0; ok && j < 2 && j < n; ++j) {
+          const uint32_t uk = u0 + k_order<false>(j);
+          ok = full(uk);
+          if (ok && elect_one()) {
+            scores(j, slot, uk);
+            mma_commit(bar(&C.empty[uk % STAGES]));
+            if (j + 1 == n) mma_commit(bar(&C.q_empty[slot]));
+          }
+          __syncwarp();
+        }
+        for (int j = 0; ok && j < n; ++j) {
+          const int st = j & 1;
+          const uint32_t uv = u0 + v_order<false>(j, n), uk = u0 + k_order<false>(j + 2);
+          ok = full(uv) && warp_wait(bar(&C.p_full[st]), p_use[st] & 1, A.status, abort);
+          ++p_use[st];
+          if (!ok) break;
+          tc_after();
+          if (elect_one()) {
+            values(st, uv, j >= 2);
+            mma_commit(bar(&C.empty[uv % STAGES]));
+            if (j + 2 >= n) mma_commit(bar(&C.o_full[st]));
+          }
+          __syncwarp();
+          if (j + 2 < n) {
+            ok = full(uk);
+            if (ok && elect_one()) {
+              scores(st, slot, uk);
+              mma_commit(bar(&C.empty[uk % STAGES]));
+              if (j + 3 == n) mma_commit(bar(&C.q_empty[slot]));
+            }
+            __syncwarp();
+          }
+        }
+      }
+      idx += 2 * n;
+      ++segs;
+    }
+    if (!ok && lane == 0) {  // the products in flight end before TMEM is freed
+      mma_commit(bar(&C.drain));
+      const unsigned long long t0 = globaltimer();
+      while (!mbar_try(bar(&C.drain), 0) && globaltimer() - t0 < WAIT_LIMIT_NS) {
+      }
+    }
+    __syncwarp();
+    }
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == MMA_WARP)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "n"(TM_COLS)
+                 : "memory");
+}
+
+// Join of the items that the CTAs' runs cut, from the parts' maxima, sums and
+// outputs.  A warp takes one unit of a cut item at a time: one row's columns, a
+// lane each four of them (NQ > 0), or 32 rows' 16 columns, a lane each a row.
+// First the common maximum and the sum, then the outputs, so that the loads of
+// different parts do not wait for one another.
+constexpr int JOIN_WARPS = 8;
+template <int DP, int NQ, bool PAIR, bool BF>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) sv_attn_join(const __grid_constant__ AttnParams A,
+                                                               int ctas) {
+  constexpr int ROWS = NQ ? NQ : PAIR ? 2 * TILE : TILE;
+  constexpr int VECS = NQ ? 1 : 4;  // four-column pieces per lane
+  __shared__ int2 cuts[MAX_CTAS];   // (first CTA of the item, CTAs of it)
+  __shared__ int found_s[JOIN_WARPS];
+  const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The cut items, in the order of their first CTAs (every block has to find
+  // the same list).  CTA c holds an item's first part when its last segment is
+  // cut and did not itself begin inside the item.
+  static_assert(MAX_CTAS <= JOIN_WARPS * 32, "one thread per CTA of the main kernel");
+  int parts = 0;
+  if (tid + 1 < ctas) {
+    const int4 d = A.desc[tid];
+    if ((d.x & DESC_OUT) && !(d.x & DESC_THROUGH)) {
+      int e = tid + 1;
+      while (e + 1 < ctas && (A.desc[e].x & DESC_THROUGH)) ++e;
+      parts = e - tid + 1;
+    }
+  }
+  const unsigned found = __ballot_sync(0xffffffffu, parts != 0);
+  if (lane == 0) found_s[warp] = __popc(found);
+  __syncthreads();
+  int at = __popc(found & ((1u << lane) - 1)), count = 0;
+  for (int w = 0; w < JOIN_WARPS; ++w) {
+    if (w < warp) at += found_s[w];
+    count += found_s[w];
+  }
+  if (parts) cuts[at] = make_int2(tid, parts);
+  __syncthreads();
+  const int row_groups = (min(A.tpt, A.N) * A.G + 31) / 32;
+  const int per_item = NQ ? A.N * A.G : row_groups * (PAIR ? 2 : 1) * (DP / 16);
+  const int units = count * per_item;
+  const float4* const src = reinterpret_cast<const float4*>(A.part_o);
+  // neighbouring units on different SMs
+  for (int u = int(blockIdx.x + gridDim.x * warp); u < units; u += int(gridDim.x) * JOIN_WARPS) {
+    const int2 cut = cuts[u / per_item];
+    const int w = u % per_item;
+    const int cg = w % (DP / 16), rgp = w / (DP / 16);
+    const int st = PAIR ? rgp / row_groups : 0;
+    const int row = NQ ? w : (rgp % row_groups) * 32 + lane;
+    const int4 d1 = A.desc[cut.x + 1];  // its first segment is of this item
+    const int item = d1.y, b = d1.z;
+    const int h = item / A.MT, mt = item - h * A.MT;
+    const int rt = row / A.G, rg = row - rt * A.G;
+    const int tok = mt * (PAIR ? 2 : 1) * A.tpt + st * A.tpt + rt;
+    if (NQ ? lane >= DP / 4 : row >= TILE || rt >= A.tpt || tok >= A.N) continue;
+    const size_t s0 = size_t(cut.x) * 2 + (A.desc[cut.x].x & DESC_LAST1 ? 1 : 0);
+    auto slot = [&](int p) { return p ? size_t(cut.x + p) * 2 : s0; };
+    float m = -INFINITY, l = 0.0f;
+    bool bad = false;
+#pragma unroll 4
+    for (int p = 0; p < cut.y; ++p) {
+      const float2 ml = A.part_ml[slot(p) * ROWS + st * TILE + row];
+      bad |= ml.y == -1.0f;
+      m = fmaxf(m, ml.x);
+    }
+    if (m == -INFINITY) m = 0.0f;
+    float4 acc[VECS];
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) acc[i] = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int p = 0; p < cut.y; ++p) {
+      const size_t s = slot(p);
+      const float2 ml = A.part_ml[s * ROWS + st * TILE + row];
+      const float g = ex2(ml.x - m);
+      l += ml.y * g;
+#pragma unroll
+      for (int i = 0; i < VECS; ++i) {
+        const float4 o = NQ ? src[(s * ROWS + row) * (DP / 4) + lane]
+                            : src[(s * (DP / 4) + cg * 4 + i) * ROWS + st * TILE + row];
+        acc[i].x += o.x * g;
+        acc[i].y += o.y * g;
+        acc[i].z += o.z * g;
+        acc[i].w += o.w * g;
+      }
+    }
+    const float f = 1.0f / l;
+    uint16_t* const o = A.out + ((size_t(b) * A.N + tok) * A.Hq + h * A.G + rg) * A.D;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+      const int col = NQ ? lane * 4 : cg * 16 + i * 4;
+      uint2 x = make_uint2(pack16<BF>(acc[i].x * f, acc[i].y * f),
+                           pack16<BF>(acc[i].z * f, acc[i].w * f));
+      if (bad) x = make_uint2(0, 0);
+      if (col < A.D) *reinterpret_cast<uint2*>(o + col) = x;
+    }
+  }
+}
+
+// -------------------------------------------------------------- launches
+
+// Columns of the turned products, or 0 for a row per lane; rows of an item.
+struct Layout { int nq, rows; };
+
+template <int DP, int NQ, bool PAIR, bool PR, bool BF>
+int launch_as(const AttnParams& A, int grid, int ctas, cudaStream_t st) {
+  if (cudaFuncSetAttribute(sv_attn<DP, NQ, PAIR, PR, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (Smem<DP, NQ>::TOTAL)) != cudaSuccess)
+    return SV_ERR_CUDA;
+  sv_attn<DP, NQ, PAIR, PR, BF><<<grid, THREADS, (Smem<DP, NQ>::TOTAL), st>>>(A);
+  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  if (PR) return SV_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(2 * ctas));
+  cfg.blockDim = dim3(JOIN_WARPS * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sv_attn_join<DP, NQ, PAIR, BF>, A, ctas) == cudaSuccess ? SV_OK
+                                                                                : SV_ERR_CUDA;
+}
+
+template <int DP, bool BF>
+int launch_dp(const AttnParams& A, Layout l, int grid, int ctas, cudaStream_t st) {
+  if (A.kind == PROMPT)
+    return l.rows == TILE ? launch_as<DP, 0, false, true, BF>(A, grid, ctas, st)
+                          : launch_as<DP, 0, true, true, BF>(A, grid, ctas, st);
+  if (l.nq == 16) return launch_as<DP, 16, false, false, BF>(A, grid, ctas, st);
+  if (l.nq == 32) return launch_as<DP, 32, false, false, BF>(A, grid, ctas, st);
+  if (l.nq == 64) return launch_as<DP, 64, false, false, BF>(A, grid, ctas, st);
+  if (l.rows == TILE) return launch_as<DP, 0, false, false, BF>(A, grid, ctas, st);
+  return launch_as<DP, 0, true, false, BF>(A, grid, ctas, st);
+}
+
+// One translation unit per storage type (attn_bf16.cu, attn_f16.cu), compiled
+// side by side.
+int launch_bf16(const AttnParams& A, Layout l, int grid, int ctas, cudaStream_t st);
+int launch_f16(const AttnParams& A, Layout l, int grid, int ctas, cudaStream_t st);
+
+}  // namespace svattn
+
+#endif  // SV_ATTENTION_CUH
