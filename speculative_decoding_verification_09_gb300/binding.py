@@ -127,7 +127,7 @@ def _dev(t: torch.Tensor | None, dtype: torch.dtype | None = None, name: str = "
 
 def _stream(stream, device) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        return torch._C._cuda_getCurrentRawStream(device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -172,11 +172,22 @@ def sv_set_stage_events(events) -> None:
     _check(lib().sv_set_stage_events(handles if events else None, len(events)))
 
 
-def _counts(B: int, **tensors) -> None:
-    """Each tensor has the given number of elements."""
-    for name, (t, n) in tensors.items():
-        if t is not None and t.numel() != n:
-            raise SpecVerifyError(f"{name} must have {n} elements, got {t.numel()}")
+def _buf(t: torch.Tensor, shape, dtype: torch.dtype, device, name: str) -> int:
+    """The address of a contiguous tensor of this shape and type on this device."""
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise SpecVerifyError(f"{name} must be contiguous {list(shape)} {dtype} on {device}, got "
+                              f"{list(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _status(t: torch.Tensor | None, device) -> int | None:
+    return None if t is None else _buf(t, t.shape, torch.int32, device, "dev_status")
+
+
+def _cuda_device(t: torch.Tensor, name: str):
+    if not t.is_cuda:
+        raise SpecVerifyError(f"{name} must be a CUDA tensor")
+    return t.device
 
 
 def _shapes(target_logits: torch.Tensor):
@@ -343,18 +354,14 @@ def sv_kv_fill(k, v, cu_seqlens, k_pool, v_pool, pos, sink: int, window: int, he
     if k.dim() != 3 or k_pool.dim() != 4:
         raise SpecVerifyError("k must be [T][Hkv][D], pools [B][LH][sink+window][D]")
     T, Hkv, D = k.shape
-    B, LH, C, Dp = k_pool.shape
-    if (tuple(v.shape) != tuple(k.shape) or tuple(v_pool.shape) != tuple(k_pool.shape) or Dp != D
-            or C != sink + window):
-        raise SpecVerifyError("KV shapes disagree")
-    if len({k.dtype, v.dtype, k_pool.dtype, v_pool.dtype}) != 1:
-        raise SpecVerifyError("KV buffers must share one dtype")
-    _counts(B, cu_seqlens=(cu_seqlens, B + 1), pos=(pos, B))
+    B, LH = k_pool.shape[:2]
+    dev, dt, pool = _cuda_device(k, "k"), k.dtype, (B, LH, sink + window, D)
     _check(lib().sv_kv_fill(
-        _dev(k, None, "k"), _dev(v, None, "v"), _dev(cu_seqlens, torch.int32, "cu_seqlens"),
-        _dev(k_pool, None, "k_pool"), _dev(v_pool, None, "v_pool"),
-        _dev(pos, torch.int32, "pos"), B, T, Hkv, LH, head0, D * k.element_size(), sink, window,
-        _dev(dev_status, torch.int32, "dev_status"), _stream(stream, k_pool.device)))
+        _buf(k, k.shape, dt, dev, "k"), _buf(v, k.shape, dt, dev, "v"),
+        _buf(cu_seqlens, (B + 1,), torch.int32, dev, "cu_seqlens"),
+        _buf(k_pool, pool, dt, dev, "k_pool"), _buf(v_pool, pool, dt, dev, "v_pool"),
+        _buf(pos, (B,), torch.int32, dev, "pos"), B, T, Hkv, LH, head0, D * k.element_size(),
+        sink, window, _status(dev_status, dev), _stream(stream, dev)))
 
 
 def sv_page_commit(k_pages, v_pages, k_new, v_new, block_table, seq_lens, nodes, num_accepted,
@@ -368,24 +375,19 @@ def sv_page_commit(k_pages, v_pages, k_new, v_new, block_table, seq_lens, nodes,
         raise SpecVerifyError("pages must be [P][LH][page][D], staged entries [B][LH][N][D], "
                               "block_table [B][cols]")
     P, LH, page, D = k_pages.shape
-    B, _, N, _ = k_new.shape
-    if (tuple(v_pages.shape) != tuple(k_pages.shape) or tuple(v_new.shape) != tuple(k_new.shape)
-            or tuple(k_new.shape) != (B, LH, N, D) or block_table.shape[0] != B):
-        raise SpecVerifyError("KV shapes disagree")
-    if nodes is not None and tuple(nodes.shape) != (B, N):
-        raise SpecVerifyError("nodes must be [B][N]")
-    if len({k_pages.dtype, v_pages.dtype, k_new.dtype, v_new.dtype}) != 1:
-        raise SpecVerifyError("KV buffers must share one dtype")
-    _counts(B, seq_lens=(seq_lens, B), num_accepted=(num_accepted, B),
-            out_seq_lens=(out_seq_lens, B))
+    B, N, cols = k_new.shape[0], k_new.shape[2], block_table.shape[1]
+    dev, dt, new = _cuda_device(k_pages, "k_pages"), k_pages.dtype, (B, LH, N, D)
+    i32 = torch.int32
     _check(lib().sv_page_commit(
-        _dev(k_pages, None, "k_pages"), _dev(v_pages, None, "v_pages"),
-        _dev(k_new, None, "k_new"), _dev(v_new, None, "v_new"),
-        _dev(block_table, torch.int32, "block_table"), _dev(seq_lens, torch.int32, "seq_lens"),
-        _dev(nodes, torch.int32, "nodes"), _dev(num_accepted, torch.int32, "num_accepted"),
-        B, LH, N, D * k_pages.element_size(), P, page, block_table.shape[1],
-        _dev(out_seq_lens, torch.int32, "out_seq_lens"),
-        _dev(dev_status, torch.int32, "dev_status"), _stream(stream, k_pages.device)))
+        _buf(k_pages, k_pages.shape, dt, dev, "k_pages"),
+        _buf(v_pages, k_pages.shape, dt, dev, "v_pages"), _buf(k_new, new, dt, dev, "k_new"),
+        _buf(v_new, new, dt, dev, "v_new"), _buf(block_table, (B, cols), i32, dev, "block_table"),
+        _buf(seq_lens, (B,), i32, dev, "seq_lens"),
+        None if nodes is None else _buf(nodes, (B, N), i32, dev, "nodes"),
+        _buf(num_accepted, (B,), i32, dev, "num_accepted"), B, LH, N,
+        D * k_pages.element_size(), P, page, cols,
+        _buf(out_seq_lens, (B,), i32, dev, "out_seq_lens"), _status(dev_status, dev),
+        _stream(stream, dev)))
 
 
 def sv_kv_valid_slots(pos, sink: int, window: int, out_slots, out_len, dev_status=None,
@@ -468,16 +470,14 @@ def sv_tree_set_warps(warps: int = 0) -> None:
 
 # ------------------------------------------------------- attention over the caches
 
-def _attn_dtype(q, *others) -> int:
-    if any(t.dtype != q.dtype for t in others):
-        raise SpecVerifyError("queries, keys, values and output must share one dtype")
-    if any(t.device != q.device for t in others):
-        raise SpecVerifyError("queries, keys, values and output must be on one device")
-    if q.dtype == torch.bfloat16:
-        return SV_BF16
-    if q.dtype == torch.float16:
-        return SV_F16
-    raise SpecVerifyError(f"attention takes bfloat16 or float16, got {q.dtype}")
+_ATTN_DTYPES = {torch.bfloat16: SV_BF16, torch.float16: SV_F16}
+
+
+def _attn_dtype(q) -> int:
+    dt = _ATTN_DTYPES.get(q.dtype)
+    if dt is None:
+        raise SpecVerifyError(f"attention takes bfloat16 or float16, got {q.dtype}")
+    return dt
 
 
 def sv_attn_workspace_bytes(N: int, Hq: int, Hkv: int, D: int) -> int:
@@ -493,18 +493,9 @@ def make_attn_workspace(B: int, N: int, Hq: int, Hkv: int, D: int, device) -> to
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _staged_shapes(q, k_cache, v_cache, k_new, v_new, out, head0, kv_heads):
-    """(B, N, Hq, Hkv, D, LH) of queries [B][N][Hq][D], a cache [..][LH][..][D] and staged
-    entries [B][LH][N][D]."""
-    if q.dim() != 4 or k_cache.dim() != 4 or k_new.dim() != 4:
-        raise SpecVerifyError("queries, caches and staged entries must have four dimensions")
-    B, N, Hq, D = q.shape
-    LH = k_cache.shape[1]
-    if (tuple(out.shape) != tuple(q.shape) or tuple(v_cache.shape) != tuple(k_cache.shape)
-            or k_cache.shape[3] != D or tuple(k_new.shape) != (B, LH, N, D)
-            or tuple(v_new.shape) != tuple(k_new.shape)):
-        raise SpecVerifyError("shapes of queries, cache, staged entries and output disagree")
-    return B, N, Hq, (LH - head0 if kv_heads is None else kv_heads), D, LH
+def _workspace(t: torch.Tensor, device) -> tuple[int, int]:
+    n = t.numel() * t.element_size()
+    return _buf(t, t.shape, t.dtype, device, "workspace"), n
 
 
 def sv_tree_attn(q, k_pages, v_pages, block_table, seq_lens, k_new, v_new, parent, out, workspace,
@@ -515,22 +506,27 @@ def sv_tree_attn(q, k_pages, v_pages, block_table, seq_lens, k_new, v_new, paren
     block_table [B][cols] and seq_lens [B] int32, staged k_new/v_new
     [B][LH][N][D]; KV heads are rows head0 .. head0 + kv_heads - 1 of LH (all
     from head0 when None); scale defaults to 1 / sqrt(D)."""
-    B, N, Hq, Hkv, D, LH = _staged_shapes(q, k_pages, v_pages, k_new, v_new, out, head0, kv_heads)
-    dt = _attn_dtype(q, k_pages, v_pages, k_new, v_new, out)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise SpecVerifyError("block_table must be [B][cols]")
-    if parent is not None and tuple(parent.shape) != (B, N):
-        raise SpecVerifyError("parent must be [B][N]")
-    _counts(B, seq_lens=(seq_lens, B))
+    if q.dim() != 4 or k_pages.dim() != 4 or block_table.dim() != 2:
+        raise SpecVerifyError("q must be [B][N][Hq][D], pages [P][LH][page][D], block_table "
+                              "[B][cols]")
+    code = _attn_dtype(q)
+    B, N, Hq, D = q.shape
+    P, LH, page, _ = k_pages.shape
+    cols = block_table.shape[1]
+    dev, dt, i32 = _cuda_device(q, "q"), q.dtype, torch.int32
+    pages, new = (P, LH, page, D), (B, LH, N, D)
+    ws, ws_bytes = _workspace(workspace, dev)
     _check(lib().sv_tree_attn(
-        dt, _dev(q, None, "q"), _dev(k_pages, None, "k_pages"), _dev(v_pages, None, "v_pages"),
-        _dev(block_table, torch.int32, "block_table"), _dev(seq_lens, torch.int32, "seq_lens"),
-        _dev(k_new, None, "k_new"), _dev(v_new, None, "v_new"),
-        _dev(parent, torch.int32, "parent"), D ** -0.5 if scale is None else scale, B, N, Hq, Hkv,
-        D, k_pages.shape[0], LH, head0, k_pages.shape[2], block_table.shape[1],
-        _dev(out, None, "out"), _dev(workspace, None, "workspace"),
-        workspace.numel() * workspace.element_size(),
-        _dev(dev_status, torch.int32, "dev_status"), _stream(stream, q.device)))
+        code, _buf(q, q.shape, dt, dev, "q"), _buf(k_pages, pages, dt, dev, "k_pages"),
+        _buf(v_pages, pages, dt, dev, "v_pages"),
+        _buf(block_table, (B, cols), i32, dev, "block_table"),
+        _buf(seq_lens, (B,), i32, dev, "seq_lens"), _buf(k_new, new, dt, dev, "k_new"),
+        _buf(v_new, new, dt, dev, "v_new"),
+        None if parent is None else _buf(parent, (B, N), i32, dev, "parent"),
+        D ** -0.5 if scale is None else scale, B, N, Hq,
+        LH - head0 if kv_heads is None else kv_heads, D, P, LH, head0, page, cols,
+        _buf(out, q.shape, dt, dev, "out"), ws, ws_bytes, _status(dev_status, dev),
+        _stream(stream, dev)))
 
 
 def sv_ring_attn(q, k_pool, v_pool, pos, k_new, v_new, sink: int, window: int, out, workspace,
@@ -539,36 +535,38 @@ def sv_ring_attn(q, k_pool, v_pool, pos, k_new, v_new, sink: int, window: int, o
     """Attention of the newest R tokens over a sink + ring cache: q/out
     [B][R][Hq][D], pools [B][LH][sink+window][D], pos [B] int32, staged
     k_new/v_new [B][LH][R][D]; heads and scale as for sv_tree_attn."""
-    B, R, Hq, Hkv, D, LH = _staged_shapes(q, k_pool, v_pool, k_new, v_new, out, head0, kv_heads)
-    dt = _attn_dtype(q, k_pool, v_pool, k_new, v_new, out)
-    if k_pool.shape[0] != B or k_pool.shape[2] != sink + window:
-        raise SpecVerifyError("pools must be [B][LH][sink+window][D]")
-    _counts(B, pos=(pos, B))
+    if q.dim() != 4 or k_pool.dim() != 4:
+        raise SpecVerifyError("q must be [B][R][Hq][D], pools [B][LH][sink+window][D]")
+    code = _attn_dtype(q)
+    B, R, Hq, D = q.shape
+    LH = k_pool.shape[1]
+    dev, dt = _cuda_device(q, "q"), q.dtype
+    pool, new = (B, LH, sink + window, D), (B, LH, R, D)
+    ws, ws_bytes = _workspace(workspace, dev)
     _check(lib().sv_ring_attn(
-        dt, _dev(q, None, "q"), _dev(k_pool, None, "k_pool"), _dev(v_pool, None, "v_pool"),
-        _dev(pos, torch.int32, "pos"), _dev(k_new, None, "k_new"), _dev(v_new, None, "v_new"),
-        D ** -0.5 if scale is None else scale, B, R, Hq, Hkv, D, LH, head0, sink, window,
-        _dev(out, None, "out"), _dev(workspace, None, "workspace"),
-        workspace.numel() * workspace.element_size(),
-        _dev(dev_status, torch.int32, "dev_status"), _stream(stream, q.device)))
+        code, _buf(q, q.shape, dt, dev, "q"), _buf(k_pool, pool, dt, dev, "k_pool"),
+        _buf(v_pool, pool, dt, dev, "v_pool"), _buf(pos, (B,), torch.int32, dev, "pos"),
+        _buf(k_new, new, dt, dev, "k_new"), _buf(v_new, new, dt, dev, "v_new"),
+        D ** -0.5 if scale is None else scale, B, R, Hq,
+        LH - head0 if kv_heads is None else kv_heads, D, LH, head0, sink, window,
+        _buf(out, q.shape, dt, dev, "out"), ws, ws_bytes, _status(dev_status, dev),
+        _stream(stream, dev)))
 
 
 def sv_prompt_attn(q, k, v, cu_seqlens, sink: int, window: int, out, scale: float | None = None,
                    dev_status=None, stream=None) -> None:
     """Attention of packed prompts under a sliding window with sinks: q/out
     [T][Hq][D], k/v [T][Hkv][D], cu_seqlens [B+1] int32."""
-    if q.dim() != 3 or k.dim() != 3:
-        raise SpecVerifyError("q must be [T][Hq][D], k and v [T][Hkv][D]")
+    if q.dim() != 3 or k.dim() != 3 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise SpecVerifyError("q must be [T][Hq][D], k and v [T][Hkv][D], cu_seqlens [B+1]")
+    code = _attn_dtype(q)
     T, Hq, D = q.shape
     Hkv = k.shape[1]
-    if (tuple(out.shape) != tuple(q.shape) or tuple(k.shape) != (T, Hkv, D)
-            or tuple(v.shape) != tuple(k.shape)):
-        raise SpecVerifyError("shapes of queries, keys, values and output disagree")
-    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
-        raise SpecVerifyError("cu_seqlens must be [B+1]")
-    dt = _attn_dtype(q, k, v, out)
+    dev, dt, kv = _cuda_device(q, "q"), q.dtype, (T, Hkv, D)
     _check(lib().sv_prompt_attn(
-        dt, _dev(q, None, "q"), _dev(k, None, "k"), _dev(v, None, "v"),
-        _dev(cu_seqlens, torch.int32, "cu_seqlens"), D ** -0.5 if scale is None else scale,
-        cu_seqlens.shape[0] - 1, T, Hq, Hkv, D, sink, window, _dev(out, None, "out"),
-        _dev(dev_status, torch.int32, "dev_status"), _stream(stream, q.device)))
+        code, _buf(q, q.shape, dt, dev, "q"), _buf(k, kv, dt, dev, "k"),
+        _buf(v, kv, dt, dev, "v"),
+        _buf(cu_seqlens, cu_seqlens.shape, torch.int32, dev, "cu_seqlens"),
+        D ** -0.5 if scale is None else scale, cu_seqlens.shape[0] - 1, T, Hq, Hkv, D, sink,
+        window, _buf(out, q.shape, dt, dev, "out"), _status(dev_status, dev),
+        _stream(stream, dev)))

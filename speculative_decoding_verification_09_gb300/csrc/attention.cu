@@ -130,7 +130,7 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
     A.MT = 1;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return (dtype == SV_BF16 ? launch_bf16 : launch_f16)(A, lay, grid, ctas, st);
+  return (dtype == SV_BF16 ? launch_bf16 : launch_f16)(A, lay, dev, grid, ctas, st);
 }
 
 bool misaligned(const void* p, unsigned a) {

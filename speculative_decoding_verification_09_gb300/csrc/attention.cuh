@@ -8,6 +8,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "specverify.h"
 #include "svattn.h"
 #include "svkv.h"
@@ -749,6 +751,9 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
   tc_before();
   __syncthreads();
   tc_after();
+  // the join may be launched now: its blocks find room when this grid's CTAs
+  // leave, and wait for the last of them before they read anything
+  if (!PR) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = C.tmem;
   const int start_b = C.start_b;
   const long long start_at = C.start_at;
@@ -1505,10 +1510,17 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) sv_attn_join(const __grid_con
 struct Layout { int nq, rows; };
 
 template <int DP, int NQ, bool PAIR, bool PR, bool BF>
-int launch_as(const AttnParams& A, int grid, int ctas, cudaStream_t st) {
-  if (cudaFuncSetAttribute(sv_attn<DP, NQ, PAIR, PR, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (Smem<DP, NQ>::TOTAL)) != cudaSuccess)
-    return SV_ERR_CUDA;
+int launch_as(const AttnParams& A, int device, int grid, int ctas, cudaStream_t st) {
+  // the kernel's shared-memory limit, raised once per device (ordinals past 63: every time)
+  static std::atomic<uint64_t> raised{0};
+  const uint64_t mark = device < 64 ? uint64_t(1) << device : 0;
+  if (!(raised.load(std::memory_order_acquire) & mark)) {
+    if (cudaFuncSetAttribute(sv_attn<DP, NQ, PAIR, PR, BF>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (Smem<DP, NQ>::TOTAL)) != cudaSuccess)
+      return SV_ERR_CUDA;
+    raised.fetch_or(mark, std::memory_order_release);
+  }
   sv_attn<DP, NQ, PAIR, PR, BF><<<grid, THREADS, (Smem<DP, NQ>::TOTAL), st>>>(A);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
   if (PR) return SV_OK;
@@ -1526,21 +1538,21 @@ int launch_as(const AttnParams& A, int grid, int ctas, cudaStream_t st) {
 }
 
 template <int DP, bool BF>
-int launch_dp(const AttnParams& A, Layout l, int grid, int ctas, cudaStream_t st) {
+int launch_dp(const AttnParams& A, Layout l, int device, int grid, int ctas, cudaStream_t st) {
   if (A.kind == PROMPT)
-    return l.rows == TILE ? launch_as<DP, 0, false, true, BF>(A, grid, ctas, st)
-                          : launch_as<DP, 0, true, true, BF>(A, grid, ctas, st);
-  if (l.nq == 16) return launch_as<DP, 16, false, false, BF>(A, grid, ctas, st);
-  if (l.nq == 32) return launch_as<DP, 32, false, false, BF>(A, grid, ctas, st);
-  if (l.nq == 64) return launch_as<DP, 64, false, false, BF>(A, grid, ctas, st);
-  if (l.rows == TILE) return launch_as<DP, 0, false, false, BF>(A, grid, ctas, st);
-  return launch_as<DP, 0, true, false, BF>(A, grid, ctas, st);
+    return l.rows == TILE ? launch_as<DP, 0, false, true, BF>(A, device, grid, ctas, st)
+                          : launch_as<DP, 0, true, true, BF>(A, device, grid, ctas, st);
+  if (l.nq == 16) return launch_as<DP, 16, false, false, BF>(A, device, grid, ctas, st);
+  if (l.nq == 32) return launch_as<DP, 32, false, false, BF>(A, device, grid, ctas, st);
+  if (l.nq == 64) return launch_as<DP, 64, false, false, BF>(A, device, grid, ctas, st);
+  if (l.rows == TILE) return launch_as<DP, 0, false, false, BF>(A, device, grid, ctas, st);
+  return launch_as<DP, 0, true, false, BF>(A, device, grid, ctas, st);
 }
 
 // One translation unit per storage type (attn_bf16.cu, attn_f16.cu), compiled
 // side by side.
-int launch_bf16(const AttnParams& A, Layout l, int grid, int ctas, cudaStream_t st);
-int launch_f16(const AttnParams& A, Layout l, int grid, int ctas, cudaStream_t st);
+int launch_bf16(const AttnParams& A, Layout l, int device, int grid, int ctas, cudaStream_t st);
+int launch_f16(const AttnParams& A, Layout l, int device, int grid, int ctas, cudaStream_t st);
 
 }  // namespace svattn
 

@@ -2,7 +2,8 @@
 
 #include "attention.cuh"
 
-int svattn::launch_bf16(const AttnParams& A, Layout l, int grid, int ctas, cudaStream_t st) {
-  return A.D > 64 ? launch_dp<128, true>(A, l, grid, ctas, st)
-                  : launch_dp<64, true>(A, l, grid, ctas, st);
+int svattn::launch_bf16(const AttnParams& A, Layout l, int device, int grid, int ctas,
+                         cudaStream_t st) {
+  return A.D > 64 ? launch_dp<128, true>(A, l, device, grid, ctas, st)
+                  : launch_dp<64, true>(A, l, device, grid, ctas, st);
 }

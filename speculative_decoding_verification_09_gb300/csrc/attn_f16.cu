@@ -2,7 +2,8 @@
 
 #include "attention.cuh"
 
-int svattn::launch_f16(const AttnParams& A, Layout l, int grid, int ctas, cudaStream_t st) {
-  return A.D > 64 ? launch_dp<128, false>(A, l, grid, ctas, st)
-                  : launch_dp<64, false>(A, l, grid, ctas, st);
+int svattn::launch_f16(const AttnParams& A, Layout l, int device, int grid, int ctas,
+                         cudaStream_t st) {
+  return A.D > 64 ? launch_dp<128, false>(A, l, device, grid, ctas, st)
+                  : launch_dp<64, false>(A, l, device, grid, ctas, st);
 }
