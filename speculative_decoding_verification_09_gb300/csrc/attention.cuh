@@ -312,6 +312,8 @@ __device__ __forceinline__ int group_or(int id, int n, int x) {
 
 // -------------------------------------------------------------- what a CTA works on
 
+__device__ __forceinline__ int tiles_of(int n) { return (n + TILE - 1) / TILE; }
+
 // A segment: key tiles j0 .. j0 + n - 1 of the nt tiles of an item.  An item is
 // the query rows of one KV head that share the tiles: tokens mt * tokens(item)
 // on of request b, with the Hq / Hkv query heads of h.
@@ -321,9 +323,27 @@ struct Seg {
   int bad;    // SV_ST_BAD_LENGTH for a length outside its range
   int pos;    // committed positions (RING)
   int start;  // first packed row (PROMPT)
-  // PROMPT: tiles t = j below `near`, then lo + (j - near)
-  int near, lo;
+  // PROMPT: `near` tiles over the sinks that have left the window (of every
+  // token of the item), then tiles from key `first` to the last token's
+  int near, first, last;
 };
+
+// Tile j of a segment's item: its first key (of the cache, the staged entries or
+// the sequence) and its keys.
+struct Keys { int k0, n; bool staged; };
+template <bool PR>
+__device__ __forceinline__ Keys keys_of(const AttnParams& A, const Seg& s, int j) {
+  if (PR) {
+    if (j < s.near) return {j * TILE, min(TILE, A.sink - j * TILE), false};
+    const int k0 = s.first + (j - s.near) * TILE;
+    return {k0, min(TILE, s.last + 1 - k0), false};
+  }
+  const int ct = tiles_of(s.len);
+  if (j < ct) return {j * TILE, min(TILE, s.len - j * TILE), false};
+  return {(j - ct) * TILE, min(TILE, A.N - (j - ct) * TILE), true};
+}
+// The products take keys in sixteens.
+__device__ __forceinline__ int width_of(const Keys& k) { return (k.n + 15) & ~15; }
 
 // Cache entries of request b (0 with `bad` set for a length out of range).
 __device__ __forceinline__ int cache_len(const AttnParams& A, int b, int& bad, int& pos) {
@@ -337,7 +357,6 @@ __device__ __forceinline__ int cache_len(const AttnParams& A, int b, int& bad, i
   const long long C = (long long)A.sink + A.window;
   return bad ? 0 : int(n < C ? n : C);
 }
-__device__ __forceinline__ int tiles_of(int n) { return (n + TILE - 1) / TILE; }
 
 // The segments of a CTA, in order, taken by whole warps.
 // TREE and RING: the tiles of all items, in the order request, KV head, item of
@@ -441,16 +460,17 @@ struct Cursor<PAIR, true> {
     s.len = __shfl_sync(0xffffffffu, w_len, src);
     const int tpi = PAIR ? 2 * A.tpt : A.tpt;
     const long long r = i - cum - before;
-    const int back = int(r / A.Hkv);
+    const int back = r >> 32 ? int(r / A.Hkv) : int(uint32_t(r) / uint32_t(A.Hkv));
     s.h = int(r - (long long)back * A.Hkv);
     s.mt = (s.len + tpi - 1) / tpi - 1 - back;
     s.bad = 0;
     s.j0 = 0;
     const int q0 = s.mt * tpi, q1 = min(q0 + tpi, s.len) - 1;
-    const int first = q0 - A.window + 1;  // (window >= 1: no overflow)
-    s.lo = first > 0 ? first / TILE : 0;
-    s.near = min(tiles_of(min(A.sink, q1 + 1)), s.lo);
-    s.n = s.nt = s.near + q1 / TILE - s.lo + 1;
+    s.first = max(0, q0 - A.window + 1);  // (window >= 1: no overflow)
+    s.last = q1;
+    if (A.sink >= s.first) s.first = 0;
+    s.near = s.first ? tiles_of(A.sink) : 0;
+    s.n = s.nt = s.near + tiles_of(q1 + 1 - s.first);
     i += gridDim.x;
     return true;
   }
@@ -521,6 +541,19 @@ constexpr int DESC_IN = 1 << 30;       // the first segment starts inside its it
 constexpr int DESC_THROUGH = 1 << 29;  // and runs to the CTA's end without finishing it
 constexpr int DESC_OUT = 1 << 28;      // the last segment leaves its item unfinished
 constexpr int DESC_LAST1 = 1 << 27;    // the last segment's partials are in slot 1
+
+// A step of a 4 x 4 transposition between lanes: the lane without bit x keeps
+// `a` and gets its partner's `a` as its `b`; the other the reverse.
+__device__ __forceinline__ void swap_pieces(uint4& a, uint4& b, int x, int lane) {
+  const bool up = lane & x;
+  uint4 give = up ? a : b;
+  give.x = __shfl_xor_sync(0xffffffffu, give.x, x);
+  give.y = __shfl_xor_sync(0xffffffffu, give.y, x);
+  give.z = __shfl_xor_sync(0xffffffffu, give.z, x);
+  give.w = __shfl_xor_sync(0xffffffffu, give.w, x);
+  if (up) a = give;
+  else b = give;
+}
 
 // Sums of the columns over a warp's 32 lanes: lane i gets column i's (i mod 16's
 // with 16 columns) in v[0], and column 32 + i's in v[32] with 64.
@@ -832,28 +865,29 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       int done = 0;
       for (int jj = PAIR ? 0 : st; jj < n; jj += PAIR ? 1 : 2, ++done) {
         const int j = s.j0 + jj;
-        const int k0 = PR ? (j < s.near ? j : s.lo + (j - s.near)) * TILE
-                                        : (j < ct ? j : j - ct) * TILE;
-        // does the tile need a mask, and value rows that no query of the item sees zeroed?
-        bool masked, clean = false, dead = false;
+        const Keys ky = keys_of<PR>(A, s, j);
+        const int k0 = ky.k0, w = width_of(ky);
+        // does the tile need a mask, and value rows that no query of the item sees
+        // (among the w that the products take) zeroed?
+        bool masked = NQ == 0 ? (w & 31) != 0 : false, clean = ky.n < w, dead = row >= ky.n;
         if (PR) {
-          masked = k0 + TILE - 1 > w0 || (k0 <= w1 - A.window && k0 + TILE > A.sink);
-          clean = k0 + TILE - 1 > q1 || (k0 <= q0 - A.window && k0 + TILE > A.sink);
-          dead = k0 + row > q1 || (k0 + row <= q0 - A.window && k0 + row >= A.sink);
-        } else if (j >= ct) {
+          masked |= clean;
+          if (j >= s.near) masked |= k0 + w - 1 > w0 || (k0 <= w1 - A.window && k0 + w > A.sink);
+        } else if (ky.staged) {
           masked = true;
+          clean = dead = false;  // (rows past the staged entries arrived as zeros)
         } else {
-          masked = clean = k0 + TILE > s.len;
-          dead = k0 + row >= s.len;
+          masked |= k0 + (NQ ? TILE : w) > s.len;
           if (ring_at >= 0) {
             const int a = A.sink + ring_at, e = ring_at + A.N - A.window;
-            masked |= (k0 < a + A.N && k0 + TILE > a) || (e > 0 && k0 < A.sink + e && k0 + TILE > A.sink);
+            masked |= (k0 < a + A.N && k0 + w > a) || (e > 0 && k0 < A.sink + e && k0 + w > A.sink);
             if (ring_full) {
-              clean |= a >= k0 && a < k0 + TILE;
+              clean |= a >= k0 && a < k0 + w;
               dead |= k0 + row == a;
             }
           }
         }
+        dead = dead && row < w;
         if (!warp_wait(bar(&C.s_full[st]), s_use & 1, A.status, abort)) {
           ok = false;
           break;
@@ -882,7 +916,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           unsigned long long sees = ~0ull;
           if (masked) {
             const int k = k0 + row;
-            if (j < ct) {
+            if (!ky.staged) {
               if (k >= s.len) {
                 sees = 0;
               } else if (ring_at >= 0 && k >= A.sink) {
@@ -901,19 +935,22 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
         } else if (warp_active) {
           uint32_t r[4][32];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) tm_ld32(ts + x * 32, r[x]);
+          for (int x = 0; x < 4; ++x)
+            if (x * 32 < w) tm_ld32(ts + x * 32, r[x]);
           tm_wait_ld(r[0]);
           tm_loaded(r[1]);
           tm_loaded(r[2]);
           tm_loaded(r[3]);
           if (masked) {
-            uint32_t see[4] = {0, 0, 0, 0};
+            uint32_t see[4];
             if (PR) {
+              // near tiles: the sinks; others: the window, and the sinks when they adjoin it
+              const int lo = j < s.near ? 0 : tok - A.window + 1;
+              const int hi = j < s.near ? A.sink : tok + 1, sk = min(A.sink, tok + 1);
 #pragma unroll
               for (int x = 0; x < 4; ++x)
-                see[x] = span(0, min(A.sink, tok + 1), k0 + 32 * x) |
-                         span(tok - A.window + 1, tok + 1, k0 + 32 * x);
-            } else if (j < ct) {
+                see[x] = span(lo, hi, k0 + 32 * x) | span(0, sk, k0 + 32 * x);
+            } else if (!ky.staged) {
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 see[x] = span(0, s.len, k0 + 32 * x);
@@ -923,6 +960,8 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
                               span(A.sink, A.sink + ring_at + tok + 1 - A.window, k0 + 32 * x));
               }
             } else if (A.parent) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) see[x] = 0;
               for (int i = active ? tok : 0;; i = C.parent[st][i]) {
                 const int y = i - k0;
 #pragma unroll
@@ -934,20 +973,29 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
 #pragma unroll
               for (int x = 0; x < 4; ++x) see[x] = span(0, tok + 1, k0 + 32 * x);
             }
+            // (columns past the tile's width hold an earlier tile's)
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
+            for (int x = 0; x < 4; ++x) {
+              see[x] &= span(0, w, 32 * x);
+              if (x * 32 < w && !__all_sync(0xffffffffu, see[x] == 0xffffffffu)) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!(see[x] >> i & 1)) r[x][i] = 0xff800000u;
+                for (int i = 0; i < 32; ++i)
+                  if (!(see[x] >> i & 1)) r[x][i] = 0xff800000u;
+              }
+            }
           }
-          float mx[4];
+          float mt = -INFINITY;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            mx[x] = __uint_as_float(r[x][0]);
+          for (int x = 0; x < 4; ++x)
+            if (x * 32 < w) {
+              float mx[2] = {__uint_as_float(r[x][0]), __uint_as_float(r[x][1])};
 #pragma unroll
-            for (int i = 1; i < 32; ++i) mx[x] = fmaxf(mx[x], __uint_as_float(r[x][i]));
-          }
-          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+              for (int i = 2; i < 32; i += 2) {
+                mx[0] = fmaxf(mx[0], __uint_as_float(r[x][i]));
+                mx[1] = fmaxf(mx[1], __uint_as_float(r[x][i + 1]));
+              }
+              mt = fmaxf(mt, fmaxf(mx[0], mx[1]));
+            }
           if (done == 0) {
             m = mt;
           } else {
@@ -972,16 +1020,17 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           float2 sum[2] = {make_float2(0, 0), make_float2(0, 0)};
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            uint32_t w[16];
+            if (x * 32 >= w) break;
+            uint32_t pw[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float2 e = fma2(make_float2(__uint_as_float(r[x][2 * i]),
                                                 __uint_as_float(r[x][2 * i + 1])), c2, mc2);
               const float2 p = make_float2(ex2(e.x), ex2(e.y));
               sum[i & 1] = add2(sum[i & 1], p);
-              w[i] = pack16<BF>(p.x, p.y);
+              pw[i] = pack16<BF>(p.x, p.y);
             }
-            tm_st16(ts + x * 16, w);
+            tm_st16(ts + x * 16, pw);
           }
           sum[0] = add2(sum[0], sum[1]);
           l += sum[0].x + sum[0].y;
@@ -1000,19 +1049,32 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       uint16_t* const orow = A.out + (token_row * A.Hq + s.h * A.G + rg) * A.D;
       float4* const prow = reinterpret_cast<float4*>(A.part_o);
       const size_t pcol0 = (size_t(blockIdx.x) * 2 + slot) * (DP / 4);
+      const unsigned rows_on = __ballot_sync(0xffffffffu, active);
       auto put = [&](const float (&v)[32], int col) {  // 32 columns from col on
         if (whole) {
-          if (!active) return;
+          // Four lanes exchange their rows' 16-byte pieces, so that they write
+          // 64 bytes of one row at a time instead of 16 of four.
+          uint4 u[4];
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            if (col + i < A.D) {
-              uint4 o;
-              o.x = pack16<BF>(v[i], v[i + 1]);
-              o.y = pack16<BF>(v[i + 2], v[i + 3]);
-              o.z = pack16<BF>(v[i + 4], v[i + 5]);
-              o.w = pack16<BF>(v[i + 6], v[i + 7]);
-              *reinterpret_cast<uint4*>(orow + col + i) = bad ? make_uint4(0, 0, 0, 0) : o;
-            }
+          for (int i = 0; i < 4; ++i) {
+            u[i].x = pack16<BF>(v[8 * i], v[8 * i + 1]);
+            u[i].y = pack16<BF>(v[8 * i + 2], v[8 * i + 3]);
+            u[i].z = pack16<BF>(v[8 * i + 4], v[8 * i + 5]);
+            u[i].w = pack16<BF>(v[8 * i + 6], v[8 * i + 7]);
+          }
+          swap_pieces(u[0], u[1], 1, lane);
+          swap_pieces(u[2], u[3], 1, lane);
+          swap_pieces(u[0], u[2], 2, lane);
+          swap_pieces(u[1], u[3], 2, lane);
+          const int c = col + (lane & 3) * 8;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int from = (lane & 28) + i;
+            uint16_t* const o = reinterpret_cast<uint16_t*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(orow), from));
+            if ((rows_on >> from & 1) && c < A.D)
+              *reinterpret_cast<uint4*>(o + c) = bad ? make_uint4(0, 0, 0, 0) : u[i];
+          }
         } else if (active) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
@@ -1190,38 +1252,36 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       const uint32_t fb = bar(&C.full[st]);
       const uint32_t dst = base + SM::STAGE_AT + st * BYTES;
       if (use > 0 && !warp_wait(bar(&C.empty[st]), (use - 1) & 1, A.status, abort)) return false;
-      const int j = s.j0 + jj;
+      const Keys ky = keys_of<PR>(A, s, s.j0 + jj);
       if (PR) {
-        const int t = j < s.near ? j : s.lo + (j - s.near);
         if (elect_one()) {
           mbar_arrive_tx(fb, BYTES);
           for (int x = 0; x < HALVES; ++x)
-            tma_3d(dst + x * 16384, is_v ? &A.mv : &A.mk, fb, x * 64, s.h, s.start + t * TILE);
+            tma_3d(dst + x * 16384, is_v ? &A.mv : &A.mk, fb, x * 64, s.h, s.start + ky.k0);
         }
       } else {
-        const int ct = tiles_of(s.len);
-        if (j >= ct) {
+        if (ky.staged) {
           if (elect_one()) {
             mbar_arrive_tx(fb, BYTES);
             for (int x = 0; x < HALVES; ++x)
-              tma_3d(dst + x * 16384, is_v ? &A.mvn : &A.mkn, fb, x * 64, (j - ct) * TILE,
+              tma_3d(dst + x * 16384, is_v ? &A.mvn : &A.mkn, fb, x * 64, ky.k0,
                      s.b * A.LH + A.head0 + s.h);
           }
         } else if (A.kind == RING) {
           if (elect_one()) {
             mbar_arrive_tx(fb, BYTES);
             for (int x = 0; x < HALVES; ++x)
-              tma_3d(dst + x * 16384, is_v ? &A.mv : &A.mk, fb, x * 64, j * TILE,
+              tma_3d(dst + x * 16384, is_v ? &A.mv : &A.mk, fb, x * 64, ky.k0,
                      s.b * A.LH + A.head0 + s.h);
           }
         } else {
           // one lane per box of page rows; a page outside the pool is read as
           // page 0 (the softmax warps report it and drop the result)
-          const int boxes = min(TILE, s.len - j * TILE + A.box - 1) / A.box;
+          const int boxes = (ky.n + A.box - 1) / A.box;
           if (lane == 0) mbar_arrive_tx(fb, boxes * A.box * DP * 2);
           __syncwarp();
           if (lane < boxes) {
-            const int t = j * TILE + lane * A.box;
+            const int t = ky.k0 + lane * A.box;
             const int col = t / A.page;
             int pg = __ldg(A.table + size_t(s.b) * A.cols + col);
             if (pg < 0 || pg >= A.num_pages) pg = 0;
@@ -1276,7 +1336,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
     int segs = 0;
     unsigned p_use[2] = {0, 0};
     // (the turned products: N = NQ, and V^T is an operand whose dimensions are contiguous)
-    const uint32_t id_s = instr_desc(BF, false, false, NQ ? NQ : TILE);
+    const uint32_t id_s = instr_desc(BF, false, false, NQ);  // (0: the tile's width goes there)
     const uint32_t id_o = instr_desc(BF, NQ > 0, NQ == 0, NQ ? NQ : DP);
     bool ok = true;
     auto full = [&](uint32_t u) {
@@ -1284,23 +1344,25 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       tc_after();
       return true;
     };
-    auto scores = [&](int st, int q, uint32_t u) {  // S[st] = Q[q] K^T, or K Q[q]^T
+    auto scores = [&](int st, int q, uint32_t u, int w) {  // S[st] = Q[q] K^T, or K Q[q]^T
       const uint64_t qa = desc_rows(base + q * SM::Q_BYTES);
       const uint64_t ka = desc_rows(base + SM::STAGE_AT + (u % STAGES) * BYTES);
 #pragma unroll
       for (int k = 0; k < DP / 16; ++k) {
         const uint64_t dq = qa + (((k / 4) * (SM::Q_BYTES / HALVES) + (k % 4) * 32) >> 4);
         const uint64_t dk = ka + (((k / 4) * 16384 + (k % 4) * 32) >> 4);
-        mma_ss(tmem + st * S_COLS, NQ ? dk : dq, NQ ? dq : dk, id_s, k > 0);
+        mma_ss(tmem + st * S_COLS, NQ ? dk : dq, NQ ? dq : dk,
+               NQ ? id_s : id_s | uint32_t(w >> 3) << 17, k > 0);
       }
       mma_commit(bar(&C.s_full[st]));
     };
-    auto values = [&](int st, uint32_t u, bool more) {  // O[st] (+)= P[st] V, or V^T P[st]^T
+    auto values = [&](int st, uint32_t u, int w, bool more) {  // O[st] (+)= P[st] V, or V^T P[st]^T
       const uint64_t va = desc_cols(base + SM::STAGE_AT + (u % STAGES) * BYTES,
                                     NQ && DP == 64 ? 0 : 16384);
       const uint64_t pa = desc_rows(base + SM::P_AT + st * SM::P_BYTES);
 #pragma unroll
       for (int k = 0; k < TILE / 16; ++k) {
+        if (k * 16 >= w) break;
         const uint64_t dv = va + ((k * 2048) >> 4);
         const uint64_t dp = pa + (((k / 4) * (NQ * 128) + (k % 4) * 32) >> 4);
         if (NQ) mma_ss(tmem + O_AT + st * S_COLS, dv, dp, id_o, more || k > 0);
@@ -1313,18 +1375,22 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       ok = warp_wait(bar(&C.q_full[slot]), use & 1, A.status, abort);
       const int n = s.n;
       const uint32_t u0 = idx;
+      auto width = [&](int j) { return width_of(keys_of<PR>(A, s, s.j0 + j)); };
       if (PAIR) {
+        int w = width(0);
         ok = ok && full(u0);
         if (ok && elect_one()) {
-          scores(0, 0, u0);
-          scores(1, 1, u0);
+          scores(0, 0, u0, w);
+          scores(1, 1, u0, w);
           mma_commit(bar(&C.empty[u0 % STAGES]));
           if (n == 1) mma_commit(bar(&C.q_empty[0]));
         }
         __syncwarp();
         for (int j = 0; ok && j < n; ++j) {
           const uint32_t uv = u0 + v_order<true>(j, n), uk = u0 + k_order<true>(j + 1);
-          ok = full(uv);
+          const bool more = j + 1 < n;
+          const int w2 = more ? width(j + 1) : 0;
+          ok = full(uv) && (!more || full(uk));
 #pragma unroll
           for (int st = 0; st < 2; ++st) {
             ok = ok && warp_wait(bar(&C.p_full[st]), p_use[st] & 1, A.status, abort);
@@ -1332,30 +1398,29 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
             if (!ok) break;
             tc_after();
             if (elect_one()) {
-              values(st, uv, j > 0);
+              values(st, uv, w, j > 0);
               if (st == 1) mma_commit(bar(&C.empty[uv % STAGES]));
-              if (j + 1 == n) mma_commit(bar(&C.o_full[st]));
-            }
-            __syncwarp();
-            if (j + 1 < n) {
-              if (st == 0 && !(ok = full(uk))) break;
-              if (elect_one()) {
-                scores(st, st, uk);
+              if (more) {
+                scores(st, st, uk, w2);
                 if (st == 1) {
                   mma_commit(bar(&C.empty[uk % STAGES]));
                   if (j + 2 == n) mma_commit(bar(&C.q_empty[0]));
                 }
+              } else {
+                mma_commit(bar(&C.o_full[st]));
               }
-              __syncwarp();
             }
+            __syncwarp();
           }
+          w = w2;
         }
       } else {
         for (int j = 0; ok && j < 2 && j < n; ++j) {
           const uint32_t uk = u0 + k_order<false>(j);
+          const int w = width(j);
           ok = full(uk);
           if (ok && elect_one()) {
-            scores(j, slot, uk);
+            scores(j, slot, uk, w);
             mma_commit(bar(&C.empty[uk % STAGES]));
             if (j + 1 == n) mma_commit(bar(&C.q_empty[slot]));
           }
@@ -1364,25 +1429,25 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
         for (int j = 0; ok && j < n; ++j) {
           const int st = j & 1;
           const uint32_t uv = u0 + v_order<false>(j, n), uk = u0 + k_order<false>(j + 2);
-          ok = full(uv) && warp_wait(bar(&C.p_full[st]), p_use[st] & 1, A.status, abort);
+          const bool more = j + 2 < n;
+          const int w = width(j), w2 = more ? width(j + 2) : 0;
+          ok = full(uv) && (!more || full(uk)) &&
+               warp_wait(bar(&C.p_full[st]), p_use[st] & 1, A.status, abort);
           ++p_use[st];
           if (!ok) break;
           tc_after();
           if (elect_one()) {
-            values(st, uv, j >= 2);
+            values(st, uv, w, j >= 2);
             mma_commit(bar(&C.empty[uv % STAGES]));
-            if (j + 2 >= n) mma_commit(bar(&C.o_full[st]));
-          }
-          __syncwarp();
-          if (j + 2 < n) {
-            ok = full(uk);
-            if (ok && elect_one()) {
-              scores(st, slot, uk);
+            if (more) {
+              scores(st, slot, uk, w2);
               mma_commit(bar(&C.empty[uk % STAGES]));
               if (j + 3 == n) mma_commit(bar(&C.q_empty[slot]));
+            } else {
+              mma_commit(bar(&C.o_full[st]));
             }
-            __syncwarp();
           }
+          __syncwarp();
         }
       }
       idx += 2 * n;
