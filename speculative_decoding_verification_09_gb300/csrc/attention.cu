@@ -126,7 +126,8 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
     lay = {0, (long long)A.Hkv * (A.T / (2 * A.tpt)) >= ctas ? 2 * TILE : TILE};
     const int tpi = lay.rows == 2 * TILE ? 2 * A.tpt : A.tpt;
     const long long items = (long long)A.Hkv * ((A.T + tpi - 1) / tpi + A.B);
-    if (items < grid) grid = int(items);
+    if (items > 0x7fffffff) return SV_ERR_INVALID_ARG;
+    grid = int(items);
     A.MT = 1;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);

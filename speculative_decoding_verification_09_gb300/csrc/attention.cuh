@@ -31,7 +31,7 @@ constexpr int THREADS = 384;    // two softmax warpgroups, and one with a copy a
 // hold a row of scores each thread and take over what the third does not need.
 constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
 static_assert(256 * SOFTMAX_REGS + 128 * OTHER_REGS <= THREADS * 168, "register split");
-constexpr int COPY_WARP = 8, MMA_WARP = 9;
+constexpr int COPY_WARP = 8, MMA_WARP = 9, PLAN_WARP = 10;
 constexpr int MAX_CTAS = 152;   // one per SM
 constexpr unsigned long long WAIT_LIMIT_NS = 1000000000ull;
 constexpr uint32_t SUSPEND_HINT_NS = 20000;
@@ -363,8 +363,9 @@ __device__ __forceinline__ int cache_len(const AttnParams& A, int b, int& bad, i
 // the head, are cut into equal runs, one per CTA; an item cut by a run's end is
 // joined by the second kernel.  An item counts ITEM_COST tiles more than it has
 // (its queries, output and first tile's latency).
-// PROMPT: whole items, dealt out to the CTAs in turn; a sequence's last tokens
-// (whose items are the longest) come first.
+// PROMPT: whole items, one per CTA of the grid; a CTA that is done takes over
+// the next one that has not been launched.  A sequence's last tokens (whose
+// items are the longest) come first.
 template <bool PAIR, bool PR>
 struct Cursor;
 
@@ -373,7 +374,7 @@ struct Cursor<PAIR, false> {
   int b, item, j, nt, len, bad, pos;
   long long left;
 
-  __device__ void open(const AttnParams& A, int b0, long long at, long long count, bool = false) {
+  __device__ void open(const AttnParams& A, int b0, long long at, long long count) {
     left = count;
     if (count <= 0) return;
     b = b0;
@@ -382,7 +383,7 @@ struct Cursor<PAIR, false> {
     item = int(at / (nt + ITEM_COST));
     j = int(at - (long long)item * (nt + ITEM_COST));
   }
-  __device__ bool next(const AttnParams& A, Seg& s, bool = false) {
+  __device__ bool next(const AttnParams& A, Seg& s) {
     for (;;) {
       if (left <= 0) return false;
       if (j >= nt) {  // the item's fixed cost, counted behind its tiles
@@ -415,7 +416,7 @@ struct Cursor<PAIR, false> {
 
 template <bool PAIR>
 struct Cursor<PAIR, true> {
-  long long i, cum, incl;     // this CTA's next item; items before, and up to, the lane's sequence
+  long long cum, incl;        // items before the 32 sequences, and up to the lane's
   int wb, w_start, w_len;     // the 32 sequences from wb on, one per lane
 
   __device__ void load_window(const AttnParams& A, bool report) {
@@ -437,13 +438,13 @@ struct Cursor<PAIR, true> {
       if (lane >= x) incl += y;
     }
   }
-  __device__ void open(const AttnParams& A, int, long long, long long, bool report = false) {
-    i = blockIdx.x;
+  __device__ void open(const AttnParams& A, bool report) {
     cum = 0;
     wb = 0;
     load_window(A, report);
   }
-  __device__ bool next(const AttnParams& A, Seg& s, bool report = false) {
+  // Item i (never before an earlier one); false past the last.
+  __device__ bool item(const AttnParams& A, long long i, Seg& s, bool report) {
     for (;;) {
       const long long total = __shfl_sync(0xffffffffu, incl, 31);
       if (i < cum + total) break;
@@ -471,7 +472,6 @@ struct Cursor<PAIR, true> {
     if (A.sink >= s.first) s.first = 0;
     s.near = s.first ? tiles_of(A.sink) : 0;
     s.n = s.nt = s.near + tiles_of(q1 + 1 - s.first);
-    i += gridDim.x;
     return true;
   }
 };
@@ -517,24 +517,39 @@ struct Smem {
   static constexpr int CTRL = STAGE_AT + STAGES * BYTES;         // offset of the control part
   static constexpr int TOTAL = CTRL + 3072;
 };
+template <int NQ, class A, class B>
+struct Either { using T = A; };
+template <class A, class B>
+struct Either<0, A, B> { using T = B; };
+constexpr int SEGS = 4;        // segments planned ahead
+constexpr int PROMPT_SEGS = 2; // of prompts, whose CTAs take items as they finish others
+template <bool PAIR>
+struct Exchange {              // NQ == 0: softmax state exchanged between the streams
+  float2 ml[2][PAIR ? 1 : TILE];
+};
+struct Few {                   // NQ > 0, per stream and column
+  unsigned long long sees[2][64];  // columns that see a staged entry
+  alignas(16) float nmc[2][64];    // minus the running maximum, in base-2 units; -inf: none yet
+  alignas(16) float fac[2][64];    // rescaling, and at the end the streams' shares
+};
+template <int NQ, bool PAIR>
 struct Ctrl {
   unsigned long long full[12], empty[12], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2],
-      drain;
-  union {
-    float2 ml[2][TILE];  // NQ == 0: softmax state exchanged between the streams
-    struct {             // NQ > 0, per stream and column
-      unsigned long long sees[2][64];  // columns that see a staged entry
-      alignas(16) float nmc[2][64];    // minus the running maximum, in base-2 units; -inf: none yet
-      alignas(16) float fac[2][64];                // rescaling, and at the end the streams' shares
-    } few;
-  };
-  uint8_t parent[2][MAX_N];  // one copy per softmax warpgroup
-  long long scan[12];
+      seg_full[SEGS], seg_empty[SEGS], drain, next_full;
+  alignas(16) uint4 next;    // PROMPT: the answer to a request for another item
+  Seg seg[SEGS];
   long long start_at;
   int start_b, abort;
   uint32_t tmem;
+  uint8_t parent[2][NQ ? NQ : PAIR ? MAX_N : TILE];  // one copy per softmax warpgroup
+  union {
+    typename Either<NQ, Few, Exchange<PAIR>>::T x;
+    long long scan[12];
+  };
 };
-static_assert(sizeof(Ctrl) <= 3072, "control part");
+static_assert(sizeof(Ctrl<0, true>) <= 3072 && sizeof(Ctrl<0, false>) <= 3072 &&
+                  sizeof(Ctrl<64, false>) <= 3072,
+              "control part");
 
 // desc[cta]: x = item index within the request | flags, y = request
 constexpr int DESC_IN = 1 << 30;       // the first segment starts inside its item
@@ -582,13 +597,13 @@ __device__ __forceinline__ void sum_columns(float* v, int lane) {
 // key.  All keys of a tile use one maximum per column; it is raised, the sums
 // and O (columns from to) rescaled, when a score exceeds it by 2^RAISE_LOG2.
 template <int NQ, bool BF>
-__device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl& C, int st, int key,
+__device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>& C, int st, int key,
                                             uint32_t ts, uint32_t to, unsigned long long sees,
                                             bool masked, bool started, bool& unset, float* lq,
                                             unsigned char* pbuf) {
   constexpr int W = NQ < 32 ? NQ : 32;
   const int lane = key & 31, warp = key >> 5;
-  float* const nmc = C.few.nmc[st];
+  float* const nmc = C.x.nmc[st];
   const float2 c2 = make_float2(A.c, A.c);
   uint32_t r[NQ / W][W];
   auto score = [&](int q) -> uint32_t& { return r[q / W][q % W]; };
@@ -651,13 +666,13 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl& C, int st
         old = t;
       }
       nmc[key] = -old;
-      C.few.fac[st][key] = f;
+      C.x.fac[st][key] = f;
       none = old == INFINITY;
     }
     unset = group_or(1 + st, TILE, none);
     if (started) {
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) lq[q] *= C.few.fac[st][q];
+      for (int q = 0; q < NQ; ++q) lq[q] *= C.x.fac[st][q];
 #pragma unroll
       for (int x = 0; x < NQ / W; ++x) {
         uint32_t o[W];
@@ -665,7 +680,7 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl& C, int st
         tm_waitn<W>(o);
 #pragma unroll
         for (int q = 0; q < W; ++q)
-          o[q] = __float_as_uint(__uint_as_float(o[q]) * C.few.fac[st][x * W + q]);
+          o[q] = __float_as_uint(__uint_as_float(o[q]) * C.x.fac[st][x * W + q]);
         tm_stn<W>(to + x * W, o);
       }
       tm_wait_st();
@@ -705,7 +720,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
   constexpr int TM_COLS = NQ ? 256 : 512;               // TMEM: S of both streams, then O
   constexpr int S_COLS = NQ ? 64 : 128, O_AT = TM_COLS / 2;
   extern __shared__ __align__(1024) unsigned char smem[];
-  Ctrl& C = *reinterpret_cast<Ctrl*>(smem + SM::CTRL);
+  Ctrl<NQ, PAIR>& C = *reinterpret_cast<Ctrl<NQ, PAIR>*>(smem + SM::CTRL);
   const uint32_t base = smem_addr(smem);
   const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   auto bar = [&](unsigned long long* p) { return smem_addr(p); };
@@ -723,7 +738,12 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       mbar_init(bar(&C.p_full[i]), 4);
       mbar_init(bar(&C.o_full[i]), 1);
     }
+    for (int i = 0; i < SEGS; ++i) {
+      mbar_init(bar(&C.seg_full[i]), 1);
+      mbar_init(bar(&C.seg_empty[i]), COPY_WARP + 2);  // every warp that reads it
+    }
     mbar_init(bar(&C.drain), 1);
+    mbar_init(bar(&C.next_full), 1);
     C.abort = 0;
     C.start_b = 0;
     C.start_at = 0;
@@ -791,6 +811,15 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
   const int start_b = C.start_b;
   const long long start_at = C.start_at;
   volatile int* abort = &C.abort;
+  // the planned segments: a ring, read by every other role's warps
+  constexpr int AHEAD = PR ? PROMPT_SEGS : SEGS;
+  auto seg_wait = [&](int i) {
+    return warp_wait(bar(&C.seg_full[i % AHEAD]), (i / AHEAD) & 1, A.status, abort);
+  };
+  auto seg_done = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(&C.seg_empty[i % AHEAD]));
+  };
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
@@ -800,16 +829,20 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
     const int rt = row / A.G, rg = row - rt * A.G;
     const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's TMEM lanes
     const uint32_t ts = tmem + lanes + st * S_COLS, to = tmem + lanes + O_AT + st * S_COLS;
-    Cursor<PAIR, PR> cur;
-    cur.open(A, start_b, start_at, run);
-    Seg s;
     uint32_t idx = 0;
     int segs = 0, parent_b = -1, parent_bad = 0;
     unsigned s_use = 0, o_use[2] = {0, 0};
     bool ok = true;
     int d_flags = 0, d_item = 0, d_b = 0;
-    while (ok && cur.next(A, s)) {
+    for (;;) {
+      // The warps go on, or stop after a wait that gave up, together; and (two
+      // streams over one O) both have read O before either lets it be overwritten.
+      ok = ok && seg_wait(segs);
+      if (group_or(PAIR ? 1 + st : 3, PAIR ? TILE : 2 * TILE, !ok)) break;
+      tc_after();
+      const Seg& s = C.seg[segs % AHEAD];
       const int n = s.n;
+      if (n == 0) break;
       const int tpi = PAIR ? 2 * A.tpt : A.tpt;
       const int tok = s.mt * tpi + (PAIR ? st * A.tpt : 0) + rt;  // this row's token
       const int tokens = PR ? s.len : A.N;
@@ -827,7 +860,8 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
             pages_bad |= pg < 0 || pg >= A.num_pages;
           }
         if (A.parent && s.b != parent_b && s.j0 + n > ct) {
-          if (NQ && row < 64) C.few.sees[st][row] = 0;
+          if constexpr (NQ > 0)
+            if (row < 64) C.x.sees[st][row] = 0;
           int wrong = 0;
           for (int i = row; i < A.N; i += TILE) {
             const int p = __ldg(A.parent + size_t(s.b) * A.N + i);
@@ -837,10 +871,10 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           }
           parent_bad = group_or(1 + st, TILE, wrong) ? SV_ST_BAD_TOKEN : 0;
           parent_b = s.b;
-          if (NQ) {  // column `row` sees its token and those above it
+          if constexpr (NQ > 0) {  // column `row` sees its token and those above it
             if (row < A.N * A.G)
               for (int i = row / A.G;; i = C.parent[st][i]) {
-                atomicOr(&C.few.sees[st][i], 1ull << row);
+                atomicOr(&C.x.sees[st][i], 1ull << row);
                 if (i == 0) break;
               }
             group_sync(1 + st, TILE);
@@ -850,7 +884,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
         if (s.j0 + n > ct && A.parent) bad |= parent_bad;
       }
       if (bad && tid == 0) set_status(A.status, bad);
-      // RING: the ring slot after the newest entry holds the oldest
+      // AHEAD: the ring slot after the newest entry holds the oldest
       int ring_at = -1;
       if (!PR && A.kind == RING && !s.bad && s.pos > A.sink) ring_at = (s.pos - A.sink) % A.window;
       const bool ring_full = ring_at >= 0 && s.pos - A.sink >= A.window;
@@ -927,7 +961,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
             } else if (k >= A.N) {
               sees = 0;
             } else {
-              sees = A.parent ? C.few.sees[st][k] : ~0ull << (k * A.G);
+              sees = A.parent ? C.x.sees[st][k] : ~0ull << (k * A.G);
             }
           }
           softmax_few<NQ, BF>(A, C, st, row, ts, to, sees, masked, done > 0, unset, lq,
@@ -1103,7 +1137,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
             l0 += sums[w * NQ + tid];
             l1 += sums[(4 + w) * NQ + tid];
           }
-          float a = -C.few.nmc[0][tid], b = n > 1 ? -C.few.nmc[1][tid] : INFINITY;
+          float a = -C.x.nmc[0][tid], b = n > 1 ? -C.x.nmc[1][tid] : INFINITY;
           if (a == INFINITY) a = -INFINITY;  // nothing seen
           if (b == INFINITY) b = -INFINITY;
           const float mm = fmaxf(a, b), mu = mm == -INFINITY ? 0.0f : mm;
@@ -1113,8 +1147,8 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
             f0 /= ll;
             f1 /= ll;
           }
-          C.few.fac[0][tid] = f0;
-          C.few.fac[1][tid] = f1;
+          C.x.fac[0][tid] = f0;
+          C.x.fac[1][tid] = f1;
           if (!whole)
             A.part_ml[(size_t(blockIdx.x) * 2 + slot) * NQ + tid] =
                 make_float2(mm, bad ? -1.0f : ll);
@@ -1130,8 +1164,8 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           if (n > 1) tm_loadedn<HALF>(o1);
 #pragma unroll
           for (int q = 0; q < HALF; ++q) {
-            float v = __uint_as_float(o0[q]) * C.few.fac[0][q0 + q];
-            if (n > 1) v = fmaf(__uint_as_float(o1[q]), C.few.fac[1][q0 + q], v);
+            float v = __uint_as_float(o0[q]) * C.x.fac[0][q0 + q];
+            if (n > 1) v = fmaf(__uint_as_float(o1[q]), C.x.fac[1][q0 + q], v);
             o0[q] = __float_as_uint(v);
           }
           if (!whole) {
@@ -1180,7 +1214,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
         tc_before();
       } else {
         // join the two streams; warpgroup st takes half of the columns
-        C.ml[st][row] = make_float2(m, l);
+        C.x.ml[st][row] = make_float2(m, l);
         for (int x = 0; x < 2; ++x) {
           if (x >= n) break;
           ok = ok && warp_wait(bar(&C.o_full[x]), o_use[x] & 1, A.status, abort);
@@ -1189,7 +1223,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
         tc_after();
         group_sync(3, 2 * TILE);
         if (ok && warp_active) {
-          const float2 a = C.ml[0][row], b = C.ml[1][row];
+          const float2 a = C.x.ml[0][row], b = C.x.ml[1][row];
           const float mm = fmaxf(a.x, b.x);
           const float mu = mm == -INFINITY ? 0.0f : mm;
           float f0 = ex2((a.x - mu) * A.c), f1 = ex2((b.x - mu) * A.c);
@@ -1230,20 +1264,76 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       }
       d_flags = s.j0 + n < s.nt ? d_flags | DESC_OUT : d_flags & ~DESC_OUT;
       idx += 2 * n;
+      seg_done(segs);
       ++segs;
-      // The warps go on, or stop after a wait that gave up, together; and (two
-      // streams over one O) both have read O before either lets it be overwritten.
-      ok = !group_or(PAIR ? 1 + st : 3, PAIR ? TILE : 2 * TILE, !ok);
-      tc_after();
     }
     if (!PR && tid == 0) A.desc[blockIdx.x] = make_int4(d_flags, d_item, d_b, 0);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
-  if (warp == COPY_WARP) {
-    // ------------------------------------------------------------ copies
+  if (warp == PLAN_WARP) {
+    // ------------------------------------------------------------ the plan
     Cursor<PAIR, PR> cur;
-    cur.open(A, start_b, start_at, run, blockIdx.x == 0);
     Seg s;
+    auto plan = [&](int i, bool more) {  // segment i, or the end
+      if (i >= AHEAD &&
+          !warp_wait(bar(&C.seg_empty[i % AHEAD]), (i / AHEAD - 1) & 1, A.status, abort))
+        return false;
+      if (lane == 0) {
+        if (!more) s.n = 0;
+        C.seg[i % AHEAD] = s;
+        mbar_arrive(bar(&C.seg_full[i % AHEAD]));
+      }
+      __syncwarp();
+      return more;
+    };
+    if constexpr (PR) {
+      const bool report = blockIdx.x == 0;
+      cur.open(A, report);
+      long long i = blockIdx.x;
+      int seg_count = 0;
+      for (int k = 0;; ++k) {
+        // another item is asked for before this one is planned
+        if (lane == 0) {
+          mbar_arrive_tx(bar(&C.next_full), 16);
+          asm volatile(
+              "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+              "[%0], [%1];" ::"r"(smem_addr(&C.next)),
+              "r"(bar(&C.next_full))
+              : "memory");
+        }
+        __syncwarp();
+        const bool have = cur.item(A, i, s, report);  // (none past the last sequence)
+        const bool go = !have || plan(seg_count, true);
+        if (have) ++seg_count;
+        if (!warp_wait(bar(&C.next_full), k & 1, A.status, abort)) {
+          const unsigned long long t0 = globaltimer();  // the answer lands before the CTA ends
+          while (!mbar_try(bar(&C.next_full), k & 1) && globaltimer() - t0 < WAIT_LIMIT_NS) {
+          }
+          break;
+        }
+        uint32_t x, got;
+        asm volatile(
+            "{\n .reg .pred p;\n .reg .b128 r;\n .reg .b32 y, z;\n ld.shared.b128 r, [%2];\n"
+            " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n"
+            " selp.u32 %1, 1, 0, p;\n mov.u32 %0, 0;\n"
+            " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n}"
+            : "=r"(x), "=r"(got)
+            : "r"(smem_addr(&C.next))
+            : "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (!got || !go) break;
+        i = x;
+      }
+      if (report) cur.item(A, 0x7fffffffffffffffll, s, true);  // the other sequences' bounds
+      plan(seg_count, false);
+    } else {
+      cur.open(A, start_b, start_at, run);
+      int k = 0;
+      while (plan(k, cur.next(A, s))) ++k;
+    }
+  } else if (warp == COPY_WARP) {
+    // ------------------------------------------------------------ copies
     uint32_t idx = 0;   // copies issued (low bits: stage and phase)
     int segs = 0;
     bool ok = true;
@@ -1295,7 +1385,9 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       ++idx;
       return true;
     };
-    while (ok && cur.next(A, s, blockIdx.x == 0)) {
+    while (ok && seg_wait(segs) && C.seg[segs % AHEAD].n) {
+      const Seg s = C.seg[segs % AHEAD];
+      seg_done(segs);
       const int slot = PAIR ? 0 : segs & 1;
       const int use = PAIR ? segs : segs >> 1;
       if (use > 0 && !warp_wait(bar(&C.q_empty[slot]), (use - 1) & 1, A.status, abort)) break;
@@ -1329,9 +1421,6 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
     }
   } else if (warp == MMA_WARP) {
     // ------------------------------------------------------------ products
-    Cursor<PAIR, PR> cur;
-    cur.open(A, start_b, start_at, run);
-    Seg s;
     uint32_t idx = 0;
     int segs = 0;
     unsigned p_use[2] = {0, 0};
@@ -1369,7 +1458,9 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
         else mma_ts(tmem + O_AT + st * S_COLS, tmem + st * S_COLS + k * 8, dv, id_o, more || k > 0);
       }
     };
-    while (ok && cur.next(A, s)) {
+    while (ok && seg_wait(segs) && C.seg[segs % AHEAD].n) {
+      const Seg s = C.seg[segs % AHEAD];
+      seg_done(segs);
       const int slot = PAIR ? 0 : segs & 1;
       const int use = PAIR ? segs : segs >> 1;
       ok = warp_wait(bar(&C.q_full[slot]), use & 1, A.status, abort);
