@@ -127,7 +127,8 @@ def _dev(t: torch.Tensor | None, dtype: torch.dtype | None = None, name: str = "
 
 def _stream(stream, device) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return torch._C._cuda_getCurrentRawStream(
+            device if isinstance(device, int) else device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -172,11 +173,12 @@ def sv_set_stage_events(events) -> None:
     _check(lib().sv_set_stage_events(handles if events else None, len(events)))
 
 
-def _buf(t: torch.Tensor, shape, dtype: torch.dtype, device, name: str) -> int:
-    """The address of a contiguous tensor of this shape and type on this device."""
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise SpecVerifyError(f"{name} must be contiguous {list(shape)} {dtype} on {device}, got "
-                              f"{list(t.shape)} {t.dtype} on {t.device}")
+def _buf(t: torch.Tensor, shape, dtype: torch.dtype, device: int, name: str) -> int:
+    """The address of a contiguous tensor of this shape and type on this CUDA device."""
+    if (t.get_device() != device or t.dtype is not dtype or t.shape != shape
+            or not t.is_contiguous()):
+        raise SpecVerifyError(f"{name} must be contiguous {list(shape)} {dtype} on cuda:{device}, "
+                              f"got {list(t.shape)} {t.dtype} on {t.device}")
     return t.data_ptr()
 
 
@@ -184,10 +186,10 @@ def _status(t: torch.Tensor | None, device) -> int | None:
     return None if t is None else _buf(t, t.shape, torch.int32, device, "dev_status")
 
 
-def _cuda_device(t: torch.Tensor, name: str):
+def _cuda_device(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise SpecVerifyError(f"{name} must be a CUDA tensor")
-    return t.device
+    return t.get_device()
 
 
 def _shapes(target_logits: torch.Tensor):

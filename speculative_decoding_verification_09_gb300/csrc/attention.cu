@@ -57,6 +57,8 @@ size_t workspace_for(int N, int G, int D) {
   return size_t(MAX_CTAS) * (2 * rows * (dp * 4 + 8) + sizeof(int4));
 }
 
+constexpr int WHOLE_TILES = 6;
+
 int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v,
            const void* k_new, const void* v_new, void* workspace, void* stream) {
   int dev = 0, sms = 0;
@@ -116,6 +118,11 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
     lay = layout_of(A.N, A.G);
     const int tpi = lay.rows == 2 * TILE ? 2 * A.tpt : A.tpt;
     A.MT = (A.N + tpi - 1) / tpi;
+    // Items of few tiles are not cut: the two streams of a CTA take them in less
+    // time than the join takes to be launched (see DESIGN's table).
+    const long long most = A.kind == TREE ? (long long)A.cols * A.page
+                                          : (long long)A.sink + A.window;
+    A.whole = (most + TILE - 1) / TILE + (A.N + TILE - 1) / TILE <= WHOLE_TILES;
     const size_t rows = lay.rows, dp = A.D > 64 ? 128 : 64;
     unsigned char* w = static_cast<unsigned char*>(workspace);
     A.part_o = reinterpret_cast<float*>(w);

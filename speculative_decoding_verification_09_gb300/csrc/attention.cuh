@@ -58,6 +58,7 @@ struct AttnParams {
   int tpt;                // tokens per query tile, floor(128 / G)
   int q_rows;             // rows of one query copy
   int MT;                 // items per KV head (TREE, RING)
+  int whole;              // items are not cut (TREE, RING)
 };
 
 __device__ __forceinline__ void set_status(int32_t* status, int bits) {
@@ -298,6 +299,7 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 }
 __device__ __forceinline__ void group_sync(int id, int n) {
   asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+  __syncwarp();
 }
 __device__ __forceinline__ int group_or(int id, int n, int x) {
   int r;
@@ -307,6 +309,7 @@ __device__ __forceinline__ int group_or(int id, int n, int x) {
       : "=r"(r)
       : "r"(id), "r"(n), "r"(x)
       : "memory");
+  __syncwarp();  // (what follows may be an instruction of the whole warp)
   return r;
 }
 
@@ -361,7 +364,8 @@ __device__ __forceinline__ int cache_len(const AttnParams& A, int b, int& bad, i
 // The segments of a CTA, in order, taken by whole warps.
 // TREE and RING: the tiles of all items, in the order request, KV head, item of
 // the head, are cut into equal runs, one per CTA; an item cut by a run's end is
-// joined by the second kernel.  An item counts ITEM_COST tiles more than it has
+// joined by the second kernel, or (whole) is taken by the CTA of its first
+// tile.  An item counts ITEM_COST tiles more than it has
 // (its queries, output and first tile's latency).
 // PROMPT: whole items, one per CTA of the grid; a CTA that is done takes over
 // the next one that has not been launched.  A sequence's last tokens (whose
@@ -372,7 +376,7 @@ struct Cursor;
 template <bool PAIR>
 struct Cursor<PAIR, false> {
   int b, item, j, nt, len, bad, pos;
-  long long left;
+  long long left;  // tiles of the run ahead
 
   __device__ void open(const AttnParams& A, int b0, long long at, long long count) {
     left = count;
@@ -380,29 +384,37 @@ struct Cursor<PAIR, false> {
     b = b0;
     len = cache_len(A, b, bad, pos);
     nt = tiles_of(len) + tiles_of(A.N);
-    item = int(at / (nt + ITEM_COST));
-    j = int(at - (long long)item * (nt + ITEM_COST));
+    const int cost = nt + ITEM_COST;
+    item = at >> 32 ? int(at / cost) : int(uint32_t(at) / uint32_t(cost));
+    j = int(at - (long long)item * cost);
+    if (A.whole && j > 0) {  // an earlier CTA's item
+      left -= cost - j;
+      step(A);
+    }
+  }
+  __device__ void step(const AttnParams& A) {  // to the next item
+    j = 0;
+    if (++item == A.MT * A.Hkv) {
+      item = 0;
+      if (left <= 0) return;
+      ++b;
+      len = cache_len(A, b, bad, pos);
+      nt = tiles_of(len) + tiles_of(A.N);
+    }
   }
   __device__ bool next(const AttnParams& A, Seg& s) {
     for (;;) {
       if (left <= 0) return false;
       if (j >= nt) {  // the item's fixed cost, counted behind its tiles
         left -= nt + ITEM_COST - j;
-        j = 0;
-        if (++item == A.MT * A.Hkv) {
-          item = 0;
-          if (left <= 0) return false;
-          ++b;
-          len = cache_len(A, b, bad, pos);
-          nt = tiles_of(len) + tiles_of(A.N);
-        }
+        step(A);
         continue;
       }
       s.b = b;
       s.h = item / A.MT;
       s.mt = item - s.h * A.MT;
       s.j0 = j;
-      s.n = int(left < nt - j ? left : nt - j);
+      s.n = A.whole || left >= nt - j ? nt - j : int(left);
       s.nt = nt;
       s.len = len;
       s.bad = bad;
@@ -534,7 +546,8 @@ struct Few {                   // NQ > 0, per stream and column
 };
 template <int NQ, bool PAIR>
 struct Ctrl {
-  unsigned long long full[12], empty[12], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2],
+  unsigned long long full[12], empty[12], q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2],
+      o_full[2],
       seg_full[SEGS], seg_empty[SEGS], drain, next_full;
   alignas(16) uint4 next;    // PROMPT: the answer to a request for another item
   Seg seg[SEGS];
@@ -556,6 +569,22 @@ constexpr int DESC_IN = 1 << 30;       // the first segment starts inside its it
 constexpr int DESC_THROUGH = 1 << 29;  // and runs to the CTA's end without finishing it
 constexpr int DESC_OUT = 1 << 28;      // the last segment leaves its item unfinished
 constexpr int DESC_LAST1 = 1 << 27;    // the last segment's partials are in slot 1
+
+// The largest of N values, in eight chains of three-operand maxima.
+template <int N, class F>
+__device__ __forceinline__ float max_of(F v) {
+  float a[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) a[k] = v(k);
+#pragma unroll
+  for (int i = 8; i + 16 <= N; i += 16)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a[k] = fmaxf(fmaxf(a[k], v(i + 2 * k)), v(i + 2 * k + 1));
+#pragma unroll
+  for (int k = 0; k < 8; ++k) a[k] = fmaxf(a[k], v(N - 8 + k));  // (N mod 16 is 0: the last eight)
+  return fmaxf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])),
+               fmaxf(fmaxf(a[4], a[5]), fmaxf(a[6], a[7])));
+}
 
 // A step of a 4 x 4 transposition between lanes: the lane without bit x keeps
 // `a` and gets its partner's `a` as its `b`; the other the reverse.
@@ -735,6 +764,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       mbar_init(bar(&C.q_full[i]), 1);
       mbar_init(bar(&C.q_empty[i]), 1);
       mbar_init(bar(&C.s_full[i]), 1);
+      mbar_init(bar(&C.p_half[i]), 4);
       mbar_init(bar(&C.p_full[i]), 4);
       mbar_init(bar(&C.o_full[i]), 1);
     }
@@ -785,8 +815,9 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       total += C.scan[w];
     }
     const long long ctas = min((long long)gridDim.x, total), c = blockIdx.x;
-    const long long lo = c < ctas ? c * total / ctas : total;
-    const long long hi = c < ctas ? (c + 1) * total / ctas : total;
+    const long long each = total / ctas, more = total - each * ctas;
+    const long long lo = c < ctas ? c * each + min(c, more) : total;
+    const long long hi = c < ctas ? lo + each + (c < more) : total;
     run = hi - lo;
     if (run > 0 && lo >= before && lo < before + mine) {
       long long at = before;
@@ -806,7 +837,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
   tc_after();
   // the join may be launched now: its blocks find room when this grid's CTAs
   // leave, and wait for the last of them before they read anything
-  if (!PR) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!PR && !A.whole) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = C.tmem;
   const int start_b = C.start_b;
   const long long start_at = C.start_at;
@@ -821,6 +852,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
     if (lane == 0) mbar_arrive(bar(&C.seg_empty[i % AHEAD]));
   };
 
+  __syncwarp();  // (whole warps from here)
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
     // ------------------------------------------------------------ softmax
@@ -922,21 +954,19 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           }
         }
         dead = dead && row < w;
-        if (!warp_wait(bar(&C.s_full[st]), s_use & 1, A.status, abort)) {
-          ok = false;
-          break;
-        }
+        // (With keys on the lanes the warps meet at barriers within a tile: after a
+        // wait that gave up they walk the rest of the segment's tiles together.)
+        ok = ok && warp_wait(bar(&C.s_full[st]), s_use & 1, A.status, abort);
+        if (NQ == 0 && !ok) break;
         ++s_use;
         tc_after();
         // (The scores' keys have arrived, and so has every copy before them, among
         // them the last one into this tile's stage: its phase is the next.)
         if (clean && (!PAIR || st == 0)) {
           const uint32_t u = idx + v_order<PAIR>(jj, n);
-          if (!warp_wait(bar(&C.full[u % STAGES]), (u / STAGES) & 1, A.status, abort)) {
-            ok = false;
-            break;
-          }
-          if (dead) {
+          ok = ok && warp_wait(bar(&C.full[u % STAGES]), (u / STAGES) & 1, A.status, abort);
+          if (NQ == 0 && !ok) break;
+          if (ok && dead) {
             uint4* v = reinterpret_cast<uint4*>(smem + SM::STAGE_AT + (u % STAGES) * BYTES + row * 128);
 #pragma unroll
             for (int x = 0; x < HALVES; ++x)
@@ -945,6 +975,14 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
+        auto half_done = [&] {  // PAIR: the weights of the tile's first 64 keys are stored
+          if (!PAIR) return;
+          tm_wait_st();
+          tc_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(&C.p_half[st]));
+        };
+        __syncwarp();
         if constexpr (NQ > 0) {
           // one key per thread, all rows
           unsigned long long sees = ~0ull;
@@ -966,7 +1004,9 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           }
           softmax_few<NQ, BF>(A, C, st, row, ts, to, sees, masked, done > 0, unset, lq,
                           smem + SM::P_AT + st * SM::P_BYTES);
-        } else if (warp_active) {
+        } else if (!warp_active) {
+          half_done();
+        } else {
           uint32_t r[4][32];
 #pragma unroll
           for (int x = 0; x < 4; ++x)
@@ -1018,18 +1058,16 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
               }
             }
           }
-          float mt = -INFINITY;
+          float mt;
+          if (w == TILE) {
+            mt = max_of<128>([&](int i) { return __uint_as_float(r[i >> 5][i & 31]); });
+          } else {
+            mt = -INFINITY;
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (x * 32 < w) {
-              float mx[2] = {__uint_as_float(r[x][0]), __uint_as_float(r[x][1])};
-#pragma unroll
-              for (int i = 2; i < 32; i += 2) {
-                mx[0] = fmaxf(mx[0], __uint_as_float(r[x][i]));
-                mx[1] = fmaxf(mx[1], __uint_as_float(r[x][i + 1]));
-              }
-              mt = fmaxf(mt, fmaxf(mx[0], mx[1]));
-            }
+            for (int x = 0; x < 4; ++x)
+              if (x * 32 < w)
+                mt = fmaxf(mt, max_of<32>([&](int i) { return __uint_as_float(r[x][i]); }));
+          }
           if (done == 0) {
             m = mt;
           } else {
@@ -1051,22 +1089,34 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           }
           const float mc = m == -INFINITY ? 0.0f : m * A.c;
           const float2 c2 = make_float2(A.c, A.c), mc2 = make_float2(-mc, -mc);
-          float2 sum[2] = {make_float2(0, 0), make_float2(0, 0)};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            if (x * 32 >= w) break;
+          float2 sum[4] = {};
+          auto chunk = [&](int x) {  // the weights of 32 keys
             uint32_t pw[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float2 e = fma2(make_float2(__uint_as_float(r[x][2 * i]),
                                                 __uint_as_float(r[x][2 * i + 1])), c2, mc2);
               const float2 p = make_float2(ex2(e.x), ex2(e.y));
-              sum[i & 1] = add2(sum[i & 1], p);
+              sum[i & 3] = add2(sum[i & 3], p);
               pw[i] = pack16<BF>(p.x, p.y);
             }
             tm_st16(ts + x * 16, pw);
+          };
+          // the products with the first 64 keys' values start under the others' weights
+          if (w == TILE) {
+            chunk(0);
+            chunk(1);
+            half_done();
+            chunk(2);
+            chunk(3);
+          } else {
+            chunk(0);
+            if (w > 32) chunk(1);
+            half_done();
+            if (w > 64) chunk(2);
+            if (w > 96) chunk(3);
           }
-          sum[0] = add2(sum[0], sum[1]);
+          sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
           l += sum[0].x + sum[0].y;
           tm_wait_st();
         }
@@ -1267,7 +1317,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       seg_done(segs);
       ++segs;
     }
-    if (!PR && tid == 0) A.desc[blockIdx.x] = make_int4(d_flags, d_item, d_b, 0);
+    if (!PR && !A.whole && tid == 0) A.desc[blockIdx.x] = make_int4(d_flags, d_item, d_b, 0);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
   if (warp == PLAN_WARP) {
@@ -1429,7 +1479,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
     const uint32_t id_o = instr_desc(BF, NQ > 0, NQ == 0, NQ ? NQ : DP);
     bool ok = true;
     auto full = [&](uint32_t u) {
-      if (!warp_wait(bar(&C.full[u % STAGES]), (u / STAGES) & 1, A.status, abort)) return false;
+      if (!mbar_wait(bar(&C.full[u % STAGES]), (u / STAGES) & 1, A.status, abort)) return false;
       tc_after();
       return true;
     };
@@ -1445,12 +1495,13 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       }
       mma_commit(bar(&C.s_full[st]));
     };
-    auto values = [&](int st, uint32_t u, int w, bool more) {  // O[st] (+)= P[st] V, or V^T P[st]^T
+    // O[st] (+)= P[st] V, or V^T P[st]^T, over sixteens k0 .. k1 - 1 of the tile's keys
+    auto values = [&](int st, uint32_t u, int w, bool more, int k0, int k1) {
       const uint64_t va = desc_cols(base + SM::STAGE_AT + (u % STAGES) * BYTES,
                                     NQ && DP == 64 ? 0 : 16384);
       const uint64_t pa = desc_rows(base + SM::P_AT + st * SM::P_BYTES);
 #pragma unroll
-      for (int k = 0; k < TILE / 16; ++k) {
+      for (int k = k0; k < k1; ++k) {
         if (k * 16 >= w) break;
         const uint64_t dv = va + ((k * 2048) >> 4);
         const uint64_t dp = pa + (((k / 4) * (NQ * 128) + (k % 4) * 32) >> 4);
@@ -1458,25 +1509,36 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
         else mma_ts(tmem + O_AT + st * S_COLS, tmem + st * S_COLS + k * 8, dv, id_o, more || k > 0);
       }
     };
-    while (ok && seg_wait(segs) && C.seg[segs % AHEAD].n) {
+    auto first_half = [&](int st, uint32_t uv, int w, bool more) {
+      if (!PAIR) return true;
+      if (!mbar_wait(bar(&C.p_half[st]), p_use[st] & 1, A.status, abort)) return false;
+      tc_after();
+      values(st, uv, w, more, 0, 4);
+      return true;
+    };
+    // One thread from here on: the waits, too, are its own.
+    if (elect_one()) {
+    while (ok) {
+      ok = mbar_wait(bar(&C.seg_full[segs % AHEAD]), (segs / AHEAD) & 1, A.status, abort);
+      if (!ok) break;
       const Seg s = C.seg[segs % AHEAD];
-      seg_done(segs);
+      if (s.n == 0) break;
+      mbar_arrive(bar(&C.seg_empty[segs % AHEAD]));
       const int slot = PAIR ? 0 : segs & 1;
       const int use = PAIR ? segs : segs >> 1;
-      ok = warp_wait(bar(&C.q_full[slot]), use & 1, A.status, abort);
+      ok = mbar_wait(bar(&C.q_full[slot]), use & 1, A.status, abort);
       const int n = s.n;
       const uint32_t u0 = idx;
       auto width = [&](int j) { return width_of(keys_of<PR>(A, s, s.j0 + j)); };
       if (PAIR) {
         int w = width(0);
         ok = ok && full(u0);
-        if (ok && elect_one()) {
+        if (ok) {
           scores(0, 0, u0, w);
           scores(1, 1, u0, w);
           mma_commit(bar(&C.empty[u0 % STAGES]));
           if (n == 1) mma_commit(bar(&C.q_empty[0]));
         }
-        __syncwarp();
         for (int j = 0; ok && j < n; ++j) {
           const uint32_t uv = u0 + v_order<true>(j, n), uk = u0 + k_order<true>(j + 1);
           const bool more = j + 1 < n;
@@ -1484,12 +1546,13 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           ok = full(uv) && (!more || full(uk));
 #pragma unroll
           for (int st = 0; st < 2; ++st) {
-            ok = ok && warp_wait(bar(&C.p_full[st]), p_use[st] & 1, A.status, abort);
+            ok = ok && first_half(st, uv, w, j > 0) &&
+                 mbar_wait(bar(&C.p_full[st]), p_use[st] & 1, A.status, abort);
             ++p_use[st];
             if (!ok) break;
             tc_after();
-            if (elect_one()) {
-              values(st, uv, w, j > 0);
+            {
+              values(st, uv, w, true, 4, 8);
               if (st == 1) mma_commit(bar(&C.empty[uv % STAGES]));
               if (more) {
                 scores(st, st, uk, w2);
@@ -1501,8 +1564,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
                 mma_commit(bar(&C.o_full[st]));
               }
             }
-            __syncwarp();
-          }
+            }
           w = w2;
         }
       } else {
@@ -1510,12 +1572,11 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           const uint32_t uk = u0 + k_order<false>(j);
           const int w = width(j);
           ok = full(uk);
-          if (ok && elect_one()) {
+          if (ok) {
             scores(j, slot, uk, w);
             mma_commit(bar(&C.empty[uk % STAGES]));
             if (j + 1 == n) mma_commit(bar(&C.q_empty[slot]));
           }
-          __syncwarp();
         }
         for (int j = 0; ok && j < n; ++j) {
           const int st = j & 1;
@@ -1523,12 +1584,12 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           const bool more = j + 2 < n;
           const int w = width(j), w2 = more ? width(j + 2) : 0;
           ok = full(uv) && (!more || full(uk)) &&
-               warp_wait(bar(&C.p_full[st]), p_use[st] & 1, A.status, abort);
+               mbar_wait(bar(&C.p_full[st]), p_use[st] & 1, A.status, abort);
           ++p_use[st];
           if (!ok) break;
           tc_after();
-          if (elect_one()) {
-            values(st, uv, w, j >= 2);
+          {
+            values(st, uv, w, j >= 2, 0, 8);
             mma_commit(bar(&C.empty[uv % STAGES]));
             if (more) {
               scores(st, slot, uk, w2);
@@ -1538,17 +1599,17 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
               mma_commit(bar(&C.o_full[st]));
             }
           }
-          __syncwarp();
         }
       }
       idx += 2 * n;
       ++segs;
     }
-    if (!ok && lane == 0) {  // the products in flight end before TMEM is freed
+    if (!ok) {  // the products in flight end before TMEM is freed
       mma_commit(bar(&C.drain));
       const unsigned long long t0 = globaltimer();
       while (!mbar_try(bar(&C.drain), 0) && globaltimer() - t0 < WAIT_LIMIT_NS) {
       }
+    }
     }
     __syncwarp();
     }
@@ -1679,7 +1740,7 @@ int launch_as(const AttnParams& A, int device, int grid, int ctas, cudaStream_t 
   }
   sv_attn<DP, NQ, PAIR, PR, BF><<<grid, THREADS, (Smem<DP, NQ>::TOTAL), st>>>(A);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
-  if (PR) return SV_OK;
+  if (PR || A.whole) return SV_OK;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(2 * ctas));
   cfg.blockDim = dim3(JOIN_WARPS * 32);
