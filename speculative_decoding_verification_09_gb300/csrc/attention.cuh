@@ -324,7 +324,8 @@ struct Seg {
   int b, h, mt, j0, n, nt;
   int len;    // cache entries (TREE, RING; 0 when bad), or tokens of the sequence
   int bad;    // SV_ST_BAD_LENGTH for a length outside its range
-  int pos;    // committed positions (RING)
+  int ring;   // RING: the ring slot after the newest entry, which holds the oldest; -1: none
+  int full;   // and whether it does
   int start;  // first packed row (PROMPT)
   // PROMPT: `near` tiles over the sinks that have left the window (of every
   // token of the item), then tiles from key `first` to the last token's
@@ -418,7 +419,12 @@ struct Cursor<PAIR, false> {
       s.nt = nt;
       s.len = len;
       s.bad = bad;
-      s.pos = pos;
+      s.ring = -1;
+      s.full = 0;
+      if (A.kind == RING && !bad && pos > A.sink) {
+        s.ring = (pos - A.sink) % A.window;
+        s.full = pos - A.sink >= A.window;
+      }
       j += s.n;
       left -= s.n;
       return true;
@@ -539,10 +545,12 @@ template <bool PAIR>
 struct Exchange {              // NQ == 0: softmax state exchanged between the streams
   float2 ml[2][PAIR ? 1 : TILE];
 };
+template <int NQ>
 struct Few {                   // NQ > 0, per stream and column
-  unsigned long long sees[2][64];  // columns that see a staged entry
-  alignas(16) float nmc[2][64];    // minus the running maximum, in base-2 units; -inf: none yet
-  alignas(16) float fac[2][64];    // rescaling, and at the end the streams' shares
+  unsigned long long sees[2][NQ];  // columns that see a staged entry
+  alignas(16) float nmc[2][NQ];    // minus the running maximum, in base-2 units; -inf: none yet
+  alignas(16) float fac[2][NQ];    // rescaling, and at the end the streams' shares
+  float sums[NQ <= 32 ? 8 : 1][NQ];  // per warp, at the end (NQ == 64: in P's room)
 };
 template <int NQ, bool PAIR>
 struct Ctrl {
@@ -556,7 +564,7 @@ struct Ctrl {
   uint32_t tmem;
   uint8_t parent[2][NQ ? NQ : PAIR ? MAX_N : TILE];  // one copy per softmax warpgroup
   union {
-    typename Either<NQ, Few, Exchange<PAIR>>::T x;
+    typename Either<NQ, Few<NQ>, Exchange<PAIR>>::T x;
     long long scan[12];
   };
 };
@@ -893,7 +901,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           }
         if (A.parent && s.b != parent_b && s.j0 + n > ct) {
           if constexpr (NQ > 0)
-            if (row < 64) C.x.sees[st][row] = 0;
+            if (row < NQ) C.x.sees[st][row] = 0;
           int wrong = 0;
           for (int i = row; i < A.N; i += TILE) {
             const int p = __ldg(A.parent + size_t(s.b) * A.N + i);
@@ -916,10 +924,8 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
         if (s.j0 + n > ct && A.parent) bad |= parent_bad;
       }
       if (bad && tid == 0) set_status(A.status, bad);
-      // AHEAD: the ring slot after the newest entry holds the oldest
-      int ring_at = -1;
-      if (!PR && A.kind == RING && !s.bad && s.pos > A.sink) ring_at = (s.pos - A.sink) % A.window;
-      const bool ring_full = ring_at >= 0 && s.pos - A.sink >= A.window;
+      const int ring_at = PR ? -1 : s.ring;
+      const bool ring_full = !PR && s.full;
       const int q0 = s.mt * tpi, q1 = min(q0 + tpi, tokens) - 1;  // the item's tokens
       const int w0 = q0 + (PAIR ? st * A.tpt : 0), w1 = min(w0 + A.tpt, tokens) - 1;  // the tile's
 
@@ -974,6 +980,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
               for (int i = 0; i < 8; ++i) v[x * 1024 + i] = make_uint4(0, 0, 0, 0);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
         }
         auto half_done = [&] {  // PAIR: the weights of the tile's first 64 keys are stored
           if (!PAIR) return;
@@ -982,7 +989,6 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(&C.p_half[st]));
         };
-        __syncwarp();
         if constexpr (NQ > 0) {
           // one key per thread, all rows
           unsigned long long sees = ~0ull;
@@ -1167,18 +1173,21 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
         }
       };
       if constexpr (NQ > 0) {
-        for (int x = 0; x < 2; ++x) {
-          if (x >= n) break;
-          ok = ok && warp_wait(bar(&C.o_full[x]), o_use[x] & 1, A.status, abort);
-          ++o_use[x];
-        }
-        tc_after();
         // sums over the keys: 32 lanes here, the four warps and two streams below
-        float* const sums = reinterpret_cast<float*>(smem + SM::P_AT);  // [stream][warp][NQ]
+        float* const sums = NQ <= 32 ? &C.x.sums[0][0] : reinterpret_cast<float*>(smem + SM::P_AT);
         sum_columns<NQ>(lq, lane);
+        auto o_done = [&] {
+          for (int x = 0; x < 2; ++x) {
+            if (x >= n) break;
+            ok = ok && warp_wait(bar(&C.o_full[x]), o_use[x] & 1, A.status, abort);
+            ++o_use[x];
+          }
+          tc_after();
+        };
+        if (NQ > 32) o_done();  // P is free
         if (lane < NQ) {
-          sums[(st * 4 + (warp & 3)) * NQ + lane] = lq[0];
-          if (NQ == 64) sums[(st * 4 + (warp & 3)) * NQ + 32 + lane] = lq[NQ / 2];
+          sums[warp * NQ + lane] = lq[0];
+          if (NQ == 64) sums[warp * NQ + 32 + lane] = lq[NQ / 2];
         }
         group_sync(3, 2 * TILE);
         if (tid < NQ) {
@@ -1203,6 +1212,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
             A.part_ml[(size_t(blockIdx.x) * 2 + slot) * NQ + tid] =
                 make_float2(mm, bad ? -1.0f : ll);
         }
+        if (NQ <= 32) o_done();
         group_sync(3, 2 * TILE);
         if (ok) {
           constexpr int HALF = NQ / 2;  // columns of this warpgroup
@@ -1488,6 +1498,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       const uint64_t ka = desc_rows(base + SM::STAGE_AT + (u % STAGES) * BYTES);
 #pragma unroll
       for (int k = 0; k < DP / 16; ++k) {
+        if (k * 16 >= A.D) break;  // (the rest of the tiles is zeros)
         const uint64_t dq = qa + (((k / 4) * (SM::Q_BYTES / HALVES) + (k % 4) * 32) >> 4);
         const uint64_t dk = ka + (((k / 4) * 16384 + (k % 4) * 32) >> 4);
         mma_ss(tmem + st * S_COLS, NQ ? dk : dq, NQ ? dq : dk,
