@@ -28,7 +28,7 @@
  * errors OR-ed into *dev_status (may be NULL), nothing traps.
  *   dtype: SV_BF16, or SV_F16 (16-bit IEEE floats); SV_F32 is SV_ERR_DTYPE.
  *   Hq a multiple of Hkv with Hq / Hkv <= 128; D a multiple of 8 in [8, 128];
- *   scale finite and > 0; all 16-bit buffers aligned to 16 bytes, int32 ones
+ *   scale > 0, and scale * log2(e) finite; all 16-bit buffers aligned to 16 bytes, int32 ones
  *   to 4.  `out` overlaps no input.
  *   A NaN or infinity in a visible key or value reaches rows of its own
  *   request (sequence) only, there also rows that do not see it; cache

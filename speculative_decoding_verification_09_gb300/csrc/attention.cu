@@ -8,6 +8,8 @@ namespace {
 
 using namespace svattn;
 
+constexpr float LOG2E = 1.44269504088896341f;
+
 // -------------------------------------------------------------- host side
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -56,8 +58,6 @@ size_t workspace_for(int N, int G, int D) {
   const size_t rows = layout_of(N, G).rows, dp = D > 64 ? 128 : 64;
   return size_t(MAX_CTAS) * (2 * rows * (dp * 4 + 8) + sizeof(int4));
 }
-
-constexpr int WHOLE_TILES = 6;
 
 int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v,
            const void* k_new, const void* v_new, void* workspace, void* stream) {
@@ -118,11 +118,15 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
     lay = layout_of(A.N, A.G);
     const int tpi = lay.rows == 2 * TILE ? 2 * A.tpt : A.tpt;
     A.MT = (A.N + tpi - 1) / tpi;
-    // Items of few tiles are not cut: the two streams of a CTA take them in less
-    // time than the join takes to be launched (see DESIGN's table).
-    const long long most = A.kind == TREE ? (long long)A.cols * A.page
-                                          : (long long)A.sink + A.window;
-    A.whole = (most + TILE - 1) / TILE + (A.N + TILE - 1) / TILE <= WHOLE_TILES;
+    // Items are not cut, and not joined, when they have at most two tiles (the two
+    // streams of a CTA take them at once), or few tiles and many items per CTA,
+    // whose sums are even without cuts.  (1024 requests over rings of 512, 27 items of
+    // 5 tiles per CTA: 146.5 us cut, 140.7 whole; one token over 500 cached, 16 items
+    // of 5 tiles in all: 14.3 us cut, 16.4 whole.)
+    const long long entries = A.kind == TREE ? (long long)A.cols * A.page
+                                             : (long long)A.sink + A.window;
+    const long long most = (entries + TILE - 1) / TILE + (A.N + TILE - 1) / TILE;
+    A.whole = most <= 2 || (most <= 8 && (long long)A.B * A.Hkv * A.MT >= 8LL * ctas);
     const size_t rows = lay.rows, dp = A.D > 64 ? 128 : 64;
     unsigned char* w = static_cast<unsigned char*>(workspace);
     A.part_o = reinterpret_cast<float*>(w);
@@ -132,7 +136,8 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
     // two query tiles per item when that leaves every SM an item
     lay = {0, (long long)A.Hkv * (A.T / (2 * A.tpt)) >= ctas ? 2 * TILE : TILE};
     const int tpi = lay.rows == 2 * TILE ? 2 * A.tpt : A.tpt;
-    const long long items = (long long)A.Hkv * ((A.T + tpi - 1) / tpi + A.B);
+    // an upper bound: every sequence that holds a token adds at most one part item
+    const long long items = (long long)A.Hkv * (A.T / tpi + (A.B < A.T ? A.B : A.T));
     if (items > 0x7fffffff) return SV_ERR_INVALID_ARG;
     grid = int(items);
     A.MT = 1;
@@ -144,6 +149,9 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
 bool misaligned(const void* p, unsigned a) {
   return (reinterpret_cast<uintptr_t>(p) % a) != 0;
 }
+
+// Finite and positive, also in base-2 units.
+bool bad_scale(float scale) { return !(scale > 0.0f) || !isfinite(scale * LOG2E); }
 
 bool bad_heads(int Hq, int Hkv, int D) {
   return Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > MAX_GROUP || D < 8 || D > MAX_D ||
@@ -168,7 +176,7 @@ int sv_tree_attn(int dtype, const void* q, const void* k_pages, const void* v_pa
   if (dtype != SV_BF16 && dtype != SV_F16) return SV_ERR_DTYPE;
   if (B < 0 || B > 65535 || N < 1 || N > MAX_N || bad_heads(Hq, Hkv, D) || num_pages < 1 ||
       LH < 1 || head0 < 0 || head0 > LH - Hkv || page_size < 8 || page_size > 65536 ||
-      page_size % 8 != 0 || cols < 1 || !isfinite(scale) || !(scale > 0.0f))
+      page_size % 8 != 0 || cols < 1 || bad_scale(scale))
     return SV_ERR_INVALID_ARG;
   if (B == 0) return SV_OK;
   if (!q || !k_pages || !v_pages || !block_table || !seq_lens || !k_new || !v_new || !out)
@@ -188,7 +196,7 @@ int sv_tree_attn(int dtype, const void* q, const void* k_pages, const void* v_pa
   A.parent = parent;
   A.out = static_cast<uint16_t*>(out);
   A.status = dev_status;
-  A.c = scale * 1.44269504088896341f;
+  A.c = scale * LOG2E;
   A.B = B; A.N = N; A.Hq = Hq; A.Hkv = Hkv; A.D = D;
   A.LH = LH; A.head0 = head0; A.num_pages = num_pages; A.page = page_size; A.cols = cols;
   return launch(A, dtype, q, k_pages, v_pages, k_new, v_new, workspace, stream);
@@ -202,7 +210,7 @@ int sv_ring_attn(int dtype, const void* q, const void* k_pool, const void* v_poo
   if (dtype != SV_BF16 && dtype != SV_F16) return SV_ERR_DTYPE;
   if (B < 0 || B > 65535 || R < 1 || R > MAX_R || bad_heads(Hq, Hkv, D) || LH < 1 || head0 < 0 ||
       head0 > LH - Hkv || (long long)B * LH > 0x7fffffffLL || sink < 0 || window < R ||
-      (long long)sink + window > MAX_KEYS || !isfinite(scale) || !(scale > 0.0f))
+      (long long)sink + window > MAX_KEYS || bad_scale(scale))
     return SV_ERR_INVALID_ARG;
   if (B == 0) return SV_OK;
   if (!q || !k_pool || !v_pool || !pos || !k_new || !v_new || !out) return SV_ERR_INVALID_ARG;
@@ -218,7 +226,7 @@ int sv_ring_attn(int dtype, const void* q, const void* k_pool, const void* v_poo
   A.lens = pos;
   A.out = static_cast<uint16_t*>(out);
   A.status = dev_status;
-  A.c = scale * 1.44269504088896341f;
+  A.c = scale * LOG2E;
   A.B = B; A.N = R; A.Hq = Hq; A.Hkv = Hkv; A.D = D;
   A.LH = LH; A.head0 = head0; A.sink = sink; A.window = window;
   return launch(A, dtype, q, k_pool, v_pool, k_new, v_new, workspace, stream);
@@ -229,7 +237,7 @@ int sv_prompt_attn(int dtype, const void* q, const void* k, const void* v,
                    int sink, int window, void* out, int32_t* dev_status, void* stream) {
   if (dtype != SV_BF16 && dtype != SV_F16) return SV_ERR_DTYPE;
   if (B < 0 || B > 65535 || T < 0 || T > 0x7fffffff - 511 || bad_heads(Hq, Hkv, D) || sink < 0 ||
-      window < 1 || !isfinite(scale) || !(scale > 0.0f))
+      window < 1 || bad_scale(scale))
     return SV_ERR_INVALID_ARG;
   if (B == 0 || T == 0) return SV_OK;
   if (!q || !k || !v || !cu_seqlens || !out) return SV_ERR_INVALID_ARG;
@@ -241,7 +249,7 @@ int sv_prompt_attn(int dtype, const void* q, const void* k, const void* v,
   A.lens = cu_seqlens;
   A.out = static_cast<uint16_t*>(out);
   A.status = dev_status;
-  A.c = scale * 1.44269504088896341f;
+  A.c = scale * LOG2E;
   A.B = B; A.T = T; A.Hq = Hq; A.Hkv = Hkv; A.D = D;
   A.sink = sink; A.window = window;
   return launch(A, dtype, q, k, v, nullptr, nullptr, nullptr, stream);

@@ -468,7 +468,10 @@ struct Cursor<PAIR, true> {
       if (i < cum + total) break;
       cum += total;
       wb += 32;
-      if (wb >= A.B) return false;
+      if (wb >= A.B) {
+        incl = 0;  // nothing in the windows past the last
+        return false;
+      }
       load_window(A, report);
     }
     const unsigned hit = __ballot_sync(0xffffffffu, i < cum + incl);

@@ -646,6 +646,54 @@ def test_long_runs():
             assert torch.equal(first, call(x)[0])
 
 
+def test_many_requests():
+    """More requests than a block has threads, most of them short or empty; more sequences than a warp plans at once."""
+    rng = np.random.default_rng(77)
+    B = 1500
+    lens = [int(x) for x in rng.choice([0, 1, 5, 130], B, p=[0.5, 0.3, 0.15, 0.05])]
+    lens[-1] = 700
+    c = tree_inputs(78, B, 2, 2, 1, 64, 16, lens, BF)
+    out, st = tree_call(c)
+    r = ring_inputs(79, B, 2, 2, 1, 64, 2, 300, lens, BF)
+    rout, rst = ring_call(r)
+    p = prompt_inputs(80, lens, 2, 1, 64, 2, 50, BF)
+    pout, pst = prompt_call(p)
+    assert int(st.item()) == int(rst.item()) == int(pst.item()) == 0
+    for b in [*range(0, B, 97), *np.flatnonzero(np.array(lens) == 130)[:3].tolist(), B - 1]:
+        au.check(out[b], *tree_reference(c, b), f"tree {b}")
+        au.check(rout[b], *ring_reference(r, b), f"ring {b}")
+        a, e = int(p["cu"][b]), int(p["cu"][b + 1])
+        if e > a:
+            at = range(e - a)
+            au.check(pout[a:e], *au.attend(p["q"][a:e], p["k"][a:e], p["v"][a:e],
+                                           au.window_visible(at, at, 2, 50).to(DEV), 64 ** -0.5, BF), f"prompt {b}")
+
+
+def test_prompt_all_empty():
+    p = prompt_inputs(81, [0] * 70, 4, 2, 64, 2, 50, BF, tail=5)
+    out, st = prompt_call(p)
+    assert int(st.item()) == 0 and (out == 7.0).all()
+
+
+def test_two_calls_at_once():
+    """Two streams, each with its own workspace and outputs, many calls in flight on both."""
+    c = tree_inputs(82, 6, 9, 8, 2, 128, 16, [300, 100, 1200, 5, 0, 2000], BF)
+    r = ring_inputs(83, 6, 3, 8, 2, 128, 4, 500, [300, 100, 1200, 5, 0, 2000], BF)
+    want = tree_call(c)[0], ring_call(r)[0]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.zeros_like(w) for w in want]
+    ws = [binding.make_attn_workspace(6, n, 8, 2, 128, DEV) for n in (9, 3)]
+    d = [i32(c["table"]), i32(c["lens"]), i32(c["parent"]), i32(r["pos"])]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        binding.sv_tree_attn(c["q"], c["kp"], c["vp"], d[0], d[1], c["kn"], c["vn"], d[2], outs[0], ws[0],
+                             stream=streams[0])
+        binding.sv_ring_attn(r["q"], r["kp"], r["vp"], d[3], r["kn"], r["vn"], 4, 500, outs[1], ws[1],
+                             stream=streams[1])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
 def test_other_stream_and_graph():
     """Calls on a side stream, and captured ones replayed on new data, two graphs sharing a workspace in turn."""
     c = tree_inputs(71, 3, 9, 8, 2, 64, 16, [300, 100, 1200], HF)
