@@ -299,7 +299,6 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 }
 __device__ __forceinline__ void group_sync(int id, int n) {
   asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
-  __syncwarp();
 }
 __device__ __forceinline__ int group_or(int id, int n, int x) {
   int r;
@@ -309,7 +308,6 @@ __device__ __forceinline__ int group_or(int id, int n, int x) {
       : "=r"(r)
       : "r"(id), "r"(n), "r"(x)
       : "memory");
-  __syncwarp();  // (what follows may be an instruction of the whole warp)
   return r;
 }
 
@@ -681,6 +679,7 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
   bool raise = !started || unset;
   if (!raise) {
     raise = group_or(1 + st, TILE, exponents() > RAISE_LOG2);
+    __syncwarp();
     if (raise) load();
   }
   if (raise) {
@@ -710,6 +709,7 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
       none = old == INFINITY;
     }
     unset = group_or(1 + st, TILE, none);
+    __syncwarp();
     if (started) {
 #pragma unroll
       for (int q = 0; q < NQ; ++q) lq[q] *= C.x.fac[st][q];
@@ -1217,6 +1217,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
         }
         if (NQ <= 32) o_done();
         group_sync(3, 2 * TILE);
+        __syncwarp();
         if (ok) {
           constexpr int HALF = NQ / 2;  // columns of this warpgroup
           const int q0 = st * HALF;
@@ -1285,6 +1286,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
         }
         tc_after();
         group_sync(3, 2 * TILE);
+        __syncwarp();
         if (ok && warp_active) {
           const float2 a = C.x.ml[0][row], b = C.x.ml[1][row];
           const float mm = fmaxf(a.x, b.x);
