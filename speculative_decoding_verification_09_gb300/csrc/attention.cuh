@@ -29,7 +29,7 @@ constexpr int TILE = 128;       // query rows of a tile, and keys of a tile
 constexpr int THREADS = 384;    // two softmax warpgroups, and one with a copy and a product warp
 // Registers: launched with 168 a thread (64512 a CTA); the softmax warpgroups
 // hold a row of scores each thread and take over what the third does not need.
-constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
+constexpr int SOFTMAX_REGS = 216, OTHER_REGS = 72;
 static_assert(256 * SOFTMAX_REGS + 128 * OTHER_REGS <= THREADS * 168, "register split");
 constexpr int COPY_WARP = 8, MMA_WARP = 9, PLAN_WARP = 10;
 constexpr int MAX_CTAS = 152;   // one per SM
@@ -1016,16 +1016,8 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
         } else if (!warp_active) {
           half_done();
         } else {
-          uint32_t r[4][32];
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (x * 32 < w) tm_ld32(ts + x * 32, r[x]);
-          tm_wait_ld(r[0]);
-          tm_loaded(r[1]);
-          tm_loaded(r[2]);
-          tm_loaded(r[3]);
-          if (masked) {
-            uint32_t see[4];
+          // the tile's keys that this row sees, 32 to a word
+          auto visible = [&](uint32_t (&see)[4]) {
             if (PR) {
               // near tiles: the sinks; others: the window, and the sinks when they adjoin it
               const int lo = j < s.near ? 0 : tok - A.window + 1;
@@ -1056,77 +1048,165 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
 #pragma unroll
               for (int x = 0; x < 4; ++x) see[x] = span(0, tok + 1, k0 + 32 * x);
             }
-            // (columns past the tile's width hold an earlier tile's)
+          };
+          // the row's maximum, raised to mt when that is far above it, and O and l with it
+          auto raise_to = [&](float mt) {
+            if (done == 0) {
+              m = mt;
+            } else {
+              const bool rise = active && (mt - m) * A.c > RAISE_LOG2;  // (-inf before: inf > 8)
+              if (__any_sync(0xffffffffu, rise)) {
+                const float f = rise ? ex2((m - mt) * A.c) : 1.0f;
+                if (rise) m = mt;
+                l *= f;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              see[x] &= span(0, w, 32 * x);
-              if (x * 32 < w && !__all_sync(0xffffffffu, see[x] == 0xffffffffu)) {
+                for (int x = 0; x < DP / 32; ++x) {
+                  uint32_t o[32];
+                  tm_ld32(to + x * 32, o);
+                  tm_wait_ld(o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (!(see[x] >> i & 1)) r[x][i] = 0xff800000u;
+                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  tm_st32(to + x * 32, o);
+                }
               }
             }
-          }
-          float mt;
-          if (w == TILE) {
-            mt = max_of<128>([&](int i) { return __uint_as_float(r[i >> 5][i & 31]); });
-          } else {
-            mt = -INFINITY;
+          };
+          if constexpr (PAIR) {
+            uint32_t r[4][32];
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-              if (x * 32 < w)
-                mt = fmaxf(mt, max_of<32>([&](int i) { return __uint_as_float(r[x][i]); }));
-          }
-          if (done == 0) {
-            m = mt;
-          } else {
-            const bool rise = active && (mt - m) * A.c > RAISE_LOG2;  // (-inf before: inf > 8)
-            if (__any_sync(0xffffffffu, rise)) {
-              const float f = rise ? ex2((m - mt) * A.c) : 1.0f;
-              if (rise) m = mt;
-              l *= f;
+              if (x * 32 < w) tm_ld32(ts + x * 32, r[x]);
+            tm_wait_ld(r[0]);
+            tm_loaded(r[1]);
+            tm_loaded(r[2]);
+            tm_loaded(r[3]);
+            if (masked) {
+              uint32_t see[4];
+              visible(see);
+              // (columns past the tile's width hold an earlier tile's)
 #pragma unroll
-              for (int x = 0; x < DP / 32; ++x) {
-                uint32_t o[32];
-                tm_ld32(to + x * 32, o);
-                tm_wait_ld(o);
+              for (int x = 0; x < 4; ++x) {
+                see[x] &= span(0, w, 32 * x);
+                if (x * 32 < w && !__all_sync(0xffffffffu, see[x] == 0xffffffffu)) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tm_st32(to + x * 32, o);
+                  for (int i = 0; i < 32; ++i)
+                    if (!(see[x] >> i & 1)) r[x][i] = 0xff800000u;
+                }
               }
             }
-          }
-          const float mc = m == -INFINITY ? 0.0f : m * A.c;
-          const float2 c2 = make_float2(A.c, A.c), mc2 = make_float2(-mc, -mc);
-          float2 sum[4] = {};
-          auto chunk = [&](int x) {  // the weights of 32 keys
-            uint32_t pw[16];
+            float mt;
+            if (w == TILE) {
+              mt = max_of<128>([&](int i) { return __uint_as_float(r[i >> 5][i & 31]); });
+            } else {
+              mt = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 e = fma2(make_float2(__uint_as_float(r[x][2 * i]),
-                                                __uint_as_float(r[x][2 * i + 1])), c2, mc2);
-              const float2 p = make_float2(ex2(e.x), ex2(e.y));
-              sum[i & 3] = add2(sum[i & 3], p);
-              pw[i] = pack16<BF>(p.x, p.y);
+              for (int x = 0; x < 4; ++x)
+                if (x * 32 < w)
+                  mt = fmaxf(mt, max_of<32>([&](int i) { return __uint_as_float(r[x][i]); }));
             }
-            tm_st16(ts + x * 16, pw);
-          };
-          // the products with the first 64 keys' values start under the others' weights
-          if (w == TILE) {
-            chunk(0);
-            chunk(1);
-            half_done();
-            chunk(2);
-            chunk(3);
+            raise_to(mt);
+            const float mc = m == -INFINITY ? 0.0f : m * A.c;
+            const float2 c2 = make_float2(A.c, A.c), mc2 = make_float2(-mc, -mc);
+            float2 sum[4] = {};
+            auto chunk = [&](int x) {  // the weights of 32 keys
+              uint32_t pw[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float2 e = fma2(make_float2(__uint_as_float(r[x][2 * i]),
+                                                  __uint_as_float(r[x][2 * i + 1])), c2, mc2);
+                const float2 p = make_float2(ex2(e.x), ex2(e.y));
+                sum[i & 3] = add2(sum[i & 3], p);
+                pw[i] = pack16<BF>(p.x, p.y);
+              }
+              tm_st16(ts + x * 16, pw);
+            };
+            // the products with the first 64 keys' values start under the others' weights
+            if (w == TILE) {
+              chunk(0);
+              chunk(1);
+              half_done();
+              chunk(2);
+              chunk(3);
+            } else {
+              chunk(0);
+              if (w > 32) chunk(1);
+              half_done();
+              if (w > 64) chunk(2);
+              if (w > 96) chunk(3);
+            }
+            sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+            l += sum[0].x + sum[0].y;
           } else {
-            chunk(0);
-            if (w > 32) chunk(1);
+            // One tile of rows: 64 scores at a time, the maximum of the tile's second half,
+            // then of its first, whose weights follow from registers; the second half is
+            // loaded again behind them.  (64 requests of 88 rows: 243 us, and 266 with all
+            // scores in registers as below, which spills; a pair's 8192 tokens take 372 us
+            // by halves and 334 as below.)
+            uint32_t r0[32], r1[32], see[4] = {~0u, ~0u, ~0u, ~0u};
+            if (masked) {
+              visible(see);
+              // (columns past the tile's width hold an earlier tile's)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) see[x] &= span(0, w, 32 * x);
+            }
+            auto hide = [&](uint32_t (&r)[32], uint32_t bits) {
+              if (masked && !__all_sync(0xffffffffu, bits == 0xffffffffu)) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (!(bits >> i & 1)) r[i] = 0xff800000u;
+              }
+            };
+            auto two = [&](int x) {  // chunks x and x + 1, and their maximum
+              tm_ld32(ts + x * 32, r0);
+              if ((x + 1) * 32 < w) tm_ld32(ts + x * 32 + 32, r1);
+              tm_wait_ld(r0);
+              tm_loaded(r1);
+              hide(r0, see[x]);
+              float t = max_of<32>([&](int i) { return __uint_as_float(r0[i]); });
+              if ((x + 1) * 32 < w) {
+                hide(r1, see[x + 1]);
+                t = fmaxf(t, max_of<32>([&](int i) { return __uint_as_float(r1[i]); }));
+              }
+              return t;
+            };
+            float mt = w > 64 ? two(2) : -INFINITY;
+            mt = fmaxf(mt, two(0));
+            raise_to(mt);
+            const float mc = m == -INFINITY ? 0.0f : m * A.c;
+            const float2 c2 = make_float2(A.c, A.c), mc2 = make_float2(-mc, -mc);
+            float2 sum[4] = {};
+            auto weights = [&](int x, uint32_t (&r)[32]) {  // of 32 keys
+              uint32_t pw[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float2 e = fma2(
+                    make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), c2, mc2);
+                const float2 p = make_float2(ex2(e.x), ex2(e.y));
+                sum[i & 3] = add2(sum[i & 3], p);
+                pw[i] = pack16<BF>(p.x, p.y);
+              }
+              tm_st16(ts + x * 16, pw);
+            };
+            // (P's columns lie over scores of the first half only; a pair's products
+            // with the first half's values start under the second's weights)
+            weights(0, r0);
+            if (w > 64) tm_ld32(ts + 64, r0);
+            if (w > 32) weights(1, r1);
             half_done();
-            if (w > 64) chunk(2);
-            if (w > 96) chunk(3);
+            if (w > 64) {
+              tm_wait_ld(r0);
+              hide(r0, see[2]);
+              if (w > 96) tm_ld32(ts + 96, r1);
+              weights(2, r0);
+              if (w > 96) {
+                tm_wait_ld(r1);
+                hide(r1, see[3]);
+                weights(3, r1);
+              }
+            }
+            sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+            l += sum[0].x + sum[0].y;
           }
-          sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-          l += sum[0].x + sum[0].y;
           tm_wait_st();
         }
         tc_before();
