@@ -1,7 +1,7 @@
 """GB300 (sm_103a) speculative-decoding verification.
 
 The product is libspecverify.so (C ABI in include/specverify.h, kernels in
-csrc/specverify.cu); `binding` is its thin Python marshalling layer and
+csrc/); `binding` is its thin Python marshalling layer and
 `synth` draws seeded synthetic inputs.  Importing the package loads nothing;
 the binding's names are resolved on first use.
 """

@@ -1,5 +1,26 @@
 // attention.cuh -- sm_103a kernels of the attention over the caches (the calls
 // are in attention.cu, the operations in include/svattn.h).
+//
+//   sv_attn       per query row, over its visible keys t in tiles of 128:
+//                   s_t = scale q . k_t,  m = max s,  l = sum exp(s_t - m),
+//                   O = sum exp(s_t - m) v_t,  out = O / l
+//                 in one pass: a tile's weights use the maximum so far, and O and l
+//                 are rescaled when it has risen (exactly: exp(m_old - m_new))
+//   sv_attn_join  the same sum over parts: m = max m_i, l = sum l_i exp(m_i - m),
+//                 O = sum O_i exp(m_i - m)
+//
+// What bounds them.  Tokens over a cache (trees, the ring): the cache is read
+// once, 4 D bytes per key and KV head, and the products are small beside it: HBM,
+// as long as a key tile's chain of products and softmax (about 1 us) hides under
+// its 64 KB (1.5 us of an SM's share).  Hence two streams of key tiles per SM, so
+// that one's products run under the other's softmax, copies five to twelve stages
+// ahead, and runs of equal length whatever the requests' lengths.  64 requests of
+// 22 nodes over 2000 to 9000 tokens (1.39 GB): 240 us, 5.8 TB/s, 0.85 of the
+// measured copy bandwidth.  Prompts: 4 D flops per pair of tokens and query head;
+// the tensor cores are busy 0.55 of the time, and the softmax of the two tiles of
+// queries that share an SM (two warps per quarter, in turn with the products that
+// wait for their weights) is what the rest waits for.  8192 tokens under a window
+// of 4096, 32 heads of 128: 335 us, 1.23 PFLOP/s, 0.64 of the measured bf16 rate.
 #ifndef SV_ATTENTION_CUH
 #define SV_ATTENTION_CUH
 
@@ -28,7 +49,8 @@ constexpr int ITEM_COST = 1;    // an item's fixed cost in tiles
 constexpr int TILE = 128;       // query rows of a tile, and keys of a tile
 constexpr int THREADS = 384;    // two softmax warpgroups, and one with a copy and a product warp
 // Registers: launched with 168 a thread (64512 a CTA); the softmax warpgroups
-// hold a row of scores each thread and take over what the third does not need.
+// hold up to 128 scores a thread and take over what the third does not need.
+// (Ragged prompts: 107 us with 208 / 88, 101 with 216 / 72, 132 with 184 / 136.)
 constexpr int SOFTMAX_REGS = 216, OTHER_REGS = 72;
 static_assert(256 * SOFTMAX_REGS + 128 * OTHER_REGS <= THREADS * 168, "register split");
 constexpr int COPY_WARP = 8, MMA_WARP = 9, PLAN_WARP = 10;
@@ -49,7 +71,7 @@ struct AttnParams {
   int32_t* status;
   float* part_o;          // partial outputs  [2 * CTAs][rows][DP / 4] x 4, columns outermost
   float2* part_ml;        // their maxima and sums [2 * CTAs][rows]
-  int4* desc;             // [CTAs] what each CTA's first and last segments are (see Desc bits)
+  int4* desc;             // [CTAs] what each CTA's first and last segments are (DESC_*)
   float c;                // scale * log2(e)
   int kind;
   int B, N, Hq, Hkv, D, G;
@@ -522,8 +544,8 @@ __device__ __forceinline__ uint32_t span(int a, int b, int k0) {
 //   NQ > 0: at most NQ rows.  The products are turned over, S^T = K Q^T and
 //     O^T = V^T P^T, so that the lanes hold keys (dimensions) and the few rows
 //     are columns: every thread has work however few the rows are, and the
-//     products cost NQ / 128 of a full tile's.  (A ring batch of 32 rows per
-//     item took 104 us with a row per lane.)
+//     products cost less.  (1024 requests of 12 rows per item: 444 us with a row
+//     per lane, 260 so, when both were first built.)
 template <int DP, int NQ>
 struct Smem {
   static constexpr int BYTES = TILE * DP * 2;                    // a tile of keys or values
@@ -573,7 +595,7 @@ static_assert(sizeof(Ctrl<0, true>) <= 3072 && sizeof(Ctrl<0, false>) <= 3072 &&
                   sizeof(Ctrl<64, false>) <= 3072,
               "control part");
 
-// desc[cta]: x = item index within the request | flags, y = request
+// desc[cta]: x = flags, y = item (of its request) and z = request of the first segment
 constexpr int DESC_IN = 1 << 30;       // the first segment starts inside its item
 constexpr int DESC_THROUGH = 1 << 29;  // and runs to the CTA's end without finishing it
 constexpr int DESC_OUT = 1 << 28;      // the last segment leaves its item unfinished
@@ -745,12 +767,16 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// The attention kernel.  Per CTA one copy warp (tiles by TMA into a ring of
-// stages), one product warp (S = Q K^T and O += P V on the tensor cores, S, P
-// and O in TMEM) and two softmax warpgroups, one row of a 128-row tile per
-// thread: the running maximum and sum of the softmax live in the thread's
-// registers, P overwrites S in TMEM as 16-bit weights, and O is rescaled only
-// when the maximum has risen by 2^RAISE_LOG2.
+// The attention kernel, one CTA per SM.  Warps:
+//   plan      the segments, a few ahead, with the loads and divisions they take
+//   copy      queries and key and value tiles by TMA into a ring of stages
+//   products  one thread: S and O += P V on the tensor cores (S, P and O in TMEM;
+//             the turned layout's P in shared memory), and the waits before them
+//   softmax   two warpgroups, one per stream.  A row per lane: the maximum and sum
+//             of a row in its thread, P over S as 16-bit weights.  Keys on the
+//             lanes: a maximum per column, agreed on by the warpgroup.
+// The weights are rounded once to the storage type (half a step each); their sum
+// l is taken before that, in 32 bits.
 template <int DP, int NQ, bool PAIR, bool PR, bool BF>
 __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ AttnParams A) {
   static_assert(!(NQ && (PAIR || PR)), "few rows make one tile, and prompts have many");
@@ -1721,29 +1747,32 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
 
 // Join of the items that the CTAs' runs cut, from the parts' maxima, sums and
 // outputs.  A warp takes one unit of a cut item at a time: one row's columns, a
-// lane each four of them (NQ > 0), or 32 rows' 16 columns, a lane each a row.
-// First the common maximum and the sum, then the outputs, so that the loads of
-// different parts do not wait for one another.
-constexpr int JOIN_WARPS = 8;
+// lane each four of them (NQ > 0), or 32 rows' 16 columns, a lane each a row.  It
+// is bound by the latency of its loads, so what the CTAs were about is read once
+// per block, and the parts' values are loaded four parts at a time.
+constexpr int JOIN_WARPS = 8, JOIN_BLOCKS = 4;  // blocks per SM
 template <int DP, int NQ, bool PAIR, bool BF>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) sv_attn_join(const __grid_constant__ AttnParams A,
                                                                int ctas) {
   constexpr int ROWS = NQ ? NQ : PAIR ? 2 * TILE : TILE;
   constexpr int VECS = NQ ? 1 : 4;  // four-column pieces per lane
+  __shared__ int4 desc[MAX_CTAS];
   __shared__ int2 cuts[MAX_CTAS];   // (first CTA of the item, CTAs of it)
   __shared__ int found_s[JOIN_WARPS];
   const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  static_assert(MAX_CTAS <= JOIN_WARPS * 32, "one thread per CTA of the main kernel");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (tid < ctas) desc[tid] = A.desc[tid];
+  __syncthreads();
   // The cut items, in the order of their first CTAs (every block has to find
   // the same list).  CTA c holds an item's first part when its last segment is
   // cut and did not itself begin inside the item.
-  static_assert(MAX_CTAS <= JOIN_WARPS * 32, "one thread per CTA of the main kernel");
   int parts = 0;
   if (tid + 1 < ctas) {
-    const int4 d = A.desc[tid];
-    if ((d.x & DESC_OUT) && !(d.x & DESC_THROUGH)) {
+    const int x = desc[tid].x;
+    if ((x & DESC_OUT) && !(x & DESC_THROUGH)) {
       int e = tid + 1;
-      while (e + 1 < ctas && (A.desc[e].x & DESC_THROUGH)) ++e;
+      while (e + 1 < ctas && (desc[e].x & DESC_THROUGH)) ++e;
       parts = e - tid + 1;
     }
   }
@@ -1768,41 +1797,61 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) sv_attn_join(const __grid_con
     const int cg = w % (DP / 16), rgp = w / (DP / 16);
     const int st = PAIR ? rgp / row_groups : 0;
     const int row = NQ ? w : (rgp % row_groups) * 32 + lane;
-    const int4 d1 = A.desc[cut.x + 1];  // its first segment is of this item
+    const int4 d1 = desc[cut.x + 1];  // its first segment is of this item
     const int item = d1.y, b = d1.z;
     const int h = item / A.MT, mt = item - h * A.MT;
     const int rt = row / A.G, rg = row - rt * A.G;
     const int tok = mt * (PAIR ? 2 : 1) * A.tpt + st * A.tpt + rt;
     if (NQ ? lane >= DP / 4 : row >= TILE || rt >= A.tpt || tok >= A.N) continue;
-    const size_t s0 = size_t(cut.x) * 2 + (A.desc[cut.x].x & DESC_LAST1 ? 1 : 0);
-    auto slot = [&](int p) { return p ? size_t(cut.x + p) * 2 : s0; };
+    const size_t s0 = size_t(cut.x) * 2 + (desc[cut.x].x & DESC_LAST1 ? 1 : 0);
     float m = -INFINITY, l = 0.0f;
     bool bad = false;
-#pragma unroll 4
-    for (int p = 0; p < cut.y; ++p) {
-      const float2 ml = A.part_ml[slot(p) * ROWS + st * TILE + row];
-      bad |= ml.y == -1.0f;
-      m = fmaxf(m, ml.x);
-    }
-    if (m == -INFINITY) m = 0.0f;
     float4 acc[VECS];
 #pragma unroll
     for (int i = 0; i < VECS; ++i) acc[i] = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-    for (int p = 0; p < cut.y; ++p) {
-      const size_t s = slot(p);
-      const float2 ml = A.part_ml[s * ROWS + st * TILE + row];
-      const float g = ex2(ml.x - m);
-      l += ml.y * g;
+    constexpr int AT_ONCE = 4;
+    for (int p0 = 0; p0 < cut.y; p0 += AT_ONCE) {
+      float2 ml[AT_ONCE];
+      float4 o[AT_ONCE][VECS];
+#pragma unroll
+      for (int k = 0; k < AT_ONCE; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.0f);
+        if (p0 + k < cut.y) {
+          const size_t s = p0 + k ? size_t(cut.x + p0 + k) * 2 : s0;
+          ml[k] = A.part_ml[s * ROWS + st * TILE + row];
+#pragma unroll
+          for (int i = 0; i < VECS; ++i)
+            o[k][i] = NQ ? src[(s * ROWS + row) * (DP / 4) + lane]
+                         : src[(s * (DP / 4) + cg * 4 + i) * ROWS + st * TILE + row];
+        }
+      }
+      float m2 = m;
+#pragma unroll
+      for (int k = 0; k < AT_ONCE; ++k) m2 = fmaxf(m2, ml[k].x);
+      const float mu = m2 == -INFINITY ? 0.0f : m2, f = ex2(m - mu);
+      m = m2;
+      l *= f;
 #pragma unroll
       for (int i = 0; i < VECS; ++i) {
-        const float4 o = NQ ? src[(s * ROWS + row) * (DP / 4) + lane]
-                            : src[(s * (DP / 4) + cg * 4 + i) * ROWS + st * TILE + row];
-        acc[i].x += o.x * g;
-        acc[i].y += o.y * g;
-        acc[i].z += o.z * g;
-        acc[i].w += o.w * g;
+        acc[i].x *= f;
+        acc[i].y *= f;
+        acc[i].z *= f;
+        acc[i].w *= f;
       }
+#pragma unroll
+      for (int k = 0; k < AT_ONCE; ++k)
+        if (p0 + k < cut.y) {
+          const float g = ex2(ml[k].x - mu);
+          bad |= ml[k].y == -1.0f;
+          l += ml[k].y * g;
+#pragma unroll
+          for (int i = 0; i < VECS; ++i) {
+            acc[i].x += o[k][i].x * g;
+            acc[i].y += o[k][i].y * g;
+            acc[i].z += o[k][i].z * g;
+            acc[i].w += o[k][i].w * g;
+          }
+        }
     }
     const float f = 1.0f / l;
     uint16_t* const o = A.out + ((size_t(b) * A.N + tok) * A.Hq + h * A.G + rg) * A.D;
@@ -1838,7 +1887,7 @@ int launch_as(const AttnParams& A, int device, int grid, int ctas, cudaStream_t 
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
   if (PR || A.whole) return SV_OK;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(2 * ctas));
+  cfg.gridDim = dim3(unsigned(JOIN_BLOCKS * ctas));
   cfg.blockDim = dim3(JOIN_WARPS * 32);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
