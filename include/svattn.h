@@ -70,7 +70,7 @@ size_t sv_attn_workspace_bytes(int N, int Hq, int Hkv, int D);
  *   k_new, v_new   [B][LH][N][D]: the tree's own entries
  * The call attends for one layer: rows head0 .. head0 + Hkv - 1 of LH.
  * Requires page_size a multiple of 8 in [8, 65536], 1 <= N <= 256,
- * 0 <= head0, head0 + Hkv <= LH, B <= 65535.  sv_window_block_table's
+ * 0 <= head0, head0 + Hkv <= LH, B * LH < 2^31, B <= 65535.  sv_window_block_table's
  * outputs are a block_table and seq_lens of this call (the draft model's
  * window).
  * A request with a length outside its range (SV_ST_BAD_LENGTH), a malformed

@@ -176,7 +176,7 @@ int sv_tree_attn(int dtype, const void* q, const void* k_pages, const void* v_pa
   if (dtype != SV_BF16 && dtype != SV_F16) return SV_ERR_DTYPE;
   if (B < 0 || B > 65535 || N < 1 || N > MAX_N || bad_heads(Hq, Hkv, D) || num_pages < 1 ||
       LH < 1 || head0 < 0 || head0 > LH - Hkv || page_size < 8 || page_size > 65536 ||
-      page_size % 8 != 0 || cols < 1 || bad_scale(scale))
+      page_size % 8 != 0 || cols < 1 || (long long)B * LH > 0x7fffffffLL || bad_scale(scale))
     return SV_ERR_INVALID_ARG;
   if (B == 0) return SV_OK;
   if (!q || !k_pages || !v_pages || !block_table || !seq_lens || !k_new || !v_new || !out)

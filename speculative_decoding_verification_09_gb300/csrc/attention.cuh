@@ -193,7 +193,8 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 // single thread issues, and keeps the products' descriptors in uniform registers.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
-  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}"
+               : "=r"(p));
   return p != 0;
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
@@ -256,14 +257,18 @@ __device__ __forceinline__ void tm_ld8(uint32_t addr, uint32_t (&r)[8]) {
                : "r"(addr));
 }
 __device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t (&r)[16]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
                       "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
                       "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                : "r"(addr));
 }
 __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[16]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
                       "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
                       "r"(r[13]), "r"(r[14]), "r"(r[15])
@@ -382,7 +387,7 @@ __device__ __forceinline__ int cache_len(const AttnParams& A, int b, int& bad, i
   return bad ? 0 : int(n < C ? n : C);
 }
 
-// The segments of a CTA, in order, taken by whole warps.
+// The segments of a CTA, in order, found by a whole warp.
 // TREE and RING: the tiles of all items, in the order request, KV head, item of
 // the head, are cut into equal runs, one per CTA; an item cut by a run's end is
 // joined by the second kernel, or (whole) is taken by the CTA of its first
@@ -577,9 +582,10 @@ struct Few {                   // NQ > 0, per stream and column
 };
 template <int NQ, bool PAIR>
 struct Ctrl {
+  // barriers: stages filled and free, queries, scores, weights (a pair's first half, all),
+  // output complete, segments planned and taken, the end after a wait gave up, another item
   unsigned long long full[12], empty[12], q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2],
-      o_full[2],
-      seg_full[SEGS], seg_empty[SEGS], drain, next_full;
+      o_full[2], seg_full[SEGS], seg_empty[SEGS], drain, next_full;
   alignas(16) uint4 next;    // PROMPT: the answer to a request for another item
   Seg seg[SEGS];
   long long start_at;
@@ -592,6 +598,7 @@ struct Ctrl {
   };
 };
 static_assert(sizeof(Ctrl<0, true>) <= 3072 && sizeof(Ctrl<0, false>) <= 3072 &&
+                  sizeof(Ctrl<16, false>) <= 3072 && sizeof(Ctrl<32, false>) <= 3072 &&
                   sizeof(Ctrl<64, false>) <= 3072,
               "control part");
 
@@ -657,8 +664,8 @@ __device__ __forceinline__ void sum_columns(float* v, int lane) {
 // key.  All keys of a tile use one maximum per column; it is raised, the sums
 // and O (columns from to) rescaled, when a score exceeds it by 2^RAISE_LOG2.
 template <int NQ, bool BF>
-__device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>& C, int st, int key,
-                                            uint32_t ts, uint32_t to, unsigned long long sees,
+__device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>& C, int st,
+                                            int key, uint32_t ts, uint32_t to, unsigned long long sees,
                                             bool masked, bool started, bool& unset, float* lq,
                                             unsigned char* pbuf) {
   constexpr int W = NQ < 32 ? NQ : 32;
@@ -755,7 +762,8 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
   const int piece = (key & 63) >> 3;
 #pragma unroll
   for (int q = 0; q < NQ; q += 2) {
-    const float2 p = make_float2(ex2(__uint_as_float(score(q))), ex2(__uint_as_float(score(q + 1))));
+    const float2 p =
+        make_float2(ex2(__uint_as_float(score(q))), ex2(__uint_as_float(score(q + 1))));
     const float2 l = add2(make_float2(lq[q], lq[q + 1]), p);
     lq[q] = l.x;
     lq[q + 1] = l.y;
@@ -859,7 +867,8 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
     if (run > 0 && lo >= before && lo < before + mine) {
       long long at = before;
       for (int b = b0; b < b1; ++b) {
-        const long long t = items * (tiles_of(cache_len(A, b, bad, pos)) + tiles_of(A.N) + ITEM_COST);
+        const long long t =
+            items * (tiles_of(cache_len(A, b, bad, pos)) + tiles_of(A.N) + ITEM_COST);
         if (lo < at + t) {
           C.start_b = b;
           C.start_at = lo - at;
@@ -1002,7 +1011,8 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           ok = ok && warp_wait(bar(&C.full[u % STAGES]), (u / STAGES) & 1, A.status, abort);
           if (NQ == 0 && !ok) break;
           if (ok && dead) {
-            uint4* v = reinterpret_cast<uint4*>(smem + SM::STAGE_AT + (u % STAGES) * BYTES + row * 128);
+            uint4* v =
+                reinterpret_cast<uint4*>(smem + SM::STAGE_AT + (u % STAGES) * BYTES + row * 128);
 #pragma unroll
             for (int x = 0; x < HALVES; ++x)
 #pragma unroll
@@ -1421,7 +1431,8 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
             }
             put(v, col);
           }
-          if (!whole && st == 0 && active) A.part_ml[part] = make_float2(mm * A.c, bad ? -1.0f : ll);
+          if (!whole && st == 0 && active)
+            A.part_ml[part] = make_float2(mm * A.c, bad ? -1.0f : ll);
         }
         tc_before();
       }
@@ -1568,7 +1579,8 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
         const int tok = PR ? s.start : s.b * A.N;
         for (int q = 0; q < (PAIR ? 2 : 1); ++q)
           for (int x = 0; x < HALVES; ++x)
-            tma_4d(base + (PAIR ? q : slot) * SM::Q_BYTES + x * (SM::Q_BYTES / HALVES), &A.mq, fb, x * 64, 0, s.h,
+            tma_4d(base + (PAIR ? q : slot) * SM::Q_BYTES + x * (SM::Q_BYTES / HALVES), &A.mq, fb,
+                   x * 64, 0, s.h,
                    tok + (s.mt * (PAIR ? 2 : 1) + q) * A.tpt);
       }
       __syncwarp();

@@ -190,7 +190,8 @@ __global__ void __launch_bounds__(KV_THREADS) sv_kv_fill_copy(const FillParams K
 }
 
 constexpr int PC_ROWS = 16;     // layer/head rows per CTA
-constexpr int PC_ENTRIES = 64;  // path entries per CTA
+constexpr int PC_ENTRIES = 64;  // path entries per CTA and pass
+constexpr int PC_SPANS = 64;    // CTAs along the entries
 
 struct PageParams {
   uint4* k_pages;
@@ -232,7 +233,7 @@ __device__ int page_commit_faults(const PageParams& K, int b, int k, long long l
 }
 
 // Path entries into pages: PC_ROWS rows x PC_ENTRIES entries of request
-// blockIdx.y per CTA (entries blockIdx.z * PC_ENTRIES on), KV_UNROLL vectors of
+// blockIdx.y per CTA and pass (passes of gridDim.z spans), KV_UNROLL vectors of
 // K and of V per thread loaded before any is stored.  IN_PLACE: the lengths
 // are updated by the next kernel instead, after every CTA has read them.
 template <bool IN_PLACE>
@@ -243,51 +244,54 @@ __global__ void __launch_bounds__(KV_THREADS) sv_page_copy(const PageParams K) {
   const int b = int(blockIdx.y);
   const int k = __ldg(K.num_accepted + b);
   const long long len = __ldg(K.seq_lens + b);
-  const int j0 = int(blockIdx.z) * PC_ENTRIES;
+  const int first = int(blockIdx.z) * PC_ENTRIES;
   const bool writer = blockIdx.x == 0 && blockIdx.z == 0;
-  if (!writer && j0 > k) return;
+  if (!writer && first > k) return;
   const int bad = k < 0 ? 0 : page_commit_faults(K, b, k, len);
   if (writer && threadIdx.x == 0 && !IN_PLACE) {
     K.out_seq_lens[b] = int32_t(k < 0 || bad ? len : len + k + 1);
     set_status(K.status, bad);
   }
   if (k < 0 || bad) return;
-  const int cnt = min(PC_ENTRIES, k + 1 - j0);
-  if (int(threadIdx.x) < cnt) {
-    const int j = j0 + int(threadIdx.x);
-    const long long at = len + j;
-    const int pg = __ldg(K.table + size_t(b) * K.cols + at / K.page);
-    dst_of[threadIdx.x] = size_t(pg) * K.LH * K.page + size_t(at % K.page);
-    src_of[threadIdx.x] = K.nodes && j > 0 ? __ldg(K.nodes + size_t(b) * K.N + j - 1) : j;
-  }
-  __syncthreads();
   const int r0 = int(blockIdx.x) * PC_ROWS, rows = min(PC_ROWS, K.LH - r0);
-  const int total = cnt * PC_ROWS * K.nvec;  // <= 64 * 16 * 512
-  for (int f0 = int(threadIdx.x); f0 < total; f0 += KV_THREADS * KV_UNROLL) {
-    uint4 kv[KV_UNROLL], vv[KV_UNROLL];
-    size_t dst[KV_UNROLL];
-    bool use[KV_UNROLL];
+  for (int j0 = first; j0 <= k; j0 += int(gridDim.z) * PC_ENTRIES) {
+    const int cnt = min(PC_ENTRIES, k + 1 - j0);
+    if (int(threadIdx.x) < cnt) {
+      const int j = j0 + int(threadIdx.x);
+      const long long at = len + j;
+      const int pg = __ldg(K.table + size_t(b) * K.cols + at / K.page);
+      dst_of[threadIdx.x] = size_t(pg) * K.LH * K.page + size_t(at % K.page);
+      src_of[threadIdx.x] = K.nodes && j > 0 ? __ldg(K.nodes + size_t(b) * K.N + j - 1) : j;
+    }
+    __syncthreads();
+    const int total = cnt * PC_ROWS * K.nvec;  // <= 64 * 16 * 512
+    for (int f0 = int(threadIdx.x); f0 < total; f0 += KV_THREADS * KV_UNROLL) {
+      uint4 kv[KV_UNROLL], vv[KV_UNROLL];
+      size_t dst[KV_UNROLL];
+      bool use[KV_UNROLL];
 #pragma unroll
-    for (int u = 0; u < KV_UNROLL; ++u) {
-      const int f = f0 + u * KV_THREADS;
-      const int row = div_by(f, K.m_nvec), q = f - row * K.nvec;
-      const int r = row % PC_ROWS, j = row / PC_ROWS;
-      use[u] = f < total && r < rows;
-      dst[u] = 0;
-      if (use[u]) {
-        const size_t src = ((size_t(b) * K.LH + r0 + r) * K.N + src_of[j]) * K.nvec + q;
-        dst[u] = (dst_of[j] + size_t(r0 + r) * K.page) * K.nvec + q;
-        kv[u] = __ldg(K.k_new + src);
-        vv[u] = __ldg(K.v_new + src);
+      for (int u = 0; u < KV_UNROLL; ++u) {
+        const int f = f0 + u * KV_THREADS;
+        const int row = div_by(f, K.m_nvec), q = f - row * K.nvec;
+        const int r = row % PC_ROWS, j = row / PC_ROWS;
+        use[u] = f < total && r < rows;
+        dst[u] = 0;
+        if (use[u]) {
+          const size_t src = ((size_t(b) * K.LH + r0 + r) * K.N + src_of[j]) * K.nvec + q;
+          dst[u] = (dst_of[j] + size_t(r0 + r) * K.page) * K.nvec + q;
+          kv[u] = __ldg(K.k_new + src);
+          vv[u] = __ldg(K.v_new + src);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < KV_UNROLL; ++u) {
+        if (use[u]) {
+          K.k_pages[dst[u]] = kv[u];
+          K.v_pages[dst[u]] = vv[u];
+        }
       }
     }
-#pragma unroll
-    for (int u = 0; u < KV_UNROLL; ++u) {
-      if (use[u]) {
-        K.k_pages[dst[u]] = kv[u];
-        K.v_pages[dst[u]] = vv[u];
-      }
-    }
+    __syncthreads();  // the entries' places are used up
   }
 }
 
@@ -500,7 +504,8 @@ int sv_page_commit(void* k_pages, void* v_pages, const void* k_new, const void* 
   K.num_pages = num_pages; K.page = page_size; K.cols = cols;
   K.m_nvec = div_magic(K.nvec);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid(unsigned(gx), unsigned(B), unsigned((N + PC_ENTRIES - 1) / PC_ENTRIES));
+  const int spans = (N + PC_ENTRIES - 1) / PC_ENTRIES;
+  const dim3 grid(unsigned(gx), unsigned(B), unsigned(spans < PC_SPANS ? spans : PC_SPANS));
   if (!in_place) {
     sv_page_copy<false><<<grid, KV_THREADS, 0, st>>>(K);
     return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;

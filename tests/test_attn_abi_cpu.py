@@ -49,7 +49,8 @@ def test_tree_refusals(L):
     for bad in (dict(B=-1), dict(B=65536), dict(N=0), dict(N=257), dict(Hq=6), dict(Hq=0), dict(Hkv=0), dict(D=0),
                 dict(D=60), dict(D=136), dict(P=0), dict(LH=3), dict(h0=1), dict(h0=-1), dict(page=0), dict(page=12),
                 dict(page=65544), dict(cols=0), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
-                dict(scale=float("inf")), dict(scale=3e38), dict(Hq=1032, Hkv=8, LH=8)):
+                dict(scale=float("inf")), dict(scale=3e38), dict(Hq=1032, Hkv=8, LH=8),
+                dict(B=65535, LH=1 << 16)):
         assert tree(L, **bad) == BAD, bad
     for p in ("q", "k", "v", "bt", "sl", "kn", "vn", "out"):
         assert tree(L, **{p: None}) == BAD, p
