@@ -156,37 +156,37 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* m, uint3
 
 // Tensor-core products.  Tiles lie in shared memory as 64-element (128-byte)
 // wide blocks of 128 rows in the 128-byte swizzle, one block after another.
+// A descriptor's low word has the address; the high word is a constant of the
+// operand's order, so that only the low words have to be moved for a product.
 // K-major operand (queries, keys): rows 128 bytes apart, 8-row groups 1024.
-__device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {
-  return uint64_t((addr >> 4) & 0x3fff) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) |
-         (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
+constexpr uint32_t DESC_HI = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_rows(uint32_t addr) { return (addr >> 4) | (1u << 16); }
 // MN-major operand (values: the 64 dimensions of a block are contiguous):
 // 8-key groups 1024 bytes apart, 64-dimension blocks `blocks` bytes.  (0: a
 // head of at most 64 dimensions taken twice to make up the 128 rows of V^T;
 // the second half of O^T is not read.)
-__device__ __forceinline__ uint64_t desc_cols(uint32_t addr, uint32_t blocks) {
-  return uint64_t((addr >> 4) & 0x3fff) | (uint64_t(blocks >> 4) << 16) |
-         (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+__device__ __forceinline__ uint32_t desc_cols(uint32_t addr, uint32_t blocks) {
+  return (addr >> 4) | (blocks >> 4 << 16);
 }
 __device__ __forceinline__ uint32_t instr_desc(int bf16, bool a_cols, bool b_cols, int n) {
   return (1u << 4) | (uint32_t(bf16) << 7) | (uint32_t(bf16) << 10) | (a_cols ? 1u << 15 : 0u) |
          (b_cols ? 1u << 16 : 0u) | (uint32_t(n >> 3) << 17) | (uint32_t(TILE >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b),
-      "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.u32 p, %4, 0;\n"
+      " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}" ::"r"(d), "r"(a), "r"(b),
+      "r"(idesc), "r"(accumulate), "n"(DESC_HI)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b),
-      "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.u32 p, %4, 0;\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}" ::"r"(d), "r"(a), "r"(b),
+      "r"(idesc), "r"(accumulate), "n"(DESC_HI)
       : "memory");
 }
 // One lane of the (converged) warp: the form in which the compiler knows that a
@@ -1617,13 +1617,13 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       return true;
     };
     auto scores = [&](int st, int q, uint32_t u, int w) {  // S[st] = Q[q] K^T, or K Q[q]^T
-      const uint64_t qa = desc_rows(base + q * SM::Q_BYTES);
-      const uint64_t ka = desc_rows(base + SM::STAGE_AT + (u % STAGES) * BYTES);
+      const uint32_t qa = desc_rows(base + q * SM::Q_BYTES);
+      const uint32_t ka = desc_rows(base + SM::STAGE_AT + (u % STAGES) * BYTES);
 #pragma unroll
       for (int k = 0; k < DP / 16; ++k) {
         if (k * 16 >= A.D) break;  // (the rest of the tiles is zeros)
-        const uint64_t dq = qa + (((k / 4) * (SM::Q_BYTES / HALVES) + (k % 4) * 32) >> 4);
-        const uint64_t dk = ka + (((k / 4) * 16384 + (k % 4) * 32) >> 4);
+        const uint32_t dq = qa + (((k / 4) * (SM::Q_BYTES / HALVES) + (k % 4) * 32) >> 4);
+        const uint32_t dk = ka + (((k / 4) * 16384 + (k % 4) * 32) >> 4);
         mma_ss(tmem + st * S_COLS, NQ ? dk : dq, NQ ? dq : dk,
                NQ ? id_s : id_s | uint32_t(w >> 3) << 17, k > 0);
       }
@@ -1631,14 +1631,14 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
     };
     // O[st] (+)= P[st] V, or V^T P[st]^T, over sixteens k0 .. k1 - 1 of the tile's keys
     auto values = [&](int st, uint32_t u, int w, bool more, int k0, int k1) {
-      const uint64_t va = desc_cols(base + SM::STAGE_AT + (u % STAGES) * BYTES,
+      const uint32_t va = desc_cols(base + SM::STAGE_AT + (u % STAGES) * BYTES,
                                     NQ && DP == 64 ? 0 : 16384);
-      const uint64_t pa = desc_rows(base + SM::P_AT + st * SM::P_BYTES);
+      const uint32_t pa = desc_rows(base + SM::P_AT + st * SM::P_BYTES);
 #pragma unroll
       for (int k = k0; k < k1; ++k) {
         if (k * 16 >= w) break;
-        const uint64_t dv = va + ((k * 2048) >> 4);
-        const uint64_t dp = pa + (((k / 4) * (NQ * 128) + (k % 4) * 32) >> 4);
+        const uint32_t dv = va + ((k * 2048) >> 4);
+        const uint32_t dp = pa + (((k / 4) * (NQ * 128) + (k % 4) * 32) >> 4);
         if (NQ) mma_ss(tmem + O_AT + st * S_COLS, dv, dp, id_o, more || k > 0);
         else mma_ts(tmem + O_AT + st * S_COLS, tmem + st * S_COLS + k * 8, dv, id_o, more || k > 0);
       }
