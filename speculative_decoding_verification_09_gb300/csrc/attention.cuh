@@ -563,6 +563,8 @@ struct Smem {
   static constexpr int CTRL = STAGE_AT + STAGES * BYTES;         // offset of the control part
   static constexpr int TOTAL = CTRL + 3072;
 };
+template <bool V>
+struct Yes { static constexpr bool value = V; };
 template <int NQ, class A, class B>
 struct Either { using T = A; };
 template <class A, class B>
@@ -1516,91 +1518,108 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
     }
   } else if (warp == COPY_WARP) {
     // ------------------------------------------------------------ copies
-    uint32_t idx = 0;   // copies issued (low bits: stage and phase)
-    int segs = 0;
-    bool ok = true;
-    auto tile = [&](const Seg& s, int jj, bool is_v) {
-      const uint32_t st = idx % STAGES, use = idx / STAGES;
-      const uint32_t fb = bar(&C.full[st]);
-      const uint32_t dst = base + SM::STAGE_AT + st * BYTES;
-      if (use > 0 && !warp_wait(bar(&C.empty[st]), (use - 1) & 1, A.status, abort)) return false;
-      const Keys ky = keys_of<PR>(A, s, s.j0 + jj);
-      if (PR) {
-        if (elect_one()) {
-          mbar_arrive_tx(fb, BYTES);
-          for (int x = 0; x < HALVES; ++x)
-            tma_3d(dst + x * 16384, is_v ? &A.mv : &A.mk, fb, x * 64, s.h, s.start + ky.k0);
+    // One thread, or (pages) a warp with a lane per box of page rows.
+    auto copies = [&](auto solo) {
+      constexpr bool SOLO = decltype(solo)::value;
+      const bool lead = SOLO || lane == 0;
+      auto wait = [&](uint32_t bar, unsigned parity) {
+        return SOLO ? mbar_wait(bar, parity, A.status, abort)
+                    : warp_wait(bar, parity, A.status, abort);
+      };
+      auto together = [&] {
+        if (!SOLO) __syncwarp();
+      };
+      uint32_t st = 0, lap = 0, idx = 0;  // stage, times around the ring, copies
+      int segs = 0;
+      bool ok = true;
+      for (;;) {
+        ok = wait(bar(&C.seg_full[segs % AHEAD]), (segs / AHEAD) & 1);
+        if (!ok) break;
+        const Seg s = C.seg[segs % AHEAD];
+        if (s.n == 0) break;
+        together();
+        if (lead) mbar_arrive(bar(&C.seg_empty[segs % AHEAD]));
+        const int slot = PAIR ? 0 : segs & 1;
+        const int use = PAIR ? segs : segs >> 1;
+        ok = wait(bar(&C.q_empty[slot]), (use & 1) ^ 1);  // (passes before the first use)
+        if (!ok) break;
+        if (lead) {
+          const uint32_t fb = bar(&C.q_full[slot]);
+          mbar_arrive_tx(fb, (PAIR ? 2 : 1) * A.q_rows * DP * 2);
+          const int tok = PR ? s.start : s.b * A.N;
+          for (int q = 0; q < (PAIR ? 2 : 1); ++q)
+            for (int x = 0; x < HALVES; ++x)
+              tma_4d(base + (PAIR ? q : slot) * SM::Q_BYTES + x * (SM::Q_BYTES / HALVES), &A.mq,
+                     fb, x * 64, 0, s.h, tok + (s.mt * (PAIR ? 2 : 1) + q) * A.tpt);
         }
-      } else {
-        if (ky.staged) {
-          if (elect_one()) {
-            mbar_arrive_tx(fb, BYTES);
-            for (int x = 0; x < HALVES; ++x)
-              tma_3d(dst + x * 16384, is_v ? &A.mvn : &A.mkn, fb, x * 64, ky.k0,
-                     s.b * A.LH + A.head0 + s.h);
+        together();
+        ++segs;
+        const int plane = PR ? s.h : s.b * A.LH + A.head0 + s.h;
+        auto tile = [&](int jj, bool is_v) {
+          const uint32_t fb = bar(&C.full[st]);
+          const uint32_t dst = base + SM::STAGE_AT + st * BYTES;
+          if (!wait(bar(&C.empty[st]), (lap & 1) ^ 1)) return false;
+          const Keys ky = keys_of<PR>(A, s, s.j0 + jj);
+          if (SOLO || ky.staged) {
+            if (lead) {
+              const CUtensorMap* const m = !PR && ky.staged ? (is_v ? &A.mvn : &A.mkn)
+                                                            : (is_v ? &A.mv : &A.mk);
+              mbar_arrive_tx(fb, BYTES);
+#pragma unroll
+              for (int x = 0; x < HALVES; ++x) {
+                if (PR) tma_3d(dst + x * 16384, m, fb, x * 64, plane, s.start + ky.k0);
+                else tma_3d(dst + x * 16384, m, fb, x * 64, ky.k0, plane);
+              }
+            }
+          } else {
+            // a page outside the pool is read as page 0 (the softmax warps report it
+            // and drop the result)
+            const int boxes = (ky.n + A.box - 1) / A.box;
+            if (lead) mbar_arrive_tx(fb, boxes * A.box * DP * 2);
+            __syncwarp();
+            if (lane < boxes) {
+              const int t = ky.k0 + lane * A.box;
+              const int col = t / A.page;
+              int pg = __ldg(A.table + size_t(s.b) * A.cols + col);
+              if (pg < 0 || pg >= A.num_pages) pg = 0;
+#pragma unroll
+              for (int x = 0; x < HALVES; ++x)
+                tma_4d(dst + x * 16384 + lane * A.box * 128, is_v ? &A.mv : &A.mk, fb, x * 64,
+                       t - col * A.page, A.head0 + s.h, pg);
+            }
           }
-        } else if (A.kind == RING) {
-          if (elect_one()) {
-            mbar_arrive_tx(fb, BYTES);
-            for (int x = 0; x < HALVES; ++x)
-              tma_3d(dst + x * 16384, is_v ? &A.mv : &A.mk, fb, x * 64, ky.k0,
-                     s.b * A.LH + A.head0 + s.h);
+          together();
+          ++idx;
+          if (++st == STAGES) {
+            st = 0;
+            ++lap;
           }
-        } else {
-          // one lane per box of page rows; a page outside the pool is read as
-          // page 0 (the softmax warps report it and drop the result)
-          const int boxes = (ky.n + A.box - 1) / A.box;
-          if (lane == 0) mbar_arrive_tx(fb, boxes * A.box * DP * 2);
-          __syncwarp();
-          if (lane < boxes) {
-            const int t = ky.k0 + lane * A.box;
-            const int col = t / A.page;
-            int pg = __ldg(A.table + size_t(s.b) * A.cols + col);
-            if (pg < 0 || pg >= A.num_pages) pg = 0;
-            for (int x = 0; x < HALVES; ++x)
-              tma_4d(dst + x * 16384 + lane * A.box * 128, is_v ? &A.mv : &A.mk, fb, x * 64,
-                     t - col * A.page, A.head0 + s.h, pg);
-          }
+          return true;
+        };
+        constexpr int LAG = PAIR ? 0 : 1;
+        for (int i = 0; ok && i < s.n + LAG; ++i) {
+          if (i < s.n) ok = tile(i, false);
+          if (ok && i >= LAG) ok = tile(i - LAG, true);
         }
+        if (!ok) break;
       }
-      __syncwarp();
-      ++idx;
-      return true;
+      if (*abort) {  // the copies in flight land before the CTA ends
+        const unsigned long long t0 = globaltimer();
+        for (uint32_t u = idx > STAGES ? idx - STAGES : 0; u < idx; ++u)
+          while (!mbar_try(bar(&C.full[u % STAGES]), (u / STAGES) & 1) &&
+                 globaltimer() - t0 < WAIT_LIMIT_NS) {
+          }
+        for (int u = max(0, segs - (PAIR ? 1 : 2)); u < segs; ++u)
+          while (!mbar_try(bar(&C.q_full[PAIR ? 0 : u & 1]), (PAIR ? u : u >> 1) & 1) &&
+                 globaltimer() - t0 < WAIT_LIMIT_NS) {
+          }
+      }
     };
-    while (ok && seg_wait(segs) && C.seg[segs % AHEAD].n) {
-      const Seg s = C.seg[segs % AHEAD];
-      seg_done(segs);
-      const int slot = PAIR ? 0 : segs & 1;
-      const int use = PAIR ? segs : segs >> 1;
-      if (use > 0 && !warp_wait(bar(&C.q_empty[slot]), (use - 1) & 1, A.status, abort)) break;
-      if (elect_one()) {
-        const uint32_t fb = bar(&C.q_full[slot]);
-        mbar_arrive_tx(fb, (PAIR ? 2 : 1) * A.q_rows * DP * 2);
-        const int tok = PR ? s.start : s.b * A.N;
-        for (int q = 0; q < (PAIR ? 2 : 1); ++q)
-          for (int x = 0; x < HALVES; ++x)
-            tma_4d(base + (PAIR ? q : slot) * SM::Q_BYTES + x * (SM::Q_BYTES / HALVES), &A.mq, fb,
-                   x * 64, 0, s.h,
-                   tok + (s.mt * (PAIR ? 2 : 1) + q) * A.tpt);
-      }
+    if (PR || A.kind == RING) {
+      if (elect_one()) copies(Yes<true>());
       __syncwarp();
-      ++segs;
-      constexpr int LAG = PAIR ? 0 : 1;
-      for (int i = 0; ok && i < s.n + LAG; ++i) {
-        if (i < s.n) ok = tile(s, i, false);
-        if (ok && i >= LAG) ok = tile(s, i - LAG, true);
-      }
-    }
-    if (*abort) {  // the copies in flight land before the CTA ends
-      const unsigned long long t0 = globaltimer();
-      for (uint32_t u = idx > STAGES ? idx - STAGES : 0; u < idx; ++u)
-        while (!mbar_try(bar(&C.full[u % STAGES]), (u / STAGES) & 1) &&
-               globaltimer() - t0 < WAIT_LIMIT_NS) {
-        }
-      for (int u = max(0, segs - (PAIR ? 1 : 2)); u < segs; ++u)
-        while (!mbar_try(bar(&C.q_full[PAIR ? 0 : u & 1]), (PAIR ? u : u >> 1) & 1) &&
-               globaltimer() - t0 < WAIT_LIMIT_NS) {
-        }
+    } else {
+      copies(Yes<false>());
     }
   } else if (warp == MMA_WARP) {
     // ------------------------------------------------------------ products
