@@ -45,7 +45,7 @@ constexpr int MAX_GROUP = 128;  // query heads per KV head
 constexpr int MAX_D = 128;
 constexpr int MAX_KEYS = 0x7fffffff - 1023;  // cache entries: a tile more fits an int
 
-constexpr int ITEM_COST = 2;    // an item's fixed cost in tiles (0 to 3 measured: within 2 %)
+constexpr int ITEM_COST = 2;    // an item's fixed cost in tiles (1 to 3: within 2 %)
 constexpr int TILE = 128;       // query rows of a tile, and keys of a tile
 constexpr int THREADS = 384;    // two softmax warpgroups, and one with a copy and a product warp
 // Registers: launched with 168 a thread (64512 a CTA); the softmax warpgroups
@@ -552,6 +552,7 @@ __device__ __forceinline__ uint32_t span(int a, int b, int k0) {
 //     are columns: every thread has work however few the rows are, and the
 //     products cost less.  (1024 requests of 12 rows per item: 444 us with a row
 //     per lane, 260 so, when both were first built.)
+constexpr int CTRL_BYTES = 3 * 1024;  // what 227 KB leave beside seven tiles of 32 KB
 template <int DP, int NQ>
 struct Smem {
   static constexpr int BYTES = TILE * DP * 2;                    // a tile of keys or values
@@ -562,7 +563,7 @@ struct Smem {
   static constexpr int FIT = (229376 - STAGE_AT) / BYTES;
   static constexpr int STAGES = FIT < 12 ? FIT : 12;
   static constexpr int CTRL = STAGE_AT + STAGES * BYTES;         // offset of the control part
-  static constexpr int TOTAL = CTRL + 3072;
+  static constexpr int TOTAL = CTRL + CTRL_BYTES;
 };
 template <bool V>
 struct Yes { static constexpr bool value = V; };
@@ -600,9 +601,9 @@ struct Ctrl {
     long long scan[12];
   };
 };
-static_assert(sizeof(Ctrl<0, true>) <= 3072 && sizeof(Ctrl<0, false>) <= 3072 &&
-                  sizeof(Ctrl<16, false>) <= 3072 && sizeof(Ctrl<32, false>) <= 3072 &&
-                  sizeof(Ctrl<64, false>) <= 3072,
+static_assert(sizeof(Ctrl<0, true>) <= CTRL_BYTES && sizeof(Ctrl<0, false>) <= CTRL_BYTES &&
+                  sizeof(Ctrl<16, false>) <= CTRL_BYTES && sizeof(Ctrl<32, false>) <= CTRL_BYTES &&
+                  sizeof(Ctrl<64, false>) <= CTRL_BYTES,
               "control part");
 
 // desc[cta]: x = flags, y = item (of its request) and z = request of the first segment
