@@ -15,12 +15,12 @@
 // its 64 KB (1.5 us of an SM's share).  Hence two streams of key tiles per SM, so
 // that one's products run under the other's softmax, copies five to twelve stages
 // ahead, and runs of equal length whatever the requests' lengths.  64 requests of
-// 22 nodes over 2000 to 9000 tokens (1.39 GB): 240 us, 5.8 TB/s, 0.85 of the
+// 22 nodes over 2000 to 9000 tokens (1.39 GB): 231 us, 6.0 TB/s, 0.89 of the
 // measured copy bandwidth.  Prompts: 4 D flops per pair of tokens and query head;
-// the tensor cores are busy 0.55 of the time, and the softmax of the two tiles of
-// queries that share an SM (two warps per quarter, in turn with the products that
-// wait for their weights) is what the rest waits for.  8192 tokens under a window
-// of 4096, 32 heads of 128: 335 us, 1.23 PFLOP/s, 0.64 of the measured bf16 rate.
+// the tensor cores are busy 0.6 of the time, and each of the two tiles of queries
+// that share an SM is a chain: scores, softmax, the weights' product, the next
+// scores (which take the weights' place).  8192 tokens under a window of 4096, 32
+// heads of 128: 319 us, 1.29 PFLOP/s, 0.67 of the measured bf16 rate.
 #ifndef SV_ATTENTION_CUH
 #define SV_ATTENTION_CUH
 

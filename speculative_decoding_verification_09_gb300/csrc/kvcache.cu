@@ -247,7 +247,32 @@ __global__ void __launch_bounds__(KV_THREADS) sv_page_copy(const PageParams K) {
   const int first = int(blockIdx.z) * PC_ENTRIES;
   const bool writer = blockIdx.x == 0 && blockIdx.z == 0;
   if (!writer && first > k) return;
-  const int bad = k < 0 ? 0 : page_commit_faults(K, b, k, len);
+  // One pass holds every entry of a short path: then the thread of an entry checks
+  // what it needs anyway, its node read beside the count and the length.  (One
+  // path of 32 rows: 11.4 us with a check of its own, 9.4 so, launch included; 64
+  // paths of 384 rows: 21.7 and 20.6.)
+  const bool short_path = K.N <= PC_ENTRIES;
+  int bad = 0;
+  if (short_path) {
+    const int j = int(threadIdx.x);
+    const int node = K.nodes && j > 0 && j < K.N ? __ldg(K.nodes + size_t(b) * K.N + j - 1) : j;
+    if (k >= K.N || len < 0 || len + k + 1 > (long long)K.cols * K.page ||
+        len + k + 1 > 0x7fffffffLL) {
+      bad = k < 0 ? 0 : SV_ST_BAD_LENGTH;
+    } else if (j <= k) {
+      const unsigned at = unsigned(len) + unsigned(j), col = at / unsigned(K.page);
+      const int pg = __ldg(K.table + size_t(b) * K.cols + col);
+      if (node < 0 || node >= K.N) bad |= SV_ST_BAD_TOKEN;
+      if (pg < 0 || pg >= K.num_pages) bad |= SV_ST_BAD_PAGE;
+      dst_of[j] = size_t(pg) * K.LH * K.page + (at - col * unsigned(K.page));
+      src_of[j] = node;
+    }
+    const int tok = __syncthreads_or(bad & SV_ST_BAD_TOKEN);
+    const int pg = __syncthreads_or(bad & SV_ST_BAD_PAGE);
+    bad = (bad & SV_ST_BAD_LENGTH) | (tok ? SV_ST_BAD_TOKEN : 0) | (pg ? SV_ST_BAD_PAGE : 0);
+  } else if (k >= 0) {
+    bad = page_commit_faults(K, b, k, len);
+  }
   if (writer && threadIdx.x == 0 && !IN_PLACE) {
     K.out_seq_lens[b] = int32_t(k < 0 || bad ? len : len + k + 1);
     set_status(K.status, bad);
@@ -256,7 +281,7 @@ __global__ void __launch_bounds__(KV_THREADS) sv_page_copy(const PageParams K) {
   const int r0 = int(blockIdx.x) * PC_ROWS, rows = min(PC_ROWS, K.LH - r0);
   for (int j0 = first; j0 <= k; j0 += int(gridDim.z) * PC_ENTRIES) {
     const int cnt = min(PC_ENTRIES, k + 1 - j0);
-    if (int(threadIdx.x) < cnt) {
+    if (!short_path && int(threadIdx.x) < cnt) {
       const int j = j0 + int(threadIdx.x);
       const long long at = len + j;
       const int pg = __ldg(K.table + size_t(b) * K.cols + at / K.page);
