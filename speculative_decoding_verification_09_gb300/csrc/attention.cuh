@@ -607,8 +607,8 @@ static_assert(sizeof(Ctrl<0, true>) <= CTRL_BYTES && sizeof(Ctrl<0, false>) <= C
               "control part");
 
 // desc[cta]: x = flags, y = item (of its request) and z = request of the first segment
-constexpr int DESC_IN = 1 << 30;       // the first segment starts inside its item
-constexpr int DESC_THROUGH = 1 << 29;  // and runs to the CTA's end without finishing it
+constexpr int DESC_THROUGH = 1 << 29;  // the first segment starts inside its item and runs to
+                                       // the CTA's end without finishing it
 constexpr int DESC_OUT = 1 << 28;      // the last segment leaves its item unfinished
 constexpr int DESC_LAST1 = 1 << 27;    // the last segment's partials are in slot 1
 
@@ -1443,7 +1443,6 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       if (segs == 0) {
         d_item = s.h * A.MT + s.mt;
         d_b = s.b;
-        if (s.j0 > 0) d_flags |= DESC_IN;
         if (s.j0 > 0 && s.j0 + n < s.nt) d_flags |= DESC_THROUGH;
       } else {
         d_flags |= DESC_LAST1;
