@@ -128,11 +128,17 @@ def test_tree_dead_places(dead, dtype):
     tree_check(tree_inputs(6, 2, 40, 8, 1, 128, 128, [100, 700], dtype, dead=dead, LH=2))
 
 
-def test_tree_chain_without_parent():
-    c = tree_inputs(8, 3, 6, 8, 4, 128, 16, [100, 0, 513], BF, "chain")
+@pytest.mark.parametrize("N,D", [(6, 128), (30, 64), (50, 128), (140, 64), (256, 128)])
+def test_tree_chain_without_parent(N, D):
+    c = tree_inputs(8, 3, N, 8, 4, D, 16, [100, 0, 513], BF, "chain")
     a = tree_check(c)
     b, _ = tree_call(c, parent=False)
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("page", [8, 40, 192, 1024, 65536])
+def test_tree_page_sizes(page):
+    tree_check(tree_inputs(17, 2, 4, 4, 2, 64, page, [1500, 77], BF))
 
 
 def test_tree_scales():
@@ -431,6 +437,58 @@ def test_prompt_other_sequences_hold_anything():
     assert (out[577:] == 7.0).all()
 
 
+def test_ring_and_prompt_scales():
+    r, p = ring_inputs(18, 3, 5, 8, 2, 64, 4, 90, [20, 94, 400], BF), prompt_inputs(19, [150, 40], 8, 2, 64, 4, 90, BF)
+    for scale in (1e-3, 0.7):
+        out, _ = ring_call(r, scale=scale)
+        for b in range(3):
+            q = dict(r, q=r["q"])
+            pp, S, W, H = q["pos"][b], 4, 90, 2
+            held = au.ring_positions(pp, S, W)
+            slots = torch.tensor([au.slot(t, S, W) for t in held], dtype=torch.long, device=DEV)
+            k, v = (torch.cat([x[b][:, slots].transpose(0, 1), y[b].transpose(0, 1)])
+                    for x, y in ((r["kp"], r["kn"]), (r["vp"], r["vn"])))
+            at = [pp + j for j in range(5)]
+            au.check(out[b], *au.attend(r["q"][b], k, v, au.window_visible(at, held + at, S, W).to(DEV), scale, BF))
+        out, _ = prompt_call(p, scale=scale)
+        for a, e in ((0, 150), (150, 190)):
+            at = range(e - a)
+            au.check(out[a:e], *au.attend(p["q"][a:e], p["k"][a:e], p["v"][a:e],
+                                          au.window_visible(at, at, 4, 90).to(DEV), scale, BF))
+
+
+def test_prompt_far_rows():
+    """More than 2^31 query elements: the last tokens of a long prompt, and of the sequence before it."""
+    T0, T, Hq, D, S, W = 500, 140000, 128, 128, 3, 40
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(3)
+    q = torch.empty(T0 + T, Hq, D, dtype=BF, device=DEV).normal_(generator=gen)
+    assert q.numel() > 1 << 31
+    k, v = (torch.empty(T0 + T, 1, D, dtype=BF, device=DEV).normal_(generator=gen) for _ in "kv")
+    out, st = torch.empty_like(q), status()
+    binding.sv_prompt_attn(q, k, v, i32([0, T0, T0 + T]), S, W, out, dev_status=st)
+    assert int(st.item()) == 0
+    for a, e in ((0, T0), (T0, T0 + T)):
+        n = e - a
+        at = [n - 3, n - 2, n - 1]
+        seen = sorted(set(range(S)) | set(range(n - 3 - W, n)))
+        rows = torch.tensor(seen, device=DEV) + a
+        au.check(out[e - 3:e], *au.attend(q[e - 3:e], k[rows], v[rows], au.window_visible(at, seen, S, W).to(DEV),
+                                          D ** -0.5, BF))
+
+
+def test_empty_batches_and_strides():
+    c = tree_inputs(20, 2, 3, 4, 2, 64, 16, [40, 50], BF)
+    e = dict(c, B=0, q=c["q"][:0], kn=c["kn"][:0], vn=c["vn"][:0], table=c["table"][:0], lens=[], parent=c["parent"][:0])
+    assert tree_call(e)[0].numel() == 0
+    p = prompt_inputs(21, [0], 4, 2, 64, 0, 8, BF)
+    assert prompt_call(p)[0].numel() == 0 and prompt_call(dict(p, cu=np.zeros(1, np.int32)))[0].numel() == 0
+    with pytest.raises(binding.SpecVerifyError):
+        tree_call(dict(c, kp=c["kp"].transpose(1, 2).contiguous().transpose(1, 2)))
+    with pytest.raises(binding.SpecVerifyError):
+        tree_call(c, ws=torch.empty(64, dtype=torch.uint8, device=DEV))
+
+
 def test_prompt_invalid_bounds():
     """A sequence whose bounds decrease or leave the rows is skipped, the others are not."""
     c = prompt_inputs(7, [50, 60, 70], 4, 2, 64, 4, 30, BF)
@@ -578,6 +636,32 @@ def test_page_commit_invalid_requests(in_place):
         left[7][1] = -1
         wk, wv, wout = commit_plain(*left)
         assert np.array_equal(k, wk) and np.array_equal(v, wv) and np.array_equal(out, wout), what
+
+
+def test_copies_far_rows():
+    """Pools of more than 2^31 elements: a commit and a fill behind it."""
+    P, LH, page, D = 9000, 16, 128, 128
+    kp, vp = (torch.zeros(P, LH, page, D, dtype=BF, device=DEV) for _ in "kv")
+    assert kp.numel() > 1 << 31
+    kn, vn = (torch.randn(1, LH, 3, D, device=DEV).to(BF) for _ in "kv")
+    lens = i32([126])
+    binding.sv_page_commit(kp, vp, kn, vn, i32([[P - 1, P - 2]]), lens, None, i32([2]), lens)
+    assert lens.tolist() == [129]
+    for pool, new in ((kp, kn), (vp, vn)):
+        assert torch.equal(pool[P - 1, :, 126:], new[0, :, :2]) and torch.equal(pool[P - 2, :, 0], new[0, :, 2])
+        assert torch.count_nonzero(pool) == torch.count_nonzero(new)
+    kp, vp = kp.view(P, LH, page, D), vp.view(P, LH, page, D)  # as rings of 126 behind 2 sinks
+    kp.zero_(), vp.zero_()
+    k, v = (torch.randn(200, 2, D, device=DEV).to(BF) for _ in "kv")
+    cu = torch.zeros(P + 1, dtype=torch.int32, device=DEV)
+    cu[P] = 200  # the last sequence holds all
+    pos = torch.empty(P, dtype=torch.int32, device=DEV)
+    binding.sv_kv_fill(k, v, cu, kp, vp, pos, 2, 126, head0=14)
+    assert pos[P - 1] == 200 and torch.count_nonzero(pos) == 1
+    for pool, new in ((kp, k), (vp, v)):
+        for t in (0, 1, 74, 100, 199):
+            assert torch.equal(pool[P - 1, 14:, au.slot(t, 2, 126)], new[t])
+        assert torch.count_nonzero(pool[:P - 1]) == 0 and torch.count_nonzero(pool[P - 1, :14]) == 0
 
 
 def test_tree_steps():
