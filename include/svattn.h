@@ -112,8 +112,9 @@ int sv_ring_attn(int dtype, const void* q, const void* k_pool, const void* v_poo
  *              cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (none: an empty sequence)
  * Rows of `out` in no sequence are left as they were.  A sequence whose
  * bounds are not 0 <= cu_seqlens[b] <= cu_seqlens[b + 1] <= T is skipped
- * (SV_ST_BAD_LENGTH).  Requires T <= 2^31 - 512, sink >= 0, window >= 1,
- * B <= 65535.  No workspace.
+ * (SV_ST_BAD_LENGTH); where such bounds give rows to two sequences, those rows
+ * and the ones of later sequences are not defined.
+ * Requires T <= 2^31 - 512, sink >= 0, window >= 1, B <= 65535.  No workspace.
  */
 int sv_prompt_attn(int dtype, const void* q, const void* k, const void* v,
                    const int32_t* cu_seqlens, float scale, int B, int T, int Hq, int Hkv, int D,

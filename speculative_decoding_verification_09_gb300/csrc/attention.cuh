@@ -1094,7 +1094,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
             if (done == 0) {
               m = mt;
             } else {
-              const bool rise = active && (mt - m) * A.c > RAISE_LOG2;  // (-inf before: inf > 8)
+              const bool rise = active && (mt - m) * A.c > RAISE_LOG2;  // (-inf before: always)
               if (__any_sync(0xffffffffu, rise)) {
                 const float f = rise ? ex2((m - mt) * A.c) : 1.0f;
                 if (rise) m = mt;
