@@ -50,7 +50,6 @@ Layout layout_of(int N, int G) {
   const int rows = N * G;
   if (rows <= 16) return {16, 16};
   if (rows <= 32) return {32, 32};
-  if (rows <= 64) return {64, 64};
   return {0, N <= TILE / G ? TILE : 2 * TILE};
 }
 

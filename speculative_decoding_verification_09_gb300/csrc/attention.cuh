@@ -546,12 +546,14 @@ __device__ __forceinline__ uint32_t span(int a, int b, int k0) {
 // a KV head) that share its keys:
 //   NQ == 0, PAIR: more than 128 rows.  Two tiles of 128 rows; S = Q K^T has a
 //     row per TMEM lane, every key tile serves both.
-//   NQ == 0, !PAIR: 65 to 128 rows.  One such tile, in two streams.
+//   NQ == 0, !PAIR: 33 to 128 rows.  One such tile, in two streams.
 //   NQ > 0: at most NQ rows.  The products are turned over, S^T = K Q^T and
 //     O^T = V^T P^T, so that the lanes hold keys (dimensions) and the few rows
 //     are columns: every thread has work however few the rows are, and the
 //     products cost less.  (1024 requests of 12 rows per item: 444 us with a row
-//     per lane, 260 so, when both were first built.)
+//     per lane, 260 so, when both were first built.  Later: 64 requests of 5000, 24 rows
+//     of 128 dimensions, 207 us so and 215 with a row per lane, 32 rows 210 and 217;
+//     but 64 rows, for which a warp agrees on 64 maxima, 258 and 218.)
 constexpr int CTRL_BYTES = 3 * 1024;  // what 227 KB leave beside seven tiles of 32 KB
 template <int DP, int NQ>
 struct Smem {
@@ -579,10 +581,10 @@ struct Exchange {              // NQ == 0: softmax state exchanged between the s
 };
 template <int NQ>
 struct Few {                   // NQ > 0, per stream and column
-  unsigned long long sees[2][NQ];  // columns that see a staged entry
+  uint32_t sees[2][NQ];            // columns that see a staged entry
   alignas(16) float nmc[2][NQ];    // minus the running maximum, in base-2 units; -inf: none yet
   alignas(16) float fac[2][NQ];    // rescaling, and at the end the streams' shares
-  float sums[NQ <= 32 ? 8 : 1][NQ];  // per warp, at the end (NQ == 64: in P's room)
+  float sums[8][NQ];               // per warp, at the end
 };
 template <int NQ, bool PAIR>
 struct Ctrl {
@@ -602,8 +604,7 @@ struct Ctrl {
   };
 };
 static_assert(sizeof(Ctrl<0, true>) <= CTRL_BYTES && sizeof(Ctrl<0, false>) <= CTRL_BYTES &&
-                  sizeof(Ctrl<16, false>) <= CTRL_BYTES && sizeof(Ctrl<32, false>) <= CTRL_BYTES &&
-                  sizeof(Ctrl<64, false>) <= CTRL_BYTES,
+                  sizeof(Ctrl<16, false>) <= CTRL_BYTES && sizeof(Ctrl<32, false>) <= CTRL_BYTES,
               "control part");
 
 // desc[cta]: x = flags, y = item (of its request) and z = request of the first segment
@@ -642,23 +643,19 @@ __device__ __forceinline__ void swap_pieces(uint4& a, uint4& b, int x, int lane)
 }
 
 // Sums of the columns over a warp's 32 lanes: lane i gets column i's (i mod 16's
-// with 16 columns) in v[0], and column 32 + i's in v[32] with 64.
+// with 16 columns) in v[0].
 template <int NQ>
 __device__ __forceinline__ void sum_columns(float* v, int lane) {
-  constexpr int SPAN = NQ < 32 ? NQ : 32;
 #pragma unroll
-  for (int c = 0; c < NQ; c += SPAN) {
+  for (int x = NQ / 2; x; x >>= 1) {
+    const bool up = lane & x;
 #pragma unroll
-    for (int x = SPAN / 2; x; x >>= 1) {
-      const bool up = lane & x;
-#pragma unroll
-      for (int i = 0; i < x; ++i) {
-        const float give = up ? v[c + i] : v[c + i + x], keep = up ? v[c + i + x] : v[c + i];
-        v[c + i] = keep + __shfl_xor_sync(0xffffffffu, give, x);
-      }
+    for (int i = 0; i < x; ++i) {
+      const float give = up ? v[i] : v[i + x], keep = up ? v[i + x] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, x);
     }
-    if (SPAN == 16) v[c] += __shfl_xor_sync(0xffffffffu, v[c], 16);
   }
+  if (NQ == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 
 // One tile's softmax with keys on the lanes: thread `key` takes its key's
@@ -669,24 +666,20 @@ __device__ __forceinline__ void sum_columns(float* v, int lane) {
 // and O (columns from to) rescaled, when a score exceeds it by 2^RAISE_LOG2.
 template <int NQ, bool BF>
 __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>& C, int st,
-                                            int key, uint32_t ts, uint32_t to, unsigned long long sees,
+                                            int key, uint32_t ts, uint32_t to, uint32_t sees,
                                             bool masked, bool started, bool& unset, float* lq,
                                             unsigned char* pbuf) {
-  constexpr int W = NQ < 32 ? NQ : 32;
   const int lane = key & 31, warp = key >> 5;
   float* const nmc = C.x.nmc[st];
   const float2 c2 = make_float2(A.c, A.c);
-  uint32_t r[NQ / W][W];
-  auto score = [&](int q) -> uint32_t& { return r[q / W][q % W]; };
+  uint32_t r[NQ];
   auto load = [&] {
-#pragma unroll
-    for (int x = 0; x < NQ / W; ++x) tm_ldn<W>(ts + x * W, r[x]);
-    tm_waitn<W>(r[0]);
-    if (NQ > W) tm_loadedn<W>(r[NQ / W - 1]);
+    tm_ldn<NQ>(ts, r);
+    tm_waitn<NQ>(r);
     if (masked) {
 #pragma unroll
       for (int q = 0; q < NQ; ++q)
-        if (!(sees >> q & 1)) score(q) = 0xff800000u;
+        if (!(sees >> q & 1)) r[q] = 0xff800000u;
     }
   };
   // the weights' exponents in place of the scores, and the largest
@@ -695,15 +688,15 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
 #pragma unroll
     for (int q = 0; q < NQ; q += 4) {
       const float4 n = *reinterpret_cast<const float4*>(nmc + q);
-      const float2 a = fma2(make_float2(__uint_as_float(score(q)), __uint_as_float(score(q + 1))),
+      const float2 a = fma2(make_float2(__uint_as_float(r[q]), __uint_as_float(r[q + 1])),
                             c2, make_float2(n.x, n.y));
       const float2 b =
-          fma2(make_float2(__uint_as_float(score(q + 2)), __uint_as_float(score(q + 3))), c2,
+          fma2(make_float2(__uint_as_float(r[q + 2]), __uint_as_float(r[q + 3])), c2,
                make_float2(n.z, n.w));
-      score(q) = __float_as_uint(a.x);
-      score(q + 1) = __float_as_uint(a.y);
-      score(q + 2) = __float_as_uint(b.x);
-      score(q + 3) = __float_as_uint(b.y);
+      r[q] = __float_as_uint(a.x);
+      r[q + 1] = __float_as_uint(a.y);
+      r[q + 2] = __float_as_uint(b.x);
+      r[q + 3] = __float_as_uint(b.y);
       over = fmaxf(over, fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y)));
     }
     return over;
@@ -722,8 +715,8 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
       float t;
       asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;"
                    : "=f"(t)
-                   : "f"(__uint_as_float(score(q))));
-      if (lane == (q & 31)) wmax[warp * NQ + q] = t;
+                   : "f"(__uint_as_float(r[q])));
+      if (lane == q) wmax[warp * NQ + q] = t;
     }
     group_sync(1 + st, TILE);
     int none = 0;
@@ -746,16 +739,13 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
     if (started) {
 #pragma unroll
       for (int q = 0; q < NQ; ++q) lq[q] *= C.x.fac[st][q];
+      uint32_t o[NQ];
+      tm_ldn<NQ>(to, o);
+      tm_waitn<NQ>(o);
 #pragma unroll
-      for (int x = 0; x < NQ / W; ++x) {
-        uint32_t o[W];
-        tm_ldn<W>(to + x * W, o);
-        tm_waitn<W>(o);
-#pragma unroll
-        for (int q = 0; q < W; ++q)
-          o[q] = __float_as_uint(__uint_as_float(o[q]) * C.x.fac[st][x * W + q]);
-        tm_stn<W>(to + x * W, o);
-      }
+      for (int q = 0; q < NQ; ++q)
+        o[q] = __float_as_uint(__uint_as_float(o[q]) * C.x.fac[st][q]);
+      tm_stn<NQ>(to, o);
       tm_wait_st();
     }
     exponents();
@@ -767,7 +757,7 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
 #pragma unroll
   for (int q = 0; q < NQ; q += 2) {
     const float2 p =
-        make_float2(ex2(__uint_as_float(score(q))), ex2(__uint_as_float(score(q + 1))));
+        make_float2(ex2(__uint_as_float(r[q])), ex2(__uint_as_float(r[q + 1])));
     const float2 l = add2(make_float2(lq[q], lq[q + 1]), p);
     lq[q] = l.x;
     lq[q + 1] = l.y;
@@ -956,7 +946,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           if constexpr (NQ > 0) {  // column `row` sees its token and those above it
             if (row < A.N * A.G)
               for (int i = row / A.G;; i = C.parent[st][i]) {
-                atomicOr(&C.x.sees[st][i], 1ull << row);
+                atomicOr(&C.x.sees[st][i], 1u << row);
                 if (i == 0) break;
               }
             group_sync(1 + st, TILE);
@@ -1034,7 +1024,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
         };
         if constexpr (NQ > 0) {
           // one key per thread, all rows
-          unsigned long long sees = ~0ull;
+          uint32_t sees = ~0u;
           if (masked) {
             const int k = k0 + row;
             if (!ky.staged) {
@@ -1043,12 +1033,12 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
               } else if (ring_at >= 0 && k >= A.sink) {
                 int v = k - A.sink - ring_at;  // tokens that still have the slot in their window
                 if (v < 0) v += A.window;
-                if (v < A.N) sees = (1ull << (v * A.G)) - 1;
+                if (v < A.N) sees = (1u << (v * A.G)) - 1;
               }
             } else if (k >= A.N) {
               sees = 0;
             } else {
-              sees = A.parent ? C.x.sees[st][k] : ~0ull << (k * A.G);
+              sees = A.parent ? C.x.sees[st][k] : ~0u << (k * A.G);
             }
           }
           softmax_few<NQ, BF>(A, C, st, row, ts, to, sees, masked, done > 0, unset, lq,
@@ -1297,27 +1287,14 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       };
       if constexpr (NQ > 0) {
         // sums over the keys: 32 lanes here, the four warps and two streams below
-        float* const sums = NQ <= 32 ? &C.x.sums[0][0] : reinterpret_cast<float*>(smem + SM::P_AT);
         sum_columns<NQ>(lq, lane);
-        auto o_done = [&] {
-          for (int x = 0; x < 2; ++x) {
-            if (x >= n) break;
-            ok = ok && warp_wait(bar(&C.o_full[x]), o_use[x] & 1, A.status, abort);
-            ++o_use[x];
-          }
-          tc_after();
-        };
-        if (NQ > 32) o_done();  // P is free
-        if (lane < NQ) {
-          sums[warp * NQ + lane] = lq[0];
-          if (NQ == 64) sums[warp * NQ + 32 + lane] = lq[NQ / 2];
-        }
+        if (lane < NQ) C.x.sums[warp][lane] = lq[0];
         group_sync(3, 2 * TILE);
         if (tid < NQ) {
           float l0 = 0.0f, l1 = 0.0f;
           for (int w = 0; w < 4; ++w) {
-            l0 += sums[w * NQ + tid];
-            l1 += sums[(4 + w) * NQ + tid];
+            l0 += C.x.sums[w][tid];
+            l1 += C.x.sums[4 + w][tid];
           }
           float a = -C.x.nmc[0][tid], b = n > 1 ? -C.x.nmc[1][tid] : INFINITY;
           if (a == INFINITY) a = -INFINITY;  // nothing seen
@@ -1335,7 +1312,12 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
             A.part_ml[(size_t(blockIdx.x) * 2 + slot) * NQ + tid] =
                 make_float2(mm, bad ? -1.0f : ll);
         }
-        if (NQ <= 32) o_done();
+        for (int x = 0; x < 2; ++x) {
+          if (x >= n) break;
+          ok = ok && warp_wait(bar(&C.o_full[x]), o_use[x] & 1, A.status, abort);
+          ++o_use[x];
+        }
+        tc_after();
         group_sync(3, 2 * TILE);
         __syncwarp();
         if (ok) {
@@ -1938,7 +1920,6 @@ int launch_dp(const AttnParams& A, Layout l, int device, int grid, int ctas, cud
                           : launch_as<DP, 0, true, true, BF>(A, device, grid, ctas, st);
   if (l.nq == 16) return launch_as<DP, 16, false, false, BF>(A, device, grid, ctas, st);
   if (l.nq == 32) return launch_as<DP, 32, false, false, BF>(A, device, grid, ctas, st);
-  if (l.nq == 64) return launch_as<DP, 64, false, false, BF>(A, device, grid, ctas, st);
   if (l.rows == TILE) return launch_as<DP, 0, false, false, BF>(A, device, grid, ctas, st);
   return launch_as<DP, 0, true, false, BF>(A, device, grid, ctas, st);
 }
