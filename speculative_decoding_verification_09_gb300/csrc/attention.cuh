@@ -602,6 +602,7 @@ struct Ctrl {
     typename Either<NQ, Few<NQ>, Exchange<PAIR>>::T x;
     long long scan[12];
   };
+  unsigned long long out_at[NQ ? NQ : 1];  // NQ > 0: elements from an item's output to a column's
 };
 static_assert(sizeof(Ctrl<0, true>) <= CTRL_BYTES && sizeof(Ctrl<0, false>) <= CTRL_BYTES &&
                   sizeof(Ctrl<16, false>) <= CTRL_BYTES && sizeof(Ctrl<32, false>) <= CTRL_BYTES,
@@ -826,7 +827,9 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (NQ) {  // columns past the item's rows: finite, and never used
+  if (NQ) {
+    if (tid < NQ) C.out_at[tid] = ((unsigned long long)(tid / A.G) * A.Hq + tid % A.G) * A.D;
+    // columns past the item's rows: finite, and never used
     for (int i = tid; i < SM::P_AT / 16; i += THREADS)
       reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1342,20 +1345,13 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
               for (int q = 0; q < HALF; ++q) to_part[q * DP] = __uint_as_float(o0[q]);
             }
           } else if (row < A.D) {
-            // column q is token q / G, head q mod G of the group
-            const int t = q0 / A.G, rows = A.N * A.G - q0;
-            int g = q0 - t * A.G;
-            uint16_t* o = A.out + ((size_t(s.b) * A.N + t) * A.Hq + s.h * A.G + g) * A.D + row;
-            const size_t wrap = size_t(A.Hq - A.G) * A.D;
+            // (column q is token q / G, head q mod G of the group)
+            const int rows = A.N * A.G - q0;
+            uint16_t* const o = A.out + (size_t(s.b) * A.N * A.Hq + size_t(s.h) * A.G) * A.D + row;
 #pragma unroll
-            for (int q = 0; q < HALF; ++q) {
-              if (q < rows) *o = bad ? 0 : uint16_t(pack16<BF>(__uint_as_float(o0[q]), 0.0f));
-              o += A.D;
-              if (++g == A.G) {
-                g = 0;
-                o += wrap;
-              }
-            }
+            for (int q = 0; q < HALF; ++q)
+              if (q < rows)
+                o[C.out_at[q0 + q]] = bad ? 0 : uint16_t(pack16<BF>(__uint_as_float(o0[q]), 0.0f));
           }
         }
         tc_before();
