@@ -117,15 +117,20 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
     lay = layout_of(A.N, A.G);
     const int tpi = lay.rows == 2 * TILE ? 2 * A.tpt : A.tpt;
     A.MT = (A.N + tpi - 1) / tpi;
-    // Items are not cut, and not joined, when they have at most two tiles (the two
-    // streams of a CTA take them at once), or few tiles and many items per CTA,
-    // whose sums are even without cuts.  (1024 requests over rings of 512, 27 items of
-    // 5 tiles per CTA: 146.5 us cut, 140.7 whole; one token over 500 cached, 16 items
-    // of 5 tiles in all: 14.3 us cut, 16.4 whole.)
+    // Items are not cut, and not joined, when they have few tiles: a cut item's partials
+    // and the join cost more than runs that differ by up to an item, the more so the
+    // more rows an item has; unless they are too few to keep the SMs' loads going.  (8 KV
+    // heads of 128, lengths up to 8 times apart, inputs from HBM, us cut and whole.
+    // 4 rows, 3 tiles: 16 items 12.9 and 11.4, 1280 49.1 and 45.8; 5 tiles: 16 items 13.4
+    // and 13.6 (pages of 16: 13.4 and 16.4), 80 16.5 and 14.4; 8 tiles: 80 17.1 and 16.8,
+    // 1280 69.5 and 71.5, but with 32 rows 83.2 and 79.2.  200 rows, 8 tiles: 16 items
+    // 20.8 and 22.8, 80 31.6 and 25.6; 12 tiles: 320 82.6 and 69.7, 1280 256 and 247.)
     const long long entries = A.kind == TREE ? (long long)A.cols * A.page
                                              : (long long)A.sink + A.window;
     const long long most = (entries + TILE - 1) / TILE + (A.N + TILE - 1) / TILE;
-    A.whole = most <= 2 || (most <= 8 && (long long)A.B * A.Hkv * A.MT >= 8LL * ctas);
+    const long long items = (long long)A.B * A.Hkv * A.MT;
+    A.whole = most <= 3 || (2 * items >= ctas &&
+                            most <= (lay.nq == 0 ? 12 : items >= 8LL * ctas ? 8 : 5));
     const size_t rows = lay.rows, dp = A.D > 64 ? 128 : 64;
     unsigned char* w = static_cast<unsigned char*>(workspace);
     A.part_o = reinterpret_cast<float*>(w);
