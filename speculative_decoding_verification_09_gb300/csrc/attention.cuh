@@ -15,7 +15,7 @@
 // its 64 KB (1.5 us of an SM's share).  Hence two streams of key tiles per SM, so
 // that one's products run under the other's softmax, copies five to twelve stages
 // ahead, and runs of equal length whatever the requests' lengths.  64 requests of
-// 22 nodes over 2000 to 9000 tokens (1.39 GB): 231 us, 6.0 TB/s, 0.89 of the
+// 22 nodes over 2000 to 9000 tokens (1.39 GB): 225 us, 6.2 TB/s, 0.91 of the
 // measured copy bandwidth.  Prompts: 4 D flops per pair of tokens and query head;
 // the tensor cores are busy 0.6 of the time, and each of the two tiles of queries
 // that share an SM is a chain: scores, softmax, the weights' product, the next
@@ -1092,7 +1092,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
                 const float f = rise ? ex2((m - mt) * A.c) : 1.0f;
                 if (rise) m = mt;
                 l *= f;
-#pragma unroll
+#pragma unroll 1
                 for (int x = 0; x < DP / 32; ++x) {
                   uint32_t o[32];
                   tm_ld32(to + x * 32, o);
@@ -1288,6 +1288,10 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
                 make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
       };
+      // (Loops that are not unrolled below, and where the maximum is raised: what runs once
+      // an item costs its instructions' fetches, which the caches' data push out of L2.
+      // 1280 items of 200 rows and 16 tiles: 291 us unrolled, 244 not; 64 trees of 88 rows
+      // over 2000 to 9000: 231 and 225.)
       if constexpr (NQ > 0) {
         // sums over the keys: 32 lanes here, the four warps and two streams below
         sum_columns<NQ>(lq, lane);
@@ -1361,7 +1365,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
         tc_after();
         if (ok && warp_active) {
           const float f = whole ? 1.0f / l : 1.0f;
-#pragma unroll
+#pragma unroll 1
           for (int x = 0; x < DP / 32; ++x) {
             uint32_t o[32];
             float v[32];
@@ -1396,7 +1400,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
             f1 /= ll;
           }
           const uint32_t t0 = tmem + lanes + O_AT;
-#pragma unroll
+#pragma unroll 1
           for (int x = 0; x < DP / 64; ++x) {
             const int col = st * (DP / 2) + x * 32;
             uint32_t o[32];
