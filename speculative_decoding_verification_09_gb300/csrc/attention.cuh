@@ -20,7 +20,7 @@
 // the tensor cores are busy 0.6 of the time, and each of the two tiles of queries
 // that share an SM is a chain: scores, softmax, the weights' product, the next
 // scores (which take the weights' place).  8192 tokens under a window of 4096, 32
-// heads of 128: 319 us, 1.29 PFLOP/s, 0.67 of the measured bf16 rate.
+// heads of 128: 318 us, 1.30 PFLOP/s, 0.67 of the measured bf16 rate.
 #ifndef SV_ATTENTION_CUH
 #define SV_ATTENTION_CUH
 
@@ -1154,19 +1154,13 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
               tm_st16(ts + x * 16, pw);
             };
             // the products with the first 64 keys' values start under the others' weights
-            if (w == TILE) {
-              chunk(0);
-              chunk(1);
-              half_done();
-              chunk(2);
-              chunk(3);
-            } else {
-              chunk(0);
-              if (w > 32) chunk(1);
-              half_done();
-              if (w > 64) chunk(2);
-              if (w > 96) chunk(3);
-            }
+            // (One copy for all widths, fewer instructions to fetch: a second one for whole
+            // tiles took 1280 items of 16 tiles from 222 us to 244, 8192 tokens to 318 as now.)
+            chunk(0);
+            if (w > 32) chunk(1);
+            half_done();
+            if (w > 64) chunk(2);
+            if (w > 96) chunk(3);
             sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
             l += sum[0].x + sum[0].y;
           } else {
