@@ -121,10 +121,10 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
     // and the join cost more than runs that differ by up to an item, the more so the
     // more rows an item has; unless they are too few to keep the SMs' loads going.  (8 KV
     // heads of 128, lengths up to 8 times apart, inputs from HBM, us cut and whole.
-    // 4 rows, 3 tiles: 16 items 12.9 and 11.4, 1280 49.1 and 45.8; 5 tiles: 16 items 13.4
-    // and 13.6 (pages of 16: 13.4 and 16.4), 80 16.5 and 14.4; 8 tiles: 80 17.1 and 16.8,
-    // 1280 69.5 and 71.5, but with 32 rows 83.2 and 79.2.  200 rows, 8 tiles: 16 items
-    // 20.8 and 22.8, 80 31.6 and 25.6; 12 tiles: 320 82.6 and 69.7, 1280 256 and 247.)
+    // 4 rows, 3 tiles: 16 items 12.5 and 10.9, 1280 49.0 and 45.6; 5 tiles: 16 items 13.1
+    // and 13.6 (pages of 16: 13.4 and 16.4), 80 15.9 and 14.5; 8 tiles: 80 16.8 and 16.8,
+    // 1280 69.0 and 71.8, but with 32 rows 83.2 and 78.8.  200 rows, 8 tiles: 16 items
+    // 19.4 and 20.9, 80 29.1 and 24.6; 12 tiles: 320 66.3 and 61.9, 1280 196 and 188.)
     const long long entries = A.kind == TREE ? (long long)A.cols * A.page
                                              : (long long)A.sink + A.window;
     const long long most = (entries + TILE - 1) / TILE + (A.N + TILE - 1) / TILE;

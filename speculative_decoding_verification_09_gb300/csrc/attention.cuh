@@ -1282,8 +1282,9 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
                 make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
       };
-      // (Loops that are not unrolled below, and where the maximum is raised: what runs once
-      // an item costs its instructions' fetches, which the caches' data push out of L2.
+      // (Loops that are not unrolled below, and where the maximum is raised: less code is
+      // faster where it runs once an item, most so among much data, which looks like the
+      // cost of fetching it, though that was not measured by itself.
       // 1280 items of 200 rows and 16 tiles: 291 us unrolled, 244 not; 64 trees of 88 rows
       // over 2000 to 9000: 231 and 225.)
       if constexpr (NQ > 0) {
