@@ -101,6 +101,13 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, unsigned count) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// The same by one lane of a warp, without a branch that would split it.
+__device__ __forceinline__ void mbar_arrive_if(uint32_t bar, bool on) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n"
+      " @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar), "r"(uint32_t(on))
+      : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_tx(uint32_t bar, unsigned bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
@@ -209,11 +216,21 @@ __device__ __forceinline__ void tc_before() {
 __device__ __forceinline__ void tc_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
+// Tensor-memory loads, stores and their waits are instructions of a whole, converged
+// warp.  What stands before them may go by lane (mask bits found along a tree path,
+// output stores, one lane's arrival at a barrier), and the language promises no
+// convergence after that: hence a warp sync in each of them, but for those (<false>) that
+// stand behind one with nothing that goes by lane in between: a pair's tile has eleven,
+// and 8192 tokens take 334 us with a sync in each, 319 with the two that it needs.
+template <bool SYNC = true>
 __device__ __forceinline__ void tm_wait_st() {
+  if (SYNC) __syncwarp();
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 // 32 columns of the warp's 32 lanes, one row per thread.
+template <bool SYNC = true>
 __device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t (&r)[32]) {
+  if (SYNC) __syncwarp();
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
@@ -233,13 +250,16 @@ __device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t (&r)[32]) {
       "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),             \
       "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),             \
       "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+template <bool SYNC = true>
 __device__ __forceinline__ void tm_wait_ld(uint32_t (&r)[32]) {
+  if (SYNC) __syncwarp();
   asm volatile("tcgen05.wait::ld.sync.aligned;" : TM_REGS(r)::"memory");
 }
 __device__ __forceinline__ void tm_loaded(uint32_t (&r)[32]) {  // after tm_wait_ld
   asm volatile("" : TM_REGS(r)::"memory");
 }
 __device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  __syncwarp();
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
       "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
@@ -252,12 +272,14 @@ __device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t (&r)[32]) 
       : "memory");
 }
 __device__ __forceinline__ void tm_ld8(uint32_t addr, uint32_t (&r)[8]) {
+  __syncwarp();
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
                       "=r"(r[6]), "=r"(r[7])
                : "r"(addr));
 }
 __device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t (&r)[16]) {
+  __syncwarp();
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -266,7 +288,9 @@ __device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t (&r)[16]) {
                       "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                : "r"(addr));
 }
+template <bool SYNC = true>
 __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  if (SYNC) __syncwarp();
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
       "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
@@ -293,6 +317,7 @@ __device__ __forceinline__ void tm_loadedn(uint32_t (&r)[N]) {
 }
 template <int N>
 __device__ __forceinline__ void tm_waitn(uint32_t (&r)[N]) {
+  __syncwarp();
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
   tm_loadedn<N>(r);
 }
@@ -821,6 +846,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   if (warp == MMA_WARP) {
+    __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(&C.tmem)),
                  "n"(TM_COLS)
@@ -895,8 +921,8 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
     if (lane == 0) mbar_arrive(bar(&C.seg_empty[i % AHEAD]));
   };
 
-  __syncwarp();  // (whole warps from here)
   if (warp < 8) {
+    __syncwarp();
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
     // ------------------------------------------------------------ softmax
     const int st = warp >> 2;             // the stream of this warpgroup
@@ -1020,10 +1046,10 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
         }
         auto half_done = [&] {  // PAIR: the weights of the tile's first 64 keys are stored
           if (!PAIR) return;
-          tm_wait_st();
+          tm_wait_st<false>();
           tc_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(&C.p_half[st]));
+          mbar_arrive_if(bar(&C.p_half[st]), lane == 0);
         };
         if constexpr (NQ > 0) {
           // one key per thread, all rows
@@ -1047,6 +1073,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           softmax_few<NQ, BF>(A, C, st, row, ts, to, sees, masked, done > 0, unset, lq,
                           smem + SM::P_AT + st * SM::P_BYTES);
         } else if (!warp_active) {
+          __syncwarp();
           half_done();
         } else {
           // the tile's keys that this row sees, 32 to a word
@@ -1106,10 +1133,11 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           };
           if constexpr (PAIR) {
             uint32_t r[4][32];
+            __syncwarp();
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-              if (x * 32 < w) tm_ld32(ts + x * 32, r[x]);
-            tm_wait_ld(r[0]);
+              if (x * 32 < w) tm_ld32<false>(ts + x * 32, r[x]);
+            tm_wait_ld<false>(r[0]);
             tm_loaded(r[1]);
             tm_loaded(r[2]);
             tm_loaded(r[3]);
@@ -1141,8 +1169,8 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
             const float mc = m == -INFINITY ? 0.0f : m * A.c;
             const float2 c2 = make_float2(A.c, A.c), mc2 = make_float2(-mc, -mc);
             float2 sum[4] = {};
+            uint32_t pw[16];
             auto chunk = [&](int x) {  // the weights of 32 keys
-              uint32_t pw[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 const float2 e = fma2(make_float2(__uint_as_float(r[x][2 * i]),
@@ -1151,16 +1179,26 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
                 sum[i & 3] = add2(sum[i & 3], p);
                 pw[i] = pack16<BF>(p.x, p.y);
               }
-              tm_st16(ts + x * 16, pw);
             };
             // the products with the first 64 keys' values start under the others' weights
             // (One copy for all widths, fewer instructions to fetch: a second one for whole
             // tiles took 1280 items of 16 tiles from 222 us to 244, 8192 tokens to 318 as now.)
+            __syncwarp();
             chunk(0);
-            if (w > 32) chunk(1);
+            tm_st16<false>(ts, pw);
+            if (w > 32) {
+              chunk(1);
+              tm_st16<false>(ts + 16, pw);
+            }
             half_done();
-            if (w > 64) chunk(2);
-            if (w > 96) chunk(3);
+            if (w > 64) {
+              chunk(2);
+              tm_st16<false>(ts + 32, pw);
+            }
+            if (w > 96) {
+              chunk(3);
+              tm_st16<false>(ts + 48, pw);
+            }
             sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
             l += sum[0].x + sum[0].y;
           } else {
@@ -1234,7 +1272,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
             sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
             l += sum[0].x + sum[0].y;
           }
-          tm_wait_st();
+          tm_wait_st<false>();
         }
         tc_before();
         __syncwarp();
@@ -1431,6 +1469,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
     }
     if (!PR && !A.whole && tid == 0) A.desc[blockIdx.x] = make_int4(d_flags, d_item, d_b, 0);
   } else {
+    __syncwarp();
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
   if (warp == PLAN_WARP) {
     // ------------------------------------------------------------ the plan
@@ -1748,10 +1787,12 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == MMA_WARP)
+  if (warp == MMA_WARP) {
+    __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "n"(TM_COLS)
                  : "memory");
+  }
 }
 
 // Join of the items that the CTAs' runs cut, from the parts' maxima, sums and
