@@ -512,8 +512,11 @@ struct Cursor<PAIR, true> {
     wb = 0;
     load_window(A, report);
   }
-  // Item i (never before an earlier one); false past the last.
+  // Item i; false past the last.  The search goes on from the item before, and anew when
+  // i lies before that one's sequences: in which order blocks are taken over is not
+  // promised.
   __device__ bool item(const AttnParams& A, long long i, Seg& s, bool report) {
+    if (i < cum) open(A, report);
     for (;;) {
       const long long total = __shfl_sync(0xffffffffu, incl, 31);
       if (i < cum + total) break;
@@ -1488,7 +1491,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       return more;
     };
     if constexpr (PR) {
-      const bool report = blockIdx.x == 0;
+      bool report = blockIdx.x == 0;  // bad bounds are reported by the CTA of item 0
       cur.open(A, report);
       long long i = blockIdx.x;
       int seg_count = 0;
@@ -1525,6 +1528,10 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
         __syncwarp();
         if (!got || !go) break;
         i = x;
+        if (i == 0) {
+          report = true;
+          cur.open(A, true);
+        }
       }
       if (report) cur.item(A, 0x7fffffffffffffffll, s, true);  // the other sequences' bounds
       plan(seg_count, false);
