@@ -37,6 +37,8 @@
  *   workspace: sv_attn_workspace_bytes() bytes, 256-byte aligned; its
  *   contents need no preparation and nothing is kept in it between calls.
  *   Calls that may overlap on the GPU need separate workspaces.
+ *   SV_ST_TIMEOUT in *dev_status: an internal wait gave up, and the contents
+ *   of `out` are void.
  */
 #ifndef SVATTN_H
 #define SVATTN_H
@@ -119,6 +121,14 @@ int sv_ring_attn(int dtype, const void* q, const void* k_pool, const void* v_poo
 int sv_prompt_attn(int dtype, const void* q, const void* k, const void* v,
                    const int32_t* cu_seqlens, float scale, int B, int T, int Hq, int Hkv, int D,
                    int sink, int window, void* out, int32_t* dev_status, void* stream);
+
+/*
+ * Failure-handling test aid, as sv_test_withhold_slot: while enabled, block 0 of
+ * the next attention calls leaves out one of its copies, so that the waits for it
+ * run out after their one-second limit (SV_ST_TIMEOUT).  No fault, trap or endless
+ * wait is involved.  Not thread-safe.  Returns SV_OK.
+ */
+int sv_attn_test_withhold(int enable);
 
 #ifdef __cplusplus
 }

@@ -31,7 +31,8 @@ EXPORTED = ("sv_workspace_bytes", "sv_workspace_init", "spec_verify", "spec_veri
             "sv_kv_commit", "sv_kv_fill", "sv_page_commit", "sv_kv_valid_slots",
             "sv_window_cols", "sv_window_block_table", "sv_window_seq_lens_host", "sv_tree_verify", "sv_tree_set_cluster",
             "sv_tree_set_warps")
-EXPORTED_ATTN = ("sv_attn_workspace_bytes", "sv_tree_attn", "sv_ring_attn", "sv_prompt_attn")
+EXPORTED_ATTN = ("sv_attn_workspace_bytes", "sv_tree_attn", "sv_ring_attn", "sv_prompt_attn",
+                 "sv_attn_test_withhold")
 SV_TREE_MAX_N = 256
 SV_NOALLOC_MAX_WORKSPACE = 16 << 20
 
@@ -77,6 +78,7 @@ def lib() -> ctypes.CDLL:
         L.sv_ring_attn.argtypes = [I, P, P, P, P, P, P, F, I, I, I, I, I, I, I, I, I, P, P, Z, P,
                                    P]
         L.sv_prompt_attn.argtypes = [I, P, P, P, P, F, I, I, I, I, I, I, I, P, P, P]
+        L.sv_attn_test_withhold.argtypes = [I]
         L.sv_tree_set_cluster.argtypes = [I]
         L.sv_tree_set_warps.argtypes = [I]
         L.sv_set_tuning.argtypes = [I]
@@ -92,7 +94,7 @@ def lib() -> ctypes.CDLL:
                      "sv_test_withhold_slot",
                      "sv_kv_commit", "sv_kv_valid_slots", "sv_window_cols",
                      "sv_kv_fill", "sv_page_commit", "sv_tree_attn", "sv_ring_attn",
-                     "sv_prompt_attn",
+                     "sv_prompt_attn", "sv_attn_test_withhold",
                      "sv_window_block_table", "sv_window_seq_lens_host", "sv_tree_verify",
                      "sv_tree_set_cluster", "sv_tree_set_warps"):
             getattr(L, name).restype = I
@@ -493,6 +495,12 @@ def make_attn_workspace(B: int, N: int, Hq: int, Hkv: int, D: int, device) -> to
     if n == 0:
         raise SpecVerifyError("sizes the attention calls refuse")
     return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def sv_attn_test_withhold(enable: bool) -> None:
+    """Failure-handling test aid: block 0 of the next attention calls leaves
+    one of its copies out, so its bounded waits run out (SV_ST_TIMEOUT)."""
+    _check(lib().sv_attn_test_withhold(1 if enable else 0))
 
 
 def _workspace(t: torch.Tensor, device) -> tuple[int, int]:

@@ -10,6 +10,8 @@ using namespace svattn;
 
 constexpr float LOG2E = 1.44269504088896341f;
 
+int g_withhold = 0;  // failure-handling test (sv_attn_test_withhold)
+
 // -------------------------------------------------------------- host side
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -68,6 +70,7 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
   const int ctas = sms < MAX_CTAS ? sms : MAX_CTAS;
   A.G = A.Hq / A.Hkv;
   A.tpt = TILE / A.G;
+  A.withhold = g_withhold;
   const uint64_t D = A.D, tokens = A.kind == PROMPT ? uint64_t(A.T) : uint64_t(A.B) * A.N;
   const uint32_t q_tok = uint32_t(
       A.tpt < (A.kind == PROMPT ? A.T : A.N) ? A.tpt : (A.kind == PROMPT ? A.T : A.N));
@@ -167,6 +170,11 @@ bool bad_heads(int Hq, int Hkv, int D) {
 }  // namespace
 
 extern "C" {
+
+int sv_attn_test_withhold(int enable) {
+  g_withhold = enable ? 1 : 0;
+  return SV_OK;
+}
 
 size_t sv_attn_workspace_bytes(int N, int Hq, int Hkv, int D) {
   if (N < 1 || N > MAX_N || bad_heads(Hq, Hkv, D)) return 0;
