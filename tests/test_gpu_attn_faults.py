@@ -54,3 +54,30 @@ def test_bounded_waits_report_timeout_and_context_recovers():
         for _ in range(2):
             again, st = call(c)
             assert int(st.item()) == 0 and torch.equal(again, want), name
+
+
+def test_a_long_item_before_others_is_no_timeout():
+    """An item that takes longer than a wait may: the CTA's plan waits for it to end before it plans the fifth after it.
+    No queries, so every weight is 1, and ones in one value row of the page that all tables name: the output is exact."""
+    page, groups, cols = 65536, 152, 9216
+    lens = []
+    for _ in range(groups):
+        lens += [cols * page, 8, 8, 8, 8, 8]
+    B = len(lens)
+    dev = ta.DEV
+    q = torch.zeros(B, 1, 1, 8, dtype=BF, device=dev)
+    kp, vp = torch.randn(1, 1, page, 8, device=dev).to(BF), torch.zeros(1, 1, page, 8, dtype=BF, device=dev)
+    vp[0, 0, 5] = 1.0
+    kn, vn = torch.randn(B, 1, 1, 8, device=dev).to(BF), torch.zeros(B, 1, 1, 8, dtype=BF, device=dev)
+    table, out, st = torch.zeros(B, cols, dtype=torch.int32, device=dev), torch.empty_like(q), ta.status()
+    ws = binding.make_attn_workspace(B, 1, 1, 1, 8, dev)
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in "be")
+    begin.record()
+    binding.sv_tree_attn(q, kp, vp, table, ta.i32(lens), kn, vn, None, out, ws, dev_status=st)
+    end.record()
+    torch.cuda.synchronize()
+    assert begin.elapsed_time(end) > 1200.0  # the long item alone outlasts the limit
+    assert int(st.item()) == 0
+    n = torch.tensor(lens, device=dev, dtype=torch.float64)
+    seen = torch.where(n == 8, 1.0, n / page)
+    assert torch.equal(out[:, 0, 0], (seen / (n + 1)).to(BF)[:, None].expand(B, 8))
