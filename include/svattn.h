@@ -123,9 +123,9 @@ int sv_prompt_attn(int dtype, const void* q, const void* k, const void* v,
                    int sink, int window, void* out, int32_t* dev_status, void* stream);
 
 /*
- * Failure-handling test aid, as sv_test_withhold_slot: while enabled, block 0 of
- * the next attention calls leaves out one of its copies, so that the waits for it
- * run out after their one-second limit (SV_ST_TIMEOUT).  No fault, trap or endless
+ * Failure-handling test aid, as sv_test_withhold_slot: while enabled, one of
+ * the slots of block 0 of the next attention calls never counts as filled, so that
+ * the waits for it run out after their one-second limit (SV_ST_TIMEOUT).  No fault, trap or endless
  * wait is involved.  Not thread-safe.  Returns SV_OK.
  */
 int sv_attn_test_withhold(int enable);

@@ -498,8 +498,8 @@ def make_attn_workspace(B: int, N: int, Hq: int, Hkv: int, D: int, device) -> to
 
 
 def sv_attn_test_withhold(enable: bool) -> None:
-    """Failure-handling test aid: block 0 of the next attention calls leaves
-    one of its copies out, so its bounded waits run out (SV_ST_TIMEOUT)."""
+    """Failure-handling test aid: one slot of block 0 of the next attention
+    calls never counts as filled, so its bounded waits run out (SV_ST_TIMEOUT)."""
     _check(lib().sv_attn_test_withhold(1 if enable else 0))
 
 

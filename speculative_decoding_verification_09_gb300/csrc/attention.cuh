@@ -82,7 +82,7 @@ struct AttnParams {
   int q_rows;             // rows of one query copy
   int MT;                 // items per KV head (TREE, RING)
   int whole;              // items are not cut (TREE, RING)
-  int withhold;           // failure-handling test: CTA 0 leaves its second copy out
+  int withhold;           // failure-handling test: CTA 0's second stage never fills
 };
 
 __device__ __forceinline__ void set_status(int32_t* status, int bits) {
@@ -858,7 +858,8 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
   // ---- set-up: barriers, TMEM, and where this CTA's run of tiles starts
   if (tid == 0) {
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(bar(&C.full[i]), 1);
+      // (withheld: one arrival too many, and every wait for that stage runs out)
+      mbar_init(bar(&C.full[i]), A.withhold && blockIdx.x == 0 && i == 1 ? 2 : 1);
       mbar_init(bar(&C.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -1590,7 +1591,6 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
         if (!SOLO) __syncwarp();
       };
       uint32_t st = 0, lap = 0, idx = 0;  // stage, times around the ring, copies
-      const uint32_t left_out = A.withhold && blockIdx.x == 0 ? 1u : ~0u;
       int segs = 0;
       bool ok = true;
       for (;;) {
@@ -1621,9 +1621,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
           const uint32_t dst = base + SM::STAGE_AT + st * BYTES;
           if (!wait(bar(&C.empty[st]), (lap & 1) ^ 1)) return false;
           const Keys ky = keys_of<PR>(A, s, s.j0 + jj);
-          if (idx == left_out) {
-            // (the stage never fills: every wait for it runs out)
-          } else if (SOLO || ky.staged) {
+          if (SOLO || ky.staged) {
             if (lead) {
               const CUtensorMap* const m = !PR && ky.staged ? (is_v ? &A.mvn : &A.mkn)
                                                             : (is_v ? &A.mv : &A.mk);

@@ -36,7 +36,7 @@ def calls():
 
 
 def test_bounded_waits_report_timeout_and_context_recovers():
-    """With one copy left out, the waits for it run out after their one-second limit: the call reports SV_ST_TIMEOUT and
+    """With a slot that never fills, the waits for it run out after their one-second limit: the call reports SV_ST_TIMEOUT and
     returns, and the same call afterwards gives the bits that it gave before."""
     for name, (call, c) in calls().items():
         want, st = call(c)
