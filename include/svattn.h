@@ -20,7 +20,10 @@
  * The products run on the tensor cores in the storage type; scores, the
  * softmax's running maximum and sum, and the output's sums are 32-bit floats.
  * The softmax weights are rounded once to the storage type for the product
- * with v (half a step of that type each), and the output once at the end.
+ * with v (half a step of that type each; in 16-bit IEEE floats, whose smallest
+ * values are coarser, such errors of all the keys that the sizes allow add up
+ * to half a step of the largest weight at most, up to 2^28 keys), and the
+ * output once at the end.
  *
  * Conventions as in specverify.h: caller-owned device buffers (row-major,
  * contiguous), calls enqueued on `stream` (a cudaStream_t, NULL = legacy

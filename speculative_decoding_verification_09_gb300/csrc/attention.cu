@@ -71,6 +71,16 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
   A.G = A.Hq / A.Hkv;
   A.tpt = TILE / A.G;
   A.withhold = g_withhold;
+  if (dtype == SV_F16) {
+    // the keys that a row may see, times a weight's error of 2^-(25 + lift): below 2^-11
+    const long long window = (long long)A.sink + A.window;
+    const long long keys = A.kind == TREE   ? (long long)A.cols * A.page + A.N
+                           : A.kind == RING ? window + A.N
+                                            : (window < A.T ? window : A.T);
+    int lift = 0;
+    while (lift < MOST_LIFT && keys >> (14 + lift)) ++lift;
+    A.lift = float(lift);
+  }
   const uint64_t D = A.D, tokens = A.kind == PROMPT ? uint64_t(A.T) : uint64_t(A.B) * A.N;
   const uint32_t q_tok = uint32_t(
       A.tpt < (A.kind == PROMPT ? A.T : A.N) ? A.tpt : (A.kind == PROMPT ? A.T : A.N));

@@ -57,11 +57,16 @@ constexpr int COPY_WARP = 8, MMA_WARP = 9, PLAN_WARP = 10;
 constexpr int MAX_CTAS = 152;   // one per SM
 constexpr unsigned long long WAIT_LIMIT_NS = 1000000000ull;
 constexpr uint32_t SUSPEND_HINT_NS = 20000;
-// A row's running maximum is raised only when a score exceeds it by 2^14 in
-// the weights: until then weights of up to 2^14 are summed, which fp32 sums and
-// 16-bit weights (fp16: up to 2^16) hold as exactly as those below 1, and the
-// output tile needs no rescaling.  (8192 tokens: 325 us with 2^8, 314 with 2^12.)
-constexpr float RAISE_LOG2 = 14.0f;
+// A row's running maximum is raised only when a score would get a weight above 2^most,
+// and has the weight 2^lift when it is; until the next time weights of up to 2^most are
+// summed, which 32-bit sums hold as exactly as those below 1, and the output tile needs
+// no rescaling.  bf16 weights are as exact at any size: no lift (8192 tokens: 325 us with
+// a `most` of 8, 314 with 12).  fp16 ones end at 2^16 and get steps of 2^-24 below 2^-14:
+// a weight is off by up to 2^-(25 + lift) of the largest one, and the launch chooses the
+// lift by the number of keys so that all of them together stay below half a step of the
+// type.  (Ragged prompts: 89.6 us with 0 and 14, 90.1 with 4 and 15, 93.0 with 8 and 15.)
+constexpr float MOST_BF16 = 14.0f, MOST_F16 = 15.0f;
+constexpr int MOST_LIFT = 14;
 
 struct AttnParams {
   CUtensorMap mq, mk, mv, mkn, mvn;  // queries, cache (or prompt) K and V, staged K and V
@@ -74,6 +79,7 @@ struct AttnParams {
   float2* part_ml;        // their maxima and sums [2 * CTAs][rows]
   int4* desc;             // [CTAs] what each CTA's first and last segments are (DESC_*)
   float c;                // scale * log2(e)
+  float lift;             // fp16: weight of a row's maximum (log2)
   int kind;
   int B, N, Hq, Hkv, D, G;
   int LH, head0, num_pages, page, cols, sink, window, T;
@@ -643,7 +649,7 @@ struct Exchange {              // NQ == 0: softmax state exchanged between the s
 template <int NQ>
 struct Few {                   // NQ > 0, per stream and column
   uint32_t sees[2][NQ];            // columns that see a staged entry
-  alignas(16) float nmc[2][NQ];    // minus the running maximum, in base-2 units; -inf: none yet
+  alignas(16) float nmc[2][NQ];    // the lift less the running maximum, in base-2 units; -inf: none yet
   alignas(16) float fac[2][NQ];    // rescaling, and at the end the streams' shares
   float sums[8][NQ];               // per warp, at the end
 };
@@ -725,12 +731,14 @@ __device__ __forceinline__ void sum_columns(float* v, int lane) {
 // lq and stores them, rounded, as column `key` of P (a K-major operand of two
 // 64-key blocks in the 128-byte swizzle).  `sees`: the columns that see the
 // key.  All keys of a tile use one maximum per column; it is raised, the sums
-// and O (columns from to) rescaled, when a score exceeds it by 2^RAISE_LOG2.
+// and O (columns from to) rescaled, when a weight would exceed 2^most.
 template <int NQ, bool BF>
 __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>& C, int st,
                                             int key, uint32_t ts, uint32_t to, uint32_t sees,
                                             bool masked, bool started, bool& unset, float* lq,
                                             unsigned char* pbuf) {
+  constexpr float MOST = BF ? MOST_BF16 : MOST_F16;
+  const float lift = BF ? 0.0f : A.lift;
   const int lane = key & 31, warp = key >> 5;
   float* const nmc = C.x.nmc[st];
   const float2 c2 = make_float2(A.c, A.c);
@@ -766,7 +774,7 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
   load();
   bool raise = !started || unset;
   if (!raise) {
-    raise = group_or(1 + st, TILE, exponents() > RAISE_LOG2);
+    raise = group_or(1 + st, TILE, exponents() > MOST);
     __syncwarp();
     if (raise) load();
   }
@@ -787,10 +795,10 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
                             fmaxf(wmax[2 * NQ + key], wmax[3 * NQ + key])) * A.c;
       float old = started ? -nmc[key] : INFINITY, f = 1.0f;
       if (old == INFINITY) {
-        if (t > -INFINITY) old = t;
-      } else if (t - old > RAISE_LOG2) {
-        f = ex2(old - t);
-        old = t;
+        if (t > -INFINITY) old = t - lift;
+      } else if (t - old > MOST) {
+        f = ex2(old - (t - lift));
+        old = t - lift;
       }
       nmc[key] = -old;
       C.x.fac[st][key] = f;
@@ -1027,6 +1035,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       const int q0 = s.mt * tpi, q1 = min(q0 + tpi, tokens) - 1;  // the item's tokens
       const int w0 = q0 + (PAIR ? st * A.tpt : 0), w1 = min(w0 + A.tpt, tokens) - 1;  // the tile's
 
+      const float lift = BF ? 0.0f : A.lift, raise = BF ? MOST_BF16 : MOST_F16 - A.lift;
       float m = -INFINITY, l = 0.0f;
       float lq[NQ ? NQ : 1];  // NQ > 0: this key's share of the columns' sums
       bool unset = true;      // NQ > 0: a column has seen nothing yet
@@ -1151,7 +1160,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
             if (done == 0) {
               m = mt;
             } else {
-              const bool rise = active && (mt - m) * A.c > RAISE_LOG2;  // (-inf before: always)
+              const bool rise = active && (mt - m) * A.c > raise;  // (-inf before: always)
               if (__any_sync(0xffffffffu, rise)) {
                 const float f = rise ? ex2((m - mt) * A.c) : 1.0f;
                 if (rise) m = mt;
@@ -1203,8 +1212,8 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
                   mt = fmaxf(mt, max_of<32>([&](int i) { return __uint_as_float(r[x][i]); }));
             }
             raise_to(mt);
-            const float mc = m == -INFINITY ? 0.0f : m * A.c;
-            const float2 c2 = make_float2(A.c, A.c), mc2 = make_float2(-mc, -mc);
+            const float nm = m == -INFINITY ? 0.0f : lift - m * A.c;
+            const float2 c2 = make_float2(A.c, A.c), mc2 = make_float2(nm, nm);
             float2 sum[4] = {};
             uint32_t pw[16];
             auto chunk = [&](int x) {  // the weights of 32 keys
@@ -1274,8 +1283,8 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
             float mt = w > 64 ? two(2) : -INFINITY;
             mt = fmaxf(mt, two(0));
             raise_to(mt);
-            const float mc = m == -INFINITY ? 0.0f : m * A.c;
-            const float2 c2 = make_float2(A.c, A.c), mc2 = make_float2(-mc, -mc);
+            const float nm = m == -INFINITY ? 0.0f : lift - m * A.c;
+            const float2 c2 = make_float2(A.c, A.c), mc2 = make_float2(nm, nm);
             float2 sum[4] = {};
             auto weights = [&](int x, uint32_t (&r)[32]) {  // of 32 keys
               uint32_t pw[16];

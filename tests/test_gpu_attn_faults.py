@@ -81,3 +81,33 @@ def test_a_long_item_before_others_is_no_timeout():
     n = torch.tensor(lens, device=dev, dtype=torch.float64)
     seen = torch.where(n == 8, 1.0, n / page)
     assert torch.equal(out[:, 0, 0], (seen / (n + 1)).to(BF)[:, None].expand(B, 8))
+
+
+@pytest.mark.parametrize("N,G", [(1, 4), (4, 6), (20, 4), (60, 4)])
+def test_many_small_weights_in_16_bits(N, G):
+    """A million keys whose weights are 2^-25.5 of one key's, in 16-bit floats: together 2 % of the sum, and all of the
+    output.  With 2^20 keys (and no more than 2^21 in all) the kernel's 16-bit weights are at least 2^7 for a row's largest,
+    in steps of 2^-24 at the least: a weight is off by at most 2^-32 of the largest, beside half a step of its own (2^-11),
+    which also bounds the output's rounding; 32-bit sums and scores add 2^-23 of the sum for each of the L / 16 products' terms, and 2 (D + 8) E 2^-23 as
+    in attn_util.  A request for every SM, so that none is cut: a part of its own would have a maximum of its own."""
+    page, cols, D, Hkv, B = 4096, 256, 8, 1, 152
+    L = page * cols
+    dev = ta.DEV
+    kp, vp = torch.zeros(cols, Hkv, page, D, dtype=HF, device=dev), torch.ones(cols, Hkv, page, D, dtype=HF, device=dev)
+    kp[:, :, :, 0] = -25.5
+    kn, vn = torch.zeros(B, Hkv, N, D, dtype=HF, device=dev), torch.zeros(B, Hkv, N, D, dtype=HF, device=dev)
+    q = torch.zeros(B, N, Hkv * G, D, dtype=HF, device=dev)
+    q[..., 0] = 1.0
+    kp[0, 0, 7, 0], vp[0, 0, 7] = 0.0, 0.0  # the one key, early: the others never raise the maximum
+    kn[..., 0] = -60.0  # the staged entries weigh nothing
+    parent = ta.i32([[-1] + [0] * (N - 1)] * B)
+    out, st = torch.empty_like(q), ta.status()
+    ws = binding.make_attn_workspace(B, N, Hkv * G, Hkv, D, dev)
+    binding.sv_tree_attn(q, kp, vp, ta.i32([range(cols)] * B), ta.i32([L] * B), kn, vn, parent, out, ws,
+                         scale=float(np.log(2.0)), dev_status=st)
+    assert int(st.item()) == 0
+    small = (L - 1) * 2.0 ** -25.5
+    want = small / (1.0 + small)
+    tol = 2.0 ** -32 * L + want * (2 * 2.0 ** -11 + (L / 16 + 2 * (D + 8) * 25.5) * 2.0 ** -23)
+    assert float((out.double() - want).abs().max()) <= tol
+    assert tol < want / 40
