@@ -111,3 +111,63 @@ def test_many_small_weights_in_16_bits(N, G):
     tol = 2.0 ** -32 * L + want * (2 * 2.0 ** -11 + (L / 16 + 2 * (D + 8) * 25.5) * 2.0 ** -23)
     assert float((out.double() - want).abs().max()) <= tol
     assert tol < want / 40
+
+
+# ------------------------------------------------------------------ invalid requests whose items are cut
+
+LAYOUTS = [(3, 4, 64), (5, 5, 128), (22, 4, 128), (61, 4, 64), (200, 2, 128)]  # 12, 25, 88, 244 and 400 rows
+
+
+@pytest.mark.parametrize("N,G,D", LAYOUTS)
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_cut_invalid_trees(N, G, D, dtype):
+    """Items cut over many blocks, of which one or a few see what is wrong: the whole request is zeros."""
+    lens, page = [4100, 3000, 5000], 16
+    good = ta.tree_inputs(21, 3, N, 2 * G, 2, D, page, lens, dtype)
+    want, st = ta.tree_call(good)
+    assert int(st.item()) == 0
+    for b in range(3):
+        ta.au.check(want[b], *ta.tree_reference(good, b), f"request {b}")
+    cases = [("page", at, binding.SV_ST_BAD_PAGE) for at in (0, 94, 187)]  # the first, a middle and the last part
+    cases += [("parent", at, binding.SV_ST_BAD_TOKEN) for at in (0, N - 1)]
+    cases += [("length", n, binding.SV_ST_BAD_LENGTH) for n in (-1, 1 << 30)]
+    for what, at, bit in cases:
+        c = dict(good, lens=list(lens), table=good["table"].copy(), parent=good["parent"].copy())
+        if what == "page":
+            c["table"][1, at] = c["kp"].shape[0] if at else -1
+        elif what == "parent":
+            c["parent"][1, at] = at
+        else:
+            c["lens"][1] = at
+        out, st = ta.tree_call(c)
+        assert int(st.item()) == bit, (what, at)
+        assert torch.count_nonzero(out[1]) == 0, (what, at)
+        for b in (0, 2):
+            if what == "length":  # (the others' items are cut elsewhere)
+                ta.au.check(out[b], *ta.tree_reference(good, b), f"{what} {at}, request {b}")
+            else:
+                assert torch.equal(out[b], want[b]), (what, at, b)
+
+
+@pytest.mark.parametrize("N,G,D", [(3, 4, 64), (5, 5, 128), (22, 4, 128), (61, 4, 64)])
+def test_cut_invalid_positions(N, G, D):
+    good = ta.ring_inputs(22, 3, N, 2 * G, 2, D, 4, 5000, [9000, 4321, 5004], BF)
+    for p in (-1, 2147483647, 2147483647 - N + 1):
+        c = dict(good, pos=[9000, p, 5004])
+        out, st = ta.ring_call(c)
+        assert int(st.item()) == binding.SV_ST_BAD_LENGTH and torch.count_nonzero(out[1]) == 0, p
+        for b in (0, 2):
+            ta.au.check(out[b], *ta.ring_reference(good, b), f"position {p}, request {b}")
+
+
+@pytest.mark.parametrize("N,G,D", LAYOUTS)
+def test_whole_invalid_trees(N, G, D):
+    """The same with items left whole (short tables)."""
+    good = ta.tree_inputs(23, 3, N, 2 * G, 2, D, 16, [100, 60, 120], BF)
+    want, _ = ta.tree_call(good)
+    for what, bit in (("page", binding.SV_ST_BAD_PAGE), ("parent", binding.SV_ST_BAD_TOKEN)):
+        c = dict(good, table=good["table"].copy(), parent=good["parent"].copy())
+        c["table" if what == "page" else "parent"][1, 1] = 1 << 20
+        out, st = ta.tree_call(c)
+        assert int(st.item()) == bit and torch.count_nonzero(out[1]) == 0, what
+        assert torch.equal(out[[0, 2]], want[[0, 2]]), what
