@@ -142,8 +142,12 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
                                              : (long long)A.sink + A.window;
     const long long most = (entries + TILE - 1) / TILE + (A.N + TILE - 1) / TILE;
     const long long items = (long long)A.B * A.Hkv * A.MT;
-    A.whole = most <= 3 || (2 * items >= ctas &&
-                            most <= (lay.nq == 0 ? 12 : items >= 8LL * ctas ? 8 : 5));
+    // The kernel decides by the batch's longest request, and the join, which then finds
+    // nothing to do, is launched unless no request of this cache can be longer.  (Tables of
+    // 32768 positions, by their extent and by the lengths, of 893: 160 requests of 200 rows
+    // 212 us and 168, 10 such requests 28.5 and 24.6.)
+    A.whole_tiles = 2 * items >= ctas ? (lay.nq == 0 ? 12 : items >= 8LL * ctas ? 8 : 5) : 3;
+    A.join = most > A.whole_tiles;
     const size_t rows = lay.rows, dp = A.D > 64 ? 128 : 64;
     unsigned char* w = static_cast<unsigned char*>(workspace);
     A.part_o = reinterpret_cast<float*>(w);

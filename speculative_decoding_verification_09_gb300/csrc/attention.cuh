@@ -87,7 +87,8 @@ struct AttnParams {
   int tpt;                // tokens per query tile, floor(128 / G)
   int q_rows;             // rows of one query copy
   int MT;                 // items per KV head (TREE, RING)
-  int whole;              // items are not cut (TREE, RING)
+  int whole_tiles;        // no item is cut when none has more tiles than this (TREE, RING)
+  int join;               // and some may have, by the cache's extent
   int withhold;           // failure-handling test: CTA 0's second stage never fills
 };
 
@@ -467,9 +468,11 @@ struct Cursor;
 template <bool PAIR>
 struct Cursor<PAIR, false> {
   int b, item, j, nt, len, bad, pos;
+  bool whole;      // items are not cut
   long long left;  // tiles of the run ahead
 
-  __device__ void open(const AttnParams& A, int b0, long long at, long long count) {
+  __device__ void open(const AttnParams& A, int b0, long long at, long long count, bool w) {
+    whole = w;
     left = count;
     if (count <= 0) return;
     b = b0;
@@ -478,7 +481,7 @@ struct Cursor<PAIR, false> {
     const int cost = nt + ITEM_COST;
     item = at >> 32 ? int(at / cost) : int(uint32_t(at) / uint32_t(cost));
     j = int(at - (long long)item * cost);
-    if (A.whole && j > 0) {  // an earlier CTA's item
+    if (whole && j > 0) {  // an earlier CTA's item
       left -= cost - j;
       step(A);
     }
@@ -505,7 +508,7 @@ struct Cursor<PAIR, false> {
       s.h = item / A.MT;
       s.mt = item - s.h * A.MT;
       s.j0 = j;
-      s.n = A.whole || left >= nt - j ? nt - j : int(left);
+      s.n = whole || left >= nt - j ? nt - j : int(left);
       s.nt = nt;
       s.len = len;
       s.bad = bad;
@@ -667,7 +670,7 @@ struct Ctrl {
   uint8_t parent[2][NQ ? NQ : PAIR ? MAX_N : TILE];  // one copy per softmax warpgroup
   union {
     typename Either<NQ, Few<NQ>, Exchange<PAIR>>::T x;
-    long long scan[12];
+    struct { long long sum[THREADS / 32]; int most[THREADS / 32]; } scan;
   };
   unsigned long long out_at[NQ ? NQ : 1];  // NQ > 0: elements from an item's output to a column's
 };
@@ -906,27 +909,37 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   long long run = 0;  // tiles of this CTA (TREE, RING)
+  bool whole_items = false;
   if (!PR) {
     // thread t sums requests t * per .. of the batch
     const int per = (A.B + THREADS - 1) / THREADS;
     const int b0 = min(tid * per, A.B), b1 = min(b0 + per, A.B);
     const long long items = (long long)A.MT * A.Hkv;
     long long mine = 0;
-    int bad, pos;
-    for (int b = b0; b < b1; ++b)
-      mine += items * (tiles_of(cache_len(A, b, bad, pos)) + tiles_of(A.N) + ITEM_COST);
+    int bad, pos, most = 0;
+    for (int b = b0; b < b1; ++b) {
+      const int nt = tiles_of(cache_len(A, b, bad, pos)) + tiles_of(A.N);
+      mine += items * (nt + ITEM_COST);
+      most = max(most, nt);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
     long long incl = mine;
     for (int x = 1; x < 32; x <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, incl, x);
       if (lane >= x) incl += y;
     }
-    if (lane == 31) C.scan[warp] = incl;
+    if (lane == 31) {
+      C.scan.sum[warp] = incl;
+      C.scan.most[warp] = most;
+    }
     __syncthreads();
     long long total = 0, before = incl - mine;
     for (int w = 0; w < THREADS / 32; ++w) {
-      if (w < warp) before += C.scan[w];
-      total += C.scan[w];
+      if (w < warp) before += C.scan.sum[w];
+      total += C.scan.sum[w];
+      most = max(most, C.scan.most[w]);
     }
+    whole_items = most <= A.whole_tiles;
     const long long ctas = min((long long)gridDim.x, total), c = blockIdx.x;
     const long long each = total / ctas, more = total - each * ctas;
     const long long lo = c < ctas ? c * each + min(c, more) : total;
@@ -951,7 +964,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
   tc_after();
   // the join may be launched now: its blocks find room when this grid's CTAs
   // leave, and wait for the last of them before they read anything
-  if (!PR && !A.whole) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!PR && A.join) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = C.tmem;
   const int start_b = C.start_b;
   const long long start_at = C.start_at;
@@ -1513,7 +1526,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       seg_done(segs);
       ++segs;
     }
-    if (!PR && !A.whole && tid == 0) A.desc[blockIdx.x] = make_int4(d_flags, d_item, d_b, 0);
+    if (!PR && A.join && tid == 0) A.desc[blockIdx.x] = make_int4(d_flags, d_item, d_b, 0);
   } else {
     __syncwarp();
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
@@ -1582,7 +1595,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       if (report) cur.item(A, 0x7fffffffffffffffll, s, true);  // the other sequences' bounds
       plan(seg_count, false);
     } else {
-      cur.open(A, start_b, start_at, run);
+      cur.open(A, start_b, start_at, run, whole_items);
       int k = 0;
       while (plan(k, cur.next(A, s))) ++k;
     }
@@ -1988,7 +2001,7 @@ int launch_as(const AttnParams& A, int device, int grid, int ctas, cudaStream_t 
   }
   sv_attn<DP, NQ, PAIR, PR, BF><<<grid, THREADS, (Smem<DP, NQ>::TOTAL), st>>>(A);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
-  if (PR || A.whole) return SV_OK;
+  if (PR || !A.join) return SV_OK;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(JOIN_BLOCKS * ctas));
   cfg.blockDim = dim3(JOIN_WARPS * 32);

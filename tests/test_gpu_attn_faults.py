@@ -171,3 +171,19 @@ def test_whole_invalid_trees(N, G, D):
         out, st = ta.tree_call(c)
         assert int(st.item()) == bit and torch.count_nonzero(out[1]) == 0, what
         assert torch.equal(out[[0, 2]], want[[0, 2]]), what
+
+
+# ------------------------------------------------------------------ wide tables
+
+@pytest.mark.parametrize("B,N,G,D,n", [(160, 1, 4, 64, 500), (90, 20, 2, 64, 1300), (80, 50, 4, 64, 900), (5, 6, 4, 64, 330)])
+def test_a_tables_width_changes_nothing(B, N, G, D, n):
+    """Whether items are cut goes by the requests' lengths: the columns that no length reaches change no bit."""
+    lens = [n - 7 * (b % 11) for b in range(B)]
+    c = ta.tree_inputs(31, B, N, 2 * G, 2, D, 16, lens, BF)
+    out, st = ta.tree_call(c)
+    wide = dict(c, table=np.concatenate([c["table"], np.full((B, 2000), -1, np.int32)], 1))
+    again, st2 = ta.tree_call(wide)
+    assert int(st.item()) == 0 and int(st2.item()) == 0
+    assert torch.equal(out, again)
+    for b in (0, 7 % B, B - 1):
+        ta.au.check(out[b], *ta.tree_reference(c, b), f"request {b}")
