@@ -156,7 +156,7 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
   } else {
     // Two query tiles per item when that leaves every SM an item, else one: half the
     // work per item, for twice the loads of keys.  (Enough items: 24 ragged prompts
-    // 97 us in pairs, 108 singly; 8192 tokens 310 and 353.)
+    // 90 us in pairs, 108 singly; 8192 tokens 321 and 380.)
     lay = {0, (long long)A.Hkv * (A.T / (2 * A.tpt)) >= ctas ? 2 * TILE : TILE};
     const int tpi = lay.rows == 2 * TILE ? 2 * A.tpt : A.tpt;
     // an upper bound: every sequence that holds a token adds at most one part item

@@ -17,10 +17,10 @@
 // ahead, and runs of equal length whatever the requests' lengths.  64 requests of
 // 22 nodes over 2000 to 9000 tokens (1.39 GB): 225 us, 6.2 TB/s, 0.91 of the
 // measured copy bandwidth.  Prompts: 4 D flops per pair of tokens and query head;
-// the tensor cores are busy 0.6 of the time, and each of the two tiles of queries
+// the tensor cores are busy 0.61 of the time, and each of the two tiles of queries
 // that share an SM is a chain: scores, softmax, the weights' product, the next
 // scores (which take the weights' place).  8192 tokens under a window of 4096, 32
-// heads of 128: 318 us, 1.30 PFLOP/s, 0.67 of the measured bf16 rate.
+// heads of 128: 319 us, 1.29 PFLOP/s, 0.67 of the measured bf16 rate.
 #ifndef SV_ATTENTION_CUH
 #define SV_ATTENTION_CUH
 
