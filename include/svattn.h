@@ -26,9 +26,10 @@
  * output once at the end.
  *
  * Conventions as in specverify.h: caller-owned device buffers (row-major,
- * contiguous), calls enqueued on `stream` (a cudaStream_t, NULL = legacy
- * default stream), host-detectable errors returned (SV_ERR_* codes), data
- * errors OR-ed into *dev_status (may be NULL), nothing traps.
+ * contiguous) of the current device, calls enqueued on `stream` (a
+ * cudaStream_t, NULL = legacy default stream), host-detectable errors returned
+ * (SV_ERR_* codes), data errors OR-ed into *dev_status (may be NULL), nothing
+ * traps.
  *   dtype: SV_BF16, or SV_F16 (16-bit IEEE floats); SV_F32 is SV_ERR_DTYPE.
  *   Hq a multiple of Hkv with Hq / Hkv <= 128; D a multiple of 8 in [8, 128];
  *   scale > 0, and scale * log2(e) finite; all 16-bit buffers aligned to 16 bytes, int32 ones
@@ -127,9 +128,9 @@ int sv_prompt_attn(int dtype, const void* q, const void* k, const void* v,
 
 /*
  * Failure-handling test aid, as sv_test_withhold_slot: while enabled, one of
- * the slots of block 0 of the next attention calls never counts as filled, so that
- * the waits for it run out after their one-second limit (SV_ST_TIMEOUT).  No fault, trap or endless
- * wait is involved.  Not thread-safe.  Returns SV_OK.
+ * the slots of block 0 of the next attention calls never counts as filled, so
+ * that the waits for it run out after their one-second limit (SV_ST_TIMEOUT).
+ * No fault, trap or endless wait is involved.  Not thread-safe.  Returns SV_OK.
  */
 int sv_attn_test_withhold(int enable);
 

@@ -8,6 +8,7 @@ loading it raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -188,10 +189,19 @@ def _status(t: torch.Tensor | None, device) -> int | None:
     return None if t is None else _buf(t, t.shape, torch.int32, device, "dev_status")
 
 
+@functools.cache
+def _several_devices() -> bool:  # (asking for the current device costs a call 0.5 us)
+    return torch.cuda.device_count() > 1
+
+
 def _cuda_device(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise SpecVerifyError(f"{name} must be a CUDA tensor")
-    return t.get_device()
+    dev = t.get_device()
+    if _several_devices() and dev != torch.cuda.current_device():  # the library launches there
+        raise SpecVerifyError(f"{name} is on cuda:{dev}, the current device is "
+                              f"cuda:{torch.cuda.current_device()}")
+    return dev
 
 
 def _shapes(target_logits: torch.Tensor):
