@@ -9,10 +9,11 @@ from concurrent.futures import ThreadPoolExecutor
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", f) for f in ("specverify.cu", "kvcache.cu", "tree.cu",
-                                              "attention.cu", "attn_bf16.cu", "attn_f16.cu")]
-INCLUDED = [os.path.join(PKG, "csrc", "attention.cuh")]
+                                              "attention.cu", "attn_bf16.cu", "attn_f16.cu",
+                                              "attn8_bf16.cu", "attn8_f16.cu", "rope.cu", "kv8.cu")]
+INCLUDED = [os.path.join(PKG, "csrc", f) for f in ("attention.cuh", "rope.cuh")]
 HEADERS = [os.path.join(ROOT, "include", f) for f in ("specverify.h", "svkv.h", "svtree.h",
-                                                     "svattn.h")]
+                                                     "svattn.h", "svrope.h", "svkv8.h")]
 OUT_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libspecverify.so")
 

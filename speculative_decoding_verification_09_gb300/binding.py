@@ -34,7 +34,10 @@ EXPORTED = ("sv_workspace_bytes", "sv_workspace_init", "spec_verify", "spec_veri
             "sv_tree_set_warps")
 EXPORTED_ATTN = ("sv_attn_workspace_bytes", "sv_tree_attn", "sv_ring_attn", "sv_prompt_attn",
                  "sv_attn_test_withhold")
+EXPORTED_ROPE = ("sv_rope_table", "sv_rope", "sv_page_append")
+EXPORTED_KV8 = ("sv_page_append8", "sv_page_commit8", "sv_tree_attn8")
 SV_TREE_MAX_N = 256
+SV_ROPE_NONE, SV_ROPE_LINEAR, SV_ROPE_BASE, SV_ROPE_RAMP, SV_ROPE_WAVE = range(5)
 SV_NOALLOC_MAX_WORKSPACE = 16 << 20
 
 _lib = None
@@ -80,6 +83,17 @@ def lib() -> ctypes.CDLL:
                                    P]
         L.sv_prompt_attn.argtypes = [I, P, P, P, P, F, I, I, I, I, I, I, I, P, P, P]
         L.sv_attn_test_withhold.argtypes = [I]
+        D, W = ctypes.c_double, ctypes.c_longlong
+        L.sv_rope_table.argtypes = [I, D, D, I, D, D, D, I, I, I, P, P]
+        L.sv_rope.argtypes = [I, P, W, P, W, P, P, I, I, I, I, I, I, I, P, W, P, W, P, P]
+        L.sv_page_append.argtypes = [I, P, W, P, W, P, P, P, P, P, P, I, I, I, P, P, W, P, W, P, W,
+                                     I, I, I, I, I, I, I, I, I, I, P, P, P]
+        L.sv_page_append8.argtypes = [I, P, W, P, W, P, P, P, P, P, P, P, P, I, I, I, P, I, I, I, I,
+                                      I, I, I, I, I, I, P, P, P]
+        L.sv_page_commit8.argtypes = [I, P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, P,
+                                      P]
+        L.sv_tree_attn8.argtypes = [I, P, P, P, P, P, P, P, P, P, P, F, I, I, I, I, I, I, I, I, I,
+                                    I, I, P, P, Z, P, P]
         L.sv_tree_set_cluster.argtypes = [I]
         L.sv_tree_set_warps.argtypes = [I]
         L.sv_set_tuning.argtypes = [I]
@@ -97,7 +111,7 @@ def lib() -> ctypes.CDLL:
                      "sv_kv_fill", "sv_page_commit", "sv_tree_attn", "sv_ring_attn",
                      "sv_prompt_attn", "sv_attn_test_withhold",
                      "sv_window_block_table", "sv_window_seq_lens_host", "sv_tree_verify",
-                     "sv_tree_set_cluster", "sv_tree_set_warps"):
+                     "sv_tree_set_cluster", "sv_tree_set_warps", *EXPORTED_ROPE, *EXPORTED_KV8):
             getattr(L, name).restype = I
         _lib = L
     return _lib
@@ -589,4 +603,206 @@ def sv_prompt_attn(q, k, v, cu_seqlens, sink: int, window: int, out, scale: floa
         _buf(cu_seqlens, cu_seqlens.shape, torch.int32, dev, "cu_seqlens"),
         D ** -0.5 if scale is None else scale, cu_seqlens.shape[0] - 1, T, Hq, Hkv, D, sink,
         window, _buf(out, q.shape, dt, dev, "out"), _status(dev_status, dev),
+        _stream(stream, dev)))
+
+
+# ------------------------------------------------------- rotary positions, appending to pages
+
+def _packed(t, heads, D, dtype, device, name: str) -> tuple[int, int]:
+    """(address, stride) of packed tokens [T][H][D] whose rows may be slices of wider ones."""
+    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, D):
+        raise SpecVerifyError(f"{name} must be [T][{heads}][{D}], got {tuple(t.shape)}")
+    if not t.is_cuda or t.get_device() != device:
+        raise SpecVerifyError(f"{name} must be on the call's CUDA device")
+    if t.dtype != dtype:
+        raise SpecVerifyError(f"{name} must be {dtype}, got {t.dtype}")
+    T = t.shape[0]
+    row, head, one = t.stride()
+    if T and ((D > 1 and one != 1) or (heads > 1 and head != D)):
+        raise SpecVerifyError(f"{name}'s rows must be contiguous")
+    return t.data_ptr(), row if T > 1 else heads * D
+
+
+def _same_tokens(T: int, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.shape[0] != T:
+            raise SpecVerifyError(f"{name} must have {T} tokens, got {t.shape[0]}")
+
+
+def _angles(table, device) -> tuple[int | None, int, int]:
+    """(address, rows, rotated dimensions) of a rotation table [rows][2][rot / 2], or of none."""
+    if table is None:
+        return None, 0, 0
+    if table.dim() != 3 or table.shape[1] != 2:
+        raise SpecVerifyError("table must be [rows][2][rot / 2]")
+    return (_buf(table, table.shape, torch.float32, device, "table"), table.shape[0],
+            2 * table.shape[2])
+
+
+def sv_rope_table(table, base: float = 10000.0, scaling: int = SV_ROPE_NONE, factor: float = 1.0,
+                  original: int = 0, low: float = 1.0, high: float = 32.0, gain: float = 1.0,
+                  first: int = 0, stream=None) -> None:
+    """Fill a rotation table [rows][2][rot / 2] (float32: cosines, then sines) for the positions
+    first, first + 1, ...; scaling: one of SV_ROPE_*, with the context's factor over the original
+    one and, for SV_ROPE_RAMP and SV_ROPE_WAVE, its bounds in turns over the original context."""
+    dev = _cuda_device(table, "table")
+    at, rows, rot = _angles(table, dev)
+    _check(lib().sv_rope_table(scaling, base, factor, original, low, high, gain, rot, first, rows,
+                               at, _stream(stream, dev)))
+
+
+def sv_rope(q, k, positions, table, q_out, k_out=None, interleaved: bool = False, dev_status=None,
+            stream=None) -> None:
+    """Rotate queries q [T][Hq][D] and keys k [T][Hk][D] (or None) at positions [T] int32 by a
+    table of sv_rope_table; the outputs may be the inputs.  Rows may be slices of wider ones."""
+    if q.dim() != 3:
+        raise SpecVerifyError("q must be [T][Hq][D]")
+    T, Hq, D = q.shape
+    code, dev = _attn_dtype(q), _cuda_device(q, "q")
+    _same_tokens(T, k=k, q_out=q_out, k_out=k_out)
+    if (k is None) != (k_out is None):
+        raise SpecVerifyError("k and k_out come together")
+    Hk = 0 if k is None else k.shape[1]
+    qp, qs = _packed(q, Hq, D, q.dtype, dev, "q")
+    qo, qos = _packed(q_out, Hq, D, q.dtype, dev, "q_out")
+    kp, ks = (None, 0) if k is None else _packed(k, Hk, D, q.dtype, dev, "k")
+    ko, kos = (None, 0) if k is None else _packed(k_out, Hk, D, q.dtype, dev, "k_out")
+    at, rows, rot = _angles(table, dev)
+    _check(lib().sv_rope(
+        code, qp, qs, kp, ks, _buf(positions, (T,), torch.int32, dev, "positions"), at, rows, rot,
+        int(interleaved), T, Hq, Hk, D, qo, qos, ko, kos, _status(dev_status, dev),
+        _stream(stream, dev)))
+
+
+def sv_page_append(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, table=None,
+                   positions=None, q=None, q_out=None, k_out=None, out_seq_lens=None,
+                   head0: int = 0, interleaved: bool = False, dev_status=None,
+                   stream=None) -> None:
+    """Append packed tokens' keys and values [T][Hkv][D] (cu_seqlens [B+1] int32) to the pages
+    [P][LH][page][D] of requests of seq_lens [B] entries, in rows head0 .. head0 + Hkv - 1, keys
+    rotated by `table` (None: as they are) at their positions in the cache or at positions [T];
+    with q, queries rotated to q_out, and with k_out the rotated keys packed, too (both may be the
+    inputs).  out_seq_lens [B] gets the new lengths."""
+    if k.dim() != 3 or k_pages.dim() != 4 or block_table.dim() != 2:
+        raise SpecVerifyError("k and v must be [T][Hkv][D], pages [P][LH][page][D], block_table "
+                              "[B][cols]")
+    T, Hkv, D = k.shape
+    P, LH, page, _ = k_pages.shape
+    B, cols = block_table.shape
+    code, dev, dt, i32 = _attn_dtype(k), _cuda_device(k, "k"), k.dtype, torch.int32
+    _same_tokens(T, v=v, q=q, q_out=q_out, k_out=k_out)
+    if (q is None) != (q_out is None):
+        raise SpecVerifyError("q and q_out come together")
+    Hq = 0 if q is None else q.shape[1]
+    kp, ks = _packed(k, Hkv, D, dt, dev, "k")
+    vp, vs = _packed(v, Hkv, D, dt, dev, "v")
+    qp, qs = (None, 0) if q is None else _packed(q, Hq, D, dt, dev, "q")
+    qo, qos = (None, 0) if q is None else _packed(q_out, Hq, D, dt, dev, "q_out")
+    ko, kos = (None, 0) if k_out is None else _packed(k_out, Hkv, D, dt, dev, "k_out")
+    at, rows, rot = _angles(table, dev)
+    _check(lib().sv_page_append(
+        code, kp, ks, vp, vs, _buf(k_pages, (P, LH, page, D), dt, dev, "k_pages"),
+        _buf(v_pages, (P, LH, page, D), dt, dev, "v_pages"),
+        _buf(block_table, (B, cols), i32, dev, "block_table"),
+        _buf(seq_lens, (B,), i32, dev, "seq_lens"),
+        _buf(cu_seqlens, (B + 1,), i32, dev, "cu_seqlens"), at, rows, rot, int(interleaved),
+        None if positions is None else _buf(positions, (T,), i32, dev, "positions"),
+        qp, qs, qo, qos, ko, kos, B, T, Hq, Hkv, D, P, LH, head0, page, cols,
+        None if out_seq_lens is None else _buf(out_seq_lens, (B,), i32, dev, "out_seq_lens"),
+        _status(dev_status, dev), _stream(stream, dev)))
+
+
+# ------------------------------------------------------- the paged cache in 8 bits
+
+def _pages8(k_pages, v_pages, k_scales, v_scales, device):
+    """Addresses and sizes (P, LH, page, D, block) of an 8-bit cache."""
+    if k_pages.dim() != 4 or k_scales.dim() != 3:
+        raise SpecVerifyError("pages must be [P][LH][page][D], scales [P][LH][page / block]")
+    P, LH, page, D = k_pages.shape
+    blocks = k_scales.shape[2]
+    block = page // blocks if blocks else 0
+    if block * blocks != page:
+        raise SpecVerifyError(f"a page of {page} tokens has no {blocks} blocks")
+    e4m3, e8m0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+    at = [_buf(t, (P, LH, page, D), e4m3, device, n)
+          for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages"))]
+    at += [_buf(t, (P, LH, blocks), e8m0, device, n)
+           for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales"))]
+    return at, P, LH, page, D, block
+
+
+def sv_page_append8(k, v, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_seqlens,
+                    table=None, positions=None, out_seq_lens=None, head0: int = 0,
+                    interleaved: bool = False, dev_status=None, stream=None) -> None:
+    """sv_page_append (without queries and packed keys) into 8-bit pages: k_pages / v_pages
+    [P][LH][page][D] float8_e4m3fn and k_scales / v_scales [P][LH][page / block] float8_e8m0fnu."""
+    if k.dim() != 3 or block_table.dim() != 2:
+        raise SpecVerifyError("k and v must be [T][Hkv][D], block_table [B][cols]")
+    T, Hkv, D = k.shape
+    B, cols = block_table.shape
+    code, dev, dt, i32 = _attn_dtype(k), _cuda_device(k, "k"), k.dtype, torch.int32
+    _same_tokens(T, v=v)
+    pools, P, LH, page, Dp, block = _pages8(k_pages, v_pages, k_scales, v_scales, dev)
+    if Dp != D:
+        raise SpecVerifyError(f"pages have {Dp} dimensions, keys {D}")
+    kp, ks = _packed(k, Hkv, D, dt, dev, "k")
+    vp, vs = _packed(v, Hkv, D, dt, dev, "v")
+    at, rows, rot = _angles(table, dev)
+    _check(lib().sv_page_append8(
+        code, kp, ks, vp, vs, *pools, _buf(block_table, (B, cols), i32, dev, "block_table"),
+        _buf(seq_lens, (B,), i32, dev, "seq_lens"),
+        _buf(cu_seqlens, (B + 1,), i32, dev, "cu_seqlens"), at, rows, rot, int(interleaved),
+        None if positions is None else _buf(positions, (T,), i32, dev, "positions"),
+        B, T, Hkv, D, P, LH, head0, page, block, cols,
+        None if out_seq_lens is None else _buf(out_seq_lens, (B,), i32, dev, "out_seq_lens"),
+        _status(dev_status, dev), _stream(stream, dev)))
+
+
+def sv_page_commit8(k_pages, v_pages, k_scales, v_scales, k_new, v_new, block_table, seq_lens,
+                    nodes, num_accepted, out_seq_lens, dev_status=None, stream=None) -> None:
+    """sv_page_commit into 8-bit pages (as for sv_page_append8): the verified path of the staged
+    entries k_new / v_new [B][LH][N][D]; out_seq_lens may be seq_lens itself."""
+    if k_new.dim() != 4 or block_table.dim() != 2:
+        raise SpecVerifyError("staged entries must be [B][LH][N][D], block_table [B][cols]")
+    B, cols = block_table.shape
+    N = k_new.shape[2]
+    code, dev, i32 = _attn_dtype(k_new), _cuda_device(k_new, "k_new"), torch.int32
+    pools, P, LH, page, D, block = _pages8(k_pages, v_pages, k_scales, v_scales, dev)
+    new = (B, LH, N, D)
+    _check(lib().sv_page_commit8(
+        code, *pools, _buf(k_new, new, k_new.dtype, dev, "k_new"),
+        _buf(v_new, new, k_new.dtype, dev, "v_new"),
+        _buf(block_table, (B, cols), i32, dev, "block_table"),
+        _buf(seq_lens, (B,), i32, dev, "seq_lens"),
+        None if nodes is None else _buf(nodes, (B, N), i32, dev, "nodes"),
+        _buf(num_accepted, (B,), i32, dev, "num_accepted"), B, LH, N, D, P, page, block, cols,
+        _buf(out_seq_lens, (B,), i32, dev, "out_seq_lens"), _status(dev_status, dev),
+        _stream(stream, dev)))
+
+
+def sv_tree_attn8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, k_new, v_new,
+                  parent, out, workspace, head0: int = 0, kv_heads: int | None = None,
+                  scale: float | None = None, dev_status=None, stream=None) -> None:
+    """sv_tree_attn over 8-bit pages (as for sv_page_append8); queries, output and the tree's
+    staged entries are bfloat16 or float16."""
+    if q.dim() != 4 or block_table.dim() != 2:
+        raise SpecVerifyError("q must be [B][N][Hq][D], block_table [B][cols]")
+    code = _attn_dtype(q)
+    B, N, Hq, D = q.shape
+    cols = block_table.shape[1]
+    dev, dt, i32 = _cuda_device(q, "q"), q.dtype, torch.int32
+    pools, P, LH, page, Dp, block = _pages8(k_pages, v_pages, k_scales, v_scales, dev)
+    if Dp != D:
+        raise SpecVerifyError(f"pages have {Dp} dimensions, queries {D}")
+    new = (B, LH, N, D)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _check(lib().sv_tree_attn8(
+        code, _buf(q, q.shape, dt, dev, "q"), *pools,
+        _buf(block_table, (B, cols), i32, dev, "block_table"),
+        _buf(seq_lens, (B,), i32, dev, "seq_lens"), _buf(k_new, new, dt, dev, "k_new"),
+        _buf(v_new, new, dt, dev, "v_new"),
+        None if parent is None else _buf(parent, (B, N), i32, dev, "parent"),
+        D ** -0.5 if scale is None else scale, B, N, Hq,
+        LH - head0 if kv_heads is None else kv_heads, D, P, LH, head0, page, block, cols,
+        _buf(out, q.shape, dt, dev, "out"), ws, ws_bytes, _status(dev_status, dev),
         _stream(stream, dev)))

@@ -3,6 +3,7 @@
 // attention.cuh).
 
 #include "attention.cuh"
+#include "svkv8.h"
 
 namespace {
 
@@ -30,6 +31,18 @@ EncodeTiled encode_tiled() {
     return reinterpret_cast<EncodeTiled>(p);
   }();
   return fn;
+}
+
+// A map of 8-bit elements: dims[0] innermost, strides of dims 1.. in elements.
+bool make_map8(CUtensorMap* m, const void* p, int rank, const uint64_t* dims,
+               const uint64_t* strides, const uint32_t* box) {
+  cuuint64_t bytes[4];
+  cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  for (int i = 0; i + 1 < rank; ++i) bytes[i] = strides[i];
+  return encode_tiled()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, cuuint32_t(rank), const_cast<void*>(p),
+                        dims, bytes, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A map of 16-bit elements: dims[0] innermost, strides of dims 1.. in elements.
@@ -96,9 +109,10 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
     while (A.page % A.box) A.box /= 2;
     const uint64_t dims[4] = {D, uint64_t(A.page), uint64_t(A.LH), uint64_t(A.num_pages)};
     const uint64_t str[3] = {D, D * A.page, D * A.page * A.LH};
-    const uint32_t box[4] = {64, uint32_t(A.box), 1, 1};
-    if (!make_map(&A.mk, dtype, k, 4, dims, str, box) ||
-        !make_map(&A.mv, dtype, v, 4, dims, str, box))
+    const uint32_t box[4] = {A.k_scales ? (A.D > 64 ? 128u : 64u) : 64u, uint32_t(A.box), 1, 1};
+    if (A.k_scales ? !make_map8(&A.mk, k, 4, dims, str, box) || !make_map8(&A.mv, v, 4, dims, str, box)
+                   : !make_map(&A.mk, dtype, k, 4, dims, str, box) ||
+                         !make_map(&A.mv, dtype, v, 4, dims, str, box))
       return SV_ERR_CUDA;
   } else if (A.kind == RING) {
     const uint64_t C = uint64_t(A.sink) + A.window;
@@ -124,8 +138,8 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
     const uint64_t dims[3] = {D, uint64_t(A.N), uint64_t(A.B) * A.LH};
     const uint64_t str[2] = {D, D * A.N};
     const uint32_t box[3] = {64, TILE, 1};
-    if (!make_map(&A.mkn, dtype, k_new, 3, dims, str, box) ||
-        !make_map(&A.mvn, dtype, v_new, 3, dims, str, box))
+    if (!A.k_scales && (!make_map(&A.mkn, dtype, k_new, 3, dims, str, box) ||
+                        !make_map(&A.mvn, dtype, v_new, 3, dims, str, box)))
       return SV_ERR_CUDA;
     lay = layout_of(A.N, A.G);
     const int tpi = lay.rows == 2 * TILE ? 2 * A.tpt : A.tpt;
@@ -166,6 +180,8 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
     A.MT = 1;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (A.k_scales)
+    return (dtype == SV_BF16 ? launch8_bf16 : launch8_f16)(A, lay, dev, grid, ctas, st);
   return (dtype == SV_BF16 ? launch_bf16 : launch_f16)(A, lay, dev, grid, ctas, st);
 }
 
@@ -228,6 +244,50 @@ int sv_tree_attn(int dtype, const void* q, const void* k_pages, const void* v_pa
   A.B = B; A.N = N; A.Hq = Hq; A.Hkv = Hkv; A.D = D;
   A.LH = LH; A.head0 = head0; A.num_pages = num_pages; A.page = page_size; A.cols = cols;
   return launch(A, dtype, q, k_pages, v_pages, k_new, v_new, workspace, stream);
+}
+
+int sv_tree_attn8(int dtype, const void* q, const void* k_pages, const void* v_pages,
+                  const void* k_scales, const void* v_scales, const int32_t* block_table,
+                  const int32_t* seq_lens, const void* k_new, const void* v_new,
+                  const int32_t* parent, float scale, int B, int N, int Hq, int Hkv, int D,
+                  int num_pages, int LH, int head0, int page_size, int block, int cols, void* out,
+                  void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  if (dtype != SV_BF16 && dtype != SV_F16) return SV_ERR_DTYPE;
+  int block_log = 3;
+  while (block_log < 7 && 1 << block_log != block) ++block_log;
+  if (B < 0 || B > 65535 || N < 1 || N > MAX_N || bad_heads(Hq, Hkv, D) || D % 16 != 0 ||
+      num_pages < 1 || LH < 1 || head0 < 0 || head0 > LH - Hkv || page_size < 8 ||
+      page_size > 65536 || 1 << block_log != block || page_size % block != 0 || cols < 1 ||
+      (long long)B * LH > 0x7fffffffLL || bad_scale(scale))
+    return SV_ERR_INVALID_ARG;
+  if (B == 0) return SV_OK;
+  if (!q || !k_pages || !v_pages || !k_scales || !v_scales || !block_table || !seq_lens ||
+      !k_new || !v_new || !out)
+    return SV_ERR_INVALID_ARG;
+  if (misaligned(q, 16) || misaligned(k_pages, 16) || misaligned(v_pages, 16) ||
+      misaligned(k_new, 16) || misaligned(v_new, 16) || misaligned(out, 16) ||
+      misaligned(block_table, 4) || misaligned(seq_lens, 4) || misaligned(parent, 4) ||
+      misaligned(dev_status, 4))
+    return SV_ERR_INVALID_ARG;
+  if (!workspace || misaligned(workspace, 256) ||
+      workspace_bytes < sv_attn_workspace_bytes(N, Hq, Hkv, D))
+    return SV_ERR_WORKSPACE;
+  AttnParams A = {};
+  A.kind = TREE;
+  A.table = block_table;
+  A.lens = seq_lens;
+  A.parent = parent;
+  A.out = static_cast<uint16_t*>(out);
+  A.status = dev_status;
+  A.k_scales = static_cast<const uint8_t*>(k_scales);
+  A.v_scales = static_cast<const uint8_t*>(v_scales);
+  A.k_new = static_cast<const uint16_t*>(k_new);
+  A.v_new = static_cast<const uint16_t*>(v_new);
+  A.block_log = block_log;
+  A.c = scale * LOG2E;
+  A.B = B; A.N = N; A.Hq = Hq; A.Hkv = Hkv; A.D = D;
+  A.LH = LH; A.head0 = head0; A.num_pages = num_pages; A.page = page_size; A.cols = cols;
+  return launch(A, dtype, q, k_pages, v_pages, nullptr, nullptr, workspace, stream);
 }
 
 int sv_ring_attn(int dtype, const void* q, const void* k_pool, const void* v_pool,

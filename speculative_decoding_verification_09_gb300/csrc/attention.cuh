@@ -48,12 +48,22 @@ constexpr int MAX_KEYS = 0x7fffffff - 1023;  // cache entries: a tile more fits 
 constexpr int ITEM_COST = 2;    // an item's fixed cost in tiles (1 to 3: within 2 %)
 constexpr int TILE = 128;       // query rows of a tile, and keys of a tile
 constexpr int THREADS = 384;    // two softmax warpgroups, and one with a copy and a product warp
+constexpr int THREADS8 = 512;   // and (8-bit caches) one that widens the keys and values
 // Registers: launched with 168 a thread (64512 a CTA); the softmax warpgroups
 // hold up to 128 scores a thread and take over what the third does not need.
 // (Ragged prompts: 107 us with 208 / 88, 101 with 216 / 72, 132 with 184 / 136.)
 constexpr int SOFTMAX_REGS = 216, OTHER_REGS = 72;
 static_assert(256 * SOFTMAX_REGS + 128 * OTHER_REGS <= THREADS * 168, "register split");
-constexpr int COPY_WARP = 8, MMA_WARP = 9, PLAN_WARP = 10;
+// With 8-bit caches the launch has 128 a thread (65536 a CTA), and a row per lane takes
+// more than few rows do.
+template <int NQ, bool Q8>
+struct Regs {
+  static constexpr int SOFTMAX = !Q8 ? SOFTMAX_REGS : NQ ? 144 : 200;
+  static constexpr int OTHER = !Q8 ? OTHER_REGS : NQ ? 72 : 56, WIDEN = NQ ? 128 : 56;
+  static_assert(!Q8 || 256 * SOFTMAX + 128 * OTHER + 128 * WIDEN <= THREADS8 * 128,
+                "register split");
+};
+constexpr int COPY_WARP = 8, MMA_WARP = 9, PLAN_WARP = 10, WIDEN_WARP = 12, WIDEN_WARPS = 4;
 constexpr int MAX_CTAS = 152;   // one per SM
 constexpr unsigned long long WAIT_LIMIT_NS = 1000000000ull;
 constexpr uint32_t SUSPEND_HINT_NS = 20000;
@@ -90,6 +100,12 @@ struct AttnParams {
   int whole_tiles;        // no item is cut when none has more tiles than this (TREE, RING)
   int join;               // and some may have, by the cache's extent
   int withhold;           // failure-handling test: CTA 0's second stage never fills
+  // 8-bit caches: the blocks' scales [num_pages][LH][page / block] and the staged entries
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  int block_log;          // log2 of the tokens of a block
 };
 
 __device__ __forceinline__ void set_status(int32_t* status, int bits) {
@@ -625,7 +641,10 @@ __device__ __forceinline__ uint32_t span(int a, int b, int k0) {
 //     of 128 dimensions, 207 us so and 215 with a row per lane, 32 rows 210 and 217;
 //     but 64 rows, for which a warp agrees on 64 maxima, 258 and 218.)
 constexpr int CTRL_BYTES = 3 * 1024;  // what 227 KB leave beside seven tiles of 32 KB
-template <int DP, int NQ>
+// 8-bit caches (Q8): tiles arrive as bytes in stages of their own, from which the widening
+// warps fill the 16-bit stages that the products read.  Few of those are enough, since
+// they are filled from shared memory; the bytes' stages cover the copies' latency.
+template <int DP, int NQ, bool Q8 = false>
 struct Smem {
   static constexpr int BYTES = TILE * DP * 2;                    // a tile of keys or values
   static constexpr int Q_BYTES = (NQ ? NQ : TILE) * DP * 2;      // a tile of queries
@@ -633,8 +652,12 @@ struct Smem {
   static constexpr int P_AT = 2 * Q_BYTES;
   static constexpr int STAGE_AT = P_AT + 2 * P_BYTES;
   static constexpr int FIT = (229376 - STAGE_AT) / BYTES;
-  static constexpr int STAGES = FIT < 12 ? FIT : 12;
-  static constexpr int CTRL = STAGE_AT + STAGES * BYTES;         // offset of the control part
+  static constexpr int STAGES = Q8 ? (DP == 64 ? 5 : NQ ? 4 : 3) : FIT < 12 ? FIT : 12;
+  static constexpr int RAW = TILE * DP;                          // a tile of bytes
+  static constexpr int RAW_AT = STAGE_AT + STAGES * BYTES;
+  static constexpr int RAW_FIT = (229376 - RAW_AT) / RAW;
+  static constexpr int RAWS = !Q8 ? 0 : RAW_FIT < 12 - STAGES ? RAW_FIT : 12 - STAGES;
+  static constexpr int CTRL = RAW_AT + RAWS * RAW;               // offset of the control part
   static constexpr int TOTAL = CTRL + CTRL_BYTES;
 };
 template <bool V>
@@ -658,7 +681,7 @@ struct Few {                   // NQ > 0, per stream and column
 };
 template <int NQ, bool PAIR>
 struct Ctrl {
-  // barriers: stages filled and free, queries, scores, weights (a pair's first half, all),
+  // barriers: stages filled and free (16-bit ones, then those of bytes), queries, scores, weights (a pair's first half, all),
   // output complete, segments planned and taken, the end after a wait gave up, another item
   unsigned long long full[12], empty[12], q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2],
       o_full[2], seg_full[SEGS], seg_empty[SEGS], drain, next_full;
@@ -670,7 +693,7 @@ struct Ctrl {
   uint8_t parent[2][NQ ? NQ : PAIR ? MAX_N : TILE];  // one copy per softmax warpgroup
   union {
     typename Either<NQ, Few<NQ>, Exchange<PAIR>>::T x;
-    struct { long long sum[THREADS / 32]; int most[THREADS / 32]; } scan;
+    struct { long long sum[THREADS8 / 32]; int most[THREADS8 / 32]; } scan;
   };
   unsigned long long out_at[NQ ? NQ : 1];  // NQ > 0: elements from an item's output to a column's
 };
@@ -842,6 +865,205 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Two e4m3 values of a word's half to 16 bits times the power of two in `f` (both halves).
+// fp16: the instruction's values are exact, and so are the products within the exponents
+// that the calls allow; a NaN stays one.
+__device__ __forceinline__ uint32_t widen_f16(uint16_t w, uint32_t f) {
+  uint32_t r;
+  asm("{\n .reg .b32 h;\n cvt.rn.f16x2.e4m3x2 h, %1;\n mul.rn.f16x2 %0, h, %2;\n}"
+      : "=r"(r)
+      : "h"(w), "r"(f));
+  return r;
+}
+// bf16: a byte's seven exponent and mantissa bits, four places up in the 16, are the value
+// times 2^-120 (subnormal ones too), so the factor has 2^120 more.  `seen` collects the
+// largest such bits: a NaN's, which are not one's here, are 0x7f0.
+__device__ __forceinline__ uint32_t widen_bf16(uint32_t w, bool upper, uint32_t f, uint32_t& seen) {
+  // each byte under eight copies of its sign
+  uint32_t h;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(h) : "r"(w), "r"(upper ? 0xb3a2u : 0x9180u));
+  const uint32_t bits = (h << 4) & 0x87f087f0u;
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(bits), "r"(f));
+  seen = __vmaxu2(seen, bits & 0x07f007f0u);
+  return r;
+}
+__device__ __forceinline__ uint32_t nan_of(uint32_t w, bool upper, uint32_t r) {
+  const uint32_t a = upper ? w >> 16 : w;
+  if ((a & 0x7f) == 0x7f) r = (r & 0xffff0000u) | 0x7fffu;
+  if ((a & 0x7f00) == 0x7f00) r = (r & 0xffffu) | 0x7fff0000u;
+  return r;
+}
+// A block's scale byte as the factor(s) of its values: bf16's second one is the part of 2^e
+// that does not fit beside 2^120.  Exponents whose values would not be exact: NaN.
+template <bool BF>
+__device__ __forceinline__ uint32_t factor_of(int byte, uint32_t& rest) {
+  const int e = byte - 127;
+  rest = 0x3f803f80u;  // 1
+  if (BF) {
+    if (e < -117 || e > 119) return 0x7fff7fffu;
+    const int a = min(e, 7);
+    rest = uint32_t(e - a + 127) << 7;
+    rest |= rest << 16;
+    const uint32_t f = uint32_t(a + 120 + 127) << 7;
+    return f | f << 16;
+  }
+  if (e < -15 || e > 7) return 0x7fff7fffu;
+  const uint32_t f = e < -14 ? 0x0200u : uint32_t(e + 15) << 10;  // (2^-15 is subnormal)
+  return f | f << 16;
+}
+
+// The widening warps: each tile of every segment in the order of the products, a quarter
+// of its rows' pieces per warp.  A thread takes 16 bytes (16 dimensions of a token) and
+// writes two 16-byte pieces of a 64-dimension block in the 128-byte swizzle; lanes of a
+// row's two blocks write their pieces in opposite order, so that eight lanes fall on
+// eight pieces.  Scales are read a tile ahead, their pages two.
+template <int DP, int NQ, bool PAIR, bool BF>
+__device__ __forceinline__ void widen_tiles(const AttnParams& A, Ctrl<NQ, PAIR>& C,
+                                            unsigned char* smem, volatile int* abort) {
+  using SM = Smem<DP, NQ, true>;
+  constexpr int STAGES = SM::STAGES, RAWS = SM::RAWS;
+  constexpr int PER_ROW = DP / 16;                       // pieces of a row
+  constexpr int STEPS = TILE * PER_ROW / (32 * WIDEN_WARPS);  // pieces of a thread
+  constexpr int ROWS = 32 * WIDEN_WARPS / PER_ROW;       // rows of a step
+  constexpr int BATCH = 2;
+  static_assert(STEPS % BATCH == 0, "whole rounds");
+  const int tid = int(threadIdx.x) - WIDEN_WARP * 32, lane = tid & 31;
+  const int row0 = tid / PER_ROW, piece = tid % PER_ROW;
+  uint32_t out = 0, in = 0;  // 16-bit stages filled, stages of bytes used up
+  bool ok = true;
+  for (int segs = 0;; ++segs) {
+    ok = warp_wait(smem_addr(&C.seg_full[segs % SEGS]), (segs / SEGS) & 1, A.status, abort);
+    if (!ok) break;
+    const Seg s = C.seg[segs % SEGS];
+    if (s.n == 0) break;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&C.seg_empty[segs % SEGS]));
+    const int blocks = TILE >> A.block_log, per_page = A.page >> A.block_log;
+    // the page of this lane's block of tile j (-1: none), and the scales there
+    auto place = [&](int j) {
+      const int t = j * TILE + (lane << A.block_log);
+      if (lane >= blocks || t >= s.len) return -1;
+      const int pg = __ldg(A.table + size_t(s.b) * A.cols + t / A.page);
+      return pg < 0 || pg >= A.num_pages ? 0 : pg;
+    };
+    auto scales = [&](int j, int pg, int& k, int& v) {
+      k = v = 127;
+      if (pg < 0) return;
+      const int t = j * TILE + (lane << A.block_log);
+      const size_t at = (size_t(pg) * A.LH + A.head0 + s.h) * per_page +
+                        ((t - t / A.page * A.page) >> A.block_log);
+      k = __ldg(A.k_scales + at);
+      v = __ldg(A.v_scales + at);
+    };
+    int k_now = 127, v_now = 127, k_next, v_next, v_before = 127;
+    scales(s.j0, place(s.j0), k_next, v_next);
+    int page_next = place(s.j0 + 1);
+    // (one copy of a tile's code for keys and values, its loops rolled)
+    constexpr int LAG = PAIR ? 0 : 1;
+#pragma unroll 1
+    for (int x = 0; x < 2 * (s.n + LAG); ++x) {
+      const bool is_v = x & 1;
+      const int i = x >> 1, jj = is_v ? i - LAG : i;
+      if (!is_v) {
+        v_before = v_now;
+        k_now = k_next;
+        v_now = v_next;
+        if (i < s.n) {
+          scales(s.j0 + i + 1, page_next, k_next, v_next);
+          page_next = place(s.j0 + i + 2);
+        }
+      }
+      if (jj < 0 || jj >= s.n) continue;
+      const int byte = !is_v ? k_now : PAIR ? v_now : v_before;
+      const Keys ky = keys_of<false>(A, s, s.j0 + jj);
+      const uint32_t st = out % STAGES, lap = out / STAGES;
+      unsigned char* const dst = smem + SM::STAGE_AT + st * SM::BYTES;
+      if (ky.staged) {
+        const uint16_t* const src =
+            (is_v ? A.v_new : A.k_new) +
+            ((size_t(s.b) * A.LH + A.head0 + s.h) * A.N + ky.k0) * A.D;
+        ok = warp_wait(smem_addr(&C.empty[st]), (lap & 1) ^ 1, A.status, abort);
+        if (!ok) break;
+#pragma unroll 1
+        for (int g = 0; g < STEPS; g += BATCH) {
+          uint4 u[2 * BATCH];
+#pragma unroll
+          for (int i = 0; i < 2 * BATCH; ++i) {
+            const int row = row0 + (g + i / 2) * ROWS, d = piece * 16 + (i & 1) * 8;
+            u[i] = make_uint4(0, 0, 0, 0);  // (rows behind the entries, and columns past D)
+            if (row < ky.n && d < A.D)
+              u[i] = __ldg(reinterpret_cast<const uint4*>(src + size_t(row) * A.D + d));
+          }
+#pragma unroll
+          for (int i = 0; i < 2 * BATCH; ++i) {
+            const int row = row0 + (g + i / 2) * ROWS, at = (piece & 3) * 2 + (i & 1);
+            *reinterpret_cast<uint4*>(dst + (piece >> 2) * 16384 + row * 128 +
+                                      ((at ^ (row & 7)) << 4)) = u[i];
+          }
+        }
+      } else {
+        const uint32_t rs = in % RAWS, rlap = in / RAWS;
+        const unsigned char* const src = smem + SM::RAW_AT + rs * SM::RAW + tid * 16;
+        uint32_t rest, factor = factor_of<BF>(byte, rest);
+        const bool large = BF && __any_sync(0xffffffffu, rest != 0x3f803f80u);
+        ok = warp_wait(smem_addr(&C.full[STAGES + rs]), rlap & 1, A.status, abort) &&
+             warp_wait(smem_addr(&C.empty[st]), (lap & 1) ^ 1, A.status, abort);
+        if (!ok) break;
+#pragma unroll 1
+        for (int g = 0; g < STEPS; g += BATCH) {
+          uint4 u[BATCH];
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i)
+            u[i] = *reinterpret_cast<const uint4*>(src + (g + i) * (32 * WIDEN_WARPS * 16));
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            const int row = row0 + (g + i) * ROWS;
+            const uint32_t f = __shfl_sync(0xffffffffu, factor, row >> A.block_log);
+            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+            uint32_t y[8];
+            if (BF) {
+              uint32_t seen = 0;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                y[2 * q] = widen_bf16(w[q], false, f, seen);
+                y[2 * q + 1] = widen_bf16(w[q], true, f, seen);
+              }
+              if (large) {
+                const uint32_t f2 = __shfl_sync(0xffffffffu, rest, row >> A.block_log);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(y[q]) : "r"(f2));
+              }
+              if ((seen & 0xffffu) == 0x7f0u || seen >> 16 == 0x7f0u) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) y[q] = nan_of(w[q / 2], q & 1, y[q]);
+              }
+            } else {
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                y[q] = widen_f16(uint16_t(w[q / 2] >> (q & 1 ? 16 : 0)), f);
+            }
+            const uint4 a = make_uint4(y[0], y[1], y[2], y[3]), b = make_uint4(y[4], y[5], y[6], y[7]);
+            unsigned char* const line = dst + (piece >> 2) * 16384 + row * 128;
+            const int at = (piece & 3) * 2, swap = piece >> 2;
+            *reinterpret_cast<uint4*>(line + (((at + swap) ^ (row & 7)) << 4)) = swap ? b : a;
+            *reinterpret_cast<uint4*>(line + (((at + 1 - swap) ^ (row & 7)) << 4)) = swap ? a : b;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&C.empty[STAGES + rs]));
+        ++in;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&C.full[st]));
+      ++out;
+    }
+    if (!ok) break;
+  }
+}
+
 // The attention kernel, one CTA per SM.  Warps:
 //   plan      the segments, a few ahead, with the loads and divisions they take
 //   copy      queries and key and value tiles by TMA into a ring of stages
@@ -852,10 +1074,16 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
 //             lanes: a maximum per column, agreed on by the warpgroup.
 // The weights are rounded once to the storage type (half a step each); their sum
 // l is taken before that, in 32 bits.
-template <int DP, int NQ, bool PAIR, bool PR, bool BF>
-__global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ AttnParams A) {
+// 8-bit caches (Q8) add
+//   widen     a warpgroup: cached tiles from bytes to 16 bits times their blocks' powers of
+//             two (exactly), staged ones from global memory, into the products' stages
+template <int DP, int NQ, bool PAIR, bool PR, bool BF, bool Q8 = false>
+__global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
+    sv_attn(const __grid_constant__ AttnParams A) {
   static_assert(!(NQ && (PAIR || PR)), "few rows make one tile, and prompts have many");
-  using SM = Smem<DP, NQ>;
+  static_assert(!(Q8 && PR), "8-bit entries are in pages");
+  using SM = Smem<DP, NQ, Q8>;
+  constexpr int NT = Q8 ? THREADS8 : THREADS;
   constexpr int STAGES = SM::STAGES, BYTES = SM::BYTES, HALVES = DP / 64;
   constexpr int ROWS = NQ ? NQ : PAIR ? 2 * TILE : TILE;
   constexpr int TM_COLS = NQ ? 256 : 512;               // TMEM: S of both streams, then O
@@ -870,9 +1098,15 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
   if (tid == 0) {
     for (int i = 0; i < STAGES; ++i) {
       // (withheld: one arrival too many, and every wait for that stage runs out)
-      mbar_init(bar(&C.full[i]), A.withhold && blockIdx.x == 0 && i == 1 ? 2 : 1);
+      const int arrivals = Q8 ? WIDEN_WARPS : 1;
+      mbar_init(bar(&C.full[i]), A.withhold && blockIdx.x == 0 && i == 1 ? arrivals + 1 : arrivals);
       mbar_init(bar(&C.empty[i]), 1);
     }
+    if (Q8)
+      for (int i = STAGES; i < STAGES + SM::RAWS; ++i) {
+        mbar_init(bar(&C.full[i]), 1);
+        mbar_init(bar(&C.empty[i]), WIDEN_WARPS);
+      }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(&C.q_full[i]), 1);
       mbar_init(bar(&C.q_empty[i]), 1);
@@ -883,7 +1117,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
     }
     for (int i = 0; i < SEGS; ++i) {
       mbar_init(bar(&C.seg_full[i]), 1);
-      mbar_init(bar(&C.seg_empty[i]), COPY_WARP + 2);  // every warp that reads it
+      mbar_init(bar(&C.seg_empty[i]), COPY_WARP + 2 + (Q8 ? WIDEN_WARPS : 0));  // its readers
     }
     mbar_init(bar(&C.drain), 1);
     mbar_init(bar(&C.next_full), 1);
@@ -904,7 +1138,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
   if (NQ) {
     if (tid < NQ) C.out_at[tid] = ((unsigned long long)(tid / A.G) * A.Hq + tid % A.G) * A.D;
     // columns past the item's rows: finite, and never used
-    for (int i = tid; i < SM::P_AT / 16; i += THREADS)
+    for (int i = tid; i < SM::P_AT / 16; i += NT)
       reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -912,7 +1146,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
   bool whole_items = false;
   if (!PR) {
     // thread t sums requests t * per .. of the batch
-    const int per = (A.B + THREADS - 1) / THREADS;
+    const int per = (A.B + NT - 1) / NT;
     const int b0 = min(tid * per, A.B), b1 = min(b0 + per, A.B);
     const long long items = (long long)A.MT * A.Hkv;
     long long mine = 0;
@@ -934,7 +1168,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
     }
     __syncthreads();
     long long total = 0, before = incl - mine;
-    for (int w = 0; w < THREADS / 32; ++w) {
+    for (int w = 0; w < NT / 32; ++w) {
       if (w < warp) before += C.scan.sum[w];
       total += C.scan.sum[w];
       most = max(most, C.scan.most[w]);
@@ -981,7 +1215,7 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
 
   if (warp < 8) {
     __syncwarp();
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<NQ, Q8>::SOFTMAX));
     // ------------------------------------------------------------ softmax
     const int st = warp >> 2;             // the stream of this warpgroup
     const int row = tid & (TILE - 1);     // query row of the tile, and key of a value tile
@@ -1527,9 +1761,17 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       ++segs;
     }
     if (!PR && A.join && tid == 0) A.desc[blockIdx.x] = make_int4(d_flags, d_item, d_b, 0);
+  } else if (Q8 && warp >= WIDEN_WARP) {
+    if constexpr (Q8) {
+      if constexpr (Regs<NQ, Q8>::WIDEN < 128) {
+        __syncwarp();
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<NQ, Q8>::WIDEN));
+      }
+      widen_tiles<DP, NQ, PAIR, BF>(A, C, smem, abort);
+    }
   } else {
     __syncwarp();
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<NQ, Q8>::OTHER));
   if (warp == PLAN_WARP) {
     // ------------------------------------------------------------ the plan
     Cursor<PAIR, PR> cur;
@@ -1602,6 +1844,9 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
   } else if (warp == COPY_WARP) {
     // ------------------------------------------------------------ copies
     // One thread, or (pages) a warp with a lane per box of page rows.
+    // COPIED stages, whose barriers begin at RAW0.
+    constexpr int RAW0 = Q8 ? STAGES : 0;
+    constexpr uint32_t COPIED = Q8 ? SM::RAWS : STAGES;
     auto copies = [&](auto solo) {
       constexpr bool SOLO = decltype(solo)::value;
       const bool lead = SOLO || lane == 0;
@@ -1639,10 +1884,11 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
         ++segs;
         const int plane = PR ? s.h : s.b * A.LH + A.head0 + s.h;
         auto tile = [&](int jj, bool is_v) {
-          const uint32_t fb = bar(&C.full[st]);
-          const uint32_t dst = base + SM::STAGE_AT + st * BYTES;
-          if (!wait(bar(&C.empty[st]), (lap & 1) ^ 1)) return false;
           const Keys ky = keys_of<PR>(A, s, s.j0 + jj);
+          if (Q8 && ky.staged) return true;  // (the widening warps')
+          const uint32_t fb = bar(&C.full[RAW0 + st]);
+          const uint32_t dst = base + (Q8 ? SM::RAW_AT + st * SM::RAW : SM::STAGE_AT + st * BYTES);
+          if (!wait(bar(&C.empty[RAW0 + st]), (lap & 1) ^ 1)) return false;
           if (SOLO || ky.staged) {
             if (lead) {
               const CUtensorMap* const m = !PR && ky.staged ? (is_v ? &A.mvn : &A.mkn)
@@ -1658,22 +1904,25 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
             // a page outside the pool is read as page 0 (the softmax warps report it
             // and drop the result)
             const int boxes = (ky.n + A.box - 1) / A.box;
-            if (lead) mbar_arrive_tx(fb, boxes * A.box * DP * 2);
+            if (lead) mbar_arrive_tx(fb, boxes * A.box * DP * (Q8 ? 1 : 2));
             __syncwarp();
             if (lane < boxes) {
               const int t = ky.k0 + lane * A.box;
               const int col = t / A.page;
               int pg = __ldg(A.table + size_t(s.b) * A.cols + col);
               if (pg < 0 || pg >= A.num_pages) pg = 0;
+              if (Q8)
+                tma_4d(dst + lane * A.box * DP, is_v ? &A.mv : &A.mk, fb, 0, t - col * A.page,
+                       A.head0 + s.h, pg);
 #pragma unroll
-              for (int x = 0; x < HALVES; ++x)
+              for (int x = 0; x < (Q8 ? 0 : HALVES); ++x)
                 tma_4d(dst + x * 16384 + lane * A.box * 128, is_v ? &A.mv : &A.mk, fb, x * 64,
                        t - col * A.page, A.head0 + s.h, pg);
             }
           }
           together();
           ++idx;
-          if (++st == STAGES) {
+          if (++st == COPIED) {
             st = 0;
             ++lap;
           }
@@ -1688,8 +1937,8 @@ __global__ void __launch_bounds__(THREADS, 1) sv_attn(const __grid_constant__ At
       }
       if (*abort) {  // the copies in flight land before the CTA ends
         const unsigned long long t0 = globaltimer();
-        for (uint32_t u = idx > STAGES ? idx - STAGES : 0; u < idx; ++u)
-          while (!mbar_try(bar(&C.full[u % STAGES]), (u / STAGES) & 1) &&
+        for (uint32_t u = idx > COPIED ? idx - COPIED : 0; u < idx; ++u)
+          while (!mbar_try(bar(&C.full[RAW0 + u % COPIED]), (u / COPIED) & 1) &&
                  globaltimer() - t0 < WAIT_LIMIT_NS) {
           }
         for (int u = max(0, segs - (PAIR ? 1 : 2)); u < segs; ++u)
@@ -1987,19 +2236,20 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) sv_attn_join(const __grid_con
 // Columns of the turned products, or 0 for a row per lane; rows of an item.
 struct Layout { int nq, rows; };
 
-template <int DP, int NQ, bool PAIR, bool PR, bool BF>
+template <int DP, int NQ, bool PAIR, bool PR, bool BF, bool Q8 = false>
 int launch_as(const AttnParams& A, int device, int grid, int ctas, cudaStream_t st) {
   // the kernel's shared-memory limit, raised once per device (ordinals past 63: every time)
   static std::atomic<uint64_t> raised{0};
   const uint64_t mark = device < 64 ? uint64_t(1) << device : 0;
   if (!(raised.load(std::memory_order_acquire) & mark)) {
-    if (cudaFuncSetAttribute(sv_attn<DP, NQ, PAIR, PR, BF>,
+    if (cudaFuncSetAttribute(sv_attn<DP, NQ, PAIR, PR, BF, Q8>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (Smem<DP, NQ>::TOTAL)) != cudaSuccess)
+                             (Smem<DP, NQ, Q8>::TOTAL)) != cudaSuccess)
       return SV_ERR_CUDA;
     raised.fetch_or(mark, std::memory_order_release);
   }
-  sv_attn<DP, NQ, PAIR, PR, BF><<<grid, THREADS, (Smem<DP, NQ>::TOTAL), st>>>(A);
+  sv_attn<DP, NQ, PAIR, PR, BF, Q8>
+      <<<grid, Q8 ? THREADS8 : THREADS, (Smem<DP, NQ, Q8>::TOTAL), st>>>(A);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
   if (PR || !A.join) return SV_OK;
   cudaLaunchConfig_t cfg = {};
@@ -2026,10 +2276,21 @@ int launch_dp(const AttnParams& A, Layout l, int device, int grid, int ctas, cud
   return launch_as<DP, 0, true, false, BF>(A, device, grid, ctas, st);
 }
 
-// One translation unit per storage type (attn_bf16.cu, attn_f16.cu), compiled
-// side by side.
+// The same over an 8-bit cache.
+template <int DP, bool BF>
+int launch_dp8(const AttnParams& A, Layout l, int device, int grid, int ctas, cudaStream_t st) {
+  if (l.nq == 16) return launch_as<DP, 16, false, false, BF, true>(A, device, grid, ctas, st);
+  if (l.nq == 32) return launch_as<DP, 32, false, false, BF, true>(A, device, grid, ctas, st);
+  if (l.rows == TILE) return launch_as<DP, 0, false, false, BF, true>(A, device, grid, ctas, st);
+  return launch_as<DP, 0, true, false, BF, true>(A, device, grid, ctas, st);
+}
+
+// One translation unit per storage type and cache (attn_bf16.cu, attn_f16.cu, attn8_bf16.cu,
+// attn8_f16.cu), compiled side by side.
 int launch_bf16(const AttnParams& A, Layout l, int device, int grid, int ctas, cudaStream_t st);
 int launch_f16(const AttnParams& A, Layout l, int device, int grid, int ctas, cudaStream_t st);
+int launch8_bf16(const AttnParams& A, Layout l, int device, int grid, int ctas, cudaStream_t st);
+int launch8_f16(const AttnParams& A, Layout l, int device, int grid, int ctas, cudaStream_t st);
 
 }  // namespace svattn
 

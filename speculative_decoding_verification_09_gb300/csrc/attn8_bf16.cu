@@ -1,0 +1,9 @@
+// attn8_bf16.cu -- the attention kernels of attention.cuh over 8-bit caches, for bfloat16 queries.
+
+#include "attention.cuh"
+
+int svattn::launch8_bf16(const AttnParams& A, Layout l, int device, int grid, int ctas,
+                         cudaStream_t st) {
+  return A.D > 64 ? launch_dp8<128, true>(A, l, device, grid, ctas, st)
+                  : launch_dp8<64, true>(A, l, device, grid, ctas, st);
+}
