@@ -35,13 +35,13 @@ EncodeTiled encode_tiled() {
 
 // A map of 8-bit elements: dims[0] innermost, strides of dims 1.. in elements.
 bool make_map8(CUtensorMap* m, const void* p, int rank, const uint64_t* dims,
-               const uint64_t* strides, const uint32_t* box) {
+               const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
   cuuint64_t bytes[4];
   cuuint32_t one[5] = {1, 1, 1, 1, 1};
   for (int i = 0; i + 1 < rank; ++i) bytes[i] = strides[i];
   return encode_tiled()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, cuuint32_t(rank), const_cast<void*>(p),
                         dims, bytes, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -84,7 +84,7 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
   A.G = A.Hq / A.Hkv;
   A.tpt = TILE / A.G;
   A.withhold = g_withhold;
-  if (dtype == SV_F16) {
+  if (dtype == SV_F16 || A.k_scales) {  // (weights in fp16)
     // the keys that a row may see, times a weight's error of 2^-(25 + lift): below 2^-11
     const long long window = (long long)A.sink + A.window;
     const long long keys = A.kind == TREE   ? (long long)A.cols * A.page + A.N
@@ -92,13 +92,15 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
                                             : (window < A.T ? window : A.T);
     int lift = 0;
     while (lift < MOST_LIFT && keys >> (14 + lift)) ++lift;
+    if (A.k_scales) lift = lift + VALUE_SLACK < MOST_LIFT ? lift + VALUE_SLACK : MOST_LIFT;
     A.lift = float(lift);
   }
   const uint64_t D = A.D, tokens = A.kind == PROMPT ? uint64_t(A.T) : uint64_t(A.B) * A.N;
   const uint32_t q_tok = uint32_t(
       A.tpt < (A.kind == PROMPT ? A.T : A.N) ? A.tpt : (A.kind == PROMPT ? A.T : A.N));
   A.q_rows = int(q_tok) * A.G;
-  {
+  A.q = static_cast<const uint16_t*>(q);
+  if (!A.k_scales) {
     const uint64_t dims[4] = {D, uint64_t(A.G), uint64_t(A.Hkv), tokens};
     const uint64_t str[3] = {D, D * A.G, D * A.Hq};
     const uint32_t box[4] = {64, uint32_t(A.G), 1, q_tok};
@@ -110,7 +112,10 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
     const uint64_t dims[4] = {D, uint64_t(A.page), uint64_t(A.LH), uint64_t(A.num_pages)};
     const uint64_t str[3] = {D, D * A.page, D * A.page * A.LH};
     const uint32_t box[4] = {A.k_scales ? (A.D > 64 ? 128u : 64u) : 64u, uint32_t(A.box), 1, 1};
-    if (A.k_scales ? !make_map8(&A.mk, k, 4, dims, str, box) || !make_map8(&A.mv, v, 4, dims, str, box)
+    // (keys go to products as they are; values are read by threads)
+    if (A.k_scales ? !make_map8(&A.mk, k, 4, dims, str, box,
+                                A.D > 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
+                         !make_map8(&A.mv, v, 4, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE)
                    : !make_map(&A.mk, dtype, k, 4, dims, str, box) ||
                          !make_map(&A.mv, dtype, v, 4, dims, str, box))
       return SV_ERR_CUDA;

@@ -58,12 +58,13 @@ static_assert(256 * SOFTMAX_REGS + 128 * OTHER_REGS <= THREADS * 168, "register 
 // more than few rows do.
 template <int NQ, bool Q8>
 struct Regs {
-  static constexpr int SOFTMAX = !Q8 ? SOFTMAX_REGS : NQ ? 144 : 200;
-  static constexpr int OTHER = !Q8 ? OTHER_REGS : NQ ? 72 : 56, WIDEN = NQ ? 128 : 56;
+  static constexpr int SOFTMAX = !Q8 ? SOFTMAX_REGS : NQ ? 144 : 192;
+  static constexpr int OTHER = !Q8 ? OTHER_REGS : NQ ? 72 : 56, WIDEN = NQ ? 128 : 72;
   static_assert(!Q8 || 256 * SOFTMAX + 128 * OTHER + 128 * WIDEN <= THREADS8 * 128,
                 "register split");
 };
-constexpr int COPY_WARP = 8, MMA_WARP = 9, PLAN_WARP = 10, WIDEN_WARP = 12, WIDEN_WARPS = 4;
+constexpr int COPY_WARP = 8, MMA_WARP = 9, PLAN_WARP = 10, SCALE_WARP = 11, WIDEN_WARP = 12,
+              WIDEN_WARPS = 4;
 constexpr int MAX_CTAS = 152;   // one per SM
 constexpr unsigned long long WAIT_LIMIT_NS = 1000000000ull;
 constexpr uint32_t SUSPEND_HINT_NS = 20000;
@@ -77,6 +78,9 @@ constexpr uint32_t SUSPEND_HINT_NS = 20000;
 // type.  (Ragged prompts: 89.6 us with 0 and 14, 90.1 with 4 and 15, 93.0 with 8 and 15.)
 constexpr float MOST_BF16 = 14.0f, MOST_F16 = 15.0f;
 constexpr int MOST_LIFT = 14;
+// 8-bit caches: the values' powers of two count relative to 2^VALUE_SLACK times the largest, so
+// that O need not be rescaled for the next tile's somewhat larger one; the lift makes up for it.
+constexpr int VALUE_SLACK = 2;
 
 struct AttnParams {
   CUtensorMap mq, mk, mv, mkn, mvn;  // queries, cache (or prompt) K and V, staged K and V
@@ -99,8 +103,10 @@ struct AttnParams {
   int MT;                 // items per KV head (TREE, RING)
   int whole_tiles;        // no item is cut when none has more tiles than this (TREE, RING)
   int join;               // and some may have, by the cache's extent
-  int withhold;           // failure-handling test: CTA 0's second stage never fills
-  // 8-bit caches: the blocks' scales [num_pages][LH][page / block] and the staged entries
+  int withhold;           // failure-handling test: one of CTA 0's stages never fills
+  // 8-bit caches: the queries, the blocks' scales [num_pages][LH][page / block] and the staged
+  // entries
+  const uint16_t* q;
   const uint8_t* k_scales;
   const uint8_t* v_scales;
   const uint16_t* k_new;
@@ -253,6 +259,22 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
       "r"(idesc), "r"(accumulate), "n"(DESC_HI)
       : "memory");
 }
+// Products of 8-bit operands (e4m3), K-major tiles of DP bytes a row in the swizzle of that
+// width; 32 dimensions a product.
+template <int DP>
+__device__ __forceinline__ void mma8_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+  constexpr uint32_t HI = DP == 128 ? DESC_HI : (512 >> 4) | (1u << 14) | (4u << 29);
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.u32 p, %4, 0;\n"
+      " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n}" ::"r"(d), "r"(a), "r"(b),
+      "r"(idesc), "r"(accumulate), "n"(HI)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t instr_desc8(int n) {  // 32-bit sums
+  return (1u << 4) | (uint32_t(n >> 3) << 17) | (uint32_t(TILE >> 4) << 24);
+}
 // One lane of the (converged) warp: the form in which the compiler knows that a
 // single thread issues, and keeps the products' descriptors in uniform registers.
 __device__ __forceinline__ bool elect_one() {
@@ -389,6 +411,14 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       " mov.b64 c, {%6, %7};\n fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
@@ -620,6 +650,24 @@ __device__ __forceinline__ int v_order(int j, int n) {
   return PAIR ? 2 * j + 1 : (j < n - 1 ? 2 * j + 2 : 2 * n - 1);
 }
 
+// 8-bit caches: the order is K_0 .. V_(i - LAG) K_i .. there, too.  Bytes have a ring for keys
+// and one for values; the 16-bit ring has all values of a segment of n tiles, c of them
+// cached, and `parts` stages with the terms of each staged tile's keys.
+template <bool PAIR>
+constexpr int LAG8 = PAIR ? 0 : 1;
+template <bool PAIR>
+__device__ __forceinline__ int wide_k(int i, int c, int parts) {
+  return parts * (i - c) + max(0, i - LAG8<PAIR>);
+}
+template <bool PAIR>
+__device__ __forceinline__ int wide_v(int j, int n, int c, int parts) {
+  return j + parts * max(0, min(j + LAG8<PAIR>, n - 1) - c + 1);
+}
+// The cached tiles of a segment.
+__device__ __forceinline__ int cached_of(const Seg& s) {
+  return min(max(tiles_of(s.len) - s.j0, 0), s.n);
+}
+
 // Bits a .. b - 1 of the 32 keys from k0 on.
 __device__ __forceinline__ uint32_t span(int a, int b, int k0) {
   a = max(a - k0, 0);
@@ -641,24 +689,36 @@ __device__ __forceinline__ uint32_t span(int a, int b, int k0) {
 //     of 128 dimensions, 207 us so and 215 with a row per lane, 32 rows 210 and 217;
 //     but 64 rows, for which a warp agrees on 64 maxima, 258 and 218.)
 constexpr int CTRL_BYTES = 3 * 1024;  // what 227 KB leave beside seven tiles of 32 KB
-// 8-bit caches (Q8): tiles arrive as bytes in stages of their own, from which the widening
-// warps fill the 16-bit stages that the products read.  Few of those are enough, since
-// they are filled from shared memory; the bytes' stages cover the copies' latency.
-template <int DP, int NQ, bool Q8 = false>
+constexpr int CTRL8_BYTES = 4864;  // more of it with 8-bit caches
+// 8-bit caches (Q8).  Keys stay bytes: scores are products of e4m3 with e4m3, the queries
+// split into TERMS such terms whose sum is theirs exactly (4 bits of a mantissa each; see
+// split_terms).  Values arrive as bytes, too, and the widening warps fill the 16-bit stages
+// that their products read, as fp16 whatever the queries are: every e4m3 value is one, by one
+// instruction for two.  Their powers of two go to the weights, which are fp16 then, relative
+// to the largest of them so far.  Few 16-bit stages are enough, since they are filled from
+// shared memory; the bytes' stages cover the copies' latency.
+template <bool BF>
+constexpr int TERMS_OF = BF ? 2 : 3;
+template <int DP, int NQ, int TERMS = 0>  // TERMS: 0 for 16-bit caches
 struct Smem {
+  static constexpr bool Q8 = TERMS > 0;
   static constexpr int BYTES = TILE * DP * 2;                    // a tile of keys or values
-  static constexpr int Q_BYTES = (NQ ? NQ : TILE) * DP * 2;      // a tile of queries
+  static constexpr int TERM = (NQ ? NQ : TILE) * DP;             // a term of a tile of queries
+  static constexpr int Q_BYTES = TERM * (Q8 ? TERMS : 2);        // a tile of queries
   static constexpr int P_BYTES = NQ * TILE * 2;                  // weights of a stream (NQ > 0)
   static constexpr int P_AT = 2 * Q_BYTES;
   static constexpr int STAGE_AT = P_AT + 2 * P_BYTES;
-  static constexpr int FIT = (229376 - STAGE_AT) / BYTES;
-  static constexpr int STAGES = Q8 ? (DP == 64 ? 5 : NQ ? 4 : 3) : FIT < 12 ? FIT : 12;
+  static constexpr int ROOM = 232448 - CTRL_BYTES - (Q8 ? CTRL8_BYTES : 0);
+  static constexpr int FIT = (ROOM - STAGE_AT) / BYTES;
+  static constexpr int STAGES = Q8 ? (DP == 128 && NQ == 0 ? 2 : 3) : FIT < 12 ? FIT : 12;
   static constexpr int RAW = TILE * DP;                          // a tile of bytes
   static constexpr int RAW_AT = STAGE_AT + STAGES * BYTES;
-  static constexpr int RAW_FIT = (229376 - RAW_AT) / RAW;
+  static constexpr int RAW_FIT = (ROOM - RAW_AT) / RAW;
   static constexpr int RAWS = !Q8 ? 0 : RAW_FIT < 12 - STAGES ? RAW_FIT : 12 - STAGES;
+  static constexpr int RAW_K = (RAWS + 1) / 2, RAW_V = RAWS / 2;  // keys' stages, then values'
   static constexpr int CTRL = RAW_AT + RAWS * RAW;               // offset of the control part
-  static constexpr int TOTAL = CTRL + CTRL_BYTES;
+  static constexpr int TOTAL = CTRL + CTRL_BYTES + (Q8 ? CTRL8_BYTES : 0);
+  static_assert(!Q8 || RAWS >= 3, "bytes on their way");
 };
 template <bool V>
 struct Yes { static constexpr bool value = V; };
@@ -700,6 +760,36 @@ struct Ctrl {
 static_assert(sizeof(Ctrl<0, true>) <= CTRL_BYTES && sizeof(Ctrl<0, false>) <= CTRL_BYTES &&
                   sizeof(Ctrl<16, false>) <= CTRL_BYTES && sizeof(Ctrl<32, false>) <= CTRL_BYTES,
               "control part");
+
+// The control part's rest with 8-bit caches.  A tile's powers of two, eight keys at a time:
+// of the keys, 2^ek; of the values, ev less the tile's largest, and 2^ that (NQ > 0) or one
+// over it (a row per lane).  They are kept above -30: what they would take from a weight
+// further down is 2^-30 of the largest value at most.
+struct Tile8 {
+  alignas(16) float kf[16];
+  float vd[16], vf[16];
+  int top;        // the values' largest exponent
+  int count;      // staged tiles: warps that have written their eights of keys,
+  int8_t ev[16];  // and the exponents of these keys' values
+};
+constexpr int SCALES = 8;        // cached tiles whose scales are read ahead
+constexpr int LEAST = -30;
+template <int NQ>
+struct Ctrl8 {
+  unsigned long long full[SCALES], empty[SCALES];
+  Tile8 tile[SCALES], staged[SEGS][2];
+  // powers of two of the queries' rows: floats of the columns, or exponent bytes
+  alignas(16) float qf[SEGS][NQ ? NQ : 1];
+  uint8_t qx[SEGS][NQ ? 1 : 2 * TILE];
+  int kept[2];                     // at a segment's end, per stream
+  float lost[2];
+};
+static_assert(sizeof(Ctrl8<0>) <= CTRL8_BYTES && sizeof(Ctrl8<32>) <= CTRL8_BYTES, "control part");
+// 2^(byte - 127); 255: NaN
+__device__ __forceinline__ float power_of(uint32_t byte) {
+  return __uint_as_float(byte == 255 ? 0x7fffffffu : byte << 23);
+}
+__device__ __forceinline__ float power(int e) { return __int_as_float((e + 127) << 23); }
 
 // desc[cta]: x = flags, y = item (of its request) and z = request of the first segment
 constexpr int DESC_THROUGH = 1 << 29;  // the first segment starts inside its item and runs to
@@ -758,13 +848,27 @@ __device__ __forceinline__ void sum_columns(float* v, int lane) {
 // 64-key blocks in the 128-byte swizzle).  `sees`: the columns that see the
 // key.  All keys of a tile use one maximum per column; it is raised, the sums
 // and O (columns from to) rescaled, when a weight would exceed 2^most.
-template <int NQ, bool BF>
+// Q8: the scores are taken in base-2 units, times the powers of two of the key (t8) and of the
+// columns (qf); the weights stored, but not their sums, times the value's, relative to
+// 2^top, and `sink` has what O is multiplied by when that rises.
+template <int NQ, bool BF, bool Q8>
 __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>& C, int st,
                                             int key, uint32_t ts, uint32_t to, uint32_t sees,
                                             bool masked, bool started, bool& unset, float* lq,
-                                            unsigned char* pbuf) {
-  constexpr float MOST = BF ? MOST_BF16 : MOST_F16;
-  const float lift = BF ? 0.0f : A.lift;
+                                            unsigned char* pbuf, const Tile8* t8, const float* qf,
+                                            int& top) {
+  constexpr bool HALF = Q8 || !BF;  // the weights' type
+  constexpr float MOST = HALF ? MOST_F16 : MOST_BF16;
+  const float lift = HALF ? A.lift : 0.0f, unit = Q8 ? 1.0f : A.c;
+  const float kc = Q8 ? A.c * t8->kf[key >> 3] : 0.0f;
+  float sink = 1.0f, vf = 1.0f;
+  if (Q8) {
+    if (!started || t8->top > top) {
+      if (started) sink = power(max(top - (t8->top + VALUE_SLACK), -126));
+      top = t8->top + VALUE_SLACK;
+    }
+    vf = t8->vf[key >> 3] * power(max(t8->top - top, LEAST));
+  }
   const int lane = key & 31, warp = key >> 5;
   float* const nmc = C.x.nmc[st];
   const float2 c2 = make_float2(A.c, A.c);
@@ -772,6 +876,21 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
   auto load = [&] {
     tm_ldn<NQ>(ts, r);
     tm_waitn<NQ>(r);
+    if (Q8) {
+      const float2 k2 = make_float2(kc, kc);
+#pragma unroll
+      for (int q = 0; q < NQ; q += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(qf + q);
+        const float2 a = mul2(make_float2(__uint_as_float(r[q]), __uint_as_float(r[q + 1])),
+                              mul2(make_float2(f.x, f.y), k2));
+        const float2 b = mul2(make_float2(__uint_as_float(r[q + 2]), __uint_as_float(r[q + 3])),
+                              mul2(make_float2(f.z, f.w), k2));
+        r[q] = __float_as_uint(a.x);
+        r[q + 1] = __float_as_uint(a.y);
+        r[q + 2] = __float_as_uint(b.x);
+        r[q + 3] = __float_as_uint(b.y);
+      }
+    }
     if (masked) {
 #pragma unroll
       for (int q = 0; q < NQ; ++q)
@@ -784,11 +903,10 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
 #pragma unroll
     for (int q = 0; q < NQ; q += 4) {
       const float4 n = *reinterpret_cast<const float4*>(nmc + q);
-      const float2 a = fma2(make_float2(__uint_as_float(r[q]), __uint_as_float(r[q + 1])),
-                            c2, make_float2(n.x, n.y));
-      const float2 b =
-          fma2(make_float2(__uint_as_float(r[q + 2]), __uint_as_float(r[q + 3])), c2,
-               make_float2(n.z, n.w));
+      const float2 u = make_float2(__uint_as_float(r[q]), __uint_as_float(r[q + 1]));
+      const float2 v = make_float2(__uint_as_float(r[q + 2]), __uint_as_float(r[q + 3]));
+      const float2 a = Q8 ? add2(u, make_float2(n.x, n.y)) : fma2(u, c2, make_float2(n.x, n.y));
+      const float2 b = Q8 ? add2(v, make_float2(n.z, n.w)) : fma2(v, c2, make_float2(n.z, n.w));
       r[q] = __float_as_uint(a.x);
       r[q + 1] = __float_as_uint(a.y);
       r[q + 2] = __float_as_uint(b.x);
@@ -798,7 +916,7 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
     return over;
   };
   load();
-  bool raise = !started || unset;
+  bool raise = !started || unset || sink != 1.0f;
   if (!raise) {
     raise = group_or(1 + st, TILE, exponents() > MOST);
     __syncwarp();
@@ -818,7 +936,7 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
     int none = 0;
     if (key < NQ) {
       const float t = fmaxf(fmaxf(wmax[key], wmax[NQ + key]),
-                            fmaxf(wmax[2 * NQ + key], wmax[3 * NQ + key])) * A.c;
+                            fmaxf(wmax[2 * NQ + key], wmax[3 * NQ + key])) * unit;
       float old = started ? -nmc[key] : INFINITY, f = 1.0f;
       if (old == INFINITY) {
         if (t > -INFINITY) old = t - lift;
@@ -840,7 +958,7 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
       tm_waitn<NQ>(o);
 #pragma unroll
       for (int q = 0; q < NQ; ++q)
-        o[q] = __float_as_uint(__uint_as_float(o[q]) * C.x.fac[st][q]);
+        o[q] = __float_as_uint(__uint_as_float(o[q]) * (C.x.fac[st][q] * sink));
       tm_stn<NQ>(to, o);
       tm_wait_st();
     }
@@ -857,7 +975,8 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
     const float2 l = add2(make_float2(lq[q], lq[q + 1]), p);
     lq[q] = l.x;
     lq[q + 1] = l.y;
-    const uint32_t w = pack16<BF>(p.x, p.y);
+    const float2 y = Q8 ? mul2(p, make_float2(vf, vf)) : p;
+    const uint32_t w = pack16<!HALF>(y.x, y.y);
     *reinterpret_cast<uint16_t*>(prow + q * 128 + ((piece ^ (q & 7)) << 4)) = uint16_t(w);
     *reinterpret_cast<uint16_t*>(prow + (q + 1) * 128 + ((piece ^ ((q + 1) & 7)) << 4)) =
         uint16_t(w >> 16);
@@ -865,202 +984,366 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Two e4m3 values of a word's half to 16 bits times the power of two in `f` (both halves).
-// fp16: the instruction's values are exact, and so are the products within the exponents
-// that the calls allow; a NaN stays one.
-__device__ __forceinline__ uint32_t widen_f16(uint16_t w, uint32_t f) {
-  uint32_t r;
-  asm("{\n .reg .b32 h;\n cvt.rn.f16x2.e4m3x2 h, %1;\n mul.rn.f16x2 %0, h, %2;\n}"
-      : "=r"(r)
-      : "h"(w), "r"(f));
+// Four e4m3 values to fp16, exactly; a NaN stays one.
+__device__ __forceinline__ uint2 widen4(uint32_t w) {
+  uint2 r;
+  asm("{\n .reg .b16 u, v;\n mov.b32 {u, v}, %2;\n"
+      " cvt.rn.f16x2.e4m3x2 %0, u;\n cvt.rn.f16x2.e4m3x2 %1, v;\n}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(w));
   return r;
-}
-// bf16: a byte's seven exponent and mantissa bits, four places up in the 16, are the value
-// times 2^-120 (subnormal ones too), so the factor has 2^120 more.  `seen` collects the
-// largest such bits: a NaN's, which are not one's here, are 0x7f0.
-__device__ __forceinline__ uint32_t widen_bf16(uint32_t w, bool upper, uint32_t f, uint32_t& seen) {
-  // each byte under eight copies of its sign
-  uint32_t h;
-  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(h) : "r"(w), "r"(upper ? 0xb3a2u : 0x9180u));
-  const uint32_t bits = (h << 4) & 0x87f087f0u;
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(bits), "r"(f));
-  seen = __vmaxu2(seen, bits & 0x07f007f0u);
-  return r;
-}
-__device__ __forceinline__ uint32_t nan_of(uint32_t w, bool upper, uint32_t r) {
-  const uint32_t a = upper ? w >> 16 : w;
-  if ((a & 0x7f) == 0x7f) r = (r & 0xffff0000u) | 0x7fffu;
-  if ((a & 0x7f00) == 0x7f00) r = (r & 0xffffu) | 0x7fff0000u;
-  return r;
-}
-// A block's scale byte as the factor(s) of its values: bf16's second one is the part of 2^e
-// that does not fit beside 2^120.  Exponents whose values would not be exact: NaN.
-template <bool BF>
-__device__ __forceinline__ uint32_t factor_of(int byte, uint32_t& rest) {
-  const int e = byte - 127;
-  rest = 0x3f803f80u;  // 1
-  if (BF) {
-    if (e < -117 || e > 119) return 0x7fff7fffu;
-    const int a = min(e, 7);
-    rest = uint32_t(e - a + 127) << 7;
-    rest |= rest << 16;
-    const uint32_t f = uint32_t(a + 120 + 127) << 7;
-    return f | f << 16;
-  }
-  if (e < -15 || e > 7) return 0x7fff7fffu;
-  const uint32_t f = e < -14 ? 0x0200u : uint32_t(e + 15) << 10;  // (2^-15 is subnormal)
-  return f | f << 16;
 }
 
-// The widening warps: each tile of every segment in the order of the products, a quarter
-// of its rows' pieces per warp.  A thread takes 16 bytes (16 dimensions of a token) and
-// writes two 16-byte pieces of a 64-dimension block in the 128-byte swizzle; lanes of a
-// row's two blocks write their pieces in opposite order, so that eight lanes fall on
-// eight pieces.  Scales are read a tile ahead, their pages two.
+// A value's terms in e4m3: x = t1 + t2 (+ t3), each the rest rounded to nearest (16 values of
+// a thread, 16 bytes a term).  A rounding leaves at most 1/16 of a value, and of 8 bits of a
+// mantissa (bf16) what is left has at most 4, so two terms are exact, of 11 (fp16) three; but
+// for what falls below the format's last step, 2^-9 where the largest value of the rows that
+// share a power of two is 224 or more: 2^-18 of that value, less than the rounding of the
+// sums of 32-bit products.  What is not finite is NaN in the first term.
+template <int TERMS>
+__device__ __forceinline__ void split_terms(float (&x)[16], float by, uint4 (&out)[TERMS]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = fabsf(x[i]) < INFINITY ? x[i] * by : __int_as_float(0x7fffffff);
+#pragma unroll
+  for (int t = 0; t < TERMS; ++t) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint16_t p[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float& a = x[4 * i + 2 * k];
+        float& b = x[4 * i + 2 * k + 1];
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p[k]) : "f"(b), "f"(a));
+        if (t + 1 < TERMS) {
+          uint32_t h;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(p[k]));
+          float lo, hi;
+          asm("{\n .reg .b16 u, v;\n mov.b32 {u, v}, %2;\n cvt.f32.f16 %0, u;\n cvt.f32.f16 %1, v;\n}"
+              : "=f"(lo), "=f"(hi)
+              : "r"(h));
+          a -= lo;
+          b -= hi;
+        }
+      }
+      w[i] = uint32_t(p[0]) | uint32_t(p[1]) << 16;
+    }
+    out[t] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+// Sixteen 16-bit values in 32 bits, and the largest finite size among them, as bits.
+template <bool BF>
+__device__ __forceinline__ uint32_t widen16(const uint4 (&u)[2], float (&x)[16]) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint4& q = u[i / 4];
+    const uint32_t w = i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w;
+    if (BF) {
+      x[2 * i] = __uint_as_float(w << 16);
+      x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+    } else {
+      asm("{\n .reg .b16 u, v;\n mov.b32 {u, v}, %2;\n cvt.f32.f16 %0, u;\n cvt.f32.f16 %1, v;\n}"
+          : "=f"(x[2 * i]), "=f"(x[2 * i + 1])
+          : "r"(w));
+    }
+#pragma unroll
+    for (int k = 2 * i; k < 2 * i + 2; ++k) {
+      const uint32_t a = __float_as_uint(x[k]) & 0x7fffffffu;
+      if (a < 0x7f800000u) most = max(most, a);
+    }
+  }
+  return most;
+}
+// The smallest e with a <= 448 * 2^e (a finite size's bits), kept in the bytes' range.
+__device__ __forceinline__ int exponent_over(uint32_t a) {
+  const int e = int(a >> 23) - 127 - 8 + ((a & 0x7fffff) > 0x600000);
+  return min(max(e, -117), 119);
+}
+// The 16-byte piece of a row of DP bytes where products of bytes look for piece p.
+template <int DP>
+__device__ __forceinline__ int swizzled(int row, int p) {
+  return DP == 128 ? row * 128 + ((p ^ (row & 7)) << 4) : row * 64 + ((p ^ (row >> 1 & 3)) << 4);
+}
+
+// The widening warps, per segment: the queries' terms; then, in the order of the products,
+// the cached tiles' values from bytes to 16 bits (a thread takes 16 bytes, 16 dimensions of
+// a token, and writes two 16-byte pieces of a 64-dimension block in the 128-byte swizzle;
+// lanes of a row's two blocks write their pieces in opposite order, so that eight lanes
+// fall on eight pieces), the staged tiles' keys as terms, and their values.
+// One copy of each piece of code, loops rolled: much of it runs once a segment, and the
+// rest is bound by fetching instructions when it is longer.
 template <int DP, int NQ, bool PAIR, bool BF>
-__device__ __forceinline__ void widen_tiles(const AttnParams& A, Ctrl<NQ, PAIR>& C,
+__device__ __forceinline__ void widen_tiles(const AttnParams& A, Ctrl<NQ, PAIR>& C, Ctrl8<NQ>& C8,
                                             unsigned char* smem, volatile int* abort) {
-  using SM = Smem<DP, NQ, true>;
-  constexpr int STAGES = SM::STAGES, RAWS = SM::RAWS;
-  constexpr int PER_ROW = DP / 16;                       // pieces of a row
+  constexpr int TERMS = TERMS_OF<BF>, PARTS = (TERMS + 1) / 2, LAG = LAG8<PAIR>;
+  using SM = Smem<DP, NQ, TERMS>;
+  constexpr int STAGES = SM::STAGES;
+  constexpr int PER_ROW = DP / 16;                            // pieces of a row
   constexpr int STEPS = TILE * PER_ROW / (32 * WIDEN_WARPS);  // pieces of a thread
-  constexpr int ROWS = 32 * WIDEN_WARPS / PER_ROW;       // rows of a step
-  constexpr int BATCH = 2;
+  constexpr int ROWS = 32 * WIDEN_WARPS / PER_ROW;            // rows of a step
+  constexpr int BATCH = 4;
+  constexpr int Q_ROWS = NQ ? NQ : TILE;
   static_assert(STEPS % BATCH == 0, "whole rounds");
-  const int tid = int(threadIdx.x) - WIDEN_WARP * 32, lane = tid & 31;
+  const int tid = int(threadIdx.x) - WIDEN_WARP * 32, warp = tid >> 5, lane = tid & 31;
   const int row0 = tid / PER_ROW, piece = tid % PER_ROW;
-  uint32_t out = 0, in = 0;  // 16-bit stages filled, stages of bytes used up
+  uint32_t out = 0, raw0 = 0;  // 16-bit stages and cached tiles so far
   bool ok = true;
+  auto filled = [&](unsigned long long* full) {  // what was written is there for the products
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(full));
+  };
+  // 16 dimensions of a row of 16-bit values; zeros where there are none
+  auto fetch = [&](const uint16_t* src, bool on, uint4 (&u)[2]) {
+    u[0] = u[1] = make_uint4(0, 0, 0, 0);
+    if (on && piece * 16 < A.D) {
+      const uint4* const p = reinterpret_cast<const uint4*>(src + piece * 16);
+      u[0] = __ldg(p);
+      u[1] = __ldg(p + 1);
+    }
+  };
   for (int segs = 0;; ++segs) {
+    ok = warp_wait(smem_addr(&C.seg_full[segs % SEGS]), (segs / SEGS) & 1, A.status, abort);
+    if (!ok) break;
+    const Seg s = C.seg[segs % SEGS];
+    if (s.n == 0) break;
+    const int n = s.n, c = cached_of(s);
+    // ---- queries
+    {
+      const int slot = PAIR ? 0 : segs & 1, use = PAIR ? segs : segs >> 1;
+      ok = warp_wait(smem_addr(&C.q_empty[slot]), (use & 1) ^ 1, A.status, abort);
+      if (!ok) break;
+#pragma unroll 1
+      for (int r = row0; r < (PAIR ? 2 : 1) * Q_ROWS; r += ROWS) {
+        const int tile = r / Q_ROWS, rr = r - tile * Q_ROWS, rt = rr / A.G;
+        const int tok = (s.mt * (PAIR ? 2 : 1) + tile) * A.tpt + rt;
+        uint4 u[2];
+        fetch(A.q + ((size_t(s.b) * A.N + tok) * A.Hq + s.h * A.G + (rr - rt * A.G)) * A.D,
+              rt < A.tpt && tok < A.N, u);
+        float x[16];
+        uint32_t most = widen16<BF>(u, x);
+        // (lanes of a row are neighbours, and every lane of a warp goes round as often)
+#pragma unroll
+        for (int k = 1; k < PER_ROW; k *= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, k));
+        const int e = exponent_over(most);
+        uint4 t[TERMS];
+        split_terms<TERMS>(x, power(-e), t);
+        unsigned char* const dst = smem + (PAIR ? tile : slot) * SM::Q_BYTES + swizzled<DP>(rr, piece);
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k) *reinterpret_cast<uint4*>(dst + k * SM::TERM) = t[k];
+        if (piece == 0) {
+          if (NQ) C8.qf[segs % SEGS][rr] = power(e);
+          else C8.qx[segs % SEGS][r] = uint8_t(e + 127);
+        }
+      }
+      filled(&C.q_full[slot]);
+    }
+    // ---- tiles
+#pragma unroll 1
+    for (int x = 0; x < 2 * (n + LAG); ++x) {
+      const bool is_v = x & 1;
+      const int j = is_v ? (x >> 1) - LAG : x >> 1;
+      if (j < 0 || j >= n || (!is_v && j < c)) continue;
+      const Keys ky = keys_of<false>(A, s, s.j0 + j);
+      const uint32_t st = out % STAGES;
+      unsigned char* const dst = smem + SM::STAGE_AT + st * SM::BYTES;
+      ok = warp_wait(smem_addr(&C.empty[st]), ((out / STAGES) & 1) ^ 1, A.status, abort);
+      if (!ok) break;
+      // a row's piece of the 16-bit tile, as two pieces of 16 bytes
+      auto put = [&](int row, const uint4& lo, const uint4& hi) {
+        unsigned char* const line = dst + (piece >> 2) * 16384 + row * 128;
+        const int at = (piece & 3) * 2, swap = piece >> 2;
+        *reinterpret_cast<uint4*>(line + (((at + swap) ^ (row & 7)) << 4)) = swap ? hi : lo;
+        *reinterpret_cast<uint4*>(line + (((at + 1 - swap) ^ (row & 7)) << 4)) = swap ? lo : hi;
+      };
+      if (is_v && j < c) {
+        const uint32_t u = raw0 + j, rs = SM::RAW_K + u % SM::RAW_V;
+        const unsigned char* const src = smem + SM::RAW_AT + rs * SM::RAW + tid * 16;
+        ok = warp_wait(smem_addr(&C.full[STAGES + rs]), (u / SM::RAW_V) & 1, A.status, abort);
+        if (!ok) break;
+#pragma unroll 1
+        for (int g = 0; g < STEPS; g += BATCH) {
+          uint4 b[BATCH];
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            b[i] = *reinterpret_cast<const uint4*>(src + (g + i) * (32 * WIDEN_WARPS * 16));
+            // (behind the entries: whatever the bytes are, weights of 0 take zeros)
+            if (row0 + (g + i) * ROWS >= ky.n) b[i] = make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            const uint2 p = widen4(b[i].x), q = widen4(b[i].y), y = widen4(b[i].z), z = widen4(b[i].w);
+            put(row0 + (g + i) * ROWS, make_uint4(p.x, p.y, q.x, q.y), make_uint4(y.x, y.y, z.x, z.y));
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&C.empty[STAGES + rs]));
+        filled(&C.full[st]);
+        ++out;
+        continue;
+      }
+      const size_t from = ((size_t(s.b) * A.LH + A.head0 + s.h) * A.N + ky.k0) * A.D;
+      Tile8& t8 = C8.staged[segs % SEGS][ky.k0 / TILE];
+      constexpr int V = PER_ROW / 4;  // pieces of a lane in eight rows
+      if (is_v) {  // staged values, eight rows at a power of two (the warp's own eights)
+#pragma unroll 1
+        for (int g = warp; g * 8 < width_of(ky); g += WIDEN_WARPS) {  // (products read no further)
+          const float by = g * 8 < ky.n ? power(-int(t8.ev[g])) : 0.0f;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const int row = g * 8 + i * 4 + lane / PER_ROW;
+            uint4 u[2];
+            fetch(A.v_new + from + size_t(row) * A.D, row < ky.n, u);
+            float v[16];
+            widen16<BF>(u, v);
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = pack16<false>(v[2 * k] * by, v[2 * k + 1] * by);
+            put(row, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
+          }
+        }
+        filled(&C.full[st]);
+        ++out;
+        continue;
+      }
+      // staged keys: a warp takes eight rows at a time, which share a power of two; and the
+      // values' powers of two, which the weights need before the values
+#pragma unroll 1
+      for (int part = 0; part < PARTS; ++part) {
+        if (part) {
+          const uint32_t s2 = out % STAGES;
+          ok = warp_wait(smem_addr(&C.empty[s2]), ((out / STAGES) & 1) ^ 1, A.status, abort);
+          if (!ok) break;
+        }
+        unsigned char* const to = smem + SM::STAGE_AT + (out % STAGES) * SM::BYTES;
+#pragma unroll 1
+        for (int g = warp; g * 8 < ky.n; g += WIDEN_WARPS) {
+          float v[V][16];
+          uint32_t most = 0, v_most = 0;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const int row = g * 8 + i * 4 + lane / PER_ROW;
+            uint4 u[2];
+            if (part == 0) {
+              fetch(A.v_new + from + size_t(row) * A.D, row < ky.n, u);
+              v_most = max(v_most, widen16<BF>(u, v[i]));
+            }
+            fetch(A.k_new + from + size_t(row) * A.D, row < ky.n, u);
+            most = max(most, widen16<BF>(u, v[i]));
+          }
+          const int e = exponent_over(__reduce_max_sync(0xffffffffu, most));
+          if (part == 0) {
+            const int ev = exponent_over(__reduce_max_sync(0xffffffffu, v_most));
+            if (lane == 0) {
+              t8.kf[g] = power(e);
+              t8.ev[g] = int8_t(ev);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const int row = g * 8 + i * 4 + lane / PER_ROW;
+            uint4 t[TERMS];
+            split_terms<TERMS>(v[i], power(-e), t);
+            unsigned char* const at = to + swizzled<DP>(row, piece);
+            if (part == 0) {
+              *reinterpret_cast<uint4*>(at) = t[0];
+              if (TERMS > 1) *reinterpret_cast<uint4*>(at + SM::RAW) = t[1];
+            } else {
+              *reinterpret_cast<uint4*>(at) = t[TERMS - 1];
+            }
+          }
+        }
+        if (part == 0) {  // the last warp to get here puts the values' powers of two together
+          __syncwarp();
+          __threadfence_block();
+          int last = 0;
+          if (lane == 0) last = atomicAdd(&t8.count, 1) == WIDEN_WARPS - 1;
+          if (__shfl_sync(0xffffffffu, last, 0)) {
+            __threadfence_block();
+            const int ev = lane < 16 && lane * 8 < ky.n ? int(reinterpret_cast<volatile int8_t*>(t8.ev)[lane]) : -1000;
+            const int top = __reduce_max_sync(0xffffffffu, ev), by = max(ev - top, LEAST);
+            if (lane < 16) {
+              t8.vd[lane] = float(by);
+              t8.vf[lane] = power(NQ ? by : -by);
+            }
+            if (lane == 0) {
+              t8.top = top;
+              t8.count = 0;
+            }
+          }
+        }
+        filled(&C.full[out % STAGES]);
+        ++out;
+      }
+      if (!ok) break;
+    }
+    if (!ok) break;
+    raw0 += c;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&C.seg_empty[segs % SEGS]));
+  }
+}
+
+// The scales of every segment's cached tiles, as powers of two of eight tokens each, up to
+// SCALES tiles ahead.  As many tiles at once as their blocks fill lanes, since the loads of
+// a page's number and then of its scales take longer than a tile does.
+template <int NQ, bool PAIR, bool BF>
+__device__ __forceinline__ void read_scales(const AttnParams& A, Ctrl<NQ, PAIR>& C, Ctrl8<NQ>& C8,
+                                            volatile int* abort) {
+  const int lane = int(threadIdx.x) & 31;
+  const int log = 7 - A.block_log, blocks = 1 << log;  // of a tile
+  const int mine = lane >> log, block = lane & (blocks - 1), per_page = A.page >> A.block_log;
+  const int at_once = min(32 >> log, 4), rep = 1 << (A.block_log - 3);
+  uint32_t tiles = 0;
+  bool ok = true;
+  for (int segs = 0; ok; ++segs) {
     ok = warp_wait(smem_addr(&C.seg_full[segs % SEGS]), (segs / SEGS) & 1, A.status, abort);
     if (!ok) break;
     const Seg s = C.seg[segs % SEGS];
     if (s.n == 0) break;
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_addr(&C.seg_empty[segs % SEGS]));
-    const int blocks = TILE >> A.block_log, per_page = A.page >> A.block_log;
-    // the page of this lane's block of tile j (-1: none), and the scales there
-    auto place = [&](int j) {
-      const int t = j * TILE + (lane << A.block_log);
-      if (lane >= blocks || t >= s.len) return -1;
-      const int pg = __ldg(A.table + size_t(s.b) * A.cols + t / A.page);
-      return pg < 0 || pg >= A.num_pages ? 0 : pg;
-    };
-    auto scales = [&](int j, int pg, int& k, int& v) {
-      k = v = 127;
-      if (pg < 0) return;
-      const int t = j * TILE + (lane << A.block_log);
-      const size_t at = (size_t(pg) * A.LH + A.head0 + s.h) * per_page +
-                        ((t - t / A.page * A.page) >> A.block_log);
-      k = __ldg(A.k_scales + at);
-      v = __ldg(A.v_scales + at);
-    };
-    int k_now = 127, v_now = 127, k_next, v_next, v_before = 127;
-    scales(s.j0, place(s.j0), k_next, v_next);
-    int page_next = place(s.j0 + 1);
-    // (one copy of a tile's code for keys and values, its loops rolled)
-    constexpr int LAG = PAIR ? 0 : 1;
-#pragma unroll 1
-    for (int x = 0; x < 2 * (s.n + LAG); ++x) {
-      const bool is_v = x & 1;
-      const int i = x >> 1, jj = is_v ? i - LAG : i;
-      if (!is_v) {
-        v_before = v_now;
-        k_now = k_next;
-        v_now = v_next;
-        if (i < s.n) {
-          scales(s.j0 + i + 1, page_next, k_next, v_next);
-          page_next = place(s.j0 + i + 2);
-        }
+    const int c = cached_of(s);
+    for (int j = 0; ok && j < c; j += at_once) {
+      // (blocks behind the entries: no part in the tile's largest exponent)
+      int k = 0, v = -1000;
+      bool nan = false;
+      const int t = (s.j0 + j + mine) * TILE + (block << A.block_log);
+      if (mine < at_once && j + mine < c && t < s.len) {
+        const int col = t / A.page;
+        int pg = __ldg(A.table + size_t(s.b) * A.cols + col);
+        if (pg < 0 || pg >= A.num_pages) pg = 0;  // (reported, and its result dropped, elsewhere)
+        const size_t at = (size_t(pg) * A.LH + A.head0 + s.h) * per_page +
+                          ((t - col * A.page) >> A.block_log);
+        k = int(__ldg(A.k_scales + at)) - 127;
+        v = int(__ldg(A.v_scales + at)) - 127;
+        // exponents at which dtype does not hold every value: NaN
+        const int lo = BF ? -117 : -15, hi = BF ? 119 : 7;
+        nan = k < lo || k > hi || v < lo || v > hi;
+        if (nan) k = v = 0;
       }
-      if (jj < 0 || jj >= s.n) continue;
-      const int byte = !is_v ? k_now : PAIR ? v_now : v_before;
-      const Keys ky = keys_of<false>(A, s, s.j0 + jj);
-      const uint32_t st = out % STAGES, lap = out / STAGES;
-      unsigned char* const dst = smem + SM::STAGE_AT + st * SM::BYTES;
-      if (ky.staged) {
-        const uint16_t* const src =
-            (is_v ? A.v_new : A.k_new) +
-            ((size_t(s.b) * A.LH + A.head0 + s.h) * A.N + ky.k0) * A.D;
-        ok = warp_wait(smem_addr(&C.empty[st]), (lap & 1) ^ 1, A.status, abort);
+      int top = v;  // of the tile
+      for (int x = 1; x < blocks; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const float kf = power(k), vd = nan ? __int_as_float(0x7fffffff) : float(max(v - top, LEAST));
+      const float vf = nan ? vd : power(NQ ? max(v - top, LEAST) : -max(v - top, LEAST));
+      for (int x = 0; ok && x < at_once && j + x < c; ++x, ++tiles) {
+        const uint32_t sc = tiles % SCALES;
+        ok = warp_wait(smem_addr(&C8.empty[sc]), ((tiles / SCALES) & 1) ^ 1, A.status, abort);
         if (!ok) break;
-#pragma unroll 1
-        for (int g = 0; g < STEPS; g += BATCH) {
-          uint4 u[2 * BATCH];
-#pragma unroll
-          for (int i = 0; i < 2 * BATCH; ++i) {
-            const int row = row0 + (g + i / 2) * ROWS, d = piece * 16 + (i & 1) * 8;
-            u[i] = make_uint4(0, 0, 0, 0);  // (rows behind the entries, and columns past D)
-            if (row < ky.n && d < A.D)
-              u[i] = __ldg(reinterpret_cast<const uint4*>(src + size_t(row) * A.D + d));
+        if (mine == x) {
+          Tile8& t8 = C8.tile[sc];
+          for (int i = block * rep; i < block * rep + rep; ++i) {
+            t8.kf[i] = kf;
+            t8.vd[i] = vd;
+            t8.vf[i] = vf;
           }
-#pragma unroll
-          for (int i = 0; i < 2 * BATCH; ++i) {
-            const int row = row0 + (g + i / 2) * ROWS, at = (piece & 3) * 2 + (i & 1);
-            *reinterpret_cast<uint4*>(dst + (piece >> 2) * 16384 + row * 128 +
-                                      ((at ^ (row & 7)) << 4)) = u[i];
-          }
-        }
-      } else {
-        const uint32_t rs = in % RAWS, rlap = in / RAWS;
-        const unsigned char* const src = smem + SM::RAW_AT + rs * SM::RAW + tid * 16;
-        uint32_t rest, factor = factor_of<BF>(byte, rest);
-        const bool large = BF && __any_sync(0xffffffffu, rest != 0x3f803f80u);
-        ok = warp_wait(smem_addr(&C.full[STAGES + rs]), rlap & 1, A.status, abort) &&
-             warp_wait(smem_addr(&C.empty[st]), (lap & 1) ^ 1, A.status, abort);
-        if (!ok) break;
-#pragma unroll 1
-        for (int g = 0; g < STEPS; g += BATCH) {
-          uint4 u[BATCH];
-#pragma unroll
-          for (int i = 0; i < BATCH; ++i)
-            u[i] = *reinterpret_cast<const uint4*>(src + (g + i) * (32 * WIDEN_WARPS * 16));
-#pragma unroll
-          for (int i = 0; i < BATCH; ++i) {
-            const int row = row0 + (g + i) * ROWS;
-            const uint32_t f = __shfl_sync(0xffffffffu, factor, row >> A.block_log);
-            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-            uint32_t y[8];
-            if (BF) {
-              uint32_t seen = 0;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                y[2 * q] = widen_bf16(w[q], false, f, seen);
-                y[2 * q + 1] = widen_bf16(w[q], true, f, seen);
-              }
-              if (large) {
-                const uint32_t f2 = __shfl_sync(0xffffffffu, rest, row >> A.block_log);
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(y[q]) : "r"(f2));
-              }
-              if ((seen & 0xffffu) == 0x7f0u || seen >> 16 == 0x7f0u) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q) y[q] = nan_of(w[q / 2], q & 1, y[q]);
-              }
-            } else {
-#pragma unroll
-              for (int q = 0; q < 8; ++q)
-                y[q] = widen_f16(uint16_t(w[q / 2] >> (q & 1 ? 16 : 0)), f);
-            }
-            const uint4 a = make_uint4(y[0], y[1], y[2], y[3]), b = make_uint4(y[4], y[5], y[6], y[7]);
-            unsigned char* const line = dst + (piece >> 2) * 16384 + row * 128;
-            const int at = (piece & 3) * 2, swap = piece >> 2;
-            *reinterpret_cast<uint4*>(line + (((at + swap) ^ (row & 7)) << 4)) = swap ? b : a;
-            *reinterpret_cast<uint4*>(line + (((at + 1 - swap) ^ (row & 7)) << 4)) = swap ? a : b;
-          }
+          if (block == 0) t8.top = top;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&C.empty[STAGES + rs]));
-        ++in;
+        if (lane == 0) mbar_arrive(smem_addr(&C8.full[sc]));
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&C.full[st]));
-      ++out;
     }
-    if (!ok) break;
   }
 }
 
@@ -1075,14 +1358,15 @@ __device__ __forceinline__ void widen_tiles(const AttnParams& A, Ctrl<NQ, PAIR>&
 // The weights are rounded once to the storage type (half a step each); their sum
 // l is taken before that, in 32 bits.
 // 8-bit caches (Q8) add
-//   widen     a warpgroup: cached tiles from bytes to 16 bits times their blocks' powers of
-//             two (exactly), staged ones from global memory, into the products' stages
+//   widen     a warpgroup: queries and staged keys to terms in e4m3, values to fp16
+//   scales    the blocks' powers of two, a few tiles ahead
 template <int DP, int NQ, bool PAIR, bool PR, bool BF, bool Q8 = false>
 __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
     sv_attn(const __grid_constant__ AttnParams A) {
   static_assert(!(NQ && (PAIR || PR)), "few rows make one tile, and prompts have many");
   static_assert(!(Q8 && PR), "8-bit entries are in pages");
-  using SM = Smem<DP, NQ, Q8>;
+  constexpr int TERMS = Q8 ? TERMS_OF<BF> : 0, PARTS = (TERMS + 1) / 2;
+  using SM = Smem<DP, NQ, TERMS>;
   constexpr int NT = Q8 ? THREADS8 : THREADS;
   constexpr int STAGES = SM::STAGES, BYTES = SM::BYTES, HALVES = DP / 64;
   constexpr int ROWS = NQ ? NQ : PAIR ? 2 * TILE : TILE;
@@ -1090,6 +1374,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
   constexpr int S_COLS = NQ ? 64 : 128, O_AT = TM_COLS / 2;
   extern __shared__ __align__(1024) unsigned char smem[];
   Ctrl<NQ, PAIR>& C = *reinterpret_cast<Ctrl<NQ, PAIR>*>(smem + SM::CTRL);
+  Ctrl8<NQ>& C8 = *reinterpret_cast<Ctrl8<NQ>*>(smem + SM::CTRL + (Q8 ? CTRL_BYTES : 0));  // Q8
   const uint32_t base = smem_addr(smem);
   const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   auto bar = [&](unsigned long long* p) { return smem_addr(p); };
@@ -1099,16 +1384,23 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
     for (int i = 0; i < STAGES; ++i) {
       // (withheld: one arrival too many, and every wait for that stage runs out)
       const int arrivals = Q8 ? WIDEN_WARPS : 1;
-      mbar_init(bar(&C.full[i]), A.withhold && blockIdx.x == 0 && i == 1 ? arrivals + 1 : arrivals);
+      const bool withheld = A.withhold && blockIdx.x == 0 && i == (Q8 ? 0 : 1);
+      mbar_init(bar(&C.full[i]), withheld ? arrivals + 1 : arrivals);
       mbar_init(bar(&C.empty[i]), 1);
     }
-    if (Q8)
+    if (Q8) {
       for (int i = STAGES; i < STAGES + SM::RAWS; ++i) {
         mbar_init(bar(&C.full[i]), 1);
-        mbar_init(bar(&C.empty[i]), WIDEN_WARPS);
+        mbar_init(bar(&C.empty[i]), i < STAGES + SM::RAW_K ? 1 : WIDEN_WARPS);
       }
+      for (int i = 0; i < SEGS; ++i) C8.staged[i][0].count = C8.staged[i][1].count = 0;
+      for (int i = 0; i < SCALES; ++i) {
+        mbar_init(bar(&C8.full[i]), 1);
+        mbar_init(bar(&C8.empty[i]), PAIR ? 8 : 4);
+      }
+    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(&C.q_full[i]), 1);
+      mbar_init(bar(&C.q_full[i]), Q8 ? WIDEN_WARPS : 1);
       mbar_init(bar(&C.q_empty[i]), 1);
       mbar_init(bar(&C.s_full[i]), 1);
       mbar_init(bar(&C.p_half[i]), 4);
@@ -1117,7 +1409,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
     }
     for (int i = 0; i < SEGS; ++i) {
       mbar_init(bar(&C.seg_full[i]), 1);
-      mbar_init(bar(&C.seg_empty[i]), COPY_WARP + 2 + (Q8 ? WIDEN_WARPS : 0));  // its readers
+      mbar_init(bar(&C.seg_empty[i]), COPY_WARP + 2 + (Q8 ? WIDEN_WARPS + 1 : 0));  // its readers
     }
     mbar_init(bar(&C.drain), 1);
     mbar_init(bar(&C.next_full), 1);
@@ -1222,7 +1514,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
     const int rt = row / A.G, rg = row - rt * A.G;
     const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's TMEM lanes
     const uint32_t ts = tmem + lanes + st * S_COLS, to = tmem + lanes + O_AT + st * S_COLS;
-    uint32_t idx = 0;
+    uint32_t idx = 0, tiles8 = 0;  // (Q8: cached tiles before the segment)
     int segs = 0, parent_b = -1, parent_bad = 0;
     unsigned s_use = 0, o_use[2] = {0, 0};
     bool ok = true;
@@ -1282,10 +1574,14 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
       const int q0 = s.mt * tpi, q1 = min(q0 + tpi, tokens) - 1;  // the item's tokens
       const int w0 = q0 + (PAIR ? st * A.tpt : 0), w1 = min(w0 + A.tpt, tokens) - 1;  // the tile's
 
-      const float lift = BF ? 0.0f : A.lift, raise = BF ? MOST_BF16 : MOST_F16 - A.lift;
+      constexpr bool HALF = Q8 || !BF;  // the weights' type
+      const float lift = HALF ? A.lift : 0.0f, raise = HALF ? MOST_F16 - A.lift : MOST_BF16;
+      const float unit = Q8 ? 1.0f : A.c;  // of the maxima, in base-2 units
+      int top = 0;            // Q8: O's power of two, VALUE_SLACK above the values' largest
       float m = -INFINITY, l = 0.0f;
       float lq[NQ ? NQ : 1];  // NQ > 0: this key's share of the columns' sums
       bool unset = true;      // NQ > 0: a column has seen nothing yet
+      const int cached = Q8 ? cached_of(s) : 0;
 #pragma unroll
       for (int q = 0; q < NQ; ++q) lq[q] = 0.0f;
       int done = 0;
@@ -1314,6 +1610,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
           }
         }
         dead = dead && row < w;
+        if (Q8) clean = false;  // (the widening warps' rows behind the entries are zeros)
         // (With keys on the lanes the warps meet at barriers within a tile: after a
         // wait that gave up they walk the rest of the segment's tiles together.)
         ok = ok && warp_wait(bar(&C.s_full[st]), s_use & 1, A.status, abort);
@@ -1336,6 +1633,15 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
+        }
+        // Q8: the tile's powers of two
+        const Tile8* t8 = nullptr;
+        const uint32_t sc = (tiles8 + jj) % SCALES;
+        if (Q8) {
+          t8 = ky.staged ? &C8.staged[segs % SEGS][ky.k0 / TILE] : &C8.tile[sc];
+          if (!ky.staged)
+            ok = ok && warp_wait(bar(&C8.full[sc]), ((tiles8 + jj) / SCALES) & 1, A.status, abort);
+          if (NQ == 0 && !ok) break;
         }
         auto half_done = [&] {  // PAIR: the weights of the tile's first 64 keys are stored
           if (!PAIR) return;
@@ -1363,12 +1669,76 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
               sees = A.parent ? C.x.sees[st][k] : ~0u << (k * A.G);
             }
           }
-          softmax_few<NQ, BF>(A, C, st, row, ts, to, sees, masked, done > 0, unset, lq,
-                          smem + SM::P_AT + st * SM::P_BYTES);
+          softmax_few<NQ, BF, Q8>(A, C, st, row, ts, to, sees, masked, done > 0, unset, lq,
+                                  smem + SM::P_AT + st * SM::P_BYTES,
+                                  t8, C8.qf[segs % SEGS], top);
         } else if (!warp_active) {
           __syncwarp();
           half_done();
         } else {
+          // Q8: what the scores of eight keys are multiplied by, and the weights' exponents moved by
+          float qc = 0.0f, adj = 0.0f, sink = 1.0f;
+          if (Q8) {
+            qc = A.c * power_of(C8.qx[segs % SEGS][(PAIR ? st * TILE : 0) + row]);
+            if (done == 0 || t8->top > top) {
+              if (done) sink = power(max(top - (t8->top + VALUE_SLACK), -126));
+              top = t8->top + VALUE_SLACK;
+            }
+            adj = float(max(t8->top - top, LEAST));
+          }
+          auto factors = [&](int x) {  // (not 0: hidden scores stay at -infinity)
+            const float4 k = *reinterpret_cast<const float4*>(t8->kf + 4 * x);
+            return make_float4(fmaxf(qc * k.x, 1e-37f), fmaxf(qc * k.y, 1e-37f),
+                               fmaxf(qc * k.z, 1e-37f), fmaxf(qc * k.w, 1e-37f));
+          };
+          auto most = [&](int x, uint32_t (&r)[32]) {  // the largest of 32 scores
+            if (!Q8) return max_of<32>([&](int i) { return __uint_as_float(r[i]); });
+            const float4 f = factors(x);
+            float t[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              auto v = [&](int i) { return __uint_as_float(r[8 * g + i]); };
+              t[g] = fmaxf(fmaxf(fmaxf(v(0), v(1)), v(2)),
+                           fmaxf(fmaxf(fmaxf(v(3), v(4)), v(5)), fmaxf(v(6), v(7))));
+            }
+            return fmaxf(fmaxf(t[0] * f.x, t[1] * f.y), fmaxf(t[2] * f.z, t[3] * f.w));
+          };
+          // the weights of 32 keys, and their sum
+          auto weigh = [&](int x, const uint32_t (&r)[32], float nm, uint32_t (&pw)[16],
+                           float2 (&sum)[4]) {
+            if (Q8) {
+              const float4 f = factors(x);
+              const float4 d = *reinterpret_cast<const float4*>(t8->vd + 4 * x);
+              const float4 v = *reinterpret_cast<const float4*>(t8->vf + 4 * x);
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                const float fg = g == 0 ? f.x : g == 1 ? f.y : g == 2 ? f.z : f.w;
+                const float dg = nm + (g == 0 ? d.x : g == 1 ? d.y : g == 2 ? d.z : d.w);
+                const float vg = g == 0 ? v.x : g == 1 ? v.y : g == 2 ? v.z : v.w;
+                float2 t = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int i = 4 * g; i < 4 * g + 4; ++i) {
+                  const float2 e = fma2(
+                      make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
+                      make_float2(fg, fg), make_float2(dg, dg));
+                  const float2 p = make_float2(ex2(e.x), ex2(e.y));
+                  t = add2(t, p);
+                  pw[i] = pack16<false>(p.x, p.y);
+                }
+                sum[g] = fma2(t, make_float2(vg, vg), sum[g]);
+              }
+              return;
+            }
+            const float2 c2 = make_float2(A.c, A.c), mc2 = make_float2(nm, nm);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 e = fma2(make_float2(__uint_as_float(r[2 * i]),
+                                                __uint_as_float(r[2 * i + 1])), c2, mc2);
+              const float2 p = make_float2(ex2(e.x), ex2(e.y));
+              sum[i & 3] = add2(sum[i & 3], p);
+              pw[i] = pack16<BF>(p.x, p.y);
+            }
+          };
           // the tile's keys that this row sees, 32 to a word
           auto visible = [&](uint32_t (&see)[4]) {
             if (PR) {
@@ -1407,11 +1777,12 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
             if (done == 0) {
               m = mt;
             } else {
-              const bool rise = active && (mt - m) * A.c > raise;  // (-inf before: always)
-              if (__any_sync(0xffffffffu, rise)) {
-                const float f = rise ? ex2((m - mt) * A.c) : 1.0f;
+              const bool rise = active && (mt - m) * unit > raise;  // (-inf before: always)
+              if (__any_sync(0xffffffffu, rise || sink != 1.0f)) {
+                float f = rise ? ex2((m - mt) * unit) : 1.0f;
                 if (rise) m = mt;
                 l *= f;
+                f *= sink;
 #pragma unroll 1
                 for (int x = 0; x < DP / 32; ++x) {
                   uint32_t o[32];
@@ -1449,30 +1820,19 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
               }
             }
             float mt;
-            if (w == TILE) {
+            if (!Q8 && w == TILE) {
               mt = max_of<128>([&](int i) { return __uint_as_float(r[i >> 5][i & 31]); });
             } else {
               mt = -INFINITY;
 #pragma unroll
               for (int x = 0; x < 4; ++x)
-                if (x * 32 < w)
-                  mt = fmaxf(mt, max_of<32>([&](int i) { return __uint_as_float(r[x][i]); }));
+                if (x * 32 < w) mt = fmaxf(mt, most(x, r[x]));
             }
             raise_to(mt);
-            const float nm = m == -INFINITY ? 0.0f : lift - m * A.c;
-            const float2 c2 = make_float2(A.c, A.c), mc2 = make_float2(nm, nm);
+            const float nm = (m == -INFINITY ? 0.0f : lift - m * unit) + adj;
             float2 sum[4] = {};
             uint32_t pw[16];
-            auto chunk = [&](int x) {  // the weights of 32 keys
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float2 e = fma2(make_float2(__uint_as_float(r[x][2 * i]),
-                                                  __uint_as_float(r[x][2 * i + 1])), c2, mc2);
-                const float2 p = make_float2(ex2(e.x), ex2(e.y));
-                sum[i & 3] = add2(sum[i & 3], p);
-                pw[i] = pack16<BF>(p.x, p.y);
-              }
-            };
+            auto chunk = [&](int x) { weigh(x, r[x], nm, pw, sum); };  // the weights of 32 keys
             // the products with the first 64 keys' values start under the others' weights
             // (One copy for all widths, fewer instructions to fetch: a second one for whole
             // tiles took 1280 items of 16 tiles from 222 us to 244, 8192 tokens to 318 as now.)
@@ -1493,7 +1853,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
               tm_st16<false>(ts + 48, pw);
             }
             sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-            l += sum[0].x + sum[0].y;
+            l += Q8 ? (sum[0].x + sum[0].y) * power(int(-adj)) : sum[0].x + sum[0].y;
           } else {
             // One tile of rows: 64 scores at a time, the maximum of the tile's second half,
             // then of its first, whose weights follow from registers; the second half is
@@ -1520,29 +1880,21 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
               tm_wait_ld(r0);
               tm_loaded(r1);
               hide(r0, see[x]);
-              float t = max_of<32>([&](int i) { return __uint_as_float(r0[i]); });
+              float t = most(x, r0);
               if ((x + 1) * 32 < w) {
                 hide(r1, see[x + 1]);
-                t = fmaxf(t, max_of<32>([&](int i) { return __uint_as_float(r1[i]); }));
+                t = fmaxf(t, most(x + 1, r1));
               }
               return t;
             };
             float mt = w > 64 ? two(2) : -INFINITY;
             mt = fmaxf(mt, two(0));
             raise_to(mt);
-            const float nm = m == -INFINITY ? 0.0f : lift - m * A.c;
-            const float2 c2 = make_float2(A.c, A.c), mc2 = make_float2(nm, nm);
+            const float nm = (m == -INFINITY ? 0.0f : lift - m * unit) + adj;
             float2 sum[4] = {};
             auto weights = [&](int x, uint32_t (&r)[32]) {  // of 32 keys
               uint32_t pw[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float2 e = fma2(
-                    make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), c2, mc2);
-                const float2 p = make_float2(ex2(e.x), ex2(e.y));
-                sum[i & 3] = add2(sum[i & 3], p);
-                pw[i] = pack16<BF>(p.x, p.y);
-              }
+              weigh(x, r, nm, pw, sum);
               tm_st16(ts + x * 16, pw);
             };
             // (P's columns lie over scores of the first half only; a pair's products
@@ -1563,16 +1915,23 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
               }
             }
             sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-            l += sum[0].x + sum[0].y;
+            l += Q8 ? (sum[0].x + sum[0].y) * power(int(-adj)) : sum[0].x + sum[0].y;
           }
           tm_wait_st<false>();
         }
         tc_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(&C.p_full[st]));
+        if (lane == 0) {
+          mbar_arrive(bar(&C.p_full[st]));
+          if (Q8 && !ky.staged) mbar_arrive(bar(&C8.empty[sc]));
+        }
       }
 
       // ---- the segment's end: the output rows, or their partials
+      // Q8: O stands for 2^top times itself.  That goes to the maximum, and out of the sum l, as
+      // far as 32 bits hold it; `lost` is the rest.
+      const int kept = Q8 ? min(max(top, -60), 60) : 0;
+      const float lost = Q8 ? power(top - kept) : 1.0f, unkept = power(-kept);
       const bool whole = n == s.nt;
       const int slot = segs == 0 ? 0 : 1;
       const size_t part = (size_t(blockIdx.x) * 2 + slot) * ROWS + (PAIR ? st * TILE : 0) + row;
@@ -1622,6 +1981,10 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         // sums over the keys: 32 lanes here, the four warps and two streams below
         sum_columns<NQ>(lq, lane);
         if (lane < NQ) C.x.sums[warp][lane] = lq[0];
+        if (Q8 && row == 0) {
+          C8.kept[st] = kept;
+          C8.lost[st] = lost;
+        }
         group_sync(3, 2 * TILE);
         if (tid < NQ) {
           float l0 = 0.0f, l1 = 0.0f;
@@ -1632,12 +1995,23 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
           float a = -C.x.nmc[0][tid], b = n > 1 ? -C.x.nmc[1][tid] : INFINITY;
           if (a == INFINITY) a = -INFINITY;  // nothing seen
           if (b == INFINITY) b = -INFINITY;
+          if (Q8) {
+            const int k0 = C8.kept[0], k1 = n > 1 ? C8.kept[1] : 0;
+            a += float(k0);
+            b += float(k1);
+            l0 *= power(-k0);
+            l1 *= power(-k1);
+          }
           const float mm = fmaxf(a, b), mu = mm == -INFINITY ? 0.0f : mm;
           float f0 = ex2(a - mu), f1 = ex2(b - mu);
           const float ll = l0 * f0 + (n > 1 ? l1 * f1 : 0.0f);
           if (whole) {
             f0 /= ll;
             f1 /= ll;
+          }
+          if (Q8) {
+            f0 *= C8.lost[0];
+            f1 *= n > 1 ? C8.lost[1] : 1.0f;
           }
           C.x.fac[0][tid] = f0;
           C.x.fac[1][tid] = f1;
@@ -1690,7 +2064,8 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         ++o_use[st];
         tc_after();
         if (ok && warp_active) {
-          const float f = whole ? 1.0f / l : 1.0f;
+          if (Q8) l *= unkept;
+          const float f = (whole ? 1.0f / l : 1.0f) * lost;
 #pragma unroll 1
           for (int x = 0; x < DP / 32; ++x) {
             uint32_t o[32];
@@ -1701,12 +2076,14 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * f;
             put(v, x * 32);
           }
-          if (!whole && active) A.part_ml[part] = make_float2(m * A.c, bad ? -1.0f : l);
+          if (!whole && active)
+            A.part_ml[part] = make_float2(m * unit + float(kept), bad ? -1.0f : l);
         }
         tc_before();
       } else {
         // join the two streams; warpgroup st takes half of the columns
-        C.x.ml[st][row] = make_float2(m, l);
+        C.x.ml[st][row] = Q8 ? make_float2(m + float(kept), l * unkept) : make_float2(m, l);
+        if (Q8 && row == 0) C8.lost[st] = lost;
         for (int x = 0; x < 2; ++x) {
           if (x >= n) break;
           ok = ok && warp_wait(bar(&C.o_full[x]), o_use[x] & 1, A.status, abort);
@@ -1719,11 +2096,15 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
           const float2 a = C.x.ml[0][row], b = C.x.ml[1][row];
           const float mm = fmaxf(a.x, b.x);
           const float mu = mm == -INFINITY ? 0.0f : mm;
-          float f0 = ex2((a.x - mu) * A.c), f1 = ex2((b.x - mu) * A.c);
+          float f0 = ex2((a.x - mu) * unit), f1 = ex2((b.x - mu) * unit);
           const float ll = a.y * f0 + (n > 1 ? b.y * f1 : 0.0f);
           if (whole) {
             f0 /= ll;
             f1 /= ll;
+          }
+          if (Q8) {
+            f0 *= C8.lost[0];
+            f1 *= n > 1 ? C8.lost[1] : 1.0f;
           }
           const uint32_t t0 = tmem + lanes + O_AT;
 #pragma unroll 1
@@ -1744,7 +2125,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
             put(v, col);
           }
           if (!whole && st == 0 && active)
-            A.part_ml[part] = make_float2(mm * A.c, bad ? -1.0f : ll);
+            A.part_ml[part] = make_float2(mm * unit, bad ? -1.0f : ll);
         }
         tc_before();
       }
@@ -1757,6 +2138,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
       }
       d_flags = s.j0 + n < s.nt ? d_flags | DESC_OUT : d_flags & ~DESC_OUT;
       idx += 2 * n;
+      tiles8 += cached;
       seg_done(segs);
       ++segs;
     }
@@ -1767,7 +2149,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         __syncwarp();
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<NQ, Q8>::WIDEN));
       }
-      widen_tiles<DP, NQ, PAIR, BF>(A, C, smem, abort);
+      widen_tiles<DP, NQ, PAIR, BF>(A, C, C8, smem, abort);
     }
   } else {
     __syncwarp();
@@ -1844,9 +2226,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
   } else if (warp == COPY_WARP) {
     // ------------------------------------------------------------ copies
     // One thread, or (pages) a warp with a lane per box of page rows.
-    // COPIED stages, whose barriers begin at RAW0.
-    constexpr int RAW0 = Q8 ? STAGES : 0;
-    constexpr uint32_t COPIED = Q8 ? SM::RAWS : STAGES;
+    constexpr int RAW0 = Q8 ? STAGES : 0;  // the stages' barriers begin there
     auto copies = [&](auto solo) {
       constexpr bool SOLO = decltype(solo)::value;
       const bool lead = SOLO || lane == 0;
@@ -1858,6 +2238,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         if (!SOLO) __syncwarp();
       };
       uint32_t st = 0, lap = 0, idx = 0;  // stage, times around the ring, copies
+      uint32_t k_at = 0, v_at = 0;        // Q8: copies of keys and of values
       int segs = 0;
       bool ok = true;
       for (;;) {
@@ -1869,9 +2250,9 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         if (lead) mbar_arrive(bar(&C.seg_empty[segs % AHEAD]));
         const int slot = PAIR ? 0 : segs & 1;
         const int use = PAIR ? segs : segs >> 1;
-        ok = wait(bar(&C.q_empty[slot]), (use & 1) ^ 1);  // (passes before the first use)
+        if (!Q8) ok = wait(bar(&C.q_empty[slot]), (use & 1) ^ 1);  // (passes before the first use)
         if (!ok) break;
-        if (lead) {
+        if (!Q8 && lead) {
           const uint32_t fb = bar(&C.q_full[slot]);
           mbar_arrive_tx(fb, (PAIR ? 2 : 1) * A.q_rows * DP * 2);
           const int tok = PR ? s.start : s.b * A.N;
@@ -1886,9 +2267,20 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         auto tile = [&](int jj, bool is_v) {
           const Keys ky = keys_of<PR>(A, s, s.j0 + jj);
           if (Q8 && ky.staged) return true;  // (the widening warps')
+          if constexpr (Q8) {  // of the keys' stages, or the values'
+            const uint32_t u = is_v ? v_at : k_at;
+            st = is_v ? SM::RAW_K + u % SM::RAW_V : u % SM::RAW_K;
+            lap = u / (is_v ? SM::RAW_V : SM::RAW_K);
+            if (is_v) ++v_at;
+            else ++k_at;
+          }
           const uint32_t fb = bar(&C.full[RAW0 + st]);
           const uint32_t dst = base + (Q8 ? SM::RAW_AT + st * SM::RAW : SM::STAGE_AT + st * BYTES);
-          if (!wait(bar(&C.empty[RAW0 + st]), (lap & 1) ^ 1)) return false;
+          if (!wait(bar(&C.empty[RAW0 + st]), (lap & 1) ^ 1)) {
+            if (Q8 && is_v) --v_at;  // (not begun)
+            else if (Q8) --k_at;
+            return false;
+          }
           if (SOLO || ky.staged) {
             if (lead) {
               const CUtensorMap* const m = !PR && ky.staged ? (is_v ? &A.mvn : &A.mkn)
@@ -1922,7 +2314,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
           }
           together();
           ++idx;
-          if (++st == COPIED) {
+          if (!Q8 && ++st == STAGES) {
             st = 0;
             ++lap;
           }
@@ -1937,11 +2329,19 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
       }
       if (*abort) {  // the copies in flight land before the CTA ends
         const unsigned long long t0 = globaltimer();
-        for (uint32_t u = idx > COPIED ? idx - COPIED : 0; u < idx; ++u)
-          while (!mbar_try(bar(&C.full[RAW0 + u % COPIED]), (u / COPIED) & 1) &&
-                 globaltimer() - t0 < WAIT_LIMIT_NS) {
-          }
-        for (int u = max(0, segs - (PAIR ? 1 : 2)); u < segs; ++u)
+        auto land = [&](uint32_t at, uint32_t first, uint32_t count) {
+          for (uint32_t u = at > count ? at - count : 0; u < at; ++u)
+            while (!mbar_try(bar(&C.full[first + u % count]), (u / count) & 1) &&
+                   globaltimer() - t0 < WAIT_LIMIT_NS) {
+            }
+        };
+        if constexpr (Q8) {
+          land(k_at, STAGES, SM::RAW_K);
+          land(v_at, STAGES + SM::RAW_K, SM::RAW_V);
+        } else {
+          land(idx, 0, STAGES);
+        }
+        for (int u = Q8 ? segs : max(0, segs - (PAIR ? 1 : 2)); u < segs; ++u)
           while (!mbar_try(bar(&C.q_full[PAIR ? 0 : u & 1]), (PAIR ? u : u >> 1) & 1) &&
                  globaltimer() - t0 < WAIT_LIMIT_NS) {
           }
@@ -1953,6 +2353,8 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
     } else {
       copies(Yes<false>());
     }
+  } else if (Q8 && warp == SCALE_WARP) {
+    if constexpr (Q8) read_scales<NQ, PAIR, BF>(A, C, C8, abort);
   } else if (warp == MMA_WARP) {
     // ------------------------------------------------------------ products
     uint32_t idx = 0;
@@ -1960,7 +2362,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
     unsigned p_use[2] = {0, 0};
     // (the turned products: N = NQ, and V^T is an operand whose dimensions are contiguous)
     const uint32_t id_s = instr_desc(BF, false, false, NQ);  // (0: the tile's width goes there)
-    const uint32_t id_o = instr_desc(BF, NQ > 0, NQ == 0, NQ ? NQ : DP);
+    const uint32_t id_o = instr_desc(BF && !Q8, NQ > 0, NQ == 0, NQ ? NQ : DP);
     bool ok = true;
     auto full = [&](uint32_t u) {
       if (!mbar_wait(bar(&C.full[u % STAGES]), (u / STAGES) & 1, A.status, abort)) return false;
@@ -2003,7 +2405,100 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
     };
     // One thread from here on: the waits, too, are its own.
     if (elect_one()) {
-    while (ok) {
+    if constexpr (Q8) {
+      const uint32_t id_8 = instr_desc8(NQ);  // (0: the tile's width goes there)
+      uint32_t raw0 = 0;                      // cached tiles before the segment
+      while (ok) {
+        ok = mbar_wait(bar(&C.seg_full[segs % AHEAD]), (segs / AHEAD) & 1, A.status, abort);
+        if (!ok) break;
+        const Seg s = C.seg[segs % AHEAD];
+        if (s.n == 0) break;
+        mbar_arrive(bar(&C.seg_empty[segs % AHEAD]));
+        const int slot = PAIR ? 0 : segs & 1;
+        const int use = PAIR ? segs : segs >> 1;
+        ok = mbar_wait(bar(&C.q_full[slot]), use & 1, A.status, abort);
+        tc_after();
+        const int n = s.n, c = cached_of(s);
+        // (tiles are whole but for the last cached and the staged ones)
+        auto width = [&](int j) { return j + 1 < c ? TILE : width_of(keys_of<PR>(A, s, s.j0 + j)); };
+        // S[st] (+)= the terms of query tile q with the term of keys at `ka`
+        auto term = [&](int st, int q, uint32_t ka, int w, bool more) {
+          const uint32_t id = NQ ? id_8 : id_8 | uint32_t(w >> 3) << 17;
+          const uint32_t dk = desc_rows(ka), dq = desc_rows(base + q * SM::Q_BYTES);
+#pragma unroll
+          for (int t = 0; t < TERMS; ++t)
+#pragma unroll
+            for (int k = 0; k < DP / 32; ++k) {
+              if (k * 32 >= A.D) break;
+              const uint32_t a = dq + ((t * SM::TERM + k * 32) >> 4), b = dk + ((k * 32) >> 4);
+              mma8_ss<DP>(tmem + st * S_COLS, NQ ? b : a, NQ ? a : b, id, more || t > 0 || k > 0);
+            }
+        };
+        // a staged tile's scores, all of its terms (pairs: for both query tiles)
+        auto staged_scores = [&](int st, int q, int i) {
+          const int w = width(i);
+#pragma unroll 1
+          for (int p = 0; p < PARTS; ++p) {
+            const uint32_t u = idx + wide_k<PAIR>(i, c, PARTS) + p;
+            if (!full(u)) return false;
+            const uint32_t at = base + SM::STAGE_AT + (u % STAGES) * BYTES;
+#pragma unroll 1
+            for (int x = 0; x < (PAIR ? 4 : 2); ++x) {
+              const int kt = x & 1, y = x >> 1;
+              if (2 * p + kt < TERMS) term(st + y, q + y, at + kt * SM::RAW, w, p > 0 || kt > 0);
+            }
+            mma_commit(bar(&C.empty[u % STAGES]));
+          }
+          mma_commit(bar(&C.s_full[st]));
+          if (PAIR) mma_commit(bar(&C.s_full[st + 1]));
+          return true;
+        };
+        // One copy of the scores' code: step j first finishes tile j - AHEAD8's values.
+        constexpr int AHEAD8 = PAIR ? 1 : 2;
+#pragma unroll 1
+        for (int i = 0; ok && i < n + AHEAD8; ++i) {
+          const int j = i - AHEAD8;  // the tile whose weights are next
+          const bool raw = i < c;
+          const uint32_t ku = raw0 + i, ks = ku % SM::RAW_K;
+          const uint32_t ka = base + SM::RAW_AT + ks * SM::RAW;
+          auto raw_here = [&] {
+            if (!mbar_wait(bar(&C.full[STAGES + ks]), (ku / SM::RAW_K) & 1, A.status, abort))
+              return false;
+            tc_after();
+            return true;
+          };
+          const uint32_t uv = idx + wide_v<PAIR>(j, n, c, PARTS);
+          const int w = width(j);
+          if (j >= 0) ok = full(uv);
+          if (raw) ok = ok && raw_here();
+#pragma unroll
+          for (int x = 0; x < (PAIR ? 2 : 1); ++x) {
+            const int st = PAIR ? x : i & 1;
+            if (j >= 0) {
+              ok = ok && first_half(st, uv, w, j > 0) &&
+                   mbar_wait(bar(&C.p_full[st]), p_use[st] & 1, A.status, abort);
+              ++p_use[st];
+              if (!ok) break;
+              tc_after();
+              values(st, uv, w, PAIR || j >= 2, PAIR ? 4 : 0, 8);
+              if (!PAIR || x == 1) mma_commit(bar(&C.empty[uv % STAGES]));
+              if (i >= n) mma_commit(bar(&C.o_full[st]));
+            }
+            if (ok && raw) {
+              term(st, PAIR ? x : slot, ka, width(i), false);
+              mma_commit(bar(&C.s_full[st]));
+              if (!PAIR || x == 1) mma_commit(bar(&C.empty[STAGES + ks]));
+            }
+          }
+          if (ok && i >= c && i < n) ok = staged_scores(PAIR ? 0 : i & 1, PAIR ? 0 : slot, i);
+          if (ok && i + 1 == n) mma_commit(bar(&C.q_empty[slot]));  // (queries done with)
+        }
+        idx += n + PARTS * (n - c);
+        raw0 += c;
+        ++segs;
+      }
+    }
+    while (!Q8 && ok) {
       ok = mbar_wait(bar(&C.seg_full[segs % AHEAD]), (segs / AHEAD) & 1, A.status, abort);
       if (!ok) break;
       const Seg s = C.seg[segs % AHEAD];
@@ -2244,12 +2739,12 @@ int launch_as(const AttnParams& A, int device, int grid, int ctas, cudaStream_t 
   if (!(raised.load(std::memory_order_acquire) & mark)) {
     if (cudaFuncSetAttribute(sv_attn<DP, NQ, PAIR, PR, BF, Q8>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (Smem<DP, NQ, Q8>::TOTAL)) != cudaSuccess)
+                             (Smem<DP, NQ, Q8 ? TERMS_OF<BF> : 0>::TOTAL)) != cudaSuccess)
       return SV_ERR_CUDA;
     raised.fetch_or(mark, std::memory_order_release);
   }
   sv_attn<DP, NQ, PAIR, PR, BF, Q8>
-      <<<grid, Q8 ? THREADS8 : THREADS, (Smem<DP, NQ, Q8>::TOTAL), st>>>(A);
+      <<<grid, Q8 ? THREADS8 : THREADS, (Smem<DP, NQ, Q8 ? TERMS_OF<BF> : 0>::TOTAL), st>>>(A);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
   if (PR || !A.join) return SV_OK;
   cudaLaunchConfig_t cfg = {};
