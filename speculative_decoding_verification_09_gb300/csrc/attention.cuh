@@ -58,8 +58,8 @@ static_assert(256 * SOFTMAX_REGS + 128 * OTHER_REGS <= THREADS * 168, "register 
 // more than few rows do.
 template <int NQ, bool Q8>
 struct Regs {
-  static constexpr int SOFTMAX = !Q8 ? SOFTMAX_REGS : NQ ? 144 : 192;
-  static constexpr int OTHER = !Q8 ? OTHER_REGS : NQ ? 72 : 56, WIDEN = NQ ? 128 : 72;
+  static constexpr int SOFTMAX = !Q8 ? SOFTMAX_REGS : NQ == 32 ? 160 : 144;
+  static constexpr int OTHER = !Q8 ? OTHER_REGS : NQ == 32 ? 80 : 96, WIDEN = NQ == 32 ? 112 : 128;
   static_assert(!Q8 || 256 * SOFTMAX + 128 * OTHER + 128 * WIDEN <= THREADS8 * 128,
                 "register split");
 };
@@ -1617,6 +1617,15 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         if (NQ == 0 && !ok) break;
         ++s_use;
         tc_after();
+        // Q8: the tile's powers of two
+        const Tile8* t8 = nullptr;
+        const uint32_t sc = (tiles8 + jj) % SCALES;
+        if (Q8) {
+          t8 = ky.staged ? &C8.staged[segs % SEGS][ky.k0 / TILE] : &C8.tile[sc];
+          if (!ky.staged)
+            ok = ok && warp_wait(bar(&C8.full[sc]), ((tiles8 + jj) / SCALES) & 1, A.status, abort);
+          if (NQ == 0 && !ok) break;
+        }
         // (The scores' keys have arrived, and so has every copy before them, among
         // them the last one into this tile's stage: its phase is the next.)
         if (clean && (!PAIR || st == 0)) {
@@ -1633,15 +1642,6 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-        }
-        // Q8: the tile's powers of two
-        const Tile8* t8 = nullptr;
-        const uint32_t sc = (tiles8 + jj) % SCALES;
-        if (Q8) {
-          t8 = ky.staged ? &C8.staged[segs % SEGS][ky.k0 / TILE] : &C8.tile[sc];
-          if (!ky.staged)
-            ok = ok && warp_wait(bar(&C8.full[sc]), ((tiles8 + jj) / SCALES) & 1, A.status, abort);
-          if (NQ == 0 && !ok) break;
         }
         auto half_done = [&] {  // PAIR: the weights of the tile's first 64 keys are stored
           if (!PAIR) return;
@@ -1795,7 +1795,54 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
               }
             }
           };
-          if constexpr (PAIR) {
+          if constexpr (Q8) {
+            // 32 scores at a time, for the maximum and again for the weights, in loops that are
+            // not unrolled: with the powers of two the code of a whole tile is longer than what
+            // is fetched in time (64 trees of 88 rows: 447 us unrolled).
+            uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+            if (masked) {
+              visible(see);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) see[x] &= span(0, w, 32 * x);
+            }
+            auto scores = [&](int x, uint32_t (&r)[32]) {
+              tm_ld32(ts + x * 32, r);
+              tm_wait_ld(r);
+              if (masked) {
+                const uint32_t bits = x == 0 ? see[0] : x == 1 ? see[1] : x == 2 ? see[2] : see[3];
+                if (!__all_sync(0xffffffffu, bits == 0xffffffffu)) {
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    if (!(bits >> i & 1)) r[i] = 0xff800000u;
+                }
+              }
+            };
+            float mt = -INFINITY;
+#pragma unroll 1
+            for (int x = 0; x * 32 < w; ++x) {
+              uint32_t r[32];
+              scores(x, r);
+              mt = fmaxf(mt, most(x, r));
+            }
+            raise_to(mt);
+            const float nm = (m == -INFINITY ? 0.0f : lift - m) + adj;
+            float2 sum[4] = {};
+#pragma unroll 1
+            for (int x = 0; x * 32 < w; ++x) {  // (P's columns lie over scores that are done with)
+              uint32_t r[32], pw[16];
+              scores(x, r);
+              weigh(x, r, nm, pw, sum);
+              tm_st16(ts + x * 16, pw);
+              if (x == 1) half_done();
+            }
+            if (w <= 32) {
+              __syncwarp();
+              half_done();
+            }
+            sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+            l += (sum[0].x + sum[0].y) * power(int(-adj));
+            __syncwarp();
+          } else if constexpr (PAIR) {
             uint32_t r[4][32];
             __syncwarp();
 #pragma unroll
@@ -1820,7 +1867,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
               }
             }
             float mt;
-            if (!Q8 && w == TILE) {
+            if (w == TILE) {
               mt = max_of<128>([&](int i) { return __uint_as_float(r[i >> 5][i & 31]); });
             } else {
               mt = -INFINITY;
@@ -1829,7 +1876,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
                 if (x * 32 < w) mt = fmaxf(mt, most(x, r[x]));
             }
             raise_to(mt);
-            const float nm = (m == -INFINITY ? 0.0f : lift - m * unit) + adj;
+            const float nm = m == -INFINITY ? 0.0f : lift - m * A.c;
             float2 sum[4] = {};
             uint32_t pw[16];
             auto chunk = [&](int x) { weigh(x, r[x], nm, pw, sum); };  // the weights of 32 keys
@@ -1853,7 +1900,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
               tm_st16<false>(ts + 48, pw);
             }
             sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-            l += Q8 ? (sum[0].x + sum[0].y) * power(int(-adj)) : sum[0].x + sum[0].y;
+            l += sum[0].x + sum[0].y;
           } else {
             // One tile of rows: 64 scores at a time, the maximum of the tile's second half,
             // then of its first, whose weights follow from registers; the second half is
@@ -1890,7 +1937,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
             float mt = w > 64 ? two(2) : -INFINITY;
             mt = fmaxf(mt, two(0));
             raise_to(mt);
-            const float nm = (m == -INFINITY ? 0.0f : lift - m * unit) + adj;
+            const float nm = m == -INFINITY ? 0.0f : lift - m * A.c;
             float2 sum[4] = {};
             auto weights = [&](int x, uint32_t (&r)[32]) {  // of 32 keys
               uint32_t pw[16];
@@ -1915,7 +1962,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
               }
             }
             sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-            l += Q8 ? (sum[0].x + sum[0].y) * power(int(-adj)) : sum[0].x + sum[0].y;
+            l += sum[0].x + sum[0].y;
           }
           tm_wait_st<false>();
         }
