@@ -59,12 +59,15 @@ static_assert(256 * SOFTMAX_REGS + 128 * OTHER_REGS <= THREADS * 168, "register 
 template <int NQ, bool Q8>
 struct Regs {
   static constexpr int SOFTMAX = !Q8 ? SOFTMAX_REGS : NQ == 32 ? 160 : 144;
-  static constexpr int OTHER = !Q8 ? OTHER_REGS : NQ == 32 ? 80 : 96, WIDEN = NQ == 32 ? 112 : 128;
-  static_assert(!Q8 || 256 * SOFTMAX + 128 * OTHER + 128 * WIDEN <= THREADS8 * 128,
+  static constexpr int OTHER = !Q8 ? OTHER_REGS : NQ == 32 ? 96 : 112;
+  static_assert(!Q8 || 256 * SOFTMAX + 256 * OTHER <= THREADS8 * 128,
                 "register split");
 };
-constexpr int COPY_WARP = 8, MMA_WARP = 9, PLAN_WARP = 10, SCALE_WARP = 11, WIDEN_WARP = 12,
-              WIDEN_WARPS = 4;
+constexpr int COPY_WARP = 8, MMA_WARP = 9, PLAN_WARP = 10;
+// 8-bit caches: 8 copies, 9 products, 12 plan, 13 scales; 10, 11, 14 and 15 widen.  A warp's
+// place goes by its number modulo 4, so no quarter of the SM fetches the code of more than
+// the softmax and two others.
+constexpr int PLAN8_WARP = 12, SCALE_WARP = 13, WIDEN_WARPS = 4;
 constexpr int MAX_CTAS = 152;   // one per SM
 constexpr unsigned long long WAIT_LIMIT_NS = 1000000000ull;
 constexpr uint32_t SUSPEND_HINT_NS = 20000;
@@ -472,8 +475,14 @@ struct Seg {
 // Tile j of a segment's item: its first key (of the cache, the staged entries or
 // the sequence) and its keys.
 struct Keys { int k0, n; bool staged; };
-template <bool PR>
+// (8-bit caches: the staged tiles come first, since what is made of them takes longest.)
+template <bool PR, bool Q8 = false>
 __device__ __forceinline__ Keys keys_of(const AttnParams& A, const Seg& s, int j) {
+  if (Q8) {
+    const int ts = tiles_of(A.N);
+    if (j < ts) return {j * TILE, min(TILE, A.N - j * TILE), true};
+    return {(j - ts) * TILE, min(TILE, s.len - (j - ts) * TILE), false};
+  }
   if (PR) {
     if (j < s.near) return {j * TILE, min(TILE, A.sink - j * TILE), false};
     const int k0 = s.first + (j - s.near) * TILE;
@@ -651,21 +660,20 @@ __device__ __forceinline__ int v_order(int j, int n) {
 }
 
 // 8-bit caches: the order is K_0 .. V_(i - LAG) K_i .. there, too.  Bytes have a ring for keys
-// and one for values; the 16-bit ring has all values of a segment of n tiles, c of them
-// cached, and `parts` stages with the terms of each staged tile's keys.
+// and one for values.  The 16-bit ring has all values of a segment, whose first g tiles are
+// staged, and `parts` stages with the terms of each staged tile's keys.
 template <bool PAIR>
 constexpr int LAG8 = PAIR ? 0 : 1;
 template <bool PAIR>
-__device__ __forceinline__ int wide_k(int i, int c, int parts) {
-  return parts * (i - c) + max(0, i - LAG8<PAIR>);
+__device__ __forceinline__ int wide_k(int i, int parts) {
+  return parts * i + max(0, i - LAG8<PAIR>);
 }
 template <bool PAIR>
-__device__ __forceinline__ int wide_v(int j, int n, int c, int parts) {
-  return j + parts * max(0, min(j + LAG8<PAIR>, n - 1) - c + 1);
+__device__ __forceinline__ int wide_v(int j, int g, int parts) {
+  return j + parts * min(j + LAG8<PAIR> + 1, g);
 }
-// The cached tiles of a segment.
-__device__ __forceinline__ int cached_of(const Seg& s) {
-  return min(max(tiles_of(s.len) - s.j0, 0), s.n);
+__device__ __forceinline__ int staged_of(const AttnParams& A, const Seg& s) {
+  return min(max(tiles_of(A.N) - s.j0, 0), s.n);
 }
 
 // Bits a .. b - 1 of the 32 keys from k0 on.
@@ -699,18 +707,21 @@ constexpr int CTRL8_BYTES = 4864;  // more of it with 8-bit caches
 // shared memory; the bytes' stages cover the copies' latency.
 template <bool BF>
 constexpr int TERMS_OF = BF ? 2 : 3;
-template <int DP, int NQ, int TERMS = 0>  // TERMS: 0 for 16-bit caches
+template <int DP, int NQ, int TERMS = 0, bool PAIR = false>  // TERMS: 0 for 16-bit caches
 struct Smem {
   static constexpr bool Q8 = TERMS > 0;
   static constexpr int BYTES = TILE * DP * 2;                    // a tile of keys or values
   static constexpr int TERM = (NQ ? NQ : TILE) * DP;             // a term of a tile of queries
   static constexpr int Q_BYTES = TERM * (Q8 ? TERMS : 2);        // a tile of queries
   static constexpr int P_BYTES = NQ * TILE * 2;                  // weights of a stream (NQ > 0)
-  static constexpr int P_AT = 2 * Q_BYTES;
+  // the next segment's queries have a place of their own, but for three terms of 128 rows of
+  // 128 dimensions, beside which three stages of bytes would remain
+  static constexpr int Q_SLOTS = TERMS == 3 && NQ == 0 && DP == 128 && !PAIR ? 1 : 2;
+  static constexpr int P_AT = Q_SLOTS * Q_BYTES;
   static constexpr int STAGE_AT = P_AT + 2 * P_BYTES;
   static constexpr int ROOM = 232448 - CTRL_BYTES - (Q8 ? CTRL8_BYTES : 0);
   static constexpr int FIT = (ROOM - STAGE_AT) / BYTES;
-  static constexpr int STAGES = Q8 ? (DP == 128 && NQ == 0 ? 2 : 3) : FIT < 12 ? FIT : 12;
+  static constexpr int STAGES = Q8 ? (DP == 128 ? 2 : 3) : FIT < 12 ? FIT : 12;
   static constexpr int RAW = TILE * DP;                          // a tile of bytes
   static constexpr int RAW_AT = STAGE_AT + STAGES * BYTES;
   static constexpr int RAW_FIT = (ROOM - RAW_AT) / RAW;
@@ -994,292 +1005,307 @@ __device__ __forceinline__ uint2 widen4(uint32_t w) {
   return r;
 }
 
-// A value's terms in e4m3: x = t1 + t2 (+ t3), each the rest rounded to nearest (16 values of
-// a thread, 16 bytes a term).  A rounding leaves at most 1/16 of a value, and of 8 bits of a
+// A value's terms in e4m3: x = t1 + t2 (+ t3), each the rest rounded to nearest (8 values, in
+// fp16, of a thread; 8 bytes a term).  A rounding leaves at most 1/16 of a value, and of 8 bits of a
 // mantissa (bf16) what is left has at most 4, so two terms are exact, of 11 (fp16) three; but
 // for what falls below the format's last step, 2^-9 where the largest value of the rows that
 // share a power of two is 224 or more: 2^-18 of that value, less than the rounding of the
-// sums of 32-bit products.  What is not finite is NaN in the first term.
+// sums of 32-bit products.
 template <int TERMS>
-__device__ __forceinline__ void split_terms(float (&x)[16], float by, uint4 (&out)[TERMS]) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = fabsf(x[i]) < INFINITY ? x[i] * by : __int_as_float(0x7fffffff);
+__device__ __forceinline__ void split_terms(const uint4& x, uint2 (&out)[TERMS]) {
+  uint32_t h[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
   for (int t = 0; t < TERMS; ++t) {
-    uint32_t w[4];
+    uint16_t p[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint16_t p[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float& a = x[4 * i + 2 * k];
-        float& b = x[4 * i + 2 * k + 1];
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p[k]) : "f"(b), "f"(a));
-        if (t + 1 < TERMS) {
-          uint32_t h;
-          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(p[k]));
-          float lo, hi;
-          asm("{\n .reg .b16 u, v;\n mov.b32 {u, v}, %2;\n cvt.f32.f16 %0, u;\n cvt.f32.f16 %1, v;\n}"
-              : "=f"(lo), "=f"(hi)
-              : "r"(h));
-          a -= lo;
-          b -= hi;
-        }
-      }
-      w[i] = uint32_t(p[0]) | uint32_t(p[1]) << 16;
+    for (int k = 0; k < 4; ++k) {
+      asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(p[k]) : "r"(h[k]));
+      if (t + 1 < TERMS)  // (exact: the rest is a multiple of the value's last step)
+        asm("{\n .reg .b32 y;\n cvt.rn.f16x2.e4m3x2 y, %1;\n sub.rn.f16x2 %0, %0, y;\n}"
+            : "+r"(h[k])
+            : "h"(p[k]));
     }
-    out[t] = make_uint4(w[0], w[1], w[2], w[3]);
+    out[t] = make_uint2(uint32_t(p[0]) | uint32_t(p[1]) << 16, uint32_t(p[2]) | uint32_t(p[3]) << 16);
   }
 }
-// Sixteen 16-bit values in 32 bits, and the largest finite size among them, as bits.
+// Eight 16-bit values times `by`, a power of two that makes them 448 at most, in fp16: exact
+// down to its smallest steps, 2^-33 of the largest.
 template <bool BF>
-__device__ __forceinline__ uint32_t widen16(const uint4 (&u)[2], float (&x)[16]) {
-  uint32_t most = 0;
+__device__ __forceinline__ uint4 to_half(const uint4& u, float by) {
+  uint32_t r[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint4& q = u[i / 4];
-    const uint32_t w = i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
+    float lo, hi;
     if (BF) {
-      x[2 * i] = __uint_as_float(w << 16);
-      x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+      lo = __uint_as_float(w << 16);
+      hi = __uint_as_float(w & 0xffff0000u);
     } else {
       asm("{\n .reg .b16 u, v;\n mov.b32 {u, v}, %2;\n cvt.f32.f16 %0, u;\n cvt.f32.f16 %1, v;\n}"
-          : "=f"(x[2 * i]), "=f"(x[2 * i + 1])
+          : "=f"(lo), "=f"(hi)
           : "r"(w));
     }
-#pragma unroll
-    for (int k = 2 * i; k < 2 * i + 2; ++k) {
-      const uint32_t a = __float_as_uint(x[k]) & 0x7fffffffu;
-      if (a < 0x7f800000u) most = max(most, a);
-    }
+    r[i] = pack16<false>(lo * by, hi * by);
   }
-  return most;
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
-// The smallest e with a <= 448 * 2^e (a finite size's bits), kept in the bytes' range.
+// The largest size among eight 16-bit values, as 32-bit float bits (of a NaN, a NaN's or more).
+template <bool BF>
+__device__ __forceinline__ uint32_t size_of(const uint4& u) {
+  uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
+                        __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+  m = max(m & 0xffffu, m >> 16);
+  if (BF) return m << 16;
+  float f;
+  asm("{\n .reg .b16 u, v;\n mov.b32 {u, v}, %1;\n cvt.f32.f16 %0, u;\n}" : "=f"(f) : "r"(m));
+  return __float_as_uint(f) & 0x7fffffffu;
+}
+// The smallest e with a <= 448 * 2^e (a size's bits), kept in the bytes' range; NOT_FINITE for
+// what is not: then the power of two is NaN, whatever the terms are.
+constexpr int NOT_FINITE = 127;
 __device__ __forceinline__ int exponent_over(uint32_t a) {
   const int e = int(a >> 23) - 127 - 8 + ((a & 0x7fffff) > 0x600000);
-  return min(max(e, -117), 119);
+  return a >= 0x7f800000u ? NOT_FINITE : min(max(e, -117), 119);
 }
-// The 16-byte piece of a row of DP bytes where products of bytes look for piece p.
+__device__ __forceinline__ float power_or_nan(int e) {
+  return e == NOT_FINITE ? __int_as_float(0x7fffffff) : power(e);
+}
+
+// Where products of bytes look for byte d of a row of DP bytes.
 template <int DP>
-__device__ __forceinline__ int swizzled(int row, int p) {
-  return DP == 128 ? row * 128 + ((p ^ (row & 7)) << 4) : row * 64 + ((p ^ (row >> 1 & 3)) << 4);
+__device__ __forceinline__ int swizzled(int row, int d) {
+  const int p = d >> 4;
+  return (DP == 128 ? row * 128 + ((p ^ (row & 7)) << 4) : row * 64 + ((p ^ (row >> 1 & 3)) << 4)) +
+         (d & 15);
 }
 
 // The widening warps, per segment: the queries' terms; then, in the order of the products,
-// the cached tiles' values from bytes to 16 bits (a thread takes 16 bytes, 16 dimensions of
-// a token, and writes two 16-byte pieces of a 64-dimension block in the 128-byte swizzle;
-// lanes of a row's two blocks write their pieces in opposite order, so that eight lanes
-// fall on eight pieces), the staged tiles' keys as terms, and their values.
-// One copy of each piece of code, loops rolled: much of it runs once a segment, and the
-// rest is bound by fetching instructions when it is longer.
+// the staged tiles' keys as terms, and their values, and the cached tiles' values from bytes to
+// 16 bits: a thread takes 16 bytes, 16 dimensions of a token, and writes two 16-byte pieces of a
+// 64-dimension block in the 128-byte swizzle.
+// One copy of each piece of code, and loops rolled: with 34 KB of code here (118 to 133 KB in
+// the kernel) whatever runs once an item was fetched anew each time.
 template <int DP, int NQ, bool PAIR, bool BF>
 __device__ __forceinline__ void widen_tiles(const AttnParams& A, Ctrl<NQ, PAIR>& C, Ctrl8<NQ>& C8,
                                             unsigned char* smem, volatile int* abort) {
   constexpr int TERMS = TERMS_OF<BF>, PARTS = (TERMS + 1) / 2, LAG = LAG8<PAIR>;
-  using SM = Smem<DP, NQ, TERMS>;
+  using SM = Smem<DP, NQ, TERMS, PAIR>;
   constexpr int STAGES = SM::STAGES;
-  constexpr int PER_ROW = DP / 16;                            // pieces of a row
-  constexpr int STEPS = TILE * PER_ROW / (32 * WIDEN_WARPS);  // pieces of a thread
+  constexpr int PER_ROW = DP / 16;                            // threads of a row
   constexpr int ROWS = 32 * WIDEN_WARPS / PER_ROW;            // rows of a step
+  constexpr int STEPS = TILE / ROWS, WARP_ROWS = 32 / PER_ROW;
   constexpr int BATCH = 4;
   constexpr int Q_ROWS = NQ ? NQ : TILE;
   static_assert(STEPS % BATCH == 0, "whole rounds");
-  const int tid = int(threadIdx.x) - WIDEN_WARP * 32, warp = tid >> 5, lane = tid & 31;
-  const int row0 = tid / PER_ROW, piece = tid % PER_ROW;
+  const int lane = int(threadIdx.x) & 31;
+  const int warp = (int(threadIdx.x) >> 5 & 1) | (int(threadIdx.x) >> 6 & 2), tid = warp * 32 + lane;
+  const int row0 = tid / PER_ROW, dim = tid % PER_ROW * 16, lane_row = lane / PER_ROW;
   uint32_t out = 0, raw0 = 0;  // 16-bit stages and cached tiles so far
   bool ok = true;
+  auto wait = [&](unsigned long long* b, uint32_t parity) {
+    ok = ok && warp_wait(smem_addr(b), parity, A.status, abort);
+  };
   auto filled = [&](unsigned long long* full) {  // what was written is there for the products
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_addr(full));
   };
   // 16 dimensions of a row of 16-bit values; zeros where there are none
-  auto fetch = [&](const uint16_t* src, bool on, uint4 (&u)[2]) {
-    u[0] = u[1] = make_uint4(0, 0, 0, 0);
-    if (on && piece * 16 < A.D) {
-      const uint4* const p = reinterpret_cast<const uint4*>(src + piece * 16);
-      u[0] = __ldg(p);
-      u[1] = __ldg(p + 1);
+  struct Row { uint4 lo, hi; };
+  auto fetch = [&](const uint16_t* src, bool on) {
+    Row r = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (on && dim < A.D) {
+      r.lo = __ldg(reinterpret_cast<const uint4*>(src + dim));
+      r.hi = __ldg(reinterpret_cast<const uint4*>(src + dim) + 1);
     }
+    return r;
   };
-  for (int segs = 0;; ++segs) {
-    ok = warp_wait(smem_addr(&C.seg_full[segs % SEGS]), (segs / SEGS) & 1, A.status, abort);
-    if (!ok) break;
-    const Seg s = C.seg[segs % SEGS];
-    if (s.n == 0) break;
-    const int n = s.n, c = cached_of(s);
-    // ---- queries
-    {
-      const int slot = PAIR ? 0 : segs & 1, use = PAIR ? segs : segs >> 1;
-      ok = warp_wait(smem_addr(&C.q_empty[slot]), (use & 1) ^ 1, A.status, abort);
-      if (!ok) break;
+  auto size = [](const Row& r) { return max(size_of<BF>(r.lo), size_of<BF>(r.hi)); };
+  // their terms, written where the products look for them
+  auto terms = [&](const Row& u, float by, unsigned char* to, int stride, int first, int count) {
+    uint2 lo[TERMS], hi[TERMS];
+    split_terms<TERMS>(to_half<BF>(u.lo, by), lo);
+    split_terms<TERMS>(to_half<BF>(u.hi, by), hi);
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t)
+      if (t >= first && t < first + count)
+        *reinterpret_cast<uint4*>(to + (t - first) * stride) =
+            make_uint4(lo[t].x, lo[t].y, hi[t].x, hi[t].y);
+  };
+  // the queries of segment `segs`, once it is planned and their place is free
+  constexpr bool TURNS = !PAIR && SM::Q_SLOTS == 2;
+  auto queries = [&](int segs) {
+    wait(&C.seg_full[segs % SEGS], (segs / SEGS) & 1);
+    if (!ok) return;
+    const Seg& s = C.seg[segs % SEGS];
+    if (s.n == 0) return;
+    const int slot = TURNS ? segs & 1 : 0, use = TURNS ? segs >> 1 : segs;
+    wait(&C.q_empty[slot], (use & 1) ^ 1);
+    if (!ok) return;
+    const int first = s.mt * (PAIR ? 2 : 1) * A.tpt;
+    auto row_of = [&](int r) {  // of a query row of the tiles
+      const int tile = r / Q_ROWS, rr = r - tile * Q_ROWS, rt = rr / A.G;
+      const int tok = first + tile * A.tpt + rt;
+      return fetch(A.q + ((size_t(s.b) * A.N + tok) * A.Hq + s.h * A.G + (rr - rt * A.G)) * A.D,
+                   rt < A.tpt && tok < A.N);
+    };
+    // (two rows at once, the next two on their way; every lane of a warp goes round as often)
+    constexpr int ALL = (PAIR ? 2 : 1) * Q_ROWS;
+    Row next[2] = {row_of(row0), row_of(row0 + ROWS)};
 #pragma unroll 1
-      for (int r = row0; r < (PAIR ? 2 : 1) * Q_ROWS; r += ROWS) {
-        const int tile = r / Q_ROWS, rr = r - tile * Q_ROWS, rt = rr / A.G;
-        const int tok = (s.mt * (PAIR ? 2 : 1) + tile) * A.tpt + rt;
-        uint4 u[2];
-        fetch(A.q + ((size_t(s.b) * A.N + tok) * A.Hq + s.h * A.G + (rr - rt * A.G)) * A.D,
-              rt < A.tpt && tok < A.N, u);
-        float x[16];
-        uint32_t most = widen16<BF>(u, x);
-        // (lanes of a row are neighbours, and every lane of a warp goes round as often)
+    for (int r0 = row0; r0 < ALL; r0 += 2 * ROWS) {
+      const Row u[2] = {next[0], next[1]};
+      next[0] = row_of(r0 + 2 * ROWS);  // (behind the last: not used)
+      next[1] = row_of(r0 + 3 * ROWS);
 #pragma unroll
-        for (int k = 1; k < PER_ROW; k *= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, k));
+      for (int i = 0; i < 2; ++i) {
+        const int r = r0 + i * ROWS;
+        uint32_t most = size(u[i]);
+#pragma unroll
+        for (int k = 1; k < PER_ROW; k *= 2)  // (a row's lanes are neighbours)
+          most = max(most, __shfl_xor_sync(0xffffffffu, most, k));
         const int e = exponent_over(most);
-        uint4 t[TERMS];
-        split_terms<TERMS>(x, power(-e), t);
-        unsigned char* const dst = smem + (PAIR ? tile : slot) * SM::Q_BYTES + swizzled<DP>(rr, piece);
-#pragma unroll
-        for (int k = 0; k < TERMS; ++k) *reinterpret_cast<uint4*>(dst + k * SM::TERM) = t[k];
-        if (piece == 0) {
-          if (NQ) C8.qf[segs % SEGS][rr] = power(e);
-          else C8.qx[segs % SEGS][r] = uint8_t(e + 127);
+        const int tile = r / Q_ROWS, rr = r - tile * Q_ROWS;
+        if (r < ALL) {
+          terms(u[i], power(-min(e, 119)),
+                smem + (PAIR ? tile : slot) * SM::Q_BYTES + swizzled<DP>(rr, dim), SM::TERM, 0, TERMS);
+          if (dim == 0) {
+            if (NQ) C8.qf[segs % SEGS][rr] = power_or_nan(e);
+            else C8.qx[segs % SEGS][r] = e == NOT_FINITE ? 255 : uint8_t(e + 127);
+          }
         }
       }
-      filled(&C.q_full[slot]);
     }
-    // ---- tiles
+    filled(&C.q_full[slot]);
+  };
+  int asked = 0;  // segments whose queries are done
+  for (int segs = 0;; ++segs) {
+    Seg s;
+    int n = 0, g0 = 0;
 #pragma unroll 1
-    for (int x = 0; x < 2 * (n + LAG); ++x) {
+    for (int x = -1; x < 2 * (n + LAG); ++x) {
+      // the next segment's queries, ahead of its first product (or, at the start, this one's)
+      if (x < 0 ? asked == segs : TURNS && asked == segs + 1 && (x == 2 * (g0 + 2) || x == 2 * n)) {
+        queries(asked);
+        ++asked;
+        if (!ok) break;
+      }
+      if (x < 0) {
+        s = C.seg[segs % SEGS];
+        n = s.n;
+        if (n == 0) break;
+        g0 = staged_of(A, s);
+        continue;
+      }
       const bool is_v = x & 1;
       const int j = is_v ? (x >> 1) - LAG : x >> 1;
-      if (j < 0 || j >= n || (!is_v && j < c)) continue;
-      const Keys ky = keys_of<false>(A, s, s.j0 + j);
-      const uint32_t st = out % STAGES;
-      unsigned char* const dst = smem + SM::STAGE_AT + st * SM::BYTES;
-      ok = warp_wait(smem_addr(&C.empty[st]), ((out / STAGES) & 1) ^ 1, A.status, abort);
-      if (!ok) break;
-      // a row's piece of the 16-bit tile, as two pieces of 16 bytes
-      auto put = [&](int row, const uint4& lo, const uint4& hi) {
-        unsigned char* const line = dst + (piece >> 2) * 16384 + row * 128;
-        const int at = (piece & 3) * 2, swap = piece >> 2;
-        *reinterpret_cast<uint4*>(line + (((at + swap) ^ (row & 7)) << 4)) = swap ? hi : lo;
-        *reinterpret_cast<uint4*>(line + (((at + 1 - swap) ^ (row & 7)) << 4)) = swap ? lo : hi;
-      };
-      if (is_v && j < c) {
-        const uint32_t u = raw0 + j, rs = SM::RAW_K + u % SM::RAW_V;
-        const unsigned char* const src = smem + SM::RAW_AT + rs * SM::RAW + tid * 16;
-        ok = warp_wait(smem_addr(&C.full[STAGES + rs]), (u / SM::RAW_V) & 1, A.status, abort);
-        if (!ok) break;
-#pragma unroll 1
-        for (int g = 0; g < STEPS; g += BATCH) {
-          uint4 b[BATCH];
-#pragma unroll
-          for (int i = 0; i < BATCH; ++i) {
-            b[i] = *reinterpret_cast<const uint4*>(src + (g + i) * (32 * WIDEN_WARPS * 16));
-            // (behind the entries: whatever the bytes are, weights of 0 take zeros)
-            if (row0 + (g + i) * ROWS >= ky.n) b[i] = make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int i = 0; i < BATCH; ++i) {
-            const uint2 p = widen4(b[i].x), q = widen4(b[i].y), y = widen4(b[i].z), z = widen4(b[i].w);
-            put(row0 + (g + i) * ROWS, make_uint4(p.x, p.y, q.x, q.y), make_uint4(y.x, y.y, z.x, z.y));
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&C.empty[STAGES + rs]));
-        filled(&C.full[st]);
-        ++out;
-        continue;
-      }
+      if (j < 0 || j >= n || (!is_v && j >= g0)) continue;
+      const Keys ky = keys_of<false, true>(A, s, s.j0 + j);
+      const int w = width_of(ky);
       const size_t from = ((size_t(s.b) * A.LH + A.head0 + s.h) * A.N + ky.k0) * A.D;
-      Tile8& t8 = C8.staged[segs % SEGS][ky.k0 / TILE];
-      constexpr int V = PER_ROW / 4;  // pieces of a lane in eight rows
-      if (is_v) {  // staged values, eight rows at a power of two (the warp's own eights)
+      Tile8& t8 = C8.staged[segs % SEGS][ky.k0 / TILE & 1];  // (of a staged tile)
 #pragma unroll 1
-        for (int g = warp; g * 8 < width_of(ky); g += WIDEN_WARPS) {  // (products read no further)
-          const float by = g * 8 < ky.n ? power(-int(t8.ev[g])) : 0.0f;
+      for (int part = 0; part < (is_v ? 1 : PARTS); ++part) {
+        const uint32_t st = out % STAGES;
+        unsigned char* const dst = smem + SM::STAGE_AT + st * SM::BYTES;
+        // a row's 16 dimensions of the 16-bit tile: lanes of a row's two blocks write their
+        // pieces in opposite order, so that eight lanes fall on eight pieces
+        auto put = [&](int row, const uint4& lo, const uint4& hi) {
+          unsigned char* const line = dst + (dim >> 6) * 16384 + row * 128;
+          const int at = dim >> 3 & 7, swap = dim >> 6;
+          *reinterpret_cast<uint4*>(line + (((at + swap) ^ (row & 7)) << 4)) = swap ? hi : lo;
+          *reinterpret_cast<uint4*>(line + (((at + 1 - swap) ^ (row & 7)) << 4)) = swap ? lo : hi;
+        };
+        const uint32_t u = raw0 + j - g0, rs = SM::RAW_K + u % SM::RAW_V;
+        wait(&C.empty[st], ((out / STAGES) & 1) ^ 1);
+        if (j >= g0) wait(&C.full[STAGES + rs], (u / SM::RAW_V) & 1);
+        if (!ok) break;
+        if (j >= g0) {
+          // ---- cached values
+          const unsigned char* const src = smem + SM::RAW_AT + rs * SM::RAW + tid * 16;
+#pragma unroll 1
+          for (int g = 0; g < STEPS; g += BATCH) {
+            uint4 b[BATCH];
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const int row = g * 8 + i * 4 + lane / PER_ROW;
-            uint4 u[2];
-            fetch(A.v_new + from + size_t(row) * A.D, row < ky.n, u);
-            float v[16];
-            widen16<BF>(u, v);
-            uint32_t w[8];
+            for (int i = 0; i < BATCH; ++i)
+              b[i] = *reinterpret_cast<const uint4*>(src + (g + i) * (32 * WIDEN_WARPS * 16));
 #pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = pack16<false>(v[2 * k] * by, v[2 * k + 1] * by);
-            put(row, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
+            for (int i = 0; i < BATCH; ++i) {
+              const uint2 p = widen4(b[i].x), q = widen4(b[i].y), y = widen4(b[i].z), z = widen4(b[i].w);
+              put(row0 + (g + i) * ROWS, make_uint4(p.x, p.y, q.x, q.y), make_uint4(y.x, y.y, z.x, z.y));
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&C.empty[STAGES + rs]));
+          // behind the entries: whatever the bytes are, weights of 0 take zeros
+          if (ky.n < w) {
+#pragma unroll 1
+            for (int row = row0; row < w; row += ROWS)
+              if (row >= ky.n) put(row, make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0));
+          }
+        } else {
+          // ---- staged: a warp takes eight rows at a time, which share a power of two
+#pragma unroll 1
+          for (int g = warp; g * 8 < w; g += WIDEN_WARPS) {
+            constexpr int V = 8 / WARP_ROWS;  // rows of a lane: 1 or 2
+            Row k[V];
+            uint32_t k_most = 0, v_most = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              const int row = g * 8 + i * WARP_ROWS + lane_row;
+              const uint16_t* const at = (is_v ? A.v_new : A.k_new) + from + size_t(row) * A.D;
+              k[i] = fetch(at, row < ky.n);
+              k_most = max(k_most, size(k[i]));
+              if (!is_v && part == 0)
+                v_most = max(v_most, size(fetch(A.v_new + from + size_t(row) * A.D, row < ky.n)));
+            }
+            const int e = is_v ? int(t8.ev[g]) : exponent_over(__reduce_max_sync(0xffffffffu, k_most));
+            if (!is_v && part == 0) {
+              const int ev = exponent_over(__reduce_max_sync(0xffffffffu, v_most));
+              if (lane == 0) {
+                t8.kf[g] = power_or_nan(e);
+                t8.ev[g] = int8_t(e == NOT_FINITE ? e : ev);
+              }
+            }
+            const float by = power(-min(e, 119));
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              const int row = g * 8 + i * WARP_ROWS + lane_row;
+              if (is_v) put(row, to_half<BF>(k[i].lo, by), to_half<BF>(k[i].hi, by));
+              else terms(k[i], by, dst + swizzled<DP>(row, dim), SM::RAW, 2 * part, 2);
+            }
+          }
+          if (!is_v && part == 0) {  // the last warp to get here puts the values' powers of two together
+            __syncwarp();
+            __threadfence_block();
+            int last = 0;
+            if (lane == 0) last = atomicAdd(&t8.count, 1) == WIDEN_WARPS - 1;
+            if (__shfl_sync(0xffffffffu, last, 0)) {
+              __threadfence_block();
+              const int ev = lane < 16 && lane * 8 < ky.n
+                                 ? int(reinterpret_cast<volatile int8_t*>(t8.ev)[lane])
+                                 : -1000;
+              const int top = __reduce_max_sync(0xffffffffu, ev == NOT_FINITE ? 0 : ev);
+              const int by = max(ev - top, LEAST);
+              const float nan = __int_as_float(0x7fffffff);
+              if (lane < 16) {
+                t8.vd[lane] = ev == NOT_FINITE ? nan : float(by);
+                t8.vf[lane] = ev == NOT_FINITE ? nan : power(NQ ? by : -by);
+              }
+              if (lane == 0) {
+                t8.top = top;
+                t8.count = 0;
+              }
+            }
           }
         }
         filled(&C.full[st]);
-        ++out;
-        continue;
-      }
-      // staged keys: a warp takes eight rows at a time, which share a power of two; and the
-      // values' powers of two, which the weights need before the values
-#pragma unroll 1
-      for (int part = 0; part < PARTS; ++part) {
-        if (part) {
-          const uint32_t s2 = out % STAGES;
-          ok = warp_wait(smem_addr(&C.empty[s2]), ((out / STAGES) & 1) ^ 1, A.status, abort);
-          if (!ok) break;
-        }
-        unsigned char* const to = smem + SM::STAGE_AT + (out % STAGES) * SM::BYTES;
-#pragma unroll 1
-        for (int g = warp; g * 8 < ky.n; g += WIDEN_WARPS) {
-          float v[V][16];
-          uint32_t most = 0, v_most = 0;
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const int row = g * 8 + i * 4 + lane / PER_ROW;
-            uint4 u[2];
-            if (part == 0) {
-              fetch(A.v_new + from + size_t(row) * A.D, row < ky.n, u);
-              v_most = max(v_most, widen16<BF>(u, v[i]));
-            }
-            fetch(A.k_new + from + size_t(row) * A.D, row < ky.n, u);
-            most = max(most, widen16<BF>(u, v[i]));
-          }
-          const int e = exponent_over(__reduce_max_sync(0xffffffffu, most));
-          if (part == 0) {
-            const int ev = exponent_over(__reduce_max_sync(0xffffffffu, v_most));
-            if (lane == 0) {
-              t8.kf[g] = power(e);
-              t8.ev[g] = int8_t(ev);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const int row = g * 8 + i * 4 + lane / PER_ROW;
-            uint4 t[TERMS];
-            split_terms<TERMS>(v[i], power(-e), t);
-            unsigned char* const at = to + swizzled<DP>(row, piece);
-            if (part == 0) {
-              *reinterpret_cast<uint4*>(at) = t[0];
-              if (TERMS > 1) *reinterpret_cast<uint4*>(at + SM::RAW) = t[1];
-            } else {
-              *reinterpret_cast<uint4*>(at) = t[TERMS - 1];
-            }
-          }
-        }
-        if (part == 0) {  // the last warp to get here puts the values' powers of two together
-          __syncwarp();
-          __threadfence_block();
-          int last = 0;
-          if (lane == 0) last = atomicAdd(&t8.count, 1) == WIDEN_WARPS - 1;
-          if (__shfl_sync(0xffffffffu, last, 0)) {
-            __threadfence_block();
-            const int ev = lane < 16 && lane * 8 < ky.n ? int(reinterpret_cast<volatile int8_t*>(t8.ev)[lane]) : -1000;
-            const int top = __reduce_max_sync(0xffffffffu, ev), by = max(ev - top, LEAST);
-            if (lane < 16) {
-              t8.vd[lane] = float(by);
-              t8.vf[lane] = power(NQ ? by : -by);
-            }
-            if (lane == 0) {
-              t8.top = top;
-              t8.count = 0;
-            }
-          }
-        }
-        filled(&C.full[out % STAGES]);
         ++out;
       }
       if (!ok) break;
     }
-    if (!ok) break;
-    raw0 += c;
+    if (!ok || n == 0) break;
+    raw0 += n - g0;
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_addr(&C.seg_empty[segs % SEGS]));
   }
@@ -1304,12 +1330,13 @@ __device__ __forceinline__ void read_scales(const AttnParams& A, Ctrl<NQ, PAIR>&
     if (s.n == 0) break;
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_addr(&C.seg_empty[segs % SEGS]));
-    const int c = cached_of(s);
+    const int g = staged_of(A, s), c = s.n - g;
+    const int first = s.j0 + g - tiles_of(A.N);  // cached tile
     for (int j = 0; ok && j < c; j += at_once) {
       // (blocks behind the entries: no part in the tile's largest exponent)
       int k = 0, v = -1000;
       bool nan = false;
-      const int t = (s.j0 + j + mine) * TILE + (block << A.block_log);
+      const int t = (first + j + mine) * TILE + (block << A.block_log);
       if (mine < at_once && j + mine < c && t < s.len) {
         const int col = t / A.page;
         int pg = __ldg(A.table + size_t(s.b) * A.cols + col);
@@ -1366,7 +1393,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
   static_assert(!(NQ && (PAIR || PR)), "few rows make one tile, and prompts have many");
   static_assert(!(Q8 && PR), "8-bit entries are in pages");
   constexpr int TERMS = Q8 ? TERMS_OF<BF> : 0, PARTS = (TERMS + 1) / 2;
-  using SM = Smem<DP, NQ, TERMS>;
+  using SM = Smem<DP, NQ, TERMS, PAIR>;
   constexpr int NT = Q8 ? THREADS8 : THREADS;
   constexpr int STAGES = SM::STAGES, BYTES = SM::BYTES, HALVES = DP / 64;
   constexpr int ROWS = NQ ? NQ : PAIR ? 2 * TILE : TILE;
@@ -1534,17 +1561,22 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
       const bool active = rt < A.tpt && tok < tokens;
       const bool warp_active = __any_sync(0xffffffffu, active);
       const int ct = tiles_of(s.len);
+      const int staged = Q8 ? staged_of(A, s) : 0;  // (the first tiles)
+      // the segment's cached tiles, of the request's, and whether it has staged ones
+      const int c0 = Q8 ? max(s.j0 - tiles_of(A.N), 0) : s.j0;
+      const int c1 = Q8 ? s.j0 + n - tiles_of(A.N) : s.j0 + n;
+      const bool has_staged = Q8 ? staged > 0 : s.j0 + n > ct;
       int bad = s.bad;
-      if (!PR && A.kind == TREE) {
+      if (!PR && (Q8 || A.kind == TREE)) {
         // pages in use by this segment, and the parent array
         int pages_bad = 0;
-        const int t1 = min(s.len, (s.j0 + n) * TILE);
-        if (s.j0 * TILE < t1)
-          for (int c = s.j0 * TILE / A.page + row; c <= (t1 - 1) / A.page; c += TILE) {
+        const int t1 = min(s.len, c1 * TILE);
+        if (c0 * TILE < t1)
+          for (int c = c0 * TILE / A.page + row; c <= (t1 - 1) / A.page; c += TILE) {
             const int pg = __ldg(A.table + size_t(s.b) * A.cols + c);
             pages_bad |= pg < 0 || pg >= A.num_pages;
           }
-        if (A.parent && s.b != parent_b && s.j0 + n > ct) {
+        if (A.parent && s.b != parent_b && has_staged) {
           if constexpr (NQ > 0)
             if (row < NQ) C.x.sees[st][row] = 0;
           int wrong = 0;
@@ -1566,11 +1598,11 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
           }
         }
         if (group_or(1 + st, TILE, pages_bad)) bad |= SV_ST_BAD_PAGE;
-        if (s.j0 + n > ct && A.parent) bad |= parent_bad;
+        if (has_staged && A.parent) bad |= parent_bad;
       }
       if (bad && tid == 0) set_status(A.status, bad);
-      const int ring_at = PR ? -1 : s.ring;
-      const bool ring_full = !PR && s.full;
+      const int ring_at = PR || Q8 ? -1 : s.ring;  // (8-bit entries are in pages)
+      const bool ring_full = !PR && !Q8 && s.full;
       const int q0 = s.mt * tpi, q1 = min(q0 + tpi, tokens) - 1;  // the item's tokens
       const int w0 = q0 + (PAIR ? st * A.tpt : 0), w1 = min(w0 + A.tpt, tokens) - 1;  // the tile's
 
@@ -1581,13 +1613,12 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
       float m = -INFINITY, l = 0.0f;
       float lq[NQ ? NQ : 1];  // NQ > 0: this key's share of the columns' sums
       bool unset = true;      // NQ > 0: a column has seen nothing yet
-      const int cached = Q8 ? cached_of(s) : 0;
 #pragma unroll
       for (int q = 0; q < NQ; ++q) lq[q] = 0.0f;
       int done = 0;
       for (int jj = PAIR ? 0 : st; jj < n; jj += PAIR ? 1 : 2, ++done) {
         const int j = s.j0 + jj;
-        const Keys ky = keys_of<PR>(A, s, j);
+        const Keys ky = keys_of<PR, Q8>(A, s, j);
         const int k0 = ky.k0, w = width_of(ky);
         // does the tile need a mask, and value rows that no query of the item sees
         // (among the w that the products take) zeroed?
@@ -1619,11 +1650,11 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         tc_after();
         // Q8: the tile's powers of two
         const Tile8* t8 = nullptr;
-        const uint32_t sc = (tiles8 + jj) % SCALES;
+        const uint32_t tile8 = tiles8 + jj - staged, sc = tile8 % SCALES;
         if (Q8) {
           t8 = ky.staged ? &C8.staged[segs % SEGS][ky.k0 / TILE] : &C8.tile[sc];
           if (!ky.staged)
-            ok = ok && warp_wait(bar(&C8.full[sc]), ((tiles8 + jj) / SCALES) & 1, A.status, abort);
+            ok = ok && warp_wait(bar(&C8.full[sc]), (tile8 / SCALES) & 1, A.status, abort);
           if (NQ == 0 && !ok) break;
         }
         // (The scores' keys have arrived, and so has every copy before them, among
@@ -1677,7 +1708,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
           half_done();
         } else {
           // Q8: what the scores of eight keys are multiplied by, and the weights' exponents moved by
-          float qc = 0.0f, adj = 0.0f, sink = 1.0f;
+          float qc = 0.0f, adj = 0.0f, spoilt = 0.0f, sink = 1.0f;
           if (Q8) {
             qc = A.c * power_of(C8.qx[segs % SEGS][(PAIR ? st * TILE : 0) + row]);
             if (done == 0 || t8->top > top) {
@@ -1685,6 +1716,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
               top = t8->top + VALUE_SLACK;
             }
             adj = float(max(t8->top - top, LEAST));
+            spoilt = qc - qc;  // NaN with the row's power of two, else 0
           }
           auto factors = [&](int x) {  // (not 0: hidden scores stay at -infinity)
             const float4 k = *reinterpret_cast<const float4*>(t8->kf + 4 * x);
@@ -1692,7 +1724,6 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
                                fmaxf(qc * k.z, 1e-37f), fmaxf(qc * k.w, 1e-37f));
           };
           auto most = [&](int x, uint32_t (&r)[32]) {  // the largest of 32 scores
-            if (!Q8) return max_of<32>([&](int i) { return __uint_as_float(r[i]); });
             const float4 f = factors(x);
             float t[4];
 #pragma unroll
@@ -1706,37 +1737,25 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
           // the weights of 32 keys, and their sum
           auto weigh = [&](int x, const uint32_t (&r)[32], float nm, uint32_t (&pw)[16],
                            float2 (&sum)[4]) {
-            if (Q8) {
-              const float4 f = factors(x);
-              const float4 d = *reinterpret_cast<const float4*>(t8->vd + 4 * x);
-              const float4 v = *reinterpret_cast<const float4*>(t8->vf + 4 * x);
+            const float4 f = factors(x);
+            const float4 d = *reinterpret_cast<const float4*>(t8->vd + 4 * x);
+            const float4 v = *reinterpret_cast<const float4*>(t8->vf + 4 * x);
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                const float fg = g == 0 ? f.x : g == 1 ? f.y : g == 2 ? f.z : f.w;
-                const float dg = nm + (g == 0 ? d.x : g == 1 ? d.y : g == 2 ? d.z : d.w);
-                const float vg = g == 0 ? v.x : g == 1 ? v.y : g == 2 ? v.z : v.w;
-                float2 t = make_float2(0.0f, 0.0f);
+            for (int g = 0; g < 4; ++g) {
+              const float fg = g == 0 ? f.x : g == 1 ? f.y : g == 2 ? f.z : f.w;
+              const float dg = nm + (g == 0 ? d.x : g == 1 ? d.y : g == 2 ? d.z : d.w);
+              const float vg = g == 0 ? v.x : g == 1 ? v.y : g == 2 ? v.z : v.w;
+              float2 t = make_float2(0.0f, 0.0f);
 #pragma unroll
-                for (int i = 4 * g; i < 4 * g + 4; ++i) {
-                  const float2 e = fma2(
-                      make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
-                      make_float2(fg, fg), make_float2(dg, dg));
-                  const float2 p = make_float2(ex2(e.x), ex2(e.y));
-                  t = add2(t, p);
-                  pw[i] = pack16<false>(p.x, p.y);
-                }
-                sum[g] = fma2(t, make_float2(vg, vg), sum[g]);
+              for (int i = 4 * g; i < 4 * g + 4; ++i) {
+                const float2 e = fma2(
+                    make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
+                    make_float2(fg, fg), make_float2(dg, dg));
+                const float2 p = make_float2(ex2(e.x), ex2(e.y));
+                t = add2(t, p);
+                pw[i] = pack16<false>(p.x, p.y);
               }
-              return;
-            }
-            const float2 c2 = make_float2(A.c, A.c), mc2 = make_float2(nm, nm);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 e = fma2(make_float2(__uint_as_float(r[2 * i]),
-                                                __uint_as_float(r[2 * i + 1])), c2, mc2);
-              const float2 p = make_float2(ex2(e.x), ex2(e.y));
-              sum[i & 3] = add2(sum[i & 3], p);
-              pw[i] = pack16<BF>(p.x, p.y);
+              sum[g] = fma2(t, make_float2(vg, vg), sum[g]);
             }
           };
           // the tile's keys that this row sees, 32 to a word
@@ -1825,7 +1844,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
               mt = fmaxf(mt, most(x, r));
             }
             raise_to(mt);
-            const float nm = (m == -INFINITY ? 0.0f : lift - m) + adj;
+            const float nm = (m == -INFINITY ? 0.0f : lift - m) + adj + spoilt;
             float2 sum[4] = {};
 #pragma unroll 1
             for (int x = 0; x * 32 < w; ++x) {  // (P's columns lie over scores that are done with)
@@ -1873,13 +1892,24 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
               mt = -INFINITY;
 #pragma unroll
               for (int x = 0; x < 4; ++x)
-                if (x * 32 < w) mt = fmaxf(mt, most(x, r[x]));
+                if (x * 32 < w)
+                  mt = fmaxf(mt, max_of<32>([&](int i) { return __uint_as_float(r[x][i]); }));
             }
             raise_to(mt);
             const float nm = m == -INFINITY ? 0.0f : lift - m * A.c;
+            const float2 c2 = make_float2(A.c, A.c), mc2 = make_float2(nm, nm);
             float2 sum[4] = {};
             uint32_t pw[16];
-            auto chunk = [&](int x) { weigh(x, r[x], nm, pw, sum); };  // the weights of 32 keys
+            auto chunk = [&](int x) {  // the weights of 32 keys
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float2 e = fma2(make_float2(__uint_as_float(r[x][2 * i]),
+                                                  __uint_as_float(r[x][2 * i + 1])), c2, mc2);
+                const float2 p = make_float2(ex2(e.x), ex2(e.y));
+                sum[i & 3] = add2(sum[i & 3], p);
+                pw[i] = pack16<BF>(p.x, p.y);
+              }
+            };
             // the products with the first 64 keys' values start under the others' weights
             // (One copy for all widths, fewer instructions to fetch: a second one for whole
             // tiles took 1280 items of 16 tiles from 222 us to 244, 8192 tokens to 318 as now.)
@@ -1927,10 +1957,10 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
               tm_wait_ld(r0);
               tm_loaded(r1);
               hide(r0, see[x]);
-              float t = most(x, r0);
+              float t = max_of<32>([&](int i) { return __uint_as_float(r0[i]); });
               if ((x + 1) * 32 < w) {
                 hide(r1, see[x + 1]);
-                t = fmaxf(t, most(x + 1, r1));
+                t = fmaxf(t, max_of<32>([&](int i) { return __uint_as_float(r1[i]); }));
               }
               return t;
             };
@@ -1938,10 +1968,18 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
             mt = fmaxf(mt, two(0));
             raise_to(mt);
             const float nm = m == -INFINITY ? 0.0f : lift - m * A.c;
+            const float2 c2 = make_float2(A.c, A.c), mc2 = make_float2(nm, nm);
             float2 sum[4] = {};
             auto weights = [&](int x, uint32_t (&r)[32]) {  // of 32 keys
               uint32_t pw[16];
-              weigh(x, r, nm, pw, sum);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float2 e = fma2(
+                    make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), c2, mc2);
+                const float2 p = make_float2(ex2(e.x), ex2(e.y));
+                sum[i & 3] = add2(sum[i & 3], p);
+                pw[i] = pack16<BF>(p.x, p.y);
+              }
               tm_st16(ts + x * 16, pw);
             };
             // (P's columns lie over scores of the first half only; a pair's products
@@ -2185,23 +2223,17 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
       }
       d_flags = s.j0 + n < s.nt ? d_flags | DESC_OUT : d_flags & ~DESC_OUT;
       idx += 2 * n;
-      tiles8 += cached;
+      tiles8 += n - staged;
       seg_done(segs);
       ++segs;
     }
     if (!PR && A.join && tid == 0) A.desc[blockIdx.x] = make_int4(d_flags, d_item, d_b, 0);
-  } else if (Q8 && warp >= WIDEN_WARP) {
-    if constexpr (Q8) {
-      if constexpr (Regs<NQ, Q8>::WIDEN < 128) {
-        __syncwarp();
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<NQ, Q8>::WIDEN));
-      }
-      widen_tiles<DP, NQ, PAIR, BF>(A, C, C8, smem, abort);
-    }
   } else {
     __syncwarp();
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<NQ, Q8>::OTHER));
-  if (warp == PLAN_WARP) {
+  if (Q8 && (warp & 2)) {
+    if constexpr (Q8) widen_tiles<DP, NQ, PAIR, BF>(A, C, C8, smem, abort);
+  } else if (warp == (Q8 ? PLAN8_WARP : PLAN_WARP)) {
     // ------------------------------------------------------------ the plan
     Cursor<PAIR, PR> cur;
     Seg s;
@@ -2312,7 +2344,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         ++segs;
         const int plane = PR ? s.h : s.b * A.LH + A.head0 + s.h;
         auto tile = [&](int jj, bool is_v) {
-          const Keys ky = keys_of<PR>(A, s, s.j0 + jj);
+          const Keys ky = keys_of<PR, Q8>(A, s, s.j0 + jj);
           if (Q8 && ky.staged) return true;  // (the widening warps')
           if constexpr (Q8) {  // of the keys' stages, or the values'
             const uint32_t u = is_v ? v_at : k_at;
@@ -2368,9 +2400,17 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
           return true;
         };
         constexpr int LAG = PAIR ? 0 : 1;
-        for (int i = 0; ok && i < s.n + LAG; ++i) {
-          if (i < s.n) ok = tile(i, false);
-          if (ok && i >= LAG) ok = tile(i - LAG, true);
+        if constexpr (Q8) {
+#pragma unroll 1
+          for (int x = 0; ok && x < 2 * (s.n + LAG); ++x) {  // (one copy of the code)
+            const int i = (x >> 1) - (x & 1 ? LAG : 0);
+            if (i >= 0 && i < s.n) ok = tile(i, x & 1);
+          }
+        } else {
+          for (int i = 0; ok && i < s.n + LAG; ++i) {
+            if (i < s.n) ok = tile(i, false);
+            if (ok && i >= LAG) ok = tile(i - LAG, true);
+          }
         }
         if (!ok) break;
       }
@@ -2394,8 +2434,9 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
           }
       }
     };
-    if (PR || A.kind == RING) {
-      if (elect_one()) copies(Yes<true>());
+    if (!Q8 && (PR || A.kind == RING)) {
+      if constexpr (!Q8)
+        if (elect_one()) copies(Yes<true>());
       __syncwarp();
     } else {
       copies(Yes<false>());
@@ -2461,13 +2502,15 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         const Seg s = C.seg[segs % AHEAD];
         if (s.n == 0) break;
         mbar_arrive(bar(&C.seg_empty[segs % AHEAD]));
-        const int slot = PAIR ? 0 : segs & 1;
-        const int use = PAIR ? segs : segs >> 1;
+        constexpr bool TURNS = !PAIR && SM::Q_SLOTS == 2;
+        const int slot = TURNS ? segs & 1 : 0, use = TURNS ? segs >> 1 : segs;
         ok = mbar_wait(bar(&C.q_full[slot]), use & 1, A.status, abort);
         tc_after();
-        const int n = s.n, c = cached_of(s);
-        // (tiles are whole but for the last cached and the staged ones)
-        auto width = [&](int j) { return j + 1 < c ? TILE : width_of(keys_of<PR>(A, s, s.j0 + j)); };
+        const int n = s.n, g = staged_of(A, s);
+        // (tiles are whole but for the staged and the last cached ones)
+        auto width = [&](int j) {
+          return j >= g && j + 1 < n ? TILE : width_of(keys_of<PR, Q8>(A, s, s.j0 + j));
+        };
         // S[st] (+)= the terms of query tile q with the term of keys at `ka`
         auto term = [&](int st, int q, uint32_t ka, int w, bool more) {
           const uint32_t id = NQ ? id_8 : id_8 | uint32_t(w >> 3) << 17;
@@ -2486,7 +2529,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
           const int w = width(i);
 #pragma unroll 1
           for (int p = 0; p < PARTS; ++p) {
-            const uint32_t u = idx + wide_k<PAIR>(i, c, PARTS) + p;
+            const uint32_t u = idx + wide_k<PAIR>(i, PARTS) + p;
             if (!full(u)) return false;
             const uint32_t at = base + SM::STAGE_AT + (u % STAGES) * BYTES;
 #pragma unroll 1
@@ -2505,8 +2548,8 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
 #pragma unroll 1
         for (int i = 0; ok && i < n + AHEAD8; ++i) {
           const int j = i - AHEAD8;  // the tile whose weights are next
-          const bool raw = i < c;
-          const uint32_t ku = raw0 + i, ks = ku % SM::RAW_K;
+          const bool raw = i >= g && i < n;
+          const uint32_t ku = raw0 + i - g, ks = ku % SM::RAW_K;
           const uint32_t ka = base + SM::RAW_AT + ks * SM::RAW;
           auto raw_here = [&] {
             if (!mbar_wait(bar(&C.full[STAGES + ks]), (ku / SM::RAW_K) & 1, A.status, abort))
@@ -2514,7 +2557,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
             tc_after();
             return true;
           };
-          const uint32_t uv = idx + wide_v<PAIR>(j, n, c, PARTS);
+          const uint32_t uv = idx + wide_v<PAIR>(j, g, PARTS);
           const int w = width(j);
           if (j >= 0) ok = full(uv);
           if (raw) ok = ok && raw_here();
@@ -2537,11 +2580,11 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
               if (!PAIR || x == 1) mma_commit(bar(&C.empty[STAGES + ks]));
             }
           }
-          if (ok && i >= c && i < n) ok = staged_scores(PAIR ? 0 : i & 1, PAIR ? 0 : slot, i);
+          if (ok && i < g) ok = staged_scores(PAIR ? 0 : i & 1, PAIR ? 0 : slot, i);
           if (ok && i + 1 == n) mma_commit(bar(&C.q_empty[slot]));  // (queries done with)
         }
-        idx += n + PARTS * (n - c);
-        raw0 += c;
+        idx += n + PARTS * g;
+        raw0 += n - g;
         ++segs;
       }
     }
@@ -2786,12 +2829,12 @@ int launch_as(const AttnParams& A, int device, int grid, int ctas, cudaStream_t 
   if (!(raised.load(std::memory_order_acquire) & mark)) {
     if (cudaFuncSetAttribute(sv_attn<DP, NQ, PAIR, PR, BF, Q8>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (Smem<DP, NQ, Q8 ? TERMS_OF<BF> : 0>::TOTAL)) != cudaSuccess)
+                             (Smem<DP, NQ, Q8 ? TERMS_OF<BF> : 0, PAIR>::TOTAL)) != cudaSuccess)
       return SV_ERR_CUDA;
     raised.fetch_or(mark, std::memory_order_release);
   }
   sv_attn<DP, NQ, PAIR, PR, BF, Q8>
-      <<<grid, Q8 ? THREADS8 : THREADS, (Smem<DP, NQ, Q8 ? TERMS_OF<BF> : 0>::TOTAL), st>>>(A);
+      <<<grid, Q8 ? THREADS8 : THREADS, (Smem<DP, NQ, Q8 ? TERMS_OF<BF> : 0, PAIR>::TOTAL), st>>>(A);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
   if (PR || !A.join) return SV_OK;
   cudaLaunchConfig_t cfg = {};
