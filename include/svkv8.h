@@ -73,9 +73,15 @@ int sv_page_commit8(int dtype, void* k_pages, void* v_pages, void* k_scales, voi
  * sv_tree_attn over 8-bit pages: queries, output and the tree's own staged
  * entries are of dtype; the cache's values are used exactly (a value that
  * dtype cannot hold exactly, through a scale outside the range above, counts
- * as NaN).  Workspace, requirements and faults as for sv_tree_attn, with
- * page_size <= 65536.
+ * as NaN).  Requirements and faults as for sv_tree_attn, with page_size <=
+ * 65536; the workspace has sv_attn8_workspace_bytes() bytes, which go by the
+ * batch, too: the queries and staged entries are split there into 8-bit terms
+ * whose sums are theirs (two for bf16, three for fp16), but for what lies
+ * 2^18 below the largest value of a query row, or of eight staged keys.
  */
+/* Bytes of workspace for sv_tree_attn8; 0 for sizes that it refuses. */
+size_t sv_attn8_workspace_bytes(int B, int N, int Hq, int Hkv, int D);
+
 int sv_tree_attn8(int dtype, const void* q, const void* k_pages, const void* v_pages,
                   const void* k_scales, const void* v_scales, const int32_t* block_table,
                   const int32_t* seq_lens, const void* k_new, const void* v_new,

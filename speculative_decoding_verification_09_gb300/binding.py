@@ -35,7 +35,7 @@ EXPORTED = ("sv_workspace_bytes", "sv_workspace_init", "spec_verify", "spec_veri
 EXPORTED_ATTN = ("sv_attn_workspace_bytes", "sv_tree_attn", "sv_ring_attn", "sv_prompt_attn",
                  "sv_attn_test_withhold")
 EXPORTED_ROPE = ("sv_rope_table", "sv_rope", "sv_page_append")
-EXPORTED_KV8 = ("sv_page_append8", "sv_page_commit8", "sv_tree_attn8")
+EXPORTED_KV8 = ("sv_page_append8", "sv_page_commit8", "sv_tree_attn8", "sv_attn8_workspace_bytes")
 SV_TREE_MAX_N = 256
 SV_ROPE_NONE, SV_ROPE_LINEAR, SV_ROPE_BASE, SV_ROPE_RAMP, SV_ROPE_WAVE = range(5)
 SV_NOALLOC_MAX_WORKSPACE = 16 << 20
@@ -92,6 +92,8 @@ def lib() -> ctypes.CDLL:
                                       I, I, I, I, I, I, P, P, P]
         L.sv_page_commit8.argtypes = [I, P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, P,
                                       P]
+        L.sv_attn8_workspace_bytes.argtypes = [I, I, I, I, I]
+        L.sv_attn8_workspace_bytes.restype = Z
         L.sv_tree_attn8.argtypes = [I, P, P, P, P, P, P, P, P, P, P, F, I, I, I, I, I, I, I, I, I,
                                     I, I, P, P, Z, P, P]
         L.sv_tree_set_cluster.argtypes = [I]
@@ -111,7 +113,7 @@ def lib() -> ctypes.CDLL:
                      "sv_kv_fill", "sv_page_commit", "sv_tree_attn", "sv_ring_attn",
                      "sv_prompt_attn", "sv_attn_test_withhold",
                      "sv_window_block_table", "sv_window_seq_lens_host", "sv_tree_verify",
-                     "sv_tree_set_cluster", "sv_tree_set_warps", *EXPORTED_ROPE, *EXPORTED_KV8):
+                     "sv_tree_set_cluster", "sv_tree_set_warps", *EXPORTED_ROPE, *EXPORTED_KV8[:3]):
             getattr(L, name).restype = I
         _lib = L
     return _lib
@@ -512,10 +514,15 @@ def sv_attn_workspace_bytes(N: int, Hq: int, Hkv: int, D: int) -> int:
     return int(lib().sv_attn_workspace_bytes(N, Hq, Hkv, D))
 
 
+def sv_attn8_workspace_bytes(B: int, N: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(lib().sv_attn8_workspace_bytes(B, N, Hq, Hkv, D))
+
+
 def make_attn_workspace(B: int, N: int, Hq: int, Hkv: int, D: int, device) -> torch.Tensor:
-    """Allocate a workspace for sv_tree_attn (N nodes) or sv_ring_attn (N = R
-    tokens); its size does not depend on the batch."""
+    """Allocate a workspace for sv_tree_attn or sv_tree_attn8 (N nodes) or sv_ring_attn (N = R
+    tokens) with a batch of B (of which only sv_tree_attn8's depends)."""
     n = sv_attn_workspace_bytes(N, Hq, Hkv, D)
+    n = n and max(n, sv_attn8_workspace_bytes(B, N, Hq, Hkv, D))
     if n == 0:
         raise SpecVerifyError("sizes the attention calls refuse")
     return torch.empty(n, dtype=torch.uint8, device=device)

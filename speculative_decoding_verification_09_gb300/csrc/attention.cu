@@ -73,8 +73,28 @@ size_t workspace_for(int N, int G, int D) {
   return size_t(MAX_CTAS) * (2 * rows * (dp * 4 + 8) + sizeof(int4));
 }
 
+// What the first kernel of a call over 8-bit pages leaves for the second, behind the partials:
+// the queries' and staged keys' terms, staged values, and their powers of two.
+struct Space8 {
+  size_t q8, k8, v16, qf, t8, all;
+};
+Space8 space_for8(int B, int N, int Hq, int Hkv, int D) {
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  const size_t tokens = size_t(B) * N, most = 3;  // terms
+  Space8 s;
+  s.q8 = up(workspace_for(N, Hq / Hkv, D));
+  s.k8 = s.q8 + up(most * tokens * Hq * D);
+  s.v16 = s.k8 + up(most * tokens * Hkv * D);
+  s.qf = s.v16 + up(2 * tokens * Hkv * D);
+  s.t8 = s.qf + up(4 * tokens * Hq);
+  s.all = s.t8 + up(size_t(B) * Hkv * ((N + TILE - 1) / TILE) * sizeof(Tile8));
+  return s;
+}
+
+// q, k_new and v_new of 8-bit calls come in `prep`.
 int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v,
-           const void* k_new, const void* v_new, void* workspace, void* stream) {
+           const void* k_new, const void* v_new, void* workspace, void* stream,
+           Prep8* prep = nullptr) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
@@ -99,8 +119,33 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
   const uint32_t q_tok = uint32_t(
       A.tpt < (A.kind == PROMPT ? A.T : A.N) ? A.tpt : (A.kind == PROMPT ? A.T : A.N));
   A.q_rows = int(q_tok) * A.G;
-  A.q = static_cast<const uint16_t*>(q);
-  if (!A.k_scales) {
+  if (prep) {
+    const Space8 s = space_for8(A.B, A.N, A.Hq, A.Hkv, A.D);
+    unsigned char* const w = static_cast<unsigned char*>(workspace);
+    const uint64_t terms = dtype == SV_BF16 ? TERMS_OF<true> : TERMS_OF<false>;
+    prep->q8 = w + s.q8;
+    prep->k8 = w + s.k8;
+    prep->v16 = reinterpret_cast<uint16_t*>(w + s.v16);
+    prep->qf = reinterpret_cast<float*>(w + s.qf);
+    prep->t8 = reinterpret_cast<Tile8*>(w + s.t8);
+    prep->turned = layout_of(A.N, A.G).nq > 0;
+    A.qf = prep->qf;
+    A.t8 = prep->t8;
+    const uint32_t dp = A.D > 64 ? 128 : 64;
+    const CUtensorMapSwizzle swizzle =
+        A.D > 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    const uint64_t qd[5] = {D, uint64_t(A.G), uint64_t(A.Hkv), tokens, terms};
+    const uint64_t qs[4] = {D, D * A.G, D * A.Hq, D * A.Hq * tokens};
+    const uint32_t qb[5] = {dp, uint32_t(A.G), 1, q_tok, 1};
+    const uint64_t kd[3] = {D, uint64_t(A.N), uint64_t(A.B) * A.Hkv * terms};
+    const uint64_t vd[3] = {D, uint64_t(A.N), uint64_t(A.B) * A.Hkv};
+    const uint64_t ks[2] = {D, D * A.N};
+    const uint32_t kb[3] = {dp, TILE, 1}, vb[3] = {64, TILE, 1};
+    if (!make_map8(&A.mq, prep->q8, 5, qd, qs, qb, swizzle) ||
+        !make_map8(&A.mkn, prep->k8, 3, kd, ks, kb, swizzle) ||
+        !make_map(&A.mvn, SV_F16, prep->v16, 3, vd, ks, vb))
+      return SV_ERR_CUDA;
+  } else {
     const uint64_t dims[4] = {D, uint64_t(A.G), uint64_t(A.Hkv), tokens};
     const uint64_t str[3] = {D, D * A.G, D * A.Hq};
     const uint32_t box[4] = {64, uint32_t(A.G), 1, q_tok};
@@ -186,7 +231,7 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (A.k_scales)
-    return (dtype == SV_BF16 ? launch8_bf16 : launch8_f16)(A, lay, dev, grid, ctas, st);
+    return (dtype == SV_BF16 ? launch8_bf16 : launch8_f16)(A, *prep, lay, dev, grid, ctas, st);
   return (dtype == SV_BF16 ? launch_bf16 : launch_f16)(A, lay, dev, grid, ctas, st);
 }
 
@@ -251,6 +296,11 @@ int sv_tree_attn(int dtype, const void* q, const void* k_pages, const void* v_pa
   return launch(A, dtype, q, k_pages, v_pages, k_new, v_new, workspace, stream);
 }
 
+size_t sv_attn8_workspace_bytes(int B, int N, int Hq, int Hkv, int D) {
+  if (B < 0 || B > 65535 || N < 1 || N > MAX_N || bad_heads(Hq, Hkv, D) || D % 16 != 0) return 0;
+  return space_for8(B, N, Hq, Hkv, D).all;
+}
+
 int sv_tree_attn8(int dtype, const void* q, const void* k_pages, const void* v_pages,
                   const void* k_scales, const void* v_scales, const int32_t* block_table,
                   const int32_t* seq_lens, const void* k_new, const void* v_new,
@@ -275,7 +325,7 @@ int sv_tree_attn8(int dtype, const void* q, const void* k_pages, const void* v_p
       misaligned(dev_status, 4))
     return SV_ERR_INVALID_ARG;
   if (!workspace || misaligned(workspace, 256) ||
-      workspace_bytes < sv_attn_workspace_bytes(N, Hq, Hkv, D))
+      workspace_bytes < sv_attn8_workspace_bytes(B, N, Hq, Hkv, D))
     return SV_ERR_WORKSPACE;
   AttnParams A = {};
   A.kind = TREE;
@@ -286,13 +336,16 @@ int sv_tree_attn8(int dtype, const void* q, const void* k_pages, const void* v_p
   A.status = dev_status;
   A.k_scales = static_cast<const uint8_t*>(k_scales);
   A.v_scales = static_cast<const uint8_t*>(v_scales);
-  A.k_new = static_cast<const uint16_t*>(k_new);
-  A.v_new = static_cast<const uint16_t*>(v_new);
   A.block_log = block_log;
   A.c = scale * LOG2E;
   A.B = B; A.N = N; A.Hq = Hq; A.Hkv = Hkv; A.D = D;
   A.LH = LH; A.head0 = head0; A.num_pages = num_pages; A.page = page_size; A.cols = cols;
-  return launch(A, dtype, q, k_pages, v_pages, nullptr, nullptr, workspace, stream);
+  Prep8 P = {};
+  P.q = static_cast<const uint16_t*>(q);
+  P.k_new = static_cast<const uint16_t*>(k_new);
+  P.v_new = static_cast<const uint16_t*>(v_new);
+  P.B = B; P.N = N; P.Hq = Hq; P.Hkv = Hkv; P.D = D; P.LH = LH; P.head0 = head0;
+  return launch(A, dtype, q, k_pages, v_pages, nullptr, nullptr, workspace, stream, &P);
 }
 
 int sv_ring_attn(int dtype, const void* q, const void* k_pool, const void* v_pool,

@@ -107,13 +107,13 @@ struct AttnParams {
   int whole_tiles;        // no item is cut when none has more tiles than this (TREE, RING)
   int join;               // and some may have, by the cache's extent
   int withhold;           // failure-handling test: one of CTA 0's stages never fills
-  // 8-bit caches: the queries, the blocks' scales [num_pages][LH][page / block] and the staged
-  // entries
-  const uint16_t* q;
+  // 8-bit caches (mq: the queries' terms, mkn: the staged keys', mvn: staged values in fp16): the
+  // blocks' scales [num_pages][LH][page / block], and powers of two that the first kernel found,
+  // of the queries' rows [B][N][Hq] and of the staged tiles [B][Hkv][tiles]
   const uint8_t* k_scales;
   const uint8_t* v_scales;
-  const uint16_t* k_new;
-  const uint16_t* v_new;
+  const float* qf;
+  const struct Tile8* t8;
   int block_log;          // log2 of the tokens of a block
 };
 
@@ -224,6 +224,15 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* m, uint3
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
       "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst), "l"(m), "r"(bar), "r"(x), "r"(y),
       "r"(z), "r"(w)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x,
+                                       int y, int z, int w, int v) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst), "l"(m), "r"(bar), "r"(x), "r"(y),
+      "r"(z), "r"(w), "r"(v)
       : "memory");
 }
 
@@ -659,19 +668,9 @@ __device__ __forceinline__ int v_order(int j, int n) {
   return PAIR ? 2 * j + 1 : (j < n - 1 ? 2 * j + 2 : 2 * n - 1);
 }
 
-// 8-bit caches: the order is K_0 .. V_(i - LAG) K_i .. there, too.  Bytes have a ring for keys
-// and one for values.  The 16-bit ring has all values of a segment, whose first g tiles are
-// staged, and `parts` stages with the terms of each staged tile's keys.
-template <bool PAIR>
-constexpr int LAG8 = PAIR ? 0 : 1;
-template <bool PAIR>
-__device__ __forceinline__ int wide_k(int i, int parts) {
-  return parts * i + max(0, i - LAG8<PAIR>);
-}
-template <bool PAIR>
-__device__ __forceinline__ int wide_v(int j, int g, int parts) {
-  return j + parts * min(j + LAG8<PAIR> + 1, g);
-}
+// 8-bit caches: bytes have a ring for keys (TERMS stages for a staged tile's) and one for values,
+// filled in the order K_i V_(i - LAG), and the 16-bit ring has all values of a segment, whose
+// first tiles are the staged ones.
 __device__ __forceinline__ int staged_of(const AttnParams& A, const Seg& s) {
   return min(max(tiles_of(A.N) - s.j0, 0), s.n);
 }
@@ -697,7 +696,7 @@ __device__ __forceinline__ uint32_t span(int a, int b, int k0) {
 //     of 128 dimensions, 207 us so and 215 with a row per lane, 32 rows 210 and 217;
 //     but 64 rows, for which a warp agrees on 64 maxima, 258 and 218.)
 constexpr int CTRL_BYTES = 3 * 1024;  // what 227 KB leave beside seven tiles of 32 KB
-constexpr int CTRL8_BYTES = 4864;  // more of it with 8-bit caches
+constexpr int CTRL8_BYTES = 2304;  // more of it with 8-bit caches
 // 8-bit caches (Q8).  Keys stay bytes: scores are products of e4m3 with e4m3, the queries
 // split into TERMS such terms whose sum is theirs exactly (4 bits of a mantissa each; see
 // split_terms).  Values arrive as bytes, too, and the widening warps fill the 16-bit stages
@@ -779,27 +778,19 @@ static_assert(sizeof(Ctrl<0, true>) <= CTRL_BYTES && sizeof(Ctrl<0, false>) <= C
 struct Tile8 {
   alignas(16) float kf[16];
   float vd[16], vf[16];
-  int top;        // the values' largest exponent
-  int count;      // staged tiles: warps that have written their eights of keys,
-  int8_t ev[16];  // and the exponents of these keys' values
+  int top;  // the values' largest exponent
 };
 constexpr int SCALES = 8;        // cached tiles whose scales are read ahead
 constexpr int LEAST = -30;
 template <int NQ>
 struct Ctrl8 {
   unsigned long long full[SCALES], empty[SCALES];
-  Tile8 tile[SCALES], staged[SEGS][2];
-  // powers of two of the queries' rows: floats of the columns, or exponent bytes
-  alignas(16) float qf[SEGS][NQ ? NQ : 1];
-  uint8_t qx[SEGS][NQ ? 1 : 2 * TILE];
+  Tile8 tile[SCALES];
+  alignas(16) float qf[2][NQ ? NQ : 1];  // the columns' powers of two, per stream
   int kept[2];                     // at a segment's end, per stream
   float lost[2];
 };
 static_assert(sizeof(Ctrl8<0>) <= CTRL8_BYTES && sizeof(Ctrl8<32>) <= CTRL8_BYTES, "control part");
-// 2^(byte - 127); 255: NaN
-__device__ __forceinline__ float power_of(uint32_t byte) {
-  return __uint_as_float(byte == 255 ? 0x7fffffffu : byte << 23);
-}
 __device__ __forceinline__ float power(int e) { return __int_as_float((e + 127) << 23); }
 
 // desc[cta]: x = flags, y = item (of its request) and z = request of the first segment
@@ -1071,249 +1062,105 @@ __device__ __forceinline__ float power_or_nan(int e) {
   return e == NOT_FINITE ? __int_as_float(0x7fffffff) : power(e);
 }
 
-// Where products of bytes look for byte d of a row of DP bytes.
-template <int DP>
-__device__ __forceinline__ int swizzled(int row, int d) {
-  const int p = d >> 4;
-  return (DP == 128 ? row * 128 + ((p ^ (row & 7)) << 4) : row * 64 + ((p ^ (row >> 1 & 3)) << 4)) +
-         (d & 15);
-}
-
-// The widening warps, per segment: the queries' terms; then, in the order of the products,
-// the staged tiles' keys as terms, and their values, and the cached tiles' values from bytes to
-// 16 bits: a thread takes 16 bytes, 16 dimensions of a token, and writes two 16-byte pieces of a
-// 64-dimension block in the 128-byte swizzle.
-// One copy of each piece of code, and loops rolled: with 34 KB of code here (118 to 133 KB in
-// the kernel) whatever runs once an item was fetched anew each time.
+// The widening warps: a segment's values, tile by tile, to fp16.  Cached ones from bytes: a
+// thread takes 16, 16 dimensions of a token, and writes two 16-byte pieces of a 64-dimension
+// block in the 128-byte swizzle; lanes of a row's two blocks write their pieces in opposite
+// order, so that eight lanes fall on eight pieces.  Staged ones are copied as they are.
 template <int DP, int NQ, bool PAIR, bool BF>
-__device__ __forceinline__ void widen_tiles(const AttnParams& A, Ctrl<NQ, PAIR>& C, Ctrl8<NQ>& C8,
+__device__ __forceinline__ void widen_tiles(const AttnParams& A, Ctrl<NQ, PAIR>& C,
                                             unsigned char* smem, volatile int* abort) {
-  constexpr int TERMS = TERMS_OF<BF>, PARTS = (TERMS + 1) / 2, LAG = LAG8<PAIR>;
-  using SM = Smem<DP, NQ, TERMS, PAIR>;
+  using SM = Smem<DP, NQ, TERMS_OF<BF>, PAIR>;
   constexpr int STAGES = SM::STAGES;
   constexpr int PER_ROW = DP / 16;                            // threads of a row
   constexpr int ROWS = 32 * WIDEN_WARPS / PER_ROW;            // rows of a step
-  constexpr int STEPS = TILE / ROWS, WARP_ROWS = 32 / PER_ROW;
-  constexpr int BATCH = 4;
-  constexpr int Q_ROWS = NQ ? NQ : TILE;
+  constexpr int STEPS = TILE / ROWS, BATCH = 4;
   static_assert(STEPS % BATCH == 0, "whole rounds");
   const int lane = int(threadIdx.x) & 31;
   const int warp = (int(threadIdx.x) >> 5 & 1) | (int(threadIdx.x) >> 6 & 2), tid = warp * 32 + lane;
-  const int row0 = tid / PER_ROW, dim = tid % PER_ROW * 16, lane_row = lane / PER_ROW;
-  uint32_t out = 0, raw0 = 0;  // 16-bit stages and cached tiles so far
+  const int row0 = tid / PER_ROW, dim = tid % PER_ROW * 16;
+  uint32_t out = 0, raw0 = 0;  // 16-bit stages, and stages of bytes, so far
   bool ok = true;
   auto wait = [&](unsigned long long* b, uint32_t parity) {
     ok = ok && warp_wait(smem_addr(b), parity, A.status, abort);
   };
-  auto filled = [&](unsigned long long* full) {  // what was written is there for the products
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_addr(full));
-  };
-  // 16 dimensions of a row of 16-bit values; zeros where there are none
-  struct Row { uint4 lo, hi; };
-  auto fetch = [&](const uint16_t* src, bool on) {
-    Row r = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (on && dim < A.D) {
-      r.lo = __ldg(reinterpret_cast<const uint4*>(src + dim));
-      r.hi = __ldg(reinterpret_cast<const uint4*>(src + dim) + 1);
-    }
-    return r;
-  };
-  auto size = [](const Row& r) { return max(size_of<BF>(r.lo), size_of<BF>(r.hi)); };
-  // their terms, written where the products look for them
-  auto terms = [&](const Row& u, float by, unsigned char* to, int stride, int first, int count) {
-    uint2 lo[TERMS], hi[TERMS];
-    split_terms<TERMS>(to_half<BF>(u.lo, by), lo);
-    split_terms<TERMS>(to_half<BF>(u.hi, by), hi);
-#pragma unroll
-    for (int t = 0; t < TERMS; ++t)
-      if (t >= first && t < first + count)
-        *reinterpret_cast<uint4*>(to + (t - first) * stride) =
-            make_uint4(lo[t].x, lo[t].y, hi[t].x, hi[t].y);
-  };
-  // the queries of segment `segs`, once it is planned and their place is free
-  constexpr bool TURNS = !PAIR && SM::Q_SLOTS == 2;
-  auto queries = [&](int segs) {
-    wait(&C.seg_full[segs % SEGS], (segs / SEGS) & 1);
-    if (!ok) return;
-    const Seg& s = C.seg[segs % SEGS];
-    if (s.n == 0) return;
-    const int slot = TURNS ? segs & 1 : 0, use = TURNS ? segs >> 1 : segs;
-    wait(&C.q_empty[slot], (use & 1) ^ 1);
-    if (!ok) return;
-    const int first = s.mt * (PAIR ? 2 : 1) * A.tpt;
-    auto row_of = [&](int r) {  // of a query row of the tiles
-      const int tile = r / Q_ROWS, rr = r - tile * Q_ROWS, rt = rr / A.G;
-      const int tok = first + tile * A.tpt + rt;
-      return fetch(A.q + ((size_t(s.b) * A.N + tok) * A.Hq + s.h * A.G + (rr - rt * A.G)) * A.D,
-                   rt < A.tpt && tok < A.N);
-    };
-    // (two rows at once, the next two on their way; every lane of a warp goes round as often)
-    constexpr int ALL = (PAIR ? 2 : 1) * Q_ROWS;
-    Row next[2] = {row_of(row0), row_of(row0 + ROWS)};
-#pragma unroll 1
-    for (int r0 = row0; r0 < ALL; r0 += 2 * ROWS) {
-      const Row u[2] = {next[0], next[1]};
-      next[0] = row_of(r0 + 2 * ROWS);  // (behind the last: not used)
-      next[1] = row_of(r0 + 3 * ROWS);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = r0 + i * ROWS;
-        uint32_t most = size(u[i]);
-#pragma unroll
-        for (int k = 1; k < PER_ROW; k *= 2)  // (a row's lanes are neighbours)
-          most = max(most, __shfl_xor_sync(0xffffffffu, most, k));
-        const int e = exponent_over(most);
-        const int tile = r / Q_ROWS, rr = r - tile * Q_ROWS;
-        if (r < ALL) {
-          terms(u[i], power(-min(e, 119)),
-                smem + (PAIR ? tile : slot) * SM::Q_BYTES + swizzled<DP>(rr, dim), SM::TERM, 0, TERMS);
-          if (dim == 0) {
-            if (NQ) C8.qf[segs % SEGS][rr] = power_or_nan(e);
-            else C8.qx[segs % SEGS][r] = e == NOT_FINITE ? 255 : uint8_t(e + 127);
-          }
-        }
-      }
-    }
-    filled(&C.q_full[slot]);
-  };
-  int asked = 0;  // segments whose queries are done
   for (int segs = 0;; ++segs) {
-    Seg s;
-    int n = 0, g0 = 0;
-#pragma unroll 1
-    for (int x = -1; x < 2 * (n + LAG); ++x) {
-      // the next segment's queries, ahead of its first product (or, at the start, this one's)
-      if (x < 0 ? asked == segs : TURNS && asked == segs + 1 && (x == 2 * (g0 + 2) || x == 2 * n)) {
-        queries(asked);
-        ++asked;
-        if (!ok) break;
-      }
-      if (x < 0) {
-        s = C.seg[segs % SEGS];
-        n = s.n;
-        if (n == 0) break;
-        g0 = staged_of(A, s);
-        continue;
-      }
-      const bool is_v = x & 1;
-      const int j = is_v ? (x >> 1) - LAG : x >> 1;
-      if (j < 0 || j >= n || (!is_v && j >= g0)) continue;
-      const Keys ky = keys_of<false, true>(A, s, s.j0 + j);
-      const int w = width_of(ky);
-      const size_t from = ((size_t(s.b) * A.LH + A.head0 + s.h) * A.N + ky.k0) * A.D;
-      Tile8& t8 = C8.staged[segs % SEGS][ky.k0 / TILE & 1];  // (of a staged tile)
-#pragma unroll 1
-      for (int part = 0; part < (is_v ? 1 : PARTS); ++part) {
-        const uint32_t st = out % STAGES;
-        unsigned char* const dst = smem + SM::STAGE_AT + st * SM::BYTES;
-        // a row's 16 dimensions of the 16-bit tile: lanes of a row's two blocks write their
-        // pieces in opposite order, so that eight lanes fall on eight pieces
-        auto put = [&](int row, const uint4& lo, const uint4& hi) {
-          unsigned char* const line = dst + (dim >> 6) * 16384 + row * 128;
-          const int at = dim >> 3 & 7, swap = dim >> 6;
-          *reinterpret_cast<uint4*>(line + (((at + swap) ^ (row & 7)) << 4)) = swap ? hi : lo;
-          *reinterpret_cast<uint4*>(line + (((at + 1 - swap) ^ (row & 7)) << 4)) = swap ? lo : hi;
-        };
-        const uint32_t u = raw0 + j - g0, rs = SM::RAW_K + u % SM::RAW_V;
-        wait(&C.empty[st], ((out / STAGES) & 1) ^ 1);
-        if (j >= g0) wait(&C.full[STAGES + rs], (u / SM::RAW_V) & 1);
-        if (!ok) break;
-        if (j >= g0) {
-          // ---- cached values
-          const unsigned char* const src = smem + SM::RAW_AT + rs * SM::RAW + tid * 16;
-#pragma unroll 1
-          for (int g = 0; g < STEPS; g += BATCH) {
-            uint4 b[BATCH];
-#pragma unroll
-            for (int i = 0; i < BATCH; ++i)
-              b[i] = *reinterpret_cast<const uint4*>(src + (g + i) * (32 * WIDEN_WARPS * 16));
-#pragma unroll
-            for (int i = 0; i < BATCH; ++i) {
-              const uint2 p = widen4(b[i].x), q = widen4(b[i].y), y = widen4(b[i].z), z = widen4(b[i].w);
-              put(row0 + (g + i) * ROWS, make_uint4(p.x, p.y, q.x, q.y), make_uint4(y.x, y.y, z.x, z.y));
-            }
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&C.empty[STAGES + rs]));
-          // behind the entries: whatever the bytes are, weights of 0 take zeros
-          if (ky.n < w) {
-#pragma unroll 1
-            for (int row = row0; row < w; row += ROWS)
-              if (row >= ky.n) put(row, make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0));
-          }
-        } else {
-          // ---- staged: a warp takes eight rows at a time, which share a power of two
-#pragma unroll 1
-          for (int g = warp; g * 8 < w; g += WIDEN_WARPS) {
-            constexpr int V = 8 / WARP_ROWS;  // rows of a lane: 1 or 2
-            Row k[V];
-            uint32_t k_most = 0, v_most = 0;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-              const int row = g * 8 + i * WARP_ROWS + lane_row;
-              const uint16_t* const at = (is_v ? A.v_new : A.k_new) + from + size_t(row) * A.D;
-              k[i] = fetch(at, row < ky.n);
-              k_most = max(k_most, size(k[i]));
-              if (!is_v && part == 0)
-                v_most = max(v_most, size(fetch(A.v_new + from + size_t(row) * A.D, row < ky.n)));
-            }
-            const int e = is_v ? int(t8.ev[g]) : exponent_over(__reduce_max_sync(0xffffffffu, k_most));
-            if (!is_v && part == 0) {
-              const int ev = exponent_over(__reduce_max_sync(0xffffffffu, v_most));
-              if (lane == 0) {
-                t8.kf[g] = power_or_nan(e);
-                t8.ev[g] = int8_t(e == NOT_FINITE ? e : ev);
-              }
-            }
-            const float by = power(-min(e, 119));
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-              const int row = g * 8 + i * WARP_ROWS + lane_row;
-              if (is_v) put(row, to_half<BF>(k[i].lo, by), to_half<BF>(k[i].hi, by));
-              else terms(k[i], by, dst + swizzled<DP>(row, dim), SM::RAW, 2 * part, 2);
-            }
-          }
-          if (!is_v && part == 0) {  // the last warp to get here puts the values' powers of two together
-            __syncwarp();
-            __threadfence_block();
-            int last = 0;
-            if (lane == 0) last = atomicAdd(&t8.count, 1) == WIDEN_WARPS - 1;
-            if (__shfl_sync(0xffffffffu, last, 0)) {
-              __threadfence_block();
-              const int ev = lane < 16 && lane * 8 < ky.n
-                                 ? int(reinterpret_cast<volatile int8_t*>(t8.ev)[lane])
-                                 : -1000;
-              const int top = __reduce_max_sync(0xffffffffu, ev == NOT_FINITE ? 0 : ev);
-              const int by = max(ev - top, LEAST);
-              const float nan = __int_as_float(0x7fffffff);
-              if (lane < 16) {
-                t8.vd[lane] = ev == NOT_FINITE ? nan : float(by);
-                t8.vf[lane] = ev == NOT_FINITE ? nan : power(NQ ? by : -by);
-              }
-              if (lane == 0) {
-                t8.top = top;
-                t8.count = 0;
-              }
-            }
-          }
-        }
-        filled(&C.full[st]);
-        ++out;
-      }
-      if (!ok) break;
-    }
-    if (!ok || n == 0) break;
-    raw0 += n - g0;
+    wait(&C.seg_full[segs % SEGS], (segs / SEGS) & 1);
+    if (!ok) break;
+    const Seg s = C.seg[segs % SEGS];
+    if (s.n == 0) break;
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_addr(&C.seg_empty[segs % SEGS]));
+#pragma unroll 1
+    for (int j = 0; j < s.n; ++j, ++out) {
+      const Keys ky = keys_of<false, true>(A, s, s.j0 + j);
+      const uint32_t st = out % STAGES, rs = SM::RAW_K + raw0 % SM::RAW_V;
+      unsigned char* const dst = smem + SM::STAGE_AT + st * SM::BYTES;
+      wait(&C.empty[st], ((out / STAGES) & 1) ^ 1);
+      if (!ky.staged) wait(&C.full[STAGES + rs], (raw0 / SM::RAW_V) & 1);
+      if (!ok) break;
+      if (ky.staged) {
+        if (lane == 0) {
+          const uint32_t fb = smem_addr(&C.full[st]);
+          if (warp == 0) {
+            mbar_arrive_tx(fb, SM::BYTES);
+            for (int x = 0; x < DP / 64; ++x)
+              tma_3d(smem_addr(dst) + x * 16384, &A.mvn, fb, x * 64, ky.k0, s.b * A.Hkv + s.h);
+          } else {
+            mbar_arrive(fb);
+          }
+        }
+        __syncwarp();
+        continue;
+      }
+      // a row's 16 dimensions of the tile
+      auto put = [&](int row, const uint4& lo, const uint4& hi) {
+        unsigned char* const line = dst + (dim >> 6) * 16384 + row * 128;
+        const int at = dim >> 3 & 7, swap = dim >> 6;
+        *reinterpret_cast<uint4*>(line + (((at + swap) ^ (row & 7)) << 4)) = swap ? hi : lo;
+        *reinterpret_cast<uint4*>(line + (((at + 1 - swap) ^ (row & 7)) << 4)) = swap ? lo : hi;
+      };
+      const unsigned char* const src = smem + SM::RAW_AT + rs * SM::RAW + tid * 16;
+#pragma unroll 1
+      for (int g = 0; g < STEPS; g += BATCH) {
+        uint4 b[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+          b[i] = *reinterpret_cast<const uint4*>(src + (g + i) * (32 * WIDEN_WARPS * 16));
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const uint2 p = widen4(b[i].x), q = widen4(b[i].y), y = widen4(b[i].z), z = widen4(b[i].w);
+          put(row0 + (g + i) * ROWS, make_uint4(p.x, p.y, q.x, q.y), make_uint4(y.x, y.y, z.x, z.y));
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&C.empty[STAGES + rs]));
+      ++raw0;
+      // behind the entries: whatever the bytes are, weights of 0 take zeros
+      const int w = width_of(ky);
+      if (ky.n < w) {
+#pragma unroll 1
+        for (int row = row0; row < w; row += ROWS)
+          if (row >= ky.n) put(row, make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0));
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&C.full[st]));
+    }
+    if (!ok) break;
+  }
+  if (*abort) {  // a staged copy in flight lands before the CTA ends
+    const unsigned long long t0 = globaltimer();
+    for (uint32_t u = out > STAGES ? out - STAGES : 0; u < out; ++u)
+      while (!mbar_try(smem_addr(&C.full[u % STAGES]), (u / STAGES) & 1) &&
+             globaltimer() - t0 < WAIT_LIMIT_NS) {
+      }
   }
 }
 
-// The scales of every segment's cached tiles, as powers of two of eight tokens each, up to
-// SCALES tiles ahead.  As many tiles at once as their blocks fill lanes, since the loads of
-// a page's number and then of its scales take longer than a tile does.
+// The scales of every segment's tiles, as powers of two of eight tokens each, up to SCALES
+// tiles ahead: staged ones as the first kernel left them, cached ones as many tiles at once
+// as their blocks fill lanes, since the loads of a page's number and then of its scales take
+// longer than a tile does.
 template <int NQ, bool PAIR, bool BF>
 __device__ __forceinline__ void read_scales(const AttnParams& A, Ctrl<NQ, PAIR>& C, Ctrl8<NQ>& C8,
                                             volatile int* abort) {
@@ -1330,36 +1177,51 @@ __device__ __forceinline__ void read_scales(const AttnParams& A, Ctrl<NQ, PAIR>&
     if (s.n == 0) break;
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_addr(&C.seg_empty[segs % SEGS]));
-    const int g = staged_of(A, s), c = s.n - g;
-    const int first = s.j0 + g - tiles_of(A.N);  // cached tile
-    for (int j = 0; ok && j < c; j += at_once) {
+    const int g = staged_of(A, s), ts = tiles_of(A.N);
+#pragma unroll 1
+    for (int j = 0; ok && j < s.n;) {
+      const int count = j < g ? 1 : min(at_once, s.n - j);
       // (blocks behind the entries: no part in the tile's largest exponent)
       int k = 0, v = -1000;
       bool nan = false;
-      const int t = (first + j + mine) * TILE + (block << A.block_log);
-      if (mine < at_once && j + mine < c && t < s.len) {
-        const int col = t / A.page;
-        int pg = __ldg(A.table + size_t(s.b) * A.cols + col);
-        if (pg < 0 || pg >= A.num_pages) pg = 0;  // (reported, and its result dropped, elsewhere)
-        const size_t at = (size_t(pg) * A.LH + A.head0 + s.h) * per_page +
-                          ((t - col * A.page) >> A.block_log);
-        k = int(__ldg(A.k_scales + at)) - 127;
-        v = int(__ldg(A.v_scales + at)) - 127;
-        // exponents at which dtype does not hold every value: NaN
-        const int lo = BF ? -117 : -15, hi = BF ? 119 : 7;
-        nan = k < lo || k > hi || v < lo || v > hi;
-        if (nan) k = v = 0;
+      float word[2] = {0.0f, 0.0f};
+      if (j < g) {
+        const float* const from = reinterpret_cast<const float*>(
+            A.t8 + (size_t(s.b) * A.Hkv + s.h) * ts + s.j0 + j);
+        word[0] = __ldg(from + lane);
+        if (lane < int(sizeof(Tile8) / 4) - 32) word[1] = __ldg(from + 32 + lane);
+      } else {
+        const int t = (s.j0 + j - ts + mine) * TILE + (block << A.block_log);
+        if (mine < count && t < s.len) {
+          const int col = t / A.page;
+          int pg = __ldg(A.table + size_t(s.b) * A.cols + col);
+          if (pg < 0 || pg >= A.num_pages) pg = 0;  // (reported, and its result dropped, elsewhere)
+          const size_t at = (size_t(pg) * A.LH + A.head0 + s.h) * per_page +
+                            ((t - col * A.page) >> A.block_log);
+          k = int(__ldg(A.k_scales + at)) - 127;
+          v = int(__ldg(A.v_scales + at)) - 127;
+          // exponents at which dtype does not hold every value: NaN
+          const int lo = BF ? -117 : -15, hi = BF ? 119 : 7;
+          nan = k < lo || k > hi || v < lo || v > hi;
+          if (nan) k = v = 0;
+        }
       }
       int top = v;  // of the tile
       for (int x = 1; x < blocks; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
       const float kf = power(k), vd = nan ? __int_as_float(0x7fffffff) : float(max(v - top, LEAST));
       const float vf = nan ? vd : power(NQ ? max(v - top, LEAST) : -max(v - top, LEAST));
-      for (int x = 0; ok && x < at_once && j + x < c; ++x, ++tiles) {
+#pragma unroll 1
+      for (int x = 0; x < count; ++x, ++tiles) {
         const uint32_t sc = tiles % SCALES;
         ok = warp_wait(smem_addr(&C8.empty[sc]), ((tiles / SCALES) & 1) ^ 1, A.status, abort);
         if (!ok) break;
-        if (mine == x) {
-          Tile8& t8 = C8.tile[sc];
+        Tile8& t8 = C8.tile[sc];
+        if (j < g) {
+          float* const to = reinterpret_cast<float*>(&t8);
+          to[lane] = word[0];
+          if (lane < int(sizeof(Tile8) / 4) - 32) to[32 + lane] = word[1];
+        } else if (mine == x) {
+#pragma unroll 1
           for (int i = block * rep; i < block * rep + rep; ++i) {
             t8.kf[i] = kf;
             t8.vd[i] = vd;
@@ -1370,7 +1232,129 @@ __device__ __forceinline__ void read_scales(const AttnParams& A, Ctrl<NQ, PAIR>&
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&C8.full[sc]));
       }
+      j += count;
     }
+  }
+}
+
+// -------------------------------------------------------------- queries and staged entries
+
+// What the kernel before the attention over 8-bit pages makes of the queries and the staged
+// entries, so that they arrive there by copies like everything else: the terms of both, the
+// staged values in fp16, and their powers of two.  (Made by the attention kernel's own warps
+// first: 6 us more per item, in which the tiles waited.)
+struct Prep8 {
+  const uint16_t* q;
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  uint8_t* q8;    // [TERMS][B][N][Hq][D]
+  uint8_t* k8;    // [TERMS][B][Hkv][N][D]
+  uint16_t* v16;  // [B][Hkv][N][D]
+  float* qf;      // [B][N][Hq]
+  Tile8* t8;      // [B][Hkv][tiles]
+  int B, N, Hq, Hkv, D, LH, head0, turned;
+};
+constexpr int PREP_THREADS = 128, PREP_ROWS = 64;  // query rows of a CTA
+inline long long prep8_blocks(const Prep8& P) {
+  return (long long)P.B * P.Hkv * ((P.N + TILE - 1) / TILE) +
+         ((long long)P.B * P.N * P.Hq + PREP_ROWS - 1) / PREP_ROWS;
+}
+
+// The first B * Hkv * tiles CTAs a staged tile each, eight keys of which share a power of two;
+// the others PREP_ROWS query rows.  A thread takes 16 dimensions of a row.
+template <int DP, bool BF>
+__global__ void __launch_bounds__(PREP_THREADS) sv_attn8_prep(const __grid_constant__ Prep8 P) {
+  constexpr int TERMS = TERMS_OF<BF>, PER_ROW = DP / 16, WARP_ROWS = 32 / PER_ROW;
+  __shared__ int exps[16];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  const int dim = lane % PER_ROW * 16, lane_row = lane / PER_ROW;
+  struct Row { uint4 lo, hi; };
+  auto fetch = [&](const uint16_t* src, bool on) {  // zeros where there is nothing
+    Row r = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (on && dim < P.D) {
+      r.lo = __ldg(reinterpret_cast<const uint4*>(src + dim));
+      r.hi = __ldg(reinterpret_cast<const uint4*>(src + dim) + 1);
+    }
+    return r;
+  };
+  auto size = [](const Row& r) { return max(size_of<BF>(r.lo), size_of<BF>(r.hi)); };
+  auto terms = [&](const Row& u, int e, uint8_t* to, size_t stride) {
+    const float by = power(-min(e, 119));
+    uint2 lo[TERMS], hi[TERMS];
+    split_terms<TERMS>(to_half<BF>(u.lo, by), lo);
+    split_terms<TERMS>(to_half<BF>(u.hi, by), hi);
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t)
+      *reinterpret_cast<uint4*>(to + t * stride + dim) = make_uint4(lo[t].x, lo[t].y, hi[t].x, hi[t].y);
+  };
+  const int ts = tiles_of(P.N);
+  const long long staged = (long long)P.B * P.Hkv * ts;
+  if (blockIdx.x < staged) {
+    const int tile = int(blockIdx.x) % ts, bh = int(blockIdx.x) / ts, b = bh / P.Hkv, h = bh - b * P.Hkv;
+    const int k0 = tile * TILE, n = min(TILE, P.N - k0);
+    const size_t from = ((size_t(b) * P.LH + P.head0 + h) * P.N + k0) * P.D;
+    const size_t to = (size_t(bh) * P.N + k0) * P.D, stride = size_t(P.B) * P.Hkv * P.N * P.D;
+    Tile8& t8 = P.t8[blockIdx.x];
+    for (int g = warp; g < 16; g += PREP_THREADS / 32) {
+      constexpr int V = 8 / WARP_ROWS;  // rows of a lane
+      Row k[V], v[V];
+      uint32_t k_most = 0, v_most = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int row = g * 8 + i * WARP_ROWS + lane_row;
+        k[i] = fetch(P.k_new + from + size_t(row) * P.D, row < n);
+        v[i] = fetch(P.v_new + from + size_t(row) * P.D, row < n);
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        k_most = max(k_most, size(k[i]));
+        v_most = max(v_most, size(v[i]));
+      }
+      const int e = exponent_over(__reduce_max_sync(0xffffffffu, k_most));
+      const int ev = exponent_over(__reduce_max_sync(0xffffffffu, v_most));
+      if (lane == 0) {
+        t8.kf[g] = power_or_nan(e);
+        exps[g] = g * 8 >= n ? -1000 : e == NOT_FINITE ? e : ev;
+      }
+      const float by = power(-min(ev, 119));
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int row = g * 8 + i * WARP_ROWS + lane_row;
+        if (row < n && dim < P.D) {
+          terms(k[i], e, P.k8 + to + size_t(row) * P.D, stride);
+          uint4* const out = reinterpret_cast<uint4*>(P.v16 + to + size_t(row) * P.D + dim);
+          out[0] = to_half<BF>(v[i].lo, by);
+          out[1] = to_half<BF>(v[i].hi, by);
+        }
+      }
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const int ev = lane < 16 ? exps[lane] : -1000;
+      const int top = __reduce_max_sync(0xffffffffu, ev == NOT_FINITE ? 0 : ev);
+      const int by = max(ev - top, LEAST);
+      const float nan = __int_as_float(0x7fffffff);
+      if (lane < 16) {
+        t8.vd[lane] = ev == NOT_FINITE ? nan : float(by);
+        t8.vf[lane] = ev == NOT_FINITE ? nan : power(P.turned ? by : -by);
+      }
+      if (lane == 0) t8.top = top;
+    }
+    return;
+  }
+  const long long rows = (long long)P.B * P.N * P.Hq, r0 = (blockIdx.x - staged) * PREP_ROWS;
+#pragma unroll
+  for (int i = 0; i < PREP_ROWS / (4 * WARP_ROWS); ++i) {
+    const long long r = r0 + (i * 4 + warp) * WARP_ROWS + lane_row;
+    const Row u = fetch(P.q + r * P.D, r < rows);
+    uint32_t most = size(u);
+#pragma unroll
+    for (int k = 1; k < PER_ROW; k *= 2)  // (a row's lanes are neighbours)
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, k));
+    const int e = exponent_over(most);
+    if (r < rows && dim < P.D) terms(u, e, P.q8 + r * P.D, size_t(rows) * P.D);
+    if (r < rows && dim == 0) P.qf[r] = power_or_nan(e);
   }
 }
 
@@ -1385,14 +1369,14 @@ __device__ __forceinline__ void read_scales(const AttnParams& A, Ctrl<NQ, PAIR>&
 // The weights are rounded once to the storage type (half a step each); their sum
 // l is taken before that, in 32 bits.
 // 8-bit caches (Q8) add
-//   widen     a warpgroup: queries and staged keys to terms in e4m3, values to fp16
+//   widen     four warps: cached values from bytes to fp16
 //   scales    the blocks' powers of two, a few tiles ahead
 template <int DP, int NQ, bool PAIR, bool PR, bool BF, bool Q8 = false>
 __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
     sv_attn(const __grid_constant__ AttnParams A) {
   static_assert(!(NQ && (PAIR || PR)), "few rows make one tile, and prompts have many");
   static_assert(!(Q8 && PR), "8-bit entries are in pages");
-  constexpr int TERMS = Q8 ? TERMS_OF<BF> : 0, PARTS = (TERMS + 1) / 2;
+  constexpr int TERMS = Q8 ? TERMS_OF<BF> : 0;
   using SM = Smem<DP, NQ, TERMS, PAIR>;
   constexpr int NT = Q8 ? THREADS8 : THREADS;
   constexpr int STAGES = SM::STAGES, BYTES = SM::BYTES, HALVES = DP / 64;
@@ -1420,14 +1404,13 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         mbar_init(bar(&C.full[i]), 1);
         mbar_init(bar(&C.empty[i]), i < STAGES + SM::RAW_K ? 1 : WIDEN_WARPS);
       }
-      for (int i = 0; i < SEGS; ++i) C8.staged[i][0].count = C8.staged[i][1].count = 0;
       for (int i = 0; i < SCALES; ++i) {
         mbar_init(bar(&C8.full[i]), 1);
         mbar_init(bar(&C8.empty[i]), PAIR ? 8 : 4);
       }
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(&C.q_full[i]), Q8 ? WIDEN_WARPS : 1);
+      mbar_init(bar(&C.q_full[i]), 1);
       mbar_init(bar(&C.q_empty[i]), 1);
       mbar_init(bar(&C.s_full[i]), 1);
       mbar_init(bar(&C.p_half[i]), 4);
@@ -1518,6 +1501,8 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
   // the join may be launched now: its blocks find room when this grid's CTAs
   // leave, and wait for the last of them before they read anything
   if (!PR && A.join) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // (the first kernel of a call over 8-bit pages: its outputs are there from here on)
+  if (Q8) asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t tmem = C.tmem;
   const int start_b = C.start_b;
   const long long start_at = C.start_at;
@@ -1541,7 +1526,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
     const int rt = row / A.G, rg = row - rt * A.G;
     const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's TMEM lanes
     const uint32_t ts = tmem + lanes + st * S_COLS, to = tmem + lanes + O_AT + st * S_COLS;
-    uint32_t idx = 0, tiles8 = 0;  // (Q8: cached tiles before the segment)
+    uint32_t idx = 0, tiles8 = 0;  // (Q8: tiles before the segment)
     int segs = 0, parent_b = -1, parent_bad = 0;
     unsigned s_use = 0, o_use[2] = {0, 0};
     bool ok = true;
@@ -1566,6 +1551,14 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
       const int c0 = Q8 ? max(s.j0 - tiles_of(A.N), 0) : s.j0;
       const int c1 = Q8 ? s.j0 + n - tiles_of(A.N) : s.j0 + n;
       const bool has_staged = Q8 ? staged > 0 : s.j0 + n > ct;
+      float qf = 1.0f;  // Q8: the row's power of two
+      if (Q8) {
+        const int r = NQ ? row : rt, t = NQ ? row / A.G : tok;  // (column `row` is of token row / G)
+        const bool on = NQ ? row < A.N * A.G : active;
+        if (on)
+          qf = __ldg(A.qf + (size_t(s.b) * A.N + t) * A.Hq + s.h * A.G + (NQ ? row - t * A.G : rg));
+        if (NQ && r < NQ) C8.qf[st][row] = qf;
+      }
       int bad = s.bad;
       if (!PR && (Q8 || A.kind == TREE)) {
         // pages in use by this segment, and the parent array
@@ -1650,11 +1643,10 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         tc_after();
         // Q8: the tile's powers of two
         const Tile8* t8 = nullptr;
-        const uint32_t tile8 = tiles8 + jj - staged, sc = tile8 % SCALES;
+        const uint32_t tile8 = tiles8 + jj, sc = tile8 % SCALES;
         if (Q8) {
-          t8 = ky.staged ? &C8.staged[segs % SEGS][ky.k0 / TILE] : &C8.tile[sc];
-          if (!ky.staged)
-            ok = ok && warp_wait(bar(&C8.full[sc]), (tile8 / SCALES) & 1, A.status, abort);
+          t8 = &C8.tile[sc];
+          ok = ok && warp_wait(bar(&C8.full[sc]), (tile8 / SCALES) & 1, A.status, abort);
           if (NQ == 0 && !ok) break;
         }
         // (The scores' keys have arrived, and so has every copy before them, among
@@ -1702,7 +1694,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
           }
           softmax_few<NQ, BF, Q8>(A, C, st, row, ts, to, sees, masked, done > 0, unset, lq,
                                   smem + SM::P_AT + st * SM::P_BYTES,
-                                  t8, C8.qf[segs % SEGS], top);
+                                  t8, C8.qf[st], top);
         } else if (!warp_active) {
           __syncwarp();
           half_done();
@@ -1710,7 +1702,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
           // Q8: what the scores of eight keys are multiplied by, and the weights' exponents moved by
           float qc = 0.0f, adj = 0.0f, spoilt = 0.0f, sink = 1.0f;
           if (Q8) {
-            qc = A.c * power_of(C8.qx[segs % SEGS][(PAIR ? st * TILE : 0) + row]);
+            qc = A.c * qf;
             if (done == 0 || t8->top > top) {
               if (done) sink = power(max(top - (t8->top + VALUE_SLACK), -126));
               top = t8->top + VALUE_SLACK;
@@ -2008,7 +2000,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar(&C.p_full[st]));
-          if (Q8 && !ky.staged) mbar_arrive(bar(&C8.empty[sc]));
+          if (Q8) mbar_arrive(bar(&C8.empty[sc]));
         }
       }
 
@@ -2223,7 +2215,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
       }
       d_flags = s.j0 + n < s.nt ? d_flags | DESC_OUT : d_flags & ~DESC_OUT;
       idx += 2 * n;
-      tiles8 += n - staged;
+      tiles8 += n;
       seg_done(segs);
       ++segs;
     }
@@ -2232,7 +2224,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
     __syncwarp();
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<NQ, Q8>::OTHER));
   if (Q8 && (warp & 2)) {
-    if constexpr (Q8) widen_tiles<DP, NQ, PAIR, BF>(A, C, C8, smem, abort);
+    if constexpr (Q8) widen_tiles<DP, NQ, PAIR, BF>(A, C, smem, abort);
   } else if (warp == (Q8 ? PLAN8_WARP : PLAN_WARP)) {
     // ------------------------------------------------------------ the plan
     Cursor<PAIR, PR> cur;
@@ -2327,15 +2319,21 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         if (s.n == 0) break;
         together();
         if (lead) mbar_arrive(bar(&C.seg_empty[segs % AHEAD]));
-        const int slot = PAIR ? 0 : segs & 1;
-        const int use = PAIR ? segs : segs >> 1;
-        if (!Q8) ok = wait(bar(&C.q_empty[slot]), (use & 1) ^ 1);  // (passes before the first use)
+        constexpr bool TURNS = !PAIR && (!Q8 || SM::Q_SLOTS == 2);
+        const int slot = TURNS ? segs & 1 : 0;
+        const int use = TURNS ? segs >> 1 : segs;
+        ok = wait(bar(&C.q_empty[slot]), (use & 1) ^ 1);  // (passes before the first use)
         if (!ok) break;
-        if (!Q8 && lead) {
+        if (lead) {
           const uint32_t fb = bar(&C.q_full[slot]);
-          mbar_arrive_tx(fb, (PAIR ? 2 : 1) * A.q_rows * DP * 2);
+          mbar_arrive_tx(fb, (PAIR ? 2 : 1) * A.q_rows * DP * (Q8 ? TERMS : 2));
           const int tok = PR ? s.start : s.b * A.N;
-          for (int q = 0; q < (PAIR ? 2 : 1); ++q)
+          if constexpr (Q8)
+#pragma unroll 1
+            for (int q = 0; q < (PAIR ? 2 : 1) * TERMS; ++q)
+              tma_5d(base + (PAIR ? q / TERMS : slot) * SM::Q_BYTES + q % TERMS * SM::TERM, &A.mq, fb, 0,
+                     0, s.h, tok + (s.mt * (PAIR ? 2 : 1) + q / TERMS) * A.tpt, q % TERMS);
+          for (int q = 0; q < (Q8 ? 0 : PAIR ? 2 : 1); ++q)
             for (int x = 0; x < HALVES; ++x)
               tma_4d(base + (PAIR ? q : slot) * SM::Q_BYTES + x * (SM::Q_BYTES / HALVES), &A.mq,
                      fb, x * 64, 0, s.h, tok + (s.mt * (PAIR ? 2 : 1) + q) * A.tpt);
@@ -2343,9 +2341,8 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         together();
         ++segs;
         const int plane = PR ? s.h : s.b * A.LH + A.head0 + s.h;
-        auto tile = [&](int jj, bool is_v) {
+        auto tile = [&](int jj, bool is_v, int term = 0) {
           const Keys ky = keys_of<PR, Q8>(A, s, s.j0 + jj);
-          if (Q8 && ky.staged) return true;  // (the widening warps')
           if constexpr (Q8) {  // of the keys' stages, or the values'
             const uint32_t u = is_v ? v_at : k_at;
             st = is_v ? SM::RAW_K + u % SM::RAW_V : u % SM::RAW_K;
@@ -2360,7 +2357,12 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
             else if (Q8) --k_at;
             return false;
           }
-          if (SOLO || ky.staged) {
+          if (Q8 && ky.staged) {  // a term of the keys
+            if (lead) {
+              mbar_arrive_tx(fb, SM::RAW);
+              tma_3d(dst, &A.mkn, fb, 0, ky.k0, (term * A.B + s.b) * A.Hkv + s.h);
+            }
+          } else if (SOLO || ky.staged) {
             if (lead) {
               const CUtensorMap* const m = !PR && ky.staged ? (is_v ? &A.mvn : &A.mkn)
                                                             : (is_v ? &A.mv : &A.mk);
@@ -2402,9 +2404,13 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         constexpr int LAG = PAIR ? 0 : 1;
         if constexpr (Q8) {
 #pragma unroll 1
-          for (int x = 0; ok && x < 2 * (s.n + LAG); ++x) {  // (one copy of the code)
+          for (int x = 0, term = 0; ok && x < 2 * (s.n + LAG);) {  // (one copy of the code)
             const int i = (x >> 1) - (x & 1 ? LAG : 0);
-            if (i >= 0 && i < s.n) ok = tile(i, x & 1);
+            const bool staged = s.j0 + i < tiles_of(A.N);  // (values: the widening warps')
+            if (i >= 0 && i < s.n && !(staged && (x & 1))) ok = tile(i, x & 1, term);
+            if (staged && !(x & 1) && i < s.n && ++term < TERMS) continue;
+            term = 0;
+            ++x;
           }
         } else {
           for (int i = 0; ok && i < s.n + LAG; ++i) {
@@ -2428,8 +2434,9 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         } else {
           land(idx, 0, STAGES);
         }
-        for (int u = Q8 ? segs : max(0, segs - (PAIR ? 1 : 2)); u < segs; ++u)
-          while (!mbar_try(bar(&C.q_full[PAIR ? 0 : u & 1]), (PAIR ? u : u >> 1) & 1) &&
+        constexpr bool TURNS = !PAIR && (!Q8 || SM::Q_SLOTS == 2);
+        for (int u = max(0, segs - (TURNS ? 2 : 1)); u < segs; ++u)
+          while (!mbar_try(bar(&C.q_full[TURNS ? u & 1 : 0]), (TURNS ? u >> 1 : u) & 1) &&
                  globaltimer() - t0 < WAIT_LIMIT_NS) {
           }
       }
@@ -2495,7 +2502,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
     if (elect_one()) {
     if constexpr (Q8) {
       const uint32_t id_8 = instr_desc8(NQ);  // (0: the tile's width goes there)
-      uint32_t raw0 = 0;                      // cached tiles before the segment
+      uint32_t raw0 = 0;                      // stages of keys before the segment
       while (ok) {
         ok = mbar_wait(bar(&C.seg_full[segs % AHEAD]), (segs / AHEAD) & 1, A.status, abort);
         if (!ok) break;
@@ -2524,43 +2531,23 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
               mma8_ss<DP>(tmem + st * S_COLS, NQ ? b : a, NQ ? a : b, id, more || t > 0 || k > 0);
             }
         };
-        // a staged tile's scores, all of its terms (pairs: for both query tiles)
-        auto staged_scores = [&](int st, int q, int i) {
-          const int w = width(i);
-#pragma unroll 1
-          for (int p = 0; p < PARTS; ++p) {
-            const uint32_t u = idx + wide_k<PAIR>(i, PARTS) + p;
-            if (!full(u)) return false;
-            const uint32_t at = base + SM::STAGE_AT + (u % STAGES) * BYTES;
-#pragma unroll 1
-            for (int x = 0; x < (PAIR ? 4 : 2); ++x) {
-              const int kt = x & 1, y = x >> 1;
-              if (2 * p + kt < TERMS) term(st + y, q + y, at + kt * SM::RAW, w, p > 0 || kt > 0);
-            }
-            mma_commit(bar(&C.empty[u % STAGES]));
-          }
-          mma_commit(bar(&C.s_full[st]));
-          if (PAIR) mma_commit(bar(&C.s_full[st + 1]));
-          return true;
-        };
         // One copy of the scores' code: step j first finishes tile j - AHEAD8's values.
         constexpr int AHEAD8 = PAIR ? 1 : 2;
 #pragma unroll 1
         for (int i = 0; ok && i < n + AHEAD8; ++i) {
           const int j = i - AHEAD8;  // the tile whose weights are next
           const bool raw = i >= g && i < n;
-          const uint32_t ku = raw0 + i - g, ks = ku % SM::RAW_K;
-          const uint32_t ka = base + SM::RAW_AT + ks * SM::RAW;
-          auto raw_here = [&] {
-            if (!mbar_wait(bar(&C.full[STAGES + ks]), (ku / SM::RAW_K) & 1, A.status, abort))
+          const uint32_t ku = raw0 + (i < g ? i * TERMS : g * TERMS + i - g), ks = ku % SM::RAW_K;
+          auto raw_here = [&](uint32_t u) {
+            if (!mbar_wait(bar(&C.full[STAGES + u % SM::RAW_K]), (u / SM::RAW_K) & 1, A.status, abort))
               return false;
             tc_after();
             return true;
           };
-          const uint32_t uv = idx + wide_v<PAIR>(j, g, PARTS);
+          const uint32_t uv = idx + j;
           const int w = width(j);
           if (j >= 0) ok = full(uv);
-          if (raw) ok = ok && raw_here();
+          if (raw) ok = ok && raw_here(ku);
 #pragma unroll
           for (int x = 0; x < (PAIR ? 2 : 1); ++x) {
             const int st = PAIR ? x : i & 1;
@@ -2575,16 +2562,30 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
               if (i >= n) mma_commit(bar(&C.o_full[st]));
             }
             if (ok && raw) {
-              term(st, PAIR ? x : slot, ka, width(i), false);
+              term(st, PAIR ? x : slot, base + SM::RAW_AT + ks * SM::RAW, width(i), false);
               mma_commit(bar(&C.s_full[st]));
               if (!PAIR || x == 1) mma_commit(bar(&C.empty[STAGES + ks]));
             }
           }
-          if (ok && i < g) ok = staged_scores(PAIR ? 0 : i & 1, PAIR ? 0 : slot, i);
+          if (i < g) {  // a staged tile, by its keys' terms (pairs: for both query tiles)
+            const int st = PAIR ? 0 : i & 1;
+#pragma unroll 1
+            for (int y = 0; ok && y < TERMS; ++y) {
+              const uint32_t u = ku + y, at = base + SM::RAW_AT + u % SM::RAW_K * SM::RAW;
+              ok = raw_here(u);
+              if (!ok) break;
+#pragma unroll 1
+              for (int x = 0; x < (PAIR ? 2 : 1); ++x)
+                term(st + x, PAIR ? x : slot, at, width(i), y > 0);
+              mma_commit(bar(&C.empty[STAGES + u % SM::RAW_K]));
+            }
+            mma_commit(bar(&C.s_full[st]));
+            if (PAIR) mma_commit(bar(&C.s_full[st + 1]));
+          }
           if (ok && i + 1 == n) mma_commit(bar(&C.q_empty[slot]));  // (queries done with)
         }
-        idx += n + PARTS * g;
-        raw0 += n - g;
+        idx += n;
+        raw0 += n - g + TERMS * g;
         ++segs;
       }
     }
@@ -2833,19 +2834,27 @@ int launch_as(const AttnParams& A, int device, int grid, int ctas, cudaStream_t 
       return SV_ERR_CUDA;
     raised.fetch_or(mark, std::memory_order_release);
   }
-  sv_attn<DP, NQ, PAIR, PR, BF, Q8>
-      <<<grid, Q8 ? THREADS8 : THREADS, (Smem<DP, NQ, Q8 ? TERMS_OF<BF> : 0, PAIR>::TOTAL), st>>>(A);
-  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
-  if (PR || !A.join) return SV_OK;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(JOIN_BLOCKS * ctas));
-  cfg.blockDim = dim3(JOIN_WARPS * 32);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  if (Q8) {  // (sets up beside the kernel that splits the queries)
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(THREADS8);
+    cfg.dynamicSmemBytes = Smem<DP, NQ, Q8 ? TERMS_OF<BF> : 0, PAIR>::TOTAL;
+    if (cudaLaunchKernelEx(&cfg, sv_attn<DP, NQ, PAIR, PR, BF, Q8>, A) != cudaSuccess)
+      return SV_ERR_CUDA;
+    cfg.dynamicSmemBytes = 0;
+  } else {
+    sv_attn<DP, NQ, PAIR, PR, BF, Q8><<<grid, THREADS, (Smem<DP, NQ>::TOTAL), st>>>(A);
+    if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  }
+  if (PR || !A.join) return SV_OK;
+  cfg.gridDim = dim3(unsigned(JOIN_BLOCKS * ctas));
+  cfg.blockDim = dim3(JOIN_WARPS * 32);
   return cudaLaunchKernelEx(&cfg, sv_attn_join<DP, NQ, PAIR, BF>, A, ctas) == cudaSuccess ? SV_OK
                                                                                 : SV_ERR_CUDA;
 }
@@ -2863,7 +2872,12 @@ int launch_dp(const AttnParams& A, Layout l, int device, int grid, int ctas, cud
 
 // The same over an 8-bit cache.
 template <int DP, bool BF>
-int launch_dp8(const AttnParams& A, Layout l, int device, int grid, int ctas, cudaStream_t st) {
+int launch_dp8(const AttnParams& A, const Prep8& P, Layout l, int device, int grid, int ctas,
+               cudaStream_t st) {
+  const long long blocks = prep8_blocks(P);
+  if (blocks > 0x7fffffffLL) return SV_ERR_INVALID_ARG;
+  sv_attn8_prep<DP, BF><<<unsigned(blocks), PREP_THREADS, 0, st>>>(P);
+  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
   if (l.nq == 16) return launch_as<DP, 16, false, false, BF, true>(A, device, grid, ctas, st);
   if (l.nq == 32) return launch_as<DP, 32, false, false, BF, true>(A, device, grid, ctas, st);
   if (l.rows == TILE) return launch_as<DP, 0, false, false, BF, true>(A, device, grid, ctas, st);
@@ -2874,8 +2888,10 @@ int launch_dp8(const AttnParams& A, Layout l, int device, int grid, int ctas, cu
 // attn8_f16.cu), compiled side by side.
 int launch_bf16(const AttnParams& A, Layout l, int device, int grid, int ctas, cudaStream_t st);
 int launch_f16(const AttnParams& A, Layout l, int device, int grid, int ctas, cudaStream_t st);
-int launch8_bf16(const AttnParams& A, Layout l, int device, int grid, int ctas, cudaStream_t st);
-int launch8_f16(const AttnParams& A, Layout l, int device, int grid, int ctas, cudaStream_t st);
+int launch8_bf16(const AttnParams& A, const Prep8& P, Layout l, int device, int grid, int ctas,
+                 cudaStream_t st);
+int launch8_f16(const AttnParams& A, const Prep8& P, Layout l, int device, int grid, int ctas,
+                cudaStream_t st);
 
 }  // namespace svattn
 

@@ -2,8 +2,8 @@
 
 #include "attention.cuh"
 
-int svattn::launch8_bf16(const AttnParams& A, Layout l, int device, int grid, int ctas,
-                         cudaStream_t st) {
-  return A.D > 64 ? launch_dp8<128, true>(A, l, device, grid, ctas, st)
-                  : launch_dp8<64, true>(A, l, device, grid, ctas, st);
+int svattn::launch8_bf16(const AttnParams& A, const Prep8& P, Layout l, int device, int grid,
+                         int ctas, cudaStream_t st) {
+  return A.D > 64 ? launch_dp8<128, true>(A, P, l, device, grid, ctas, st)
+                  : launch_dp8<64, true>(A, P, l, device, grid, ctas, st);
 }
