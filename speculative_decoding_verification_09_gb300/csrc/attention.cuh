@@ -1062,6 +1062,117 @@ __device__ __forceinline__ float power_or_nan(int e) {
   return e == NOT_FINITE ? __int_as_float(0x7fffffff) : power(e);
 }
 
+// The copies of a call over 8-bit pages, by a warp with a lane per box of page rows: a
+// segment's query terms, its staged tiles' keys' terms, then its cached tiles' keys and values.
+// Little is done per tile (pages' numbers are read a tile ahead, places found without a
+// division), since a single warp gets an instruction about every ten cycles here (64 trees of 22
+// nodes: 289 us with the loop of the 16-bit caches, whose tiles are twice as long).
+template <int DP, int NQ, bool PAIR, bool BF>
+__device__ __forceinline__ void copy_bytes(const AttnParams& A, Ctrl<NQ, PAIR>& C,
+                                           unsigned char* smem, volatile int* abort) {
+  constexpr int TERMS = TERMS_OF<BF>;
+  using SM = Smem<DP, NQ, TERMS, PAIR>;
+  constexpr bool TURNS = !PAIR && SM::Q_SLOTS == 2;
+  const int lane = int(threadIdx.x) & 31, boxes = TILE / A.box;
+  const uint32_t raw = smem_addr(smem) + SM::RAW_AT;
+  const int cols = TILE / A.page, rows = TILE - cols * A.page;  // from a tile to the next
+  uint32_t k_at = 0, v_at = 0;  // copies of keys and of values
+  int segs = 0;
+  bool ok = true;
+  auto wait = [&](unsigned long long* b, uint32_t parity) {
+    ok = ok && warp_wait(smem_addr(b), parity, A.status, abort);
+    return ok;
+  };
+  // the next stage of keys, waited for
+  auto key_stage = [&](uint32_t& fb) {
+    const uint32_t st = k_at % SM::RAW_K;
+    if (!wait(&C.empty[SM::STAGES + st], ((k_at / SM::RAW_K) & 1) ^ 1)) return 0u;
+    ++k_at;
+    fb = smem_addr(&C.full[SM::STAGES + st]);
+    return raw + st * SM::RAW;
+  };
+  for (;; ++segs) {
+    if (!wait(&C.seg_full[segs % SEGS], (segs / SEGS) & 1)) break;
+    const Seg s = C.seg[segs % SEGS];
+    if (s.n == 0) break;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&C.seg_empty[segs % SEGS]));
+    const int ts = tiles_of(A.N), g = staged_of(A, s), first = s.j0 + g - ts, n = s.n - g;
+    // the first cached tile's place of this lane's box, and its page
+    int t = first * TILE + lane * A.box, col = t / A.page, row = t - col * A.page, page = 0;
+    const int32_t* const table = A.table + size_t(s.b) * A.cols;
+    if (n > 0 && lane < boxes && t < s.len) page = __ldg(table + col);
+    // (passes before the first use)
+    const int slot = TURNS ? segs & 1 : 0;
+    if (!wait(&C.q_empty[slot], ((TURNS ? segs >> 1 : segs) & 1) ^ 1)) break;
+    if (lane == 0) {
+      const uint32_t fb = smem_addr(&C.q_full[slot]);
+      mbar_arrive_tx(fb, (PAIR ? 2 : 1) * A.q_rows * DP * TERMS);
+#pragma unroll 1
+      for (int q = 0; q < (PAIR ? 2 : 1) * TERMS; ++q)
+        tma_5d(smem_addr(smem) + (PAIR ? q / TERMS : slot) * SM::Q_BYTES + q % TERMS * SM::TERM, &A.mq,
+               fb, 0, 0, s.h, s.b * A.N + (s.mt * (PAIR ? 2 : 1) + q / TERMS) * A.tpt, q % TERMS);
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int i = 0; i < g * TERMS; ++i) {
+      uint32_t fb = 0;
+      const uint32_t dst = key_stage(fb);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_tx(fb, SM::RAW);
+        tma_3d(dst, &A.mkn, fb, 0, (s.j0 + i / TERMS) * TILE, (i % TERMS * A.B + s.b) * A.Hkv + s.h);
+      }
+      __syncwarp();
+    }
+#pragma unroll 1
+    for (int i = 0; ok && i < n; ++i) {
+      // a page outside the pool is read as page 0 (the softmax warps report it and drop the result)
+      const int pg = page < 0 || page >= A.num_pages ? 0 : page, r = row;
+      const int here = min(boxes, (s.len - (first + i) * TILE + A.box - 1) / A.box);
+      t += TILE;
+      col += cols;
+      row += rows;
+      if (row >= A.page) {
+        row -= A.page;
+        ++col;
+      }
+      if (i + 1 < n && lane < boxes && t < s.len) page = __ldg(table + col);
+      uint32_t fb = 0;
+      const uint32_t dst = key_stage(fb);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_tx(fb, here * A.box * DP);
+      __syncwarp();
+      if (lane < here) tma_4d(dst + lane * A.box * DP, &A.mk, fb, 0, r, A.head0 + s.h, pg);
+      const uint32_t st = SM::RAW_K + v_at % SM::RAW_V;
+      if (!wait(&C.empty[SM::STAGES + st], ((v_at / SM::RAW_V) & 1) ^ 1)) break;
+      ++v_at;
+      fb = smem_addr(&C.full[SM::STAGES + st]);
+      if (lane == 0) mbar_arrive_tx(fb, here * A.box * DP);
+      __syncwarp();
+      if (lane < here)
+        tma_4d(raw + st * SM::RAW + lane * A.box * DP, &A.mv, fb, 0, r, A.head0 + s.h, pg);
+      __syncwarp();
+    }
+    if (!ok) break;
+  }
+  if (*abort) {  // the copies in flight land before the CTA ends
+    const unsigned long long t0 = globaltimer();
+    auto land = [&](uint32_t at, unsigned long long* full, uint32_t count) {
+      for (uint32_t u = at > count ? at - count : 0; u < at; ++u)
+        while (!mbar_try(smem_addr(full + u % count), (u / count) & 1) &&
+               globaltimer() - t0 < WAIT_LIMIT_NS) {
+        }
+    };
+    land(k_at, C.full + SM::STAGES, SM::RAW_K);
+    land(v_at, C.full + SM::STAGES + SM::RAW_K, SM::RAW_V);
+    for (int u = max(0, segs - (TURNS ? 2 : 1)); u <= segs; ++u)
+      while (!mbar_try(smem_addr(&C.q_full[TURNS ? u & 1 : 0]), (TURNS ? u >> 1 : u) & 1) &&
+             globaltimer() - t0 < WAIT_LIMIT_NS) {
+      }
+  }
+}
+
 // The widening warps: a segment's values, tile by tile, to fp16.  Cached ones from bytes: a
 // thread takes 16, 16 dimensions of a token, and writes two 16-byte pieces of a 64-dimension
 // block in the 128-byte swizzle; lanes of a row's two blocks write their pieces in opposite
@@ -2297,7 +2408,6 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
   } else if (warp == COPY_WARP) {
     // ------------------------------------------------------------ copies
     // One thread, or (pages) a warp with a lane per box of page rows.
-    constexpr int RAW0 = Q8 ? STAGES : 0;  // the stages' barriers begin there
     auto copies = [&](auto solo) {
       constexpr bool SOLO = decltype(solo)::value;
       const bool lead = SOLO || lane == 0;
@@ -2309,7 +2419,6 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         if (!SOLO) __syncwarp();
       };
       uint32_t st = 0, lap = 0, idx = 0;  // stage, times around the ring, copies
-      uint32_t k_at = 0, v_at = 0;        // Q8: copies of keys and of values
       int segs = 0;
       bool ok = true;
       for (;;) {
@@ -2319,21 +2428,15 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         if (s.n == 0) break;
         together();
         if (lead) mbar_arrive(bar(&C.seg_empty[segs % AHEAD]));
-        constexpr bool TURNS = !PAIR && (!Q8 || SM::Q_SLOTS == 2);
-        const int slot = TURNS ? segs & 1 : 0;
-        const int use = TURNS ? segs >> 1 : segs;
+        const int slot = PAIR ? 0 : segs & 1;
+        const int use = PAIR ? segs : segs >> 1;
         ok = wait(bar(&C.q_empty[slot]), (use & 1) ^ 1);  // (passes before the first use)
         if (!ok) break;
         if (lead) {
           const uint32_t fb = bar(&C.q_full[slot]);
-          mbar_arrive_tx(fb, (PAIR ? 2 : 1) * A.q_rows * DP * (Q8 ? TERMS : 2));
+          mbar_arrive_tx(fb, (PAIR ? 2 : 1) * A.q_rows * DP * 2);
           const int tok = PR ? s.start : s.b * A.N;
-          if constexpr (Q8)
-#pragma unroll 1
-            for (int q = 0; q < (PAIR ? 2 : 1) * TERMS; ++q)
-              tma_5d(base + (PAIR ? q / TERMS : slot) * SM::Q_BYTES + q % TERMS * SM::TERM, &A.mq, fb, 0,
-                     0, s.h, tok + (s.mt * (PAIR ? 2 : 1) + q / TERMS) * A.tpt, q % TERMS);
-          for (int q = 0; q < (Q8 ? 0 : PAIR ? 2 : 1); ++q)
+          for (int q = 0; q < (PAIR ? 2 : 1); ++q)
             for (int x = 0; x < HALVES; ++x)
               tma_4d(base + (PAIR ? q : slot) * SM::Q_BYTES + x * (SM::Q_BYTES / HALVES), &A.mq,
                      fb, x * 64, 0, s.h, tok + (s.mt * (PAIR ? 2 : 1) + q) * A.tpt);
@@ -2341,28 +2444,12 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         together();
         ++segs;
         const int plane = PR ? s.h : s.b * A.LH + A.head0 + s.h;
-        auto tile = [&](int jj, bool is_v, int term = 0) {
-          const Keys ky = keys_of<PR, Q8>(A, s, s.j0 + jj);
-          if constexpr (Q8) {  // of the keys' stages, or the values'
-            const uint32_t u = is_v ? v_at : k_at;
-            st = is_v ? SM::RAW_K + u % SM::RAW_V : u % SM::RAW_K;
-            lap = u / (is_v ? SM::RAW_V : SM::RAW_K);
-            if (is_v) ++v_at;
-            else ++k_at;
-          }
-          const uint32_t fb = bar(&C.full[RAW0 + st]);
-          const uint32_t dst = base + (Q8 ? SM::RAW_AT + st * SM::RAW : SM::STAGE_AT + st * BYTES);
-          if (!wait(bar(&C.empty[RAW0 + st]), (lap & 1) ^ 1)) {
-            if (Q8 && is_v) --v_at;  // (not begun)
-            else if (Q8) --k_at;
-            return false;
-          }
-          if (Q8 && ky.staged) {  // a term of the keys
-            if (lead) {
-              mbar_arrive_tx(fb, SM::RAW);
-              tma_3d(dst, &A.mkn, fb, 0, ky.k0, (term * A.B + s.b) * A.Hkv + s.h);
-            }
-          } else if (SOLO || ky.staged) {
+        auto tile = [&](int jj, bool is_v) {
+          const uint32_t fb = bar(&C.full[st]);
+          const uint32_t dst = base + SM::STAGE_AT + st * BYTES;
+          if (!wait(bar(&C.empty[st]), (lap & 1) ^ 1)) return false;
+          const Keys ky = keys_of<PR>(A, s, s.j0 + jj);
+          if (SOLO || ky.staged) {
             if (lead) {
               const CUtensorMap* const m = !PR && ky.staged ? (is_v ? &A.mvn : &A.mkn)
                                                             : (is_v ? &A.mv : &A.mk);
@@ -2377,73 +2464,50 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
             // a page outside the pool is read as page 0 (the softmax warps report it
             // and drop the result)
             const int boxes = (ky.n + A.box - 1) / A.box;
-            if (lead) mbar_arrive_tx(fb, boxes * A.box * DP * (Q8 ? 1 : 2));
+            if (lead) mbar_arrive_tx(fb, boxes * A.box * DP * 2);
             __syncwarp();
             if (lane < boxes) {
               const int t = ky.k0 + lane * A.box;
               const int col = t / A.page;
               int pg = __ldg(A.table + size_t(s.b) * A.cols + col);
               if (pg < 0 || pg >= A.num_pages) pg = 0;
-              if (Q8)
-                tma_4d(dst + lane * A.box * DP, is_v ? &A.mv : &A.mk, fb, 0, t - col * A.page,
-                       A.head0 + s.h, pg);
 #pragma unroll
-              for (int x = 0; x < (Q8 ? 0 : HALVES); ++x)
+              for (int x = 0; x < HALVES; ++x)
                 tma_4d(dst + x * 16384 + lane * A.box * 128, is_v ? &A.mv : &A.mk, fb, x * 64,
                        t - col * A.page, A.head0 + s.h, pg);
             }
           }
           together();
           ++idx;
-          if (!Q8 && ++st == STAGES) {
+          if (++st == STAGES) {
             st = 0;
             ++lap;
           }
           return true;
         };
         constexpr int LAG = PAIR ? 0 : 1;
-        if constexpr (Q8) {
-#pragma unroll 1
-          for (int x = 0, term = 0; ok && x < 2 * (s.n + LAG);) {  // (one copy of the code)
-            const int i = (x >> 1) - (x & 1 ? LAG : 0);
-            const bool staged = s.j0 + i < tiles_of(A.N);  // (values: the widening warps')
-            if (i >= 0 && i < s.n && !(staged && (x & 1))) ok = tile(i, x & 1, term);
-            if (staged && !(x & 1) && i < s.n && ++term < TERMS) continue;
-            term = 0;
-            ++x;
-          }
-        } else {
-          for (int i = 0; ok && i < s.n + LAG; ++i) {
-            if (i < s.n) ok = tile(i, false);
-            if (ok && i >= LAG) ok = tile(i - LAG, true);
-          }
+        for (int i = 0; ok && i < s.n + LAG; ++i) {
+          if (i < s.n) ok = tile(i, false);
+          if (ok && i >= LAG) ok = tile(i - LAG, true);
         }
         if (!ok) break;
       }
       if (*abort) {  // the copies in flight land before the CTA ends
         const unsigned long long t0 = globaltimer();
-        auto land = [&](uint32_t at, uint32_t first, uint32_t count) {
-          for (uint32_t u = at > count ? at - count : 0; u < at; ++u)
-            while (!mbar_try(bar(&C.full[first + u % count]), (u / count) & 1) &&
-                   globaltimer() - t0 < WAIT_LIMIT_NS) {
-            }
-        };
-        if constexpr (Q8) {
-          land(k_at, STAGES, SM::RAW_K);
-          land(v_at, STAGES + SM::RAW_K, SM::RAW_V);
-        } else {
-          land(idx, 0, STAGES);
-        }
-        constexpr bool TURNS = !PAIR && (!Q8 || SM::Q_SLOTS == 2);
-        for (int u = max(0, segs - (TURNS ? 2 : 1)); u < segs; ++u)
-          while (!mbar_try(bar(&C.q_full[TURNS ? u & 1 : 0]), (TURNS ? u >> 1 : u) & 1) &&
+        for (uint32_t u = idx > STAGES ? idx - STAGES : 0; u < idx; ++u)
+          while (!mbar_try(bar(&C.full[u % STAGES]), (u / STAGES) & 1) &&
+                 globaltimer() - t0 < WAIT_LIMIT_NS) {
+          }
+        for (int u = max(0, segs - (PAIR ? 1 : 2)); u < segs; ++u)
+          while (!mbar_try(bar(&C.q_full[PAIR ? 0 : u & 1]), (PAIR ? u : u >> 1) & 1) &&
                  globaltimer() - t0 < WAIT_LIMIT_NS) {
           }
       }
     };
-    if (!Q8 && (PR || A.kind == RING)) {
-      if constexpr (!Q8)
-        if (elect_one()) copies(Yes<true>());
+    if constexpr (Q8) {
+      copy_bytes<DP, NQ, PAIR, BF>(A, C, smem, abort);
+    } else if (PR || A.kind == RING) {
+      if (elect_one()) copies(Yes<true>());
       __syncwarp();
     } else {
       copies(Yes<false>());
