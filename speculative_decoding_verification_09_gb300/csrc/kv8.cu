@@ -6,12 +6,14 @@
 //   sv_kv8_advance  lengths of a commit that are updated in place
 //
 // A unit is the new entries of one block of tokens and one row: they share a
-// scale, so all of them have to be seen before any is stored.  A CTA holds a unit in
-// registers, sixteen dimensions of a token's key and of its value per thread, finds
-// both largest sizes, and rounds.  Every byte is moved once (a block's older entries
-// only when its scale rises); what bounds it is HBM for prompts, and for single
-// tokens the latency of the loads that depend on one another: bounds, length, page,
-// scale.
+// scale, so all of them have to be seen before any is stored.  A CTA takes the units of one
+// block and several rows, as many at once as two pieces per thread hold (a piece: sixteen
+// dimensions of a token's key and of its value), finds each row's largest sizes, and rounds;
+// the next rows' pieces are on their way to shared memory meanwhile.  Every byte is moved once
+// (a block's older entries only when its scale rises); what bounds it is HBM and the
+// instructions for prompts, and for single tokens and short paths the latency of the loads
+// that depend on one another: bounds, length, page, entries.  (64 paths of 3 entries, 384 rows:
+// 101 us with a CTA per unit, most of whose threads had no entry.)
 
 #include "rope.cuh"
 #include "svkv8.h"
@@ -20,7 +22,9 @@ namespace {
 
 using namespace svrope;
 
-constexpr int MAX_UNIT_THREADS = 1024;  // 128 tokens of 128 dimensions
+constexpr int PIECES = 2;           // of a thread at a time
+constexpr int MAX_THREADS = 512;    // a block of 128 tokens of 128 dimensions is 1024 pieces
+constexpr int MAX_ROWS = 256;       // of a CTA
 
 __device__ __forceinline__ void allow_next_kernel() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -58,15 +62,43 @@ __device__ __forceinline__ uint32_t again(uint32_t w, float f) {
   return to_bytes(v[0].x * f, v[0].y * f, v[1].x * f, v[1].y * f);
 }
 
-// What is not finite becomes NaN; the largest size of the rest, as bits.
-__device__ __forceinline__ uint32_t largest(float (&x)[8], uint32_t most) {
+// The largest size of x and m, or NaN when either has one.
+__device__ __forceinline__ float largest(const float (&x)[8], float m) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(x[i]), "f"(x[i + 1]));
+  return m;
+}
+// That of sixteen 16-bit values.
+template <bool BF>
+__device__ __forceinline__ float largest(const uint4& a, const uint4& b) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t a = __float_as_uint(x[i]) & 0x7fffffffu;
-    if (a >= 0x7f800000u) x[i] = __int_as_float(0x7fffffff);
-    else most = max(most, a);
+    const uint32_t x = w[i] & 0x7fff7fffu;
+    if (BF) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x));
+    else asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(m) : "r"(x));
   }
-  return most;
+  const float2 f = widen<BF>(m);
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(f.x), "f"(f.y));
+  return r;
+}
+// Where some are not finite: those become NaN, and the largest size of the rest.
+__device__ __forceinline__ float largest_finite(float (&x)[8], float m) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (fabsf(x[i]) <= 3.402823466e38f) m = fmaxf(m, fabsf(x[i]));
+    else x[i] = __int_as_float(0x7fffffff);
+  }
+  return m;
+}
+__device__ __forceinline__ bool finite(float m) { return m <= 3.402823466e38f; }
+
+__device__ __forceinline__ void copy_async(uint4* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   uint32_t(__cvta_generic_to_shared(to))), "l"(from) : "memory");
 }
 
 struct Pools {
@@ -79,117 +111,207 @@ struct Pools {
   int chunks;       // D / 16
 };
 
-// The unit of one CTA: new entries in rows `off` .. off + count - 1 of the block of `page`
-// (a valid one) that begins at its row `at`, row `row` of LH.  `src` gives the thread's
-// entry of the block: pointers to its key and value, and the row of angles (or null).
+// A row's largest sizes, as bits, and the block's own exponents, when it holds entries.
+struct RowState { uint32_t k, v; int own_k, own_v; };
+struct Shared {
+  RowState state[MAX_ROWS];
+  uint4 pieces[];  // [stage of two][piece][part of four][thread]
+};
+size_t shared_bytes(int threads) { return sizeof(Shared) + size_t(2 * PIECES * 4) * threads * 16; }
+
+// Entry `e` of a unit: its key and value in the first row, and the row of angles (or null).
+struct Entry {
+  const uint16_t *k, *v;
+  const float* angles;
+};
+
+// The units of rows row0 .. row0 + rows - 1 of LH for the block of `page` (a valid one) that
+// begins at its row `at`: new entries in its rows off .. off + count - 1.  source(e): entry e;
+// the next row's lies k_row, v_row elements behind.
 template <bool BF, class Source>
-__device__ __forceinline__ void write_unit(const Pools& P, int page, int row, int at, int off,
-                                           int count, int rot, bool inter, const Source& src) {
-  __shared__ uint32_t most_of[2][MAX_UNIT_THREADS / 32];
-  const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
-  const int r = tid / P.chunks, c = tid - r * P.chunks;
-  const bool mine = r >= off && r < off + count, older = r < off;
-  const size_t line = (size_t(page) * P.LH + row) * P.page + at;  // the block's first token
-  const size_t scale_at = line / P.block;
-  int own_k = -1000, own_v = -1000;  // the block's exponents, when it holds entries
-  if (off) {
-    own_k = int(P.k_scales[scale_at]) - 127;
-    own_v = int(P.v_scales[scale_at]) - 127;
-  }
-  const bool vec = rot % 16 == 0, turned = 8 * c < rot / 2;
-  const int d0 = vec && turned && !inter ? 8 * c : 16 * c;
-  const int d1 = vec && turned && !inter ? d0 + rot / 2 : d0 + 8;
-  float ka[8], kb[8], va[8], vb[8];
-  if (mine) {
-    const uint16_t *k, *v;
-    const float* angles;
-    src(r - off, k, v, angles);
-    uint4 u, w;
-    if (vec) {
-      u = *reinterpret_cast<const uint4*>(k + d0);
-      w = *reinterpret_cast<const uint4*>(k + d1);
-    }
-    const uint4 x = *reinterpret_cast<const uint4*>(v + 16 * c);
-    const uint4 y = *reinterpret_cast<const uint4*>(v + 16 * c + 8);
-    if (vec) {
-      split<BF>(u, w, inter || !turned, ka, kb);
-      if (turned) turn8(ka, kb, angles, rot, c);
-    } else {
+__device__ __forceinline__ void write_rows(const Pools& P, Shared& S, int page, int row0, int rows,
+                                           int at, int off, int count, int rot, bool inter,
+                                           long long k_row, long long v_row, const Source& source) {
+  const int tid = int(threadIdx.x), threads = int(blockDim.x);
+  const int per_row = count * P.chunks, at_once = min(rows, max(1, PIECES * threads / per_row));
+  const bool vec = rot % 16 == 0;
+  const size_t first = (size_t(page) * P.LH + row0) * P.page + at;  // the first row's block
+  // where this thread's pieces lie: row of those at once, offset of an entry's dimensions, its
+  // source.  (n / d as n * ceil(2^22 / d) >> 22: right while n * d < 2^22; both are 1024 at most.)
+  const uint32_t by_row = ((1u << 22) + per_row - 1) / per_row;
+  const uint32_t by_chunk = ((1u << 22) + P.chunks - 1) / P.chunks;
+  int row[PIECES], chunk[PIECES], at_dim[PIECES];
+  Entry entry[PIECES];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int pair = 8 * c + e;
-        ka[e] = widen1<BF>(k[first_of(pair, rot, inter)]);
-        kb[e] = widen1<BF>(k[second_of(pair, rot, inter)]);
-        if (pair < rot / 2) turn(ka[e], kb[e], __ldg(angles + pair), __ldg(angles + rot / 2 + pair));
+  for (int u = 0; u < PIECES; ++u) {
+    const int f = tid + u * threads;
+    row[u] = int(uint32_t(f) * by_row >> 22);
+    const int rest = f - row[u] * per_row, e = int(uint32_t(rest) * by_chunk >> 22);
+    chunk[u] = rest - e * P.chunks;
+    at_dim[u] = (off + e) * P.D;
+    if (row[u] < at_once) entry[u] = source(e);
+    else row[u] = MAX_ROWS;  // never used
+  }
+  auto fetch = [&](int r0, int stage) {
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u) {
+      if (r0 + row[u] >= rows) continue;
+      uint4* const to = S.pieces + (stage * PIECES + u) * 4 * threads + tid;
+      const int c = chunk[u];
+      if (vec) {
+        const bool halves = !inter && 8 * c < rot / 2;
+        const uint16_t* const k = entry[u].k + (r0 + row[u]) * k_row + (halves ? 8 : 16) * c;
+        copy_async(to, k);
+        copy_async(to + threads, k + (halves ? rot / 2 : 8));
       }
+      const uint16_t* const v = entry[u].v + (r0 + row[u]) * v_row + 16 * c;
+      copy_async(to + 2 * threads, v);
+      copy_async(to + 3 * threads, v + 8);
     }
-    split<BF>(x, y, true, va, vb);
-  }
-  uint32_t mk = 0, mv = 0;
-  if (mine) {
-    mk = largest(kb, largest(ka, 0));
-    mv = largest(vb, largest(va, 0));
-  }
-  mk = __reduce_max_sync(0xffffffffu, mk);
-  mv = __reduce_max_sync(0xffffffffu, mv);
-  if (lane == 0) {
-    most_of[0][warp] = mk;
-    most_of[1][warp] = mv;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  fetch(0, 0);
+  __syncthreads();  // (the states of the units before these are used up)
+  for (int r = tid; r < rows; r += threads) {
+    RowState x = {0, 0, -1000, -1000};
+    if (off) {
+      const size_t s = (first + size_t(r) * P.page) / P.block;
+      x.own_k = int(P.k_scales[s]) - 127;
+      x.own_v = int(P.v_scales[s]) - 127;
+    }
+    S.state[r] = x;
   }
   __syncthreads();
-  const int warps = int(blockDim.x) >> 5;
-  mk = __reduce_max_sync(0xffffffffu, lane < warps ? most_of[0][lane] : 0);
-  mv = __reduce_max_sync(0xffffffffu, lane < warps ? most_of[1][lane] : 0);
-  __syncthreads();  // (before the next unit's)
-  const int ek = max(exponent_for(__uint_as_float(mk), P.least, P.most), own_k);
-  const int ev = max(exponent_for(__uint_as_float(mv), P.least, P.most), own_v);
-  unsigned char* const kp = P.k_pages + (line + r) * P.D;
-  unsigned char* const vp = P.v_pages + (line + r) * P.D;
-  if (mine) {
-    const float fk = power(-ek), fv = power(-ev);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      ka[e] *= fk;
-      kb[e] *= fk;
-      va[e] *= fv;
-      vb[e] *= fv;
-    }
-    if (vec && turned && !inter) {
-      *reinterpret_cast<uint2*>(kp + d0) =
-          make_uint2(to_bytes(ka[0], ka[1], ka[2], ka[3]), to_bytes(ka[4], ka[5], ka[6], ka[7]));
-      *reinterpret_cast<uint2*>(kp + d1) =
-          make_uint2(to_bytes(kb[0], kb[1], kb[2], kb[3]), to_bytes(kb[4], kb[5], kb[6], kb[7]));
-    } else if (vec) {
-      *reinterpret_cast<uint4*>(kp + 16 * c) =
-          make_uint4(to_bytes(ka[0], kb[0], ka[1], kb[1]), to_bytes(ka[2], kb[2], ka[3], kb[3]),
-                     to_bytes(ka[4], kb[4], ka[5], kb[5]), to_bytes(ka[6], kb[6], ka[7], kb[7]));
+  auto exponent_k = [&](const RowState& x) {
+    return max(exponent_for(__uint_as_float(x.k), P.least, P.most), x.own_k);
+  };
+  auto exponent_v = [&](const RowState& x) {
+    return max(exponent_for(__uint_as_float(x.v), P.least, P.most), x.own_v);
+  };
+  for (int r0 = 0, stage = 0; r0 < rows; r0 += at_once, stage ^= 1) {
+    if (r0 + at_once < rows) {
+      fetch(r0 + at_once, stage ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
     } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    float ka[PIECES][8], kb[PIECES][8];
+    uint4 va[PIECES], vb[PIECES];
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u) {
+      float mk = 0.0f, mv = 0.0f;
+      if (r0 + row[u] < rows) {
+        const uint4* const from = S.pieces + (stage * PIECES + u) * 4 * threads + tid;
+        const int c = chunk[u];
+        const float* const angles = entry[u].angles;
+        if (vec) {
+          const bool turned = 8 * c < rot / 2;
+          split<BF>(from[0], from[threads], inter || !turned, ka[u], kb[u]);
+          if (turned) turn8(ka[u], kb[u], turns(angles, rot, 8 * c, 8 * c + 4));
+        } else {
+          const uint16_t* const k = entry[u].k + (r0 + row[u]) * k_row;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int pair = 8 * c + e;
+            ka[u][e] = widen1<BF>(k[first_of(pair, rot, inter)]);
+            kb[u][e] = widen1<BF>(k[second_of(pair, rot, inter)]);
+            if (pair < rot / 2)
+              turn(ka[u][e], kb[u][e], __ldg(angles + pair), __ldg(angles + rot / 2 + pair));
+          }
+        }
+        mk = largest(kb[u], largest(ka[u], 0.0f));
+        if (!finite(mk)) mk = largest_finite(kb[u], largest_finite(ka[u], 0.0f));
+        va[u] = from[2 * threads];
+        vb[u] = from[3 * threads];
+        mv = largest<BF>(va[u], vb[u]);
+        if (!finite(mv)) {
+          float x[8], y[8];
+          split<BF>(va[u], vb[u], true, x, y);
+          mv = largest_finite(y, largest_finite(x, 0.0f));
+          merge<BF>(x, y, true, va[u], vb[u]);
+        }
+      }
+      if (per_row % 32 == 0) {  // the warp's pieces are of one row
+        const uint32_t a = __reduce_max_sync(0xffffffffu, __float_as_uint(mk));
+        const uint32_t b = __reduce_max_sync(0xffffffffu, __float_as_uint(mv));
+        if (r0 + row[u] < rows && (tid & 31) == 0) {
+          atomicMax(&S.state[r0 + row[u]].k, a);
+          atomicMax(&S.state[r0 + row[u]].v, b);
+        }
+      } else if (r0 + row[u] < rows) {
+        atomicMax(&S.state[r0 + row[u]].k, __float_as_uint(mk));
+        atomicMax(&S.state[r0 + row[u]].v, __float_as_uint(mv));
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u) {
+      if (r0 + row[u] >= rows) continue;
+      const RowState x = S.state[r0 + row[u]];
+      const float fk = power(-exponent_k(x)), fv = power(-exponent_v(x));
+      const size_t to = (first + size_t(r0 + row[u]) * P.page) * P.D + at_dim[u];
+      unsigned char* const kp = P.k_pages + to;
+      const int c = chunk[u];
+      const bool turned = 8 * c < rot / 2;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int pair = 8 * c + e;
-        const uint32_t w = to_bytes(ka[e], kb[e], 0.0f, 0.0f);
-        kp[first_of(pair, rot, inter)] = uint8_t(w);
-        kp[second_of(pair, rot, inter)] = uint8_t(w >> 8);
+        ka[u][e] *= fk;
+        kb[u][e] *= fk;
       }
-    }
-    *reinterpret_cast<uint4*>(vp + 16 * c) =
-        make_uint4(to_bytes(va[0], vb[0], va[1], vb[1]), to_bytes(va[2], vb[2], va[3], vb[3]),
-                   to_bytes(va[4], vb[4], va[5], vb[5]), to_bytes(va[6], vb[6], va[7], vb[7]));
-  } else if (older) {
+      const auto& a = ka[u];
+      const auto& b = kb[u];
+      if (vec && turned && !inter) {
+        *reinterpret_cast<uint2*>(kp + 8 * c) =
+            make_uint2(to_bytes(a[0], a[1], a[2], a[3]), to_bytes(a[4], a[5], a[6], a[7]));
+        *reinterpret_cast<uint2*>(kp + 8 * c + rot / 2) =
+            make_uint2(to_bytes(b[0], b[1], b[2], b[3]), to_bytes(b[4], b[5], b[6], b[7]));
+      } else if (vec) {
+        *reinterpret_cast<uint4*>(kp + 16 * c) =
+            make_uint4(to_bytes(a[0], b[0], a[1], b[1]), to_bytes(a[2], b[2], a[3], b[3]),
+                       to_bytes(a[4], b[4], a[5], b[5]), to_bytes(a[6], b[6], a[7], b[7]));
+      } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int by = i ? own_v - ev : own_k - ek;
-      uint4* const p = reinterpret_cast<uint4*>((i ? vp : kp) + 16 * c);
-      if (by < 0) {
-        const float f = power(by);
-        const uint4 w = *p;
-        *p = make_uint4(again(w.x, f), again(w.y, f), again(w.z, f), again(w.w, f));
+        for (int e = 0; e < 8; ++e) {
+          const int pair = 8 * c + e;
+          const uint32_t w = to_bytes(a[e], b[e], 0.0f, 0.0f);
+          kp[first_of(pair, rot, inter)] = uint8_t(w);
+          kp[second_of(pair, rot, inter)] = uint8_t(w >> 8);
+        }
       }
+      float y[8], z[8];
+      split<BF>(va[u], vb[u], true, y, z);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] *= fv;
+        z[e] *= fv;
+      }
+      *reinterpret_cast<uint4*>(P.v_pages + to + 16 * c) =
+          make_uint4(to_bytes(y[0], z[0], y[1], z[1]), to_bytes(y[2], z[2], y[3], z[3]),
+                     to_bytes(y[4], z[4], y[5], z[5]), to_bytes(y[6], z[6], y[7], z[7]));
     }
   }
-  if (tid == 0) {
-    P.k_scales[scale_at] = uint8_t(ek + 127);
-    P.v_scales[scale_at] = uint8_t(ev + 127);
+  // the rows' scales, and older entries of those whose scale has risen
+  for (int r = tid; r < rows; r += threads) {
+    const RowState x = S.state[r];
+    const size_t s = (first + size_t(r) * P.page) / P.block;
+    P.k_scales[s] = uint8_t(exponent_k(x) + 127);
+    P.v_scales[s] = uint8_t(exponent_v(x) + 127);
+  }
+  const int old = off * P.chunks;
+  for (int f = tid; f < rows * old; f += threads) {
+    const int r = f / old;
+    const RowState x = S.state[r];
+    const size_t to = (first + size_t(r) * P.page) * P.D + size_t(f - r * old) * 16;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int by = i ? x.own_v - exponent_v(x) : x.own_k - exponent_k(x);
+      if (by < 0) {
+        uint4* const p = reinterpret_cast<uint4*>((i ? P.v_pages : P.k_pages) + to);
+        const float g = power(by);
+        const uint4 w = *p;
+        *p = make_uint4(again(w.x, g), again(w.y, g), again(w.z, g), again(w.w, g));
+      }
+    }
   }
 }
 
@@ -203,16 +325,19 @@ struct AppendParams {
   const float* angles;
   long long ks, vs;
   int Hkv, head0, rot;
+  int heads;       // of a CTA
   int tokens;      // per CTA, whose units are those that begin among them
-  int token_ctas;  // CTAs behind them settle the requests (of head 0)
+  int token_ctas;  // CTAs behind them settle the requests (of the first heads)
   bool inter;
 };
 
 template <bool BF>
-__global__ void __launch_bounds__(MAX_UNIT_THREADS) sv_kv8_append(
+__global__ void __launch_bounds__(MAX_THREADS) sv_kv8_append(
     const __grid_constant__ AppendParams R) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  Shared& S = *reinterpret_cast<Shared*>(smem);
   const Appended& A = R.A;
-  const int tid = int(threadIdx.x), h = int(blockIdx.y);
+  const int tid = int(threadIdx.x), h = int(blockIdx.y) * R.heads;
   if (int(blockIdx.x) >= R.token_ctas) {
     const int warps = int(blockDim.x) >> 5;
     const int b = (int(blockIdx.x) - R.token_ctas) * warps + (tid >> 5);
@@ -220,7 +345,6 @@ __global__ void __launch_bounds__(MAX_UNIT_THREADS) sv_kv8_append(
     return;
   }
   const int t0 = int(blockIdx.x) * R.tokens, t1 = min(t0 + R.tokens, A.T);
-  const int r = tid / R.P.chunks;
   for (int t = t0; t < t1;) {
     int b, lo, hi;
     if (!request_of(A, t, b, lo, hi)) {  // no request's row: the next one may be
@@ -249,17 +373,17 @@ __global__ void __launch_bounds__(MAX_UNIT_THREADS) sv_kv8_append(
       ok = !__syncthreads_or(faults_of(A, b, lo, n, len, tid, int(blockDim.x)));
     } else if (A.rows) {
       int p = 0;
-      if (r < count) p = A.positions ? __ldg(A.positions + lo + j + r) : at + r;
+      if (tid < count) p = A.positions ? __ldg(A.positions + lo + j + tid) : at + tid;
       ok = !__syncthreads_or(p < 0 || p >= A.rows) && ok;
     }
     if (!ok) continue;
-    write_unit<BF>(R.P, pg, R.head0 + h, at - off - col * A.page, off, count, R.rot, R.inter,
-                   [&](int i, const uint16_t*& k, const uint16_t*& v, const float*& angles) {
-                     const long long token = lo + j + i;
-                     k = R.k + token * R.ks + (long long)h * R.P.D;
-                     v = R.v + token * R.vs + (long long)h * R.P.D;
-                     const int p = A.rows && A.positions ? __ldg(A.positions + token) : at + i;
-                     angles = R.angles + (long long)(A.rows ? p : 0) * R.rot;
+    const long long token = lo + j;
+    write_rows<BF>(R.P, S, pg, R.head0 + h, min(R.heads, R.Hkv - h), at - off - col * A.page, off, count,
+                   R.rot, R.inter, R.P.D, R.P.D, [&](int e) {
+                     const int p = A.rows && A.positions ? __ldg(A.positions + token + e) : at + e;
+                     return Entry{R.k + (token + e) * R.ks + (long long)h * R.P.D,
+                                  R.v + (token + e) * R.vs + (long long)h * R.P.D,
+                                  R.angles + (long long)(A.rows ? p : 0) * R.rot};
                    });
   }
 }
@@ -277,6 +401,7 @@ struct CommitParams {
   int32_t* out_lens;
   int32_t* status;
   int B, N, num_pages, cols;
+  int rows;  // of a CTA
 };
 
 // The status bits of request b's commit of k + 1 entries at `len`, agreed on by the CTA.
@@ -302,13 +427,15 @@ __device__ __forceinline__ int commit_faults(const CommitParams& R, int b, int k
   return (bad & SV_ST_BAD_LENGTH) | (tok ? SV_ST_BAD_TOKEN : 0) | (pg ? SV_ST_BAD_PAGE : 0);
 }
 
-// Unit blockIdx.y (and every gridDim.y-th from there) of the path of request blockIdx.z, row
-// blockIdx.x.  IN_PLACE: the lengths are updated by the next kernel instead.
+// Block blockIdx.y (and every gridDim.y-th from there) of the path of request blockIdx.z, rows
+// from blockIdx.x * R.rows on.  IN_PLACE: the lengths are updated by the next kernel instead.
 template <bool BF, bool IN_PLACE>
-__global__ void __launch_bounds__(MAX_UNIT_THREADS) sv_kv8_commit(
+__global__ void __launch_bounds__(MAX_THREADS) sv_kv8_commit(
     const __grid_constant__ CommitParams R) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  Shared& S = *reinterpret_cast<Shared*>(smem);
   if (IN_PLACE) allow_next_kernel();
-  const int b = int(blockIdx.z), row = int(blockIdx.x);
+  const int b = int(blockIdx.z), row = int(blockIdx.x) * R.rows;
   const int k = __ldg(R.num_accepted + b), len = __ldg(R.lens + b);
   const int block = R.P.block;
   const bool writer = row == 0 && blockIdx.y == 0;
@@ -326,15 +453,14 @@ __global__ void __launch_bounds__(MAX_UNIT_THREADS) sv_kv8_commit(
     const int j = int(j0), at = len + j, off = at % block;
     const int count = min(block - off, k + 1 - j), col = at / R.P.page;
     const int pg = __ldg(R.table + size_t(b) * R.cols + col);
-    write_unit<BF>(R.P, pg, row, at - off - col * R.P.page, off, count, 0, false,
-                   [&](int i, const uint16_t*& kp, const uint16_t*& vp, const float*& angles) {
+    const long long next = (long long)R.N * R.P.D;
+    write_rows<BF>(R.P, S, pg, row, min(R.rows, R.P.LH - row), at - off - col * R.P.page, off, count, 0,
+                   false, next, next, [&](int i) {
                      const int e = j + i;
                      const int node =
                          R.nodes && e > 0 ? __ldg(R.nodes + size_t(b) * R.N + e - 1) : e;
                      const size_t from = ((size_t(b) * R.P.LH + row) * R.N + node) * R.P.D;
-                     kp = R.k_new + from;
-                     vp = R.v_new + from;
-                     angles = nullptr;
+                     return Entry{R.k_new + from, R.v_new + from, nullptr};
                    });
   }
 }
@@ -367,7 +493,33 @@ void set_pools(Pools& P, int dtype, void* kp, void* vp, void* ks, void* vs, int 
   P.most = dtype == SV_BF16 ? 119 : 7;
   P.chunks = D / 16;
 }
-int unit_threads(const Pools& P) { return (P.block * P.chunks + 31) / 32 * 32; }
+// Threads of a CTA: a row's pieces fit twice, if it is a whole block's.
+int threads_for(const Pools& P) {
+  return P.block * P.chunks <= PIECES * 128 ? 128 : P.block * P.chunks <= PIECES * 256 ? 256 : 512;
+}
+// Rows of a CTA: enough CTAs for eight on every SM, if there is work for them.
+int rows_for(long long units, int rows, int sms) {
+  const long long n = units * rows / (8LL * sms);
+  const int most = rows < MAX_ROWS ? rows : MAX_ROWS;
+  return int(n < 1 ? 1 : n < most ? n : most);
+}
+template <class Params>
+int start(void (*kernel)(Params), dim3 grid, int threads, cudaStream_t st, const Params& R) {
+  const size_t bytes = shared_bytes(threads);
+  if (bytes > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) !=
+          cudaSuccess)
+    return SV_ERR_CUDA;
+  kernel<<<grid, threads, bytes, st>>>(R);
+  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
+}
 
 }  // namespace
 
@@ -396,10 +548,8 @@ int sv_page_append8(int dtype, const void* k, long long k_stride, const void* v,
     return SV_ERR_INVALID_ARG;
   if (out_seq_lens && out_seq_lens < seq_lens + B && seq_lens < out_seq_lens + B)
     return SV_ERR_INVALID_ARG;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
-    return SV_ERR_CUDA;
+  const int sms = sm_count();
+  if (sms < 1) return SV_ERR_CUDA;
   AppendParams R = {};
   R.A = {block_table, seq_lens, cu_seqlens, positions, out_seq_lens, dev_status,
          B, T, cols, page_size, num_pages, table ? rows : 0};
@@ -410,18 +560,17 @@ int sv_page_append8(int dtype, const void* k, long long k_stride, const void* v,
   R.ks = k_stride; R.vs = v_stride;
   R.Hkv = Hkv; R.head0 = head0; R.rot = table ? rot : 0;
   R.inter = interleaved != 0;
-  const int threads = unit_threads(R.P);
+  const int threads = threads_for(R.P);
   // A CTA per token when that is a few CTAs per SM (single tokens: every unit at once), else
   // one per block's worth of tokens (a prompt's CTAs have one unit each).
   R.tokens = (long long)T * Hkv <= 16LL * sms ? 1 : block;
   R.token_ctas = int(((long long)T + R.tokens - 1) / R.tokens);
   const long long grid = R.token_ctas + ((long long)B + threads / 32 - 1) / (threads / 32);
   if (grid > 0x7fffffffLL) return SV_ERR_INVALID_ARG;
-  const dim3 g(static_cast<unsigned>(grid), static_cast<unsigned>(Hkv));
+  R.heads = R.tokens == 1 ? 1 : rows_for(R.token_ctas, Hkv, sms);
+  const dim3 g(static_cast<unsigned>(grid), static_cast<unsigned>((Hkv + R.heads - 1) / R.heads));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == SV_BF16) sv_kv8_append<true><<<g, threads, 0, st>>>(R);
-  else sv_kv8_append<false><<<g, threads, 0, st>>>(R);
-  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return start(dtype == SV_BF16 ? sv_kv8_append<true> : sv_kv8_append<false>, g, threads, st, R);
 }
 
 int sv_page_commit8(int dtype, void* k_pages, void* v_pages, void* k_scales, void* v_scales,
@@ -456,20 +605,22 @@ int sv_page_commit8(int dtype, void* k_pages, void* v_pages, void* k_scales, voi
   R.out_lens = out_seq_lens;
   R.status = dev_status;
   R.B = B; R.N = N; R.num_pages = num_pages; R.cols = cols;
-  const int threads = unit_threads(R.P);
+  const int sms = sm_count();
+  if (sms < 1) return SV_ERR_CUDA;
+  const int threads = threads_for(R.P);
+  R.rows = rows_for(B, LH, sms);
   const int units = (N - 1 + block - 1) / block + 1;  // of a path of N entries, wherever it begins
-  const dim3 g(static_cast<unsigned>(LH), static_cast<unsigned>(units < 64 ? units : 64),
+  const dim3 g(static_cast<unsigned>((LH + R.rows - 1) / R.rows),
+               static_cast<unsigned>(units < 64 ? units : 64),
                static_cast<unsigned>(B));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = dtype == SV_BF16;
   if (!in_place) {
-    if (bf) sv_kv8_commit<true, false><<<g, threads, 0, st>>>(R);
-    else sv_kv8_commit<false, false><<<g, threads, 0, st>>>(R);
-    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+    return start(bf ? sv_kv8_commit<true, false> : sv_kv8_commit<false, false>, g, threads, st, R);
   }
-  if (bf) sv_kv8_commit<true, true><<<g, threads, 0, st>>>(R);
-  else sv_kv8_commit<false, true><<<g, threads, 0, st>>>(R);
-  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  const int rc =
+      start(bf ? sv_kv8_commit<true, true> : sv_kv8_commit<false, true>, g, threads, st, R);
+  if (rc != SV_OK) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(B));
   cfg.blockDim = dim3(128);

@@ -1,10 +1,11 @@
 // rope.cu -- sm_103a kernels and C ABI of rotary positions and of appending to
 // the paged cache (see include/svrope.h for the operations, layouts and errors):
 //
-//   sv_rope_angles  the table: one thread per angle
-//   sv_rope_tokens  packed tokens: each thread turns eight pairs of a head at a
-//                   time and writes them to every place they go (queries' and keys'
-//                   packed outputs, pages), or carries values to their pages
+//   sv_rope_angles  the table: a thread takes one pair's angle at several positions
+//   sv_rope_tokens  packed tokens: a thread takes the same eight pairs of several
+//                   heads of a token, turns them by the same angles and writes them
+//                   to every place they go (queries' and keys' packed outputs,
+//                   pages), or carries values to their pages
 //
 // Both move every byte once and are bound by that, or by their latency.
 
@@ -20,35 +21,54 @@ using namespace svrope;
 constexpr int THREADS = 256;
 constexpr int MAX_ROT = 256;
 constexpr int MAX_TOKENS = 32;   // tokens of a CTA
-constexpr int UNROLL = 2;        // chunks of a thread that are loaded before any is stored
+constexpr int UNROLL = 4;        // chunks of a thread that are loaded before any is stored
 
 // -------------------------------------------------------------- the table
 
 struct AngleParams {
   float* table;
   int half, first, rows;
+  int passes;  // rows of a thread
   float gain;
   uint64_t turn[MAX_ROT / 2];  // the angle of one position, in 2^-64 turns
 };
 
 // Position p's angle is p * turn modulo 2^64: whole turns fall off the integer product
 // without a rounding, however far p is.  (64-bit floats would do, but GB300 has few units
-// for them.)  The upper 32 bits, as a signed part of a turn, are split into a 32-bit float
-// and a rest d, and the functions at the float are moved on by the rest:
-// cos(x + d) = cos x - d sin x to within d^2 / 2 < 2^-47.
+// for them.)  Its upper 32 bits are split into the nearest quarter turn and a rest x of at
+// most pi / 4 to either side, where the Taylor polynomials of sine (to x^9) and cosine (to
+// x^10) are off by less than 2^-29; the roundings of x and of the sums add up to 2^-23.
+// What bounds it is the instructions, some 40 per angle, until the table outgrows L2.
+// (131072 positions of 64 pairs: 67 us with a division per angle and sincospif, whose
+// reduction has nothing left to do here.)
 __global__ void __launch_bounds__(THREADS) sv_rope_angles(const __grid_constant__ AngleParams R) {
-  const long long total = (long long)R.rows * R.half;
-  const long long stride = (long long)gridDim.x * THREADS;
-  for (long long f = (long long)blockIdx.x * THREADS + threadIdx.x; f < total; f += stride) {
-    const int p = int(f / R.half), i = int(f - (long long)p * R.half);
-    const int h = int(uint64_t(uint32_t(R.first + p)) * R.turn[i] >> 32);
-    const float x = __int2float_rn(h);
-    const float d = float((long long)h - (long long)x) * 1.46291807926715968e-9f;  // 2 pi / 2^32
-    float s, c;
-    sincospif(x * 0x1p-31f, &s, &c);
-    float* const row = R.table + size_t(p) * 2 * R.half;
-    row[i] = fmaf(-s, d, c) * R.gain;
-    row[R.half + i] = fmaf(c, d, s) * R.gain;
+  const int at_once = THREADS / R.half, r = int(threadIdx.x) / R.half;
+  const int i = int(threadIdx.x) - r * R.half;
+  if (r >= at_once) return;
+  const long long p0 = (long long)blockIdx.x * R.passes * at_once + r;
+  const uint64_t turn = R.turn[i], step = turn * unsigned(at_once);
+  uint64_t angle = turn * uint64_t(R.first + p0);
+  float* out = R.table + size_t(p0) * 2 * R.half + i;
+  for (int n = 0; n < R.passes && p0 + n * at_once < R.rows; ++n) {
+    const uint32_t h = uint32_t(angle >> 32), quarter = h + 0x20000000u;
+    const float x = float(int(h - (quarter & 0xc0000000u))) * 1.46291807926715968e-9f;  // 2 pi / 2^32
+    const float y = x * x;
+    float s = fmaf(y, 1.0f / 362880, -1.0f / 5040);
+    s = fmaf(y, s, 1.0f / 120);
+    s = fmaf(y, s, -1.0f / 6);
+    s = fmaf(x * y, s, x);
+    float c = fmaf(y, -1.0f / 3628800, 1.0f / 40320);
+    c = fmaf(y, c, -1.0f / 720);
+    c = fmaf(y, c, 1.0f / 24);
+    c = fmaf(y, c, -0.5f);
+    c = fmaf(y, c, 1.0f);
+    // a quarter turn more: (c, s) becomes (-s, c)
+    const bool odd = quarter & 0x40000000u, low = quarter & 0x80000000u;
+    const float u = odd ? s : c, v = odd ? c : s;
+    out[0] = (odd != low ? -u : u) * R.gain;
+    out[R.half] = (low ? -v : v) * R.gain;
+    angle += step;
+    out += size_t(at_once) * 2 * R.half;
   }
 }
 
@@ -69,26 +89,17 @@ struct TokenParams {
   int tokens;      // per CTA
   int token_ctas;  // the CTAs behind them settle the requests
   int chunks;      // of a head
-  unsigned long long m_chunks, m_heads;
+  int lanes;       // the heads of a token that are taken at once
   bool inter, pages;
 };
 
-// n / d as n * ceil(2^40 / d) >> 40: right while n * d < 2^40 (n < 2^22 and d < 2^18 here).
-unsigned long long div_magic(int d) { return ((1ull << 40) + unsigned(d) - 1) / unsigned(d); }
-__device__ __forceinline__ int div_by(int n, unsigned long long m) {
-  return int((unsigned long long)(unsigned)n * m >> 40);
-}
-
-struct Chunk {
-  uint4 u, v;
-  const uint16_t* src;
-  uint16_t* dst[2];
-  int c, pos;
-  bool on, rotates, turned;  // its row is rotated, and this chunk of it
-};
-
-// VEC: the rotated part is a multiple of 16 dimensions, and a chunk two 16-byte vectors;
-// otherwise a chunk's values are moved one by one.
+// A chunk is sixteen dimensions of a head, two vectors of eight: eight pairs that are turned,
+// or what is not.  VEC: the rotated part is a multiple of 16 dimensions, and a chunk two 16-byte
+// vectors half the head (or half the part) apart, so that neighbouring threads' vectors are
+// neighbours; otherwise a chunk's values are moved one by one.
+//
+// The first heads are loaded before it is known where they go: bounds, length, page and angles
+// are a chain of four loads, the latency of a decoding step.
 template <bool BF, bool VEC>
 __global__ void __launch_bounds__(THREADS) sv_rope_tokens(const __grid_constant__ TokenParams R) {
   __shared__ int pos_of[MAX_TOKENS];          // where a token is rotated to; -1: left out
@@ -100,115 +111,141 @@ __global__ void __launch_bounds__(THREADS) sv_rope_tokens(const __grid_constant_
     return;
   }
   const int t0 = int(blockIdx.x) * R.tokens, count = min(R.tokens, R.A.T - t0);
-  for (int i = warp; i < count; i += THREADS / 32) {
-    int pos = -1;
-    long long where = 0;
-    if (R.pages) {
-      int b, lo, hi;
-      if (request_of(R.A, t0 + i, b, lo, hi)) {
-        const int len = __ldg(R.A.lens + b);
-        if (fits(R.A, len, t0 + i - lo + 1)) {
-          const int at = len + (t0 + i - lo), col = at / R.A.page;
-          const int pg = __ldg(R.A.table + size_t(b) * R.A.cols + col);
-          const int p = R.A.rows && R.A.positions ? __ldg(R.A.positions + t0 + i) : at;
+  const int slot = tid / R.chunks, c = tid - slot * R.chunks;
+  const int i = slot / R.lanes, h0 = slot - i * R.lanes;
+  const int keys = R.Hq, values = R.Hq + R.Hk, heads = values + R.Hv;
+  const bool active = i < count;
+  const long long t = t0 + i;
+  bool turned = 8 * c < R.rot / 2;  // (half layout)
+  int a, b;                         // where the vectors lie in a head
+  if (turned && !R.inter) {
+    a = 8 * c;
+    b = a + R.rot / 2;
+  } else {
+    const int skip = R.inter ? 0 : R.rot, vectors = (R.D - skip) / 8;
+    a = 8 * c + skip / 2;
+    b = a + (vectors + 1) / 2 * 8;
+  }
+  const bool second = b < R.D, turned_b = !R.inter || b < R.rot;
+  if (R.inter) turned = a < R.rot;
+  uint4 u[UNROLL], v[UNROLL];
+  auto source = [&](int h) {
+    return h < keys ? R.q + t * R.qs + (long long)h * R.D
+           : h < values ? R.k + t * R.ks + (long long)(h - keys) * R.D
+                        : R.v + t * R.vs + (long long)(h - values) * R.D;
+  };
+  auto load = [&](int first) {
+#pragma unroll
+    for (int n = 0; n < UNROLL; ++n) {
+      const int h = first + n * R.lanes;
+      if (h < heads) {
+        const uint16_t* const src = source(h);
+        u[n] = *reinterpret_cast<const uint4*>(src + a);
+        v[n] = second ? *reinterpret_cast<const uint4*>(src + b) : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  if (VEC && active) load(h0);
+  int pos = -1;
+  long long where = 0;
+  if (R.pages) {
+    for (int j = warp; j < count; j += THREADS / 32) {
+      int r, lo, hi, to = -1;
+      long long row = 0;
+      if (request_of(R.A, t0 + j, r, lo, hi)) {
+        const int len = __ldg(R.A.lens + r);
+        if (fits(R.A, len, t0 + j - lo + 1)) {
+          const int at = len + (t0 + j - lo), col = at / R.A.page;
+          const int pg = __ldg(R.A.table + size_t(r) * R.A.cols + col);
+          const int p = R.A.rows && R.A.positions ? __ldg(R.A.positions + t0 + j) : at;
           if (pg >= 0 && pg < R.A.num_pages && p >= 0 && (!R.A.rows || p < R.A.rows)) {
-            pos = p;
-            where = (long long)pg * R.LH * R.A.page + (at - col * R.A.page);
+            to = p;
+            row = (long long)pg * R.LH * R.A.page + (at - col * R.A.page);
           }
         }
       }
-    } else {
-      const int p = __ldg(R.A.positions + t0 + i);
-      if (p >= 0 && p < R.A.rows) pos = p;
-      else if (lane == 0) set_status(R.A.status, SV_ST_BAD_LENGTH);
+      if (lane == 0) {
+        pos_of[j] = to;
+        page_of[j] = row;
+      }
     }
-    if (lane == 0) {
-      pos_of[i] = pos;
-      page_of[i] = where;
+    __syncthreads();
+    if (active) {
+      pos = pos_of[i];
+      where = page_of[i];
+    }
+  } else if (active) {
+    pos = __ldg(R.A.positions + t);
+    if (pos < 0 || pos >= R.A.rows) {
+      pos = -1;
+      if (c == 0 && h0 == 0) set_status(R.A.status, SV_ST_BAD_LENGTH);
     }
   }
-  __syncthreads();
-  const int heads = R.Hq + R.Hk + R.Hv, total = count * heads * R.chunks;
-  for (int f0 = tid; f0 < total; f0 += THREADS * UNROLL) {
-    Chunk x[UNROLL];
+  if (pos < 0) return;
+  const float* const angles = R.angles + (long long)pos * R.rot;
+  Turns w = {};
+  if (VEC && turned)
+    w = turns(angles, R.rot, R.inter ? a / 2 : a, !R.inter ? a + 4 : turned_b ? b / 2 : a / 2);
+  for (int first = h0; first < heads;) {
 #pragma unroll
     for (int n = 0; n < UNROLL; ++n) {
-      Chunk& k = x[n];
-      const int f = f0 + n * THREADS;
-      const int row = div_by(f, R.m_chunks), i = div_by(row, R.m_heads);
-      int h = row - i * heads;
-      k.c = f - row * R.chunks;
-      k.on = f < total;
-      k.pos = k.on ? pos_of[i] : -1;
-      k.on = k.pos >= 0;
-      k.dst[0] = k.dst[1] = nullptr;
-      k.rotates = true;
-      if (!k.on) continue;
-      const long long t = t0 + i;
-      if (h < R.Hq) {
-        k.src = R.q + t * R.qs + (long long)h * R.D;
-        k.dst[0] = R.q_out + t * R.qos + (long long)h * R.D;
+      const int h = first + n * R.lanes;
+      if (h >= heads) break;
+      uint16_t *packed = nullptr, *paged = nullptr;
+      if (h < keys) {
+        packed = R.q_out + t * R.qos + (long long)h * R.D;
       } else {
-        h -= R.Hq;
-        const bool is_v = h >= R.Hk;
-        if (is_v) h -= R.Hk;
-        k.src = is_v ? R.v + t * R.vs + (long long)h * R.D : R.k + t * R.ks + (long long)h * R.D;
-        k.rotates = !is_v;
-        if (!is_v && R.k_out) k.dst[0] = R.k_out + t * R.kos + (long long)h * R.D;
+        const bool is_v = h >= values;
+        const int g = h - (is_v ? values : keys);
+        if (!is_v && R.k_out) packed = R.k_out + t * R.kos + (long long)g * R.D;
         if (R.pages)
-          k.dst[1] = (is_v ? R.v_pages : R.k_pages) +
-                     (page_of[i] + (long long)(R.head0 + h) * R.A.page) * R.D;
+          paged = (is_v ? R.v_pages : R.k_pages) +
+                  (where + (long long)(R.head0 + g) * R.A.page) * R.D;
       }
-      k.turned = k.rotates && 8 * k.c < R.rot / 2;
       if (VEC) {
-        const int a = k.turned && !R.inter ? 8 * k.c : 16 * k.c;
-        const int b = k.turned && !R.inter ? a + R.rot / 2 : a + 8;
-        k.u = *reinterpret_cast<const uint4*>(k.src + a);
-        k.v = b < R.D ? *reinterpret_cast<const uint4*>(k.src + b) : make_uint4(0, 0, 0, 0);
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < UNROLL; ++n) {
-      Chunk& k = x[n];
-      if (!k.on) continue;
-      const float* const angles = R.angles + (long long)k.pos * R.rot;
-      if (VEC) {
-        if (k.turned) {
-          float a[8], b[8];
-          split<BF>(k.u, k.v, R.inter, a, b);
-          turn8(a, b, angles, R.rot, k.c);
-          merge<BF>(a, b, R.inter, k.u, k.v);
+        if (turned && h < values) {
+          float x[8], y[8];
+          const uint4 rest = v[n];
+          split<BF>(u[n], v[n], R.inter, x, y);
+          turn8(x, y, w);
+          merge<BF>(x, y, R.inter, u[n], v[n]);
+          if (!turned_b) v[n] = rest;
         }
-        const int a = k.turned && !R.inter ? 8 * k.c : 16 * k.c;
-        const int b = k.turned && !R.inter ? a + R.rot / 2 : a + 8;
-#pragma unroll
-        for (int d = 0; d < 2; ++d)
-          if (k.dst[d]) {
-            *reinterpret_cast<uint4*>(k.dst[d] + a) = k.u;
-            if (b < R.D) *reinterpret_cast<uint4*>(k.dst[d] + b) = k.v;
-          }
+        if (packed) {
+          *reinterpret_cast<uint4*>(packed + a) = u[n];
+          if (second) *reinterpret_cast<uint4*>(packed + b) = v[n];
+        }
+        if (paged) {
+          *reinterpret_cast<uint4*>(paged + a) = u[n];
+          if (second) *reinterpret_cast<uint4*>(paged + b) = v[n];
+        }
       } else {
+        const uint16_t* const src = source(h);
         for (int e = 0; e < 8; ++e) {
-          const int pair = 8 * k.c + e;
+          const int pair = 8 * c + e;
           if (pair >= R.D / 2) break;
-          const int a = first_of(pair, R.rot, R.inter), b = second_of(pair, R.rot, R.inter);
-          uint16_t u = k.src[a], v = k.src[b];
-          if (k.rotates && pair < R.rot / 2) {
-            float y = widen1<BF>(u), z = widen1<BF>(v);
-            turn(y, z, __ldg(angles + pair), __ldg(angles + R.rot / 2 + pair));
-            const uint32_t w = narrow<BF>(y, z);
-            u = uint16_t(w);
-            v = uint16_t(w >> 16);
+          const int d0 = first_of(pair, R.rot, R.inter), d1 = second_of(pair, R.rot, R.inter);
+          uint16_t x = src[d0], y = src[d1];
+          if (h < values && pair < R.rot / 2) {
+            float f = widen1<BF>(x), g = widen1<BF>(y);
+            turn(f, g, __ldg(angles + pair), __ldg(angles + R.rot / 2 + pair));
+            const uint32_t z = narrow<BF>(f, g);
+            x = uint16_t(z);
+            y = uint16_t(z >> 16);
           }
-#pragma unroll
-          for (int d = 0; d < 2; ++d)
-            if (k.dst[d]) {
-              k.dst[d][a] = u;
-              k.dst[d][b] = v;
-            }
+          if (packed) {
+            packed[d0] = x;
+            packed[d1] = y;
+          }
+          if (paged) {
+            paged[d0] = x;
+            paged[d1] = y;
+          }
         }
       }
     }
+    first += UNROLL * R.lanes;
+    if (VEC && first < heads) load(first);
   }
 }
 
@@ -224,13 +261,13 @@ int run_tokens(TokenParams& R, int dtype, void* stream) {
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     return SV_ERR_CUDA;
   R.chunks = (R.D + 15) / 16;
-  const int heads = R.Hq + R.Hk + R.Hv, per_token = heads * R.chunks;
-  R.m_chunks = div_magic(R.chunks);
-  R.m_heads = div_magic(heads);
-  // Two rounds of two chunks per thread, as long as that leaves every SM two CTAs.
-  int tokens = 4 * THREADS / per_token;
+  const int heads = R.Hq + R.Hk + R.Hv, slots = THREADS / R.chunks;
+  // Four heads per thread, as long as that leaves every SM two CTAs.
+  int tokens = UNROLL * slots / heads;
   tokens = tokens < R.A.T / (2 * sms) ? tokens : R.A.T / (2 * sms);
+  tokens = tokens < slots ? tokens : slots;
   R.tokens = tokens < 1 ? 1 : tokens > MAX_TOKENS ? MAX_TOKENS : tokens;
+  R.lanes = slots / R.tokens;
   R.token_ctas = (R.A.T + R.tokens - 1) / R.tokens;
   const long long grid =
       R.token_ctas + (R.pages ? (R.A.B + THREADS / 32 - 1) / (THREADS / 32) : 0);
@@ -290,10 +327,11 @@ int sv_rope_table(int scaling, double base, double factor, int original, double 
     const double turns = w / TWO_PI;  // whole turns of one position leave nothing behind
     R.turn[i] = uint64_t(ldexp(turns - floor(turns), 63)) << 1;
   }
-  const long long total = (long long)rows * R.half, most = 1 << 20;
-  const long long grid = (total + THREADS - 1) / THREADS;
-  sv_rope_angles<<<unsigned(grid < most ? grid : most), THREADS, 0,
-                   static_cast<cudaStream_t>(stream)>>>(R);
+  // Sixteen rows per thread, as long as that leaves some CTAs for every SM.
+  const int at_once = THREADS / R.half, passes = rows / at_once / 1024;
+  R.passes = passes < 1 ? 1 : passes > 16 ? 16 : passes;
+  const long long per_cta = (long long)at_once * R.passes, grid = (rows + per_cta - 1) / per_cta;
+  sv_rope_angles<<<unsigned(grid), THREADS, 0, static_cast<cudaStream_t>(stream)>>>(R);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 

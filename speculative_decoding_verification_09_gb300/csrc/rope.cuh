@@ -89,20 +89,26 @@ __device__ __forceinline__ void merge(const float (&a)[8], const float (&b)[8], 
   u = make_uint4(x[0], x[1], x[2], x[3]);
   v = make_uint4(y[0], y[1], y[2], y[3]);
 }
-// Pairs 8 c .. 8 c + 7 turned by a table row (cosines, then sines; 16-byte aligned there).
-__device__ __forceinline__ void turn8(float (&a)[8], float (&b)[8], const float* row, int rot,
-                                      int c) {
-  const float4* const cs = reinterpret_cast<const float4*>(row + 8 * c);
-  const float4* const sn = reinterpret_cast<const float4*>(row + rot / 2 + 8 * c);
-  const float4 c0 = __ldg(cs), c1 = __ldg(cs + 1), s0 = __ldg(sn), s1 = __ldg(sn + 1);
-  turn(a[0], b[0], c0.x, s0.x);
-  turn(a[1], b[1], c0.y, s0.y);
-  turn(a[2], b[2], c0.z, s0.z);
-  turn(a[3], b[3], c0.w, s0.w);
-  turn(a[4], b[4], c1.x, s1.x);
-  turn(a[5], b[5], c1.y, s1.y);
-  turn(a[6], b[6], c1.z, s1.z);
-  turn(a[7], b[7], c1.w, s1.w);
+// Eight pairs turned by their cosines and sines.
+struct Turns { float4 c0, c1, s0, s1; };
+__device__ __forceinline__ void turn8(float (&a)[8], float (&b)[8], const Turns& w) {
+  turn(a[0], b[0], w.c0.x, w.s0.x);
+  turn(a[1], b[1], w.c0.y, w.s0.y);
+  turn(a[2], b[2], w.c0.z, w.s0.z);
+  turn(a[3], b[3], w.c0.w, w.s0.w);
+  turn(a[4], b[4], w.c1.x, w.s1.x);
+  turn(a[5], b[5], w.c1.y, w.s1.y);
+  turn(a[6], b[6], w.c1.z, w.s1.z);
+  turn(a[7], b[7], w.c1.w, w.s1.w);
+}
+// Those of pairs p .. p + 3 and q .. q + 3 in a table's row (cosines, then sines; 16-byte
+// aligned there).
+__device__ __forceinline__ Turns turns(const float* row, int rot, int p, int q) {
+  const float* const s = row + rot / 2;
+  return {__ldg(reinterpret_cast<const float4*>(row + p)),
+          __ldg(reinterpret_cast<const float4*>(row + q)),
+          __ldg(reinterpret_cast<const float4*>(s + p)),
+          __ldg(reinterpret_cast<const float4*>(s + q))};
 }
 
 // The packed tokens of an append and where they go.
