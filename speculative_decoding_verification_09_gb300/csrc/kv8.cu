@@ -13,7 +13,8 @@
 // (a block's older entries only when its scale rises); what bounds it is HBM and the
 // instructions for prompts, and for single tokens and short paths the latency of the loads
 // that depend on one another: bounds, length, page, entries.  (64 paths of 3 entries, 384 rows:
-// 101 us with a CTA per unit, most of whose threads had no entry.)
+// 26 us; 101 with a CTA per unit, most of whose threads had no entry.  32 ragged prompts of 8
+// heads, 80,000 tokens: 116 us, 4.6 TB/s; the state's registers leave an SM sixteen warps.)
 
 #include "rope.cuh"
 #include "svkv8.h"
@@ -119,6 +120,13 @@ struct Shared {
 };
 size_t shared_bytes(int threads) { return sizeof(Shared) + size_t(2 * PIECES * 4) * threads * 16; }
 
+__device__ __forceinline__ int exponent_k(const Pools& P, const RowState& x) {
+  return max(exponent_for(__uint_as_float(x.k), P.least, P.most), x.own_k);
+}
+__device__ __forceinline__ int exponent_v(const Pools& P, const RowState& x) {
+  return max(exponent_for(__uint_as_float(x.v), P.least, P.most), x.own_v);
+}
+
 // Entry `e` of a unit: its key and value in the first row, and the row of angles (or null).
 struct Entry {
   const uint16_t *k, *v;
@@ -128,13 +136,12 @@ struct Entry {
 // The units of rows row0 .. row0 + rows - 1 of LH for the block of `page` (a valid one) that
 // begins at its row `at`: new entries in its rows off .. off + count - 1.  source(e): entry e;
 // the next row's lies k_row, v_row elements behind.
-template <bool BF, class Source>
+template <bool BF, bool VEC, class Source>
 __device__ __forceinline__ void write_rows(const Pools& P, Shared& S, int page, int row0, int rows,
                                            int at, int off, int count, int rot, bool inter,
                                            long long k_row, long long v_row, const Source& source) {
   const int tid = int(threadIdx.x), threads = int(blockDim.x);
   const int per_row = count * P.chunks, at_once = min(rows, max(1, PIECES * threads / per_row));
-  const bool vec = rot % 16 == 0;
   const size_t first = (size_t(page) * P.LH + row0) * P.page + at;  // the first row's block
   // where this thread's pieces lie: row of those at once, offset of an entry's dimensions, its
   // source.  (n / d as n * ceil(2^22 / d) >> 22: right while n * d < 2^22; both are 1024 at most.)
@@ -158,7 +165,7 @@ __device__ __forceinline__ void write_rows(const Pools& P, Shared& S, int page, 
       if (r0 + row[u] >= rows) continue;
       uint4* const to = S.pieces + (stage * PIECES + u) * 4 * threads + tid;
       const int c = chunk[u];
-      if (vec) {
+      if (VEC) {
         const bool halves = !inter && 8 * c < rot / 2;
         const uint16_t* const k = entry[u].k + (r0 + row[u]) * k_row + (halves ? 8 : 16) * c;
         copy_async(to, k);
@@ -182,12 +189,6 @@ __device__ __forceinline__ void write_rows(const Pools& P, Shared& S, int page, 
     S.state[r] = x;
   }
   __syncthreads();
-  auto exponent_k = [&](const RowState& x) {
-    return max(exponent_for(__uint_as_float(x.k), P.least, P.most), x.own_k);
-  };
-  auto exponent_v = [&](const RowState& x) {
-    return max(exponent_for(__uint_as_float(x.v), P.least, P.most), x.own_v);
-  };
   for (int r0 = 0, stage = 0; r0 < rows; r0 += at_once, stage ^= 1) {
     if (r0 + at_once < rows) {
       fetch(r0 + at_once, stage ^ 1);
@@ -196,15 +197,14 @@ __device__ __forceinline__ void write_rows(const Pools& P, Shared& S, int page, 
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     float ka[PIECES][8], kb[PIECES][8];
-    uint4 va[PIECES], vb[PIECES];
 #pragma unroll
     for (int u = 0; u < PIECES; ++u) {
       float mk = 0.0f, mv = 0.0f;
       if (r0 + row[u] < rows) {
-        const uint4* const from = S.pieces + (stage * PIECES + u) * 4 * threads + tid;
+        uint4* const from = S.pieces + (stage * PIECES + u) * 4 * threads + tid;
         const int c = chunk[u];
         const float* const angles = entry[u].angles;
-        if (vec) {
+        if (VEC) {
           const bool turned = 8 * c < rot / 2;
           split<BF>(from[0], from[threads], inter || !turned, ka[u], kb[u]);
           if (turned) turn8(ka[u], kb[u], turns(angles, rot, 8 * c, 8 * c + 4));
@@ -221,14 +221,13 @@ __device__ __forceinline__ void write_rows(const Pools& P, Shared& S, int page, 
         }
         mk = largest(kb[u], largest(ka[u], 0.0f));
         if (!finite(mk)) mk = largest_finite(kb[u], largest_finite(ka[u], 0.0f));
-        va[u] = from[2 * threads];
-        vb[u] = from[3 * threads];
-        mv = largest<BF>(va[u], vb[u]);
+        const uint4 va = from[2 * threads], vb = from[3 * threads];
+        mv = largest<BF>(va, vb);
         if (!finite(mv)) {
           float x[8], y[8];
-          split<BF>(va[u], vb[u], true, x, y);
+          split<BF>(va, vb, true, x, y);
           mv = largest_finite(y, largest_finite(x, 0.0f));
-          merge<BF>(x, y, true, va[u], vb[u]);
+          merge<BF>(x, y, true, from[2 * threads], from[3 * threads]);
         }
       }
       if (per_row % 32 == 0) {  // the warp's pieces are of one row
@@ -248,7 +247,7 @@ __device__ __forceinline__ void write_rows(const Pools& P, Shared& S, int page, 
     for (int u = 0; u < PIECES; ++u) {
       if (r0 + row[u] >= rows) continue;
       const RowState x = S.state[r0 + row[u]];
-      const float fk = power(-exponent_k(x)), fv = power(-exponent_v(x));
+      const float fk = power(-exponent_k(P, x)), fv = power(-exponent_v(P, x));
       const size_t to = (first + size_t(r0 + row[u]) * P.page) * P.D + at_dim[u];
       unsigned char* const kp = P.k_pages + to;
       const int c = chunk[u];
@@ -260,12 +259,12 @@ __device__ __forceinline__ void write_rows(const Pools& P, Shared& S, int page, 
       }
       const auto& a = ka[u];
       const auto& b = kb[u];
-      if (vec && turned && !inter) {
+      if (VEC && turned && !inter) {
         *reinterpret_cast<uint2*>(kp + 8 * c) =
             make_uint2(to_bytes(a[0], a[1], a[2], a[3]), to_bytes(a[4], a[5], a[6], a[7]));
         *reinterpret_cast<uint2*>(kp + 8 * c + rot / 2) =
             make_uint2(to_bytes(b[0], b[1], b[2], b[3]), to_bytes(b[4], b[5], b[6], b[7]));
-      } else if (vec) {
+      } else if (VEC) {
         *reinterpret_cast<uint4*>(kp + 16 * c) =
             make_uint4(to_bytes(a[0], b[0], a[1], b[1]), to_bytes(a[2], b[2], a[3], b[3]),
                        to_bytes(a[4], b[4], a[5], b[5]), to_bytes(a[6], b[6], a[7], b[7]));
@@ -279,7 +278,8 @@ __device__ __forceinline__ void write_rows(const Pools& P, Shared& S, int page, 
         }
       }
       float y[8], z[8];
-      split<BF>(va[u], vb[u], true, y, z);
+      const uint4* const from = S.pieces + (stage * PIECES + u) * 4 * threads + tid;
+      split<BF>(from[2 * threads], from[3 * threads], true, y, z);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         y[e] *= fv;
@@ -294,23 +294,22 @@ __device__ __forceinline__ void write_rows(const Pools& P, Shared& S, int page, 
   for (int r = tid; r < rows; r += threads) {
     const RowState x = S.state[r];
     const size_t s = (first + size_t(r) * P.page) / P.block;
-    P.k_scales[s] = uint8_t(exponent_k(x) + 127);
-    P.v_scales[s] = uint8_t(exponent_v(x) + 127);
+    P.k_scales[s] = uint8_t(exponent_k(P, x) + 127);
+    P.v_scales[s] = uint8_t(exponent_v(P, x) + 127);
   }
-  const int old = off * P.chunks;
-  for (int f = tid; f < rows * old; f += threads) {
-    const int r = f / old;
+  for (int r = tid >> 5; off && r < rows; r += threads >> 5) {
     const RowState x = S.state[r];
-    const size_t to = (first + size_t(r) * P.page) * P.D + size_t(f - r * old) * 16;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int by = i ? x.own_v - exponent_v(x) : x.own_k - exponent_k(x);
-      if (by < 0) {
-        uint4* const p = reinterpret_cast<uint4*>((i ? P.v_pages : P.k_pages) + to);
-        const float g = power(by);
-        const uint4 w = *p;
-        *p = make_uint4(again(w.x, g), again(w.y, g), again(w.z, g), again(w.w, g));
-      }
+    const int k_by = x.own_k - exponent_k(P, x), v_by = x.own_v - exponent_v(P, x);
+    const size_t to = (first + size_t(r) * P.page) * P.D;
+    for (int f = tid & 31; (k_by | v_by) && f < off * P.chunks; f += 32) {
+      uint4* const k = reinterpret_cast<uint4*>(P.k_pages + to) + f;
+      uint4* const v = reinterpret_cast<uint4*>(P.v_pages + to) + f;
+      uint4 a, b;
+      if (k_by) a = *k;
+      if (v_by) b = *v;
+      const float g = power(k_by), h = power(v_by);
+      if (k_by) *k = make_uint4(again(a.x, g), again(a.y, g), again(a.z, g), again(a.w, g));
+      if (v_by) *v = make_uint4(again(b.x, h), again(b.y, h), again(b.z, h), again(b.w, h));
     }
   }
 }
@@ -331,7 +330,7 @@ struct AppendParams {
   bool inter;
 };
 
-template <bool BF>
+template <bool BF, bool VEC>
 __global__ void __launch_bounds__(MAX_THREADS) sv_kv8_append(
     const __grid_constant__ AppendParams R) {
   extern __shared__ __align__(16) unsigned char smem[];
@@ -378,7 +377,7 @@ __global__ void __launch_bounds__(MAX_THREADS) sv_kv8_append(
     }
     if (!ok) continue;
     const long long token = lo + j;
-    write_rows<BF>(R.P, S, pg, R.head0 + h, min(R.heads, R.Hkv - h), at - off - col * A.page, off, count,
+    write_rows<BF, VEC>(R.P, S, pg, R.head0 + h, min(R.heads, R.Hkv - h), at - off - col * A.page, off, count,
                    R.rot, R.inter, R.P.D, R.P.D, [&](int e) {
                      const int p = A.rows && A.positions ? __ldg(A.positions + token + e) : at + e;
                      return Entry{R.k + (token + e) * R.ks + (long long)h * R.P.D,
@@ -454,7 +453,7 @@ __global__ void __launch_bounds__(MAX_THREADS) sv_kv8_commit(
     const int count = min(block - off, k + 1 - j), col = at / R.P.page;
     const int pg = __ldg(R.table + size_t(b) * R.cols + col);
     const long long next = (long long)R.N * R.P.D;
-    write_rows<BF>(R.P, S, pg, row, min(R.rows, R.P.LH - row), at - off - col * R.P.page, off, count, 0,
+    write_rows<BF, true>(R.P, S, pg, row, min(R.rows, R.P.LH - row), at - off - col * R.P.page, off, count, 0,
                    false, next, next, [&](int i) {
                      const int e = j + i;
                      const int node =
@@ -570,7 +569,10 @@ int sv_page_append8(int dtype, const void* k, long long k_stride, const void* v,
   R.heads = R.tokens == 1 ? 1 : rows_for(R.token_ctas, Hkv, sms);
   const dim3 g(static_cast<unsigned>(grid), static_cast<unsigned>((Hkv + R.heads - 1) / R.heads));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return start(dtype == SV_BF16 ? sv_kv8_append<true> : sv_kv8_append<false>, g, threads, st, R);
+  const bool bf = dtype == SV_BF16;
+  return start(R.rot % 16 == 0 ? (bf ? sv_kv8_append<true, true> : sv_kv8_append<false, true>)
+                               : (bf ? sv_kv8_append<true, false> : sv_kv8_append<false, false>),
+               g, threads, st, R);
 }
 
 int sv_page_commit8(int dtype, void* k_pages, void* v_pages, void* k_scales, void* v_scales,
@@ -610,9 +612,12 @@ int sv_page_commit8(int dtype, void* k_pages, void* v_pages, void* k_scales, voi
   const int threads = threads_for(R.P);
   R.rows = rows_for(B, LH, sms);
   const int units = (N - 1 + block - 1) / block + 1;  // of a path of N entries, wherever it begins
+  // A path's units one after another, unless there are too few CTAs otherwise: most paths have
+  // one or two, whatever N, and the CTAs that find none cost 1 us of 30 (64 paths of 3 entries out
+  // of 22 nodes, 384 rows).
+  const long long ctas = (long long)B * ((LH + R.rows - 1) / R.rows), y = 8LL * sms / ctas;
   const dim3 g(static_cast<unsigned>((LH + R.rows - 1) / R.rows),
-               static_cast<unsigned>(units < 64 ? units : 64),
-               static_cast<unsigned>(B));
+               static_cast<unsigned>(y < 1 ? 1 : y < units ? y : units), static_cast<unsigned>(B));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = dtype == SV_BF16;
   if (!in_place) {

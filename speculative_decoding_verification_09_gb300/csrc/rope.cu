@@ -21,7 +21,7 @@ using namespace svrope;
 constexpr int THREADS = 256;
 constexpr int MAX_ROT = 256;
 constexpr int MAX_TOKENS = 32;   // tokens of a CTA
-constexpr int UNROLL = 4;        // chunks of a thread that are loaded before any is stored
+constexpr int UNROLL = 2;        // chunks of a thread that are loaded before any is stored
 
 // -------------------------------------------------------------- the table
 
@@ -262,8 +262,9 @@ int run_tokens(TokenParams& R, int dtype, void* stream) {
     return SV_ERR_CUDA;
   R.chunks = (R.D + 15) / 16;
   const int heads = R.Hq + R.Hk + R.Hv, slots = THREADS / R.chunks;
-  // Four heads per thread, as long as that leaves every SM two CTAs.
-  int tokens = UNROLL * slots / heads;
+  // Four heads per thread, as long as that leaves every SM two CTAs.  (Two at once: 26750 tokens
+  // of 48 heads 77 us, 96 when all four are loaded first, whose registers halve the CTAs of an SM.)
+  int tokens = 4 * slots / heads;
   tokens = tokens < R.A.T / (2 * sms) ? tokens : R.A.T / (2 * sms);
   tokens = tokens < slots ? tokens : slots;
   R.tokens = tokens < 1 ? 1 : tokens > MAX_TOKENS ? MAX_TOKENS : tokens;
