@@ -615,35 +615,25 @@ def sv_prompt_attn(q, k, v, cu_seqlens, sink: int, window: int, out, scale: floa
 
 # ------------------------------------------------------- rotary positions, appending to pages
 
-def _packed(t, heads, D, dtype, device, name: str) -> tuple[int, int]:
+def _packed(t, T: int, heads: int, D: int, dtype, device: int, name: str) -> tuple[int, int]:
     """(address, stride) of packed tokens [T][H][D] whose rows may be slices of wider ones."""
-    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, D):
-        raise SpecVerifyError(f"{name} must be [T][{heads}][{D}], got {tuple(t.shape)}")
-    if not t.is_cuda or t.get_device() != device:
-        raise SpecVerifyError(f"{name} must be on the call's CUDA device")
-    if t.dtype != dtype:
-        raise SpecVerifyError(f"{name} must be {dtype}, got {t.dtype}")
-    T = t.shape[0]
+    if t.shape != (T, heads, D) or t.get_device() != device or t.dtype is not dtype:
+        raise SpecVerifyError(f"{name} must be [{T}][{heads}][{D}] {dtype} on cuda:{device}, got "
+                              f"{list(t.shape)} {t.dtype} on {t.device}")
     row, head, one = t.stride()
     if T and ((D > 1 and one != 1) or (heads > 1 and head != D)):
         raise SpecVerifyError(f"{name}'s rows must be contiguous")
     return t.data_ptr(), row if T > 1 else heads * D
 
 
-def _same_tokens(T: int, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.shape[0] != T:
-            raise SpecVerifyError(f"{name} must have {T} tokens, got {t.shape[0]}")
-
-
 def _angles(table, device) -> tuple[int | None, int, int]:
     """(address, rows, rotated dimensions) of a rotation table [rows][2][rot / 2], or of none."""
     if table is None:
         return None, 0, 0
-    if table.dim() != 3 or table.shape[1] != 2:
+    shape = table.shape
+    if len(shape) != 3 or shape[1] != 2:
         raise SpecVerifyError("table must be [rows][2][rot / 2]")
-    return (_buf(table, table.shape, torch.float32, device, "table"), table.shape[0],
-            2 * table.shape[2])
+    return _buf(table, shape, torch.float32, device, "table"), shape[0], 2 * shape[2]
 
 
 def sv_rope_table(table, base: float = 10000.0, scaling: int = SV_ROPE_NONE, factor: float = 1.0,
@@ -666,14 +656,14 @@ def sv_rope(q, k, positions, table, q_out, k_out=None, interleaved: bool = False
         raise SpecVerifyError("q must be [T][Hq][D]")
     T, Hq, D = q.shape
     code, dev = _attn_dtype(q), _cuda_device(q, "q")
-    _same_tokens(T, k=k, q_out=q_out, k_out=k_out)
     if (k is None) != (k_out is None):
         raise SpecVerifyError("k and k_out come together")
     Hk = 0 if k is None else k.shape[1]
-    qp, qs = _packed(q, Hq, D, q.dtype, dev, "q")
-    qo, qos = _packed(q_out, Hq, D, q.dtype, dev, "q_out")
-    kp, ks = (None, 0) if k is None else _packed(k, Hk, D, q.dtype, dev, "k")
-    ko, kos = (None, 0) if k is None else _packed(k_out, Hk, D, q.dtype, dev, "k_out")
+    dt = q.dtype
+    qp, qs = _packed(q, T, Hq, D, dt, dev, "q")
+    qo, qos = _packed(q_out, T, Hq, D, dt, dev, "q_out")
+    kp, ks = (None, 0) if k is None else _packed(k, T, Hk, D, dt, dev, "k")
+    ko, kos = (None, 0) if k is None else _packed(k_out, T, Hk, D, dt, dev, "k_out")
     at, rows, rot = _angles(table, dev)
     _check(lib().sv_rope(
         code, qp, qs, kp, ks, _buf(positions, (T,), torch.int32, dev, "positions"), at, rows, rot,
@@ -697,15 +687,14 @@ def sv_page_append(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, ta
     P, LH, page, _ = k_pages.shape
     B, cols = block_table.shape
     code, dev, dt, i32 = _attn_dtype(k), _cuda_device(k, "k"), k.dtype, torch.int32
-    _same_tokens(T, v=v, q=q, q_out=q_out, k_out=k_out)
     if (q is None) != (q_out is None):
         raise SpecVerifyError("q and q_out come together")
     Hq = 0 if q is None else q.shape[1]
-    kp, ks = _packed(k, Hkv, D, dt, dev, "k")
-    vp, vs = _packed(v, Hkv, D, dt, dev, "v")
-    qp, qs = (None, 0) if q is None else _packed(q, Hq, D, dt, dev, "q")
-    qo, qos = (None, 0) if q is None else _packed(q_out, Hq, D, dt, dev, "q_out")
-    ko, kos = (None, 0) if k_out is None else _packed(k_out, Hkv, D, dt, dev, "k_out")
+    kp, ks = _packed(k, T, Hkv, D, dt, dev, "k")
+    vp, vs = _packed(v, T, Hkv, D, dt, dev, "v")
+    qp, qs = (None, 0) if q is None else _packed(q, T, Hq, D, dt, dev, "q")
+    qo, qos = (None, 0) if q is None else _packed(q_out, T, Hq, D, dt, dev, "q_out")
+    ko, kos = (None, 0) if k_out is None else _packed(k_out, T, Hkv, D, dt, dev, "k_out")
     at, rows, rot = _angles(table, dev)
     _check(lib().sv_page_append(
         code, kp, ks, vp, vs, _buf(k_pages, (P, LH, page, D), dt, dev, "k_pages"),
@@ -748,12 +737,11 @@ def sv_page_append8(k, v, k_pages, v_pages, k_scales, v_scales, block_table, seq
     T, Hkv, D = k.shape
     B, cols = block_table.shape
     code, dev, dt, i32 = _attn_dtype(k), _cuda_device(k, "k"), k.dtype, torch.int32
-    _same_tokens(T, v=v)
     pools, P, LH, page, Dp, block = _pages8(k_pages, v_pages, k_scales, v_scales, dev)
     if Dp != D:
         raise SpecVerifyError(f"pages have {Dp} dimensions, keys {D}")
-    kp, ks = _packed(k, Hkv, D, dt, dev, "k")
-    vp, vs = _packed(v, Hkv, D, dt, dev, "v")
+    kp, ks = _packed(k, T, Hkv, D, dt, dev, "k")
+    vp, vs = _packed(v, T, Hkv, D, dt, dev, "v")
     at, rows, rot = _angles(table, dev)
     _check(lib().sv_page_append8(
         code, kp, ks, vp, vs, *pools, _buf(block_table, (B, cols), i32, dev, "block_table"),
