@@ -518,12 +518,15 @@ def sv_attn8_workspace_bytes(B: int, N: int, Hq: int, Hkv: int, D: int) -> int:
     return int(lib().sv_attn8_workspace_bytes(B, N, Hq, Hkv, D))
 
 
-def make_attn_workspace(B: int, N: int, Hq: int, Hkv: int, D: int, device) -> torch.Tensor:
+def make_attn_workspace(B: int, N: int, Hq: int, Hkv: int, D: int, device,
+                        cache_bits: int | None = None) -> torch.Tensor:
     """Allocate a workspace for sv_tree_attn or sv_tree_attn8 (N nodes) or sv_ring_attn (N = R
-    tokens) with a batch of B (of which only sv_tree_attn8's depends)."""
-    n = sv_attn_workspace_bytes(N, Hq, Hkv, D)
-    n = n and max(n, sv_attn8_workspace_bytes(B, N, Hq, Hkv, D))
-    if n == 0:
+    tokens) with a batch of up to B.  cache_bits: 16 leaves out what only sv_tree_attn8 needs,
+    which alone goes by the batch; 8 what only the others need."""
+    n = sv_attn_workspace_bytes(N, Hq, Hkv, D) if cache_bits != 8 else 0
+    if cache_bits != 16:
+        n = max(n, sv_attn8_workspace_bytes(B, N, Hq, Hkv, D))
+    if n == 0 or cache_bits not in (None, 8, 16):
         raise SpecVerifyError("sizes the attention calls refuse")
     return torch.empty(n, dtype=torch.uint8, device=device)
 

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(THREADS) sv_rope_tokens(const __grid_constant_
   const int i = slot / R.lanes, h0 = slot - i * R.lanes;
   const int keys = R.Hq, values = R.Hq + R.Hk, heads = values + R.Hv;
   const bool active = i < count;
-  const long long t = t0 + i;
+  const long long t = (long long)t0 + i;
   bool turned = 8 * c < R.rot / 2;  // (half layout)
   int a, b;                         // where the vectors lie in a head
   if (turned && !R.inter) {

@@ -655,3 +655,37 @@ def test_decoding_run(dtype):
             # twice half a step (a block's scale may rise once between near sizes), the staged rounding, the smallest step
             tol = want.abs() * (2.0 ** -3 + 2 * u) + size * 2 * ku.ROT + 2.0 ** -9 * want.abs().max() / 100
             assert bool(((got - want).abs() <= tol).all())
+
+
+# ------------------------------------------------------------------ several rows of a CTA, several at a time
+
+@pytest.mark.parametrize("i,case", list(enumerate([
+    ([0, 9], [3000, 2000], 24, 128, 128, False, 64, 32, BF, 30, 0),
+    ([0, 5, 40], [1500, 700, 900], 40, 32, 32, True, 32, 16, HF, 41, 1),
+    ([3], [2500], 24, 48, 18, True, 32, 16, HF, None, 0),
+    ([0, 120], [2000, 1900], 20, 128, 64, False, 128, 128, BF, None, 0),
+])))
+def test_append8_of_many_heads(i, case):
+    c = append_case(60 + i, *case)
+    for x, bad in (("k", float("inf")), ("v", float("nan")), ("v", -float("inf"))):
+        for t in (7, 8, 1000, c["T"] - 2):
+            c[x][t, t % c["Hkv"], t % c["k"].shape[2]] = bad
+    kp, vp, ks, vs, out, st = append_call(c)
+    assert int(st.item()) == 0 and out.tolist() == [a + b for a, b in zip(c["lens"], c["more"])]
+    (wk, wks), (wv, wvs) = append_want(c)
+    assert torch.equal(u8(ks.cpu()), u8(wks)) and torch.equal(u8(vs.cpu()), u8(wvs))
+    assert same(kp.cpu(), wk) and same(vp.cpu(), wv)
+
+
+@pytest.mark.parametrize("i,case", list(enumerate([
+    ([(3 * i) % 50 for i in range(60)], [(7 * i) % 22 for i in range(60)], 22, 70, 128, 16, 16, BF, True),
+    ([i % 8 for i in range(152)], [i % 3 - 1 for i in range(152)], 2, 2100, 16, 8, 8, BF, True),
+    ([100] * 30, [5, 127, -1] * 10, 128, 90, 32, 128, 128, HF, False),
+])))
+def test_commit8_of_many_rows(i, case):
+    c = commit_case(60 + i, *case)
+    kp, vp, ks, vs, out, st = commit_call(c, in_place=i == 1)
+    assert int(st.item()) == 0 and out.tolist() == [n + k + 1 if k >= 0 else n for n, k in zip(c["lens"], c["acc"])]
+    (wk, wks), (wv, wvs) = commit_want(c)
+    assert same(kp.cpu(), wk) and same(vp.cpu(), wv)
+    assert torch.equal(u8(ks.cpu()), u8(wks)) and torch.equal(u8(vs.cpu()), u8(wvs))

@@ -335,3 +335,30 @@ def test_pages_past_32_bit_offsets():
     want = ku.rotate32(k, table[torch.tensor([1022, 1023, 1024, 1024], device=DEV)], False).to(BF)
     for t, (pg, row) in enumerate([(P - 1, 1022), (P - 1, 1023), (0, 0), (P - 2, 0)]):
         assert torch.equal(kp[pg, :, row], want[t]) and torch.equal(vp[pg, :, row], v[t])
+
+
+@pytest.mark.parametrize("T,H,D,rot,inter,dtype", [(700, 3, 24, 16, True, BF), (3000, 3, 40, 32, True, HF), (1500, 7, 40, 16, False, BF),
+                                                   (700, 2, 72, 16, True, HF), (5000, 1, 16, 6, True, BF), (40, 5, 256, 240, True, BF)])
+def test_dimensions_behind_the_rotated_ones_keep_their_bits(T, H, D, rot, inter, dtype):
+    """Whatever they hold (any bits: infinities and NaN too), whole and in vectors of which only a part is rotated."""
+    rng = np.random.default_rng(D + rot)
+    q = normal(rng, T, H, D, dtype=dtype)
+    q.view(torch.int16)[..., rot:] = torch.from_numpy(rng.integers(-2 ** 15, 2 ** 15, (T, H, D - rot)).astype(np.int16)).to(DEV)
+    table, pos = ku.angles(300, rot).float().to(DEV), i32(rng.integers(0, 300, T))
+    out = torch.full_like(q, FILL)
+    binding.sv_rope(q, None, pos, table, out, interleaved=inter)
+    assert torch.equal(out.view(torch.int16)[..., rot:], q.view(torch.int16)[..., rot:])
+    assert torch.equal(out[..., :rot], ku.rotate32(q, table[pos.long()], inter).to(dtype)[..., :rot])
+
+
+@pytest.mark.parametrize("rot,rows", [(2, 70000), (6, 5000), (254, 3000), (256, 20000), (128, 40000)])
+def test_table_rows_of_a_thread(rot, rows):
+    """Several rows per thread, and threads that have no pair: the rows of two halves are those of the whole."""
+    whole = torch.full((rows + 1, 2, rot // 2), FILL, device=DEV)
+    binding.sv_rope_table(whole[:rows], base=5e5)
+    part = torch.empty(rows - rows // 2, 2, rot // 2, device=DEV)
+    binding.sv_rope_table(part, base=5e5, first=rows // 2)
+    assert torch.equal(whole[rows // 2:rows], part) and bool((whole[rows] == FILL).all())
+    # as in test_table: 2^-22 for the functions, and some 2^-50 of an angle on either side
+    off = (whole[:rows].double().cpu() - ku.angles(rows, rot, base=5e5)).abs().max()
+    assert off <= 2.0 ** -22 + rows * 2.0 ** -49

@@ -216,3 +216,24 @@ def test_a_planted_mistake_is_found():
                   ku.rotate32(x, cs, True).to(torch.bfloat16), torch.where(good != 0, good * (1 + 2.0 ** -7), good)):
         with pytest.raises(AssertionError):
             ku.check_rotated(wrong, x, cs, False)
+
+
+def test_attention_workspace_sizes():
+    """0 for sizes that the calls refuse; it grows with the batch and covers every call that may follow."""
+    ask = binding.sv_attn8_workspace_bytes
+    for B, N, Hq, Hkv, D in [(1, 1, 1, 1, 16), (64, 22, 16, 16, 128), (65535, 1, 8, 2, 64), (3, 128, 4, 4, 32)]:
+        n = ask(B, N, Hq, Hkv, D)
+        assert n > 0 and n >= ask(max(1, B // 2), N, Hq, Hkv, D)
+        assert ask(2 * B if B < 30000 else B, N, Hq, Hkv, D) >= n
+    for bad in [(-1, 1, 1, 1, 16), (65536, 1, 1, 1, 16), (1, 0, 1, 1, 16), (1, 1, 3, 2, 16), (1, 1, 1, 1, 24), (1, 1, 1, 1, 0),
+                (1, 1, 1, 1, 144), (1, 1, 0, 1, 16), (1, 1, 1, 0, 16), (1, 1 << 20, 1, 1, 16)]:
+        assert ask(*bad) == 0, bad
+    with pytest.raises(binding.SpecVerifyError):
+        binding.make_attn_workspace(1, 0, 1, 1, 16, "cpu")
+    make, both = binding.make_attn_workspace, (ask(400, 3, 2, 1, 32), binding.sv_attn_workspace_bytes(3, 2, 1, 32))
+    assert make(400, 3, 2, 1, 32, "cpu").numel() == max(both)
+    assert make(400, 3, 2, 1, 32, "cpu", 8).numel() == both[0] and make(400, 3, 2, 1, 32, "cpu", 16).numel() == both[1]
+    assert make(2, 3, 2, 1, 24, "cpu").numel() == binding.sv_attn_workspace_bytes(3, 2, 1, 24)
+    for bits, D in ((4, 32), (8, 24)):
+        with pytest.raises(binding.SpecVerifyError):
+            make(2, 3, 2, 1, D, "cpu", bits)
