@@ -14,7 +14,8 @@
 // instructions for prompts, and for single tokens and short paths the latency of the loads
 // that depend on one another: bounds, length, page, entries.  (64 paths of 3 entries, 384 rows:
 // 26 us; 101 with a CTA per unit, most of whose threads had no entry.  32 ragged prompts of 8
-// heads, 80,000 tokens: 116 us, 4.6 TB/s; the state's registers leave an SM sixteen warps.)
+// heads, 86,000 tokens: 103 us, 5.2 TB/s, and 116 with the angles loaded again for every head;
+// the registers leave an SM sixteen warps.)
 
 #include "rope.cuh"
 #include "svkv8.h"
@@ -116,9 +117,11 @@ struct Pools {
 struct RowState { uint32_t k, v; int own_k, own_v; };
 struct Shared {
   RowState state[MAX_ROWS];
-  uint4 pieces[];  // [stage of two][piece][part of four][thread]
+  uint4 pieces[];  // [two stages and the angles][piece][part of four][thread]
 };
-size_t shared_bytes(int threads) { return sizeof(Shared) + size_t(2 * PIECES * 4) * threads * 16; }
+size_t shared_bytes(int threads, bool angles) {
+  return sizeof(Shared) + size_t((angles ? 3 : 2) * PIECES * 4) * threads * 16;
+}
 
 __device__ __forceinline__ int exponent_k(const Pools& P, const RowState& x) {
   return max(exponent_for(__uint_as_float(x.k), P.least, P.most), x.own_k);
@@ -177,6 +180,19 @@ __device__ __forceinline__ void write_rows(const Pools& P, Shared& S, int page, 
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  // (an entry's angles are those of every row)
+  uint4* const held = S.pieces + 2 * PIECES * 4 * threads + tid;
+  if (VEC && rot) {
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u)
+      if (row[u] < at_once && 8 * chunk[u] < rot / 2) {
+        const float* const c = entry[u].angles + 8 * chunk[u];
+        copy_async(held + u * 4 * threads, c);
+        copy_async(held + (u * 4 + 1) * threads, c + 4);
+        copy_async(held + (u * 4 + 2) * threads, c + rot / 2);
+        copy_async(held + (u * 4 + 3) * threads, c + rot / 2 + 4);
+      }
+  }
   fetch(0, 0);
   __syncthreads();  // (the states of the units before these are used up)
   for (int r = tid; r < rows; r += threads) {
@@ -203,13 +219,16 @@ __device__ __forceinline__ void write_rows(const Pools& P, Shared& S, int page, 
       if (r0 + row[u] < rows) {
         uint4* const from = S.pieces + (stage * PIECES + u) * 4 * threads + tid;
         const int c = chunk[u];
-        const float* const angles = entry[u].angles;
         if (VEC) {
           const bool turned = 8 * c < rot / 2;
           split<BF>(from[0], from[threads], inter || !turned, ka[u], kb[u]);
-          if (turned) turn8(ka[u], kb[u], turns(angles, rot, 8 * c, 8 * c + 4));
+          if (turned) {
+            const float4* const w = reinterpret_cast<const float4*>(held + u * 4 * threads);
+            turn8(ka[u], kb[u], {w[0], w[threads], w[2 * threads], w[3 * threads]});
+          }
         } else {
           const uint16_t* const k = entry[u].k + (r0 + row[u]) * k_row;
+          const float* const angles = entry[u].angles;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int pair = 8 * c + e;
@@ -503,8 +522,9 @@ int rows_for(long long units, int rows, int sms) {
   return int(n < 1 ? 1 : n < most ? n : most);
 }
 template <class Params>
-int start(void (*kernel)(Params), dim3 grid, int threads, cudaStream_t st, const Params& R) {
-  const size_t bytes = shared_bytes(threads);
+int start(void (*kernel)(Params), dim3 grid, int threads, bool angles, cudaStream_t st,
+          const Params& R) {
+  const size_t bytes = shared_bytes(threads, angles);
   if (bytes > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) !=
           cudaSuccess)
@@ -572,7 +592,7 @@ int sv_page_append8(int dtype, const void* k, long long k_stride, const void* v,
   const bool bf = dtype == SV_BF16;
   return start(R.rot % 16 == 0 ? (bf ? sv_kv8_append<true, true> : sv_kv8_append<false, true>)
                                : (bf ? sv_kv8_append<true, false> : sv_kv8_append<false, false>),
-               g, threads, st, R);
+               g, threads, R.rot != 0 && R.rot % 16 == 0, st, R);
 }
 
 int sv_page_commit8(int dtype, void* k_pages, void* v_pages, void* k_scales, void* v_scales,
@@ -621,10 +641,10 @@ int sv_page_commit8(int dtype, void* k_pages, void* v_pages, void* k_scales, voi
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = dtype == SV_BF16;
   if (!in_place) {
-    return start(bf ? sv_kv8_commit<true, false> : sv_kv8_commit<false, false>, g, threads, st, R);
+    return start(bf ? sv_kv8_commit<true, false> : sv_kv8_commit<false, false>, g, threads, false, st, R);
   }
   const int rc =
-      start(bf ? sv_kv8_commit<true, true> : sv_kv8_commit<false, true>, g, threads, st, R);
+      start(bf ? sv_kv8_commit<true, true> : sv_kv8_commit<false, true>, g, threads, false, st, R);
   if (rc != SV_OK) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(B));

@@ -101,7 +101,7 @@ struct TokenParams {
 // The first heads are loaded before it is known where they go: bounds, length, page and angles
 // are a chain of four loads, the latency of a decoding step.
 template <bool BF, bool VEC>
-__global__ void __launch_bounds__(THREADS) sv_rope_tokens(const __grid_constant__ TokenParams R) {
+__global__ void __launch_bounds__(THREADS, 4) sv_rope_tokens(const __grid_constant__ TokenParams R) {
   __shared__ int pos_of[MAX_TOKENS];          // where a token is rotated to; -1: left out
   __shared__ long long page_of[MAX_TOKENS];   // its page's first row, and its row there
   const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(THREADS) sv_rope_tokens(const __grid_constant_
   const int i = slot / R.lanes, h0 = slot - i * R.lanes;
   const int keys = R.Hq, values = R.Hq + R.Hk, heads = values + R.Hv;
   const bool active = i < count;
-  const long long t = (long long)t0 + i;
+  const long long t = unsigned(t0) + unsigned(i);
   bool turned = 8 * c < R.rot / 2;  // (half layout)
   int a, b;                         // where the vectors lie in a head
   if (turned && !R.inter) {
@@ -262,7 +262,7 @@ int run_tokens(TokenParams& R, int dtype, void* stream) {
     return SV_ERR_CUDA;
   R.chunks = (R.D + 15) / 16;
   const int heads = R.Hq + R.Hk + R.Hv, slots = THREADS / R.chunks;
-  // Four heads per thread, as long as that leaves every SM two CTAs.  (Two at once: 26750 tokens
+  // Four heads per thread, as long as that leaves every SM two CTAs.  (Two at once: 17800 tokens
   // of 48 heads 77 us, 96 when all four are loaded first, whose registers halve the CTAs of an SM.)
   int tokens = 4 * slots / heads;
   tokens = tokens < R.A.T / (2 * sms) ? tokens : R.A.T / (2 * sms);
