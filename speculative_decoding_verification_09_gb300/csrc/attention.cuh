@@ -21,6 +21,12 @@
 // that share an SM is a chain: scores, softmax, the weights' product, the next
 // scores (which take the weights' place).  8192 tokens under a window of 4096, 32
 // heads of 128: 319 us, 1.29 PFLOP/s, 0.67 of the measured bf16 rate.
+//
+// Over 8-bit pages (Q8; include/svkv8.h) the cache is half as long, and a tile's chain
+// holds the blocks' powers of two and values' widening besides.  Few rows are bound by HBM
+// all the same (64 requests of 4 tokens, 16 rows: 164 us, 4.7 TB/s; 208 over 16 bits), more rows by
+// the softmax and by how many roles' code an SM has to fetch: 22 nodes, 88 rows 241 us.
+//   sv_attn8_prep  before it: queries and staged entries as 8-bit terms
 #ifndef SV_ATTENTION_CUH
 #define SV_ATTENTION_CUH
 
@@ -1066,7 +1072,7 @@ __device__ __forceinline__ float power_or_nan(int e) {
 // segment's query terms, its staged tiles' keys' terms, then its cached tiles' keys and values.
 // Little is done per tile (pages' numbers are read a tile ahead, places found without a
 // division), since a single warp gets an instruction about every ten cycles here (64 trees of 22
-// nodes: 289 us with the loop of the 16-bit caches, whose tiles are twice as long).
+// nodes: 289 us with the loop of the 16-bit caches, whose tiles are twice as long, 242 so).
 template <int DP, int NQ, bool PAIR, bool BF>
 __device__ __forceinline__ void copy_bytes(const AttnParams& A, Ctrl<NQ, PAIR>& C,
                                            unsigned char* smem, volatile int* abort) {
@@ -1920,7 +1926,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
           if constexpr (Q8) {
             // 32 scores at a time, for the maximum and again for the weights, in loops that are
             // not unrolled: with the powers of two the code of a whole tile is longer than what
-            // is fetched in time (64 trees of 88 rows: 447 us unrolled).
+            // is fetched in time (64 trees of 88 rows: 447 us unrolled, 344 so).
             uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
             if (masked) {
               visible(see);

@@ -12,8 +12,8 @@
 // the next rows' pieces are on their way to shared memory meanwhile.  Every byte is moved once
 // (a block's older entries only when its scale rises); what bounds it is HBM and the
 // instructions for prompts, and for single tokens and short paths the latency of the loads
-// that depend on one another: bounds, length, page, entries.  (64 paths of 3 entries, 384 rows:
-// 26 us; 101 with a CTA per unit, most of whose threads had no entry.  32 ragged prompts of 8
+// that depend on one another: bounds, length, page, entries.  (64 paths of 4 entries, 384 rows:
+// 25 us; 101 with a CTA per unit, most of whose threads had no entry.  32 ragged prompts of 8
 // heads, 86,000 tokens: 103 us, 5.2 TB/s, and 116 with the angles loaded again for every head;
 // the registers leave an SM sixteen warps.)
 
@@ -633,7 +633,7 @@ int sv_page_commit8(int dtype, void* k_pages, void* v_pages, void* k_scales, voi
   R.rows = rows_for(B, LH, sms);
   const int units = (N - 1 + block - 1) / block + 1;  // of a path of N entries, wherever it begins
   // A path's units one after another, unless there are too few CTAs otherwise: most paths have
-  // one or two, whatever N, and the CTAs that find none cost 1 us of 30 (64 paths of 3 entries out
+  // one or two, whatever N, and the CTAs that find none cost 1 us of 30 (64 paths of 4 entries out
   // of 22 nodes, 384 rows).
   const long long ctas = (long long)B * ((LH + R.rows - 1) / R.rows), y = 8LL * sms / ctas;
   const dim3 g(static_cast<unsigned>((LH + R.rows - 1) / R.rows),
