@@ -396,8 +396,8 @@ __global__ void __launch_bounds__(MAX_THREADS) sv_kv8_append(
     }
     if (!ok) continue;
     const long long token = lo + j;
-    write_rows<BF, VEC>(R.P, S, pg, R.head0 + h, min(R.heads, R.Hkv - h), at - off - col * A.page, off, count,
-                   R.rot, R.inter, R.P.D, R.P.D, [&](int e) {
+    write_rows<BF, VEC>(R.P, S, pg, R.head0 + h, min(R.heads, R.Hkv - h), at - off - col * A.page,
+                   off, count, R.rot, R.inter, R.P.D, R.P.D, [&](int e) {
                      const int p = A.rows && A.positions ? __ldg(A.positions + token + e) : at + e;
                      return Entry{R.k + (token + e) * R.ks + (long long)h * R.P.D,
                                   R.v + (token + e) * R.vs + (long long)h * R.P.D,
@@ -467,13 +467,14 @@ __global__ void __launch_bounds__(MAX_THREADS) sv_kv8_commit(
     set_status(R.status, bad);
   }
   if (k < 0 || bad) return;
-  for (long long j0 = before; j0 <= k; j0 += (long long)gridDim.y * block - (j0 ? 0 : len % block)) {
+  for (long long j0 = before; j0 <= k;
+       j0 += (long long)gridDim.y * block - (j0 ? 0 : len % block)) {
     const int j = int(j0), at = len + j, off = at % block;
     const int count = min(block - off, k + 1 - j), col = at / R.P.page;
     const int pg = __ldg(R.table + size_t(b) * R.cols + col);
     const long long next = (long long)R.N * R.P.D;
-    write_rows<BF, true>(R.P, S, pg, row, min(R.rows, R.P.LH - row), at - off - col * R.P.page, off, count, 0,
-                   false, next, next, [&](int i) {
+    write_rows<BF, true>(R.P, S, pg, row, min(R.rows, R.P.LH - row), at - off - col * R.P.page,
+                   off, count, 0, false, next, next, [&](int i) {
                      const int e = j + i;
                      const int node =
                          R.nodes && e > 0 ? __ldg(R.nodes + size_t(b) * R.N + e - 1) : e;
@@ -641,7 +642,8 @@ int sv_page_commit8(int dtype, void* k_pages, void* v_pages, void* k_scales, voi
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = dtype == SV_BF16;
   if (!in_place) {
-    return start(bf ? sv_kv8_commit<true, false> : sv_kv8_commit<false, false>, g, threads, false, st, R);
+    return start(bf ? sv_kv8_commit<true, false> : sv_kv8_commit<false, false>, g, threads, false,
+                 st, R);
   }
   const int rc =
       start(bf ? sv_kv8_commit<true, true> : sv_kv8_commit<false, true>, g, threads, false, st, R);

@@ -51,7 +51,8 @@ __global__ void __launch_bounds__(THREADS) sv_rope_angles(const __grid_constant_
   float* out = R.table + size_t(p0) * 2 * R.half + i;
   for (int n = 0; n < R.passes && p0 + n * at_once < R.rows; ++n) {
     const uint32_t h = uint32_t(angle >> 32), quarter = h + 0x20000000u;
-    const float x = float(int(h - (quarter & 0xc0000000u))) * 1.46291807926715968e-9f;  // 2 pi / 2^32
+    const float x =
+        float(int(h - (quarter & 0xc0000000u))) * 1.46291807926715968e-9f;  // 2 pi / 2^32
     const float y = x * x;
     float s = fmaf(y, 1.0f / 362880, -1.0f / 5040);
     s = fmaf(y, s, 1.0f / 120);
@@ -101,7 +102,8 @@ struct TokenParams {
 // The first heads are loaded before it is known where they go: bounds, length, page and angles
 // are a chain of four loads, the latency of a decoding step.
 template <bool BF, bool VEC>
-__global__ void __launch_bounds__(THREADS, 4) sv_rope_tokens(const __grid_constant__ TokenParams R) {
+__global__ void __launch_bounds__(THREADS, 4) sv_rope_tokens(
+    const __grid_constant__ TokenParams R) {
   __shared__ int pos_of[MAX_TOKENS];          // where a token is rotated to; -1: left out
   __shared__ long long page_of[MAX_TOKENS];   // its page's first row, and its row there
   const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
