@@ -38,37 +38,55 @@ struct AngleParams {
 // for them.)  Its upper 32 bits are split into the nearest quarter turn and a rest x of at
 // most pi / 4 to either side, where the Taylor polynomials of sine (to x^9) and cosine (to
 // x^10) are off by less than 2^-29; the roundings of x and of the sums add up to 2^-23.
-// What bounds it is the instructions, some 40 per angle, until the table outgrows L2.
-// (131072 positions of 64 pairs: 67 us with a division per angle and sincospif, whose
-// reduction has nothing left to do here.)
+// What bounds it is the instructions until the table outgrows L2.  (131072 positions of 64
+// pairs: 67 us with a division per angle and sincospif, whose reduction has nothing left to
+// do here, 15 with a pair per thread, 11.4 with four, 5.9 TB/s.)
+// V neighbouring pairs of a thread, stored as one vector: four where the pairs can be cut so.
+template <int V>
 __global__ void __launch_bounds__(THREADS) sv_rope_angles(const __grid_constant__ AngleParams R) {
-  const int at_once = THREADS / R.half, r = int(threadIdx.x) / R.half;
-  const int i = int(threadIdx.x) - r * R.half;
+  const int lanes = R.half / V, at_once = THREADS / lanes, r = int(threadIdx.x) / lanes;
+  const int i = (int(threadIdx.x) - r * lanes) * V;
   if (r >= at_once) return;
   const long long p0 = (long long)blockIdx.x * R.passes * at_once + r;
-  const uint64_t turn = R.turn[i], step = turn * unsigned(at_once);
-  uint64_t angle = turn * uint64_t(R.first + p0);
+  uint64_t angle[V], step[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    angle[v] = R.turn[i + v] * uint64_t(R.first + p0);
+    step[v] = R.turn[i + v] * unsigned(at_once);
+  }
   float* out = R.table + size_t(p0) * 2 * R.half + i;
+#pragma unroll 1
   for (int n = 0; n < R.passes && p0 + n * at_once < R.rows; ++n) {
-    const uint32_t h = uint32_t(angle >> 32), quarter = h + 0x20000000u;
-    const float x =
-        float(int(h - (quarter & 0xc0000000u))) * 1.46291807926715968e-9f;  // 2 pi / 2^32
-    const float y = x * x;
-    float s = fmaf(y, 1.0f / 362880, -1.0f / 5040);
-    s = fmaf(y, s, 1.0f / 120);
-    s = fmaf(y, s, -1.0f / 6);
-    s = fmaf(x * y, s, x);
-    float c = fmaf(y, -1.0f / 3628800, 1.0f / 40320);
-    c = fmaf(y, c, -1.0f / 720);
-    c = fmaf(y, c, 1.0f / 24);
-    c = fmaf(y, c, -0.5f);
-    c = fmaf(y, c, 1.0f);
-    // a quarter turn more: (c, s) becomes (-s, c)
-    const bool odd = quarter & 0x40000000u, low = quarter & 0x80000000u;
-    const float u = odd ? s : c, v = odd ? c : s;
-    out[0] = (odd != low ? -u : u) * R.gain;
-    out[R.half] = (low ? -v : v) * R.gain;
-    angle += step;
+    float cs[V], sn[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const uint32_t h = uint32_t(angle[v] >> 32), quarter = h + 0x20000000u;
+      const float x =
+          float(int(h - (quarter & 0xc0000000u))) * 1.46291807926715968e-9f;  // 2 pi / 2^32
+      const float y = x * x;
+      float s = fmaf(y, 1.0f / 362880, -1.0f / 5040);
+      s = fmaf(y, s, 1.0f / 120);
+      s = fmaf(y, s, -1.0f / 6);
+      s = fmaf(x * y, s, x);
+      float c = fmaf(y, -1.0f / 3628800, 1.0f / 40320);
+      c = fmaf(y, c, -1.0f / 720);
+      c = fmaf(y, c, 1.0f / 24);
+      c = fmaf(y, c, -0.5f);
+      c = fmaf(y, c, 1.0f);
+      // a quarter turn more: (c, s) becomes (-s, c)
+      const bool odd = quarter & 0x40000000u;
+      const uint32_t low = quarter & 0x80000000u, high = low ^ (quarter << 1 & 0x80000000u);
+      cs[v] = __uint_as_float(__float_as_uint(odd ? s : c) ^ high) * R.gain;
+      sn[v] = __uint_as_float(__float_as_uint(odd ? c : s) ^ low) * R.gain;
+      angle[v] += step[v];
+    }
+    if constexpr (V == 4) {
+      *reinterpret_cast<float4*>(out) = make_float4(cs[0], cs[1], cs[2], cs[3]);
+      *reinterpret_cast<float4*>(out + R.half) = make_float4(sn[0], sn[1], sn[2], sn[3]);
+    } else {
+      out[0] = cs[0];
+      out[R.half] = sn[0];
+    }
     out += size_t(at_once) * 2 * R.half;
   }
 }
@@ -331,10 +349,13 @@ int sv_rope_table(int scaling, double base, double factor, int original, double 
     R.turn[i] = uint64_t(ldexp(turns - floor(turns), 63)) << 1;
   }
   // Sixteen rows per thread, as long as that leaves some CTAs for every SM.
-  const int at_once = THREADS / R.half, passes = rows / at_once / 1024;
+  const bool vec = R.half % 4 == 0;
+  const int at_once = THREADS / (vec ? R.half / 4 : R.half), passes = rows / at_once / 1024;
   R.passes = passes < 1 ? 1 : passes > 16 ? 16 : passes;
   const long long per_cta = (long long)at_once * R.passes, grid = (rows + per_cta - 1) / per_cta;
-  sv_rope_angles<<<unsigned(grid), THREADS, 0, static_cast<cudaStream_t>(stream)>>>(R);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (vec) sv_rope_angles<4><<<unsigned(grid), THREADS, 0, st>>>(R);
+  else sv_rope_angles<1><<<unsigned(grid), THREADS, 0, st>>>(R);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
