@@ -516,9 +516,9 @@ void set_pools(Pools& P, int dtype, void* kp, void* vp, void* ks, void* vs, int 
 int threads_for(const Pools& P) {
   return P.block * P.chunks <= PIECES * 128 ? 128 : P.block * P.chunks <= PIECES * 256 ? 256 : 512;
 }
-// Rows of a CTA: enough CTAs for eight on every SM, if there is work for them.
-int rows_for(long long units, int rows, int sms) {
-  const long long n = units * rows / (8LL * sms);
+// Rows of a CTA: enough CTAs for `per_sm` on every SM, if there is work for them.
+int rows_for(long long units, int rows, long long sms, int per_sm) {
+  const long long n = (units * rows + per_sm * sms / 2) / (per_sm * sms);
   const int most = rows < MAX_ROWS ? rows : MAX_ROWS;
   return int(n < 1 ? 1 : n < most ? n : most);
 }
@@ -581,13 +581,18 @@ int sv_page_append8(int dtype, const void* k, long long k_stride, const void* v,
   R.Hkv = Hkv; R.head0 = head0; R.rot = table ? rot : 0;
   R.inter = interleaved != 0;
   const int threads = threads_for(R.P);
-  // A CTA per token when that is a few CTAs per SM (single tokens: every unit at once), else
-  // one per block's worth of tokens (a prompt's CTAs have one unit each).
-  R.tokens = (long long)T * Hkv <= 16LL * sms ? 1 : block;
+  // A CTA per token when that is a few CTAs per SM or most units are far shorter than a block
+  // (single tokens: every unit at once), else one per block's worth of tokens (a prompt's CTAs
+  // have one unit each).  (8 heads.  One token each of 1024 requests, blocks of 16: 9.9 us, and
+  // 55 in CTAs of 16 tokens, one unit after another; 12 tokens each of 256, blocks of 32: 16.2
+  // and 26.9; 30 tokens each of 64: 18.2 and 15.4.)
+  R.tokens = (long long)T * Hkv <= 16LL * sms || 2LL * T < (long long)B * block ? 1 : block;
   R.token_ctas = int(((long long)T + R.tokens - 1) / R.tokens);
   const long long grid = R.token_ctas + ((long long)B + threads / 32 - 1) / (threads / 32);
   if (grid > 0x7fffffffLL) return SV_ERR_INVALID_ARG;
-  R.heads = R.tokens == 1 ? 1 : rows_for(R.token_ctas, Hkv, sms);
+  // Heads of a single token are few pieces: two CTAs per SM, whose heads pass at once, beat more
+  // CTAs.  (64 tokens of 32 heads 5.0 us, 7.8 with four per SM; 512 of 8 heads 5.7 and 8.9.)
+  R.heads = rows_for(R.token_ctas, Hkv, sms, R.tokens == 1 ? 2 : 8);
   const dim3 g(static_cast<unsigned>(grid), static_cast<unsigned>((Hkv + R.heads - 1) / R.heads));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = dtype == SV_BF16;
@@ -631,7 +636,7 @@ int sv_page_commit8(int dtype, void* k_pages, void* v_pages, void* k_scales, voi
   const int sms = sm_count();
   if (sms < 1) return SV_ERR_CUDA;
   const int threads = threads_for(R.P);
-  R.rows = rows_for(B, LH, sms);
+  R.rows = rows_for(B, LH, sms, 8);
   const int units = (N - 1 + block - 1) / block + 1;  // of a path of N entries, wherever it begins
   // A path's units one after another, unless there are too few CTAs otherwise: most paths have
   // one or two, whatever N, and the CTAs that find none cost 1 us of 30 (64 paths of 4 entries out

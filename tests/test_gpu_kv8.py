@@ -664,11 +664,13 @@ def test_decoding_run(dtype):
     ([0, 5, 40], [1500, 700, 900], 40, 32, 32, True, 32, 16, HF, 41, 1),
     ([3], [2500], 24, 48, 18, True, 32, 16, HF, None, 0),
     ([0, 120], [2000, 1900], 20, 128, 64, False, 128, 128, BF, None, 0),
+    ([7 * i % 90 for i in range(900)], [(1, 1, 2, 1, 0, 1)[i % 6] for i in range(900)], 12, 64, 64, False, 32, 16, BF, 13, 1),
+    ([i % 60 for i in range(150)], [1 + 11 * i % 23 for i in range(150)], 6, 80, 48, True, 64, 64, HF, None, 0),
 ])))
 def test_append8_of_many_heads(i, case):
     c = append_case(60 + i, *case)
     for x, bad in (("k", float("inf")), ("v", float("nan")), ("v", -float("inf"))):
-        for t in (7, 8, 1000, c["T"] - 2):
+        for t in (7, 8, c["T"] // 2, c["T"] - 2):
             c[x][t, t % c["Hkv"], t % c["k"].shape[2]] = bad
     kp, vp, ks, vs, out, st = append_call(c)
     assert int(st.item()) == 0 and out.tolist() == [a + b for a, b in zip(c["lens"], c["more"])]
