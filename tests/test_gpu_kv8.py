@@ -664,7 +664,7 @@ def test_decoding_run(dtype):
     ([0, 5, 40], [1500, 700, 900], 40, 32, 32, True, 32, 16, HF, 41, 1),
     ([3], [2500], 24, 48, 18, True, 32, 16, HF, None, 0),
     ([0, 120], [2000, 1900], 20, 128, 64, False, 128, 128, BF, None, 0),
-    ([7 * i % 90 for i in range(900)], [(1, 1, 2, 1, 0, 1)[i % 6] for i in range(900)], 12, 64, 64, False, 32, 16, BF, 13, 1),
+    ([7 * i % 90 for i in range(350)], [(1, 1, 2, 1, 0, 1)[i % 6] for i in range(350)], 12, 64, 64, False, 32, 16, BF, 13, 1),
     ([i % 60 for i in range(150)], [1 + 11 * i % 23 for i in range(150)], 6, 80, 48, True, 64, 64, HF, None, 0),
 ])))
 def test_append8_of_many_heads(i, case):
