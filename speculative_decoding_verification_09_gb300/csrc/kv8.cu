@@ -17,6 +17,8 @@
 // heads, 86,000 tokens: 103 us, 5.2 TB/s, and 116 with the angles loaded again for every head;
 // the registers leave an SM sixteen warps.)
 
+#include <atomic>
+
 #include "rope.cuh"
 #include "svkv8.h"
 
@@ -522,15 +524,23 @@ int rows_for(long long units, int rows, long long sms, int per_sm) {
   const int most = rows < MAX_ROWS ? rows : MAX_ROWS;
   return int(n < 1 ? 1 : n < most ? n : most);
 }
-template <class Params>
-int start(void (*kernel)(Params), dim3 grid, int threads, bool angles, cudaStream_t st,
-          const Params& R) {
+template <auto KERNEL, class Params>
+int start(dim3 grid, int threads, bool angles, cudaStream_t st, const Params& R) {
   const size_t bytes = shared_bytes(threads, angles);
-  if (bytes > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) !=
-          cudaSuccess)
-    return SV_ERR_CUDA;
-  kernel<<<grid, threads, bytes, st>>>(R);
+  if (bytes > 48 * 1024) {
+    // the kernel's shared-memory limit, raised once per device (ordinals past 63: every time)
+    static std::atomic<uint64_t> raised{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SV_ERR_CUDA;
+    const uint64_t mark = dev < 64 ? uint64_t(1) << dev : 0;
+    if (!(raised.load(std::memory_order_acquire) & mark)) {
+      if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               int(shared_bytes(MAX_THREADS, true))) != cudaSuccess)
+        return SV_ERR_CUDA;
+      raised.fetch_or(mark, std::memory_order_release);
+    }
+  }
+  KERNEL<<<grid, threads, bytes, st>>>(R);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 int sm_count() {
@@ -596,9 +606,12 @@ int sv_page_append8(int dtype, const void* k, long long k_stride, const void* v,
   const dim3 g(static_cast<unsigned>(grid), static_cast<unsigned>((Hkv + R.heads - 1) / R.heads));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = dtype == SV_BF16;
-  return start(R.rot % 16 == 0 ? (bf ? sv_kv8_append<true, true> : sv_kv8_append<false, true>)
-                               : (bf ? sv_kv8_append<true, false> : sv_kv8_append<false, false>),
-               g, threads, R.rot != 0 && R.rot % 16 == 0, st, R);
+  const bool vec = R.rot % 16 == 0, angles = R.rot != 0 && vec;
+  if (vec)
+    return bf ? start<sv_kv8_append<true, true>>(g, threads, angles, st, R)
+              : start<sv_kv8_append<false, true>>(g, threads, angles, st, R);
+  return bf ? start<sv_kv8_append<true, false>>(g, threads, angles, st, R)
+            : start<sv_kv8_append<false, false>>(g, threads, angles, st, R);
 }
 
 int sv_page_commit8(int dtype, void* k_pages, void* v_pages, void* k_scales, void* v_scales,
@@ -646,12 +659,11 @@ int sv_page_commit8(int dtype, void* k_pages, void* v_pages, void* k_scales, voi
                static_cast<unsigned>(y < 1 ? 1 : y < units ? y : units), static_cast<unsigned>(B));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = dtype == SV_BF16;
-  if (!in_place) {
-    return start(bf ? sv_kv8_commit<true, false> : sv_kv8_commit<false, false>, g, threads, false,
-                 st, R);
-  }
-  const int rc =
-      start(bf ? sv_kv8_commit<true, true> : sv_kv8_commit<false, true>, g, threads, false, st, R);
+  if (!in_place)
+    return bf ? start<sv_kv8_commit<true, false>>(g, threads, false, st, R)
+              : start<sv_kv8_commit<false, false>>(g, threads, false, st, R);
+  const int rc = bf ? start<sv_kv8_commit<true, true>>(g, threads, false, st, R)
+                    : start<sv_kv8_commit<false, true>>(g, threads, false, st, R);
   if (rc != SV_OK) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(B));
