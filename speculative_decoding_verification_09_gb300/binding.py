@@ -659,8 +659,8 @@ def sv_rope(q, k, positions, table, q_out, k_out=None, interleaved: bool = False
         raise SpecVerifyError("q must be [T][Hq][D]")
     T, Hq, D = q.shape
     code, dev = _attn_dtype(q), _cuda_device(q, "q")
-    if (k is None) != (k_out is None):
-        raise SpecVerifyError("k and k_out come together")
+    if (k is None) != (k_out is None) or (k is not None and k.dim() != 3):
+        raise SpecVerifyError("k and k_out come together, [T][Hk][D]")
     Hk = 0 if k is None else k.shape[1]
     dt = q.dtype
     qp, qs = _packed(q, T, Hq, D, dt, dev, "q")
@@ -690,8 +690,8 @@ def sv_page_append(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, ta
     P, LH, page, _ = k_pages.shape
     B, cols = block_table.shape
     code, dev, dt, i32 = _attn_dtype(k), _cuda_device(k, "k"), k.dtype, torch.int32
-    if (q is None) != (q_out is None):
-        raise SpecVerifyError("q and q_out come together")
+    if (q is None) != (q_out is None) or (q is not None and q.dim() != 3):
+        raise SpecVerifyError("q and q_out come together, [T][Hq][D]")
     Hq = 0 if q is None else q.shape[1]
     kp, ks = _packed(k, T, Hkv, D, dt, dev, "k")
     vp, vs = _packed(v, T, Hkv, D, dt, dev, "v")

@@ -362,3 +362,15 @@ def test_table_rows_of_a_thread(rot, rows):
     # as in test_table: 2^-22 for the functions, and some 2^-50 of an angle on either side
     off = (whole[:rows].double().cpu() - ku.angles(rows, rot, base=5e5)).abs().max()
     assert off <= 2.0 ** -22 + rows * 2.0 ** -49
+
+
+def test_queries_and_keys_of_other_ranks_are_refused():
+    x = torch.zeros(4, 1, 8, dtype=BF, device=DEV)
+    flat, table, pages = torch.zeros(32, dtype=BF, device=DEV), ku.angles(4, 8).float().to(DEV), torch.zeros(1, 1, 8, 8, dtype=BF, device=DEV)
+    for bad in (flat, x[0], x[None], x[:, :, :0], x[:3]):
+        with pytest.raises(binding.SpecVerifyError):
+            binding.sv_rope(x, bad, i32([0] * 4), table, x, bad)
+        with pytest.raises(binding.SpecVerifyError):
+            binding.sv_page_append(x, x, pages, pages.clone(), i32([[0]]), i32([0]), i32([0, 4]), table, q=bad, q_out=bad)
+        with pytest.raises(binding.SpecVerifyError):
+            binding.sv_page_append(x, bad, pages, pages.clone(), i32([[0]]), i32([0]), i32([0, 4]), table)
