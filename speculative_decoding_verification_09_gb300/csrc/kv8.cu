@@ -518,7 +518,10 @@ void set_pools(Pools& P, int dtype, void* kp, void* vp, void* ks, void* vs, int 
 int threads_for(const Pools& P) {
   return P.block * P.chunks <= PIECES * 128 ? 128 : P.block * P.chunks <= PIECES * 256 ? 256 : 512;
 }
-// Rows of a CTA: enough CTAs for `per_sm` on every SM, if there is work for them.
+// Rows of a CTA: enough CTAs for `per_sm` on every SM, if there is work for them.  Otherwise
+// 1024 threads' worth, twice what an SM holds.  (Eight CTAs per SM whatever their size: paths of
+// 34 requests, 65 rows, blocks of 128: 28.3 us for 12.6; 25,000 tokens of prompts, 8 heads of
+// 96, blocks of 128: 71 for 50.)
 int rows_for(long long units, int rows, long long sms, int per_sm) {
   const long long n = (units * rows + per_sm * sms / 2) / (per_sm * sms);
   const int most = rows < MAX_ROWS ? rows : MAX_ROWS;
@@ -602,7 +605,7 @@ int sv_page_append8(int dtype, const void* k, long long k_stride, const void* v,
   if (grid > 0x7fffffffLL) return SV_ERR_INVALID_ARG;
   // Heads of a single token are few pieces: two CTAs per SM, whose heads pass at once, beat more
   // CTAs.  (64 tokens of 32 heads 5.0 us, 7.8 with four per SM; 512 of 8 heads 5.7 and 8.9.)
-  R.heads = rows_for(R.token_ctas, Hkv, sms, R.tokens == 1 ? 2 : 8);
+  R.heads = rows_for(R.token_ctas, Hkv, sms, R.tokens == 1 ? 2 : 1024 / threads);
   const dim3 g(static_cast<unsigned>(grid), static_cast<unsigned>((Hkv + R.heads - 1) / R.heads));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = dtype == SV_BF16;
@@ -649,7 +652,7 @@ int sv_page_commit8(int dtype, void* k_pages, void* v_pages, void* k_scales, voi
   const int sms = sm_count();
   if (sms < 1) return SV_ERR_CUDA;
   const int threads = threads_for(R.P);
-  R.rows = rows_for(B, LH, sms, 8);
+  R.rows = rows_for(B, LH, sms, 1024 / threads);
   const int units = (N - 1 + block - 1) / block + 1;  // of a path of N entries, wherever it begins
   // A path's units one after another, unless there are too few CTAs otherwise: most paths have
   // one or two, whatever N, and the CTAs that find none cost 1 us of 30 (64 paths of 4 entries out
