@@ -233,7 +233,7 @@ __device__ __forceinline__ void write_rows(const Pools& P, Shared& S, int page, 
           const float* const angles = entry[u].angles;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int pair = 8 * c + e;
+            const int pair = e * P.chunks + c;
             ka[u][e] = widen1<BF>(k[first_of(pair, rot, inter)]);
             kb[u][e] = widen1<BF>(k[second_of(pair, rot, inter)]);
             if (pair < rot / 2)
@@ -292,7 +292,7 @@ __device__ __forceinline__ void write_rows(const Pools& P, Shared& S, int page, 
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int pair = 8 * c + e;
+          const int pair = e * P.chunks + c;
           const uint32_t w = to_bytes(a[e], b[e], 0.0f, 0.0f);
           kp[first_of(pair, rot, inter)] = uint8_t(w);
           kp[second_of(pair, rot, inter)] = uint8_t(w >> 8);
