@@ -73,11 +73,15 @@ int sv_page_commit8(int dtype, void* k_pages, void* v_pages, void* k_scales, voi
  * sv_tree_attn over 8-bit pages: queries, output and the tree's own staged
  * entries are of dtype; the cache's values are used exactly (a value that
  * dtype cannot hold exactly, through a scale outside the range above, counts
- * as NaN).  Requirements and faults as for sv_tree_attn, with page_size <=
- * 65536; the workspace has sv_attn8_workspace_bytes() bytes, which go by the
- * batch, too: the queries and staged entries are split there into 8-bit terms
- * whose sums are theirs (two for bf16, three for fp16), but for what lies
- * 2^18 below the largest value of a query row, or of eight staged keys.
+ * as NaN), and so are staged values.  The softmax weights are rounded as by
+ * sv_tree_attn, whatever the values' sizes; the sums of their products with
+ * values are kept such that they stay finite for any that dtype has, and hold
+ * steps of 2^-104 at least.  Requirements and faults as for sv_tree_attn; the
+ * workspace has sv_attn8_workspace_bytes() bytes, which go by the batch, too:
+ * queries and staged keys are split there into 8-bit terms whose sums are
+ * theirs (two for bf16, three for fp16), but for steps of 2^-17 of the
+ * largest value of a query row, or of eight staged keys (nodes 8 i .. 8 i + 7,
+ * whoever sees them); scores have the errors of that.
  */
 /* Bytes of workspace for sv_tree_attn8; 0 for sizes that it refuses. */
 size_t sv_attn8_workspace_bytes(int B, int N, int Hq, int Hkv, int D);

@@ -74,9 +74,9 @@ size_t workspace_for(int N, int G, int D) {
 }
 
 // What the first kernel of a call over 8-bit pages leaves for the second, behind the partials:
-// the queries' and staged keys' terms, staged values, and their powers of two.
+// the queries' and staged keys' terms, and their powers of two.
 struct Space8 {
-  size_t q8, k8, v16, qf, t8, all;
+  size_t q8, k8, qf, kf, all;
 };
 Space8 space_for8(int B, int N, int Hq, int Hkv, int D) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
@@ -84,14 +84,13 @@ Space8 space_for8(int B, int N, int Hq, int Hkv, int D) {
   Space8 s;
   s.q8 = up(workspace_for(N, Hq / Hkv, D));
   s.k8 = s.q8 + up(most * tokens * Hq * D);
-  s.v16 = s.k8 + up(most * tokens * Hkv * D);
-  s.qf = s.v16 + up(2 * tokens * Hkv * D);
-  s.t8 = s.qf + up(4 * tokens * Hq);
-  s.all = s.t8 + up(size_t(B) * Hkv * ((N + TILE - 1) / TILE) * sizeof(Tile8));
+  s.qf = s.k8 + up(most * tokens * Hkv * D);
+  s.kf = s.qf + up(4 * tokens * Hq);
+  s.all = s.kf + up(size_t(B) * Hkv * ((N + TILE - 1) / TILE) * 16 * 4);
   return s;
 }
 
-// q, k_new and v_new of 8-bit calls come in `prep`.
+// q and k_new of 8-bit calls come in `prep`.
 int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v,
            const void* k_new, const void* v_new, void* workspace, void* stream,
            Prep8* prep = nullptr) {
@@ -104,16 +103,21 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
   A.G = A.Hq / A.Hkv;
   A.tpt = TILE / A.G;
   A.withhold = g_withhold;
-  if (dtype == SV_F16 || A.k_scales) {  // (weights in fp16)
-    // the keys that a row may see, times a weight's error of 2^-(25 + lift): below 2^-11
+  if (dtype == SV_F16 || A.k_scales) {
+    // the keys that a row may see, times a weight's error of 2^-(25 + lift): below 2^-11 (fp16);
+    // times a weight of up to 2^(MOST_BF16 + lift): 1 at most (bf16)
     const long long window = (long long)A.sink + A.window;
     const long long keys = A.kind == TREE   ? (long long)A.cols * A.page + A.N
                            : A.kind == RING ? window + A.N
                                             : (window < A.T ? window : A.T);
     int lift = 0;
     while (lift < MOST_LIFT && keys >> (14 + lift)) ++lift;
-    if (A.k_scales) lift = lift + VALUE_SLACK < MOST_LIFT ? lift + VALUE_SLACK : MOST_LIFT;
     A.lift = float(lift);
+    if (dtype == SV_BF16) {
+      lift = 0;
+      while (lift < 31 && keys >> lift) ++lift;  // (a length is below 2^31)
+      A.lift = -MOST_BF16 - float(lift);
+    }
   }
   const uint64_t D = A.D, tokens = A.kind == PROMPT ? uint64_t(A.T) : uint64_t(A.B) * A.N;
   const uint32_t q_tok = uint32_t(
@@ -125,12 +129,10 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
     const uint64_t terms = dtype == SV_BF16 ? TERMS_OF<true> : TERMS_OF<false>;
     prep->q8 = w + s.q8;
     prep->k8 = w + s.k8;
-    prep->v16 = reinterpret_cast<uint16_t*>(w + s.v16);
     prep->qf = reinterpret_cast<float*>(w + s.qf);
-    prep->t8 = reinterpret_cast<Tile8*>(w + s.t8);
-    prep->turned = layout_of(A.N, A.G).nq > 0;
+    prep->kf = reinterpret_cast<float*>(w + s.kf);
     A.qf = prep->qf;
-    A.t8 = prep->t8;
+    A.kf = prep->kf;
     const uint32_t dp = A.D > 64 ? 128 : 64;
     const CUtensorMapSwizzle swizzle =
         A.D > 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
@@ -138,12 +140,10 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
     const uint64_t qs[4] = {D, D * A.G, D * A.Hq, D * A.Hq * tokens};
     const uint32_t qb[5] = {dp, uint32_t(A.G), 1, q_tok, 1};
     const uint64_t kd[3] = {D, uint64_t(A.N), uint64_t(A.B) * A.Hkv * terms};
-    const uint64_t vd[3] = {D, uint64_t(A.N), uint64_t(A.B) * A.Hkv};
     const uint64_t ks[2] = {D, D * A.N};
-    const uint32_t kb[3] = {dp, TILE, 1}, vb[3] = {64, TILE, 1};
+    const uint32_t kb[3] = {dp, TILE, 1};
     if (!make_map8(&A.mq, prep->q8, 5, qd, qs, qb, swizzle) ||
-        !make_map8(&A.mkn, prep->k8, 3, kd, ks, kb, swizzle) ||
-        !make_map(&A.mvn, SV_F16, prep->v16, 3, vd, ks, vb))
+        !make_map8(&A.mkn, prep->k8, 3, kd, ks, kb, swizzle))
       return SV_ERR_CUDA;
   } else {
     const uint64_t dims[4] = {D, uint64_t(A.G), uint64_t(A.Hkv), tokens};
@@ -188,8 +188,8 @@ int launch(AttnParams& A, int dtype, const void* q, const void* k, const void* v
     const uint64_t dims[3] = {D, uint64_t(A.N), uint64_t(A.B) * A.LH};
     const uint64_t str[2] = {D, D * A.N};
     const uint32_t box[3] = {64, TILE, 1};
-    if (!A.k_scales && (!make_map(&A.mkn, dtype, k_new, 3, dims, str, box) ||
-                        !make_map(&A.mvn, dtype, v_new, 3, dims, str, box)))
+    if ((!A.k_scales && !make_map(&A.mkn, dtype, k_new, 3, dims, str, box)) ||
+        !make_map(&A.mvn, dtype, v_new, 3, dims, str, box))
       return SV_ERR_CUDA;
     lay = layout_of(A.N, A.G);
     const int tpi = lay.rows == 2 * TILE ? 2 * A.tpt : A.tpt;
@@ -343,9 +343,8 @@ int sv_tree_attn8(int dtype, const void* q, const void* k_pages, const void* v_p
   Prep8 P = {};
   P.q = static_cast<const uint16_t*>(q);
   P.k_new = static_cast<const uint16_t*>(k_new);
-  P.v_new = static_cast<const uint16_t*>(v_new);
   P.B = B; P.N = N; P.Hq = Hq; P.Hkv = Hkv; P.D = D; P.LH = LH; P.head0 = head0;
-  return launch(A, dtype, q, k_pages, v_pages, nullptr, nullptr, workspace, stream, &P);
+  return launch(A, dtype, q, k_pages, v_pages, nullptr, v_new, workspace, stream, &P);
 }
 
 int sv_ring_attn(int dtype, const void* q, const void* k_pool, const void* v_pool,

@@ -23,10 +23,11 @@
 // heads of 128: 319 us, 1.29 PFLOP/s, 0.67 of the measured bf16 rate.
 //
 // Over 8-bit pages (Q8; include/svkv8.h) the cache is half as long, and a tile's chain
-// holds the blocks' powers of two and values' widening besides.  Few rows are bound by HBM
-// all the same (64 requests of 4 tokens, 16 rows: 164 us, 4.7 TB/s; 208 over 16 bits), more rows by
-// the softmax and by how many roles' code an SM has to fetch: 22 nodes, 88 rows 241 us.
-//   sv_attn8_prep  before it: queries and staged entries as 8-bit terms
+// holds the keys' powers of two and values' widening besides.  Few rows are bound by the
+// widening (64 requests of 4 tokens, 16 rows: 182 us in bf16, 4.2 TB/s; 208 over 16 bits), more
+// rows by the softmax and by how many roles' code an SM has to fetch: 22 nodes, 88 rows 248 us
+// (225 over 16 bits).
+//   sv_attn8_prep  before it: queries and staged keys as 8-bit terms
 #ifndef SV_ATTENTION_CUH
 #define SV_ATTENTION_CUH
 
@@ -54,7 +55,7 @@ constexpr int MAX_KEYS = 0x7fffffff - 1023;  // cache entries: a tile more fits 
 constexpr int ITEM_COST = 2;    // an item's fixed cost in tiles (1 to 3: within 2 %)
 constexpr int TILE = 128;       // query rows of a tile, and keys of a tile
 constexpr int THREADS = 384;    // two softmax warpgroups, and one with a copy and a product warp
-constexpr int THREADS8 = 512;   // and (8-bit caches) one that widens the keys and values
+constexpr int THREADS8 = 512;   // and (8-bit caches) one that widens the values
 // Registers: launched with 168 a thread (64512 a CTA); the softmax warpgroups
 // hold up to 128 scores a thread and take over what the third does not need.
 // (Ragged prompts: 107 us with 208 / 88, 101 with 216 / 72, 132 with 184 / 136.)
@@ -70,10 +71,11 @@ struct Regs {
                 "register split");
 };
 constexpr int COPY_WARP = 8, MMA_WARP = 9, PLAN_WARP = 10;
-// 8-bit caches: 8 copies, 9 products, 12 plan, 13 scales; 10, 11, 14 and 15 widen.  A warp's
-// place goes by its number modulo 4, so no quarter of the SM fetches the code of more than
-// the softmax and two others.
-constexpr int PLAN8_WARP = 12, SCALE_WARP = 13, WIDEN_WARPS = 4;
+// 8-bit caches: 8 to 11 widen, and one other role beside each.  A warp's place goes by its
+// number modulo 4, so every quarter of the SM has one that widens.  (64 requests of 4 nodes, bf16,
+// 182 us, and 198 with two of them on each of two quarters; 22 nodes 248 and 264.)
+constexpr int WIDEN_WARPS = 4;
+constexpr int COPY8_WARP = 12, MMA8_WARP = 13, PLAN8_WARP = 14, SCALE_WARP = 15;
 constexpr int MAX_CTAS = 152;   // one per SM
 constexpr unsigned long long WAIT_LIMIT_NS = 1000000000ull;
 constexpr uint32_t SUSPEND_HINT_NS = 20000;
@@ -87,9 +89,8 @@ constexpr uint32_t SUSPEND_HINT_NS = 20000;
 // type.  (Ragged prompts: 89.6 us with 0 and 14, 90.1 with 4 and 15, 93.0 with 8 and 15.)
 constexpr float MOST_BF16 = 14.0f, MOST_F16 = 15.0f;
 constexpr int MOST_LIFT = 14;
-// 8-bit caches: the values' powers of two count relative to 2^VALUE_SLACK times the largest, so
-// that O need not be rescaled for the next tile's somewhat larger one; the lift makes up for it.
-constexpr int VALUE_SLACK = 2;
+// (bf16 over 8-bit caches: the launch takes a lift below 0, at which the weights of a row add up
+// to 1 at most, so that sums of weights times values as large as the type's stay finite.)
 
 struct AttnParams {
   CUtensorMap mq, mk, mv, mkn, mvn;  // queries, cache (or prompt) K and V, staged K and V
@@ -102,7 +103,7 @@ struct AttnParams {
   float2* part_ml;        // their maxima and sums [2 * CTAs][rows]
   int4* desc;             // [CTAs] what each CTA's first and last segments are (DESC_*)
   float c;                // scale * log2(e)
-  float lift;             // fp16: weight of a row's maximum (log2)
+  float lift;             // weight of a row's maximum (log2; bf16 over 16 bits: 0)
   int kind;
   int B, N, Hq, Hkv, D, G;
   int LH, head0, num_pages, page, cols, sink, window, T;
@@ -113,13 +114,13 @@ struct AttnParams {
   int whole_tiles;        // no item is cut when none has more tiles than this (TREE, RING)
   int join;               // and some may have, by the cache's extent
   int withhold;           // failure-handling test: one of CTA 0's stages never fills
-  // 8-bit caches (mq: the queries' terms, mkn: the staged keys', mvn: staged values in fp16): the
-  // blocks' scales [num_pages][LH][page / block], and powers of two that the first kernel found,
-  // of the queries' rows [B][N][Hq] and of the staged tiles [B][Hkv][tiles]
+  // 8-bit caches (mq: the queries' terms, mkn: the staged keys'): the blocks' scales
+  // [num_pages][LH][page / block], and powers of two that the first kernel found, of the queries'
+  // rows [B][N][Hq] and of the staged keys, eight at a time [B][Hkv][tiles][16]
   const uint8_t* k_scales;
   const uint8_t* v_scales;
   const float* qf;
-  const struct Tile8* t8;
+  const float* kf;
   int block_log;          // log2 of the tokens of a block
 };
 
@@ -675,8 +676,8 @@ __device__ __forceinline__ int v_order(int j, int n) {
 }
 
 // 8-bit caches: bytes have a ring for keys (TERMS stages for a staged tile's) and one for values,
-// filled in the order K_i V_(i - LAG), and the 16-bit ring has all values of a segment, whose
-// first tiles are the staged ones.
+// filled in the order K_i V_i, and the 16-bit ring has all values of a segment, whose first
+// tiles are the staged ones.
 __device__ __forceinline__ int staged_of(const AttnParams& A, const Seg& s) {
   return min(max(tiles_of(A.N) - s.j0, 0), s.n);
 }
@@ -702,14 +703,16 @@ __device__ __forceinline__ uint32_t span(int a, int b, int k0) {
 //     of 128 dimensions, 207 us so and 215 with a row per lane, 32 rows 210 and 217;
 //     but 64 rows, for which a warp agrees on 64 maxima, 258 and 218.)
 constexpr int CTRL_BYTES = 3 * 1024;  // what 227 KB leave beside seven tiles of 32 KB
-constexpr int CTRL8_BYTES = 2304;  // more of it with 8-bit caches
+constexpr int CTRL8_BYTES = 1536;  // more of it with 8-bit caches
 // 8-bit caches (Q8).  Keys stay bytes: scores are products of e4m3 with e4m3, the queries
 // split into TERMS such terms whose sum is theirs exactly (4 bits of a mantissa each; see
 // split_terms).  Values arrive as bytes, too, and the widening warps fill the 16-bit stages
-// that their products read, as fp16 whatever the queries are: every e4m3 value is one, by one
-// instruction for two.  Their powers of two go to the weights, which are fp16 then, relative
-// to the largest of them so far.  Few 16-bit stages are enough, since they are filled from
-// shared memory; the bytes' stages cover the copies' latency.
+// that their products read, times their power of two: a cache's exponents are those at which
+// the storage type has every value exactly, so weights and sums are those of the 16-bit
+// caches.  (The powers of two in the weights instead, relative to the largest so far, save the
+// widening half of its instructions, but a value that a row gives no weight then decides how
+// many bits the others' weights have.)  Few 16-bit stages are enough, since they are filled
+// from shared memory; the bytes' stages cover the copies' latency.
 template <bool BF>
 constexpr int TERMS_OF = BF ? 2 : 3;
 template <int DP, int NQ, int TERMS = 0, bool PAIR = false>  // TERMS: 0 for 16-bit caches
@@ -777,24 +780,18 @@ static_assert(sizeof(Ctrl<0, true>) <= CTRL_BYTES && sizeof(Ctrl<0, false>) <= C
                   sizeof(Ctrl<16, false>) <= CTRL_BYTES && sizeof(Ctrl<32, false>) <= CTRL_BYTES,
               "control part");
 
-// The control part's rest with 8-bit caches.  A tile's powers of two, eight keys at a time:
-// of the keys, 2^ek; of the values, ev less the tile's largest, and 2^ that (NQ > 0) or one
-// over it (a row per lane).  They are kept above -30: what they would take from a weight
-// further down is 2^-30 of the largest value at most.
+// The control part's rest with 8-bit caches.  A tile's powers of two, eight keys at a time: of
+// the keys in 32 bits, of the values in the storage type, twice in a word.
 struct Tile8 {
   alignas(16) float kf[16];
-  float vd[16], vf[16];
-  int top;  // the values' largest exponent
+  uint32_t vf[16];
 };
 constexpr int SCALES = 8;        // cached tiles whose scales are read ahead
-constexpr int LEAST = -30;
 template <int NQ>
 struct Ctrl8 {
   unsigned long long full[SCALES], empty[SCALES];
   Tile8 tile[SCALES];
   alignas(16) float qf[2][NQ ? NQ : 1];  // the columns' powers of two, per stream
-  int kept[2];                     // at a segment's end, per stream
-  float lost[2];
 };
 static_assert(sizeof(Ctrl8<0>) <= CTRL8_BYTES && sizeof(Ctrl8<32>) <= CTRL8_BYTES, "control part");
 __device__ __forceinline__ float power(int e) { return __int_as_float((e + 127) << 23); }
@@ -856,27 +853,17 @@ __device__ __forceinline__ void sum_columns(float* v, int lane) {
 // 64-key blocks in the 128-byte swizzle).  `sees`: the columns that see the
 // key.  All keys of a tile use one maximum per column; it is raised, the sums
 // and O (columns from to) rescaled, when a weight would exceed 2^most.
-// Q8: the scores are taken in base-2 units, times the powers of two of the key (t8) and of the
-// columns (qf); the weights stored, but not their sums, times the value's, relative to
-// 2^top, and `sink` has what O is multiplied by when that rises.
+// Q8: the scores are taken in base-2 units, times the powers of two of the key (kf) and of the
+// columns (qf).
 template <int NQ, bool BF, bool Q8>
 __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>& C, int st,
                                             int key, uint32_t ts, uint32_t to, uint32_t sees,
                                             bool masked, bool started, bool& unset, float* lq,
-                                            unsigned char* pbuf, const Tile8* t8, const float* qf,
-                                            int& top) {
-  constexpr bool HALF = Q8 || !BF;  // the weights' type
-  constexpr float MOST = HALF ? MOST_F16 : MOST_BF16;
-  const float lift = HALF ? A.lift : 0.0f, unit = Q8 ? 1.0f : A.c;
-  const float kc = Q8 ? A.c * t8->kf[key >> 3] : 0.0f;
-  float sink = 1.0f, vf = 1.0f;
-  if (Q8) {
-    if (!started || t8->top > top) {
-      if (started) sink = power(max(top - (t8->top + VALUE_SLACK), -126));
-      top = t8->top + VALUE_SLACK;
-    }
-    vf = t8->vf[key >> 3] * power(max(t8->top - top, LEAST));
-  }
+                                            unsigned char* pbuf, const float* kf,
+                                            const float* qf) {
+  const float lift = BF && !Q8 ? 0.0f : A.lift, unit = Q8 ? 1.0f : A.c;
+  const float heaviest = !BF ? MOST_F16 : Q8 ? MOST_BF16 + lift : MOST_BF16;
+  const float kc = Q8 ? A.c * kf[key >> 3] : 0.0f;
   const int lane = key & 31, warp = key >> 5;
   float* const nmc = C.x.nmc[st];
   const float2 c2 = make_float2(A.c, A.c);
@@ -924,9 +911,9 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
     return over;
   };
   load();
-  bool raise = !started || unset || sink != 1.0f;
+  bool raise = !started || unset;
   if (!raise) {
-    raise = group_or(1 + st, TILE, exponents() > MOST);
+    raise = group_or(1 + st, TILE, exponents() > heaviest);
     __syncwarp();
     if (raise) load();
   }
@@ -948,7 +935,7 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
       float old = started ? -nmc[key] : INFINITY, f = 1.0f;
       if (old == INFINITY) {
         if (t > -INFINITY) old = t - lift;
-      } else if (t - old > MOST) {
+      } else if (t - old > heaviest) {
         f = ex2(old - (t - lift));
         old = t - lift;
       }
@@ -966,7 +953,7 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
       tm_waitn<NQ>(o);
 #pragma unroll
       for (int q = 0; q < NQ; ++q)
-        o[q] = __float_as_uint(__uint_as_float(o[q]) * (C.x.fac[st][q] * sink));
+        o[q] = __float_as_uint(__uint_as_float(o[q]) * C.x.fac[st][q]);
       tm_stn<NQ>(to, o);
       tm_wait_st();
     }
@@ -983,8 +970,7 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
     const float2 l = add2(make_float2(lq[q], lq[q + 1]), p);
     lq[q] = l.x;
     lq[q + 1] = l.y;
-    const float2 y = Q8 ? mul2(p, make_float2(vf, vf)) : p;
-    const uint32_t w = pack16<!HALF>(y.x, y.y);
+    const uint32_t w = pack16<BF>(p.x, p.y);
     *reinterpret_cast<uint16_t*>(prow + q * 128 + ((piece ^ (q & 7)) << 4)) = uint16_t(w);
     *reinterpret_cast<uint16_t*>(prow + (q + 1) * 128 + ((piece ^ ((q + 1) & 7)) << 4)) =
         uint16_t(w >> 16);
@@ -992,13 +978,29 @@ __device__ __forceinline__ void softmax_few(const AttnParams& A, Ctrl<NQ, false>
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Four e4m3 values to fp16, exactly; a NaN stays one.
-__device__ __forceinline__ uint2 widen4(uint32_t w) {
+// Four e4m3 values to the storage type, times a power of two (twice in `by`) at which it has
+// them exactly; a NaN stays one.  (e4m3 goes to 16-bit floats by way of fp16, and to bf16 by way of
+// 32 bits.)
+template <bool BF>
+__device__ __forceinline__ uint2 widen4(uint32_t w, uint32_t by) {
   uint2 r;
   asm("{\n .reg .b16 u, v;\n mov.b32 {u, v}, %2;\n"
       " cvt.rn.f16x2.e4m3x2 %0, u;\n cvt.rn.f16x2.e4m3x2 %1, v;\n}"
       : "=r"(r.x), "=r"(r.y)
       : "r"(w));
+  auto times = [&](uint32_t h) {
+    if (BF) {
+      asm("{\n .reg .b16 u, v;\n .reg .f32 a, b;\n mov.b32 {u, v}, %0;\n cvt.f32.f16 a, u;\n"
+          " cvt.f32.f16 b, v;\n cvt.rn.bf16x2.f32 %0, b, a;\n mul.rn.bf16x2 %0, %0, %1;\n}"
+          : "+r"(h)
+          : "r"(by));
+    } else {
+      asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h) : "r"(by));
+    }
+    return h;
+  };
+  r.x = times(r.x);
+  r.y = times(r.y);
   return r;
 }
 
@@ -1006,8 +1008,7 @@ __device__ __forceinline__ uint2 widen4(uint32_t w) {
 // fp16, of a thread; 8 bytes a term).  A rounding leaves at most 1/16 of a value, and of 8 bits of a
 // mantissa (bf16) what is left has at most 4, so two terms are exact, of 11 (fp16) three; but
 // for what falls below the format's last step, 2^-9 where the largest value of the rows that
-// share a power of two is 224 or more: 2^-18 of that value, less than the rounding of the
-// sums of 32-bit products.
+// share a power of two is 224 or more: half a step is 2^-17 of that value at most.
 template <int TERMS>
 __device__ __forceinline__ void split_terms(const uint4& x, uint2 (&out)[TERMS]) {
   uint32_t h[4] = {x.x, x.y, x.z, x.w};
@@ -1026,7 +1027,7 @@ __device__ __forceinline__ void split_terms(const uint4& x, uint2 (&out)[TERMS])
   }
 }
 // Eight 16-bit values times `by`, a power of two that makes them 448 at most, in fp16: exact
-// down to its smallest steps, 2^-33 of the largest.
+// down to its smallest steps, 2^-33 of the largest.  What is not finite becomes NaN.
 template <bool BF>
 __device__ __forceinline__ uint4 to_half(const uint4& u, float by) {
   uint32_t r[4];
@@ -1042,15 +1043,23 @@ __device__ __forceinline__ uint4 to_half(const uint4& u, float by) {
           : "=f"(lo), "=f"(hi)
           : "r"(w));
     }
-    r[i] = pack16<false>(lo * by, hi * by);
+    r[i] = pack16<false>(fmaf(lo, by, lo - lo), fmaf(hi, by, hi - hi));
   }
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
-// The largest size among eight 16-bit values, as 32-bit float bits (of a NaN, a NaN's or more).
-template <bool BF>
+// The largest size among eight 16-bit values, as 32-bit float bits (of a NaN, a NaN's or more);
+// FINITE: among those that are.
+template <bool BF, bool FINITE = false>
 __device__ __forceinline__ uint32_t size_of(const uint4& u) {
-  uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
-                        __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+  uint4 x = {u.x & 0x7fff7fffu, u.y & 0x7fff7fffu, u.z & 0x7fff7fffu, u.w & 0x7fff7fffu};
+  if (FINITE) {
+    auto kept = [](uint32_t w) {
+      constexpr uint32_t LOW = BF ? 0x7f80u : 0x7c00u;  // an infinity's bits
+      return ((w & 0xffffu) < LOW ? w & 0xffffu : 0u) | (w >> 16 < LOW ? w & 0xffff0000u : 0u);
+    };
+    x = {kept(x.x), kept(x.y), kept(x.z), kept(x.w)};
+  }
+  uint32_t m = __vmaxu2(__vmaxu2(x.x, x.y), __vmaxu2(x.z, x.w));
   m = max(m & 0xffffu, m >> 16);
   if (BF) return m << 16;
   float f;
@@ -1179,23 +1188,26 @@ __device__ __forceinline__ void copy_bytes(const AttnParams& A, Ctrl<NQ, PAIR>& 
   }
 }
 
-// The widening warps: a segment's values, tile by tile, to fp16.  Cached ones from bytes: a
-// thread takes 16, 16 dimensions of a token, and writes two 16-byte pieces of a 64-dimension
-// block in the 128-byte swizzle; lanes of a row's two blocks write their pieces in opposite
-// order, so that eight lanes fall on eight pieces.  Staged ones are copied as they are.
+// The widening warps: a segment's values, tile by tile, to the storage type.  Cached ones from
+// bytes: a thread takes 16, 16 dimensions of a token, and writes two 16-byte pieces of a
+// 64-dimension block in the 128-byte swizzle; lanes of a row's two blocks write their pieces in
+// opposite order, so that eight lanes fall on eight pieces.  Staged ones are copied as they are.
 template <int DP, int NQ, bool PAIR, bool BF>
-__device__ __forceinline__ void widen_tiles(const AttnParams& A, Ctrl<NQ, PAIR>& C,
+__device__ __forceinline__ void widen_tiles(const AttnParams& A, Ctrl<NQ, PAIR>& C, Ctrl8<NQ>& C8,
                                             unsigned char* smem, volatile int* abort) {
   using SM = Smem<DP, NQ, TERMS_OF<BF>, PAIR>;
   constexpr int STAGES = SM::STAGES;
   constexpr int PER_ROW = DP / 16;                            // threads of a row
   constexpr int ROWS = 32 * WIDEN_WARPS / PER_ROW;            // rows of a step
-  constexpr int STEPS = TILE / ROWS, BATCH = 4;
+  // Steps at once: few rows are bound by this loop's chains (4 nodes, bf16: 182 us with four, 194
+  // with one), the others by how much code an SM has to fetch (8 nodes: 262 and 235; 22 nodes: 275
+  // and 248).
+  constexpr int STEPS = TILE / ROWS, BATCH = NQ == 16 ? 4 : 1;
   static_assert(STEPS % BATCH == 0, "whole rounds");
   const int lane = int(threadIdx.x) & 31;
-  const int warp = (int(threadIdx.x) >> 5 & 1) | (int(threadIdx.x) >> 6 & 2), tid = warp * 32 + lane;
+  const int tid = int(threadIdx.x) & (32 * WIDEN_WARPS - 1), warp = tid >> 5;
   const int row0 = tid / PER_ROW, dim = tid % PER_ROW * 16;
-  uint32_t out = 0, raw0 = 0;  // 16-bit stages, and stages of bytes, so far
+  uint32_t out = 0, raw0 = 0;  // 16-bit stages (tiles), and stages of bytes, so far
   bool ok = true;
   auto wait = [&](unsigned long long* b, uint32_t parity) {
     ok = ok && warp_wait(smem_addr(b), parity, A.status, abort);
@@ -1210,18 +1222,21 @@ __device__ __forceinline__ void widen_tiles(const AttnParams& A, Ctrl<NQ, PAIR>&
 #pragma unroll 1
     for (int j = 0; j < s.n; ++j, ++out) {
       const Keys ky = keys_of<false, true>(A, s, s.j0 + j);
-      const uint32_t st = out % STAGES, rs = SM::RAW_K + raw0 % SM::RAW_V;
+      const uint32_t st = out % STAGES, rs = SM::RAW_K + raw0 % SM::RAW_V, sc = out % SCALES;
       unsigned char* const dst = smem + SM::STAGE_AT + st * SM::BYTES;
       wait(&C.empty[st], ((out / STAGES) & 1) ^ 1);
+      wait(&C8.full[sc], (out / SCALES) & 1);
       if (!ky.staged) wait(&C.full[STAGES + rs], (raw0 / SM::RAW_V) & 1);
       if (!ok) break;
       if (ky.staged) {
         if (lane == 0) {
           const uint32_t fb = smem_addr(&C.full[st]);
+          mbar_arrive(smem_addr(&C8.empty[sc]));
           if (warp == 0) {
             mbar_arrive_tx(fb, SM::BYTES);
             for (int x = 0; x < DP / 64; ++x)
-              tma_3d(smem_addr(dst) + x * 16384, &A.mvn, fb, x * 64, ky.k0, s.b * A.Hkv + s.h);
+              tma_3d(smem_addr(dst) + x * 16384, &A.mvn, fb, x * 64, ky.k0,
+                     s.b * A.LH + A.head0 + s.h);
           } else {
             mbar_arrive(fb);
           }
@@ -1245,12 +1260,18 @@ __device__ __forceinline__ void widen_tiles(const AttnParams& A, Ctrl<NQ, PAIR>&
           b[i] = *reinterpret_cast<const uint4*>(src + (g + i) * (32 * WIDEN_WARPS * 16));
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
-          const uint2 p = widen4(b[i].x), q = widen4(b[i].y), y = widen4(b[i].z), z = widen4(b[i].w);
-          put(row0 + (g + i) * ROWS, make_uint4(p.x, p.y, q.x, q.y), make_uint4(y.x, y.y, z.x, z.y));
+          const int row = row0 + (g + i) * ROWS;
+          const uint32_t by = C8.tile[sc].vf[row >> 3];
+          const uint2 p = widen4<BF>(b[i].x, by), q = widen4<BF>(b[i].y, by);
+          const uint2 y = widen4<BF>(b[i].z, by), z = widen4<BF>(b[i].w, by);
+          put(row, make_uint4(p.x, p.y, q.x, q.y), make_uint4(y.x, y.y, z.x, z.y));
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&C.empty[STAGES + rs]));
+      if (lane == 0) {
+        mbar_arrive(smem_addr(&C.empty[STAGES + rs]));
+        mbar_arrive(smem_addr(&C8.empty[sc]));
+      }
       ++raw0;
       // behind the entries: whatever the bytes are, weights of 0 take zeros
       const int w = width_of(ky);
@@ -1298,15 +1319,12 @@ __device__ __forceinline__ void read_scales(const AttnParams& A, Ctrl<NQ, PAIR>&
 #pragma unroll 1
     for (int j = 0; ok && j < s.n;) {
       const int count = j < g ? 1 : min(at_once, s.n - j);
-      // (blocks behind the entries: no part in the tile's largest exponent)
-      int k = 0, v = -1000;
+      int k = 0, v = 0;  // (blocks behind the entries: any)
       bool nan = false;
-      float word[2] = {0.0f, 0.0f};
+      float staged = 0.0f;
       if (j < g) {
-        const float* const from = reinterpret_cast<const float*>(
-            A.t8 + (size_t(s.b) * A.Hkv + s.h) * ts + s.j0 + j);
-        word[0] = __ldg(from + lane);
-        if (lane < int(sizeof(Tile8) / 4) - 32) word[1] = __ldg(from + 32 + lane);
+        if (lane < 16)
+          staged = __ldg(A.kf + ((size_t(s.b) * A.Hkv + s.h) * ts + s.j0 + j) * 16 + lane);
       } else {
         const int t = (s.j0 + j - ts + mine) * TILE + (block << A.block_log);
         if (mine < count && t < s.len) {
@@ -1323,10 +1341,9 @@ __device__ __forceinline__ void read_scales(const AttnParams& A, Ctrl<NQ, PAIR>&
           if (nan) k = v = 0;
         }
       }
-      int top = v;  // of the tile
-      for (int x = 1; x < blocks; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const float kf = power(k), vd = nan ? __int_as_float(0x7fffffff) : float(max(v - top, LEAST));
-      const float vf = nan ? vd : power(NQ ? max(v - top, LEAST) : -max(v - top, LEAST));
+      const float kf = power(k);
+      uint32_t vf = nan ? 0x7fffu : BF ? uint32_t(v + 127) << 7 : v < -14 ? 0x200u : uint32_t(v + 15) << 10;
+      vf |= vf << 16;
 #pragma unroll 1
       for (int x = 0; x < count; ++x, ++tiles) {
         const uint32_t sc = tiles % SCALES;
@@ -1334,17 +1351,13 @@ __device__ __forceinline__ void read_scales(const AttnParams& A, Ctrl<NQ, PAIR>&
         if (!ok) break;
         Tile8& t8 = C8.tile[sc];
         if (j < g) {
-          float* const to = reinterpret_cast<float*>(&t8);
-          to[lane] = word[0];
-          if (lane < int(sizeof(Tile8) / 4) - 32) to[32 + lane] = word[1];
+          if (lane < 16) t8.kf[lane] = staged;
         } else if (mine == x) {
 #pragma unroll 1
           for (int i = block * rep; i < block * rep + rep; ++i) {
             t8.kf[i] = kf;
-            t8.vd[i] = vd;
             t8.vf[i] = vf;
           }
-          if (block == 0) t8.top = top;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&C8.full[sc]));
@@ -1357,19 +1370,17 @@ __device__ __forceinline__ void read_scales(const AttnParams& A, Ctrl<NQ, PAIR>&
 // -------------------------------------------------------------- queries and staged entries
 
 // What the kernel before the attention over 8-bit pages makes of the queries and the staged
-// entries, so that they arrive there by copies like everything else: the terms of both, the
-// staged values in fp16, and their powers of two.  (Made by the attention kernel's own warps
-// first: 6 us more per item, in which the tiles waited.)
+// keys, so that they arrive there by copies like everything else: the terms of both and their
+// powers of two.  (Made by the attention kernel's own warps first: 6 us more per item, in which
+// the tiles waited.)
 struct Prep8 {
   const uint16_t* q;
   const uint16_t* k_new;
-  const uint16_t* v_new;
   uint8_t* q8;    // [TERMS][B][N][Hq][D]
   uint8_t* k8;    // [TERMS][B][Hkv][N][D]
-  uint16_t* v16;  // [B][Hkv][N][D]
   float* qf;      // [B][N][Hq]
-  Tile8* t8;      // [B][Hkv][tiles]
-  int B, N, Hq, Hkv, D, LH, head0, turned;
+  float* kf;      // [B][Hkv][tiles][16]
+  int B, N, Hq, Hkv, D, LH, head0;
 };
 constexpr int PREP_THREADS = 128, PREP_ROWS = 64;  // query rows of a CTA
 inline long long prep8_blocks(const Prep8& P) {
@@ -1382,7 +1393,6 @@ inline long long prep8_blocks(const Prep8& P) {
 template <int DP, bool BF>
 __global__ void __launch_bounds__(PREP_THREADS) sv_attn8_prep(const __grid_constant__ Prep8 P) {
   constexpr int TERMS = TERMS_OF<BF>, PER_ROW = DP / 16, WARP_ROWS = 32 / PER_ROW;
-  __shared__ int exps[16];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int dim = lane % PER_ROW * 16, lane_row = lane / PER_ROW;
@@ -1412,51 +1422,30 @@ __global__ void __launch_bounds__(PREP_THREADS) sv_attn8_prep(const __grid_const
     const int k0 = tile * TILE, n = min(TILE, P.N - k0);
     const size_t from = ((size_t(b) * P.LH + P.head0 + h) * P.N + k0) * P.D;
     const size_t to = (size_t(bh) * P.N + k0) * P.D, stride = size_t(P.B) * P.Hkv * P.N * P.D;
-    Tile8& t8 = P.t8[blockIdx.x];
     for (int g = warp; g < 16; g += PREP_THREADS / 32) {
       constexpr int V = 8 / WARP_ROWS;  // rows of a lane
-      Row k[V], v[V];
-      uint32_t k_most = 0, v_most = 0;
+      Row k[V];
+      uint32_t most = 0;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int row = g * 8 + i * WARP_ROWS + lane_row;
         k[i] = fetch(P.k_new + from + size_t(row) * P.D, row < n);
-        v[i] = fetch(P.v_new + from + size_t(row) * P.D, row < n);
+        most = max(most, size(k[i]));
       }
+      int e = exponent_over(__reduce_max_sync(0xffffffffu, most));
+      if (e == NOT_FINITE) {  // (those become NaN by themselves, and the others keep their bits)
+        most = 0;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        k_most = max(k_most, size(k[i]));
-        v_most = max(v_most, size(v[i]));
+        for (int i = 0; i < V; ++i)
+          most = max(most, max(size_of<BF, true>(k[i].lo), size_of<BF, true>(k[i].hi)));
+        e = exponent_over(__reduce_max_sync(0xffffffffu, most));
       }
-      const int e = exponent_over(__reduce_max_sync(0xffffffffu, k_most));
-      const int ev = exponent_over(__reduce_max_sync(0xffffffffu, v_most));
-      if (lane == 0) {
-        t8.kf[g] = power_or_nan(e);
-        exps[g] = g * 8 >= n ? -1000 : e == NOT_FINITE ? e : ev;
-      }
-      const float by = power(-min(ev, 119));
+      if (lane == 0) P.kf[size_t(blockIdx.x) * 16 + g] = power(e);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int row = g * 8 + i * WARP_ROWS + lane_row;
-        if (row < n && dim < P.D) {
-          terms(k[i], e, P.k8 + to + size_t(row) * P.D, stride);
-          uint4* const out = reinterpret_cast<uint4*>(P.v16 + to + size_t(row) * P.D + dim);
-          out[0] = to_half<BF>(v[i].lo, by);
-          out[1] = to_half<BF>(v[i].hi, by);
-        }
+        if (row < n && dim < P.D) terms(k[i], e, P.k8 + to + size_t(row) * P.D, stride);
       }
-    }
-    __syncthreads();
-    if (warp == 0) {
-      const int ev = lane < 16 ? exps[lane] : -1000;
-      const int top = __reduce_max_sync(0xffffffffu, ev == NOT_FINITE ? 0 : ev);
-      const int by = max(ev - top, LEAST);
-      const float nan = __int_as_float(0x7fffffff);
-      if (lane < 16) {
-        t8.vd[lane] = ev == NOT_FINITE ? nan : float(by);
-        t8.vf[lane] = ev == NOT_FINITE ? nan : power(P.turned ? by : -by);
-      }
-      if (lane == 0) t8.top = top;
     }
     return;
   }
@@ -1486,7 +1475,7 @@ __global__ void __launch_bounds__(PREP_THREADS) sv_attn8_prep(const __grid_const
 // The weights are rounded once to the storage type (half a step each); their sum
 // l is taken before that, in 32 bits.
 // 8-bit caches (Q8) add
-//   widen     four warps: cached values from bytes to fp16
+//   widen     four warps: cached values from bytes to the storage type
 //   scales    the blocks' powers of two, a few tiles ahead
 template <int DP, int NQ, bool PAIR, bool PR, bool BF, bool Q8 = false>
 __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
@@ -1523,7 +1512,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
       }
       for (int i = 0; i < SCALES; ++i) {
         mbar_init(bar(&C8.full[i]), 1);
-        mbar_init(bar(&C8.empty[i]), PAIR ? 8 : 4);
+        mbar_init(bar(&C8.empty[i]), (PAIR ? 8 : 4) + WIDEN_WARPS);
       }
     }
     for (int i = 0; i < 2; ++i) {
@@ -1536,7 +1525,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
     }
     for (int i = 0; i < SEGS; ++i) {
       mbar_init(bar(&C.seg_full[i]), 1);
-      mbar_init(bar(&C.seg_empty[i]), COPY_WARP + 2 + (Q8 ? WIDEN_WARPS + 1 : 0));  // its readers
+      mbar_init(bar(&C.seg_empty[i]), 8 + 2 + (Q8 ? WIDEN_WARPS + 1 : 0));  // its readers
     }
     mbar_init(bar(&C.drain), 1);
     mbar_init(bar(&C.next_full), 1);
@@ -1546,7 +1535,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  if (warp == MMA_WARP) {
+  if (warp == (Q8 ? MMA8_WARP : MMA_WARP)) {
     __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(&C.tmem)),
@@ -1716,10 +1705,8 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
       const int q0 = s.mt * tpi, q1 = min(q0 + tpi, tokens) - 1;  // the item's tokens
       const int w0 = q0 + (PAIR ? st * A.tpt : 0), w1 = min(w0 + A.tpt, tokens) - 1;  // the tile's
 
-      constexpr bool HALF = Q8 || !BF;  // the weights' type
-      const float lift = HALF ? A.lift : 0.0f, raise = HALF ? MOST_F16 - A.lift : MOST_BF16;
+      const float lift = BF && !Q8 ? 0.0f : A.lift, raise = BF ? MOST_BF16 : MOST_F16 - A.lift;
       const float unit = Q8 ? 1.0f : A.c;  // of the maxima, in base-2 units
-      int top = 0;            // Q8: O's power of two, VALUE_SLACK above the values' largest
       float m = -INFINITY, l = 0.0f;
       float lq[NQ ? NQ : 1];  // NQ > 0: this key's share of the columns' sums
       bool unset = true;      // NQ > 0: a column has seen nothing yet
@@ -1811,20 +1798,15 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
           }
           softmax_few<NQ, BF, Q8>(A, C, st, row, ts, to, sees, masked, done > 0, unset, lq,
                                   smem + SM::P_AT + st * SM::P_BYTES,
-                                  t8, C8.qf[st], top);
+                                  t8->kf, C8.qf[st]);
         } else if (!warp_active) {
           __syncwarp();
           half_done();
         } else {
-          // Q8: what the scores of eight keys are multiplied by, and the weights' exponents moved by
-          float qc = 0.0f, adj = 0.0f, spoilt = 0.0f, sink = 1.0f;
+          // Q8: what the scores of eight keys are multiplied by
+          float qc = 0.0f, spoilt = 0.0f;
           if (Q8) {
             qc = A.c * qf;
-            if (done == 0 || t8->top > top) {
-              if (done) sink = power(max(top - (t8->top + VALUE_SLACK), -126));
-              top = t8->top + VALUE_SLACK;
-            }
-            adj = float(max(t8->top - top, LEAST));
             spoilt = qc - qc;  // NaN with the row's power of two, else 0
           }
           auto factors = [&](int x) {  // (not 0: hidden scores stay at -infinity)
@@ -1847,24 +1829,18 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
           auto weigh = [&](int x, const uint32_t (&r)[32], float nm, uint32_t (&pw)[16],
                            float2 (&sum)[4]) {
             const float4 f = factors(x);
-            const float4 d = *reinterpret_cast<const float4*>(t8->vd + 4 * x);
-            const float4 v = *reinterpret_cast<const float4*>(t8->vf + 4 * x);
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               const float fg = g == 0 ? f.x : g == 1 ? f.y : g == 2 ? f.z : f.w;
-              const float dg = nm + (g == 0 ? d.x : g == 1 ? d.y : g == 2 ? d.z : d.w);
-              const float vg = g == 0 ? v.x : g == 1 ? v.y : g == 2 ? v.z : v.w;
-              float2 t = make_float2(0.0f, 0.0f);
 #pragma unroll
               for (int i = 4 * g; i < 4 * g + 4; ++i) {
                 const float2 e = fma2(
                     make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
-                    make_float2(fg, fg), make_float2(dg, dg));
+                    make_float2(fg, fg), make_float2(nm, nm));
                 const float2 p = make_float2(ex2(e.x), ex2(e.y));
-                t = add2(t, p);
-                pw[i] = pack16<false>(p.x, p.y);
+                sum[i & 3] = add2(sum[i & 3], p);
+                pw[i] = pack16<BF>(p.x, p.y);
               }
-              sum[g] = fma2(t, make_float2(vg, vg), sum[g]);
             }
           };
           // the tile's keys that this row sees, 32 to a word
@@ -1906,11 +1882,10 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
               m = mt;
             } else {
               const bool rise = active && (mt - m) * unit > raise;  // (-inf before: always)
-              if (__any_sync(0xffffffffu, rise || sink != 1.0f)) {
-                float f = rise ? ex2((m - mt) * unit) : 1.0f;
+              if (__any_sync(0xffffffffu, rise)) {
+                const float f = rise ? ex2((m - mt) * unit) : 1.0f;
                 if (rise) m = mt;
                 l *= f;
-                f *= sink;
 #pragma unroll 1
                 for (int x = 0; x < DP / 32; ++x) {
                   uint32_t o[32];
@@ -1953,7 +1928,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
               mt = fmaxf(mt, most(x, r));
             }
             raise_to(mt);
-            const float nm = (m == -INFINITY ? 0.0f : lift - m) + adj + spoilt;
+            const float nm = (m == -INFINITY ? 0.0f : lift - m) + spoilt;
             float2 sum[4] = {};
 #pragma unroll 1
             for (int x = 0; x * 32 < w; ++x) {  // (P's columns lie over scores that are done with)
@@ -1968,7 +1943,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
               half_done();
             }
             sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-            l += (sum[0].x + sum[0].y) * power(int(-adj));
+            l += sum[0].x + sum[0].y;
             __syncwarp();
           } else if constexpr (PAIR) {
             uint32_t r[4][32];
@@ -2122,10 +2097,6 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
       }
 
       // ---- the segment's end: the output rows, or their partials
-      // Q8: O stands for 2^top times itself.  That goes to the maximum, and out of the sum l, as
-      // far as 32 bits hold it; `lost` is the rest.
-      const int kept = Q8 ? min(max(top, -60), 60) : 0;
-      const float lost = Q8 ? power(top - kept) : 1.0f, unkept = power(-kept);
       const bool whole = n == s.nt;
       const int slot = segs == 0 ? 0 : 1;
       const size_t part = (size_t(blockIdx.x) * 2 + slot) * ROWS + (PAIR ? st * TILE : 0) + row;
@@ -2175,10 +2146,6 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         // sums over the keys: 32 lanes here, the four warps and two streams below
         sum_columns<NQ>(lq, lane);
         if (lane < NQ) C.x.sums[warp][lane] = lq[0];
-        if (Q8 && row == 0) {
-          C8.kept[st] = kept;
-          C8.lost[st] = lost;
-        }
         group_sync(3, 2 * TILE);
         if (tid < NQ) {
           float l0 = 0.0f, l1 = 0.0f;
@@ -2189,23 +2156,12 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
           float a = -C.x.nmc[0][tid], b = n > 1 ? -C.x.nmc[1][tid] : INFINITY;
           if (a == INFINITY) a = -INFINITY;  // nothing seen
           if (b == INFINITY) b = -INFINITY;
-          if (Q8) {
-            const int k0 = C8.kept[0], k1 = n > 1 ? C8.kept[1] : 0;
-            a += float(k0);
-            b += float(k1);
-            l0 *= power(-k0);
-            l1 *= power(-k1);
-          }
           const float mm = fmaxf(a, b), mu = mm == -INFINITY ? 0.0f : mm;
           float f0 = ex2(a - mu), f1 = ex2(b - mu);
           const float ll = l0 * f0 + (n > 1 ? l1 * f1 : 0.0f);
           if (whole) {
             f0 /= ll;
             f1 /= ll;
-          }
-          if (Q8) {
-            f0 *= C8.lost[0];
-            f1 *= n > 1 ? C8.lost[1] : 1.0f;
           }
           C.x.fac[0][tid] = f0;
           C.x.fac[1][tid] = f1;
@@ -2258,8 +2214,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         ++o_use[st];
         tc_after();
         if (ok && warp_active) {
-          if (Q8) l *= unkept;
-          const float f = (whole ? 1.0f / l : 1.0f) * lost;
+          const float f = whole ? 1.0f / l : 1.0f;
 #pragma unroll 1
           for (int x = 0; x < DP / 32; ++x) {
             uint32_t o[32];
@@ -2271,13 +2226,12 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
             put(v, x * 32);
           }
           if (!whole && active)
-            A.part_ml[part] = make_float2(m * unit + float(kept), bad ? -1.0f : l);
+            A.part_ml[part] = make_float2(m * unit, bad ? -1.0f : l);
         }
         tc_before();
       } else {
         // join the two streams; warpgroup st takes half of the columns
-        C.x.ml[st][row] = Q8 ? make_float2(m + float(kept), l * unkept) : make_float2(m, l);
-        if (Q8 && row == 0) C8.lost[st] = lost;
+        C.x.ml[st][row] = make_float2(m, l);
         for (int x = 0; x < 2; ++x) {
           if (x >= n) break;
           ok = ok && warp_wait(bar(&C.o_full[x]), o_use[x] & 1, A.status, abort);
@@ -2295,10 +2249,6 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
           if (whole) {
             f0 /= ll;
             f1 /= ll;
-          }
-          if (Q8) {
-            f0 *= C8.lost[0];
-            f1 *= n > 1 ? C8.lost[1] : 1.0f;
           }
           const uint32_t t0 = tmem + lanes + O_AT;
 #pragma unroll 1
@@ -2340,8 +2290,8 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
   } else {
     __syncwarp();
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<NQ, Q8>::OTHER));
-  if (Q8 && (warp & 2)) {
-    if constexpr (Q8) widen_tiles<DP, NQ, PAIR, BF>(A, C, smem, abort);
+  if (Q8 && warp < 8 + WIDEN_WARPS) {
+    if constexpr (Q8) widen_tiles<DP, NQ, PAIR, BF>(A, C, C8, smem, abort);
   } else if (warp == (Q8 ? PLAN8_WARP : PLAN_WARP)) {
     // ------------------------------------------------------------ the plan
     Cursor<PAIR, PR> cur;
@@ -2411,7 +2361,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
       int k = 0;
       while (plan(k, cur.next(A, s))) ++k;
     }
-  } else if (warp == COPY_WARP) {
+  } else if (warp == (Q8 ? COPY8_WARP : COPY_WARP)) {
     // ------------------------------------------------------------ copies
     // One thread, or (pages) a warp with a lane per box of page rows.
     auto copies = [&](auto solo) {
@@ -2520,14 +2470,14 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
     }
   } else if (Q8 && warp == SCALE_WARP) {
     if constexpr (Q8) read_scales<NQ, PAIR, BF>(A, C, C8, abort);
-  } else if (warp == MMA_WARP) {
+  } else if (warp == (Q8 ? MMA8_WARP : MMA_WARP)) {
     // ------------------------------------------------------------ products
     uint32_t idx = 0;
     int segs = 0;
     unsigned p_use[2] = {0, 0};
     // (the turned products: N = NQ, and V^T is an operand whose dimensions are contiguous)
     const uint32_t id_s = instr_desc(BF, false, false, NQ);  // (0: the tile's width goes there)
-    const uint32_t id_o = instr_desc(BF && !Q8, NQ > 0, NQ == 0, NQ ? NQ : DP);
+    const uint32_t id_o = instr_desc(BF, NQ > 0, NQ == 0, NQ ? NQ : DP);
     bool ok = true;
     auto full = [&](uint32_t u) {
       if (!mbar_wait(bar(&C.full[u % STAGES]), (u / STAGES) & 1, A.status, abort)) return false;
@@ -2758,7 +2708,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == MMA_WARP) {
+  if (warp == (Q8 ? MMA8_WARP : MMA_WARP)) {
     __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "n"(TM_COLS)
