@@ -77,13 +77,16 @@ int sv_page_commit8(int dtype, void* k_pages, void* v_pages, void* k_scales, voi
  * sv_tree_attn, whatever the values' sizes; the sums of their products with
  * values are kept such that they stay finite for any that dtype has, and hold
  * steps of 2^-104 at least.  Requirements and faults as for sv_tree_attn; the
- * workspace has sv_attn8_workspace_bytes() bytes, which go by the batch, too:
- * queries and staged keys are split there into 8-bit terms whose sums are
- * theirs (two for bf16, three for fp16), but for steps of 2^-17 of the
- * largest value of a query row, or of eight staged keys (nodes 8 i .. 8 i + 7,
- * whoever sees them); scores have the errors of that.
+ * workspace has sv_attn8_workspace_bytes() bytes: queries and staged keys are
+ * split there into 8-bit terms whose sums are theirs (two for bf16, three for
+ * fp16), but for steps of 2^-17 of the largest value of a query row, or of
+ * eight staged keys (nodes 8 i .. 8 i + 7, whoever sees them); scores have the
+ * errors of that.  A batch of which that takes more than 256 MiB goes in parts,
+ * one after another in the same workspace.
  */
-/* Bytes of workspace for sv_tree_attn8; 0 for sizes that it refuses. */
+/* Bytes of workspace for sv_tree_attn8 with up to B requests: beside
+ * sv_attn_workspace_bytes() 256 MiB at most, or what one request takes; 0 for
+ * sizes that it refuses. */
 size_t sv_attn8_workspace_bytes(int B, int N, int Hq, int Hkv, int D);
 
 int sv_tree_attn8(int dtype, const void* q, const void* k_pages, const void* v_pages,

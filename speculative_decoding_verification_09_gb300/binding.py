@@ -521,8 +521,8 @@ def sv_attn8_workspace_bytes(B: int, N: int, Hq: int, Hkv: int, D: int) -> int:
 def make_attn_workspace(B: int, N: int, Hq: int, Hkv: int, D: int, device,
                         cache_bits: int | None = None) -> torch.Tensor:
     """Allocate a workspace for sv_tree_attn or sv_tree_attn8 (N nodes) or sv_ring_attn (N = R
-    tokens) with a batch of up to B.  cache_bits: 16 leaves out what only sv_tree_attn8 needs,
-    which alone goes by the batch; 8 what only the others need."""
+    tokens) with a batch of up to B.  cache_bits: 16 leaves out what only sv_tree_attn8 needs
+    (up to 256 MiB, by the batch); 8 refuses sizes that it does."""
     n = sv_attn_workspace_bytes(N, Hq, Hkv, D) if cache_bits != 8 else 0
     if cache_bits != 16:
         n = max(n, sv_attn8_workspace_bytes(B, N, Hq, Hkv, D))

@@ -73,18 +73,30 @@ size_t workspace_for(int N, int G, int D) {
   return size_t(MAX_CTAS) * (2 * rows * (dp * 4 + 8) + sizeof(int4));
 }
 
+// Requests that a call over 8-bit pages takes at a time: as many as MOST_SPACE8 bytes hold of
+// what is made of them, so that a workspace for both kinds of cache is bounded whatever the
+// batch.  (32 heads of 128: 512 requests of 64 nodes over 500 to 2000 entries 1044 us in two parts
+// and 1018 in one; 1194 in eight of 64 MiB.)
+constexpr size_t MOST_SPACE8 = 256 << 20, TERMS8 = 3;  // (terms of fp16; bf16 has two)
+int requests_at_once(int B, int N, int Hq, int Hkv, int D) {
+  const size_t one = TERMS8 * N * (size_t(Hq) + Hkv) * D + size_t(4) * N * Hq +
+                     size_t(Hkv) * ((N + TILE - 1) / TILE) * 16 * 4;
+  const size_t n = MOST_SPACE8 / one;
+  return n < 1 ? 1 : n < size_t(B) ? int(n) : B;
+}
+
 // What the first kernel of a call over 8-bit pages leaves for the second, behind the partials:
-// the queries' and staged keys' terms, and their powers of two.
+// the queries' and staged keys' terms, and their powers of two (of B requests at a time).
 struct Space8 {
   size_t q8, k8, qf, kf, all;
 };
 Space8 space_for8(int B, int N, int Hq, int Hkv, int D) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-  const size_t tokens = size_t(B) * N, most = 3;  // terms
+  const size_t tokens = size_t(B) * N;
   Space8 s;
   s.q8 = up(workspace_for(N, Hq / Hkv, D));
-  s.k8 = s.q8 + up(most * tokens * Hq * D);
-  s.qf = s.k8 + up(most * tokens * Hkv * D);
+  s.k8 = s.q8 + up(TERMS8 * tokens * Hq * D);
+  s.qf = s.k8 + up(TERMS8 * tokens * Hkv * D);
   s.kf = s.qf + up(4 * tokens * Hq);
   s.all = s.kf + up(size_t(B) * Hkv * ((N + TILE - 1) / TILE) * 16 * 4);
   return s;
@@ -298,7 +310,7 @@ int sv_tree_attn(int dtype, const void* q, const void* k_pages, const void* v_pa
 
 size_t sv_attn8_workspace_bytes(int B, int N, int Hq, int Hkv, int D) {
   if (B < 0 || B > 65535 || N < 1 || N > MAX_N || bad_heads(Hq, Hkv, D) || D % 16 != 0) return 0;
-  return space_for8(B, N, Hq, Hkv, D).all;
+  return space_for8(requests_at_once(B, N, Hq, Hkv, D), N, Hq, Hkv, D).all;
 }
 
 int sv_tree_attn8(int dtype, const void* q, const void* k_pages, const void* v_pages,
@@ -327,24 +339,33 @@ int sv_tree_attn8(int dtype, const void* q, const void* k_pages, const void* v_p
   if (!workspace || misaligned(workspace, 256) ||
       workspace_bytes < sv_attn8_workspace_bytes(B, N, Hq, Hkv, D))
     return SV_ERR_WORKSPACE;
-  AttnParams A = {};
-  A.kind = TREE;
-  A.table = block_table;
-  A.lens = seq_lens;
-  A.parent = parent;
-  A.out = static_cast<uint16_t*>(out);
-  A.status = dev_status;
-  A.k_scales = static_cast<const uint8_t*>(k_scales);
-  A.v_scales = static_cast<const uint8_t*>(v_scales);
-  A.block_log = block_log;
-  A.c = scale * LOG2E;
-  A.B = B; A.N = N; A.Hq = Hq; A.Hkv = Hkv; A.D = D;
-  A.LH = LH; A.head0 = head0; A.num_pages = num_pages; A.page = page_size; A.cols = cols;
-  Prep8 P = {};
-  P.q = static_cast<const uint16_t*>(q);
-  P.k_new = static_cast<const uint16_t*>(k_new);
-  P.B = B; P.N = N; P.Hq = Hq; P.Hkv = Hkv; P.D = D; P.LH = LH; P.head0 = head0;
-  return launch(A, dtype, q, k_pages, v_pages, nullptr, v_new, workspace, stream, &P);
+  // parts of equal size, one after another
+  const int most = requests_at_once(B, N, Hq, Hkv, D), parts = (B + most - 1) / most;
+  for (int part = 0; part < parts; ++part) {
+    const int b0 = int((long long)B * part / parts), b1 = int((long long)B * (part + 1) / parts);
+    const size_t rows = size_t(b0) * N * Hq * D, staged = size_t(b0) * LH * N * D;
+    AttnParams A = {};
+    A.kind = TREE;
+    A.table = block_table + size_t(b0) * cols;
+    A.lens = seq_lens + b0;
+    A.parent = parent ? parent + size_t(b0) * N : nullptr;
+    A.out = static_cast<uint16_t*>(out) + rows;
+    A.status = dev_status;
+    A.k_scales = static_cast<const uint8_t*>(k_scales);
+    A.v_scales = static_cast<const uint8_t*>(v_scales);
+    A.block_log = block_log;
+    A.c = scale * LOG2E;
+    A.B = b1 - b0; A.N = N; A.Hq = Hq; A.Hkv = Hkv; A.D = D;
+    A.LH = LH; A.head0 = head0; A.num_pages = num_pages; A.page = page_size; A.cols = cols;
+    Prep8 P = {};
+    P.q = static_cast<const uint16_t*>(q) + rows;
+    P.k_new = static_cast<const uint16_t*>(k_new) + staged;
+    P.B = A.B; P.N = N; P.Hq = Hq; P.Hkv = Hkv; P.D = D; P.LH = LH; P.head0 = head0;
+    const int rc = launch(A, dtype, nullptr, k_pages, v_pages, nullptr,
+                          static_cast<const uint16_t*>(v_new) + staged, workspace, stream, &P);
+    if (rc != SV_OK) return rc;
+  }
+  return SV_OK;
 }
 
 int sv_ring_attn(int dtype, const void* q, const void* k_pool, const void* v_pool,

@@ -166,3 +166,28 @@ def test_staged_entries_that_are_not_finite(dtype, N, Hq):
             G = Hq // 2
             assert bool((~out[1][at:, :G].isfinite()).any(-1).all()) if what != "q" else not bool(out[1][at, 0].isfinite().any())
             assert bool(out[1][:, G:].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_batches_beyond_the_workspace(dtype):
+    """A batch that is taken in parts: requests around their borders and elsewhere, with a parent array and without; a
+    bad page in one part is reported and its request alone gets zeros."""
+    N, Hq, Hkv, D, B = 256, 32, 8, 128, 150
+    one = 3 * N * (Hq + Hkv) * D + 4 * N * Hq + Hkv * 2 * 64
+    parts = -(-B // (2 ** 28 // one))
+    assert parts == 3 and binding.sv_attn8_workspace_bytes(B, N, Hq, Hkv, D) < B * one
+    c = tree_inputs(820, B, N, Hq, Hkv, D, 32, 16, [(37 * i) % 90 + 20 for i in range(B)], dtype, LH=Hkv + 1)
+    ws = binding.make_attn_workspace(B, N, Hq, Hkv, D, DEV, 8)
+    for parent in (True, False):
+        out, st = tree_call(c, parent=parent, ws=ws)
+        assert int(st.item()) == 0
+        for b in (0, 1, 48, 49, 50, 51, 77, 98, 99, 100, 101, 148, 149):
+            want, tol = tree_reference(c, b, parent=parent)
+            au.check(out[b], want, tol, f"request {b}")
+    again, _ = tree_call(c, parent=False, ws=ws)
+    assert torch.equal(out, again)
+    c["table"][70, 0] = -1
+    out, st = tree_call(c, parent=False, ws=ws)
+    assert int(st.item()) == binding.SV_ST_BAD_PAGE and bool((out[70] == 0).all())
+    rest = torch.arange(B, device=DEV) != 70
+    assert torch.equal(out[rest], again[rest])
