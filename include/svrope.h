@@ -58,11 +58,15 @@ enum {
 
 /*
  * The table of positions first .. first + rows - 1: gain * cos(p w_i) and
- * gain * sin(p w_i).  Angles are reduced in 64 bits, so that far positions
- * lose nothing; the functions are 32-bit ones, off by less than 2^-22.
+ * gain * sin(p w_i).  The functions are 32-bit ones, off by less than 2^-22 of
+ * the gain.  The rates are 64-bit floats by the formulas above, each with the
+ * roundings of its own computation, about 2^-49 of it: the angle p w_i is off
+ * by that part of itself (2^-32 at position 131072, 2^-18 at 2^31, with
+ * w_i = 1) and loses nothing more, as whole turns fall off exactly.
  * Requires rows >= 0, first >= 0, first + rows <= 2^31 - 1, rot even in
  * [2, 256], base > 1, factor > 0, gain finite; RAMP and WAVE: original >= 1,
- * 0 < low < high.
+ * 0 < low < high.  A rate, or the base of SV_ROPE_BASE, that no 64-bit float
+ * holds is refused.
  */
 int sv_rope_table(int scaling, double base, double factor, int original, double low, double high,
                   double gain, int rot, int first, int rows, float* table, void* stream);

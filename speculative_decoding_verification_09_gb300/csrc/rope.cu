@@ -318,10 +318,9 @@ int sv_rope_table(int scaling, double base, double factor, int original, double 
   if (scaling >= SV_ROPE_RAMP &&
       (original < 1 || !(low > 0.0) || !(high > low) || !isfinite(high)))
     return SV_ERR_INVALID_ARG;
-  if (rows == 0) return SV_OK;
-  if (!table || misaligned(table, 16)) return SV_ERR_INVALID_ARG;
   constexpr double TWO_PI = 6.283185307179586476925286766559;
   if (scaling == SV_ROPE_BASE) base *= pow(factor, double(rot) / (rot - 2));
+  if (!(base > 0.0) || !isfinite(base)) return SV_ERR_INVALID_ARG;
   double lo = 0.0, hi = 0.0;
   if (scaling == SV_ROPE_RAMP) {
     lo = floor(rot * log(original / (TWO_PI * high)) / (2.0 * log(base)));
@@ -336,7 +335,7 @@ int sv_rope_table(int scaling, double base, double factor, int original, double 
   R.first = first;
   R.rows = rows;
   R.gain = float(gain);
-  for (int i = 0; i < R.half; ++i) {
+  for (int i = 0; i < R.half; ++i) {  // (a rate that is not finite would have no turn)
     double w = pow(base, -2.0 * i / rot);
     if (scaling == SV_ROPE_LINEAR) {
       w /= factor;
@@ -347,9 +346,12 @@ int sv_rope_table(int scaling, double base, double factor, int original, double 
       const double s = fmin(fmax((original * w / TWO_PI - low) / (high - low), 0.0), 1.0);
       w = w * s + w / factor * (1.0 - s);
     }
+    if (!isfinite(w)) return SV_ERR_INVALID_ARG;
     const double turns = w / TWO_PI;  // whole turns of one position leave nothing behind
     R.turn[i] = uint64_t(ldexp(turns - floor(turns), 63)) << 1;
   }
+  if (rows == 0) return SV_OK;
+  if (!table || misaligned(table, 16)) return SV_ERR_INVALID_ARG;
   // Sixteen rows per thread, as long as that leaves some CTAs for every SM.
   const bool vec = R.half % 4 == 0;
   const int at_once = THREADS / (vec ? R.half / 4 : R.half), passes = rows / at_once / 1024;
