@@ -291,9 +291,9 @@ int run_tokens(TokenParams& R, int dtype, void* stream) {
   tokens = tokens < slots ? tokens : slots;
   R.tokens = tokens < 1 ? 1 : tokens > MAX_TOKENS ? MAX_TOKENS : tokens;
   R.lanes = slots / R.tokens;
-  R.token_ctas = (R.A.T + R.tokens - 1) / R.tokens;
+  R.token_ctas = int(((long long)R.A.T + R.tokens - 1) / R.tokens);
   const long long grid =
-      R.token_ctas + (R.pages ? (R.A.B + THREADS / 32 - 1) / (THREADS / 32) : 0);
+      (long long)R.token_ctas + (R.pages ? (R.A.B + THREADS / 32 - 1) / (THREADS / 32) : 0);
   if (grid > 0x7fffffff) return SV_ERR_INVALID_ARG;
   const bool vec = R.rot % 16 == 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
