@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(MAX_THREADS) sv_kv8_append(
     if (h == 0 && b < A.B) settle(A, b);
     return;
   }
-  const int t0 = int(blockIdx.x) * R.tokens, t1 = min(t0 + R.tokens, A.T);
+  const int t0 = int(blockIdx.x) * R.tokens, t1 = t0 + min(R.tokens, A.T - t0);
   for (int t = t0; t < t1;) {
     int b, lo, hi;
     if (!request_of(A, t, b, lo, hi)) {  // no request's row: the next one may be

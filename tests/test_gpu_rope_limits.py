@@ -64,3 +64,24 @@ def test_append_of_the_last_tokens():
     for pool in (kp, vp):
         got = pool[table[0].long()].transpose(1, 2).reshape(-1, 1, D)[5:5 + n]
         assert torch.equal(got, k[-n:])
+
+
+@pytest.mark.parametrize("block", [8, 128])
+def test_append8_of_the_last_tokens(block):
+    n, D, page, start = 300, 16, 128, 3
+    k = tokens(D, n)
+    P = 4
+    kp, vp = (torch.zeros(P, 1, page, D, dtype=torch.uint8, device=DEV).view(ku.E4M3) for _ in "kv")
+    ks, vs = (torch.zeros(P, 1, page // block, dtype=torch.uint8, device=DEV).view(ku.E8M0) for _ in "kv")
+    table, out, st = i32([[2, 0, 3]]), i32([0]), i32([0])
+    want = ku.split(kp.cpu(), ks.cpu())
+    ku.write(*want, k[-n:].transpose(0, 1).double().cpu(), [2, 0, 3], start, BF)
+    binding.sv_page_append8(k, k, kp, vp, ks, vs, table, i32([start]), i32([MOST - n, MOST]), out_seq_lens=out,
+                            dev_status=st)
+    assert int(st.item()) == 0 and out.tolist() == [start + n]
+    for pages, scales in ((kp, ks), (vp, vs)):
+        values, exps = ku.split(pages.cpu(), scales.cpu())
+        for t in range(start, start + n):  # (before them: entries of zero, whatever the scale)
+            pg, row = (2, 0, 3)[t // page], t % page
+            assert torch.equal(values[pg, 0, row], want[0][pg, 0, row]), t
+            assert int(exps[pg, 0, row // block]) == int(want[1][pg, 0, row // block]), t
