@@ -1324,7 +1324,7 @@ __device__ __forceinline__ void read_scales(const AttnParams& A, Ctrl<NQ, PAIR>&
       float staged = 0.0f;
       if (j < g) {
         if (lane < 16)
-          staged = __ldg(A.kf + ((size_t(s.b) * A.Hkv + s.h) * ts + s.j0 + j) * 16 + lane);
+          staged = __ldcg(A.kf + ((size_t(s.b) * A.Hkv + s.h) * ts + s.j0 + j) * 16 + lane);
       } else {
         const int t = (s.j0 + j - ts + mine) * TILE + (block << A.block_log);
         if (mine < count && t < s.len) {
@@ -1607,7 +1607,8 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
   // the join may be launched now: its blocks find room when this grid's CTAs
   // leave, and wait for the last of them before they read anything
   if (!PR && A.join) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // (the first kernel of a call over 8-bit pages: its outputs are there from here on)
+  // (the first kernel of a call over 8-bit pages: its outputs are there from here on, for copies and
+  // ordinary loads; it may have run beside this one, which read-only loads do not allow)
   if (Q8) asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t tmem = C.tmem;
   const int start_b = C.start_b;
@@ -1662,7 +1663,7 @@ __global__ void __launch_bounds__(Q8 ? THREADS8 : THREADS, 1)
         const int r = NQ ? row : rt, t = NQ ? row / A.G : tok;  // (column `row` is of token row / G)
         const bool on = NQ ? row < A.N * A.G : active;
         if (on)
-          qf = __ldg(A.qf + (size_t(s.b) * A.N + t) * A.Hq + s.h * A.G + (NQ ? row - t * A.G : rg));
+          qf = __ldcg(A.qf + (size_t(s.b) * A.N + t) * A.Hq + s.h * A.G + (NQ ? row - t * A.G : rg));
         if (NQ && r < NQ) C8.qf[st][row] = qf;
       }
       int bad = s.bad;
