@@ -108,8 +108,9 @@ int sv_rope(int dtype, const void* q, long long q_stride, const void* k, long lo
  * 2^31 - 1, a rotation's position is outside [0, rows) (SV_ST_BAD_LENGTH) or
  * a page in use outside [0, num_pages) (SV_ST_BAD_PAGE); what lies behind its
  * length in its pages, and its rows of q_out and k_out, are then not defined.
- * Rows of packed outputs in no request are left as they were.  No two
- * requests may write one page.
+ * Rows of packed outputs in no request are left as they were.  Where bounds
+ * decrease, which tokens of the requests around them are appended is not
+ * defined.  No two requests may write one page.
  * Requires T >= 0, B <= 65535, page_size, cols, num_pages, LH >= 1,
  * 0 <= head0, head0 + Hkv <= LH, 1 <= Hkv and Hq <= 65535, and as for sv_rope.
  */
