@@ -71,19 +71,19 @@ int sv_page_commit8(int dtype, void* k_pages, void* v_pages, void* k_scales, voi
 
 /*
  * sv_tree_attn over 8-bit pages: queries, output and the tree's own staged
- * entries are of dtype; the cache's values are used exactly (a value that
- * dtype cannot hold exactly, through a scale outside the range above, counts
- * as NaN), and so are staged values.  The softmax weights are rounded as by
- * sv_tree_attn, whatever the values' sizes; the sums of their products with
- * values are kept such that they stay finite for any that dtype has, and hold
- * steps of 2^-104 at least.  Requirements and faults as for sv_tree_attn; the
- * workspace has sv_attn8_workspace_bytes() bytes: queries and staged keys are
- * split there into 8-bit terms whose sums are theirs (two for bf16, three for
- * fp16), but for steps of 2^-17 of the largest value of a query row, or of
- * eight staged keys (nodes 8 i .. 8 i + 7, whoever sees them); scores have the
- * errors of that.  A staged key that is not finite gives NaN to the rows that
- * see its node.  A batch of which all that takes more than 256 MiB goes in
- * parts, one after another in the same workspace.
+ * entries are of dtype.  Requirements and faults as for sv_tree_attn.
+ * Values, cached and staged, are used exactly (a value that dtype cannot hold
+ * exactly, through a scale outside the range above, counts as NaN).  The
+ * softmax weights are rounded as by sv_tree_attn, whatever the values' sizes;
+ * the sums of their products with values are kept such that they stay finite
+ * for any values that dtype has, in steps of 2^-104 at most.
+ * Cached keys are used exactly; queries and staged keys are split into 8-bit
+ * terms (two for bf16, three for fp16) whose sums are off by up to 2^-17 of
+ * the largest value of a query row, or of eight staged keys (nodes 8 i .. 8 i
+ * + 7, whoever sees them): the scores have the errors of that.  A staged key
+ * that is not finite gives NaN to the rows that see its node.
+ * The terms are kept in the workspace, of sv_attn8_workspace_bytes() bytes.  A
+ * batch of which they take more than 256 MiB goes in parts, one after another.
  * Which cache: 8 bits halve it always, and the time less often.  64 requests
  * over 2000 to 9000 entries, 8 KV heads of 128, bf16, us in 8 and in 16 bits,
  * by rows of a KV head (N * Hq / Hkv): 4 179 and 208, 16 182 and 209, 32 236
